@@ -316,6 +316,7 @@ const char* qmm_status_string(int s) {
         case QMM_ERR_WORKSPACE: return "QMM_ERR_WORKSPACE: workspace missing or too small";
         case QMM_ERR_SCRATCH_LIMIT:
             return "QMM_ERR_SCRATCH_LIMIT: needs more than the fixed scratch (QMM_MOE_STATIC_SCRATCH_BYTES)";
+        case QMM_ERR_BAD_INDEX: return "QMM_ERR_BAD_INDEX: position, slot, page or length outside its range";
         default: return "QMM_ERR_UNKNOWN";
     }
 }
@@ -1039,6 +1040,7 @@ qmm_status qmm_last_device_error(void* stream) {
     }
     if (v & ERR_TIMEOUT) return QMM_ERR_TIMEOUT;
     if (v & ERR_BAD_EXPERT) return QMM_ERR_BAD_EXPERT_ID;
+    if (v & ERR_BAD_INDEX) return QMM_ERR_BAD_INDEX;
     return QMM_OK;
 }
 

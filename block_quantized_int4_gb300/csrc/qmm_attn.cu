@@ -1,0 +1,159 @@
+// qmm_attn.cu -- qmm_attn_q4_0 on the host: argument checks, the plan of a
+// launch, and the kernel that joins items cut over several CTAs.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "qmm.h"
+#include "qmm_attn.cuh"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+struct Plan {
+    int row_warps, token_warps, block_rows, blocks;
+    int ctas;  // CTAs of a cut launch; 0: one CTA an item
+    int64_t items;
+    size_t meta_bytes, part_bytes;
+    int smem;
+};
+
+constexpr int DEFAULT_SMS = 152;
+
+Plan plan_of(const qmm_attn_op& op, int sms) {
+    Plan p = {};
+    const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
+    const bool f32 = op.q.dtype == QMM_F32;
+    const int tile = attn_tile_rows(f32);
+    const int64_t rows = (int64_t)op.max_q * group;
+    p.row_warps = rows <= tile ? 1 : rows <= 2 * tile ? 2 : 4;
+    p.token_warps = ATTN_WARPS / p.row_warps;
+    p.block_rows = p.row_warps * tile;
+    p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
+    p.items = (int64_t)op.n_seqs * p.blocks * op.cache.n_heads;
+    p.smem = std::max(p.token_warps * ATTN_STAGES * record_bytes(D), ATTN_WARPS * tile * D * 4);
+    // Items of a few units are not worth a second launch that joins parts.
+    const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
+    if (units > 4) {
+        p.ctas = (int)std::min<int64_t>((int64_t)sms * attn_ctas(NB), p.items * units);
+        p.meta_bytes = ((size_t)p.ctas * sizeof(AttnMeta) + 255) / 256 * 256;
+        p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * (D + 2) * 4;
+    }
+    return p;
+}
+
+qmm_status check(const qmm_attn_op& op, bool pointers) {
+    if (op.n_seqs < 0 || op.T < 0 || op.max_q < 0 || op.max_kv < 0 || op.window < 0 || !std::isfinite(op.scale))
+        return QMM_ERR_ARG;
+    if (qmm_status s = check_cache(op.cache, pointers)) return s;
+    if (op.q.n_heads <= 0 || (op.q.dtype != QMM_F32 && op.q.dtype != QMM_F16 && op.q.dtype != QMM_BF16))
+        return QMM_ERR_ARG;
+    if (op.q.n_heads % op.cache.n_heads) return QMM_ERR_SHAPE;
+    const int64_t group = op.q.n_heads / op.cache.n_heads;
+    if (op.max_kv > 1 << 28 || op.max_q > 1 << 28 || op.max_q * group > 1 << 28 || op.T > 1 << 28 ||
+        (int64_t)op.n_seqs * op.max_q * op.q.n_heads > int64_t(1) << 30)
+        return QMM_ERR_SHAPE;
+    if (!op.q_start && op.T != (int64_t)op.n_seqs * op.max_q) return QMM_ERR_SHAPE;
+    if (op.pages_stride < (op.max_kv + op.cache.page_size - 1) / op.cache.page_size) return QMM_ERR_SHAPE;
+    if (!pointers) return QMM_OK;
+    if (qmm_status s = check_heads(op.q, 0)) return s;
+    if (op.out.data) {
+        if (qmm_status s = check_output(op.out, op.q.n_heads, op.T, op.cache.head_dim)) return s;
+        if (op.out.dtype != op.q.dtype) return QMM_ERR_ARG;
+    }
+    if ((!op.yq) != (!op.yd) || (!op.out.data && !op.yq)) return QMM_ERR_ARG;
+    if (!op.kv_len || (op.max_kv > 0 && !op.pages)) return QMM_ERR_ARG;
+    const auto off = [](const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; };
+    if (off(op.kv_len, 4) || off(op.q_start, 4) || off(op.pages, 4) || off(op.yd, 2)) return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+bool prepared(int NB, bool f32, int optin) {
+    static std::mutex mu;
+    static bool done[64][2][8];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    bool& d = done[dev][f32][NB - 1];
+    if (!d) d = f32 ? attn_prepare_f32(NB, optin) : attn_prepare_16(NB, optin);
+    return d;
+}
+
+template <int NB>
+void join(const AttnArgs& a, const Plan& p, cudaStream_t st) {
+    attn::attn_join_kernel<NB><<<dim3(p.ctas, std::max(1, p.block_rows / 8)), 128, 0, st>>>(a, p.block_rows);
+}
+
+}  // namespace
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" {
+
+qmm_status qmm_attn_workspace_size(const qmm_attn_op* op, size_t* bytes) {
+    if (!op || !bytes) return QMM_ERR_ARG;
+    if (qmm_status s = check(*op, false)) return s;
+    int sms = DEFAULT_SMS, optin = 0;
+    device_facts(&sms, &optin);
+    const Plan p = plan_of(*op, sms);
+    *bytes = op->n_seqs && op->T && op->max_q ? p.meta_bytes + p.part_bytes : 0;
+    return QMM_OK;
+}
+
+qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
+    if (!op) return QMM_ERR_ARG;
+    const bool empty = op->n_seqs == 0 || op->T == 0 || op->max_q == 0;
+    if (qmm_status s = check(*op, !empty)) return s;
+    if (empty) return QMM_OK;
+    int sms = 0, optin = 0;
+    const bool device = device_facts(&sms, &optin);
+    const Plan p = plan_of(*op, device ? sms : DEFAULT_SMS);
+    const size_t need = p.meta_bytes + p.part_bytes;
+    if (need && (!op->workspace || op->workspace_bytes < need || reinterpret_cast<uintptr_t>(op->workspace) % 16))
+        return QMM_ERR_WORKSPACE;
+    if (!device) return QMM_ERR_DEVICE;
+    AttnArgs a = {};
+    a.cache = op->cache.data;
+    a.q = kernel_heads(op->q);
+    a.out = kernel_heads(op->out);
+    a.yq = op->yq;
+    a.yd = op->yd;
+    a.q_start = op->q_start;
+    a.kv_len = op->kv_len;
+    a.pages = op->pages;
+    a.pages_stride = op->pages_stride;
+    a.T = op->T;
+    a.n_pages = op->cache.n_pages;
+    a.page_groups = op->cache.page_size / GROUP;
+    a.kv_heads = op->cache.n_heads;
+    a.group = op->q.n_heads / op->cache.n_heads;
+    a.n_seqs = op->n_seqs;
+    a.max_q = op->max_q;
+    a.max_kv = op->max_kv;
+    a.causal = op->causal != 0;
+    a.window = std::min(op->window, 1 << 29);
+    a.scale_log2 = op->scale * 1.4426950408889634f;
+    a.row_warps = p.row_warps;
+    a.blocks = p.blocks;
+    a.split = p.ctas != 0;
+    a.meta = static_cast<AttnMeta*>(op->workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
+    a.err = device_error_word();
+    const int NB = op->cache.head_dim / QK;
+    const bool f32 = op->q.dtype == QMM_F32;
+    if (!prepared(NB, f32, optin)) return QMM_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned grid = p.ctas ? (unsigned)p.ctas : (unsigned)p.items;
+    const cudaError_t e = f32 ? attn_launch_f32(NB, a, grid, p.smem, st) : attn_launch_16(NB, a, grid, p.smem, st);
+    if (e != cudaSuccess) return QMM_ERR_CUDA;
+    if (p.ctas) {
+        static constexpr void (*JOIN[8])(const AttnArgs&, const Plan&, cudaStream_t) = {
+            join<1>, join<2>, join<3>, join<4>, join<5>, join<6>, join<7>, join<8>};
+        JOIN[NB - 1](a, p, st);
+    }
+    return cudaGetLastError() == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -20,6 +20,7 @@ constexpr unsigned FULL = 0xffffffffu;
 // Device error word bits (read back by qmm_last_device_error).
 constexpr int ERR_BAD_EXPERT = 1;
 constexpr int ERR_TIMEOUT = 2;
+constexpr int ERR_BAD_INDEX = 4;
 
 // ---------------------------------------------------------------- PTX helpers
 // Streaming 16-byte load of weight bytes: read-only path, no L1 allocation

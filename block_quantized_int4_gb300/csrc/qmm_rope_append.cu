@@ -1,0 +1,545 @@
+// qmm_rope_append.cu -- what happens to q, k and v between the QKV product
+// and the attention: RMSNorm of each head, rotary positions, and the write
+// of k and v into the paged Q4_0 cache (qmm_rope_heads, qmm_kv_append_q4_0),
+// the set-up of a rotary table (qmm_rope_table) and the values of cached
+// tokens (qmm_kv_read_q4_0).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "qmm.h"
+#include "qmm_heads.cuh"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+// ---------------------------------------------------------------- rotary table
+struct Freqs {
+    double f[MAX_HEAD / 2];
+    double mag;
+};
+
+// Set-up: one thread an angle, in 64 bits.
+__global__ void rope_table_kernel(float2* table, int64_t n, int half, const __grid_constant__ Freqs fr) {
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t p = i / half;
+        double s, c;
+        sincos((double)p * fr.f[i - p * half], &s, &c);
+        table[i] = make_float2((float)(fr.mag * c), (float)(fr.mag * s));
+    }
+}
+
+// ---------------------------------------------------------------- pairs of fp32
+// A value as an unevaluated sum h + l of two fp32 (|l| <= half a step of h):
+// about 47 bits from error-free sums and products (Dekker 1971, Knuth's
+// two-sum), in a few fp32 operations where GB300's fp64 rate is 1/64 of fp32.
+// The _rn intrinsics keep the compiler from contracting them.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two fast_two_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_sum(a.h, b.h);
+    return fast_two_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    const Two p = two_prod(a.h, b.h);
+    return fast_two_sum(p.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, p.l)));
+}
+__device__ __forceinline__ Two mul(Two a, float b) {
+    const Two p = two_prod(a.h, b);
+    return fast_two_sum(p.h, __fmaf_rn(a.l, b, p.l));
+}
+
+// 1 / sqrt(sum / D + eps): rsqrtf's 22 bits and one step of the series
+// (1 - e)^(-1/2) = 1 + e/2 + 3 e^2 / 8, e = 1 - m r^2 (about 2^-22).
+__device__ __forceinline__ Two rms_inverse(Two sum, int D, float eps) {
+    const float d = (float)D, q0 = __fdiv_rn(sum.h, d);
+    const float rest = __fadd_rn(__fmaf_rn(-q0, d, sum.h), sum.l);
+    const Two m = add(fast_two_sum(q0, __fdiv_rn(rest, d)), Two{eps, 0.f});
+    const float r = rsqrtf(m.h);
+    const Two p = mul(m, two_prod(r, r));
+    const float e = __fsub_rn(__fsub_rn(1.f, p.h), p.l);
+    return fast_two_sum(r, __fmul_rn(r, __fmul_rn(e, __fmaf_rn(0.375f, e, 0.5f))));
+}
+
+// ---------------------------------------------------------------- the kernel
+enum { GROUP_Q = 0, GROUP_K = 1, GROUP_V = 2 };
+
+struct HeadsArgs {
+    Heads in[3];  // q, k, v
+    Heads out;    // of q
+    int heads[3], groups[3];  // heads, and warps a token for them (0: none)
+    const float* norm[2];     // of q, k
+    const float2* table;
+    const int* pos;
+    const int64_t* slots;
+    uint8_t* cache;
+    int64_t n_slots, n_pos, warps;  // warps: T * (sum of groups)
+    int D, lanes, n_rot, pairs, page_size;
+    int table_wide;
+    float eps;
+    int* err;
+};
+
+// The element of logical place s of a head: pairs of the rotation side by
+// side, then the values that pass.
+__device__ __forceinline__ int element_of(int s, int n_rot, int pairs) {
+    return pairs || s >= n_rot ? s : (s >> 1) + (s & 1) * (n_rot >> 1);
+}
+
+// A lane holds eight logical places (4 whole pairs), a power of two of
+// `lanes` lanes a head, 32 / lanes heads a warp: norm and rotation stay in
+// registers and sums cost log2(lanes) shuffles.  With halves of n_rot % 8 ==
+// 0 the eight are two runs of four elements, otherwise one run of eight.
+__device__ __forceinline__ void load_places(const Heads& h, int64_t at, int s0, int n_rot, int pairs, float* x) {
+    if (pairs || n_rot == 0 || (s0 >= n_rot && n_rot % 8 == 0)) {
+        loadn<8>(h.data, at + s0, h.dtype, h.wide, x);
+    } else if (n_rot % 8 == 0) {
+        float a[4], b[4];
+        loadn<4>(h.data, at + s0 / 2, h.dtype, h.wide, a);
+        loadn<4>(h.data, at + s0 / 2 + n_rot / 2, h.dtype, h.wide, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[2 * j] = a[j], x[2 * j + 1] = b[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = load1(h.data, at + element_of(s0 + j, n_rot, pairs), h.dtype);
+    }
+}
+
+__device__ __forceinline__ void store_places(const Heads& h, int64_t at, int s0, int n_rot, int pairs,
+                                             const float* x) {
+    if (pairs || n_rot == 0 || (s0 >= n_rot && n_rot % 8 == 0)) {
+        storen<8>(h.data, at + s0, h.dtype, h.wide, x);
+    } else if (n_rot % 8 == 0) {
+        const float a[4] = {x[0], x[2], x[4], x[6]}, b[4] = {x[1], x[3], x[5], x[7]};
+        storen<4>(h.data, at + s0 / 2, h.dtype, h.wide, a);
+        storen<4>(h.data, at + s0 / 2 + n_rot / 2, h.dtype, h.wide, b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) store1(h.data, at + element_of(s0 + j, n_rot, pairs), x[j], h.dtype);
+    }
+}
+
+// cos and sin of the lane's four pairs, where they are rotated.
+__device__ __forceinline__ void load_turns(const HeadsArgs& a, int64_t p, int s0, float2* cs) {
+    const float2* row = a.table + p * (a.n_rot / 2);
+    if (a.table_wide && s0 + 8 <= a.n_rot) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(row + s0 / 2));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(row + s0 / 2 + 2));
+        cs[0] = make_float2(u.x, u.y), cs[1] = make_float2(u.z, u.w);
+        cs[2] = make_float2(v.x, v.y), cs[3] = make_float2(v.z, v.w);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (s0 + 2 * j < a.n_rot) cs[j] = __ldg(row + s0 / 2 + j);
+    }
+}
+
+constexpr int HEAD_WARPS = 8;
+
+// One warp: 32 / lanes heads of one token, of q, k or v.
+__global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_constant__ HeadsArgs a) {
+    __shared__ float stage[HEAD_WARPS][32 * 8 + 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t id = blockIdx.x * (int64_t)HEAD_WARPS + warp;
+    if (id >= a.warps) return;
+    const int per_token = a.groups[0] + a.groups[1] + a.groups[2];
+    const int64_t t = id / per_token;
+    int i = (int)(id - t * per_token), kind = GROUP_Q;
+    while (i >= a.groups[kind]) i -= a.groups[kind++];
+    const Heads& in = a.in[kind];
+    const int sub = lane / a.lanes, u = lane - sub * a.lanes;
+    const int head = i * (32 / a.lanes) + sub, s0 = u * 8;
+    const bool live = head < a.heads[kind] && s0 < a.D;
+    const int n_rot = kind == GROUP_V ? 0 : a.n_rot;
+
+    float x[8] = {};
+    if (live) load_places(in, t * in.ts + head * in.hs, s0, n_rot, a.pairs, x);
+    float2 cs[4];
+    if (a.n_rot) {
+        const int p = a.pos[t];
+        if (p < 0 || p >= a.n_pos) {  // the whole warp: one token
+            if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
+            return;
+        }
+        if (kind != GROUP_V) load_turns(a, p, s0, cs);
+    }
+    int64_t slot = 0;
+    if (kind != GROUP_Q) {
+        slot = a.slots[t];
+        if (slot < 0) return;
+        if (slot >= a.n_slots) {
+            if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
+            return;
+        }
+    }
+
+    if (kind == GROUP_Q) {  // fp32, rounded once to the output's type
+        if (a.norm[GROUP_Q]) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+            for (int o = a.lanes / 2; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+            const float r = 1.f / sqrtf(s / a.D + a.eps);
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * r * a.norm[GROUP_Q][element_of(s0 + j, n_rot, a.pairs)];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (s0 + 2 * j < n_rot) {
+                const float p = x[2 * j], q = x[2 * j + 1];
+                x[2 * j] = p * cs[j].x - q * cs[j].y;
+                x[2 * j + 1] = q * cs[j].x + p * cs[j].y;
+            }
+        }
+        if (live) store_places(a.out, t * a.out.ts + head * a.out.hs, s0, n_rot, a.pairs, x);
+        return;
+    }
+
+    if (kind == GROUP_K) {  // pairs of fp32 up to the one rounding that the codes depend on
+        Two r = {1.f, 0.f};
+        const bool norm = a.norm[GROUP_K] != nullptr;
+        if (norm) {
+            Two s = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = add(s, two_prod(x[j], x[j]));
+            for (int o = a.lanes / 2; o; o >>= 1)
+                s = add(s, Two{__shfl_xor_sync(FULL, s.h, o), __shfl_xor_sync(FULL, s.l, o)});
+            r = rms_inverse(s, a.D, a.eps);
+        }
+        float* st = stage[warp] + sub * a.D;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Two p = {x[2 * j], 0.f}, q = {x[2 * j + 1], 0.f};
+            const int ep = element_of(s0 + 2 * j, n_rot, a.pairs), eq = element_of(s0 + 2 * j + 1, n_rot, a.pairs);
+            if (norm && live) {
+                p = mul(r, two_prod(p.h, a.norm[GROUP_K][ep]));
+                q = mul(r, two_prod(q.h, a.norm[GROUP_K][eq]));
+            }
+            if (s0 + 2 * j < n_rot) {
+                const Two pc = mul(p, cs[j].x), qs = mul(q, -cs[j].y), qc = mul(q, cs[j].x), ps = mul(p, cs[j].y);
+                p = add(pc, qs);
+                q = add(qc, ps);
+            }
+            if (live) {
+                st[ep] = __fadd_rn(p.h, p.l);
+                st[eq] = __fadd_rn(q.h, q.l);
+            }
+        }
+        __syncwarp();
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = st[s0 + j];
+        }
+    }
+
+    // Q4_0 of a block of 32 on four lanes: lane r holds values 8r .. 8r + 7.
+    const int r = u & 3;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
+    const float d = __fdiv_rn(m, 7.0f);
+    unsigned code[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float q = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(x[j], d)), -8.f), 7.f) : 0.f;
+        code[j] = (unsigned)((int)q + 8);
+    }
+    const int rec = record_bytes(a.D), NB = a.D / QK;
+    const int64_t page = slot / a.page_size;
+    const int in_page = (int)(slot - page * a.page_size), tok = in_page & 31;
+    uint8_t* base = a.cache + ((page * a.heads[kind] + head) * (a.page_size / GROUP) + in_page / GROUP) * rec;
+    const int blk = u >> 2;
+    if (kind == GROUP_K) {
+        // low nibbles (values 0..15) on lanes 0, 1; high ones on lanes 2, 3
+        unsigned w0 = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+        unsigned w1 = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+        if (r >= 2) w0 <<= 4, w1 <<= 4;
+        w0 |= __shfl_xor_sync(FULL, w0, 2);
+        w1 |= __shfl_xor_sync(FULL, w1, 2);
+        if (live) {
+            const int word = 2 * (r & 1) + (r >> 1);
+            *reinterpret_cast<unsigned*>(base + blk * 512 + k_word_at(tok, word)) = r >> 1 ? w1 : w0;
+            if (r == 0)
+                *reinterpret_cast<unsigned short*>(base + NB * 1024 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
+        }
+    } else {
+        // lane r's values 8r + e are nibble r of unit e
+        unsigned w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = (code[2 * j] | code[2 * j + 1] << 16) << (4 * r);
+            w[j] |= __shfl_xor_sync(FULL, w[j], 1);
+            w[j] |= __shfl_xor_sync(FULL, w[j], 2);
+        }
+        if (live) {
+            const unsigned v = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
+            uint8_t* vb = base + NB * 512 + blk * 512;
+            *reinterpret_cast<unsigned short*>(vb + v_unit_at(tok, 2 * r)) = (unsigned short)(v & 0xffff);
+            *reinterpret_cast<unsigned short*>(vb + v_unit_at(tok, 2 * r + 1)) = (unsigned short)(v >> 16);
+            if (r == 0)
+                *reinterpret_cast<unsigned short*>(base + NB * 1088 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
+        }
+    }
+}
+
+struct ReadArgs {
+    Heads out[2];  // k, v (data may be null)
+    const uint8_t* cache;
+    const int64_t* slots;
+    int64_t n_slots, warps;
+    int D, lanes, heads, page_size;
+    int* err;
+};
+
+// The values of cached tokens: a lane holds eight values of a head, as above.
+__global__ void __launch_bounds__(HEAD_WARPS * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t id = blockIdx.x * (int64_t)HEAD_WARPS + (threadIdx.x >> 5);
+    if (id >= a.warps) return;
+    const int per = (a.heads + 32 / a.lanes - 1) / (32 / a.lanes);
+    const int64_t t = id / per;
+    const int sub = lane / a.lanes, u = lane - sub * a.lanes;
+    const int head = (int)(id - t * per) * (32 / a.lanes) + sub, s0 = u * 8;
+    if (head >= a.heads || s0 >= a.D) return;
+    const int64_t slot = a.slots[t];
+    if (slot >= a.n_slots) {
+        if (u == 0) atomicOr(a.err, ERR_BAD_INDEX);
+        return;
+    }
+    float x[8] = {}, y[8] = {};
+    if (slot >= 0) {
+        const int NB = a.D / QK, blk = u >> 2, r = u & 3;
+        const int64_t page = slot / a.page_size;
+        const int in_page = (int)(slot - page * a.page_size), tok = in_page & 31;
+        const uint8_t* base = a.cache + ((page * a.heads + head) * (a.page_size / GROUP) + in_page / GROUP) *
+                                            (int64_t)record_bytes(a.D);
+        if (a.out[0].data) {
+            const float d = f16_bits_to_f32(
+                *reinterpret_cast<const unsigned short*>(base + NB * 1024 + blk * 64 + scale_at(tok)));
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const unsigned v =
+                    *reinterpret_cast<const unsigned*>(base + blk * 512 + k_word_at(tok, 2 * (r & 1) + w));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * w + j] = d * (float)((int)(v >> (8 * j + 4 * (r >> 1)) & 15) - 8);
+            }
+        }
+        if (a.out[1].data) {
+            const float d = f16_bits_to_f32(
+                *reinterpret_cast<const unsigned short*>(base + NB * 1088 + blk * 64 + scale_at(tok)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned v =
+                    *reinterpret_cast<const unsigned short*>(base + NB * 512 + blk * 512 + v_unit_at(tok, e));
+                y[e] = d * (float)((int)(v >> (4 * r) & 15) - 8);
+            }
+        }
+    }
+    if (a.out[0].data)
+        storen<8>(a.out[0].data, t * a.out[0].ts + head * a.out[0].hs + s0, a.out[0].dtype, a.out[0].wide, x);
+    if (a.out[1].data)
+        storen<8>(a.out[1].data, t * a.out[1].ts + head * a.out[1].hs + s0, a.out[1].dtype, a.out[1].wide, y);
+}
+
+// ---------------------------------------------------------------- host side
+qmm_status status_of_launch() { return cudaGetLastError() == cudaSuccess ? QMM_OK : QMM_ERR_CUDA; }
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+qmm_status check_rope(const qmm_rope& r, int D, const int32_t* pos) {
+    if (r.n_rot < 0 || r.n_pos < 0) return QMM_ERR_ARG;
+    if (r.n_rot % 2 || r.n_rot > D) return QMM_ERR_SHAPE;
+    if (r.n_rot == 0) return QMM_OK;
+    if (!r.table || !pos) return QMM_ERR_ARG;
+    if (misaligned(r.table, 8) || misaligned(pos, 4)) return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+int lanes_of(int D) {
+    int n = 4;
+    while (n * 8 < D) n *= 2;
+    return n;
+}
+
+int groups_of(int heads, int lanes) { return (heads + 32 / lanes - 1) / (32 / lanes); }
+
+void set_rope(HeadsArgs& a, const qmm_rope& r, const int32_t* pos) {
+    a.table = reinterpret_cast<const float2*>(r.table);
+    a.table_wide = r.n_rot % 8 == 0 && !misaligned(r.table, 16);
+    a.n_pos = r.n_pos;
+    a.n_rot = r.n_rot;
+    a.pairs = r.pairs != 0;
+    a.pos = pos;
+}
+
+constexpr int64_t MAX_BLOCKS = (int64_t(1) << 31) - 1;
+
+qmm_status launch_heads(const HeadsArgs& a, void* stream) {
+    const int64_t blocks = (a.warps + HEAD_WARPS - 1) / HEAD_WARPS;
+    if (blocks > MAX_BLOCKS) return QMM_ERR_SHAPE;
+    heads_kernel<<<(unsigned)blocks, HEAD_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return status_of_launch();
+}
+
+}  // namespace
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" {
+
+qmm_status qmm_rope_table(float* table, int64_t n_pos, int32_t n_rot, double base, int32_t scaling, double factor,
+                          double orig_len, double beta_fast, double beta_slow, void* stream) {
+    if (n_pos < 0 || scaling < QMM_ROPE_PLAIN || scaling > QMM_ROPE_RAMP || !(base > 1.0) || !std::isfinite(base))
+        return QMM_ERR_ARG;
+    if (scaling != QMM_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor))) return QMM_ERR_ARG;
+    if (scaling == QMM_ROPE_RAMP && !(orig_len > 0 && beta_slow > 0 && beta_fast >= beta_slow)) return QMM_ERR_ARG;
+    if (n_rot < 2 || n_rot % 2 || n_rot > MAX_HEAD || n_pos > (int64_t(1) << 31)) return QMM_ERR_SHAPE;
+    if (n_pos == 0) return QMM_OK;
+    if (!table) return QMM_ERR_ARG;
+    if (misaligned(table, 8)) return QMM_ERR_ALIGN;
+    int sms = 0, optin = 0;
+    if (!device_facts(&sms, &optin)) return QMM_ERR_DEVICE;
+    Freqs fr = {};
+    const int half = n_rot / 2;
+    const double pi = 3.14159265358979323846;
+    const auto place = [&](double turns) { return n_rot * std::log(orig_len / (2 * pi * turns)) / (2 * std::log(base)); };
+    const double lo = scaling == QMM_ROPE_RAMP ? std::max(0.0, std::floor(place(beta_fast))) : 0;
+    const double hi = scaling == QMM_ROPE_RAMP ? std::min(half - 1.0, std::ceil(place(beta_slow))) : 0;
+    for (int i = 0; i < half; ++i) {
+        const double f = std::pow(base, -2.0 * i / n_rot);
+        const double r = scaling == QMM_ROPE_LINEAR ? 1.0
+                         : scaling == QMM_ROPE_RAMP
+                             ? std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)))
+                             : 0.0;
+        fr.f[i] = r > 0 ? f * (1 - r) + f / factor * r : f;
+    }
+    fr.mag = scaling == QMM_ROPE_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    const int64_t n = n_pos * half;
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 16 * (int64_t)sms);
+    rope_table_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(reinterpret_cast<float2*>(table), n, half,
+                                                                          fr);
+    return status_of_launch();
+}
+
+qmm_status qmm_rope_heads(const qmm_rope_op* op, void* stream) {
+    if (!op || op->T < 0) return QMM_ERR_ARG;
+    if (!valid_head_dim(op->head_dim)) return QMM_ERR_SHAPE;
+    if (op->T == 0) return QMM_OK;
+    if (qmm_status s = check_heads(op->x, 0)) return s;
+    if (qmm_status s = check_output(op->y, op->x.n_heads, op->T, op->head_dim)) return s;
+    if (qmm_status s = check_rope(op->rope, op->head_dim, op->pos)) return s;
+    if (misaligned(op->norm_w, 4)) return QMM_ERR_ALIGN;
+    int* err = device_error_word();
+    if (!err) return QMM_ERR_DEVICE;
+    HeadsArgs a = {};
+    a.D = op->head_dim;
+    a.lanes = lanes_of(a.D);
+    a.in[GROUP_Q] = kernel_heads(op->x);
+    a.out = kernel_heads(op->y);
+    a.heads[GROUP_Q] = op->x.n_heads;
+    a.groups[GROUP_Q] = groups_of(op->x.n_heads, a.lanes);
+    a.norm[GROUP_Q] = op->norm_w;
+    a.eps = op->norm_eps;
+    a.err = err;
+    set_rope(a, op->rope, op->pos);
+    a.warps = op->T * a.groups[GROUP_Q];
+    return launch_heads(a, stream);
+}
+
+qmm_status qmm_kv_cache_bytes(const qmm_kv_cache* cache, size_t* bytes) {
+    if (!cache || !bytes) return QMM_ERR_ARG;
+    if (qmm_status s = check_cache(*cache, false)) return s;
+    *bytes = (size_t)cache->n_pages * cache->n_heads * (cache->page_size / GROUP) * record_bytes(cache->head_dim);
+    return QMM_OK;
+}
+
+qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
+    if (!op || op->T < 0) return QMM_ERR_ARG;
+    if (qmm_status s = check_cache(op->cache, op->T > 0)) return s;
+    if (op->T == 0) return QMM_OK;
+    const int D = op->cache.head_dim;
+    if (qmm_status s = check_heads(op->k, op->cache.n_heads)) return s;
+    if (qmm_status s = check_heads(op->v, op->cache.n_heads)) return s;
+    if (op->q.data) {
+        if (qmm_status s = check_heads(op->q, 0)) return s;
+        if (qmm_status s = check_output(op->q_out, op->q.n_heads, op->T, D)) return s;
+    }
+    if (qmm_status s = check_rope(op->rope, D, op->pos)) return s;
+    if (!op->slots) return QMM_ERR_ARG;
+    if (misaligned(op->slots, 8) || misaligned(op->k_norm, 4) || misaligned(op->q_norm, 4)) return QMM_ERR_ALIGN;
+    int* err = device_error_word();
+    if (!err) return QMM_ERR_DEVICE;
+    HeadsArgs a = {};
+    a.D = D;
+    a.lanes = lanes_of(D);
+    const qmm_heads* in[3] = {&op->q, &op->k, &op->v};
+    for (int g = op->q.data ? GROUP_Q : GROUP_K; g <= GROUP_V; ++g) {
+        a.in[g] = kernel_heads(*in[g]);
+        a.heads[g] = in[g]->n_heads;
+        a.groups[g] = groups_of(in[g]->n_heads, a.lanes);
+    }
+    if (op->q.data) a.out = kernel_heads(op->q_out);
+    a.norm[GROUP_Q] = op->q_norm;
+    a.norm[GROUP_K] = op->k_norm;
+    a.eps = op->norm_eps;
+    a.err = err;
+    set_rope(a, op->rope, op->pos);
+    a.slots = op->slots;
+    a.cache = op->cache.data;
+    a.page_size = op->cache.page_size;
+    a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
+    a.warps = op->T * (a.groups[0] + a.groups[1] + a.groups[2]);
+    return launch_heads(a, stream);
+}
+
+qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream) {
+    if (!op || op->T < 0) return QMM_ERR_ARG;
+    if (qmm_status s = check_cache(op->cache, op->T > 0)) return s;
+    if (op->T == 0 || (!op->k.data && !op->v.data)) return QMM_OK;
+    if (op->k.data)
+        if (qmm_status s = check_output(op->k, op->cache.n_heads, op->T, op->cache.head_dim)) return s;
+    if (op->v.data)
+        if (qmm_status s = check_output(op->v, op->cache.n_heads, op->T, op->cache.head_dim)) return s;
+    if (!op->slots) return QMM_ERR_ARG;
+    if (misaligned(op->slots, 8)) return QMM_ERR_ALIGN;
+    int* err = device_error_word();
+    if (!err) return QMM_ERR_DEVICE;
+    ReadArgs a = {};
+    a.D = op->cache.head_dim;
+    a.lanes = lanes_of(a.D);
+    a.heads = op->cache.n_heads;
+    a.out[0] = kernel_heads(op->k);
+    a.out[1] = kernel_heads(op->v);
+    a.cache = op->cache.data;
+    a.slots = op->slots;
+    a.page_size = op->cache.page_size;
+    a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
+    a.err = err;
+    a.warps = op->T * groups_of(a.heads, a.lanes);
+    const int64_t blocks = (a.warps + HEAD_WARPS - 1) / HEAD_WARPS;
+    if (blocks > MAX_BLOCKS) return QMM_ERR_SHAPE;
+    kv_read_kernel<<<(unsigned)blocks, HEAD_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return status_of_launch();
+}
+
+}  // extern "C"

@@ -23,7 +23,7 @@ QK = 32
 
 STATUS = {0: "QMM_OK", 1: "QMM_ERR_ARG", 2: "QMM_ERR_SHAPE", 3: "QMM_ERR_ALIGN", 4: "QMM_ERR_DEVICE",
           5: "QMM_ERR_CUDA", 6: "QMM_ERR_TIMEOUT", 7: "QMM_ERR_BAD_EXPERT_ID", 8: "QMM_ERR_WORKSPACE",
-          9: "QMM_ERR_SCRATCH_LIMIT"}
+          9: "QMM_ERR_SCRATCH_LIMIT", 10: "QMM_ERR_BAD_INDEX"}
 
 
 class QmmError(RuntimeError):
@@ -39,6 +39,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 _P, _I64, _I32, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_size_t
+_F64 = ctypes.c_double
 
 class GemvOp(ctypes.Structure):
     """qmm_gemv_op of include/qmm.h (one batch-1 GEMV of a decode step)."""
@@ -53,6 +54,53 @@ class StorePlane(ctypes.Structure):
     """qmm_store_plane of include/qmm.h (one plane of every expert)."""
     _fields_ = [("host", ctypes.c_void_p), ("host_stride", ctypes.c_int64), ("dev", ctypes.c_void_p),
                 ("bytes", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    """qmm_heads of include/qmm.h (heads of T tokens, any strides)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """qmm_rope of include/qmm.h (rotary table and pair layout)."""
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("n_rot", ctypes.c_int32),
+                ("pairs", ctypes.c_int32)]
+
+
+class RopeOp(ctypes.Structure):
+    """qmm_rope_op of include/qmm.h."""
+    _fields_ = [("x", Heads), ("y", Heads), ("rope", Rope), ("pos", ctypes.c_void_p), ("norm_w", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("head_dim", ctypes.c_int32), ("norm_eps", ctypes.c_float)]
+
+
+class KvCache(ctypes.Structure):
+    """qmm_kv_cache of include/qmm.h (paged Q4_0 keys and values)."""
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KvAppendOp(ctypes.Structure):
+    """qmm_kv_append_op of include/qmm.h."""
+    _fields_ = [("cache", KvCache), ("k", Heads), ("v", Heads), ("q", Heads), ("q_out", Heads), ("rope", Rope),
+                ("slots", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("T", ctypes.c_int64), ("norm_eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class KvReadOp(ctypes.Structure):
+    """qmm_kv_read_op of include/qmm.h."""
+    _fields_ = [("cache", KvCache), ("k", Heads), ("v", Heads), ("slots", ctypes.c_void_p), ("T", ctypes.c_int64)]
+
+
+class AttnOp(ctypes.Structure):
+    """qmm_attn_op of include/qmm.h."""
+    _fields_ = [("cache", KvCache), ("q", Heads), ("out", Heads), ("yq", ctypes.c_void_p), ("yd", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("T", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 # name -> argtypes (the trailing stream is a void*)
@@ -95,6 +143,13 @@ SIGNATURES = {
     "qmm_moe_gemv_gate_up": [_P, _P, _I32, _I64, _I64, _I32, _I32, _P, _P, _P, _INT, _P, _P, _SZ, _P],
     "qmm_moe_group_ids": [_P, _I32, _I32, _I32, _P, _SZ, _P],
     "qmm_moe_gemv_pregrouped_f32": [_P, _P, _I32, _I64, _I64, _I32, _I32, _P, _INT, _P, _P, _SZ, _P],
+    "qmm_rope_table": [_P, _I64, _I32, _F64, _I32, _F64, _F64, _F64, _F64, _P],
+    "qmm_rope_heads": [ctypes.POINTER(RopeOp), _P],
+    "qmm_kv_cache_bytes": [ctypes.POINTER(KvCache), ctypes.POINTER(_SZ)],
+    "qmm_kv_append_q4_0": [ctypes.POINTER(KvAppendOp), _P],
+    "qmm_kv_read_q4_0": [ctypes.POINTER(KvReadOp), _P],
+    "qmm_attn_workspace_size": [ctypes.POINTER(AttnOp), ctypes.POINTER(_SZ)],
+    "qmm_attn_q4_0": [ctypes.POINTER(AttnOp), _P],
     "qmm_last_device_error": [_P],
 }
 for _name, _args in SIGNATURES.items():
@@ -395,6 +450,159 @@ def qmm_moe_combine(z, gates, T, k, N, y, stream=None):
     _check(_lib.qmm_moe_combine(_ptr(z), _ptr(gates), T, k, N, _ptr(y), _stream(stream)), "qmm_moe_combine")
 
 
+# ------------------------------------------------------------------ attention over a 4-bit paged cache
+ROPE_PLAIN, ROPE_LINEAR, ROPE_RAMP = 0, 1, 2
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def heads(t):
+    """qmm_heads of a tensor [T][n_heads][head_dim] whose last dimension is contiguous (None: no heads)."""
+    if t is None:
+        return Heads()
+    if t.dim() != 3 or t.dtype not in _DTYPES or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"heads: [T][n_heads][head_dim] of fp32, fp16 or bf16 with contiguous values, got "
+                         f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1], _DTYPES[t.dtype])
+
+
+def rope(table, pairs=False):
+    """qmm_rope of a table [n_pos][n_rot / 2][2] (None: no rotation)."""
+    if table is None:
+        return Rope()
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("rope: a contiguous fp32 table [n_pos][n_rot / 2][2]")
+    r = Rope(table.data_ptr(), table.shape[0], 2 * table.shape[1], int(bool(pairs)))
+    r._keep = table
+    return r
+
+
+def kv_cache(data, page_size):
+    """qmm_kv_cache of a uint8 tensor [n_pages][n_heads][page_size / 32][36 * head_dim]."""
+    if (data.dim() != 4 or data.dtype != torch.uint8 or not data.is_contiguous() or data.shape[3] % 36
+            or data.shape[2] * 32 != page_size):
+        raise ValueError("kv_cache: a contiguous uint8 tensor [n_pages][n_heads][page_size / 32][36 * head_dim]")
+    c = KvCache(data.data_ptr(), data.shape[0], page_size, data.shape[1], data.shape[3] // 36)
+    c._keep = data
+    return c
+
+
+def _plain(t, dtype, shape, what):
+    """t, or ValueError: the index and norm tensors of the ops are contiguous."""
+    if t is not None and (t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _same(a, b, what):
+    if tuple(a.shape) != tuple(b.shape):
+        raise ValueError(f"{what}: {tuple(a.shape)} and {tuple(b.shape)} differ")
+
+
+def rope_op(x, y, pos, rope, norm_w=None, norm_eps=1e-5):
+    """A qmm_rope_op; x, y [T][n_heads][head_dim].  The op holds its tensors."""
+    T, _, D = x.shape
+    _same(x, y, "rope_op: x and y")
+    op = RopeOp(heads(x), heads(y), rope, _ptr(_plain(pos, torch.int32, (T,), "pos")),
+                _ptr(_plain(norm_w, torch.float32, (D,), "norm_w")), T, D, norm_eps)
+    op._keep = (x, y, pos, rope, norm_w)
+    return op
+
+
+def kv_append_op(cache, k, v, slots, pos=None, rope=None, q=None, q_out=None, k_norm=None, q_norm=None,
+                 norm_eps=1e-5):
+    """A qmm_kv_append_op; k, v [T][cache.n_heads][head_dim], q, q_out [T][n_heads][head_dim]."""
+    T, D = k.shape[0], cache.head_dim
+    _same(k, v, "kv_append_op: k and v")
+    if k.shape[2] != D or (q is None) != (q_out is None) or (q is not None and (q.shape[0] != T or q.shape[2] != D)):
+        raise ValueError("kv_append_op: k, v and q have the cache's head_dim and one T, q and q_out go together")
+    if q is not None:
+        _same(q, q_out, "kv_append_op: q and q_out")
+    op = KvAppendOp(cache, heads(k), heads(v), heads(q), heads(q_out), Rope() if rope is None else rope,
+                    _ptr(_plain(slots, torch.int64, (T,), "slots")), _ptr(_plain(pos, torch.int32, (T,), "pos")),
+                    _ptr(_plain(k_norm, torch.float32, (D,), "k_norm")),
+                    _ptr(_plain(q_norm, torch.float32, (D,), "q_norm")), T, norm_eps, 0)
+    op._keep = (cache, k, v, slots, pos, rope, q, q_out, k_norm, q_norm)
+    return op
+
+
+def kv_read_op(cache, slots, k=None, v=None):
+    """A qmm_kv_read_op; k, v [T][cache.n_heads][head_dim] or None."""
+    T = slots.shape[0]
+    for t in (k, v):
+        if t is not None and tuple(t.shape) != (T, cache.n_heads, cache.head_dim):
+            raise ValueError("kv_read_op: k and v are [T][cache.n_heads][head_dim]")
+    op = KvReadOp(cache, heads(k), heads(v), _ptr(_plain(slots, torch.int64, (T,), "slots")), T)
+    op._keep = (cache, slots, k, v)
+    return op
+
+
+def attn_op(cache, q, pages, kv_len, out=None, yq=None, yd=None, q_start=None, max_q=1, max_kv=None, scale=None,
+            causal=True, window=0, workspace=None):
+    """A qmm_attn_op; q, out [T][n_heads][head_dim], pages int32 [n_seqs][...], kv_len int32 [n_seqs].
+    max_kv defaults to what the page table can hold, scale to head_dim ** -0.5; without a
+    workspace one is allocated (the op holds it)."""
+    T, H, D = q.shape
+    B = kv_len.shape[0]
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != B or (pages.shape[1] > 1 and
+                                                                                   pages.stride(1) != 1):
+        raise ValueError("attn_op: pages is int32 [n_seqs][...] with contiguous rows")
+    if D != cache.head_dim:
+        raise ValueError("attn_op: q has the cache's head_dim")
+    if out is not None:
+        _same(q, out, "attn_op: q and out")
+    if max_kv is None:
+        max_kv = pages.shape[1] * cache.page_size
+    if -(-max_kv // cache.page_size) > pages.shape[1]:
+        raise ValueError("attn_op: the page table holds less than max_kv tokens")
+    op = AttnOp(cache, heads(q), heads(out), _ptr(_plain(yq, torch.int8, (T, H * D), "yq")),
+                _ptr(_plain(yd, torch.int16, (T, H * D // QK), "yd")),
+                _ptr(_plain(q_start, torch.int32, (B + 1,), "q_start")),
+                _ptr(_plain(kv_len, torch.int32, (B,), "kv_len")), pages.data_ptr(),
+                max(pages.stride(0), pages.shape[1]), T, B, max_q, max_kv, int(bool(causal)), window,
+                D ** -0.5 if scale is None else scale, None, 0)
+    n = qmm_attn_workspace_size(op)
+    if workspace is None and n:
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        op.workspace, op.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    op._keep = (cache, q, pages, kv_len, out, yq, yd, q_start, workspace)
+    return op
+
+
+def qmm_rope_table(table, n_pos, n_rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig_len=0.0, beta_fast=32.0,
+                   beta_slow=1.0, stream=None):
+    _check(_lib.qmm_rope_table(_ptr(table), n_pos, n_rot, base, scaling, factor, orig_len, beta_fast, beta_slow,
+                               _stream(stream)), "qmm_rope_table")
+
+
+def qmm_rope_heads(op, stream=None):
+    _check(_lib.qmm_rope_heads(ctypes.byref(op), _stream(stream)), "qmm_rope_heads")
+
+
+def qmm_kv_cache_bytes(cache) -> int:
+    out = _SZ(0)
+    _check(_lib.qmm_kv_cache_bytes(ctypes.byref(cache), ctypes.byref(out)), "qmm_kv_cache_bytes")
+    return out.value
+
+
+def qmm_kv_append_q4_0(op, stream=None):
+    _check(_lib.qmm_kv_append_q4_0(ctypes.byref(op), _stream(stream)), "qmm_kv_append_q4_0")
+
+
+def qmm_kv_read_q4_0(op, stream=None):
+    _check(_lib.qmm_kv_read_q4_0(ctypes.byref(op), _stream(stream)), "qmm_kv_read_q4_0")
+
+
+def qmm_attn_workspace_size(op) -> int:
+    out = _SZ(0)
+    _check(_lib.qmm_attn_workspace_size(ctypes.byref(op), ctypes.byref(out)), "qmm_attn_workspace_size")
+    return out.value
+
+
+def qmm_attn_q4_0(op, stream=None):
+    _check(_lib.qmm_attn_q4_0(ctypes.byref(op), _stream(stream)), "qmm_attn_q4_0")
+
+
 def qmm_last_device_error(stream=None) -> int:
     """Returns the status code (does not raise), after synchronising the stream."""
     return _lib.qmm_last_device_error(_stream(stream))
@@ -432,6 +640,19 @@ def quantize_q8_0(x: torch.Tensor):
     d = torch.empty(M, K // QK, dtype=torch.int16, device=x.device)
     qmm_quantize_q8_0(x, M, K, x.stride(0), q, d)
     return q, d
+
+
+def rope_table(n_pos: int, n_rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+               orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """The rotary table [n_pos][n_rot / 2][2] of qmm_rope_table."""
+    t = torch.empty(n_pos, n_rot // 2, 2, dtype=torch.float32, device=device)
+    qmm_rope_table(t, n_pos, n_rot, base, scaling, factor, orig_len, beta_fast, beta_slow)
+    return t
+
+
+def kv_cache_data(n_pages: int, page_size: int, n_heads: int, head_dim: int, device="cuda"):
+    """An empty cache tensor for kv_cache: uint8 [n_pages][n_heads][page_size / 32][36 * head_dim]."""
+    return torch.empty(n_pages, n_heads, page_size // 32, 36 * head_dim, dtype=torch.uint8, device=device)
 
 
 def gemv(qs, d, xq, xd, out=None):

@@ -66,7 +66,8 @@ typedef enum qmm_status {
     QMM_ERR_TIMEOUT = 6,        /* a bounded device-side wait gave up       */
     QMM_ERR_BAD_EXPERT_ID = 7,  /* an expert id outside [0, E) was skipped  */
     QMM_ERR_WORKSPACE = 8,      /* workspace NULL or smaller than required  */
-    QMM_ERR_SCRATCH_LIMIT = 9   /* larger than the library's fixed scratch  */
+    QMM_ERR_SCRATCH_LIMIT = 9,  /* larger than the library's fixed scratch  */
+    QMM_ERR_BAD_INDEX = 10      /* a position, slot, page or length outside its range */
 } qmm_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -610,12 +611,197 @@ QMM_API qmm_status qmm_moe_gemv_static(const uint8_t* w_qs, const uint16_t* w_d,
                                int x_per_slot, float* y, void* stream);
 
 /* ---------------------------------------------------------------------
+ * Attention over a 4-bit paged cache: rotary heads, cache append, attention
+ * (between the QKV and the O product of a decode step)
+ * ------------------------------------------------------------------- */
+
+/* Element types of the attention entries' activations. */
+typedef enum qmm_dtype { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
+
+/* Heads of T tokens: value e of head h of token t is element
+ * t * token_stride + h * head_stride + e of data, of type dtype.  Any
+ * strides; data aligned to its element (loads are wide where the strides and
+ * the address allow them). */
+typedef struct qmm_heads {
+    void*   data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t n_heads;
+    int32_t dtype;
+} qmm_heads;
+
+/* Rotary positions: the first n_rot values of a head (even, 0 <= n_rot <=
+ * head size; 0: no rotation) are n_rot / 2 pairs, pair i made of values
+ * (i, i + n_rot / 2), or with `pairs` of values (2i, 2i + 1).  A pair (a, b)
+ * at position p becomes (a c - b s, b c + a s) with (c, s) = table[p][i];
+ * the other values pass.  table: fp32 [n_pos][n_rot / 2][2], 8-byte aligned
+ * (qmm_rope_table, or any other); a position outside [0, n_pos) skips its
+ * token and sets the device error word (QMM_ERR_BAD_INDEX). */
+typedef struct qmm_rope {
+    const float* table;
+    int64_t n_pos;
+    int32_t n_rot;
+    int32_t pairs;
+} qmm_rope;
+
+typedef enum qmm_rope_scaling {
+    QMM_ROPE_PLAIN = 0,  /* f_i = base^(-2i / n_rot)                        */
+    QMM_ROPE_LINEAR = 1, /* f_i / factor                                    */
+    QMM_ROPE_RAMP = 2    /* slow pairs / factor, fast ones kept, see below  */
+} qmm_rope_scaling;
+
+/* Fill a rotary table (set-up): table[p][i] = (m cos(p f_i), m sin(p f_i)),
+ * angles and functions in 64 bits, rounded once.  QMM_ROPE_RAMP is the YaRN
+ * method (Peng et al., 2023): with x(n) = n_rot ln(orig_len / (2 pi n)) /
+ * (2 ln base), lo = max(0, floor(x(beta_fast))), hi = min(n_rot / 2 - 1,
+ * ceil(x(beta_slow))), r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):
+ * f_i = plain_i (1 - r_i) + plain_i / factor * r_i and m = 0.1 ln(factor) + 1
+ * (m = 1 otherwise; factor, orig_len and the betas are read only where they
+ * are used).  n_rot even, 2 <= n_rot <= 256; n_pos == 0 is a no-op. */
+QMM_API qmm_status qmm_rope_table(float* table, int64_t n_pos, int32_t n_rot, double base, int32_t scaling,
+                                  double factor, double orig_len, double beta_fast, double beta_slow, void* stream);
+
+/* Norm and rotation of heads, one pass: n_e = x_e * norm_w_e /
+ * sqrt(mean(x^2) + norm_eps) over each head (norm_w fp32 [head_dim], or NULL:
+ * n = x), then the rotation of qmm_rope at position pos[t]; computed in fp32,
+ * rounded once to y's type.  x and y have the same n_heads; y may be x (same
+ * type and strides), else they do not overlap.  pos int32 [T] (may be NULL
+ * when n_rot == 0).  head_dim a multiple of 32, at most 256.  T == 0 is a
+ * no-op. */
+typedef struct qmm_rope_op {
+    qmm_heads x, y;
+    qmm_rope rope;
+    const int32_t* pos;
+    const float* norm_w;
+    int64_t T;
+    int32_t head_dim;
+    float norm_eps;
+} qmm_rope_op;
+QMM_API qmm_status qmm_rope_heads(const qmm_rope_op* op, void* stream);
+
+/* A paged cache of Q4_0 keys and values (4.5 bits a value): n_pages pages of
+ * page_size tokens (a multiple of 32) for n_heads key/value heads of head_dim
+ * values (a multiple of 32, at most 256).  data is uint8
+ * [n_pages][n_heads][page_size / 32][record], 16-byte aligned
+ * (qmm_kv_cache_bytes in all).  A record holds 32 consecutive tokens of one
+ * head, with NB = head_dim / 32 blocks each: K codes [NB][512], V codes
+ * [NB][512], K scales [NB][64], V scales [NB][64] bytes (36 * head_dim).  It
+ * is laid out in the order in which the lanes of a warp multiply it, 16
+ * consecutive bytes a lane.  With token = 8i + g = 8j + 2c + h (g < 8; c < 4;
+ * h < 2) of the record:
+ *  - K codes of a block: the 16 bytes of its Q4_0 block (as in the planes
+ *    above) are words m = 0..3 of 4 bytes; word m of the token is word
+ *    (g * 4 + m) * 4 + i of the 512 bytes;
+ *  - V codes of a block: 16-bit unit e (e < 8) of the token holds the codes
+ *    u = q + 8 of values e, e + 8, e + 16, e + 24 in its nibbles from the
+ *    lowest; it is unit ((e * 4 + c) * 4 + j) * 2 + h of the 512 bytes;
+ *  - scales: fp16 bits; the token's is number (c * 4 + j) * 2 + h of its
+ *    block's 32.
+ * No byte holds values of two tokens. */
+typedef struct qmm_kv_cache {
+    uint8_t* data;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t n_heads;
+    int32_t head_dim;
+} qmm_kv_cache;
+
+/* Bytes of cache->data (data itself is not looked at). */
+QMM_API qmm_status qmm_kv_cache_bytes(const qmm_kv_cache* cache, size_t* bytes);
+
+/* Write T tokens into the cache, one launch: k is normalised (k_norm fp32
+ * [head_dim], or NULL) and rotated as by qmm_rope_heads and rounded to fp32;
+ * it and v are quantized per block of 32 as by qmm_quantize_q4_0.  The
+ * normalised, rotated k is carried in pairs of fp32 (about 45 bits) until
+ * that rounding, so its codes are those of the formulas.  Token t goes to
+ * slot slots[t] = page * page_size + place (int64 [T]); a negative slot
+ * writes nothing (padding), one beyond the cache writes nothing and sets the
+ * device error word (QMM_ERR_BAD_INDEX); two tokens of one call must not name
+ * the same slot.  When q.data is not NULL, q is normalised (q_norm) and
+ * rotated into q_out in the same launch (as by qmm_rope_heads, padding tokens
+ * too).  k.n_heads == v.n_heads == cache.n_heads.  Non-finite values, and
+ * blocks whose max|y| / 7 is above 65504, are outside the domain.  T == 0 is
+ * a no-op. */
+typedef struct qmm_kv_append_op {
+    qmm_kv_cache cache;
+    qmm_heads k, v;
+    qmm_heads q, q_out;
+    qmm_rope rope;
+    const int64_t* slots;
+    const int32_t* pos;
+    const float* k_norm;
+    const float* q_norm;
+    int64_t T;
+    float norm_eps;
+    int32_t reserved; /* 0 */
+} qmm_kv_append_op;
+QMM_API qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream);
+
+/* The values d * q of cached tokens: token t of k and v (either data may be
+ * NULL) is the token at slots[t], rounded to their type; a negative slot
+ * gives zeros, one beyond the cache leaves its token untouched and sets the
+ * device error word (QMM_ERR_BAD_INDEX). */
+typedef struct qmm_kv_read_op {
+    qmm_kv_cache cache;
+    qmm_heads k, v;
+    const int64_t* slots;
+    int64_t T;
+} qmm_kv_read_op;
+QMM_API qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream);
+
+/* Attention of query tokens over the cache.  Sequence b (of n_seqs) has
+ * kv_len[b] cached tokens (int32, the queries' own tokens among them), token
+ * j in page pages[b * pages_stride + j / page_size]; its n queries are rows
+ * [q_start[b], q_start[b + 1]) of q and out (int32 [n_seqs + 1]), or with
+ * q_start NULL rows [b * max_q, (b + 1) * max_q), where T == n_seqs * max_q.
+ * Query i sits at key position p = kv_len[b] - n + i and sees the keys j <=
+ * p (causal != 0) or all of them, and of those only j > p - window when
+ * window > 0.  Query head h reads key/value head h / (q.n_heads /
+ * cache.n_heads).  out = sum_j softmax_j(scale * q . k_j) v_j over the keys
+ * it sees, with k and v the cached values d * q; 0 where it sees none.
+ * Scores, softmax statistics and sums are fp32; with fp32 q and out the
+ * products carry 22 bits of q and of the weights, with a 16-bit type 11.
+ * out.data may be NULL when yq and yd are given: Q8_0 of the fp32 output
+ * (int8 [T][q.n_heads * head_dim], uint16 [T][q.n_heads * head_dim / 32]; as
+ * qmm_quantize_q8_0, the O product's operand).  out has q's n_heads and type.
+ *
+ * max_q and max_kv bound the queries of a sequence and kv_len; pages_stride
+ * >= ceil(max_kv / page_size).  A q_start, kv_len or page outside its range
+ * sets the device error word (QMM_ERR_BAD_INDEX): q_start and kv_len are
+ * clamped to it, and a bad page's tokens count as unseen.  Entries of pages
+ * and tokens of the cache that no query sees are not used, whatever they
+ * hold.  workspace: qmm_attn_workspace_size bytes (may be 0), 16-byte
+ * aligned, any contents, used by one call at a time.  n_seqs == 0, T == 0 or
+ * max_q == 0 is a no-op. */
+typedef struct qmm_attn_op {
+    qmm_kv_cache cache;
+    qmm_heads q, out;
+    int8_t* yq;
+    uint16_t* yd;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* pages;
+    int64_t pages_stride;
+    int64_t T;
+    int32_t n_seqs;
+    int32_t max_q;
+    int32_t max_kv;
+    int32_t causal;
+    int32_t window;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+} qmm_attn_op;
+QMM_API qmm_status qmm_attn_workspace_size(const qmm_attn_op* op, size_t* bytes);
+QMM_API qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream);
+
+/* ---------------------------------------------------------------------
  * Errors raised on the device
  * ------------------------------------------------------------------- */
 
 /* Synchronises `stream`, reads and clears the device error word of the
- * current device: QMM_OK, QMM_ERR_BAD_EXPERT_ID or QMM_ERR_TIMEOUT (a
- * bounded wait gave up).  QMM_ERR_CUDA if the synchronisation failed. */
+ * current device: QMM_OK, QMM_ERR_BAD_EXPERT_ID, QMM_ERR_BAD_INDEX or
+ * QMM_ERR_TIMEOUT (a bounded wait gave up).  QMM_ERR_CUDA if the synchronisation failed. */
 QMM_API qmm_status qmm_last_device_error(void* stream);
 
 #ifdef __cplusplus
