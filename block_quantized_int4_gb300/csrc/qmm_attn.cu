@@ -20,12 +20,12 @@ struct Plan {
 };
 
 constexpr int DEFAULT_SMS = 152;
+constexpr int64_t MAX_CTAS = 1024;  // the join kernel's parts of an item
 
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
     const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
-    const bool f32 = op.q.dtype == QMM_F32;
-    const int tile = attn_tile_rows(f32);
+    const int tile = attn_tile_rows(op.q.dtype);
     const int64_t rows = (int64_t)op.max_q * group;
     p.row_warps = rows <= tile ? 1 : rows <= 2 * tile ? 2 : 4;
     p.token_warps = ATTN_WARPS / p.row_warps;
@@ -36,8 +36,8 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     // Items of a few units are not worth a second launch that joins parts.
     const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
     if (units > 4) {
-        p.ctas = (int)std::min<int64_t>((int64_t)sms * attn_ctas(NB), p.items * units);
-        p.meta_bytes = ((size_t)p.ctas * sizeof(AttnMeta) + 255) / 256 * 256;
+        p.ctas = (int)std::min<int64_t>({(int64_t)sms * attn_ctas(NB), p.items * units, MAX_CTAS});
+        p.meta_bytes = ((size_t)p.items * sizeof(AttnMeta) + 255) / 256 * 256;
         p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * (D + 2) * 4;
     }
     return p;
@@ -69,21 +69,29 @@ qmm_status check(const qmm_attn_op& op, bool pointers) {
     return QMM_OK;
 }
 
-bool prepared(int NB, bool f32, int optin) {
+AttnKernel kernel_of(int dtype, int NB) {
+    return dtype == QMM_F32 ? attn_kernel_f32(NB) : dtype == QMM_F16 ? attn_kernel_f16(NB) : attn_kernel_bf16(NB);
+}
+
+// Opts a kernel into the shared memory of a device, once.
+bool prepared(AttnKernel k, int dtype, int NB, int optin) {
     static std::mutex mu;
-    static bool done[64][2][8];
+    static bool done[64][3][8];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
-    bool& d = done[dev][f32][NB - 1];
-    if (!d) d = f32 ? attn_prepare_f32(NB, optin) : attn_prepare_16(NB, optin);
+    bool& d = done[dev][dtype][NB - 1];
+    if (!d)
+        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 4096) == cudaSuccess &&
+            cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+                cudaSuccess;
+    if (!d) cudaGetLastError();
     return d;
 }
 
-template <int NB>
-void join(const AttnArgs& a, const Plan& p, cudaStream_t st) {
-    attn::attn_join_kernel<NB><<<dim3(p.ctas, std::max(1, p.block_rows / 8)), 128, 0, st>>>(a, p.block_rows);
-}
+constexpr void (*JOIN[8])(AttnArgs, int) = {
+    attn::attn_join_kernel<1>, attn::attn_join_kernel<2>, attn::attn_join_kernel<3>, attn::attn_join_kernel<4>,
+    attn::attn_join_kernel<5>, attn::attn_join_kernel<6>, attn::attn_join_kernel<7>, attn::attn_join_kernel<8>};
 
 }  // namespace
 }  // namespace qmm
@@ -142,18 +150,18 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
     a.err = device_error_word();
     const int NB = op->cache.head_dim / QK;
-    const bool f32 = op->q.dtype == QMM_F32;
-    if (!prepared(NB, f32, optin)) return QMM_ERR_CUDA;
+    const AttnKernel kernel = kernel_of(op->q.dtype, NB);
+    if (!prepared(kernel, op->q.dtype, NB, optin)) return QMM_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned grid = p.ctas ? (unsigned)p.ctas : (unsigned)p.items;
-    const cudaError_t e = f32 ? attn_launch_f32(NB, a, grid, p.smem, st) : attn_launch_16(NB, a, grid, p.smem, st);
-    if (e != cudaSuccess) return QMM_ERR_CUDA;
+    kernel<<<grid, ATTN_THREADS, p.smem, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return QMM_ERR_CUDA;
     if (p.ctas) {
-        static constexpr void (*JOIN[8])(const AttnArgs&, const Plan&, cudaStream_t) = {
-            join<1>, join<2>, join<3>, join<4>, join<5>, join<6>, join<7>, join<8>};
-        JOIN[NB - 1](a, p, st);
+        JOIN[NB - 1]<<<dim3((unsigned)p.items, (unsigned)std::min(p.block_rows, 16)), attn::JOIN_WARPS * 32, 0, st>>>(
+            a, p.block_rows);
+        if (cudaGetLastError() != cudaSuccess) return QMM_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+    return QMM_OK;
 }
 
 }  // extern "C"

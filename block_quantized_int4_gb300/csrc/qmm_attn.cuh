@@ -37,10 +37,10 @@ constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
 constexpr int ATTN_STAGES = 4;  // records in flight or in use per token group
 
-struct AttnMeta {  // of a CTA: the item that it leaves to the CTAs after it
-    int last;      // last CTA of the item, or -1
-    int seq, block, head;
-    int slot;      // which of this CTA's parts is the item's
+struct AttnMeta {  // of an item: the CTAs that its units are cut over
+    int first, last;  // first > last: not cut
+    int slot;         // which of the first CTA's parts is the item's
+    int pad;
 };
 
 struct AttnArgs {
@@ -58,40 +58,62 @@ struct AttnArgs {
     int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
     int split;              // 0: one CTA an item; 1: items cut where the CTAs' shares end
     float* part;            // [ctas][2][rows][D + 2]
-    AttnMeta* meta;         // [ctas]
+    AttnMeta* meta;         // [sequence][row block][head]
     int* err;
 };
 
-// Launches the kernel of head size 32 * NB (qmm_attn_f32.cu, qmm_attn_16.cu).
-cudaError_t attn_launch_f32(int NB, const AttnArgs& a, unsigned grid, int smem, cudaStream_t st);
-cudaError_t attn_launch_16(int NB, const AttnArgs& a, unsigned grid, int smem, cudaStream_t st);
-// Opt-in of the dynamic shared memory, once a device.
-bool attn_prepare_f32(int NB, int smem_optin);
-bool attn_prepare_16(int NB, int smem_optin);
+// The kernel of head size 32 * NB for one type of activations.
+using AttnKernel = void (*)(AttnArgs);
+AttnKernel attn_kernel_f32(int NB);
+AttnKernel attn_kernel_f16(int NB);
+AttnKernel attn_kernel_bf16(int NB);
 
 // Rows of a warp's tile.
-__host__ __device__ constexpr int attn_tile_rows(bool split_parts) { return split_parts ? 8 : 16; }
+__host__ __device__ constexpr int attn_tile_rows(int dtype) { return dtype == QMM_F32 ? 8 : 16; }
 // CTAs an SM by registers (launch bound).
 constexpr int attn_ctas(int NB) { return NB <= 4 ? 3 : 2; }
 
 #ifdef __CUDACC__
 namespace attn {
 
-__device__ __forceinline__ void mma16816(float* c, unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
-                                         unsigned b1) {
+// c = a b + c, and c = a b.
+__device__ __forceinline__ void mma_add(float* c, const unsigned* a, unsigned b0, unsigned b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_from(float* c, const unsigned* a, unsigned b0, unsigned b1, float x, float y) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(x), "f"(y));
 }
 
-__device__ __forceinline__ void cp16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// Two fp32 lanes in one instruction, each rounded as its scalar form.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 x, x, y, z; "
+        "mov.b64 {%0, %1}, x;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ __half2 as_half2(unsigned w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ unsigned as_bits(__half2 h) { return *reinterpret_cast<const unsigned*>(&h); }
 
 __device__ __forceinline__ float exp2_fast(float x) {  // ex2.approx: 2 ulp, results below 2^-126 are 0
     float y;
@@ -239,13 +261,6 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, in
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int NB, bool SPLIT>
-struct Shape {
-    static constexpr int D = NB * 32;
-    static constexpr int REC = record_bytes(D);
-    static constexpr int ROWS = attn_tile_rows(SPLIT);
-};
-
 // Output of a finished row of fp32 values: lane holds values 32b + lane.
 template <int NB>
 __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int head, const float* o, int lane) {
@@ -269,14 +284,25 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int 
     }
 }
 
-template <int NB, bool SPLIT>
+// Exponents: 2^e <= the largest scale < 2^(e + 1), then 2^total times the
+// scale is below 2^15 and the weights' own factor 2^(part of it) at most 2^15.
+// Scales below 2^-7 take the rest of the factor themselves.
+__device__ __forceinline__ int scale_exponent(unsigned or_bits) {  // of fp16 scales' bits, OR-ed
+    const unsigned m = (or_bits | or_bits >> 16) & 0x7C00;
+    return (int)(m >> 10) - 15 + (m == 0);  // subnormal scales count as 2^-14
+}
+
+template <int NB, int DTYPE>
 __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const __grid_constant__ AttnArgs a) {
-    using S = Shape<NB, SPLIT>;
-    constexpr int D = S::D, REC = S::REC, ROWS = S::ROWS;
+    constexpr bool SPLIT = DTYPE == QMM_F32;
+    constexpr int D = NB * 32, REC = record_bytes(D), ROWS = attn_tile_rows(DTYPE);
     constexpr int RS = SPLIT ? 1 : 2;  // rows a lane keeps statistics of
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Scan sc;
     __shared__ float s_m[ATTN_WARPS][16], s_l[ATTN_WARPS][16];
+    __shared__ uint64_t s_full[ATTN_WARPS][ATTN_STAGES];
+    __shared__ int s_gone[ATTN_WARPS][ATTN_STAGES];  // the record's page does not exist
+    __shared__ int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -284,15 +310,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     const int wr = warp / TW, wt = warp - wr * TW;
     const int block_rows = RW * ROWS;
     uint8_t* ring = smem + wt * (ATTN_STAGES * REC);
+    uint64_t* full = s_full[wt];
+
+    if (tid < ATTN_WARPS * ATTN_STAGES) mbar_init(&s_full[0][0] + tid, 1);
+    if (tid == 0) s_abort = 0;
+    fence_mbar_init();
 
     Place at;
     int64_t u0, u1, share = 0;
     if (a.split) {
-        if (tid == 0) a.meta[blockIdx.x].last = -1;
-        find_share(a, block_rows, TW, sc, u0, u1, share);
+        find_share(a, block_rows, TW, sc, u0, u1, share);  // synchronises the block
         if (u0 >= u1) return;
         at = sc.at;
     } else {  // one CTA an item, later row blocks (more keys) first
+        __syncthreads();
         const int e = blockIdx.x / a.kv_heads, b = e / a.blocks;
         at.head = blockIdx.x - e * a.kv_heads;
         at.entry = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
@@ -301,6 +332,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         u1 = 1;
     }
 
+    unsigned done = 0;  // records of this token group so far: stage and phase of the ring
     for (int64_t u = u0; u < u1;) {
         const int b = at.entry / a.blocks, block = at.entry - b * a.blocks;
         const Seq seq = sequence(a, b, !a.split && tid == 0);
@@ -311,8 +343,42 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             continue;
         }
         const int unit_end = a.split ? (int)min((int64_t)sp.units, at.unit + (u1 - u)) : sp.units;
-        const int rec0 = sp.lo / GROUP + at.unit * TW;
+        const int rec0 = sp.lo / GROUP + at.unit * TW + wt;
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * TW);
+        const int n_mine = rec_end > rec0 ? (rec_end - rec0 + TW - 1) / TW : 0;
+
+        // ---- the ring: the first lane of a token group copies a whole record
+        int next_pg = rec0 / a.page_groups, next_in = rec0 - next_pg * a.page_groups;
+        const int* table = a.pages + (int64_t)b * a.pages_stride;
+        int next_page = n_mine > 0 ? table[next_pg] : 0;
+        const auto issue = [&](int k) {
+            if (k < n_mine && wr == 0 && lane == 0) {
+                const unsigned stage = (done + k) % ATTN_STAGES;
+                const int page = next_page, in = next_in;
+                next_in += TW;
+                while (next_in >= a.page_groups) next_in -= a.page_groups, ++next_pg;
+                if (k + 1 < n_mine) next_page = table[next_pg];
+                const bool gone = page < 0 || page >= a.n_pages;
+                s_gone[wt][stage] = gone;
+                if (gone) {
+                    atomicOr(a.err, ERR_BAD_INDEX);
+                    mbar_arrive(&full[stage]);
+                } else {
+                    mbar_arrive_expect_tx(&full[stage], REC);
+                    bulk_g2s(ring + stage * REC,
+                             a.cache + (((int64_t)page * a.kv_heads + at.head) * a.page_groups + in) * (int64_t)REC,
+                             REC, &full[stage]);
+                }
+            }
+        };
+        const auto sync_group = [&]() {
+            if (RW == 1)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(RW * 32) : "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < ATTN_STAGES - 1; ++k) issue(k);
 
         // ---- the rows of this lane, q' as MMA operands
         const int rows = seq.n * a.group;
@@ -332,8 +398,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 if (live) {
-                    loadn<4>(a.q.data, at_q + 32 * k + 4 * c, a.q.dtype, a.q.wide, x[k]);
-                    loadn<4>(a.q.data, at_q + 32 * k + 16 + 4 * c, a.q.dtype, a.q.wide, x[k] + 4);
+                    loadn<4>(a.q.data, at_q + 32 * k + 4 * c, DTYPE, a.q.wide, x[k]);
+                    loadn<4>(a.q.data, at_q + 32 * k + 16 + 4 * c, DTYPE, a.q.wide, x[k] + 4);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
@@ -363,10 +429,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                     qa[k][st][r] = h0;
                     qa[k][st][2 + r] = h1;
                     if constexpr (SPLIT) {
-                        const unsigned l0 = pack_half(y[4 * st] - a0.x, y[4 * st + 2] - a0.y);
-                        const unsigned l1 = pack_half(y[4 * st + 1] - a1.x, y[4 * st + 3] - a1.y);
-                        qa[k][st][1] = l0;
-                        qa[k][st][3] = l1;
+                        qa[k][st][1] = pack_half(y[4 * st] - a0.x, y[4 * st + 2] - a0.y);
+                        qa[k][st][3] = pack_half(y[4 * st + 1] - a1.x, y[4 * st + 3] - a1.y);
                     } else {
                         const float part = a0.x + a0.y + a1.x + a1.y;
                         sum += st ? 16.f * part : part;
@@ -381,53 +445,30 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         }
 
         float acc[NB][4][4] = {};  // [block][n tile][rows g: 2 columns, rows g + 8 (or lo parts): 2 columns]
-        float top[RS], l[RS];  // running maximum of the scores (before f) and sum of the weights
-        float vs = 1.f;        // power of two that acc holds the weighted v times, from the largest scale so far
-        int vexp = 100;
+        float top[RS], l[RS];      // running maximum of the scores (before f) and sum of the weights
+        int total = 1000;          // acc holds the weighted v times 2^total, from the largest scale so far
+        float vs = 1.f, ds = 1.f;  // 2^total = vs (on the weights) * ds (on the scales)
 #pragma unroll
         for (int r = 0; r < RS; ++r) top[r] = -INFINITY, l[r] = 0.f;
 
-        // ---- the ring: one record a step and token group
-        const int64_t table = (int64_t)b * a.pages_stride;
-        const int n_mine = rec_end > rec0 + wt ? (rec_end - rec0 - wt + TW - 1) / TW : 0;
-        unsigned bad = 0;  // stages whose page does not exist
-        const auto issue = [&](int k) {
-            if (k < n_mine) {
-                const int rec = rec0 + wt + k * TW;
-                const int pg = rec / a.page_groups, in = rec - pg * a.page_groups;
-                int page = a.pages[table + pg];
-                const int stage = k % ATTN_STAGES;
-                if (page < 0 || page >= a.n_pages) {
-                    bad |= 1u << stage;
-                    if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
-                } else {
-                    bad &= ~(1u << stage);
-                    const uint8_t* src =
-                        a.cache + (((int64_t)page * a.kv_heads + at.head) * a.page_groups + in) * (int64_t)REC;
-                    uint8_t* dst = ring + stage * REC;
-                    for (int i = wr * 32 + lane; i < REC / 16; i += RW * 32) cp16(dst + 16 * i, src + 16 * i);
-                }
-            }
-            cp_commit();
-        };
-        const auto sync_group = [&]() {
-            if (RW == 1)
-                __syncwarp();
-            else
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(RW * 32) : "memory");
-        };
-#pragma unroll
-        for (int k = 0; k < ATTN_STAGES - 1; ++k) issue(k);
-
         for (int k = 0; k < n_mine; ++k) {
-            cp_wait<ATTN_STAGES - 2>();
-            sync_group();  // everyone's copies of record k are there, and its predecessor is read
+            sync_group();  // the record before is read
             issue(k + ATTN_STAGES - 1);
-            const uint8_t* rec = ring + (k % ATTN_STAGES) * REC;
-            const int tok0 = (rec0 + wt + k * TW) * GROUP;
+            const unsigned stage = (done + k) % ATTN_STAGES;
+            bool gone = false;
+            if (!mbar_wait(&full[stage], (done + k) / ATTN_STAGES & 1, (volatile int*)&s_abort)) {
+                if (lane == 0) {
+                    s_abort = 1;
+                    atomicOr(a.err, ERR_TIMEOUT);
+                }
+                gone = true;
+            }
+            gone |= s_gone[wt][stage] != 0;
+            const uint8_t* rec = ring + stage * REC;
+            const int tok0 = (rec0 + k * TW) * GROUP;
 
             // scores
-            float s[4][2 * RS] = {};
+            float2 s[4][RS] = {};
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
@@ -436,51 +477,39 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float t[4];
-                    if constexpr (SPLIT) {
-                        t[0] = t[1] = t[2] = t[3] = 0.f;
-                        mma16816(t, qa[kb][0][0], qa[kb][0][1], qa[kb][0][2], qa[kb][0][3], signed_codes<0>(w[j]),
-                                 signed_codes<0>(w[j] >> 8));
-                        mma16816(t, qa[kb][1][0], qa[kb][1][1], qa[kb][1][2], qa[kb][1][3], signed_codes<1>(w[j]),
-                                 signed_codes<1>(w[j] >> 8));
-                    } else {
-                        t[0] = t[1] = seed[0][kb], t[2] = t[3] = seed[RS - 1][kb];
-                        const unsigned w8 = w[j] >> 8;
-                        mma16816(t, qa[kb][0][0], qa[kb][0][1], qa[kb][0][2], qa[kb][0][3], w[j] & 0x000F000Fu,
-                                 w8 & 0x000F000Fu);
-                        mma16816(t, qa[kb][1][0], qa[kb][1][1], qa[kb][1][2], qa[kb][1][3], w[j] & 0x00F000F0u,
-                                 w8 & 0x00F000F0u);
-                    }
+                    const unsigned w8 = w[j] >> 8;
                     const float2 dk = unpack_half(d[j]);
                     if constexpr (SPLIT) {
-                        s[j][0] = fmaf(dk.x, t[0] + t[2], s[j][0]);
-                        s[j][1] = fmaf(dk.y, t[1] + t[3], s[j][1]);
+                        mma_from(t, qa[kb][0], signed_codes<0>(w[j]), signed_codes<0>(w8), 0.f, 0.f);
+                        mma_add(t, qa[kb][1], signed_codes<1>(w[j]), signed_codes<1>(w8));
+                        s[j][0] = fma2(dk, add2(make_float2(t[0], t[1]), make_float2(t[2], t[3])), s[j][0]);
                     } else {
-                        s[j][0] = fmaf(dk.x, t[0], s[j][0]);
-                        s[j][1] = fmaf(dk.y, t[1], s[j][1]);
-                        s[j][2] = fmaf(dk.x, t[2], s[j][2]);
-                        s[j][3] = fmaf(dk.y, t[3], s[j][3]);
+                        mma_from(t, qa[kb][0], w[j] & 0x000F000Fu, w8 & 0x000F000Fu, seed[0][kb], seed[RS - 1][kb]);
+                        mma_add(t, qa[kb][1], w[j] & 0x00F000F0u, w8 & 0x00F000F0u);
+                        s[j][0] = fma2(dk, make_float2(t[0], t[1]), s[j][0]);
+                        s[j][RS - 1] = fma2(dk, make_float2(t[2], t[3]), s[j][RS - 1]);
                     }
                 }
             }
+
             // the mask, where a row does not see all 32 keys
-            const bool gone = bad >> (k % ATTN_STAGES) & 1;
-            bool full = !gone;
+            bool whole = !gone;
 #pragma unroll
-            for (int r = 0; r < RS; ++r) full &= tok0 >= lo[r] && tok0 + GROUP <= hi[r];
-            const bool masked = __any_sync(FULL, !full);
+            for (int r = 0; r < RS; ++r) whole &= tok0 >= lo[r] && tok0 + GROUP <= hi[r];
+            const bool masked = __any_sync(FULL, !whole);
             if (masked) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2 * RS; ++e) {
-                        const int key = tok0 + 8 * j + 2 * c + (e & 1);
-                        if (gone || key < lo[e >> 1] || key >= hi[e >> 1]) s[j][e] = -INFINITY;
+                    for (int r = 0; r < RS; ++r) {
+                        const int key = tok0 + 8 * j + 2 * c;
+                        if (gone || key < lo[r] || key >= hi[r]) s[j][r].x = -INFINITY;
+                        if (gone || key + 1 < lo[r] || key + 1 >= hi[r]) s[j][r].y = -INFINITY;
                     }
             }
 
-            // scales of v, and the weights' reference
-            unsigned vd[NB][4];
-            __half2 big = __float2half2_rn(0.f);
+            // scales of v, and the power of two that they and the weights share
+            unsigned vd[NB][4], any = 0;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 d4 = lds128(rec + NB * 1088 + kb * 64 + c * 16);
@@ -493,28 +522,40 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                         if (gone || key + 1 < sp.lo || key + 1 >= sp.hi) vd[kb][j] &= 0x0000FFFFu;
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2*>(&vd[kb][j])));
+                any |= vd[kb][0] | vd[kb][1];
+                any |= vd[kb][2] | vd[kb][3];
             }
-            float dmax = fmaxf(__low2float(big), __high2float(big));
-            dmax = fmaxf(dmax, __shfl_xor_sync(FULL, dmax, 1));
-            dmax = fmaxf(dmax, __shfl_xor_sync(FULL, dmax, 2));
-            // dmax * vs < 2^14
-            const int room = 13 - (int)((__float_as_uint(dmax) >> 23) - 127);
+            any |= __shfl_xor_sync(FULL, any, 1);
+            any |= __shfl_xor_sync(FULL, any, 2);
+            const int room = 14 - scale_exponent(any);
             float ratio = 1.f;
-            if (room < vexp) {
-                vexp = max(room, -100);
-                const float now = exp2f((float)vexp);
-                ratio = now / vs;
-                vs = now;
+            if (room < total) {
+                const int before = total;
+                total = room;
+                const int w = total > 21 ? 15 : min(total, 15);
+                vs = exp2f((float)w);
+                ds = total > 21 ? exp2f((float)(total - w)) : 1.f;
+                // 2^total stops at 2^15 where the scales take none of it
+                ratio = before > 100 ? 1.f : vs * ds * exp2f((float)-(before > 21 ? before : min(before, 15)));
             }
+            if (ds != 1.f) {
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 d = unpack_half(vd[kb][j]);
+                        vd[kb][j] = pack_half(d.x * ds, d.y * ds);
+                    }
+            }
+
+            // weights
             float ref[RS], alpha[RS];
             bool moved = ratio != 1.f;
 #pragma unroll
             for (int r = 0; r < RS; ++r) {
                 float m = top[r];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
+                for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(s[j][r].x, s[j][r].y));
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
                 ref[r] = m == -INFINITY ? 0.f : m * f[r];  // nothing seen yet: every weight is 0
@@ -536,13 +577,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                         }
                 }
             }
+            unsigned ph[4][RS], pl[4];  // weights as fp16: hi parts (both rows), lo parts
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 2 * RS; ++e) {
-                    const float w = exp2_fast(fmaf(s[j][e], f[e >> 1], -ref[e >> 1]));
-                    l[e >> 1] += w;
-                    s[j][e] = w * vs;
+                for (int r = 0; r < RS; ++r) {
+                    const float2 x = fma2(s[j][r], make_float2(f[r], f[r]), make_float2(-ref[r], -ref[r]));
+                    const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                    l[r] += w.x + w.y;
+                    s[j][r] = mul2(w, make_float2(vs, vs));
+                    if (DTYPE != QMM_F16) ph[j][r] = pack_half(s[j][r].x, s[j][r].y);
+                    if (SPLIT) {
+                        const float2 h = unpack_half(ph[j][r]);
+                        pl[j] = pack_half(s[j][r].x - h.x, s[j][r].y - h.y);
+                    }
                 }
 
             // weights times v
@@ -550,34 +598,39 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 w4 = lds128(rec + NB * 512 + kb * 512 + lane * 16);
                 const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w};
-                unsigned up[4], dn[4];  // the A operand's rows 0..7 and 8..15, two tokens each
+                unsigned pa[2][4];  // A operands of the two k steps: rows 0..7, 8..15, two tokens each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 d = unpack_half(vd[kb][j]);
-                    const float x = s[j][0] * d.x, y = s[j][1] * d.y;
-                    up[j] = pack_half(x, y);
+                    unsigned &up = pa[j >> 1][2 * (j & 1)], &dn = pa[j >> 1][2 * (j & 1) + 1];
+                    const __half2 d = as_half2(vd[kb][j]);
                     if constexpr (SPLIT) {
-                        const float2 h = unpack_half(up[j]);
-                        dn[j] = pack_half(x - h.x, y - h.y);
+                        // (hi + lo) d as two parts: the product, and its exact error plus lo d
+                        const __half2 h = as_half2(ph[j][0]), pr = __hmul2(h, d);
+                        up = as_bits(pr);
+                        dn = as_bits(__hfma2(as_half2(pl[j]), d, __hfma2(h, d, __hneg2(pr))));
+                    } else if constexpr (DTYPE == QMM_BF16) {
+                        // two roundings of 2^-12, next to the output's 2^-9
+                        up = as_bits(__hmul2(as_half2(ph[j][0]), d));
+                        dn = as_bits(__hmul2(as_half2(ph[j][RS - 1]), d));
                     } else {
-                        dn[j] = pack_half(s[j][2] * d.x, s[j][3] * d.y);
+                        const float2 df = __half22float2(d), x = mul2(s[j][0], df), y = mul2(s[j][RS - 1], df);
+                        up = pack_half(x.x, x.y);
+                        dn = pack_half(y.x, y.y);
                     }
                 }
 #pragma unroll
                 for (int st = 0; st < 2; ++st) {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const unsigned x = n >= 2 ? w[2 * st] >> 8 : w[2 * st];
-                        const unsigned y = n >= 2 ? w[2 * st + 1] >> 8 : w[2 * st + 1];
-                        mma16816(acc[kb][n], up[2 * st], dn[2 * st], up[2 * st + 1], dn[2 * st + 1],
-                                 n & 1 ? signed_codes<1>(x) : signed_codes<0>(x),
-                                 n & 1 ? signed_codes<1>(y) : signed_codes<0>(y));
-                    }
+                    const unsigned x = w[2 * st], y = w[2 * st + 1], x8 = x >> 8, y8 = y >> 8;
+                    mma_add(acc[kb][0], pa[st], signed_codes<0>(x), signed_codes<0>(y));
+                    mma_add(acc[kb][1], pa[st], signed_codes<1>(x), signed_codes<1>(y));
+                    mma_add(acc[kb][2], pa[st], signed_codes<0>(x8), signed_codes<0>(y8));
+                    mma_add(acc[kb][3], pa[st], signed_codes<1>(x8), signed_codes<1>(y8));
                 }
             }
         }
+        done += n_mine;
 
-        // ---- join the token groups: O, M and l of every row
+        // ---- join the token groups: O, maximum and sum of every row
 #pragma unroll
         for (int r = 0; r < RS; ++r) {
             l[r] += __shfl_xor_sync(FULL, l[r], 1);
@@ -585,14 +638,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             top[r] *= f[r];  // -inf stays: f > 0
             if (c == 0) s_m[warp][g + 8 * r] = top[r], s_l[warp][g + 8 * r] = l[r];
         }
-        cp_wait<0>();
-        __syncthreads();  // the ring is free
+        __syncthreads();  // the ring is read
         float* buf = reinterpret_cast<float*>(smem);  // [warp][ROWS][D]
+        const float unscale = 1.f / (vs * ds);
 #pragma unroll
         for (int r = 0; r < RS; ++r) {
             float m = -INFINITY;
             for (int t = 0; t < TW; ++t) m = fmaxf(m, s_m[wr * TW + t][g + 8 * r]);
-            const float w = top[r] == -INFINITY ? 0.f : exp2_fast(top[r] - m) / vs;
+            const float w = top[r] == -INFINITY ? 0.f : exp2_fast(top[r] - m) * unscale;
             float* o = buf + (warp * ROWS + g + 8 * r) * D;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb)
@@ -608,10 +661,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 }
         }
         __syncthreads();
-        const bool whole = at.unit == 0 && unit_end == sp.units;
+        const bool uncut = at.unit == 0 && unit_end == sp.units;
         // a share's first segment keeps its part in slot 0, its last in slot 1
         float* part = nullptr;
-        if (!whole) part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * (D + 2);
+        if (!uncut) part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * (D + 2);
         for (int row = warp; row < block_rows; row += ATTN_WARPS) {
             const int rw = row / ROWS, rr = row - rw * ROWS;
             float m = -INFINITY, sum = 0.f, o[NB] = {};
@@ -624,7 +677,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             }
             const int global_row = block * block_rows + row;
             if (global_row >= rows) break;
-            if (whole) {
+            if (uncut) {
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) o[kb] *= inv;
@@ -636,54 +689,87 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 if (lane == 0) part[row * (D + 2) + D] = m, part[row * (D + 2) + D + 1] = sum;
             }
         }
-        if (a.split) {
-            if (tid == 0 && at.unit == 0 && !whole) {
-                AttnMeta& mt = a.meta[blockIdx.x];
-                mt.last = (int)((u + sp.units - 1) / share);
-                mt.seq = b, mt.block = block, mt.head = at.head, mt.slot = u != u0;
-            }
-            __syncthreads();  // buf and the statistics are read
+        if (!a.split) return;
+        if (tid == 0 && at.unit == 0) {
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (int)((u + sp.units - 1) / share);
+            a.meta[(int64_t)at.entry * a.kv_heads + at.head] = AttnMeta{first, last, u != u0, 0};
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // buf is used before the ring's next copies
+        __syncthreads();
         u += unit_end - at.unit;
         at.unit = 0;
         if (++at.head == a.kv_heads) at.head = 0, ++at.entry;
-        if (!a.split) return;
     }
 }
 
-// Joins the parts of the items that were cut: block (x, y) takes rows y, y +
-// gridDim.y, ... of the item that CTA x left unfinished, its parts in the
-// order of the CTAs.
+// Joins the parts of an item that was cut over CTAs, in the CTAs' order:
+// block (item, y) takes rows y, y + gridDim.y, ...; its warps take every
+// eighth part.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_MAX_PARTS = 1024;
+
 template <int NB>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a, int block_rows) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32)
+    attn_join_kernel(const __grid_constant__ AttnArgs a, int block_rows) {
     constexpr int D = NB * 32;
+    __shared__ float s_w[JOIN_MAX_PARTS], s_o[JOIN_WARPS][D], s_red[2][JOIN_WARPS];
+    const int entry = blockIdx.x / a.kv_heads, head = blockIdx.x - entry * a.kv_heads;
+    const int b = entry / a.blocks, block = entry - b * a.blocks;
+    const Seq seq = sequence(a, b, false);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rows = min(block_rows, seq.n * a.group - block * block_rows);
+    if (rows <= 0) return;
     const AttnMeta mt = a.meta[blockIdx.x];
-    if (mt.last < 0) return;
-    const int lane = threadIdx.x & 31;
-    const Seq seq = sequence(a, mt.seq, false);
-    const int rows = seq.n * a.group;
-    for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < block_rows; row += gridDim.y * 4) {
-        const int global_row = mt.block * block_rows + row;
-        if (global_row >= rows) return;
-        float m = -INFINITY, sum = 0.f, o[NB] = {};
-        const int64_t step = (int64_t)block_rows * (D + 2);
-        for (int x = blockIdx.x; x <= mt.last; ++x) {
-            const float* p = a.part + ((int64_t)x * 2) * step + row * (D + 2);
-            if (x == (int)blockIdx.x && mt.slot) p += step;
-            const float pm = p[D], pl = p[D + 1];
-            const float now = fmaxf(m, pm);
-            const float use = now == -INFINITY ? 0.f : now;
-            const float wo = exp2_fast(m - use), wp = exp2_fast(pm - use);
-            sum = sum * wo + pl * wp;
+    const int n = mt.last - mt.first + 1;
+    if (n <= 1) return;
+    const int64_t step = (int64_t)block_rows * (D + 2);
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        const float* base = a.part + (int64_t)mt.first * 2 * step + row * (D + 2);
+        const auto part = [&](int x) { return base + 2 * step * x + (x == 0 && mt.slot ? step : 0); };
+        float m = -INFINITY;
+        for (int x = tid; x < n; x += JOIN_WARPS * 32) m = fmaxf(m, part(x)[D]);
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) o[kb] = o[kb] * wo + p[kb * 32 + lane] * wp;
-            m = now;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+        if (lane == 0) s_red[0][warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, s_red[0][w]);
+        float sum = 0.f;
+        for (int x = tid; x < n; x += JOIN_WARPS * 32) {
+            const float w = m == -INFINITY ? 0.f : exp2_fast(part(x)[D] - m);
+            s_w[x] = w;
+            sum += w * part(x)[D + 1];
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        sum = warp_sum(sum);
+        if (lane == 0) s_red[1][warp] = sum;
+        __syncthreads();
+        float o[NB] = {};
+#pragma unroll 4
+        for (int x = warp; x < n; x += JOIN_WARPS) {
+            const float w = s_w[x];
+            const float* p = part(x);
 #pragma unroll
-        for (int kb = 0; kb < NB; ++kb) o[kb] *= inv;
-        const int i = global_row / a.group;
-        write_row<NB>(a, seq.q0 + i, mt.head * a.group + global_row - i * a.group, o, lane);
+            for (int kb = 0; kb < NB; ++kb) o[kb] = fmaf(w, p[kb * 32 + lane], o[kb]);
+        }
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) s_o[warp][kb * 32 + lane] = o[kb];
+        __syncthreads();
+        if (warp == 0) {
+            float total = 0.f;
+#pragma unroll
+            for (int w = 0; w < JOIN_WARPS; ++w) total += s_red[1][w];
+            const float inv = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < JOIN_WARPS; ++w) v += s_o[w][kb * 32 + lane];
+                o[kb] = v * inv;
+            }
+            const int global_row = block * block_rows + row, i = global_row / a.group;
+            write_row<NB>(a, seq.q0 + i, head * a.group + global_row - i * a.group, o, lane);
+        }
+        __syncthreads();
     }
 }
 
