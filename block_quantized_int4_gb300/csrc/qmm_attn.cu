@@ -16,7 +16,7 @@ struct Plan {
     int ctas;  // CTAs of a cut launch; 0: one CTA an item
     int64_t items;
     size_t meta_bytes, part_bytes;
-    int smem;
+    int ring_bytes, smem;
 };
 
 constexpr int DEFAULT_SMS = 152;
@@ -32,7 +32,8 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     p.block_rows = p.row_warps * tile;
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.items = (int64_t)op.n_seqs * p.blocks * op.cache.n_heads;
-    p.smem = std::max(p.token_warps * ATTN_STAGES * record_bytes(D), ATTN_WARPS * tile * D * 4);
+    p.ring_bytes = attn_ring_bytes(D, p.row_warps, tile);
+    p.smem = p.ring_bytes + attn_q_bytes(D, p.row_warps);
     // Items of a few units are not worth a second launch that joins parts.
     const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
     if (units > 4) {
@@ -119,6 +120,8 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     const bool device = device_facts(&sms, &optin);
     const Plan p = plan_of(*op, device ? sms : DEFAULT_SMS);
     const size_t need = p.meta_bytes + p.part_bytes;
+    // shares are counted in 31 bits
+    if (p.items * ((op->max_kv + GROUP - 1) / GROUP + 1) >= int64_t(1) << 31) return QMM_ERR_SHAPE;
     if (need && (!op->workspace || op->workspace_bytes < need || reinterpret_cast<uintptr_t>(op->workspace) % 16))
         return QMM_ERR_WORKSPACE;
     if (!device) return QMM_ERR_DEVICE;
@@ -143,6 +146,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.causal = op->causal != 0;
     a.window = std::min(op->window, 1 << 29);
     a.scale_log2 = op->scale * 1.4426950408889634f;
+    a.ring_bytes = p.ring_bytes;
     a.row_warps = p.row_warps;
     a.blocks = p.blocks;
     a.split = p.ctas != 0;
@@ -157,9 +161,19 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     kernel<<<grid, ATTN_THREADS, p.smem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return QMM_ERR_CUDA;
     if (p.ctas) {
-        JOIN[NB - 1]<<<dim3((unsigned)p.items, (unsigned)std::min(p.block_rows, 16)), attn::JOIN_WARPS * 32, 0, st>>>(
-            a, p.block_rows);
-        if (cudaGetLastError() != cudaSuccess) return QMM_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)p.items, (unsigned)std::min(p.block_rows, 16));
+        cfg.blockDim = dim3(attn::JOIN_WARPS * 32);
+        cfg.stream = st;
+        cudaLaunchAttribute pdl;
+        pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        pdl.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &pdl;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, JOIN[NB - 1], a, p.block_rows) != cudaSuccess) {
+            cudaGetLastError();
+            return QMM_ERR_CUDA;
+        }
     }
     return QMM_OK;
 }

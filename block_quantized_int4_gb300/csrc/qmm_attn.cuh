@@ -35,7 +35,7 @@ namespace qmm {
 
 constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
-constexpr int ATTN_STAGES = 4;  // records in flight or in use per token group
+constexpr int ATTN_STAGES = 2;  // a token group's records: one in use, one in flight
 
 struct AttnMeta {  // of an item: the CTAs that its units are cut over
     int first, last;  // first > last: not cut
@@ -55,6 +55,7 @@ struct AttnArgs {
     int n_pages, page_groups, kv_heads, group;  // group: query heads a key/value head
     int n_seqs, max_q, max_kv, causal, window;
     float scale_log2;
+    int ring_bytes;
     int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
     int split;              // 0: one CTA an item; 1: items cut where the CTAs' shares end
     float* part;            // [ctas][2][rows][D + 2]
@@ -68,10 +69,17 @@ AttnKernel attn_kernel_f32(int NB);
 AttnKernel attn_kernel_f16(int NB);
 AttnKernel attn_kernel_bf16(int NB);
 
+// Shared memory: the ring, later the joined rows, and the rows of q.
+inline int attn_ring_bytes(int D, int row_warps, int tile_rows) {
+    const int ring = ATTN_WARPS / row_warps * ATTN_STAGES * record_bytes(D), rows = ATTN_WARPS * tile_rows * D * 4;
+    return ring > rows ? ring : rows;
+}
+inline int attn_q_bytes(int D, int row_warps) { return row_warps * (D / QK) * 1024; }
+
 // Rows of a warp's tile.
 __host__ __device__ constexpr int attn_tile_rows(int dtype) { return dtype == QMM_F32 ? 8 : 16; }
 // CTAs an SM by registers (launch bound).
-constexpr int attn_ctas(int NB) { return NB <= 4 ? 3 : 2; }
+constexpr int attn_ctas(int NB) { return NB <= 2 ? 4 : NB <= 4 ? 3 : 2; }
 
 #ifdef __CUDACC__
 namespace attn {
@@ -132,9 +140,12 @@ __device__ __forceinline__ float2 unpack_half(unsigned w) {
 // Two codes q = u - 8 as fp16: nibbles 0 and 4 of w (HIGH: 16 q of nibbles 1
 // and 5).  An OR into fp16's exponent makes 1024 + u (1024 + 16 u), minus
 // 1024 + 8 (1024 + 128); exact.
+// `magic` is 0x64006400 in a register: with both constants as
+// immediates the compiler needs two operations where one does.
 template <int HIGH>
-__device__ __forceinline__ unsigned signed_codes(unsigned w) {
-    const unsigned bits = (w & (HIGH ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+__device__ __forceinline__ unsigned signed_codes(unsigned w, unsigned magic) {
+    unsigned bits;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(bits) : "r"(w), "n"(HIGH ? 0x00F000F0u : 0x000F000Fu), "r"(magic));
     const __half2 q =
         __hsub2(*reinterpret_cast<const __half2*>(&bits), __float2half2_rn(HIGH ? 1152.f : 1032.f));
     return *reinterpret_cast<const unsigned*>(&q);
@@ -172,9 +183,9 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int block, int block_rows, int token_warps) {
     Span r = {0, 0, 0};
-    const int64_t r0 = (int64_t)block * block_rows, rows = (int64_t)s.n * a.group;
+    const int r0 = block * block_rows, rows = s.n * a.group;  // below 2^28 (checked on the host)
     if (r0 >= rows) return r;
-    const int i0 = (int)(r0 / a.group), i1 = (int)((min(r0 + block_rows, rows) - 1) / a.group);
+    const int i0 = r0 / a.group, i1 = (min(r0 + block_rows, rows) - 1) / a.group;
     r.hi = a.causal ? max(0, min(s.L, s.L - s.n + i1 + 1)) : s.L;
     r.lo = a.window ? max(0, s.L - s.n + i0 - a.window + 1) : 0;
     if (r.lo >= r.hi) {
@@ -186,78 +197,72 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int blo
     return r;
 }
 
-// A place in the list of all units, ordered by (sequence, row block, head,
-// unit).
-struct Place {
-    int entry, head, unit;  // entry: sequence * blocks + row block
+// A CTA's share [u0, u1) of all units, ordered by (sequence, row block, head,
+// unit), and where u0 lies.  entry: sequence * blocks + row block.
+struct Share {
+    int total;  // units of one head
+    int warp_units[ATTN_WARPS];
+    int entry, start, units;  // the entry of u0, units before it (all heads) and its own (one head)
 };
 
-// The CTA's share [u0, u1) of all units and where u0 lies.
-struct Scan {
-    int64_t total;
-    int64_t warp_sum[ATTN_WARPS];
-    Place at;
-};
+__device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries, int block_rows, int token_warps,
+                                           bool report) {
+    if (e >= entries) return 0;
+    const int b = a.blocks == 1 ? e : e / a.blocks;
+    return span_of(a, sequence(a, b, report), e - b * a.blocks, block_rows, token_warps).units;
+}
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+// Inclusive sum of v over the block's threads and the block's total.
+__device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(FULL, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) warp_units[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < ATTN_WARPS; ++w) {
+        const int x = warp_units[w];
+        if (w < warp) v += x;
+        total += x;
+    }
     return v;
 }
 
-__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int token_warps, Scan& sc, int64_t& u0, int64_t& u1,
-                           int64_t& share) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int entries = a.n_seqs * a.blocks;
-    int64_t mine = 0;
+// Up to ATTN_THREADS entries are read once; more in two rounds (their units,
+// then the place of u0).  The units of all heads fit 31 bits (checked on the
+// host).
+__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int token_warps, Share& sh, int& u0,
+                                           int& u1, int& share) {
+    const int tid = threadIdx.x, entries = a.n_seqs * a.blocks;
+    const bool one = entries <= ATTN_THREADS;
+    int units = 0, mine = 0, total;
     for (int e = tid; e < entries; e += ATTN_THREADS) {
-        const int b = e / a.blocks;
-        mine += span_of(a, sequence(a, b, blockIdx.x == 0), e - b * a.blocks, block_rows, token_warps).units;
+        units = entry_units(a, e, entries, block_rows, token_warps, blockIdx.x == 0);
+        mine += units;
     }
-    mine = warp_sum64(mine);
-    if (lane == 0) sc.warp_sum[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < ATTN_WARPS; ++w) total += sc.warp_sum[w];
-    total *= a.kv_heads;
-    share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
-    u0 = share * blockIdx.x;
-    u1 = min(u0 + share, total);
-    __syncthreads();
+    int incl = block_scan(mine, sh.warp_units, total);
+    const int all = total * a.kv_heads;
+    share = max((int)(((unsigned)all + gridDim.x - 1) / gridDim.x), 1);
+    u0 = (int)min((int64_t)share * blockIdx.x, (int64_t)all);
+    u1 = (int)min((int64_t)u0 + share, (int64_t)all);
     if (u0 >= u1) return;
-    int64_t before = 0;  // units of the entries before this chunk, times the heads
-    for (int base = 0; base < entries && before <= u0; base += ATTN_THREADS) {
-        const int e = base + tid;
-        int units = 0;
-        if (e < entries) {
-            const int b = e / a.blocks;
-            units = span_of(a, sequence(a, b, false), e - b * a.blocks, block_rows, token_warps).units;
+    int before = 0;
+    for (int base = 0; base < entries; base += ATTN_THREADS) {
+        if (!one) {
+            __syncthreads();
+            units = entry_units(a, base + tid, entries, block_rows, token_warps, false);
+            incl = block_scan(units, sh.warp_units, total);
         }
-        int64_t incl = units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(FULL, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sc.warp_sum[warp] = incl;
-        __syncthreads();
-        int64_t chunk = 0, prior = 0;
-#pragma unroll
-        for (int w = 0; w < ATTN_WARPS; ++w) {
-            prior += w < warp ? sc.warp_sum[w] : 0;
-            chunk += sc.warp_sum[w];
-        }
-        const int64_t start = before + (prior + incl - units) * a.kv_heads;
-        if (units && u0 >= start && u0 < start + (int64_t)units * a.kv_heads) {
-            const int64_t off = u0 - start;
-            sc.at.entry = e;
-            sc.at.head = (int)(off / units);
-            sc.at.unit = (int)(off % units);
-        }
-        before += chunk * a.kv_heads;
-        __syncthreads();
+        const int start = before + (incl - units) * a.kv_heads;
+        if (units && u0 >= start && u0 - start < units * a.kv_heads)
+            sh.entry = base + tid, sh.start = start, sh.units = units;
+        before += total * a.kv_heads;
     }
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -284,13 +289,16 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int 
     }
 }
 
-// Exponents: 2^e <= the largest scale < 2^(e + 1), then 2^total times the
-// scale is below 2^15 and the weights' own factor 2^(part of it) at most 2^15.
+// Exponents: 2^e <= the largest scale < 2^(e + 1); weights are at most
+// 2^REF_SLACK, so 2^total times weight and scale is below 2^15, and the
+// weights' own factor 2^(part of total) at most 2^(15 - REF_SLACK).
 // Scales below 2^-7 take the rest of the factor themselves.
 __device__ __forceinline__ int scale_exponent(unsigned or_bits) {  // of fp16 scales' bits, OR-ed
     const unsigned m = (or_bits | or_bits >> 16) & 0x7C00;
     return (int)(m >> 10) - 15 + (m == 0);  // subnormal scales count as 2^-14
 }
+
+constexpr int REF_SLACK = 5;
 
 template <int NB, int DTYPE>
 __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const __grid_constant__ AttnArgs a) {
@@ -298,11 +306,12 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     constexpr int D = NB * 32, REC = record_bytes(D), ROWS = attn_tile_rows(DTYPE);
     constexpr int RS = SPLIT ? 1 : 2;  // rows a lane keeps statistics of
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Scan sc;
+    __shared__ Share sh;
     __shared__ float s_m[ATTN_WARPS][16], s_l[ATTN_WARPS][16];
     __shared__ uint64_t s_full[ATTN_WARPS][ATTN_STAGES];
     __shared__ int s_gone[ATTN_WARPS][ATTN_STAGES];  // the record's page does not exist
     __shared__ int s_abort;
+    __shared__ float s_seed[SPLIT ? 1 : ATTN_WARPS][NB][16];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -311,17 +320,25 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     const int block_rows = RW * ROWS;
     uint8_t* ring = smem + wt * (ATTN_STAGES * REC);
     uint64_t* full = s_full[wt];
+    unsigned magic;  // kept in a register (signed_codes)
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
     if (tid < ATTN_WARPS * ATTN_STAGES) mbar_init(&s_full[0][0] + tid, 1);
     if (tid == 0) s_abort = 0;
     fence_mbar_init();
 
-    Place at;
-    int64_t u0, u1, share = 0;
+    struct {
+        int entry, head, unit;
+    } at;
+    int u0, u1, share = 0;
     if (a.split) {
-        find_share(a, block_rows, TW, sc, u0, u1, share);  // synchronises the block
+        find_share(a, block_rows, TW, sh, u0, u1, share);  // synchronises the block
+        // the join kernel's blocks may come in beside the last of this one's (they wait for its end)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 >= u1) return;
-        at = sc.at;
+        at.entry = sh.entry;
+        at.head = (u0 - sh.start) / sh.units;
+        at.unit = u0 - sh.start - at.head * sh.units;
     } else {  // one CTA an item, later row blocks (more keys) first
         __syncthreads();
         const int e = blockIdx.x / a.kv_heads, b = e / a.blocks;
@@ -333,8 +350,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     }
 
     unsigned done = 0;  // records of this token group so far: stage and phase of the ring
-    for (int64_t u = u0; u < u1;) {
-        const int b = at.entry / a.blocks, block = at.entry - b * a.blocks;
+    for (int u = u0; u < u1;) {
+        const int b = a.blocks == 1 ? at.entry : at.entry / a.blocks, block = at.entry - b * a.blocks;
         const Seq seq = sequence(a, b, !a.split && tid == 0);
         const Span sp = span_of(a, seq, block, block_rows, TW);
         if (sp.units == 0) {
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             ++at.entry, at.head = 0, at.unit = 0;
             continue;
         }
-        const int unit_end = a.split ? (int)min((int64_t)sp.units, at.unit + (u1 - u)) : sp.units;
+        const int unit_end = a.split ? min(sp.units, at.unit + (u1 - u)) : sp.units;
         const int rec0 = sp.lo / GROUP + at.unit * TW + wt;
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * TW);
         const int n_mine = rec_end > rec0 ? (rec_end - rec0 + TW - 1) / TW : 0;
@@ -380,76 +397,125 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
         for (int k = 0; k < ATTN_STAGES - 1; ++k) issue(k);
 
-        // ---- the rows of this lane, q' as MMA operands
+        // ---- the rows of this lane; q' as MMA operands, its blocks spread over the token warps
         const int rows = seq.n * a.group;
         int lo[RS], hi[RS];
         float f[RS], seed[RS][NB];
-        unsigned qa[NB][2][4];  // [block][k step][a0..a3]
+        uint4* qa = reinterpret_cast<uint4*>(smem + a.ring_bytes) + wr * (NB * 64) + lane;  // [block][k step][lane]
+        constexpr int MINE = (NB + 3) / 4;  // blocks of a warp when there are four token warps
+        float x[RS][MINE][8];
+        const auto each_block = [&](auto&& body) {
+            if (TW == 4) {
+#pragma unroll
+                for (int i = 0; i < MINE; ++i)
+                    if (4 * i + wt < NB) body(x[0][i], x[RS - 1][i], 4 * i + wt);
+            } else {
+                for (int kb = wt; kb < NB; kb += TW) body(x[0][0], x[RS - 1][0], kb);
+            }
+        };
+        int64_t at_q[RS];
+        bool live[RS];
 #pragma unroll
         for (int r = 0; r < RS; ++r) {
             const int row = block * block_rows + wr * ROWS + g + 8 * r;
-            const bool live = row < rows;
-            const int i = live ? row / a.group : 0, h = live ? row - i * a.group : 0;
+            live[r] = row < rows;
+            const int i = live[r] ? row / a.group : 0, h = live[r] ? row - i * a.group : 0;
             const int p = seq.L - seq.n + i;
-            hi[r] = live && a.causal ? min(seq.L, p + 1) : sp.hi;
-            lo[r] = live && a.window ? p - a.window + 1 : sp.lo;
-            const int64_t at_q = (int64_t)(seq.q0 + i) * a.q.ts + (int64_t)(at.head * a.group + h) * a.q.hs;
-            float x[NB][8], top = 0.f;
+            hi[r] = live[r] && a.causal ? min(seq.L, p + 1) : sp.hi;
+            lo[r] = live[r] && a.window ? p - a.window + 1 : sp.lo;
+            at_q[r] = (int64_t)(seq.q0 + i) * a.q.ts + (int64_t)(at.head * a.group + h) * a.q.hs + 4 * c;
+        }
+        const auto load = [&](float* y, int r, int kb) {
+            if (!live[r]) {
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                if (live) {
-                    loadn<4>(a.q.data, at_q + 32 * k + 4 * c, DTYPE, a.q.wide, x[k]);
-                    loadn<4>(a.q.data, at_q + 32 * k + 16 + 4 * c, DTYPE, a.q.wide, x[k] + 4);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[k][e]));
+                for (int e = 0; e < 8; ++e) y[e] = 0.f;
+            } else if (a.q.wide) {  // both loads on their way before either is used
+                loadn<4>(a.q.data, at_q[r] + 32 * kb, DTYPE, 1, y);
+                loadn<4>(a.q.data, at_q[r] + 32 * kb + 16, DTYPE, 1, y + 4);
+            } else {
+                loadn<4>(a.q.data, at_q[r] + 32 * kb, DTYPE, 0, y);
+                loadn<4>(a.q.data, at_q[r] + 32 * kb + 16, DTYPE, 0, y + 4);
             }
-            top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+        };
+        float top[RS] = {};
+        each_block([&](float* x0, float* x1, int kb) {
+            load(x0, 0, kb);
+            if (!SPLIT) load(x1, RS - 1, kb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top[0] = fmaxf(top[0], fabsf(x0[e]));
+                if (!SPLIT) top[RS - 1] = fmaxf(top[RS - 1], fabsf(x1[e]));
+            }
+        });
+#pragma unroll
+        for (int r = 0; r < RS; ++r) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2));
+            if (TW > 1 && c == 0) s_m[warp][g + 8 * r] = top[r];
+        }
+        if (TW > 1) __syncthreads();
+        float mul[RS];
+#pragma unroll
+        for (int r = 0; r < RS; ++r) {
+            for (int t = 0; TW > 1 && t < TW; ++t) top[r] = fmaxf(top[r], s_m[wr * TW + t][g + 8 * r]);
             // top * 2^up in [2^13, 2^14); a negative scale goes into q', a scale of 0 makes it 0
-            const int up = top > 0.f ? 13 - min(max(ilogbf(top), -100), 100) : 0;
-            const float mul = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
+            const int up = top[r] > 0.f ? 13 - min(max(ilogbf(top[r]), -100), 100) : 0;
+            mul[r] = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
             // a masked nibble as it is (16-bit types) is the subnormal u 2^-24
             f[r] = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)((SPLIT ? 0 : 24) - up));
+        }
+        each_block([&](float* x0, float* x1, int kb) {
+            if (TW != 4) {
+                load(x0, 0, kb);
+                if (!SPLIT) load(x1, RS - 1, kb);
+            }
+            float sum[RS] = {};
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                float sum = 0.f;
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[k][e] * (e < 4 ? mul : mul * 0.0625f);  // high nibbles weigh 16
+            for (int st = 0; st < 2; ++st) {
                 // order of the operand's k places: values 4c, 4c+2 | 4c+1, 4c+3 of each half of the block
+                unsigned h[2][2];  // [row][k places]
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const unsigned h0 = pack_half(y[4 * st], y[4 * st + 2]);
-                    const unsigned h1 = pack_half(y[4 * st + 1], y[4 * st + 3]);
-                    const float2 a0 = unpack_half(h0), a1 = unpack_half(h1);
-                    qa[k][st][r] = h0;
-                    qa[k][st][2 + r] = h1;
-                    if constexpr (SPLIT) {
-                        qa[k][st][1] = pack_half(y[4 * st] - a0.x, y[4 * st + 2] - a0.y);
-                        qa[k][st][3] = pack_half(y[4 * st + 1] - a1.x, y[4 * st + 3] - a1.y);
+                for (int r = 0; r < RS; ++r) {
+                    const float by = st ? mul[r] * 0.0625f : mul[r];  // high nibbles weigh 16
+                    const float* y = (r ? x1 : x0) + 4 * st;
+                    const float y0 = y[0] * by, y1 = y[1] * by, y2 = y[2] * by, y3 = y[3] * by;
+                    h[r][0] = pack_half(y0, y2);
+                    h[r][1] = pack_half(y1, y3);
+                    const float2 p0 = unpack_half(h[r][0]), p1 = unpack_half(h[r][1]);
+                    if (SPLIT) {
+                        h[1][0] = pack_half(y0 - p0.x, y2 - p0.y);
+                        h[1][1] = pack_half(y1 - p1.x, y3 - p1.y);
                     } else {
-                        const float part = a0.x + a0.y + a1.x + a1.y;
-                        sum += st ? 16.f * part : part;
+                        const float part = p0.x + p0.y + p1.x + p1.y;
+                        sum[r] += st ? 16.f * part : part;
                     }
                 }
-                if constexpr (!SPLIT) {
-                    sum += __shfl_xor_sync(FULL, sum, 1);
-                    sum += __shfl_xor_sync(FULL, sum, 2);
-                    seed[r][k] = sum * (-8.f * 5.9604644775390625e-8f);  // -8 in units of 2^-24
+                qa[(2 * kb + st) * 32] = make_uint4(h[0][0], h[1][0], h[0][1], h[1][1]);
+            }
+            if (!SPLIT) {
+#pragma unroll
+                for (int r = 0; r < RS; ++r) {
+                    sum[r] += __shfl_xor_sync(FULL, sum[r], 1);
+                    sum[r] += __shfl_xor_sync(FULL, sum[r], 2);
+                    if (c == 0) s_seed[wr][kb][g + 8 * r] = sum[r] * (-8.f * 5.9604644775390625e-8f);  // -8 2^-24
                 }
             }
+        });
+        __syncthreads();
+        if (!SPLIT) {
+#pragma unroll
+            for (int r = 0; r < RS; ++r)
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) seed[r][kb] = s_seed[wr][kb][g + 8 * r];
         }
 
         float acc[NB][4][4] = {};  // [block][n tile][rows g: 2 columns, rows g + 8 (or lo parts): 2 columns]
-        float top[RS], l[RS];      // running maximum of the scores (before f) and sum of the weights
-        int total = 1000;          // acc holds the weighted v times 2^total, from the largest scale so far
-        float vs = 1.f, ds = 1.f;  // 2^total = vs (on the weights) * ds (on the scales)
+        float ref[RS], l[RS];      // reference of the weights, w = exp2(s - ref), and their sum
+        int total = 1000;          // acc holds the weighted v times a power of two, from the largest scale so far
+        float vs = 1.f, ds = 1.f;  // that power as vs (on the weights) * ds (on the scales)
+        float unscale = 1.f;       // 1 / (vs * ds)
 #pragma unroll
-        for (int r = 0; r < RS; ++r) top[r] = -INFINITY, l[r] = 0.f;
+        for (int r = 0; r < RS; ++r) ref[r] = -INFINITY, l[r] = 0.f;
 
         for (int k = 0; k < n_mine; ++k) {
             sync_group();  // the record before is read
@@ -474,18 +540,20 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
                 const uint4 d4 = lds128(rec + NB * 1024 + kb * 64 + c * 16);
                 const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+                const uint4 q0 = qa[2 * kb * 32], q1 = qa[(2 * kb + 1) * 32];
+                const unsigned qa0[4] = {q0.x, q0.y, q0.z, q0.w}, qa1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float t[4];
                     const unsigned w8 = w[j] >> 8;
                     const float2 dk = unpack_half(d[j]);
                     if constexpr (SPLIT) {
-                        mma_from(t, qa[kb][0], signed_codes<0>(w[j]), signed_codes<0>(w8), 0.f, 0.f);
-                        mma_add(t, qa[kb][1], signed_codes<1>(w[j]), signed_codes<1>(w8));
+                        mma_from(t, qa0, signed_codes<0>(w[j], magic), signed_codes<0>(w8, magic), 0.f, 0.f);
+                        mma_add(t, qa1, signed_codes<1>(w[j], magic), signed_codes<1>(w8, magic));
                         s[j][0] = fma2(dk, add2(make_float2(t[0], t[1]), make_float2(t[2], t[3])), s[j][0]);
                     } else {
-                        mma_from(t, qa[kb][0], w[j] & 0x000F000Fu, w8 & 0x000F000Fu, seed[0][kb], seed[RS - 1][kb]);
-                        mma_add(t, qa[kb][1], w[j] & 0x00F000F0u, w8 & 0x00F000F0u);
+                        mma_from(t, qa0, w[j] & 0x000F000Fu, w8 & 0x000F000Fu, seed[0][kb], seed[RS - 1][kb]);
+                        mma_add(t, qa1, w[j] & 0x00F000F0u, w8 & 0x00F000F0u);
                         s[j][0] = fma2(dk, make_float2(t[0], t[1]), s[j][0]);
                         s[j][RS - 1] = fma2(dk, make_float2(t[2], t[3]), s[j][RS - 1]);
                     }
@@ -508,66 +576,62 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                     }
             }
 
-            // scales of v, and the power of two that they and the weights share
-            unsigned vd[NB][4], any = 0;
+            // Scales of v, and the power of two that they and the weights share.
+            // Keys that no row of the block sees may hold anything: their
+            // scales become zeros (each warp of the token group writes the
+            // same ones).
+            uint8_t* vscale = ring + stage * REC + NB * 1088;
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < NB; ++t) {
+                    const int key = tok0 + lane;
+                    if (gone || key < sp.lo || key >= sp.hi)
+                        *reinterpret_cast<unsigned short*>(vscale + t * 64 + scale_at(lane)) = 0;
+                }
+                __syncwarp();
+            }
+            unsigned any = 0;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                const uint4 d4 = lds128(rec + NB * 1088 + kb * 64 + c * 16);
-                vd[kb][0] = d4.x, vd[kb][1] = d4.y, vd[kb][2] = d4.z, vd[kb][3] = d4.w;
-                if (masked) {  // keys that no row of the block sees may hold anything
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = tok0 + 8 * j + 2 * c;
-                        if (gone || key < sp.lo || key >= sp.hi) vd[kb][j] &= 0xFFFF0000u;
-                        if (gone || key + 1 < sp.lo || key + 1 >= sp.hi) vd[kb][j] &= 0x0000FFFFu;
-                    }
-                }
-                any |= vd[kb][0] | vd[kb][1];
-                any |= vd[kb][2] | vd[kb][3];
+                const uint4 d4 = lds128(vscale + kb * 64 + c * 16);
+                any |= d4.x | d4.y;
+                any |= d4.z | d4.w;
             }
             any |= __shfl_xor_sync(FULL, any, 1);
             any |= __shfl_xor_sync(FULL, any, 2);
-            const int room = 14 - scale_exponent(any);
+            const int room = 14 - REF_SLACK - scale_exponent(any);
             float ratio = 1.f;
             if (room < total) {
                 const int before = total;
                 total = room;
-                const int w = total > 21 ? 15 : min(total, 15);
+                const int w = min(total, 15 - REF_SLACK);
                 vs = exp2f((float)w);
-                ds = total > 21 ? exp2f((float)(total - w)) : 1.f;
-                // 2^total stops at 2^15 where the scales take none of it
-                ratio = before > 100 ? 1.f : vs * ds * exp2f((float)-(before > 21 ? before : min(before, 15)));
+                ds = total > 21 - REF_SLACK ? exp2f((float)(total - w)) : 1.f;
+                ratio = before > 100 ? 1.f : vs * ds * unscale;
+                unscale = 1.f / (vs * ds);
             }
-            if (ds != 1.f) {
-#pragma unroll
-                for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 d = unpack_half(vd[kb][j]);
-                        vd[kb][j] = pack_half(d.x * ds, d.y * ds);
-                    }
-            }
-
-            // weights
-            float ref[RS], alpha[RS];
+            // The reference follows the running maximum by steps of more than
+            // 2^REF_SLACK: few of them are left to rescale acc for.
+            float m[RS];
             bool moved = ratio != 1.f;
 #pragma unroll
             for (int r = 0; r < RS; ++r) {
-                float m = top[r];
+                m[r] = s[0][r].x;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(s[j][r].x, s[j][r].y));
-                m = fmaxf(m, __shfl_xor_sync(FULL, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(FULL, m, 2));
-                ref[r] = m == -INFINITY ? 0.f : m * f[r];  // nothing seen yet: every weight is 0
-                moved |= m != top[r];
-                alpha[r] = exp2_fast(fmaf(top[r], f[r], -ref[r]));
-                top[r] = m;
+                for (int j = 0; j < 4; ++j) m[r] = fmaxf(m[r], fmaxf(s[j][r].x, s[j][r].y));
+                m[r] *= f[r];  // f > 0
+                moved |= m[r] > ref[r] + REF_SLACK;
             }
             if (__any_sync(FULL, moved)) {
 #pragma unroll
                 for (int r = 0; r < RS; ++r) {
-                    l[r] *= alpha[r];
-                    const float by = alpha[r] * ratio;
+                    m[r] = fmaxf(m[r], __shfl_xor_sync(FULL, m[r], 1));
+                    m[r] = fmaxf(m[r], __shfl_xor_sync(FULL, m[r], 2));
+                    const float now = fmaxf(ref[r], m[r]);
+                    const float alpha = now == -INFINITY ? 0.f : exp2_fast(ref[r] - now);
+                    ref[r] = now;
+                    l[r] *= alpha;
+                    const float by = alpha * ratio;
 #pragma unroll
                     for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
@@ -577,12 +641,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                         }
                 }
             }
+            float use[RS];  // nothing seen yet: every weight is exp2(-inf - 0)
+#pragma unroll
+            for (int r = 0; r < RS; ++r) use[r] = ref[r] == -INFINITY ? 0.f : ref[r];
             unsigned ph[4][RS], pl[4];  // weights as fp16: hi parts (both rows), lo parts
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < RS; ++r) {
-                    const float2 x = fma2(s[j][r], make_float2(f[r], f[r]), make_float2(-ref[r], -ref[r]));
+                    const float2 x = fma2(s[j][r], make_float2(f[r], f[r]), make_float2(-use[r], -use[r]));
                     const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                     l[r] += w.x + w.y;
                     s[j][r] = mul2(w, make_float2(vs, vs));
@@ -597,12 +664,21 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 w4 = lds128(rec + NB * 512 + kb * 512 + lane * 16);
+                const uint4 d4 = lds128(vscale + kb * 64 + c * 16);
                 const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w};
+                unsigned vd[4] = {d4.x, d4.y, d4.z, d4.w};
+                if (ds != 1.f) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 d = unpack_half(vd[j]);
+                        vd[j] = pack_half(d.x * ds, d.y * ds);
+                    }
+                }
                 unsigned pa[2][4];  // A operands of the two k steps: rows 0..7, 8..15, two tokens each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     unsigned &up = pa[j >> 1][2 * (j & 1)], &dn = pa[j >> 1][2 * (j & 1) + 1];
-                    const __half2 d = as_half2(vd[kb][j]);
+                    const __half2 d = as_half2(vd[j]);
                     if constexpr (SPLIT) {
                         // (hi + lo) d as two parts: the product, and its exact error plus lo d
                         const __half2 h = as_half2(ph[j][0]), pr = __hmul2(h, d);
@@ -621,10 +697,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
                 for (int st = 0; st < 2; ++st) {
                     const unsigned x = w[2 * st], y = w[2 * st + 1], x8 = x >> 8, y8 = y >> 8;
-                    mma_add(acc[kb][0], pa[st], signed_codes<0>(x), signed_codes<0>(y));
-                    mma_add(acc[kb][1], pa[st], signed_codes<1>(x), signed_codes<1>(y));
-                    mma_add(acc[kb][2], pa[st], signed_codes<0>(x8), signed_codes<0>(y8));
-                    mma_add(acc[kb][3], pa[st], signed_codes<1>(x8), signed_codes<1>(y8));
+                    mma_add(acc[kb][0], pa[st], signed_codes<0>(x, magic), signed_codes<0>(y, magic));
+                    mma_add(acc[kb][1], pa[st], signed_codes<1>(x, magic), signed_codes<1>(y, magic));
+                    mma_add(acc[kb][2], pa[st], signed_codes<0>(x8, magic), signed_codes<0>(y8, magic));
+                    mma_add(acc[kb][3], pa[st], signed_codes<1>(x8, magic), signed_codes<1>(y8, magic));
                 }
             }
         }
@@ -635,17 +711,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         for (int r = 0; r < RS; ++r) {
             l[r] += __shfl_xor_sync(FULL, l[r], 1);
             l[r] += __shfl_xor_sync(FULL, l[r], 2);
-            top[r] *= f[r];  // -inf stays: f > 0
-            if (c == 0) s_m[warp][g + 8 * r] = top[r], s_l[warp][g + 8 * r] = l[r];
+            if (c == 0) s_m[warp][g + 8 * r] = ref[r], s_l[warp][g + 8 * r] = l[r];
         }
         __syncthreads();  // the ring is read
         float* buf = reinterpret_cast<float*>(smem);  // [warp][ROWS][D]
-        const float unscale = 1.f / (vs * ds);
 #pragma unroll
         for (int r = 0; r < RS; ++r) {
             float m = -INFINITY;
             for (int t = 0; t < TW; ++t) m = fmaxf(m, s_m[wr * TW + t][g + 8 * r]);
-            const float w = top[r] == -INFINITY ? 0.f : exp2_fast(top[r] - m) * unscale;
+            const float w = ref[r] == -INFINITY ? 0.f : exp2_fast(ref[r] - m) * unscale;
             float* o = buf + (warp * ROWS + g + 8 * r) * D;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb)
@@ -691,7 +765,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         }
         if (!a.split) return;
         if (tid == 0 && at.unit == 0) {
-            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (int)((u + sp.units - 1) / share);
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
             a.meta[(int64_t)at.entry * a.kv_heads + at.head] = AttnMeta{first, last, u != u0, 0};
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // buf is used before the ring's next copies
@@ -719,6 +793,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rows = min(block_rows, seq.n * a.group - block * block_rows);
     if (rows <= 0) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnMeta mt = a.meta[blockIdx.x];
     const int n = mt.last - mt.first + 1;
     if (n <= 1) return;

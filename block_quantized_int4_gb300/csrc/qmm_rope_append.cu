@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "qmm.h"
 #include "qmm_heads.cuh"
@@ -88,55 +89,77 @@ struct HeadsArgs {
     const int* pos;
     const int64_t* slots;
     uint8_t* cache;
-    int64_t n_slots, n_pos, warps;  // warps: T * (sum of groups)
+    int64_t n_slots, n_pos, warps;  // warps: T * (sum of groups), below 2^31
     int D, lanes, n_rot, pairs, page_size;
     int table_wide;
     float eps;
     int* err;
 };
 
-// The element of logical place s of a head: pairs of the rotation side by
-// side, then the values that pass.
-__device__ __forceinline__ int element_of(int s, int n_rot, int pairs) {
-    return pairs || s >= n_rot ? s : (s >> 1) + (s & 1) * (n_rot >> 1);
-}
-
-// A lane holds eight logical places (4 whole pairs), a power of two of
-// `lanes` lanes a head, 32 / lanes heads a warp: norm and rotation stay in
-// registers and sums cost log2(lanes) shuffles.  With halves of n_rot % 8 ==
-// 0 the eight are two runs of four elements, otherwise one run of eight.
-__device__ __forceinline__ void load_places(const Heads& h, int64_t at, int s0, int n_rot, int pairs, float* x) {
-    if (pairs || n_rot == 0 || (s0 >= n_rot && n_rot % 8 == 0)) {
-        loadn<8>(h.data, at + s0, h.dtype, h.wide, x);
-    } else if (n_rot % 8 == 0) {
-        float a[4], b[4];
-        loadn<4>(h.data, at + s0 / 2, h.dtype, h.wide, a);
-        loadn<4>(h.data, at + s0 / 2 + n_rot / 2, h.dtype, h.wide, b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[2 * j] = a[j], x[2 * j + 1] = b[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = load1(h.data, at + element_of(s0 + j, n_rot, pairs), h.dtype);
+// A lane holds eight values of a head, the runs A[0..3] and B[0..3], in a
+// power of two of `lanes` lanes a head and 32 / lanes heads a warp: norm and
+// rotation stay in registers and sums cost log2(lanes) shuffles.  Adjacent
+// pairs (PAIRS): A and B follow one another, pairs (A0, A1), (A2, A3), (B0, B1),
+// (B2, B3).  Halves: pairs (Aj, Bj), A in the lower and B in the upper half of
+// the rotated part; lanes past it hold what passes.  In the FAST kernels runs
+// are whole aligned vectors (n_rot % 8 == 0 for halves, and 16-byte heads);
+// else every value has its own place.
+template <bool PAIRS, bool FAST>
+struct Places {
+    int s0, n_rot, a0, b0;
+    __device__ Places(int first, int rot) : s0(first), n_rot(rot) {
+        const bool halves = !PAIRS && first < rot;
+        a0 = halves ? first >> 1 : first;
+        b0 = halves ? (first >> 1) + (rot >> 1) : first + 4;
     }
-}
+    // Element of value j (A then B).
+    __device__ int element(int j) const {
+        if (FAST || PAIRS || n_rot == 0) return j < 4 ? a0 + j : b0 + j - 4;
+        const int s = s0 + 2 * (j & 3) + (j >> 2);  // pairs side by side
+        return s >= n_rot ? s : (s >> 1) + (s & 1) * (n_rot >> 1);
+    }
+    // Whether pair j is rotated, and the values that it is made of.
+    __device__ bool rotated(int j) const { return s0 + 2 * j < n_rot; }
+    static __device__ int first(int j) { return PAIRS ? 2 * j : j; }
+    static __device__ int second(int j) { return PAIRS ? 2 * j + 1 : j + 4; }
+};
 
-__device__ __forceinline__ void store_places(const Heads& h, int64_t at, int s0, int n_rot, int pairs,
-                                             const float* x) {
-    if (pairs || n_rot == 0 || (s0 >= n_rot && n_rot % 8 == 0)) {
-        storen<8>(h.data, at + s0, h.dtype, h.wide, x);
-    } else if (n_rot % 8 == 0) {
-        const float a[4] = {x[0], x[2], x[4], x[6]}, b[4] = {x[1], x[3], x[5], x[7]};
-        storen<4>(h.data, at + s0 / 2, h.dtype, h.wide, a);
-        storen<4>(h.data, at + s0 / 2 + n_rot / 2, h.dtype, h.wide, b);
+// The bits of a lane's eight values; loaded by themselves, so that several
+// heads' loads are on their way before the first is used.
+template <int DT>
+struct Raw {
+    using Run = typename std::conditional<DT == QMM_F32, uint4, uint2>::type;
+    Run a, b;
+    __device__ void load(const char* head, int a0, int b0) {
+        constexpr int size = DT == QMM_F32 ? 4 : 2;
+        a = __ldg(reinterpret_cast<const Run*>(head + a0 * size));
+        b = __ldg(reinterpret_cast<const Run*>(head + b0 * size));
+    }
+    __device__ void values(float* x) const {
+        if constexpr (DT == QMM_F32) {
+            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z);
+            x[3] = __uint_as_float(a.w), x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
+            x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+        } else {
+            unpack2(a.x, DT, x), unpack2(a.y, DT, x + 2), unpack2(b.x, DT, x + 4), unpack2(b.y, DT, x + 6);
+        }
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ void store_runs(char* head, int a0, int b0, const float* x) {
+    if constexpr (DT == QMM_F32) {
+        *reinterpret_cast<float4*>(head + a0 * 4) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(head + b0 * 4) = make_float4(x[4], x[5], x[6], x[7]);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) store1(h.data, at + element_of(s0 + j, n_rot, pairs), x[j], h.dtype);
+        *reinterpret_cast<uint2*>(head + a0 * 2) = make_uint2(pack2(x[0], x[1], DT), pack2(x[2], x[3], DT));
+        *reinterpret_cast<uint2*>(head + b0 * 2) = make_uint2(pack2(x[4], x[5], DT), pack2(x[6], x[7], DT));
     }
 }
 
 // cos and sin of the lane's four pairs, where they are rotated.
-__device__ __forceinline__ void load_turns(const HeadsArgs& a, int64_t p, int s0, float2* cs) {
-    const float2* row = a.table + p * (a.n_rot / 2);
+__device__ __forceinline__ void load_turns(const HeadsArgs& a, int p, int s0, float2* cs) {
+    const float2* row = a.table + (int64_t)p * (a.n_rot / 2);
     if (a.table_wide && s0 + 8 <= a.n_rot) {
         const float4 u = __ldg(reinterpret_cast<const float4*>(row + s0 / 2));
         const float4 v = __ldg(reinterpret_cast<const float4*>(row + s0 / 2 + 2));
@@ -151,106 +174,10 @@ __device__ __forceinline__ void load_turns(const HeadsArgs& a, int64_t p, int s0
 
 constexpr int HEAD_WARPS = 8;
 
-// One warp: 32 / lanes heads of one token, of q, k or v.
-__global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_constant__ HeadsArgs a) {
-    __shared__ float stage[HEAD_WARPS][32 * 8 + 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t id = blockIdx.x * (int64_t)HEAD_WARPS + warp;
-    if (id >= a.warps) return;
-    const int per_token = a.groups[0] + a.groups[1] + a.groups[2];
-    const int64_t t = id / per_token;
-    int i = (int)(id - t * per_token), kind = GROUP_Q;
-    while (i >= a.groups[kind]) i -= a.groups[kind++];
-    const Heads& in = a.in[kind];
-    const int sub = lane / a.lanes, u = lane - sub * a.lanes;
-    const int head = i * (32 / a.lanes) + sub, s0 = u * 8;
-    const bool live = head < a.heads[kind] && s0 < a.D;
-    const int n_rot = kind == GROUP_V ? 0 : a.n_rot;
-
-    float x[8] = {};
-    if (live) load_places(in, t * in.ts + head * in.hs, s0, n_rot, a.pairs, x);
-    float2 cs[4];
-    if (a.n_rot) {
-        const int p = a.pos[t];
-        if (p < 0 || p >= a.n_pos) {  // the whole warp: one token
-            if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
-            return;
-        }
-        if (kind != GROUP_V) load_turns(a, p, s0, cs);
-    }
-    int64_t slot = 0;
-    if (kind != GROUP_Q) {
-        slot = a.slots[t];
-        if (slot < 0) return;
-        if (slot >= a.n_slots) {
-            if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
-            return;
-        }
-    }
-
-    if (kind == GROUP_Q) {  // fp32, rounded once to the output's type
-        if (a.norm[GROUP_Q]) {
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-            for (int o = a.lanes / 2; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-            const float r = 1.f / sqrtf(s / a.D + a.eps);
-            if (live) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * r * a.norm[GROUP_Q][element_of(s0 + j, n_rot, a.pairs)];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (s0 + 2 * j < n_rot) {
-                const float p = x[2 * j], q = x[2 * j + 1];
-                x[2 * j] = p * cs[j].x - q * cs[j].y;
-                x[2 * j + 1] = q * cs[j].x + p * cs[j].y;
-            }
-        }
-        if (live) store_places(a.out, t * a.out.ts + head * a.out.hs, s0, n_rot, a.pairs, x);
-        return;
-    }
-
-    if (kind == GROUP_K) {  // pairs of fp32 up to the one rounding that the codes depend on
-        Two r = {1.f, 0.f};
-        const bool norm = a.norm[GROUP_K] != nullptr;
-        if (norm) {
-            Two s = {0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = add(s, two_prod(x[j], x[j]));
-            for (int o = a.lanes / 2; o; o >>= 1)
-                s = add(s, Two{__shfl_xor_sync(FULL, s.h, o), __shfl_xor_sync(FULL, s.l, o)});
-            r = rms_inverse(s, a.D, a.eps);
-        }
-        float* st = stage[warp] + sub * a.D;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            Two p = {x[2 * j], 0.f}, q = {x[2 * j + 1], 0.f};
-            const int ep = element_of(s0 + 2 * j, n_rot, a.pairs), eq = element_of(s0 + 2 * j + 1, n_rot, a.pairs);
-            if (norm && live) {
-                p = mul(r, two_prod(p.h, a.norm[GROUP_K][ep]));
-                q = mul(r, two_prod(q.h, a.norm[GROUP_K][eq]));
-            }
-            if (s0 + 2 * j < n_rot) {
-                const Two pc = mul(p, cs[j].x), qs = mul(q, -cs[j].y), qc = mul(q, cs[j].x), ps = mul(p, cs[j].y);
-                p = add(pc, qs);
-                q = add(qc, ps);
-            }
-            if (live) {
-                st[ep] = __fadd_rn(p.h, p.l);
-                st[eq] = __fadd_rn(q.h, q.l);
-            }
-        }
-        __syncwarp();
-        if (live) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = st[s0 + j];
-        }
-    }
-
-    // Q4_0 of a block of 32 on four lanes: lane r holds values 8r .. 8r + 7.
-    const int r = u & 3;
+// Q4_0 of a block of 32 on four lanes (lane r of them holds values 8r .. 8r +
+// 7 in x), written to its places in the cache.
+__device__ __forceinline__ void quantize_store(const HeadsArgs& a, int kind, const float* x, bool live, int blk, int r,
+                                               uint8_t* rec, int tok) {
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
@@ -263,11 +190,7 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
         const float q = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(x[j], d)), -8.f), 7.f) : 0.f;
         code[j] = (unsigned)((int)q + 8);
     }
-    const int rec = record_bytes(a.D), NB = a.D / QK;
-    const int64_t page = slot / a.page_size;
-    const int in_page = (int)(slot - page * a.page_size), tok = in_page & 31;
-    uint8_t* base = a.cache + ((page * a.heads[kind] + head) * (a.page_size / GROUP) + in_page / GROUP) * rec;
-    const int blk = u >> 2;
+    const int NB = a.D / QK;
     if (kind == GROUP_K) {
         // low nibbles (values 0..15) on lanes 0, 1; high ones on lanes 2, 3
         unsigned w0 = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
@@ -277,9 +200,9 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
         w1 |= __shfl_xor_sync(FULL, w1, 2);
         if (live) {
             const int word = 2 * (r & 1) + (r >> 1);
-            *reinterpret_cast<unsigned*>(base + blk * 512 + k_word_at(tok, word)) = r >> 1 ? w1 : w0;
+            *reinterpret_cast<unsigned*>(rec + blk * 512 + k_word_at(tok, word)) = r >> 1 ? w1 : w0;
             if (r == 0)
-                *reinterpret_cast<unsigned short*>(base + NB * 1024 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
+                *reinterpret_cast<unsigned short*>(rec + NB * 1024 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
         }
     } else {
         // lane r's values 8r + e are nibble r of unit e
@@ -292,13 +215,157 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
         }
         if (live) {
             const unsigned v = r == 0 ? w[0] : r == 1 ? w[1] : r == 2 ? w[2] : w[3];
-            uint8_t* vb = base + NB * 512 + blk * 512;
+            uint8_t* vb = rec + NB * 512 + blk * 512;
             *reinterpret_cast<unsigned short*>(vb + v_unit_at(tok, 2 * r)) = (unsigned short)(v & 0xffff);
             *reinterpret_cast<unsigned short*>(vb + v_unit_at(tok, 2 * r + 1)) = (unsigned short)(v >> 16);
             if (r == 0)
-                *reinterpret_cast<unsigned short*>(base + NB * 1088 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
+                *reinterpret_cast<unsigned short*>(rec + NB * 1088 + blk * 64 + scale_at(tok)) = f32_to_f16_bits(d);
         }
     }
+}
+
+// One warp: heads of one token, U times 32 / lanes of q (their loads are on
+// their way before the first is used; the token's turns are read once) or 32 /
+// lanes of k or v.  DT >= 0: every heads argument has this type and whole
+// aligned runs; DT < 0: any types and strides, value by value.
+template <int DT, bool PAIRS, int U>
+__global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_constant__ HeadsArgs a) {
+    constexpr bool FAST = DT >= 0;
+    __shared__ float stage[HEAD_WARPS][MAX_HEAD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned id = blockIdx.x * HEAD_WARPS + warp;
+    if (id >= (unsigned)a.warps) return;
+    const int per_token = a.groups[0] + a.groups[1] + a.groups[2];
+    const int t = (int)(id / (unsigned)per_token);
+    int i = (int)(id - (unsigned)t * per_token), kind = GROUP_Q;
+    while (i >= a.groups[kind]) i -= a.groups[kind++];
+    const Heads& in = a.in[kind];
+    const int sub = lane / a.lanes, u = lane - sub * a.lanes, per = 32 / a.lanes;
+    const int s0 = u * 8;
+    const bool inside = s0 < a.D;
+    const Places<PAIRS, FAST> at(s0, kind == GROUP_V ? 0 : a.n_rot);
+    const int64_t row = t * in.ts;
+
+    Raw<FAST ? DT : QMM_F32> raw[U];
+    const int head0 = (kind == GROUP_Q ? i * U : i) * per + sub;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        raw[k] = {};
+        if (FAST && (k == 0 || kind == GROUP_Q) && inside && head0 + k * per < a.heads[kind])
+            raw[k].load(in.data + (row + (head0 + k * per) * in.hs) * (DT == QMM_F32 ? 4 : 2), at.a0, at.b0);
+    }
+    float2 cs[4];
+    if (a.n_rot) {
+        const int p = a.pos[t];
+        if (p < 0 || p >= a.n_pos) {  // the whole warp: one token
+            if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
+            return;
+        }
+        if (kind != GROUP_V) load_turns(a, p, s0, cs);
+    }
+    float gamma[8];
+    const float* norm = kind == GROUP_V ? nullptr : a.norm[kind];
+    if (norm && inside) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gamma[j] = __ldg(norm + at.element(j));
+    }
+    float x[8];
+    const auto values = [&](int k, bool live) {
+        if (FAST) {
+            raw[k].values(x);
+        } else {
+            const int64_t head = row + (head0 + k * per) * in.hs;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = live ? load1(in.data, head + at.element(j), in.dtype) : 0.f;
+        }
+    };
+
+    if (kind == GROUP_Q) {  // fp32, rounded once to the output's type
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int head = head0 + k * per;
+            const bool live = inside && head < a.heads[GROUP_Q];
+            values(k, live);
+            if (norm) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
+                for (int o = a.lanes / 2; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+                const float r = 1.f / sqrtf(s / a.D + a.eps);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * r * gamma[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (at.rotated(j)) {
+                    float &f = x[at.first(j)], &g = x[at.second(j)];
+                    const float p = f, q = g;
+                    f = p * cs[j].x - q * cs[j].y;
+                    g = q * cs[j].x + p * cs[j].y;
+                }
+            }
+            const int64_t to = t * a.out.ts + head * a.out.hs;
+            if (live) {
+                if constexpr (FAST) {
+                    store_runs<DT>(a.out.data + to * (DT == QMM_F32 ? 4 : 2), at.a0, at.b0, x);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) store1(a.out.data, to + at.element(j), x[j], a.out.dtype);
+                }
+            }
+        }
+        return;
+    }
+
+    const int64_t slot = a.slots[t];
+    if (slot < 0) return;
+    if (slot >= a.n_slots) {
+        if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
+        return;
+    }
+    const bool live = inside && head0 < a.heads[kind];
+    values(0, live);
+    if (kind == GROUP_K) {  // pairs of fp32 up to the one rounding that the codes depend on
+        Two r = {1.f, 0.f};
+        if (norm) {
+            Two s = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = add(s, two_prod(x[j], x[j]));
+            for (int o = a.lanes / 2; o; o >>= 1)
+                s = add(s, Two{__shfl_xor_sync(FULL, s.h, o), __shfl_xor_sync(FULL, s.l, o)});
+            r = rms_inverse(s, a.D, a.eps);
+        }
+        float* st = stage[warp] + sub * a.D;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int jp = at.first(j), jq = at.second(j);
+            Two p = {x[jp], 0.f}, q = {x[jq], 0.f};
+            if (norm) {
+                p = mul(r, two_prod(p.h, gamma[jp]));
+                q = mul(r, two_prod(q.h, gamma[jq]));
+            }
+            if (at.rotated(j)) {
+                const Two pc = mul(p, cs[j].x), qs = mul(q, -cs[j].y), qc = mul(q, cs[j].x), ps = mul(p, cs[j].y);
+                p = add(pc, qs);
+                q = add(qc, ps);
+            }
+            if (live) {
+                st[at.element(jp)] = __fadd_rn(p.h, p.l);
+                st[at.element(jq)] = __fadd_rn(q.h, q.l);
+            }
+        }
+        __syncwarp();
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = st[s0 + j];
+        }
+    }
+    const int64_t page =
+        (unsigned long long)slot >> 32 ? slot / a.page_size : (int64_t)((unsigned)slot / (unsigned)a.page_size);
+    const int in_page = (int)(slot - page * a.page_size);
+    uint8_t* rec = a.cache + ((page * a.heads[kind] + head0) * (a.page_size / GROUP) + in_page / GROUP) *
+                                 (int64_t)record_bytes(a.D);
+    quantize_store(a, kind, x, live, u >> 2, u & 3, rec, in_page & 31);
 }
 
 struct ReadArgs {
@@ -313,12 +380,12 @@ struct ReadArgs {
 // The values of cached tokens: a lane holds eight values of a head, as above.
 __global__ void __launch_bounds__(HEAD_WARPS * 32) kv_read_kernel(const __grid_constant__ ReadArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t id = blockIdx.x * (int64_t)HEAD_WARPS + (threadIdx.x >> 5);
-    if (id >= a.warps) return;
+    const unsigned id = blockIdx.x * HEAD_WARPS + (threadIdx.x >> 5);
+    if (id >= (unsigned)a.warps) return;
     const int per = (a.heads + 32 / a.lanes - 1) / (32 / a.lanes);
-    const int64_t t = id / per;
+    const int t = (int)(id / (unsigned)per);
     const int sub = lane / a.lanes, u = lane - sub * a.lanes;
-    const int head = (int)(id - t * per) * (32 / a.lanes) + sub, s0 = u * 8;
+    const int head = (int)(id - (unsigned)t * per) * (32 / a.lanes) + sub, s0 = u * 8;
     if (head >= a.heads || s0 >= a.D) return;
     const int64_t slot = a.slots[t];
     if (slot >= a.n_slots) {
@@ -328,7 +395,8 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) kv_read_kernel(const __grid_c
     float x[8] = {}, y[8] = {};
     if (slot >= 0) {
         const int NB = a.D / QK, blk = u >> 2, r = u & 3;
-        const int64_t page = slot / a.page_size;
+        const int64_t page =
+            (unsigned long long)slot >> 32 ? slot / a.page_size : (int64_t)((unsigned)slot / (unsigned)a.page_size);
         const int in_page = (int)(slot - page * a.page_size), tok = in_page & 31;
         const uint8_t* base = a.cache + ((page * a.heads + head) * (a.page_size / GROUP) + in_page / GROUP) *
                                             (int64_t)record_bytes(a.D);
@@ -391,12 +459,46 @@ void set_rope(HeadsArgs& a, const qmm_rope& r, const int32_t* pos) {
     a.pos = pos;
 }
 
-constexpr int64_t MAX_BLOCKS = (int64_t(1) << 31) - 1;
+constexpr int64_t MAX_WARPS = (int64_t(1) << 31) - 64;
+constexpr int MANY = 4;  // q's head groups a warp takes when there is plenty of work
 
-qmm_status launch_heads(const HeadsArgs& a, void* stream) {
-    const int64_t blocks = (a.warps + HEAD_WARPS - 1) / HEAD_WARPS;
-    if (blocks > MAX_BLOCKS) return QMM_ERR_SHAPE;
-    heads_kernel<<<(unsigned)blocks, HEAD_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+// Warps of T tokens at `u` of q's head groups a warp.
+int64_t set_groups(HeadsArgs& a, int64_t T, int u) {
+    for (int g = 0; g < 3; ++g) a.groups[g] = groups_of(a.heads[g], a.lanes);
+    a.groups[GROUP_Q] = (a.groups[GROUP_Q] + u - 1) / u;
+    return T * (a.groups[0] + a.groups[1] + a.groups[2]);
+}
+
+template <int DT, bool PAIRS>
+void launch_form(const HeadsArgs& a, bool many, cudaStream_t st) {
+    const unsigned blocks = (unsigned)((a.warps + HEAD_WARPS - 1) / HEAD_WARPS);
+    if (DT >= 0 && many)
+        heads_kernel<DT, PAIRS, DT >= 0 ? MANY : 1><<<blocks, HEAD_WARPS * 32, 0, st>>>(a);
+    else
+        heads_kernel<DT, PAIRS, 1><<<blocks, HEAD_WARPS * 32, 0, st>>>(a);
+}
+
+qmm_status launch_heads(HeadsArgs& a, int64_t T, int sms, void* stream) {
+    int dt = -1;
+    bool fast = a.pairs || a.n_rot % 8 == 0;
+    const Heads* all[4] = {&a.in[0], &a.in[1], &a.in[2], &a.out};
+    for (const Heads* h : all) {
+        if (!h->data) continue;
+        fast &= h->wide && (dt < 0 || dt == h->dtype);
+        dt = h->dtype;
+    }
+    if (!fast) dt = -1;
+    a.warps = set_groups(a, T, MANY);
+    const bool many = dt >= 0 && a.warps >= 32 * (int64_t)sms;
+    if (!many) a.warps = set_groups(a, T, 1);
+    if (a.warps > MAX_WARPS) return QMM_ERR_SHAPE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    static constexpr void (*FORMS[4][2])(const HeadsArgs&, bool, cudaStream_t) = {
+        {launch_form<-1, false>, launch_form<-1, true>},
+        {launch_form<QMM_F32, false>, launch_form<QMM_F32, true>},
+        {launch_form<QMM_F16, false>, launch_form<QMM_F16, true>},
+        {launch_form<QMM_BF16, false>, launch_form<QMM_BF16, true>}};
+    FORMS[dt + 1][a.pairs](a, many, st);
     return status_of_launch();
 }
 
@@ -449,21 +551,19 @@ qmm_status qmm_rope_heads(const qmm_rope_op* op, void* stream) {
     if (qmm_status s = check_output(op->y, op->x.n_heads, op->T, op->head_dim)) return s;
     if (qmm_status s = check_rope(op->rope, op->head_dim, op->pos)) return s;
     if (misaligned(op->norm_w, 4)) return QMM_ERR_ALIGN;
-    int* err = device_error_word();
-    if (!err) return QMM_ERR_DEVICE;
+    int sms = 0, optin = 0;
+    if (!device_facts(&sms, &optin)) return QMM_ERR_DEVICE;
     HeadsArgs a = {};
     a.D = op->head_dim;
     a.lanes = lanes_of(a.D);
     a.in[GROUP_Q] = kernel_heads(op->x);
     a.out = kernel_heads(op->y);
     a.heads[GROUP_Q] = op->x.n_heads;
-    a.groups[GROUP_Q] = groups_of(op->x.n_heads, a.lanes);
     a.norm[GROUP_Q] = op->norm_w;
     a.eps = op->norm_eps;
-    a.err = err;
+    a.err = device_error_word();
     set_rope(a, op->rope, op->pos);
-    a.warps = op->T * a.groups[GROUP_Q];
-    return launch_heads(a, stream);
+    return launch_heads(a, op->T, sms, stream);
 }
 
 qmm_status qmm_kv_cache_bytes(const qmm_kv_cache* cache, size_t* bytes) {
@@ -487,8 +587,8 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
     if (qmm_status s = check_rope(op->rope, D, op->pos)) return s;
     if (!op->slots) return QMM_ERR_ARG;
     if (misaligned(op->slots, 8) || misaligned(op->k_norm, 4) || misaligned(op->q_norm, 4)) return QMM_ERR_ALIGN;
-    int* err = device_error_word();
-    if (!err) return QMM_ERR_DEVICE;
+    int sms = 0, optin = 0;
+    if (!device_facts(&sms, &optin)) return QMM_ERR_DEVICE;
     HeadsArgs a = {};
     a.D = D;
     a.lanes = lanes_of(D);
@@ -496,20 +596,18 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
     for (int g = op->q.data ? GROUP_Q : GROUP_K; g <= GROUP_V; ++g) {
         a.in[g] = kernel_heads(*in[g]);
         a.heads[g] = in[g]->n_heads;
-        a.groups[g] = groups_of(in[g]->n_heads, a.lanes);
     }
     if (op->q.data) a.out = kernel_heads(op->q_out);
     a.norm[GROUP_Q] = op->q_norm;
     a.norm[GROUP_K] = op->k_norm;
     a.eps = op->norm_eps;
-    a.err = err;
+    a.err = device_error_word();
     set_rope(a, op->rope, op->pos);
     a.slots = op->slots;
     a.cache = op->cache.data;
     a.page_size = op->cache.page_size;
     a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
-    a.warps = op->T * (a.groups[0] + a.groups[1] + a.groups[2]);
-    return launch_heads(a, stream);
+    return launch_heads(a, op->T, sms, stream);
 }
 
 qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream) {
@@ -536,9 +634,8 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream) {
     a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
     a.err = err;
     a.warps = op->T * groups_of(a.heads, a.lanes);
-    const int64_t blocks = (a.warps + HEAD_WARPS - 1) / HEAD_WARPS;
-    if (blocks > MAX_BLOCKS) return QMM_ERR_SHAPE;
-    kv_read_kernel<<<(unsigned)blocks, HEAD_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    if (a.warps > MAX_WARPS) return QMM_ERR_SHAPE;
+    kv_read_kernel<<<(unsigned)((a.warps + HEAD_WARPS - 1) / HEAD_WARPS), HEAD_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return status_of_launch();
 }
 

@@ -175,7 +175,7 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream() costs 3 us
     if isinstance(s, int):
         return s
     return s.cuda_stream
