@@ -45,7 +45,12 @@ __device__ __forceinline__ unsigned short f32_to_bits(float f, int dtype) {
     return dtype == QMM_F16 ? __half_as_ushort(__float2half_rn(f)) : __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 __device__ __forceinline__ unsigned pack2(float a, float b, int dtype) {
-    return (unsigned)f32_to_bits(a, dtype) | (unsigned)f32_to_bits(b, dtype) << 16;
+    if (dtype == QMM_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const unsigned*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned*>(&h);
 }
 __device__ __forceinline__ void unpack2(unsigned w, int dtype, float* v) {
     v[0] = bits_to_f32((unsigned short)(w & 0xffff), dtype);

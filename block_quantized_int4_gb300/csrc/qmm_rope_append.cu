@@ -92,7 +92,7 @@ struct HeadsArgs {
     int64_t n_slots, n_pos, warps;  // warps: T * (sum of groups), below 2^31
     int D, lanes, n_rot, pairs, page_size;
     int table_wide;
-    float eps;
+    float eps, inv_D;
     int* err;
 };
 
@@ -126,14 +126,19 @@ struct Places {
 
 // The bits of a lane's eight values; loaded by themselves, so that several
 // heads' loads are on their way before the first is used.
-template <int DT>
+template <int DT, bool PAIRS>
 struct Raw {
     using Run = typename std::conditional<DT == QMM_F32, uint4, uint2>::type;
     Run a, b;
     __device__ void load(const char* head, int a0, int b0) {
-        constexpr int size = DT == QMM_F32 ? 4 : 2;
-        a = __ldg(reinterpret_cast<const Run*>(head + a0 * size));
-        b = __ldg(reinterpret_cast<const Run*>(head + b0 * size));
+        if constexpr (DT != QMM_F32 && PAIRS) {  // one run of 16 bytes
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(head + a0 * 2));
+            a = make_uint2(v.x, v.y), b = make_uint2(v.z, v.w);
+        } else {
+            constexpr int size = DT == QMM_F32 ? 4 : 2;
+            a = __ldg(reinterpret_cast<const Run*>(head + a0 * size));
+            b = __ldg(reinterpret_cast<const Run*>(head + b0 * size));
+        }
     }
     __device__ void values(float* x) const {
         if constexpr (DT == QMM_F32) {
@@ -146,11 +151,14 @@ struct Raw {
     }
 };
 
-template <int DT>
+template <int DT, bool PAIRS>
 __device__ __forceinline__ void store_runs(char* head, int a0, int b0, const float* x) {
     if constexpr (DT == QMM_F32) {
         *reinterpret_cast<float4*>(head + a0 * 4) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4*>(head + b0 * 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else if constexpr (PAIRS) {
+        *reinterpret_cast<uint4*>(head + a0 * 2) = make_uint4(pack2(x[0], x[1], DT), pack2(x[2], x[3], DT),
+                                                              pack2(x[4], x[5], DT), pack2(x[6], x[7], DT));
     } else {
         *reinterpret_cast<uint2*>(head + a0 * 2) = make_uint2(pack2(x[0], x[1], DT), pack2(x[2], x[3], DT));
         *reinterpret_cast<uint2*>(head + b0 * 2) = make_uint2(pack2(x[4], x[5], DT), pack2(x[6], x[7], DT));
@@ -245,14 +253,18 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
     const bool inside = s0 < a.D;
     const Places<PAIRS, FAST> at(s0, kind == GROUP_V ? 0 : a.n_rot);
     const int64_t row = t * in.ts;
+    constexpr int SIZE = DT == QMM_F32 ? 4 : 2;
 
-    Raw<FAST ? DT : QMM_F32> raw[U];
+    Raw<FAST ? DT : QMM_F32, PAIRS> raw[U];
     const int head0 = (kind == GROUP_Q ? i * U : i) * per + sub;
+    const int left = inside ? a.heads[kind] - head0 : 0;  // head k of this lane exists where k * per < left
+    const char* src = in.data + (row + head0 * in.hs) * SIZE;
+    const int64_t src_step = per * in.hs * SIZE;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         raw[k] = {};
-        if (FAST && (k == 0 || kind == GROUP_Q) && inside && head0 + k * per < a.heads[kind])
-            raw[k].load(in.data + (row + (head0 + k * per) * in.hs) * (DT == QMM_F32 ? 4 : 2), at.a0, at.b0);
+        if (FAST && (k == 0 || kind == GROUP_Q) && k * per < left) raw[k].load(src, at.a0, at.b0);
+        src += src_step;
     }
     float2 cs[4];
     if (a.n_rot) {
@@ -281,17 +293,22 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
     };
 
     if (kind == GROUP_Q) {  // fp32, rounded once to the output's type
+        const int64_t to0 = t * a.out.ts + head0 * a.out.hs;
+        char* dst = a.out.data + to0 * SIZE;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int head = head0 + k * per;
-            const bool live = inside && head < a.heads[GROUP_Q];
+            const bool live = k * per < left;
             values(k, live);
             if (norm) {
                 float s = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s = fmaf(x[j], x[j], s);
-                for (int o = a.lanes / 2; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-                const float r = 1.f / sqrtf(s / a.D + a.eps);
+                s += __shfl_xor_sync(FULL, s, 1);
+                s += __shfl_xor_sync(FULL, s, 2);
+                if (a.lanes > 4) s += __shfl_xor_sync(FULL, s, 4);
+                if (a.lanes > 8) s += __shfl_xor_sync(FULL, s, 8);
+                if (a.lanes > 16) s += __shfl_xor_sync(FULL, s, 16);
+                const float r = rsqrtf(fmaf(s, a.inv_D, a.eps));
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = x[j] * r * gamma[j];
             }
@@ -304,15 +321,15 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
                     g = q * cs[j].x + p * cs[j].y;
                 }
             }
-            const int64_t to = t * a.out.ts + head * a.out.hs;
             if (live) {
                 if constexpr (FAST) {
-                    store_runs<DT>(a.out.data + to * (DT == QMM_F32 ? 4 : 2), at.a0, at.b0, x);
-                } else {
+                    store_runs<DT, PAIRS>(dst, at.a0, at.b0, x);
+                } else {  // U == 1
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) store1(a.out.data, to + at.element(j), x[j], a.out.dtype);
+                    for (int j = 0; j < 8; ++j) store1(a.out.data, to0 + at.element(j), x[j], a.out.dtype);
                 }
             }
+            dst += per * a.out.hs * SIZE;
         }
         return;
     }
@@ -561,6 +578,7 @@ qmm_status qmm_rope_heads(const qmm_rope_op* op, void* stream) {
     a.heads[GROUP_Q] = op->x.n_heads;
     a.norm[GROUP_Q] = op->norm_w;
     a.eps = op->norm_eps;
+    a.inv_D = 1.f / a.D;
     a.err = device_error_word();
     set_rope(a, op->rope, op->pos);
     return launch_heads(a, op->T, sms, stream);
@@ -601,6 +619,7 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
     a.norm[GROUP_Q] = op->q_norm;
     a.norm[GROUP_K] = op->k_norm;
     a.eps = op->norm_eps;
+    a.inv_D = 1.f / a.D;
     a.err = device_error_word();
     set_rope(a, op->rope, op->pos);
     a.slots = op->slots;
