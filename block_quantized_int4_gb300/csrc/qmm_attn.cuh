@@ -293,9 +293,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int 
 // 2^REF_SLACK, so 2^total times weight and scale is below 2^15, and the
 // weights' own factor 2^(part of total) at most 2^(15 - REF_SLACK).
 // Scales below 2^-7 take the rest of the factor themselves.
-__device__ __forceinline__ int scale_exponent(unsigned or_bits) {  // of fp16 scales' bits, OR-ed
-    const unsigned m = (or_bits | or_bits >> 16) & 0x7C00;
-    return (int)(m >> 10) - 15 + (m == 0);  // subnormal scales count as 2^-14
+// (The OR of the scales' exponent bits stands for the largest: never below
+// it, and above it by little, as the margins of fp16 allow.)
+__device__ __forceinline__ int scale_exponent(int bits) {  // exponent bits of fp16
+    return (bits >> 10) - 15 + (bits == 0);                // subnormal scales count as 2^-14
 }
 
 constexpr int REF_SLACK = 5;
@@ -364,27 +365,32 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * TW);
         const int n_mine = rec_end > rec0 ? (rec_end - rec0 + TW - 1) / TW : 0;
 
-        // ---- the ring: the first lane of a token group copies a whole record
-        int next_pg = rec0 / a.page_groups, next_in = rec0 - next_pg * a.page_groups;
+        // ---- the ring: the first warp of a token group copies whole records; its
+        // lanes look up the next 32 records' places in the cache at once
         const int* table = a.pages + (int64_t)b * a.pages_stride;
-        int next_page = n_mine > 0 ? table[next_pg] : 0;
-        const auto issue = [&](int k) {
-            if (k < n_mine && wr == 0 && lane == 0) {
-                const unsigned stage = (done + k) % ATTN_STAGES;
-                const int page = next_page, in = next_in;
-                next_in += TW;
-                while (next_in >= a.page_groups) next_in -= a.page_groups, ++next_pg;
-                if (k + 1 < n_mine) next_page = table[next_pg];
+        int place = -1;  // of record k = base + lane, in records; -1: its page does not exist
+        const auto look_up = [&](int base) {
+            const int k = base + lane;
+            if (k < n_mine) {
+                const int rec = rec0 + k * TW, pg = rec / a.page_groups, page = table[pg];
                 const bool gone = page < 0 || page >= a.n_pages;
-                s_gone[wt][stage] = gone;
-                if (gone) {
-                    atomicOr(a.err, ERR_BAD_INDEX);
-                    mbar_arrive(&full[stage]);
-                } else {
-                    mbar_arrive_expect_tx(&full[stage], REC);
-                    bulk_g2s(ring + stage * REC,
-                             a.cache + (((int64_t)page * a.kv_heads + at.head) * a.page_groups + in) * (int64_t)REC,
-                             REC, &full[stage]);
+                if (gone) atomicOr(a.err, ERR_BAD_INDEX);
+                place = gone ? -1 : (page * a.kv_heads + at.head) * a.page_groups + rec - pg * a.page_groups;
+            }
+        };
+        const auto issue = [&](int k) {
+            if (wr == 0 && k < n_mine) {
+                if (k % 32 == 0) look_up(k);
+                const int from = __shfl_sync(FULL, place, k % 32);
+                if (lane == 0) {
+                    const unsigned stage = (done + k) % ATTN_STAGES;
+                    s_gone[wt][stage] = from < 0;
+                    if (from < 0) {
+                        mbar_arrive(&full[stage]);
+                    } else {
+                        mbar_arrive_expect_tx(&full[stage], REC);
+                        bulk_g2s(ring + stage * REC, a.cache + (int64_t)from * REC, REC, &full[stage]);
+                    }
                 }
             }
         };
@@ -510,12 +516,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         }
 
         float acc[NB][4][4] = {};  // [block][n tile][rows g: 2 columns, rows g + 8 (or lo parts): 2 columns]
-        float ref[RS], l[RS];      // reference of the weights, w = exp2(s - ref), and their sum
-        int total = 1000;          // acc holds the weighted v times a power of two, from the largest scale so far
-        float vs = 1.f, ds = 1.f;  // that power as vs (on the weights) * ds (on the scales)
+        // keys that every row of the warp sees
+        const int lo_all = __reduce_max_sync(FULL, max(lo[0], lo[RS - 1]));
+        const int hi_all = __reduce_min_sync(FULL, min(hi[0], hi[RS - 1]));
+        float ref[RS];             // reference of the weights, w = exp2(s - ref)
+        float2 l[RS];              // and their sums
+        int top_bits = -1;         // exponent bits of the largest scale of v so far
+        float vs = 1.f, ds = 1.f;  // acc holds the weighted v times vs (on the weights) * ds (on the scales)
         float unscale = 1.f;       // 1 / (vs * ds)
 #pragma unroll
-        for (int r = 0; r < RS; ++r) ref[r] = -INFINITY, l[r] = 0.f;
+        for (int r = 0; r < RS; ++r) ref[r] = -INFINITY, l[r] = make_float2(0.f, 0.f);
 
         for (int k = 0; k < n_mine; ++k) {
             sync_group();  // the record before is read
@@ -561,10 +571,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             }
 
             // the mask, where a row does not see all 32 keys
-            bool whole = !gone;
-#pragma unroll
-            for (int r = 0; r < RS; ++r) whole &= tok0 >= lo[r] && tok0 + GROUP <= hi[r];
-            const bool masked = __any_sync(FULL, !whole);
+            const bool masked = gone || tok0 < lo_all || tok0 + GROUP > hi_all;
             if (masked) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -597,23 +604,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 any |= d4.x | d4.y;
                 any |= d4.z | d4.w;
             }
-            any |= __shfl_xor_sync(FULL, any, 1);
-            any |= __shfl_xor_sync(FULL, any, 2);
-            const int room = 14 - REF_SLACK - scale_exponent(any);
-            float ratio = 1.f;
-            if (room < total) {
-                const int before = total;
-                total = room;
-                const int w = min(total, 15 - REF_SLACK);
-                vs = exp2f((float)w);
-                ds = total > 21 - REF_SLACK ? exp2f((float)(total - w)) : 1.f;
-                ratio = before > 100 ? 1.f : vs * ds * unscale;
-                unscale = 1.f / (vs * ds);
-            }
             // The reference follows the running maximum by steps of more than
-            // 2^REF_SLACK: few of them are left to rescale acc for.
+            // 2^REF_SLACK, so acc is rarely rescaled; so with the scales of v.
+            int exponent = (any | any >> 16) & 0x7C00;
             float m[RS];
-            bool moved = ratio != 1.f;
+            bool moved = exponent > top_bits;
 #pragma unroll
             for (int r = 0; r < RS; ++r) {
                 m[r] = s[0][r].x;
@@ -623,6 +618,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 moved |= m[r] > ref[r] + REF_SLACK;
             }
             if (__any_sync(FULL, moved)) {
+                exponent = __reduce_max_sync(FULL, exponent);
+                float ratio = 1.f;
+                if (exponent > top_bits) {
+                    const int room = 14 - REF_SLACK - scale_exponent(exponent), w = min(room, 15 - REF_SLACK);
+                    vs = exp2f((float)w);
+                    ds = room > 21 - REF_SLACK ? exp2f((float)(room - w)) : 1.f;
+                    ratio = top_bits < 0 ? 1.f : vs * ds * unscale;
+                    unscale = 1.f / (vs * ds);
+                    top_bits = exponent;
+                }
 #pragma unroll
                 for (int r = 0; r < RS; ++r) {
                     m[r] = fmaxf(m[r], __shfl_xor_sync(FULL, m[r], 1));
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                     const float now = fmaxf(ref[r], m[r]);
                     const float alpha = now == -INFINITY ? 0.f : exp2_fast(ref[r] - now);
                     ref[r] = now;
-                    l[r] *= alpha;
+                    l[r] = mul2(l[r], make_float2(alpha, alpha));
                     const float by = alpha * ratio;
 #pragma unroll
                     for (int kb = 0; kb < NB; ++kb)
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 for (int r = 0; r < RS; ++r) {
                     const float2 x = fma2(s[j][r], make_float2(f[r], f[r]), make_float2(-use[r], -use[r]));
                     const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                    l[r] += w.x + w.y;
+                    l[r] = add2(l[r], w);
                     s[j][r] = mul2(w, make_float2(vs, vs));
                     if (DTYPE != QMM_F16) ph[j][r] = pack_half(s[j][r].x, s[j][r].y);
                     if (SPLIT) {
@@ -709,9 +714,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         // ---- join the token groups: O, maximum and sum of every row
 #pragma unroll
         for (int r = 0; r < RS; ++r) {
-            l[r] += __shfl_xor_sync(FULL, l[r], 1);
-            l[r] += __shfl_xor_sync(FULL, l[r], 2);
-            if (c == 0) s_m[warp][g + 8 * r] = ref[r], s_l[warp][g + 8 * r] = l[r];
+            float sum = l[r].x + l[r].y;
+            sum += __shfl_xor_sync(FULL, sum, 1);
+            sum += __shfl_xor_sync(FULL, sum, 2);
+            if (c == 0) s_m[warp][g + 8 * r] = ref[r], s_l[warp][g + 8 * r] = sum;
         }
         __syncthreads();  // the ring is read
         float* buf = reinterpret_cast<float*>(smem);  // [warp][ROWS][D]
