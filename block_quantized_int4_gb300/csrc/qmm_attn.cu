@@ -12,15 +12,17 @@ namespace qmm {
 namespace {
 
 struct Plan {
-    int row_warps, token_warps, block_rows, blocks;
-    int ctas;  // CTAs of a cut launch; 0: one CTA an item
+    int mode, row_warps, token_warps, block_rows, blocks;
+    int ctas, cluster;  // CTAs of a cut launch, of a cluster
     int64_t items;
     size_t meta_bytes, part_bytes;
-    int ring_bytes, smem;
+    int ring_bytes, part_at, smem;
 };
 
 constexpr int DEFAULT_SMS = 152;
 constexpr int64_t MAX_CTAS = 1024;  // the join kernel's parts of an item
+constexpr int MAX_CLUSTER = 8;
+constexpr int64_t MAX_UNITS_UNCUT = 6;
 
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
@@ -33,11 +35,20 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.items = (int64_t)op.n_seqs * p.blocks * op.cache.n_heads;
     p.ring_bytes = attn_ring_bytes(D, p.row_warps, tile);
-    p.smem = p.ring_bytes + attn_q_bytes(D, p.row_warps);
-    // Items of a few units are not worth a second launch that joins parts.
+    p.part_at = p.smem = p.ring_bytes + attn_q_bytes(D, p.row_warps);
     const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
-    if (units > 4) {
-        p.ctas = (int)std::min<int64_t>({(int64_t)sms * attn_ctas(NB), p.items * units, MAX_CTAS});
+    const int64_t slots = (int64_t)sms * attn_ctas(NB);
+    // As many CTAs an item as find room at once, while none has much to do;
+    // beyond that equal shares, whose parts cost a second launch.
+    int64_t c = 1;
+    while (2 * c <= MAX_CLUSTER && 2 * c <= units && 2 * c * p.items <= slots) c *= 2;
+    if ((units + c - 1) / c <= MAX_UNITS_UNCUT) {
+        p.mode = c > 1 ? ATTN_CLUSTER : ATTN_WHOLE;
+        p.cluster = (int)c;
+        if (c > 1) p.smem += p.block_rows * (D + 2) * 4;
+    } else {
+        p.mode = ATTN_CUT;
+        p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
         p.meta_bytes = ((size_t)p.items * sizeof(AttnMeta) + 255) / 256 * 256;
         p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * (D + 2) * 4;
     }
@@ -149,7 +160,9 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.ring_bytes = p.ring_bytes;
     a.row_warps = p.row_warps;
     a.blocks = p.blocks;
-    a.split = p.ctas != 0;
+    a.mode = p.mode;
+    a.cluster = p.cluster;
+    a.part_at = p.part_at;
     a.meta = static_cast<AttnMeta*>(op->workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
     a.err = device_error_word();
@@ -157,18 +170,30 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     const AttnKernel kernel = kernel_of(op->q.dtype, NB);
     if (!prepared(kernel, op->q.dtype, NB, optin)) return QMM_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = p.ctas ? (unsigned)p.ctas : (unsigned)p.items;
-    kernel<<<grid, ATTN_THREADS, p.smem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return QMM_ERR_CUDA;
-    if (p.ctas) {
-        cudaLaunchConfig_t cfg = {};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.mode == ATTN_CUT ? p.ctas : p.items * p.cluster));
+    cfg.blockDim = dim3(ATTN_THREADS);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    if (p.mode == ATTN_CLUSTER) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = p.cluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return QMM_ERR_CUDA;
+    }
+    if (p.mode == ATTN_CUT) {
         cfg.gridDim = dim3((unsigned)p.items, (unsigned)std::min(p.block_rows, 16));
         cfg.blockDim = dim3(attn::JOIN_WARPS * 32);
-        cfg.stream = st;
-        cudaLaunchAttribute pdl;
-        pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        pdl.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &pdl;
+        cfg.dynamicSmemBytes = 0;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, JOIN[NB - 1], a, p.block_rows) != cudaSuccess) {
             cudaGetLastError();

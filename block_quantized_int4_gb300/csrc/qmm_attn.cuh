@@ -37,6 +37,12 @@ constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
 constexpr int ATTN_STAGES = 2;  // a token group's records: one in use, one in flight
 
+// How the items (a row block of a sequence and key/value head) meet the CTAs:
+// one CTA an item; a cluster of CTAs an item, joined through shared memory; or
+// all units in equal shares, items cut where a share ends and their parts
+// joined by a second kernel.
+enum AttnMode { ATTN_WHOLE = 0, ATTN_CLUSTER = 1, ATTN_CUT = 2 };
+
 struct AttnMeta {  // of an item: the CTAs that its units are cut over
     int first, last;  // first > last: not cut
     int slot;         // which of the first CTA's parts is the item's
@@ -55,9 +61,10 @@ struct AttnArgs {
     int n_pages, page_groups, kv_heads, group;  // group: query heads a key/value head
     int n_seqs, max_q, max_kv, causal, window;
     float scale_log2;
-    int ring_bytes;
+    int ring_bytes, part_at;  // shared memory: the rows of q, a cluster's part
     int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
-    int split;              // 0: one CTA an item; 1: items cut where the CTAs' shares end
+    int mode;               // AttnMode
+    int cluster;            // CTAs of a cluster (ATTN_CLUSTER)
     float* part;            // [ctas][2][rows][D + 2]
     AttnMeta* meta;         // [sequence][row block][head]
     int* err;
@@ -118,6 +125,24 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
+}
+
+// Shared memory of the CTA of rank `x` in the cluster, and a barrier of all its
+// threads (release and acquire).
+__device__ __forceinline__ unsigned in_cluster(unsigned addr, int x) {
+    unsigned r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(x));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(unsigned addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ __half2 as_half2(unsigned w) { return *reinterpret_cast<const __half2*>(&w); }
@@ -332,7 +357,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         int entry, head, unit;
     } at;
     int u0, u1, share = 0;
-    if (a.split) {
+    const bool cut = a.mode == ATTN_CUT;
+    int rank = 0;  // in the cluster
+    if (cut) {
         find_share(a, block_rows, TW, sh, u0, u1, share);  // synchronises the block
         // the join kernel's blocks may come in beside the last of this one's (they wait for its end)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -340,10 +367,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         at.entry = sh.entry;
         at.head = (u0 - sh.start) / sh.units;
         at.unit = u0 - sh.start - at.head * sh.units;
-    } else {  // one CTA an item, later row blocks (more keys) first
+    } else {  // later row blocks (more keys) first
         __syncthreads();
-        const int e = blockIdx.x / a.kv_heads, b = e / a.blocks;
-        at.head = blockIdx.x - e * a.kv_heads;
+        int item = blockIdx.x;
+        if (a.mode == ATTN_CLUSTER) {
+            item = (int)blockIdx.x / a.cluster;
+            rank = (int)blockIdx.x - item * a.cluster;
+        }
+        const int e = item / a.kv_heads, b = e / a.blocks;
+        at.head = item - e * a.kv_heads;
         at.entry = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
         at.unit = 0;
         u0 = 0;
@@ -353,14 +385,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     unsigned done = 0;  // records of this token group so far: stage and phase of the ring
     for (int u = u0; u < u1;) {
         const int b = a.blocks == 1 ? at.entry : at.entry / a.blocks, block = at.entry - b * a.blocks;
-        const Seq seq = sequence(a, b, !a.split && tid == 0);
+        const Seq seq = sequence(a, b, !cut && tid == 0);
         const Span sp = span_of(a, seq, block, block_rows, TW);
         if (sp.units == 0) {
-            if (!a.split) return;
+            if (!cut) return;  // of a cluster, all
             ++at.entry, at.head = 0, at.unit = 0;
             continue;
         }
-        const int unit_end = a.split ? min(sp.units, at.unit + (u1 - u)) : sp.units;
+        int unit_end = cut ? min(sp.units, at.unit + (u1 - u)) : sp.units;
+        if (a.mode == ATTN_CLUSTER) {
+            at.unit = (int)((int64_t)sp.units * rank / a.cluster);
+            unit_end = (int)((int64_t)sp.units * (rank + 1) / a.cluster);
+        }
         const int rec0 = sp.lo / GROUP + at.unit * TW + wt;
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * TW);
         const int n_mine = rec_end > rec0 ? (rec_end - rec0 + TW - 1) / TW : 0;
@@ -741,11 +777,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 }
         }
         __syncthreads();
-        const bool uncut = at.unit == 0 && unit_end == sp.units;
-        // a share's first segment keeps its part in slot 0, its last in slot 1
+        const bool uncut = a.mode != ATTN_CLUSTER && at.unit == 0 && unit_end == sp.units;
         float* part = nullptr;
-        if (!uncut) part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * (D + 2);
-        for (int row = warp; row < block_rows; row += ATTN_WARPS) {
+        if (a.mode == ATTN_CLUSTER)
+            part = reinterpret_cast<float*>(smem + a.part_at);
+        else if (!uncut)  // a share's first segment keeps its part in slot 0, its last in slot 1
+            part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * (D + 2);
+        const auto write = [&](int row, const float* o) {
+            const int global_row = block * block_rows + row, i = global_row / a.group;
+            write_row<NB>(a, seq.q0 + i, at.head * a.group + global_row - i * a.group, o, lane);
+        };
+        const int live_rows = min(block_rows, rows - block * block_rows);
+        for (int row = warp; row < live_rows; row += ATTN_WARPS) {
             const int rw = row / ROWS, rr = row - rw * ROWS;
             float m = -INFINITY, sum = 0.f, o[NB] = {};
             for (int t = 0; t < TW; ++t) m = fmaxf(m, s_m[rw * TW + t][rr]);
@@ -755,21 +798,41 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) o[kb] += buf[((rw * TW + t) * ROWS + rr) * D + kb * 32 + lane];
             }
-            const int global_row = block * block_rows + row;
-            if (global_row >= rows) break;
             if (uncut) {
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) o[kb] *= inv;
-                const int i = global_row / a.group;
-                write_row<NB>(a, seq.q0 + i, at.head * a.group + global_row - i * a.group, o, lane);
+                write(row, o);
             } else {
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) part[row * (D + 2) + kb * 32 + lane] = o[kb];
                 if (lane == 0) part[row * (D + 2) + D] = m, part[row * (D + 2) + D + 1] = sum;
             }
         }
-        if (!a.split) return;
+        if (a.mode == ATTN_CLUSTER) {
+            // every CTA of the cluster joins some of the rows, from all parts in their order
+            cluster_sync();
+            for (int row = rank + warp * a.cluster; row < live_rows; row += ATTN_WARPS * a.cluster) {
+                const unsigned mine = smem_u32(part + row * (D + 2));
+                float m = -INFINITY, sum = 0.f, o[NB] = {};
+                for (int x = 0; x < a.cluster; ++x) {
+                    const unsigned p = in_cluster(mine, x);
+                    const float pm = ld_cluster(p + D * 4), pl = ld_cluster(p + D * 4 + 4);
+                    const float now = fmaxf(m, pm), use = now == -INFINITY ? 0.f : now;
+                    const float wo = exp2_fast(m - use), wp = exp2_fast(pm - use);
+                    sum = sum * wo + pl * wp;
+#pragma unroll
+                    for (int kb = 0; kb < NB; ++kb) o[kb] = o[kb] * wo + ld_cluster(p + (kb * 32 + lane) * 4) * wp;
+                    m = now;
+                }
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) o[kb] *= inv;
+                write(row, o);
+            }
+            cluster_sync();  // the others' shared memory stays until it is read
+        }
+        if (!cut) return;
         if (tid == 0 && at.unit == 0) {
             const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
             a.meta[(int64_t)at.entry * a.kv_heads + at.head] = AttnMeta{first, last, u != u0, 0};
