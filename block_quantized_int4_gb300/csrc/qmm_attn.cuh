@@ -845,23 +845,24 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     }
 }
 
-// Joins the parts of an item that was cut over CTAs, in the CTAs' order:
-// block (item, y) takes rows y, y + gridDim.y, ...; its warps take every
-// eighth part.
+// Joins the parts of an item that was cut over CTAs: block (item, y) takes
+// rows y, y + gridDim.y, ...; warp w of it the parts w, w + 8, ..., eight at a
+// time, all of whose loads are on their way at once.  What each part gets
+// depends on its place alone, so results do not change from call to call.
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_MAX_PARTS = 1024;
+constexpr int JOIN_AT_ONCE = 8;
 
 template <int NB>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
     attn_join_kernel(const __grid_constant__ AttnArgs a, int block_rows) {
     constexpr int D = NB * 32;
-    __shared__ float s_w[JOIN_MAX_PARTS], s_o[JOIN_WARPS][D], s_red[2][JOIN_WARPS];
+    __shared__ float s_o[JOIN_WARPS][D], s_m[JOIN_WARPS], s_l[JOIN_WARPS];
     const int entry = blockIdx.x / a.kv_heads, head = blockIdx.x - entry * a.kv_heads;
-    const int b = entry / a.blocks, block = entry - b * a.blocks;
+    const int b = a.blocks == 1 ? entry : entry / a.blocks, block = entry - b * a.blocks;
     const Seq seq = sequence(a, b, false);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = min(block_rows, seq.n * a.group - block * block_rows);
-    if (rows <= 0) return;
+    if ((int)blockIdx.y >= rows) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnMeta mt = a.meta[blockIdx.x];
     const int n = mt.last - mt.first + 1;
@@ -869,49 +870,56 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
     const int64_t step = (int64_t)block_rows * (D + 2);
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
         const float* base = a.part + (int64_t)mt.first * 2 * step + row * (D + 2);
-        const auto part = [&](int x) { return base + 2 * step * x + (x == 0 && mt.slot ? step : 0); };
-        float m = -INFINITY;
-        for (int x = tid; x < n; x += JOIN_WARPS * 32) m = fmaxf(m, part(x)[D]);
+        float m = -INFINITY, sum = 0.f, o[NB] = {};
+        for (int x0 = warp; x0 < n; x0 += JOIN_WARPS * JOIN_AT_ONCE) {
+            float pm[JOIN_AT_ONCE], pl[JOIN_AT_ONCE], po[JOIN_AT_ONCE][NB];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-        if (lane == 0) s_red[0][warp] = m;
-        __syncthreads();
+            for (int i = 0; i < JOIN_AT_ONCE; ++i) {
+                const int x = x0 + i * JOIN_WARPS;
+                const float* p = base + 2 * step * x + (x == 0 && mt.slot ? step : 0);
+                const bool live = x < n;
+                pm[i] = live ? p[D] : -INFINITY;
+                pl[i] = live ? p[D + 1] : 0.f;
 #pragma unroll
-        for (int w = 0; w < JOIN_WARPS; ++w) m = fmaxf(m, s_red[0][w]);
-        float sum = 0.f;
-        for (int x = tid; x < n; x += JOIN_WARPS * 32) {
-            const float w = m == -INFINITY ? 0.f : exp2_fast(part(x)[D] - m);
-            s_w[x] = w;
-            sum += w * part(x)[D + 1];
+                for (int kb = 0; kb < NB; ++kb) po[i][kb] = live ? p[kb * 32 + lane] : 0.f;
+            }
+            float now = m;
+#pragma unroll
+            for (int i = 0; i < JOIN_AT_ONCE; ++i) now = fmaxf(now, pm[i]);
+            const float use = now == -INFINITY ? 0.f : now, w = exp2_fast(m - use);
+            sum *= w;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) o[kb] *= w;
+#pragma unroll
+            for (int i = 0; i < JOIN_AT_ONCE; ++i) {
+                const float wi = exp2_fast(pm[i] - use);
+                sum = fmaf(wi, pl[i], sum);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) o[kb] = fmaf(wi, po[i][kb], o[kb]);
+            }
+            m = now;
         }
-        sum = warp_sum(sum);
-        if (lane == 0) s_red[1][warp] = sum;
-        __syncthreads();
-        float o[NB] = {};
-#pragma unroll 4
-        for (int x = warp; x < n; x += JOIN_WARPS) {
-            const float w = s_w[x];
-            const float* p = part(x);
-#pragma unroll
-            for (int kb = 0; kb < NB; ++kb) o[kb] = fmaf(w, p[kb * 32 + lane], o[kb]);
-        }
+        if (lane == 0) s_m[warp] = m, s_l[warp] = sum;
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) s_o[warp][kb * 32 + lane] = o[kb];
         __syncthreads();
         if (warp == 0) {
-            float total = 0.f;
+            float top = -INFINITY, total = 0.f, v[NB] = {};
 #pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) total += s_red[1][w];
+            for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, s_m[w]);
+            const float use = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < JOIN_WARPS; ++w) {
+                const float by = exp2_fast(s_m[w] - use);
+                total = fmaf(by, s_l[w], total);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) v[kb] = fmaf(by, s_o[w][kb * 32 + lane], v[kb]);
+            }
             const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
-                float v = 0.f;
-#pragma unroll
-                for (int w = 0; w < JOIN_WARPS; ++w) v += s_o[w][kb * 32 + lane];
-                o[kb] = v * inv;
-            }
+            for (int kb = 0; kb < NB; ++kb) v[kb] *= inv;
             const int global_row = block * block_rows + row, i = global_row / a.group;
-            write_row<NB>(a, seq.q0 + i, head * a.group + global_row - i * a.group, o, lane);
+            write_row<NB>(a, seq.q0 + i, head * a.group + global_row - i * a.group, v, lane);
         }
         __syncthreads();
     }
