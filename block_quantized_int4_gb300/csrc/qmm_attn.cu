@@ -6,13 +6,15 @@
 
 #include "qmm.h"
 #include "qmm_attn.cuh"
+#include "qmm_attn_tc.h"
 #include "qmm_internal.h"
 
 namespace qmm {
 namespace {
 
 struct Plan {
-    int mode, row_warps, token_warps, block_rows, blocks;
+    bool tc;  // the tensor-memory kernel (qmm_attn_tc.cu)
+    int mode, row_warps, token_warps, block_rows, blocks;  // token_warps: records of a unit
     int ctas, cluster;  // CTAs of a cut launch, of a cluster
     int64_t items;
     size_t meta_bytes, part_bytes;
@@ -23,31 +25,44 @@ constexpr int DEFAULT_SMS = 152;
 constexpr int64_t MAX_CTAS = 1024;  // the join kernel's parts of an item
 constexpr int MAX_CLUSTER = 8;
 constexpr int64_t MAX_UNITS_UNCUT = 6;
+constexpr int64_t TC_MIN_ROWS = 64;
 
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
     const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
     const int tile = attn_tile_rows(op.q.dtype);
     const int64_t rows = (int64_t)op.max_q * group;
+    p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB && rows >= TC_MIN_ROWS;
     p.row_warps = rows <= tile ? 1 : rows <= 2 * tile ? 2 : 4;
     p.token_warps = ATTN_WARPS / p.row_warps;
     p.block_rows = p.row_warps * tile;
+    if (p.tc) p.token_warps = ATTN_TC_RECORDS, p.block_rows = ATTN_TC_ROWS;
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.items = (int64_t)op.n_seqs * p.blocks * op.cache.n_heads;
     p.ring_bytes = attn_ring_bytes(D, p.row_warps, tile);
     p.part_at = p.smem = p.ring_bytes + attn_q_bytes(D, p.row_warps);
     const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
-    const int64_t slots = (int64_t)sms * attn_ctas(NB);
+    const int64_t slots = p.tc ? sms : (int64_t)sms * attn_ctas(NB);
+    if (p.tc) p.smem = std::max(attn_tc_smem(NB), 120 * 1024);  // one CTA an SM: each takes all of tensor memory
     // As many CTAs an item as find room at once, while none has much to do;
     // beyond that equal shares, whose parts cost a second launch.
     int64_t c = 1;
     while (2 * c <= MAX_CLUSTER && 2 * c <= units && 2 * c * p.items <= slots) c *= 2;
-    if ((units + c - 1) / c <= MAX_UNITS_UNCUT) {
+    if (p.tc) {
+        // Whole items where they fill the SMs' rounds to three quarters; else
+        // equal shares, whose parts cost a second launch.
+        const int64_t rounds = (p.items + slots - 1) / slots;
+        c = 1;
+        p.mode = units <= 2 || 4 * p.items >= 3 * rounds * slots ? ATTN_WHOLE : ATTN_CUT;
+        p.cluster = 1;
+    } else if ((units + c - 1) / c <= MAX_UNITS_UNCUT) {
         p.mode = c > 1 ? ATTN_CLUSTER : ATTN_WHOLE;
         p.cluster = (int)c;
         if (c > 1) p.smem += p.block_rows * (D + 2) * 4;
     } else {
         p.mode = ATTN_CUT;
+    }
+    if (p.mode == ATTN_CUT) {
         p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
         p.meta_bytes = ((size_t)p.items * sizeof(AttnMeta) + 255) / 256 * 256;
         p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * (D + 2) * 4;
@@ -86,13 +101,13 @@ AttnKernel kernel_of(int dtype, int NB) {
 }
 
 // Opts a kernel into the shared memory of a device, once.
-bool prepared(AttnKernel k, int dtype, int NB, int optin) {
+bool prepared(AttnKernel k, int kind, int NB, int optin) {
     static std::mutex mu;
-    static bool done[64][3][8];
+    static bool done[64][4][8];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
-    bool& d = done[dev][dtype][NB - 1];
+    bool& d = done[dev][kind][NB - 1];
     if (!d)
         d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 4096) == cudaSuccess &&
             cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
@@ -167,12 +182,12 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
     a.err = device_error_word();
     const int NB = op->cache.head_dim / QK;
-    const AttnKernel kernel = kernel_of(op->q.dtype, NB);
-    if (!prepared(kernel, op->q.dtype, NB, optin)) return QMM_ERR_CUDA;
+    const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB);
+    if (!prepared(kernel, p.tc ? 3 : op->q.dtype, NB, optin)) return QMM_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.mode == ATTN_CUT ? p.ctas : p.items * p.cluster));
-    cfg.blockDim = dim3(ATTN_THREADS);
+    cfg.blockDim = dim3(p.tc ? attn_tc_threads() : ATTN_THREADS);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;

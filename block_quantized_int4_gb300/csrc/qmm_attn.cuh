@@ -224,9 +224,9 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int blo
 
 // A CTA's share [u0, u1) of all units, ordered by (sequence, row block, head,
 // unit), and where u0 lies.  entry: sequence * blocks + row block.
+template <int WARPS>
 struct Share {
-    int total;  // units of one head
-    int warp_units[ATTN_WARPS];
+    int warp_units[WARPS];
     int entry, start, units;  // the entry of u0, units before it (all heads) and its own (one head)
 };
 
@@ -238,6 +238,7 @@ __device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries
 }
 
 // Inclusive sum of v over the block's threads and the block's total.
+template <int WARPS>
 __device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -249,7 +250,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
     __syncthreads();
     total = 0;
 #pragma unroll
-    for (int w = 0; w < ATTN_WARPS; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         const int x = warp_units[w];
         if (w < warp) v += x;
         total += x;
@@ -257,30 +258,31 @@ __device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
     return v;
 }
 
-// Up to ATTN_THREADS entries are read once; more in two rounds (their units,
+// Up to THREADS entries are read once; more in two rounds (their units,
 // then the place of u0).  The units of all heads fit 31 bits (checked on the
 // host).
-__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int token_warps, Share& sh, int& u0,
-                                           int& u1, int& share) {
+template <int THREADS>
+__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int token_warps, Share<THREADS / 32>& sh,
+                                           int& u0, int& u1, int& share) {
     const int tid = threadIdx.x, entries = a.n_seqs * a.blocks;
-    const bool one = entries <= ATTN_THREADS;
+    const bool one = entries <= THREADS;
     int units = 0, mine = 0, total;
-    for (int e = tid; e < entries; e += ATTN_THREADS) {
+    for (int e = tid; e < entries; e += THREADS) {
         units = entry_units(a, e, entries, block_rows, token_warps, blockIdx.x == 0);
         mine += units;
     }
-    int incl = block_scan(mine, sh.warp_units, total);
+    int incl = block_scan<THREADS / 32>(mine, sh.warp_units, total);
     const int all = total * a.kv_heads;
     share = max((int)(((unsigned)all + gridDim.x - 1) / gridDim.x), 1);
     u0 = (int)min((int64_t)share * blockIdx.x, (int64_t)all);
     u1 = (int)min((int64_t)u0 + share, (int64_t)all);
     if (u0 >= u1) return;
     int before = 0;
-    for (int base = 0; base < entries; base += ATTN_THREADS) {
+    for (int base = 0; base < entries; base += THREADS) {
         if (!one) {
             __syncthreads();
             units = entry_units(a, base + tid, entries, block_rows, token_warps, false);
-            incl = block_scan(units, sh.warp_units, total);
+            incl = block_scan<THREADS / 32>(units, sh.warp_units, total);
         }
         const int start = before + (incl - units) * a.kv_heads;
         if (units && u0 >= start && u0 - start < units * a.kv_heads)
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     constexpr int D = NB * 32, REC = record_bytes(D), ROWS = attn_tile_rows(DTYPE);
     constexpr int RS = SPLIT ? 1 : 2;  // rows a lane keeps statistics of
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Share sh;
+    __shared__ Share<ATTN_WARPS> sh;
     __shared__ float s_m[ATTN_WARPS][16], s_l[ATTN_WARPS][16];
     __shared__ uint64_t s_full[ATTN_WARPS][ATTN_STAGES];
     __shared__ int s_gone[ATTN_WARPS][ATTN_STAGES];  // the record's page does not exist
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     const bool cut = a.mode == ATTN_CUT;
     int rank = 0;  // in the cluster
     if (cut) {
-        find_share(a, block_rows, TW, sh, u0, u1, share);  // synchronises the block
+        find_share<ATTN_THREADS>(a, block_rows, TW, sh, u0, u1, share);  // synchronises the block
         // the join kernel's blocks may come in beside the last of this one's (they wait for its end)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 >= u1) return;

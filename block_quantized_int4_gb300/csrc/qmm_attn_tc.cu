@@ -1,0 +1,572 @@
+// qmm_attn_tc.cu -- attention over the paged Q4_0 cache for many rows (a
+// prompt's chunk) of bf16 activations, on the 5th-generation tensor cores.
+//
+// Why another form.  The warp-MMA kernel (qmm_attn.cuh) unpacks a record once
+// for 16 rows and multiplies at the legacy rate; with hundreds of rows a
+// key/value head that is compute bound.  Here a record is unpacked once for
+// 256 rows, into fp16 operands in shared memory, and both products are
+// tcgen05.mma with accumulators in tensor memory:
+//   S = Q K^T   M = 128 rows, N = 128 keys, both operands in shared memory
+//   O += P V    M = 128 rows, N = D, P from tensor memory, V^T from shared
+// Scales meet the codes here (d * (u - 8) rounded to fp16, 2^-12), so this form
+// serves bf16 alone, whose output rounds at 2^-9.
+//
+// A CTA (one an SM, 18 warps) holds two row tiles of 128 rows and walks the
+// keys in steps of 128 (4 records):
+//  - warps 0..3 and 4..7: the softmax of tile 0 and 1, a thread a row: S from
+//    tensor memory, weights back into its place as fp16 (P), the row's sum;
+//    O is rescaled only when the row's maximum grew by more than 2^SLACK.
+//  - warps 8..15: K and V of a step as fp16 operands.  The cache's word order
+//    makes them as it makes the warp MMA's: a word of K is eight values of one
+//    key (Q is laid down in the same order of its values), a word of V two
+//    keys of four values, so every store of a warp is one run of shared memory.
+//  - warp 16: page look-ups and bulk copies of records; warp 17: issues MMAs.
+// The two tiles take turns: while one is in its softmax, the other's products
+// run.  V is double, K single buffered (K of the next step is unpacked while
+// the softmaxes of this one run).
+//
+// Operands lie as K-major core matrices of 8 rows x 16 bytes without swizzle.
+// Every wait is bounded; on expiry the error word is set and the CTA ends.
+#include <cuda_runtime.h>
+
+#include "qmm_attn.cuh"
+#include "qmm_attn_tc.h"
+
+namespace qmm {
+namespace attn_tc {
+
+using attn::Seq;
+using attn::Span;
+
+constexpr int SOFTMAX_WARPS = 8, UNPACK_WARPS = 8;
+constexpr int WARP_LOAD = SOFTMAX_WARPS + UNPACK_WARPS, WARP_MMA = WARP_LOAD + 1;
+constexpr int THREADS = (WARP_MMA + 1) * 32;
+constexpr int STEP = 128;              // keys of a step
+constexpr int STEP_RECORDS = STEP / GROUP;
+constexpr float SLACK = 5.f;           // weights reach 2^(SLACK + LIFT)
+constexpr float LIFT = 10.f;           // weights are 2^LIFT times exp2(s - reference): fp16 keeps small ones
+constexpr uint32_t TMEM_COLS = 512, S_COL = 0, O_COL = 256;  // S of tile x at 128 x, O at 256 + 128 x
+
+template <int NB>
+struct Smem {
+    static constexpr int D = NB * 32;
+    static constexpr int REC = record_bytes(D);
+    static constexpr int Q = 0;                          // [2][128][D] fp16
+    static constexpr int K = Q + 2 * 128 * D * 2;        // [128][D]
+    static constexpr int V = K + STEP * D * 2;           // [2][D][128]
+    static constexpr int RAW = V + 2 * STEP * D * 2;     // [2][4][REC]
+    static constexpr int BYTES = RAW + 2 * STEP_RECORDS * REC;
+};
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return ((addr >> 4) & 0x3FFFull) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define QMM_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                     "=r"(r[i + 6]), "=r"(r[i + 7])
+#define QMM_U8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                     "+r"(r[i + 6]), "+r"(r[i + 7])
+#define QMM_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                     "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 columns of this thread's lane; the registers are named again at the
+// wait, so that no use of them moves before it.
+__device__ __forceinline__ void ld32(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : QMM_R8(r, 0), QMM_R8(r, 8), QMM_R8(r, 16), QMM_R8(r, 24)
+        : "r"(at));
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : QMM_U8(r, 0), QMM_U8(r, 8), QMM_U8(r, 16), QMM_U8(r, 24)
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            at),
+        QMM_I8(r, 0), QMM_I8(r, 8)
+        : "memory");
+}
+__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        QMM_I8(r, 0), QMM_I8(r, 8), QMM_I8(r, 16), QMM_I8(r, 24)
+        : "memory");
+}
+
+// Two codes times a pair of scales: nibbles 0 and 4 of w.
+__device__ __forceinline__ unsigned scaled_codes(unsigned w, __half2 d, unsigned magic) {
+    return attn::as_bits(__hmul2(attn::as_half2(attn::signed_codes<0>(w, magic)), d));
+}
+
+template <int NB>
+__global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
+    using SM = Smem<NB>;
+    constexpr int D = SM::D, REC = SM::REC;
+    constexpr int BLOCK_ROWS = ATTN_TC_ROWS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ attn::Share<THREADS / 32> sh;
+    __shared__ uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
+    __shared__ int s_gone[4][STEP_RECORDS];  // four steps: a softmax reads the flags of a step two copies later
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    volatile int* abort_flag = &s_abort;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], UNPACK_WARPS);
+            mbar_init(&v_full[i], UNPACK_WARPS);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(&k_full, UNPACK_WARPS);
+        mbar_init(&k_empty, 1);
+        mbar_init(&o_full, 1);
+        mbar_init(&drain, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == WARP_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+
+    const bool cut = a.mode == ATTN_CUT;
+    int entry, head, unit = 0, u0 = 0, u1 = 1, share = 0;
+    if (cut) {
+        attn::find_share<THREADS>(a, BLOCK_ROWS, STEP_RECORDS, sh, u0, u1, share);
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (u0 < u1) {
+            entry = sh.entry;
+            head = (u0 - sh.start) / sh.units;
+            unit = u0 - sh.start - head * sh.units;
+        }
+    } else {  // later row blocks (more keys) first
+        const int e = blockIdx.x / a.kv_heads, b = e / a.blocks;
+        head = blockIdx.x - e * a.kv_heads;
+        entry = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
+    }
+
+    unsigned steps = 0, segments = 0;  // before this segment: phases of the barriers
+    unsigned tile1_steps = 0;          // of them, those of tile 1
+    for (int u = u0; u < u1;) {
+        const int b = a.blocks == 1 ? entry : entry / a.blocks, block = entry - b * a.blocks;
+        const Seq seq = attn::sequence(a, b, !cut && tid == 0);
+        const Span sp = attn::span_of(a, seq, block, BLOCK_ROWS, STEP_RECORDS);
+        if (sp.units == 0) {
+            if (!cut) break;
+            ++entry, head = 0, unit = 0;
+            continue;
+        }
+        const int unit_end = cut ? min(sp.units, unit + (u1 - u)) : sp.units;
+        const int rec0 = sp.lo / GROUP + unit * STEP_RECORDS;
+        const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * STEP_RECORDS);
+        const int n = rec_end > rec0 ? (rec_end - rec0 + STEP_RECORDS - 1) / STEP_RECORDS : 0;
+        const int rows = seq.n * a.group, first_row = block * BLOCK_ROWS;
+        const int tiles = rows - first_row > 128 ? 2 : 1;
+
+        // ---- the softmax warps lay down their rows of Q
+        const int tile = warp >> 2;  // of a softmax warp
+        const int row = first_row + (tile << 7) + (tid & 127);
+        const bool live = warp < SOFTMAX_WARPS && row < rows;
+        const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
+        float f = 1.f;
+        if (warp < SOFTMAX_WARPS && tile < tiles) {
+            const int64_t at = (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs;
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < NB * 4; ++k) {
+                float x[8] = {};
+                if (live) loadn<8>(a.q.data, at + 8 * k, QMM_BF16, a.q.wide, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+            }
+            // top * 2^up in [2^13, 2^14); a negative scale goes into q', a scale of 0 makes it 0
+            const int up = top > 0.f ? 13 - min(max(ilogbf(top), -100), 100) : 0;
+            const float mul = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
+            f = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)-up);
+            uint8_t* to = smem + SM::Q + tile * (128 * D * 2) + ((tid & 127) >> 3) * (D * 16) + (tid & 7) * 16;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float x[4] = {}, y[4] = {};
+                    if (live) {
+                        loadn<4>(a.q.data, at + 32 * kb + 4 * c, QMM_BF16, a.q.wide, x);
+                        loadn<4>(a.q.data, at + 32 * kb + 16 + 4 * c, QMM_BF16, a.q.wide, y);
+                    }
+                    *reinterpret_cast<uint4*>(to + (kb * 4 + c) * 128) =
+                        make_uint4(attn::pack_half(x[0] * mul, x[2] * mul), attn::pack_half(x[1] * mul, x[3] * mul),
+                                   attn::pack_half(y[0] * mul, y[2] * mul), attn::pack_half(y[1] * mul, y[3] * mul));
+                }
+            }
+            fence_async();
+        }
+        __syncthreads();
+
+        bool ok = true;
+        if (warp == WARP_LOAD) {
+            // ---------------- records: four a step, two steps in flight
+            const int* table = a.pages + (int64_t)b * a.pages_stride;
+            unsigned issued = steps;
+            for (int t = 0; t < n && ok; ++t) {
+                const unsigned it = steps + t, st = it & 1;
+                const int rec = rec0 + t * STEP_RECORDS + lane;
+                int place = -2;  // no record here
+                if (lane < STEP_RECORDS && rec < rec_end) {
+                    const int pg = rec / a.page_groups, page = table[pg];
+                    const bool gone = page < 0 || page >= a.n_pages;
+                    if (gone) atomicOr(a.err, ERR_BAD_INDEX);
+                    place = gone ? -1 : (page * a.kv_heads + head) * a.page_groups + rec - pg * a.page_groups;
+                }
+                const int there = __popc(__ballot_sync(FULL, place >= 0));
+                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&raw_empty[st], (it / 2 - 1) & 1, abort_flag));
+                if (!ok) break;
+                if (lane < STEP_RECORDS) s_gone[it & 3][lane] = place < 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], there * REC);
+                __syncwarp();
+                if (place >= 0)
+                    bulk_g2s(smem + SM::RAW + (st * STEP_RECORDS + lane) * REC, a.cache + (int64_t)place * REC, REC,
+                             &raw_full[st]);
+                issued = it + 1;
+            }
+            if (!ok && lane == 0) {  // copies on their way land before the CTA ends
+                const uint64_t t0 = global_ns();
+                for (unsigned it = issued - min(issued, 2u); it < issued && global_ns() - t0 < WAIT_LIMIT_NS;)
+                    it += mbar_try_wait(&raw_full[it & 1], (it / 2) & 1);
+            }
+        } else if (warp == WARP_MMA) {
+            // ---------------- products
+            if (lane == 0 && n) {
+                constexpr uint32_t IDESC_S = (1u << 4) | ((STEP >> 3) << 17) | ((128 >> 4) << 24);
+                constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128 >> 4) << 24);
+                const uint64_t qd = smem_desc(smem_u32(smem + SM::Q), 128, D * 16);
+                const uint64_t kd = smem_desc(smem_u32(smem + SM::K), 128, D * 16);
+                const uint64_t vd = smem_desc(smem_u32(smem + SM::V), 128, STEP * 16);
+                const auto scores = [&](int x) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + S_COL + x * 128, qd + (uint64_t)((x * 128 * D * 2 + k * 256) >> 4),
+                               kd + (uint64_t)((k * 256) >> 4), IDESC_S, k > 0);
+                    commit(&s_full[x]);
+                };
+                ok = mbar_wait(&k_full, steps & 1, abort_flag);
+                fence_after();
+                for (int x = 0; x < tiles && ok; ++x) scores(x);
+                if (ok) commit(&k_empty);
+                for (int t = 0; t < n && ok; ++t) {
+                    const unsigned it = steps + t;
+                    for (int x = 0; x < tiles && ok; ++x) {
+                        if (x == 0) ok = mbar_wait(&v_full[it & 1], (it / 2) & 1, abort_flag);
+                        ok = ok && mbar_wait(&p_full[x], (x ? tile1_steps + t : it) & 1, abort_flag);
+                        if (!ok) break;
+                        fence_after();
+#pragma unroll
+                        for (int k = 0; k < STEP / 16; ++k)
+                            mma_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8,
+                                   vd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_O, t > 0 || k > 0);
+                        if (x == tiles - 1) commit(&v_empty[it & 1]);
+                        if (t + 1 < n) {
+                            if (x == 0) ok = mbar_wait(&k_full, (it + 1) & 1, abort_flag);
+                            if (!ok) break;
+                            fence_after();
+                            scores(x);
+                            if (x == tiles - 1) commit(&k_empty);
+                        }
+                    }
+                }
+                if (ok) {
+                    commit(&o_full);
+                } else {  // products on their way end before tensor memory is freed
+                    commit(&drain);
+                    const uint64_t t0 = global_ns();
+                    while (!mbar_try_wait(&drain, 0) && global_ns() - t0 < WAIT_LIMIT_NS) {
+                    }
+                }
+            }
+        } else if (warp >= SOFTMAX_WARPS) {
+            // ---------------- K and V of a step as operands
+            const int w = warp - SOFTMAX_WARPS, g = lane >> 2, c = lane & 3;
+            unsigned magic;
+            asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+            for (int t = 0; t < n && ok; ++t) {
+                const unsigned it = steps + t, st = it & 1;
+                ok = __all_sync(FULL, mbar_wait(&raw_full[st], (it / 2) & 1, abort_flag));
+                const int tok0 = (rec0 + t * STEP_RECORDS) * GROUP;
+                const uint8_t* raw = smem + SM::RAW + st * (STEP_RECORDS * REC);
+                // keys of record r that any row may see: [from, to) of its 32
+                const auto seen = [&](int r, int key) {
+                    const int at = tok0 + r * GROUP + key;
+                    return !s_gone[it & 3][r] && at >= sp.lo && at < sp.hi;
+                };
+                if (ok && it >= 1) ok = __all_sync(FULL, mbar_wait(&k_empty, (it - 1) & 1, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < (STEP_RECORDS * NB + UNPACK_WARPS - 1) / UNPACK_WARPS; ++i) {
+                    const int id = w + i * UNPACK_WARPS, r = id & (STEP_RECORDS - 1), kb = id / STEP_RECORDS;
+                    if (kb < NB) {
+                        const uint8_t* rec = raw + r * REC;
+                        const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
+                        const uint4 d4 = lds128(rec + NB * 1024 + kb * 64 + (g >> 1) * 16);
+                        const unsigned ws[4] = {w4.x, w4.y, w4.z, w4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                        const bool all = !s_gone[it & 3][r] && tok0 + r * GROUP >= sp.lo && tok0 + (r + 1) * GROUP <= sp.hi;
+                        uint8_t* to = smem + SM::K + r * (4 * D * 16) + (kb * 4 + c) * 128 + g * 16;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            unsigned one = (g & 1 ? ds[j] >> 16 : ds[j]) & 0xFFFF;
+                            if (!all && !seen(r, 8 * j + g)) one = 0;
+                            const __half2 d = attn::as_half2(one | one << 16);
+                            *reinterpret_cast<uint4*>(to + j * (D * 16)) =
+                                make_uint4(scaled_codes(ws[j], d, magic), scaled_codes(ws[j] >> 8, d, magic),
+                                           scaled_codes(ws[j] >> 4, d, magic), scaled_codes(ws[j] >> 12, d, magic));
+                        }
+                    }
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_full);
+                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&v_empty[st], (it / 2 - 1) & 1, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < (STEP_RECORDS * NB + UNPACK_WARPS - 1) / UNPACK_WARPS; ++i) {
+                    const int id = w + i * UNPACK_WARPS, r = id & (STEP_RECORDS - 1), kb = id / STEP_RECORDS;
+                    if (kb < NB) {
+                        const uint8_t* rec = raw + r * REC;
+                        const uint4 w4 = lds128(rec + NB * 512 + kb * 512 + lane * 16);
+                        const uint4 d4 = lds128(rec + NB * 1088 + kb * 64 + c * 16);
+                        const unsigned ws[4] = {w4.x, w4.y, w4.z, w4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                        const bool all = !s_gone[it & 3][r] && tok0 + r * GROUP >= sp.lo && tok0 + (r + 1) * GROUP <= sp.hi;
+                        uint8_t* to =
+                            smem + SM::V + st * (STEP * D * 2) + kb * (4 * STEP * 16) + r * (4 * 128) + g * 16 + c * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            unsigned two = ds[j];
+                            if (!all) {
+                                if (!seen(r, 8 * j + 2 * c)) two &= 0xFFFF0000u;
+                                if (!seen(r, 8 * j + 2 * c + 1)) two &= 0x0000FFFFu;
+                            }
+                            const __half2 d = attn::as_half2(two);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<unsigned*>(to + e * (STEP * 16) + j * 128) =
+                                    scaled_codes(ws[j] >> (4 * e), d, magic);
+                        }
+                    }
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&v_full[st]);
+                    mbar_arrive(&raw_empty[st]);
+                }
+            }
+        } else if (tile < tiles) {
+            // ---------------- softmax: this thread's row
+            const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S_COL + tile * 128;
+            const uint32_t o_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + O_COL + tile * 128;
+            const int p = seq.L - seq.n + qi;
+            const int hi = live && a.causal ? min(seq.L, p + 1) : sp.hi;
+            const int lo = live && a.window ? p - a.window + 1 : sp.lo;
+            float ref = -INFINITY, l = 0.f;
+            uint32_t r[32];
+            for (int t = 0; t < n; ++t) {
+                __syncwarp();
+                ok = __all_sync(FULL, mbar_wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1, abort_flag));
+                if (!ok) break;
+                fence_after();
+                const int key0 = (rec0 + t * STEP_RECORDS) * GROUP;
+                bool whole = key0 >= lo && key0 + STEP <= hi;
+                const int* gone = s_gone[(steps + t) & 3];
+#pragma unroll
+                for (int q = 0; q < STEP_RECORDS; ++q) whole &= !gone[q];
+                const bool masked = __any_sync(FULL, !whole);
+                // the row's maximum
+                float m = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    ld32(s_at + 32 * q, r);
+                    wait_ld(r);
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int key = key0 + 32 * q + e;
+                            if (key >= lo && key < hi && !gone[q]) m = fmaxf(m, __uint_as_float(r[e]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) m = fmaxf(m, __uint_as_float(r[e]));
+                    }
+                }
+                m *= f;
+                // O holds the steps before (S of this step was issued after their products)
+                if (__any_sync(FULL, m > ref + SLACK)) {
+                    const float now = fmaxf(ref, m);
+                    const float alpha = now == -INFINITY ? 0.f : attn::exp2_fast(ref - now);
+                    ref = now;
+                    l *= alpha;
+                    if (t > 0) {
+#pragma unroll
+                        for (int kb = 0; kb < NB; ++kb) {
+                            ld32(o_at + 32 * kb, r);
+                            wait_ld(r);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                            st32(o_at + 32 * kb, r);
+                        }
+                    }
+                }
+                const float by = ref == -INFINITY ? LIFT : LIFT - ref;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    ld32(s_at + 32 * q, r);
+                    wait_ld(r);
+                    uint32_t packed[16];
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = attn::fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                              make_float2(f, f), make_float2(by, by));
+                        if (masked) {
+                            const int key = key0 + 32 * q + e;
+                            if (key < lo || key >= hi || gone[q]) x.x = -INFINITY;
+                            if (key + 1 < lo || key + 1 >= hi || gone[q]) x.y = -INFINITY;
+                        }
+                        x = make_float2(attn::exp2_fast(x.x), attn::exp2_fast(x.y));
+                        sum = attn::add2(sum, x);
+                        packed[e / 2] = attn::pack_half(x.x, x.y);
+                    }
+                    l += sum.x + sum.y;
+                    st16(s_at + 16 * q, packed);  // P over the part of S that has been read
+                }
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[tile]);
+            }
+            // ---- the row's output, or its part
+            if (ok && n) ok = __all_sync(FULL, mbar_wait(&o_full, segments & 1, abort_flag));
+            fence_after();
+            const bool uncut = unit == 0 && unit_end == sp.units;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            float* part = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + row - first_row) * (D + 2);
+            const int64_t at = (int64_t)(seq.q0 + qi) * a.out.ts + (int64_t)qh * a.out.hs;
+            const int64_t yat = ((int64_t)(seq.q0 + qi) * ((int64_t)a.kv_heads * a.group) + qh) * NB;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                __syncwarp();
+                if (ok && n) {
+                    ld32(o_at + 32 * kb, r);
+                    wait_ld(r);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = 0;
+                }
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = uncut ? __uint_as_float(r[e]) * inv : __uint_as_float(r[e]);
+                if (live && !uncut) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        *reinterpret_cast<float2*>(part + kb * 32 + e) = make_float2(o[e], o[e + 1]);
+                }
+                if (live && uncut && a.out.data) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) storen<8>(a.out.data, at + kb * 32 + e, QMM_BF16, a.out.wide, o + e);
+                }
+                if (live && uncut && a.yq) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(o[e]));
+                    const float d = __fdiv_rn(top, 127.0f);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float q = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(o[e], d)), -127.f), 127.f) : 0.f;
+                        a.yq[(yat + kb) * 32 + e] = (int8_t)(int)q;
+                    }
+                    a.yd[yat + kb] = f32_to_f16_bits(d);
+                }
+            }
+            if (!uncut && live) part[D] = ref - LIFT, part[D + 1] = l;
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        fence_before();
+        __syncthreads();
+        fence_after();
+        if (*abort_flag) break;
+        if (cut && tid == 0 && unit == 0) {
+            const bool uncut = unit_end == sp.units;
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
+            a.meta[(int64_t)entry * a.kv_heads + head] = AttnMeta{first, last, u != u0, 0};
+        }
+        steps += n;
+        if (tiles == 2) tile1_steps += n;
+        segments += n > 0;
+        u += unit_end - unit;
+        unit = 0;
+        if (++head == a.kv_heads) head = 0, ++entry;
+        if (!cut) break;
+    }
+    __syncthreads();
+    if (warp == WARP_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS));
+}
+
+}  // namespace attn_tc
+
+AttnKernel attn_tc_kernel(int NB) {
+    static constexpr AttnKernel kernels[ATTN_TC_MAX_NB] = {
+        attn_tc::attn_tc_kernel<1>, attn_tc::attn_tc_kernel<2>, attn_tc::attn_tc_kernel<3>, attn_tc::attn_tc_kernel<4>};
+    return kernels[NB - 1];
+}
+
+int attn_tc_smem(int NB) {
+    static constexpr int bytes[ATTN_TC_MAX_NB] = {attn_tc::Smem<1>::BYTES, attn_tc::Smem<2>::BYTES,
+                                                  attn_tc::Smem<3>::BYTES, attn_tc::Smem<4>::BYTES};
+    return bytes[NB - 1];
+}
+
+int attn_tc_threads() { return attn_tc::THREADS; }
+
+}  // namespace qmm

@@ -15,6 +15,8 @@ keys seen, u = 2^-24 (half a step of fp32):
   the bound taken whole: 2^-11) as one part; 2^-38 of the largest weight times
   the largest |v| where the part is subnormal.
 * 16-bit outputs: half a step of their type.
+* bf16 with many rows a key/value head: k and v as fp16 (2^-11 each, so a score
+  is off by up to 2^-11 |scale| sum_e |q_e k_je| <= 2^-11 X 8 / 23).
 """
 import numpy as np
 import pytest
@@ -117,6 +119,8 @@ class Case:
         tol = mag * rel + N * 2.0 ** -38 * big
         if self.dtype != torch.float32:
             half = torch.finfo(self.dtype).eps / 2
+            if self.dtype == torch.bfloat16 and self.max_q * self.Hq // self.Hkv >= 32 and self.D <= 128:
+                tol = tol + mag * 2.0 ** -11 * (2 * X * 8 / 23 + 1)
             tol = (tol + mag * 2.0 ** -11) * (1 + half) + np.abs(ref) * half + 2.0 ** -25
         err = np.abs(_np(out) - ref)
         assert np.isfinite(err).all()
@@ -171,6 +175,59 @@ def test_chunks(n, L, Hq, Hkv, D, page, dtype):
     qmm = lib()
     c = Case(qmm, [L, L // 2, n], [n] * 3, Hq, Hkv, D, page, dtype, seed=n)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128])
+@pytest.mark.parametrize("lens,nqs,causal,window,Hq,Hkv,page", [
+    ([200], [64], True, 0, 1, 1, 32),                      # one tile, half of it
+    ([300, 128], [64, 64], True, 0, 4, 1, 64),             # two tiles
+    ([150, 64, 5], [100, 64, 5], True, 0, 6, 2, 32),       # more than one row block; fewer keys than queries
+    ([3, 700, 0, 257], [130, 40, 64, 1], True, 0, 4, 2, 96),
+    ([700, 90], [70, 90], True, 100, 3, 1, 32),            # a window
+    ([700, 90], [70, 90], False, 33, 3, 1, 128),
+    ([130, 127], [80, 80], False, 0, 8, 8, 32),
+    ([1, 128, 129, 127], [64, 64, 64, 64], True, 0, 2, 1, 32),
+])
+def test_many_rows(D, lens, nqs, causal, window, Hq, Hkv, page):
+    qmm = lib()
+    c = Case(qmm, lens, nqs, Hq, Hkv, D, page, "bf16", causal, window, seed=D + len(lens), q_start=True)
+    c.check(c.run())
+
+
+def test_many_rows_of_many_keys():
+    """Few row blocks and long contexts: items are cut over the CTAs, a CTA holds parts of several."""
+    qmm = lib()
+    c = Case(qmm, [2000, 40, 1500], [64] * 3, 2, 1, 64, 64, "bf16", seed=21)
+    first = c.run()
+    c.check(first)
+    for _ in range(3):
+        assert torch.equal(first, c.run())
+    c = Case(qmm, [1000, 900], [64] * 2, 8, 4, 32, 32, "bf16", False, 0, seed=22)
+    c.check(c.run())
+
+
+def test_many_rows_strided_quantized_and_missing_pages():
+    qmm = lib()
+    qmm.qmm_last_device_error()
+    c = Case(qmm, [400, 300], [70, 70], 4, 2, 64, 32, "bf16", strided=1, seed=23)
+    base = torch.full((140, 9, 65), 7.0, dtype=c.dtype, device=DEV)
+    out = base[:, 2:6, 1:]
+    qmm.qmm_attn_q4_0(c.op(out))
+    c.check(out)
+    base[:, 2:6, 1:] = 7.0
+    assert (base == 7.0).all()
+    yq = torch.full((140, 256), 99, dtype=torch.int8, device=DEV)
+    yd = torch.full((140, 8), 99, dtype=torch.int16, device=DEV)
+    plain = torch.empty(140, 4, 64, dtype=c.dtype, device=DEV)
+    qmm.qmm_attn_q4_0(c.op(plain, yq=yq, yd=yd))
+    # bf16 of the fp32 output that was quantized: off by half a bf16 step and half a code (and fp16's step in d)
+    d = yd.view(torch.float16).double()[:, :, None].expand(-1, -1, 32).reshape(140, 256)
+    off = (yq.double() * d - plain.double().view(140, 256)).abs()
+    assert (off <= 0.5 * d + plain.double().view(140, 256).abs() * (2.0 ** -8 + 2.0 ** -10)).all()
+    c.pages[0, 3] = c.cache.n_pages
+    out = c.run()
+    assert qmm.qmm_last_device_error() == 10
+    c.check(out, lambda b, L: np.ones(L, bool) if b else np.arange(L) // 32 != 3)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
