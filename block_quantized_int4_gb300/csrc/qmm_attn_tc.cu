@@ -11,19 +11,22 @@
 // Scales meet the codes here (d * (u - 8) rounded to fp16, 2^-12), so this form
 // serves bf16 alone, whose output rounds at 2^-9.
 //
-// A CTA (one an SM, 18 warps) holds two row tiles of 128 rows and walks the
+// A CTA (one an SM, 19 warps) holds two row tiles of 128 rows and walks the
 // keys in steps of 128 (4 records):
 //  - warps 0..3 and 4..7: the softmax of tile 0 and 1, a thread a row: S from
-//    tensor memory, weights back into its place as fp16 (P), the row's sum;
-//    O is rescaled only when the row's maximum grew by more than 2^SLACK.
-//  - warps 8..15: K and V of a step as fp16 operands.  The cache's word order
-//    makes them as it makes the warp MMA's: a word of K is eight values of one
-//    key (Q is laid down in the same order of its values), a word of V two
-//    keys of four values, so every store of a warp is one run of shared memory.
-//  - warp 16: page look-ups and bulk copies of records; warp 17: issues MMAs.
+//    tensor memory, weights back into its place as fp16 (P), the row's sum.
+//    One pass: the reference of the weights is what it was, unless a score is
+//    above it by more than SLACK; then O, the sum and what is written of P are
+//    rescaled first, which is rare.
+//  - warps 8..11: K of a step as fp16 operand, warps 12..15: V, a record a
+//    warp.  The cache's word order makes them as it makes the warp MMA's: a
+//    word of K is eight values of one key (Q is laid down in the same order of
+//    its values), a word of V two keys of four values, so every store of a
+//    warp is one run of shared memory.
+//  - warps 16, 17: page look-ups and bulk copies of the records' K and V parts
+//    (rings of two steps each); warp 18: issues the MMAs.
 // The two tiles take turns: while one is in its softmax, the other's products
-// run.  V is double, K single buffered (K of the next step is unpacked while
-// the softmaxes of this one run).
+// run.  K is double, V single buffered.
 //
 // Operands lie as K-major core matrices of 8 rows x 16 bytes without swizzle.
 // Every wait is bounded; on expiry the error word is set and the CTA ends.
@@ -38,8 +41,8 @@ namespace attn_tc {
 using attn::Seq;
 using attn::Span;
 
-constexpr int SOFTMAX_WARPS = 8, UNPACK_WARPS = 8;
-constexpr int WARP_LOAD = SOFTMAX_WARPS + UNPACK_WARPS, WARP_MMA = WARP_LOAD + 1;
+constexpr int SOFTMAX_WARPS = 8, WARP_K = 8, WARP_V = 12, UNPACK_WARPS = 4;  // of K, and of V
+constexpr int WARP_LOAD_K = 16, WARP_LOAD_V = 17, WARP_MMA = 18;
 constexpr int THREADS = (WARP_MMA + 1) * 32;
 constexpr int STEP = 128;              // keys of a step
 constexpr int STEP_RECORDS = STEP / GROUP;
@@ -52,10 +55,11 @@ struct Smem {
     static constexpr int D = NB * 32;
     static constexpr int REC = record_bytes(D);
     static constexpr int Q = 0;                          // [2][128][D] fp16
-    static constexpr int K = Q + 2 * 128 * D * 2;        // [128][D]
-    static constexpr int V = K + STEP * D * 2;           // [2][D][128]
-    static constexpr int RAW = V + 2 * STEP * D * 2;     // [2][4][REC]
-    static constexpr int BYTES = RAW + 2 * STEP_RECORDS * REC;
+    static constexpr int K = Q + 2 * 128 * D * 2;        // [2][128][D]
+    static constexpr int V = K + 2 * STEP * D * 2;       // [D][128]
+    static constexpr int PART = REC / 2;                 // a record's codes and scales of K, or of V
+    static constexpr int RAW = V + STEP * D * 2;         // [K, V][2][4][PART]
+    static constexpr int BYTES = RAW + 2 * 2 * STEP_RECORDS * PART;
 };
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -115,12 +119,14 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
         QMM_I8(r, 0), QMM_I8(r, 8)
         : "memory");
 }
-__device__ __forceinline__ void st32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void ld16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-        QMM_I8(r, 0), QMM_I8(r, 8), QMM_I8(r, 16), QMM_I8(r, 24)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : QMM_R8(r, 0), QMM_R8(r, 8)
+        : "r"(at));
+}
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QMM_U8(r, 0), QMM_U8(r, 8) : : "memory");
 }
 
 // Two codes times a pair of scales: nibbles 0 and 4 of w.
@@ -135,8 +141,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     constexpr int BLOCK_ROWS = ATTN_TC_ROWS;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ attn::Share<THREADS / 32> sh;
-    __shared__ uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
-    __shared__ int s_gone[4][STEP_RECORDS];  // four steps: a softmax reads the flags of a step two copies later
+    __shared__ uint64_t raw_full[2][2], raw_empty[2][2];  // [K, V][stage]
+    __shared__ uint64_t k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], o_full, drain;
+    // records that are not there; of eight steps: a softmax reads the flags of a step while later ones are copied
+    // (a copy is at most four steps ahead of the products of a step, which follow its softmax)
+    __shared__ int s_gone[2][8][STEP_RECORDS];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
@@ -144,15 +153,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], UNPACK_WARPS);
-            mbar_init(&v_full[i], UNPACK_WARPS);
-            mbar_init(&v_empty[i], 1);
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(&raw_full[kv][i], 1);
+                mbar_init(&raw_empty[kv][i], UNPACK_WARPS);
+            }
+            mbar_init(&k_full[i], UNPACK_WARPS);
+            mbar_init(&k_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
-        mbar_init(&k_full, UNPACK_WARPS);
-        mbar_init(&k_empty, 1);
+        mbar_init(&v_full, UNPACK_WARPS);
+        mbar_init(&v_empty, 1);
         mbar_init(&o_full, 1);
         mbar_init(&drain, 1);
         s_abort = 0;
@@ -243,11 +254,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         __syncthreads();
 
         bool ok = true;
-        if (warp == WARP_LOAD) {
-            // ---------------- records: four a step, two steps in flight
+        if (warp == WARP_LOAD_K || warp == WARP_LOAD_V) {
+            // ---------------- records: four a step, two steps in flight; codes and scales of K or of V
+            const int kv = warp - WARP_LOAD_K;
             const int* table = a.pages + (int64_t)b * a.pages_stride;
             unsigned issued = steps;
-            for (int t = 0; t < n && ok; ++t) {
+            for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
                 const int rec = rec0 + t * STEP_RECORDS + lane;
                 int place = -2;  // no record here
@@ -258,21 +270,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     place = gone ? -1 : (page * a.kv_heads + head) * a.page_groups + rec - pg * a.page_groups;
                 }
                 const int there = __popc(__ballot_sync(FULL, place >= 0));
-                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&raw_empty[st], (it / 2 - 1) & 1, abort_flag));
+                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&raw_empty[kv][st], (it / 2 - 1) & 1, abort_flag));
                 if (!ok) break;
-                if (lane < STEP_RECORDS) s_gone[it & 3][lane] = place < 0;
+                if (lane < STEP_RECORDS) s_gone[kv][it & 7][lane] = place < 0;
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], there * REC);
+                if (lane == 0) mbar_arrive_expect_tx(&raw_full[kv][st], there * SM::PART);
                 __syncwarp();
-                if (place >= 0)
-                    bulk_g2s(smem + SM::RAW + (st * STEP_RECORDS + lane) * REC, a.cache + (int64_t)place * REC, REC,
-                             &raw_full[st]);
+                if (place >= 0) {
+                    uint8_t* to = smem + SM::RAW + ((kv * 2 + st) * STEP_RECORDS + lane) * SM::PART;
+                    const uint8_t* from = a.cache + (int64_t)place * REC;
+                    bulk_g2s(to, from + kv * (NB * 512), NB * 512, &raw_full[kv][st]);
+                    bulk_g2s(to + NB * 512, from + NB * 1024 + kv * (NB * 64), NB * 64, &raw_full[kv][st]);
+                }
                 issued = it + 1;
             }
             if (!ok && lane == 0) {  // copies on their way land before the CTA ends
                 const uint64_t t0 = global_ns();
                 for (unsigned it = issued - min(issued, 2u); it < issued && global_ns() - t0 < WAIT_LIMIT_NS;)
-                    it += mbar_try_wait(&raw_full[it & 1], (it / 2) & 1);
+                    it += mbar_try_wait(&raw_full[kv][it & 1], (it / 2) & 1);
             }
         } else if (warp == WARP_MMA) {
             // ---------------- products
@@ -282,35 +297,35 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 const uint64_t qd = smem_desc(smem_u32(smem + SM::Q), 128, D * 16);
                 const uint64_t kd = smem_desc(smem_u32(smem + SM::K), 128, D * 16);
                 const uint64_t vd = smem_desc(smem_u32(smem + SM::V), 128, STEP * 16);
-                const auto scores = [&](int x) {
+                const auto scores = [&](int x, unsigned it) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         mma_ss(tmem + S_COL + x * 128, qd + (uint64_t)((x * 128 * D * 2 + k * 256) >> 4),
-                               kd + (uint64_t)((k * 256) >> 4), IDESC_S, k > 0);
+                               kd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_S, k > 0);
                     commit(&s_full[x]);
                 };
-                ok = mbar_wait(&k_full, steps & 1, abort_flag);
+                ok = mbar_wait(&k_full[steps & 1], (steps / 2) & 1, abort_flag);
                 fence_after();
-                for (int x = 0; x < tiles && ok; ++x) scores(x);
-                if (ok) commit(&k_empty);
+                for (int x = 0; x < tiles && ok; ++x) scores(x, steps);
+                if (ok) commit(&k_empty[steps & 1]);
                 for (int t = 0; t < n && ok; ++t) {
                     const unsigned it = steps + t;
                     for (int x = 0; x < tiles && ok; ++x) {
-                        if (x == 0) ok = mbar_wait(&v_full[it & 1], (it / 2) & 1, abort_flag);
+                        if (x == 0) ok = mbar_wait(&v_full, it & 1, abort_flag);
                         ok = ok && mbar_wait(&p_full[x], (x ? tile1_steps + t : it) & 1, abort_flag);
                         if (!ok) break;
                         fence_after();
 #pragma unroll
                         for (int k = 0; k < STEP / 16; ++k)
                             mma_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8,
-                                   vd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_O, t > 0 || k > 0);
-                        if (x == tiles - 1) commit(&v_empty[it & 1]);
+                                   vd + (uint64_t)((k * 256) >> 4), IDESC_O, t > 0 || k > 0);
+                        if (x == tiles - 1) commit(&v_empty);
                         if (t + 1 < n) {
-                            if (x == 0) ok = mbar_wait(&k_full, (it + 1) & 1, abort_flag);
+                            if (x == 0) ok = mbar_wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1, abort_flag);
                             if (!ok) break;
                             fence_after();
-                            scores(x);
-                            if (x == tiles - 1) commit(&k_empty);
+                            scores(x, it + 1);
+                            if (x == tiles - 1) commit(&k_empty[(it + 1) & 1]);
                         }
                     }
                 }
@@ -324,70 +339,58 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 }
             }
         } else if (warp >= SOFTMAX_WARPS) {
-            // ---------------- K and V of a step as operands
-            const int w = warp - SOFTMAX_WARPS, g = lane >> 2, c = lane & 3;
+            // ---------------- K or V of a step as operands, a record a warp
+            const int kv = warp >= WARP_V, rr = warp - (kv ? WARP_V : WARP_K), g = lane >> 2, c = lane & 3;
             unsigned magic;
             asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-            for (int t = 0; t < n && ok; ++t) {
+            for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
-                ok = __all_sync(FULL, mbar_wait(&raw_full[st], (it / 2) & 1, abort_flag));
-                const int tok0 = (rec0 + t * STEP_RECORDS) * GROUP;
-                const uint8_t* raw = smem + SM::RAW + st * (STEP_RECORDS * REC);
-                // keys of record r that any row may see: [from, to) of its 32
-                const auto seen = [&](int r, int key) {
-                    const int at = tok0 + r * GROUP + key;
-                    return !s_gone[it & 3][r] && at >= sp.lo && at < sp.hi;
-                };
-                if (ok && it >= 1) ok = __all_sync(FULL, mbar_wait(&k_empty, (it - 1) & 1, abort_flag));
+                bool there = mbar_wait(&raw_full[kv][st], (it / 2) & 1, abort_flag);
+                if (kv == 0 && it >= 2) there = there && mbar_wait(&k_empty[st], (it / 2 - 1) & 1, abort_flag);
+                if (kv == 1 && it >= 1) there = there && mbar_wait(&v_empty, (it - 1) & 1, abort_flag);
+                ok = __all_sync(FULL, there);
                 if (!ok) break;
+                const uint8_t* rec = smem + SM::RAW + ((kv * 2 + st) * STEP_RECORDS + rr) * SM::PART;
+                // which of the record's keys any row may see
+                const int key0 = (rec0 + t * STEP_RECORDS + rr) * GROUP;
+                const bool gone = s_gone[kv][it & 7][rr] != 0;
+                const bool all = !gone && key0 >= sp.lo && key0 + GROUP <= sp.hi;
+                const auto seen = [&](int key) { return !gone && key0 + key >= sp.lo && key0 + key < sp.hi; };
+                if (kv == 0) {
+                    uint8_t* to = smem + SM::K + st * (STEP * D * 2) + rr * (4 * D * 16) + c * 128 + g * 16;
 #pragma unroll
-                for (int i = 0; i < (STEP_RECORDS * NB + UNPACK_WARPS - 1) / UNPACK_WARPS; ++i) {
-                    const int id = w + i * UNPACK_WARPS, r = id & (STEP_RECORDS - 1), kb = id / STEP_RECORDS;
-                    if (kb < NB) {
-                        const uint8_t* rec = raw + r * REC;
+                    for (int kb = 0; kb < NB; ++kb) {
                         const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
-                        const uint4 d4 = lds128(rec + NB * 1024 + kb * 64 + (g >> 1) * 16);
+                        const uint4 d4 = lds128(rec + NB * 512 + kb * 64 + (g >> 1) * 16);
                         const unsigned ws[4] = {w4.x, w4.y, w4.z, w4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-                        const bool all = !s_gone[it & 3][r] && tok0 + r * GROUP >= sp.lo && tok0 + (r + 1) * GROUP <= sp.hi;
-                        uint8_t* to = smem + SM::K + r * (4 * D * 16) + (kb * 4 + c) * 128 + g * 16;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            unsigned one = (g & 1 ? ds[j] >> 16 : ds[j]) & 0xFFFF;
-                            if (!all && !seen(r, 8 * j + g)) one = 0;
-                            const __half2 d = attn::as_half2(one | one << 16);
-                            *reinterpret_cast<uint4*>(to + j * (D * 16)) =
+                            unsigned one = __byte_perm(ds[j], 0, g & 1 ? 0x3232 : 0x1010);
+                            if (!all && !seen(8 * j + g)) one = 0;
+                            const __half2 d = attn::as_half2(one);
+                            *reinterpret_cast<uint4*>(to + kb * 512 + j * (D * 16)) =
                                 make_uint4(scaled_codes(ws[j], d, magic), scaled_codes(ws[j] >> 8, d, magic),
                                            scaled_codes(ws[j] >> 4, d, magic), scaled_codes(ws[j] >> 12, d, magic));
                         }
                     }
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&k_full);
-                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&v_empty[st], (it / 2 - 1) & 1, abort_flag));
-                if (!ok) break;
+                } else {
+                    uint8_t* to = smem + SM::V + rr * (4 * 128) + g * 16 + c * 4;
 #pragma unroll
-                for (int i = 0; i < (STEP_RECORDS * NB + UNPACK_WARPS - 1) / UNPACK_WARPS; ++i) {
-                    const int id = w + i * UNPACK_WARPS, r = id & (STEP_RECORDS - 1), kb = id / STEP_RECORDS;
-                    if (kb < NB) {
-                        const uint8_t* rec = raw + r * REC;
-                        const uint4 w4 = lds128(rec + NB * 512 + kb * 512 + lane * 16);
-                        const uint4 d4 = lds128(rec + NB * 1088 + kb * 64 + c * 16);
+                    for (int kb = 0; kb < NB; ++kb) {
+                        const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
+                        const uint4 d4 = lds128(rec + NB * 512 + kb * 64 + c * 16);
                         const unsigned ws[4] = {w4.x, w4.y, w4.z, w4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-                        const bool all = !s_gone[it & 3][r] && tok0 + r * GROUP >= sp.lo && tok0 + (r + 1) * GROUP <= sp.hi;
-                        uint8_t* to =
-                            smem + SM::V + st * (STEP * D * 2) + kb * (4 * STEP * 16) + r * (4 * 128) + g * 16 + c * 4;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             unsigned two = ds[j];
                             if (!all) {
-                                if (!seen(r, 8 * j + 2 * c)) two &= 0xFFFF0000u;
-                                if (!seen(r, 8 * j + 2 * c + 1)) two &= 0x0000FFFFu;
+                                if (!seen(8 * j + 2 * c)) two &= 0xFFFF0000u;
+                                if (!seen(8 * j + 2 * c + 1)) two &= 0x0000FFFFu;
                             }
                             const __half2 d = attn::as_half2(two);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<unsigned*>(to + e * (STEP * 16) + j * 128) =
+                                *reinterpret_cast<unsigned*>(to + (kb * 4 + e) * (STEP * 16) + j * 128) =
                                     scaled_codes(ws[j] >> (4 * e), d, magic);
                         }
                     }
@@ -395,8 +398,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 fence_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&v_full[st]);
-                    mbar_arrive(&raw_empty[st]);
+                    mbar_arrive(kv ? &v_full : &k_full[st]);
+                    mbar_arrive(&raw_empty[kv][st]);
                 }
             }
         } else if (tile < tiles) {
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             const int hi = live && a.causal ? min(seq.L, p + 1) : sp.hi;
             const int lo = live && a.window ? p - a.window + 1 : sp.lo;
             float ref = -INFINITY, l = 0.f;
-            uint32_t r[32];
+            uint32_t r[2][32];
             for (int t = 0; t < n; ++t) {
                 __syncwarp();
                 ok = __all_sync(FULL, mbar_wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1, abort_flag));
@@ -415,61 +418,67 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 fence_after();
                 const int key0 = (rec0 + t * STEP_RECORDS) * GROUP;
                 bool whole = key0 >= lo && key0 + STEP <= hi;
-                const int* gone = s_gone[(steps + t) & 3];
+                const int* gone = s_gone[0][(steps + t) & 7];
 #pragma unroll
                 for (int q = 0; q < STEP_RECORDS; ++q) whole &= !gone[q];
                 const bool masked = __any_sync(FULL, !whole);
-                // the row's maximum
-                float m = -INFINITY;
+                ld32(s_at, r[0]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    ld32(s_at + 32 * q, r);
-                    wait_ld(r);
+                    uint32_t(&s)[32] = r[q & 1];
+                    wait_ld(s);
+                    if (q < 3) ld32(s_at + 32 * (q + 1), r[(q + 1) & 1]);
                     if (masked) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const int key = key0 + 32 * q + e;
-                            if (key >= lo && key < hi && !gone[q]) m = fmaxf(m, __uint_as_float(r[e]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) m = fmaxf(m, __uint_as_float(r[e]));
-                    }
-                }
-                m *= f;
-                // O holds the steps before (S of this step was issued after their products)
-                if (__any_sync(FULL, m > ref + SLACK)) {
-                    const float now = fmaxf(ref, m);
-                    const float alpha = now == -INFINITY ? 0.f : attn::exp2_fast(ref - now);
-                    ref = now;
-                    l *= alpha;
-                    if (t > 0) {
-#pragma unroll
-                        for (int kb = 0; kb < NB; ++kb) {
-                            ld32(o_at + 32 * kb, r);
-                            wait_ld(r);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                            st32(o_at + 32 * kb, r);
+                            if (key < lo || key >= hi || gone[q]) s[e] = 0xFF800000u;
                         }
                     }
-                }
-                const float by = ref == -INFINITY ? LIFT : LIFT - ref;
+                    float m4[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    ld32(s_at + 32 * q, r);
-                    wait_ld(r);
+                    for (int e = 0; e < 4; ++e)
+                        m4[e] = fmaxf(fmaxf(fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4])),
+                                            fmaxf(__uint_as_float(s[e + 8]), __uint_as_float(s[e + 12]))),
+                                      fmaxf(fmaxf(__uint_as_float(s[e + 16]), __uint_as_float(s[e + 20])),
+                                            fmaxf(__uint_as_float(s[e + 24]), __uint_as_float(s[e + 28]))));
+                    const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
+                    if (__any_sync(FULL, m > ref + SLACK)) {
+                        // O holds the steps before (this S was issued after their products); all that
+                        // the row has so far, P of this step included, moves to the new reference
+                        const float now = fmaxf(ref, m);
+                        const float alpha = now == -INFINITY ? 0.f : attn::exp2_fast(ref - now);
+                        ref = now;
+                        l *= alpha;
+                        uint32_t x[16];
+                        if (t > 0) {
+#pragma unroll
+                            for (int i = 0; i < 2 * NB; ++i) {
+                                ld16(o_at + 16 * i, x);
+                                wait_ld(x);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                                st16(o_at + 16 * i, x);
+                            }
+                        }
+                        const __half2 a2 = __float2half2_rn(alpha);
+                        wait_st();
+#pragma unroll
+                        for (int i = 0; i < q; ++i) {
+                            ld16(s_at + 16 * i, x);
+                            wait_ld(x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[e] = attn::as_bits(__hmul2(attn::as_half2(x[e]), a2));
+                            st16(s_at + 16 * i, x);
+                        }
+                    }
+                    const float by = ref == -INFINITY ? LIFT : LIFT - ref;
                     uint32_t packed[16];
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = attn::fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                        float2 x = attn::fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
                                               make_float2(f, f), make_float2(by, by));
-                        if (masked) {
-                            const int key = key0 + 32 * q + e;
-                            if (key < lo || key >= hi || gone[q]) x.x = -INFINITY;
-                            if (key + 1 < lo || key + 1 >= hi || gone[q]) x.y = -INFINITY;
-                        }
                         x = make_float2(attn::exp2_fast(x.x), attn::exp2_fast(x.y));
                         sum = attn::add2(sum, x);
                         packed[e / 2] = attn::pack_half(x.x, x.y);
@@ -493,16 +502,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 __syncwarp();
+                uint32_t(&v)[32] = r[kb & 1];
                 if (ok && n) {
-                    ld32(o_at + 32 * kb, r);
-                    wait_ld(r);
+                    ld32(o_at + 32 * kb, v);
+                    wait_ld(v);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0;
+                    for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
                 float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = uncut ? __uint_as_float(r[e]) * inv : __uint_as_float(r[e]);
+                for (int e = 0; e < 32; ++e) o[e] = uncut ? __uint_as_float(v[e]) * inv : __uint_as_float(v[e]);
                 if (live && !uncut) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
