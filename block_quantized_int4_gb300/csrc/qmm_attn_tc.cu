@@ -32,6 +32,8 @@
 // Every wait is bounded; on expiry the error word is set and the CTA ends.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "qmm_attn.cuh"
 #include "qmm_attn_tc.h"
 
@@ -43,7 +45,10 @@ using attn::Span;
 
 constexpr int SOFTMAX_WARPS = 8, WARP_K = 8, WARP_V = 12, UNPACK_WARPS = 4;  // of K, and of V
 constexpr int WARP_LOAD_K = 16, WARP_LOAD_V = 17, WARP_MMA = 18;
-constexpr int THREADS = (WARP_MMA + 1) * 32;
+constexpr int THREADS = 20 * 32;  // five warpgroups; the last warp only keeps its warpgroup whole
+// Registers a thread: 96 at launch (61,440 of the SM), then 144 for the two
+// softmax warpgroups and 64 for the three others (61,440).
+constexpr int SOFTMAX_REGS = 144, OTHER_REGS = 64;
 constexpr int STEP = 128;              // keys of a step
 constexpr int STEP_RECORDS = STEP / GROUP;
 constexpr float SLACK = 5.f;           // weights reach 2^(SLACK + LIFT)
@@ -129,6 +134,17 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QMM_U8(r, 0), QMM_U8(r, 8) : : "memory");
 }
 
+// A bounded wait whose polls do little else: the hardware holds each back for
+// a while; the clock and the abort flag are looked at now and then.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (unsigned i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 31) == 0 && (*abort || global_ns() - t0 > WAIT_LIMIT_NS)) return false;
+    }
+}
+
 // Two codes times a pair of scales: nibbles 0 and 4 of w.
 __device__ __forceinline__ unsigned scaled_codes(unsigned w, __half2 d, unsigned magic) {
     return attn::as_bits(__hmul2(attn::as_half2(attn::signed_codes<0>(w, magic)), d));
@@ -196,6 +212,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         entry = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
     }
 
+    // The walk over the CTA's segments, once for each kind of warp (their register budgets differ).
+    const auto walk = [&](auto softmax_role) {
+    constexpr bool SOFTMAX = decltype(softmax_role)::value;
     unsigned steps = 0, segments = 0;  // before this segment: phases of the barriers
     unsigned tile1_steps = 0;          // of them, those of tile 1
     for (int u = u0; u < u1;) {
@@ -217,10 +236,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         // ---- the softmax warps lay down their rows of Q
         const int tile = warp >> 2;  // of a softmax warp
         const int row = first_row + (tile << 7) + (tid & 127);
-        const bool live = warp < SOFTMAX_WARPS && row < rows;
+        const bool live = SOFTMAX && row < rows;
         const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
         float f = 1.f;
-        if (warp < SOFTMAX_WARPS && tile < tiles) {
+        if (SOFTMAX && tile < tiles) {
             const int64_t at = (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs;
             float top = 0.f;
 #pragma unroll
@@ -254,6 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         __syncthreads();
 
         bool ok = true;
+        if constexpr (!SOFTMAX) {
         if (warp == WARP_LOAD_K || warp == WARP_LOAD_V) {
             // ---------------- records: four a step, two steps in flight; codes and scales of K or of V
             const int kv = warp - WARP_LOAD_K;
@@ -270,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     place = gone ? -1 : (page * a.kv_heads + head) * a.page_groups + rec - pg * a.page_groups;
                 }
                 const int there = __popc(__ballot_sync(FULL, place >= 0));
-                if (it >= 2) ok = __all_sync(FULL, mbar_wait(&raw_empty[kv][st], (it / 2 - 1) & 1, abort_flag));
+                if (it >= 2) ok = __all_sync(FULL, wait(&raw_empty[kv][st], (it / 2 - 1) & 1, abort_flag));
                 if (!ok) break;
                 if (lane < STEP_RECORDS) s_gone[kv][it & 7][lane] = place < 0;
                 __syncwarp();
@@ -304,15 +324,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                                kd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_S, k > 0);
                     commit(&s_full[x]);
                 };
-                ok = mbar_wait(&k_full[steps & 1], (steps / 2) & 1, abort_flag);
+                ok = wait(&k_full[steps & 1], (steps / 2) & 1, abort_flag);
                 fence_after();
                 for (int x = 0; x < tiles && ok; ++x) scores(x, steps);
                 if (ok) commit(&k_empty[steps & 1]);
                 for (int t = 0; t < n && ok; ++t) {
                     const unsigned it = steps + t;
                     for (int x = 0; x < tiles && ok; ++x) {
-                        if (x == 0) ok = mbar_wait(&v_full, it & 1, abort_flag);
-                        ok = ok && mbar_wait(&p_full[x], (x ? tile1_steps + t : it) & 1, abort_flag);
+                        if (x == 0) ok = wait(&v_full, it & 1, abort_flag);
+                        ok = ok && wait(&p_full[x], (x ? tile1_steps + t : it) & 1, abort_flag);
                         if (!ok) break;
                         fence_after();
 #pragma unroll
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                                    vd + (uint64_t)((k * 256) >> 4), IDESC_O, t > 0 || k > 0);
                         if (x == tiles - 1) commit(&v_empty);
                         if (t + 1 < n) {
-                            if (x == 0) ok = mbar_wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1, abort_flag);
+                            if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1, abort_flag);
                             if (!ok) break;
                             fence_after();
                             scores(x, it + 1);
@@ -338,16 +358,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     }
                 }
             }
-        } else if (warp >= SOFTMAX_WARPS) {
+        } else if (warp < WARP_LOAD_K) {
             // ---------------- K or V of a step as operands, a record a warp
             const int kv = warp >= WARP_V, rr = warp - (kv ? WARP_V : WARP_K), g = lane >> 2, c = lane & 3;
             unsigned magic;
             asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
             for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
-                bool there = mbar_wait(&raw_full[kv][st], (it / 2) & 1, abort_flag);
-                if (kv == 0 && it >= 2) there = there && mbar_wait(&k_empty[st], (it / 2 - 1) & 1, abort_flag);
-                if (kv == 1 && it >= 1) there = there && mbar_wait(&v_empty, (it - 1) & 1, abort_flag);
+                bool there = wait(&raw_full[kv][st], (it / 2) & 1, abort_flag);
+                if (kv == 0 && it >= 2) there = there && wait(&k_empty[st], (it / 2 - 1) & 1, abort_flag);
+                if (kv == 1 && it >= 1) there = there && wait(&v_empty, (it - 1) & 1, abort_flag);
                 ok = __all_sync(FULL, there);
                 if (!ok) break;
                 const uint8_t* rec = smem + SM::RAW + ((kv * 2 + st) * STEP_RECORDS + rr) * SM::PART;
@@ -402,6 +422,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     mbar_arrive(&raw_empty[kv][st]);
                 }
             }
+        }
         } else if (tile < tiles) {
             // ---------------- softmax: this thread's row
             const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + S_COL + tile * 128;
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             uint32_t r[2][32];
             for (int t = 0; t < n; ++t) {
                 __syncwarp();
-                ok = __all_sync(FULL, mbar_wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1, abort_flag));
+                ok = __all_sync(FULL, wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1, abort_flag));
                 if (!ok) break;
                 fence_after();
                 const int key0 = (rec0 + t * STEP_RECORDS) * GROUP;
@@ -492,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&p_full[tile]);
             }
             // ---- the row's output, or its part
-            if (ok && n) ok = __all_sync(FULL, mbar_wait(&o_full, segments & 1, abort_flag));
+            if (ok && n) ok = __all_sync(FULL, wait(&o_full, segments & 1, abort_flag));
             fence_after();
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -557,6 +578,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         unit = 0;
         if (++head == a.kv_heads) head = 0, ++entry;
         if (!cut) break;
+    }
+    };
+    if (warp < SOFTMAX_WARPS) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+        walk(std::true_type{});
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+        walk(std::false_type{});
     }
     __syncthreads();
     if (warp == WARP_MMA)
