@@ -100,8 +100,8 @@ AttnKernel kernel_of(int dtype, int NB) {
     return dtype == QMM_F32 ? attn_kernel_f32(NB) : dtype == QMM_F16 ? attn_kernel_f16(NB) : attn_kernel_bf16(NB);
 }
 
-// Opts a kernel into the shared memory of a device, once.
-bool prepared(AttnKernel k, int kind, int NB, int optin) {
+// Opts a kernel into `most` bytes of dynamic shared memory, once a device.
+bool prepared(AttnKernel k, int kind, int NB, int most) {
     static std::mutex mu;
     static bool done[64][4][8];
     int dev = 0;
@@ -109,7 +109,7 @@ bool prepared(AttnKernel k, int kind, int NB, int optin) {
     std::lock_guard<std::mutex> lk(mu);
     bool& d = done[dev][kind][NB - 1];
     if (!d)
-        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 4096) == cudaSuccess &&
+        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess &&
             cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
                 cudaSuccess;
     if (!d) cudaGetLastError();
@@ -183,7 +183,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.err = device_error_word();
     const int NB = op->cache.head_dim / QK;
     const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB);
-    if (!prepared(kernel, p.tc ? 3 : op->q.dtype, NB, optin)) return QMM_ERR_CUDA;
+    if (!prepared(kernel, p.tc ? 3 : op->q.dtype, NB, p.tc ? p.smem : optin - 4096)) return QMM_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.mode == ATTN_CUT ? p.ctas : p.items * p.cluster));

@@ -11,22 +11,22 @@
 // Scales meet the codes here (d * (u - 8) rounded to fp16, 2^-12), so this form
 // serves bf16 alone, whose output rounds at 2^-9.
 //
-// A CTA (one an SM, 19 warps) holds two row tiles of 128 rows and walks the
+// A CTA (one an SM, 23 warps) holds two row tiles of 128 rows and walks the
 // keys in steps of 128 (4 records):
 //  - warps 0..3 and 4..7: the softmax of tile 0 and 1, a thread a row: S from
 //    tensor memory, weights back into its place as fp16 (P), the row's sum.
 //    One pass: the reference of the weights is what it was, unless a score is
 //    above it by more than SLACK; then O, the sum and what is written of P are
 //    rescaled first, which is rare.
-//  - warps 8..11: K of a step as fp16 operand, warps 12..15: V, a record a
-//    warp.  The cache's word order makes them as it makes the warp MMA's: a
+//  - warps 8..15: V of a step as fp16 operand, half a record a warp, warps
+//    16..19: K, a record a warp.  The cache's word order makes them as it makes the warp MMA's: a
 //    word of K is eight values of one key (Q is laid down in the same order of
 //    its values), a word of V two keys of four values, so every store of a
 //    warp is one run of shared memory.
-//  - warps 16, 17: page look-ups and bulk copies of the records' K and V parts
-//    (rings of two steps each); warp 18: issues the MMAs.
+//  - warps 20, 21: page look-ups and bulk copies of the records' K and V parts
+//    (rings of records); warp 22: issues the MMAs.
 // The two tiles take turns: while one is in its softmax, the other's products
-// run.  K is double, V single buffered.
+// run.  The operands of K and V are double buffered.
 //
 // Operands lie as K-major core matrices of 8 rows x 16 bytes without swizzle.
 // Every wait is bounded; on expiry the error word is set and the CTA ends.
@@ -43,12 +43,14 @@ namespace attn_tc {
 using attn::Seq;
 using attn::Span;
 
-constexpr int SOFTMAX_WARPS = 8, WARP_K = 8, WARP_V = 12, UNPACK_WARPS = 4;  // of K, and of V
-constexpr int WARP_LOAD_K = 16, WARP_LOAD_V = 17, WARP_MMA = 18;
-constexpr int THREADS = 20 * 32;  // five warpgroups; the last warp only keeps its warpgroup whole
-// Registers a thread: 96 at launch (61,440 of the SM), then 144 for the two
-// softmax warpgroups and 64 for the three others (61,440).
-constexpr int SOFTMAX_REGS = 144, OTHER_REGS = 64;
+constexpr int SOFTMAX_WARPS = 8, WARP_V = 8, WARP_K = 16;
+constexpr int V_WARPS = 8, K_WARPS = 4;   // two warps a record of V, one a record of K
+constexpr int K_SLOTS = 8, V_SLOTS = 6;   // records of the rings (what shared memory has left at D = 128)
+constexpr int WARP_LOAD_K = 20, WARP_LOAD_V = 21, WARP_MMA = 22;
+constexpr int THREADS = 24 * 32;  // six warpgroups; the last warp only keeps its warpgroup whole
+// Registers a thread: 80 at launch (61,440 of the SM), then 144 for the two
+// softmax warpgroups and 48 for the four others (61,440).
+constexpr int SOFTMAX_REGS = 144, OTHER_REGS = 48;
 constexpr int STEP = 128;              // keys of a step
 constexpr int STEP_RECORDS = STEP / GROUP;
 constexpr float SLACK = 5.f;           // weights reach 2^(SLACK + LIFT)
@@ -61,10 +63,10 @@ struct Smem {
     static constexpr int REC = record_bytes(D);
     static constexpr int Q = 0;                          // [2][128][D] fp16
     static constexpr int K = Q + 2 * 128 * D * 2;        // [2][128][D]
-    static constexpr int V = K + 2 * STEP * D * 2;       // [D][128]
+    static constexpr int V = K + 2 * STEP * D * 2;       // [2][D][128]
     static constexpr int PART = REC / 2;                 // a record's codes and scales of K, or of V
-    static constexpr int RAW = V + STEP * D * 2;         // [K, V][2][4][PART]
-    static constexpr int BYTES = RAW + 2 * 2 * STEP_RECORDS * PART;
+    static constexpr int RAW = V + 2 * STEP * D * 2;     // rings of [K_SLOTS] and [V_SLOTS] parts
+    static constexpr int BYTES = RAW + (K_SLOTS + V_SLOTS) * PART;
 };
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -134,15 +136,25 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QMM_U8(r, 0), QMM_U8(r, 8) : : "memory");
 }
 
-// A bounded wait whose polls do little else: the hardware holds each back for
-// a while; the clock and the abort flag are looked at now and then.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (unsigned i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 31) == 0 && (*abort || global_ns() - t0 > WAIT_LIMIT_NS)) return false;
-    }
+// A bounded wait: up to 2^24 tries, each held back by the hardware for some
+// tens of cycles (seconds in all).  The loop is five instructions, for up to
+// six warps of a scheduler poll while the others compute.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 16777216;\n\t"
+        "@q bra AGAIN;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Two codes times a pair of scales: nibbles 0 and 4 of w.
@@ -157,29 +169,30 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     constexpr int BLOCK_ROWS = ATTN_TC_ROWS;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ attn::Share<THREADS / 32> sh;
-    __shared__ uint64_t raw_full[2][2], raw_empty[2][2];  // [K, V][stage]
-    __shared__ uint64_t k_full[2], k_empty[2], v_full, v_empty, s_full[2], p_full[2], o_full, drain;
+    __shared__ uint64_t raw_full[2][8], raw_empty[2][8];  // [K, V][slot]
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full, drain;
     // records that are not there; of eight steps: a softmax reads the flags of a step while later ones are copied
     // (a copy is at most four steps ahead of the products of a step, which follow its softmax)
     __shared__ int s_gone[2][8][STEP_RECORDS];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    volatile int* abort_flag = &s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&raw_full[0][i], 1);
+            mbar_init(&raw_full[1][i], 1);
+            mbar_init(&raw_empty[0][i], 1);
+            mbar_init(&raw_empty[1][i], V_WARPS / STEP_RECORDS);
+        }
         for (int i = 0; i < 2; ++i) {
-            for (int kv = 0; kv < 2; ++kv) {
-                mbar_init(&raw_full[kv][i], 1);
-                mbar_init(&raw_empty[kv][i], UNPACK_WARPS);
-            }
-            mbar_init(&k_full[i], UNPACK_WARPS);
+            mbar_init(&k_full[i], K_WARPS);
             mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], V_WARPS);
+            mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
-        mbar_init(&v_full, UNPACK_WARPS);
-        mbar_init(&v_empty, 1);
         mbar_init(&o_full, 1);
         mbar_init(&drain, 1);
         s_abort = 0;
@@ -278,9 +291,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             // ---------------- records: four a step, two steps in flight; codes and scales of K or of V
             const int kv = warp - WARP_LOAD_K;
             const int* table = a.pages + (int64_t)b * a.pages_stride;
-            unsigned issued = steps;
-            for (int t = 0; t < n; ++t) {
-                const unsigned it = steps + t, st = it & 1;
+            const unsigned slots = kv ? V_SLOTS : K_SLOTS;
+            uint8_t* ring = smem + SM::RAW + kv * (K_SLOTS * SM::PART);
+            unsigned issued = steps * STEP_RECORDS;  // records so far, one after the other over all segments
+            for (int t = 0; t < n && ok; ++t) {
+                const unsigned it = steps + t;
                 const int rec = rec0 + t * STEP_RECORDS + lane;
                 int place = -2;  // no record here
                 if (lane < STEP_RECORDS && rec < rec_end) {
@@ -289,25 +304,31 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     if (gone) atomicOr(a.err, ERR_BAD_INDEX);
                     place = gone ? -1 : (page * a.kv_heads + head) * a.page_groups + rec - pg * a.page_groups;
                 }
-                const int there = __popc(__ballot_sync(FULL, place >= 0));
-                if (it >= 2) ok = __all_sync(FULL, wait(&raw_empty[kv][st], (it / 2 - 1) & 1, abort_flag));
-                if (!ok) break;
                 if (lane < STEP_RECORDS) s_gone[kv][it & 7][lane] = place < 0;
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&raw_full[kv][st], there * SM::PART);
-                __syncwarp();
-                if (place >= 0) {
-                    uint8_t* to = smem + SM::RAW + ((kv * 2 + st) * STEP_RECORDS + lane) * SM::PART;
-                    const uint8_t* from = a.cache + (int64_t)place * REC;
-                    bulk_g2s(to, from + kv * (NB * 512), NB * 512, &raw_full[kv][st]);
-                    bulk_g2s(to + NB * 512, from + NB * 1024 + kv * (NB * 64), NB * 64, &raw_full[kv][st]);
+                for (int r = 0; r < STEP_RECORDS; ++r) {
+                    const unsigned i = it * STEP_RECORDS + r, slot = i % slots;
+                    if (i >= slots) ok = __all_sync(FULL, wait(&raw_empty[kv][slot], (i / slots - 1) & 1));
+                    if (!ok) break;
+                    if (lane == r) {
+                        uint64_t* full = &raw_full[kv][slot];
+                        if (place < 0) {
+                            mbar_arrive(full);
+                        } else {
+                            uint8_t* to = ring + slot * SM::PART;
+                            const uint8_t* from = a.cache + (int64_t)place * REC;
+                            mbar_arrive_expect_tx(full, SM::PART);
+                            bulk_g2s(to, from + kv * (NB * 512), NB * 512, full);
+                            bulk_g2s(to + NB * 512, from + NB * 1024 + kv * (NB * 64), NB * 64, full);
+                        }
+                    }
+                    __syncwarp();
+                    issued = i + 1;
                 }
-                issued = it + 1;
             }
             if (!ok && lane == 0) {  // copies on their way land before the CTA ends
-                const uint64_t t0 = global_ns();
-                for (unsigned it = issued - min(issued, 2u); it < issued && global_ns() - t0 < WAIT_LIMIT_NS;)
-                    it += mbar_try_wait(&raw_full[kv][it & 1], (it / 2) & 1);
+                for (unsigned i = issued - min(issued, slots); i < issued; ++i)
+                    if (!wait(&raw_full[kv][i % slots], (i / slots) & 1)) break;
             }
         } else if (warp == WARP_MMA) {
             // ---------------- products
@@ -324,24 +345,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                                kd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_S, k > 0);
                     commit(&s_full[x]);
                 };
-                ok = wait(&k_full[steps & 1], (steps / 2) & 1, abort_flag);
+                ok = wait(&k_full[steps & 1], (steps / 2) & 1);
                 fence_after();
                 for (int x = 0; x < tiles && ok; ++x) scores(x, steps);
                 if (ok) commit(&k_empty[steps & 1]);
                 for (int t = 0; t < n && ok; ++t) {
                     const unsigned it = steps + t;
                     for (int x = 0; x < tiles && ok; ++x) {
-                        if (x == 0) ok = wait(&v_full, it & 1, abort_flag);
-                        ok = ok && wait(&p_full[x], (x ? tile1_steps + t : it) & 1, abort_flag);
+                        if (x == 0) ok = wait(&v_full[it & 1], (it / 2) & 1);
+                        ok = ok && wait(&p_full[x], (x ? tile1_steps + t : it) & 1);
                         if (!ok) break;
                         fence_after();
 #pragma unroll
                         for (int k = 0; k < STEP / 16; ++k)
                             mma_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8,
-                                   vd + (uint64_t)((k * 256) >> 4), IDESC_O, t > 0 || k > 0);
-                        if (x == tiles - 1) commit(&v_empty);
+                                   vd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_O, t > 0 || k > 0);
+                        if (x == tiles - 1) commit(&v_empty[it & 1]);
                         if (t + 1 < n) {
-                            if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1, abort_flag);
+                            if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1);
                             if (!ok) break;
                             fence_after();
                             scores(x, it + 1);
@@ -353,24 +374,23 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     commit(&o_full);
                 } else {  // products on their way end before tensor memory is freed
                     commit(&drain);
-                    const uint64_t t0 = global_ns();
-                    while (!mbar_try_wait(&drain, 0) && global_ns() - t0 < WAIT_LIMIT_NS) {
-                    }
+                    wait(&drain, 0);
                 }
             }
         } else if (warp < WARP_LOAD_K) {
             // ---------------- K or V of a step as operands, a record a warp
-            const int kv = warp >= WARP_V, rr = warp - (kv ? WARP_V : WARP_K), g = lane >> 2, c = lane & 3;
+            const int kv = warp < WARP_K, rr = kv ? (warp - WARP_V) & 3 : warp - WARP_K, g = lane >> 2, c = lane & 3;
+            const int half = (warp - WARP_V) >> 2;  // of the blocks of V
             unsigned magic;
             asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
             for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
-                bool there = wait(&raw_full[kv][st], (it / 2) & 1, abort_flag);
-                if (kv == 0 && it >= 2) there = there && wait(&k_empty[st], (it / 2 - 1) & 1, abort_flag);
-                if (kv == 1 && it >= 1) there = there && wait(&v_empty, (it - 1) & 1, abort_flag);
+                const unsigned i = it * STEP_RECORDS + rr, slots = kv ? V_SLOTS : K_SLOTS, slot = i % slots;
+                bool there = wait(&raw_full[kv][slot], (i / slots) & 1);
+                if (it >= 2) there = there && wait(kv ? &v_empty[st] : &k_empty[st], (it / 2 - 1) & 1);
                 ok = __all_sync(FULL, there);
                 if (!ok) break;
-                const uint8_t* rec = smem + SM::RAW + ((kv * 2 + st) * STEP_RECORDS + rr) * SM::PART;
+                const uint8_t* rec = smem + SM::RAW + (kv * K_SLOTS + slot) * SM::PART;
                 // which of the record's keys any row may see
                 const int key0 = (rec0 + t * STEP_RECORDS + rr) * GROUP;
                 const bool gone = s_gone[kv][it & 7][rr] != 0;
@@ -378,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 const auto seen = [&](int key) { return !gone && key0 + key >= sp.lo && key0 + key < sp.hi; };
                 if (kv == 0) {
                     uint8_t* to = smem + SM::K + st * (STEP * D * 2) + rr * (4 * D * 16) + c * 128 + g * 16;
-#pragma unroll
+#pragma unroll 1
                     for (int kb = 0; kb < NB; ++kb) {
                         const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
                         const uint4 d4 = lds128(rec + NB * 512 + kb * 64 + (g >> 1) * 16);
@@ -394,9 +414,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                         }
                     }
                 } else {
-                    uint8_t* to = smem + SM::V + rr * (4 * 128) + g * 16 + c * 4;
-#pragma unroll
-                    for (int kb = 0; kb < NB; ++kb) {
+                    uint8_t* to = smem + SM::V + st * (STEP * D * 2) + rr * (4 * 128) + g * 16 + c * 4;
+#pragma unroll 1
+                    for (int kb = half; kb < NB; kb += 2) {
                         const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
                         const uint4 d4 = lds128(rec + NB * 512 + kb * 64 + c * 16);
                         const unsigned ws[4] = {w4.x, w4.y, w4.z, w4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
@@ -418,8 +438,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 fence_async();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(kv ? &v_full : &k_full[st]);
-                    mbar_arrive(&raw_empty[kv][st]);
+                    mbar_arrive(kv ? &v_full[st] : &k_full[st]);
+                    mbar_arrive(&raw_empty[kv][slot]);
                 }
             }
         }
@@ -434,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             uint32_t r[2][32];
             for (int t = 0; t < n; ++t) {
                 __syncwarp();
-                ok = __all_sync(FULL, wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1, abort_flag));
+                ok = __all_sync(FULL, wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1));
                 if (!ok) break;
                 fence_after();
                 const int key0 = (rec0 + t * STEP_RECORDS) * GROUP;
@@ -443,12 +463,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int q = 0; q < STEP_RECORDS; ++q) whole &= !gone[q];
                 const bool masked = __any_sync(FULL, !whole);
-                ld32(s_at, r[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t(&s)[32] = r[q & 1];
+                const auto chunk = [&](int q, uint32_t(&s)[32], uint32_t(&next)[32]) {
                     wait_ld(s);
-                    if (q < 3) ld32(s_at + 32 * (q + 1), r[(q + 1) & 1]);
+                    if (q < 3) ld32(s_at + 32 * (q + 1), next);
                     if (masked) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -484,7 +501,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                         }
                         const __half2 a2 = __float2half2_rn(alpha);
                         wait_st();
-#pragma unroll
                         for (int i = 0; i < q; ++i) {
                             ld16(s_at + 16 * i, x);
                             wait_ld(x);
@@ -506,6 +522,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     }
                     l += sum.x + sum.y;
                     st16(s_at + 16 * q, packed);  // P over the part of S that has been read
+                };
+                ld32(s_at, r[0]);
+#pragma unroll 1
+                for (int q = 0; q < 4; q += 2) {
+                    chunk(q, r[0], r[1]);
+                    chunk(q + 1, r[1], r[0]);
                 }
                 wait_st();
                 fence_before();
@@ -513,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&p_full[tile]);
             }
             // ---- the row's output, or its part
-            if (ok && n) ok = __all_sync(FULL, wait(&o_full, segments & 1, abort_flag));
+            if (ok && n) ok = __all_sync(FULL, wait(&o_full, segments & 1));
             fence_after();
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -560,12 +582,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         }
         if (!ok) {
             if (lane == 0) atomicOr(a.err, ERR_TIMEOUT);
-            *abort_flag = 1;
+            s_abort = 1;
         }
         fence_before();
         __syncthreads();
         fence_after();
-        if (*abort_flag) break;
+        if (s_abort) break;
         if (cut && tid == 0 && unit == 0) {
             const bool uncut = unit_end == sp.units;
             const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
