@@ -69,24 +69,36 @@ struct Smem {
     static constexpr int BYTES = RAW + (K_SLOTS + V_SLOTS) * PART;
 };
 
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return ((addr >> 4) & 0x3FFFull) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46);
-}
+// Shared-memory operand: the low word of its descriptor holds the address and
+// the byte distance of core matrices adjacent along K (128), the high word
+// that along the rows and the version.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | ((128u >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t row_stride) { return ((row_stride >> 4) & 0x3FFFu) | (1u << 14); }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (+)= A B.  The operands are values that the whole warp agrees on, so that
+// they live in uniform registers; with per-thread ones each instruction waits
+// for several transfers (85 to 100 cycles an MMA instead of the tensor core's
+// 45 to 64).
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((int)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "n"(ADD)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((int)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "n"(ADD)
         : "memory");
+}
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -332,44 +344,61 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             }
         } else if (warp == WARP_MMA) {
             // ---------------- products
-            if (lane == 0 && n) {
-                constexpr uint32_t IDESC_S = (1u << 4) | ((STEP >> 3) << 17) | ((128 >> 4) << 24);
-                constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128 >> 4) << 24);
-                const uint64_t qd = smem_desc(smem_u32(smem + SM::Q), 128, D * 16);
-                const uint64_t kd = smem_desc(smem_u32(smem + SM::K), 128, D * 16);
-                const uint64_t vd = smem_desc(smem_u32(smem + SM::V), 128, STEP * 16);
-                const auto scores = [&](int x, unsigned it) {
+            const int un = __shfl_sync(FULL, n, 0), ut = __shfl_sync(FULL, tiles, 0);  // uniform
+            const unsigned us = __shfl_sync(FULL, steps, 0), us1 = __shfl_sync(FULL, tile1_steps, 0);
+            const bool one = elected();
+            constexpr uint32_t IDESC_S = (1u << 4) | ((STEP >> 3) << 17) | ((128 >> 4) << 24);
+            constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(D >> 3) << 17) | ((128 >> 4) << 24);
+            constexpr uint32_t QK_HI = desc_hi(D * 16), V_HI = desc_hi(STEP * 16), BUFFER = (STEP * D * 2) >> 4;
+            const uint32_t ud = __shfl_sync(FULL, tmem, 0);
+            const uint32_t q_lo = desc_lo(smem_u32(smem + SM::Q)), k_lo = desc_lo(smem_u32(smem + SM::K));
+            const uint32_t v_lo = desc_lo(smem_u32(smem + SM::V));
+            const auto scores = [&](int x, unsigned it) {
+                const uint32_t to = ud + S_COL + x * 128, q = q_lo + x * ((128 * D * 2) >> 4);
+                const uint32_t k0 = k_lo + (it & 1) * BUFFER;
+                if (one) {
+                    mma_ss<false>(to, q, QK_HI, k0, QK_HI, IDESC_S);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + S_COL + x * 128, qd + (uint64_t)((x * 128 * D * 2 + k * 256) >> 4),
-                               kd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_S, k > 0);
+                    for (int k = 1; k < D / 16; ++k) mma_ss<true>(to, q + k * 16, QK_HI, k0 + k * 16, QK_HI, IDESC_S);
                     commit(&s_full[x]);
-                };
-                ok = wait(&k_full[steps & 1], (steps / 2) & 1);
+                    if (x == ut - 1) commit(&k_empty[it & 1]);
+                }
+                __syncwarp();
+            };
+            if (un) {
+                ok = wait(&k_full[us & 1], (us / 2) & 1);
                 fence_after();
-                for (int x = 0; x < tiles && ok; ++x) scores(x, steps);
-                if (ok) commit(&k_empty[steps & 1]);
-                for (int t = 0; t < n && ok; ++t) {
-                    const unsigned it = steps + t;
-                    for (int x = 0; x < tiles && ok; ++x) {
-                        if (x == 0) ok = wait(&v_full[it & 1], (it / 2) & 1);
-                        ok = ok && wait(&p_full[x], (x ? tile1_steps + t : it) & 1);
+                for (int x = 0; x < ut && ok; ++x) scores(x, us);
+            }
+            for (int t = 0; t < un && ok; ++t) {
+                const unsigned it = us + t;
+                const uint32_t v0 = v_lo + (it & 1) * BUFFER;
+                for (int x = 0; x < ut && ok; ++x) {
+                    if (x == 0) ok = wait(&v_full[it & 1], (it / 2) & 1);
+                    ok = ok && wait(&p_full[x], (x ? us1 + t : it) & 1);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t to = ud + O_COL + x * 128, w = ud + S_COL + x * 128;
+                    if (one) {
+                        if (t > 0)
+                            mma_ts<true>(to, w, v0, V_HI, IDESC_O);
+                        else
+                            mma_ts<false>(to, w, v0, V_HI, IDESC_O);
+#pragma unroll
+                        for (int k = 1; k < STEP / 16; ++k) mma_ts<true>(to, w + k * 8, v0 + k * 16, V_HI, IDESC_O);
+                        if (x == ut - 1) commit(&v_empty[it & 1]);
+                    }
+                    __syncwarp();
+                    if (t + 1 < un) {
+                        if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1);
                         if (!ok) break;
                         fence_after();
-#pragma unroll
-                        for (int k = 0; k < STEP / 16; ++k)
-                            mma_ts(tmem + O_COL + x * 128, tmem + S_COL + x * 128 + k * 8,
-                                   vd + (uint64_t)(((it & 1) * STEP * D * 2 + k * 256) >> 4), IDESC_O, t > 0 || k > 0);
-                        if (x == tiles - 1) commit(&v_empty[it & 1]);
-                        if (t + 1 < n) {
-                            if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1);
-                            if (!ok) break;
-                            fence_after();
-                            scores(x, it + 1);
-                            if (x == tiles - 1) commit(&k_empty[(it + 1) & 1]);
-                        }
+                        scores(x, it + 1);
                     }
                 }
+            }
+            ok = __all_sync(FULL, ok);
+            if (un && one) {
                 if (ok) {
                     commit(&o_full);
                 } else {  // products on their way end before tensor memory is freed
@@ -377,6 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     wait(&drain, 0);
                 }
             }
+            __syncwarp();
         } else if (warp < WARP_LOAD_K) {
             // ---------------- K or V of a step as operands, a record a warp
             const int kv = warp < WARP_K, rr = kv ? (warp - WARP_V) & 3 : warp - WARP_K, g = lane >> 2, c = lane & 3;
