@@ -58,14 +58,14 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     } else if ((units + c - 1) / c <= MAX_UNITS_UNCUT) {
         p.mode = c > 1 ? ATTN_CLUSTER : ATTN_WHOLE;
         p.cluster = (int)c;
-        if (c > 1) p.smem += p.block_rows * (D + 2) * 4;
+        if (c > 1) p.smem += p.block_rows * attn_part_floats(D) * 4;
     } else {
         p.mode = ATTN_CUT;
     }
     if (p.mode == ATTN_CUT) {
         p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
         p.meta_bytes = ((size_t)p.items * sizeof(AttnMeta) + 255) / 256 * 256;
-        p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * (D + 2) * 4;
+        p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * attn_part_floats(D) * 4;
     }
     return p;
 }
@@ -203,7 +203,9 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
         return QMM_ERR_CUDA;
     }
     if (p.mode == ATTN_CUT) {
-        cfg.gridDim = dim3((unsigned)p.items, (unsigned)std::min(p.block_rows, 16));
+        // a block a row while there are few, then several rows a block
+        const int64_t y = std::min<int64_t>(p.block_rows, std::max<int64_t>(16, 4096 / p.items));
+        cfg.gridDim = dim3((unsigned)p.items, (unsigned)y);
         cfg.blockDim = dim3(attn::JOIN_WARPS * 32);
         cfg.dynamicSmemBytes = 0;
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -65,7 +65,7 @@ struct AttnArgs {
     int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
     int mode;               // AttnMode
     int cluster;            // CTAs of a cluster (ATTN_CLUSTER)
-    float* part;            // [ctas][2][rows][D + 2]
+    float* part;            // [ctas][2][rows][attn_part_floats]
     AttnMeta* meta;         // [sequence][row block][head]
     int* err;
 };
@@ -82,6 +82,9 @@ inline int attn_ring_bytes(int D, int row_warps, int tile_rows) {
     return ring > rows ? ring : rows;
 }
 inline int attn_q_bytes(int D, int row_warps) { return row_warps * (D / QK) * 1024; }
+
+// Floats of a row's part: D values, the reference and the sum; 16-byte rows.
+__host__ __device__ constexpr int attn_part_floats(int D) { return D + 4; }
 
 // Rows of a warp's tile.
 __host__ __device__ constexpr int attn_tile_rows(int dtype) { return dtype == QMM_F32 ? 8 : 16; }
@@ -784,7 +787,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         if (a.mode == ATTN_CLUSTER)
             part = reinterpret_cast<float*>(smem + a.part_at);
         else if (!uncut)  // a share's first segment keeps its part in slot 0, its last in slot 1
-            part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * (D + 2);
+            part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * attn_part_floats(D);
         const auto write = [&](int row, const float* o) {
             const int global_row = block * block_rows + row, i = global_row / a.group;
             write_row<NB>(a, seq.q0 + i, at.head * a.group + global_row - i * a.group, o, lane);
@@ -807,15 +810,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 write(row, o);
             } else {
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) part[row * (D + 2) + kb * 32 + lane] = o[kb];
-                if (lane == 0) part[row * (D + 2) + D] = m, part[row * (D + 2) + D + 1] = sum;
+                for (int kb = 0; kb < NB; ++kb) part[row * attn_part_floats(D) + kb * 32 + lane] = o[kb];
+                if (lane == 0) part[row * attn_part_floats(D) + D] = m, part[row * attn_part_floats(D) + D + 1] = sum;
             }
         }
         if (a.mode == ATTN_CLUSTER) {
             // every CTA of the cluster joins some of the rows, from all parts in their order
             cluster_sync();
             for (int row = rank + warp * a.cluster; row < live_rows; row += ATTN_WARPS * a.cluster) {
-                const unsigned mine = smem_u32(part + row * (D + 2));
+                const unsigned mine = smem_u32(part + row * attn_part_floats(D));
                 float m = -INFINITY, sum = 0.f, o[NB] = {};
                 for (int x = 0; x < a.cluster; ++x) {
                     const unsigned p = in_cluster(mine, x);
@@ -869,9 +872,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
     const AttnMeta mt = a.meta[blockIdx.x];
     const int n = mt.last - mt.first + 1;
     if (n <= 1) return;
-    const int64_t step = (int64_t)block_rows * (D + 2);
+    const int64_t step = (int64_t)block_rows * attn_part_floats(D);
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        const float* base = a.part + (int64_t)mt.first * 2 * step + row * (D + 2);
+        const float* base = a.part + (int64_t)mt.first * 2 * step + row * attn_part_floats(D);
         float m = -INFINITY, sum = 0.f, o[NB] = {};
         for (int x0 = warp; x0 < n; x0 += JOIN_WARPS * JOIN_AT_ONCE) {
             float pm[JOIN_AT_ONCE], pl[JOIN_AT_ONCE], po[JOIN_AT_ONCE][NB];

@@ -265,14 +265,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
         float f = 1.f;
         if (SOFTMAX && tile < tiles) {
-            const int64_t at = (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs;
+            // the row's bits, all loads on their way before the first is used
+            const unsigned short* from = reinterpret_cast<const unsigned short*>(a.q.data) +
+                                         (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs;
+            uint4 raw[NB * 4];
+            if (a.q.wide) {
+#pragma unroll
+                for (int k = 0; k < NB * 4; ++k)
+                    raw[k] = live ? __ldg(reinterpret_cast<const uint4*>(from) + k) : make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NB * 4; ++k) {
+                    unsigned w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = live ? from[8 * k + 2 * e] | (unsigned)from[8 * k + 2 * e + 1] << 16 : 0;
+                    raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            const auto pair = [&](int e, float* x) {  // values e, e + 1 (e even)
+                const uint4& r = raw[e / 8];
+                unpack2(e % 8 == 0 ? r.x : e % 8 == 2 ? r.y : e % 8 == 4 ? r.z : r.w, QMM_BF16, x);
+            };
             float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < NB * 4; ++k) {
-                float x[8] = {};
-                if (live) loadn<8>(a.q.data, at + 8 * k, QMM_BF16, a.q.wide, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+            for (int e = 0; e < D; e += 2) {
+                float x[2];
+                pair(e, x);
+                top = fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1])));
             }
             // top * 2^up in [2^13, 2^14); a negative scale goes into q', a scale of 0 makes it 0
             const int up = top > 0.f ? 13 - min(max(ilogbf(top), -100), 100) : 0;
@@ -283,11 +303,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             for (int kb = 0; kb < NB; ++kb) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float x[4] = {}, y[4] = {};
-                    if (live) {
-                        loadn<4>(a.q.data, at + 32 * kb + 4 * c, QMM_BF16, a.q.wide, x);
-                        loadn<4>(a.q.data, at + 32 * kb + 16 + 4 * c, QMM_BF16, a.q.wide, y);
-                    }
+                    float x[4], y[4];
+                    pair(32 * kb + 4 * c, x);
+                    pair(32 * kb + 4 * c + 2, x + 2);
+                    pair(32 * kb + 16 + 4 * c, y);
+                    pair(32 * kb + 16 + 4 * c + 2, y + 2);
                     *reinterpret_cast<uint4*>(to + (kb * 4 + c) * 128) =
                         make_uint4(attn::pack_half(x[0] * mul, x[2] * mul), attn::pack_half(x[1] * mul, x[3] * mul),
                                    attn::pack_half(y[0] * mul, y[2] * mul), attn::pack_half(y[1] * mul, y[3] * mul));
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             fence_after();
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            float* part = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + row - first_row) * (D + 2);
+            float* part = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + row - first_row) * attn_part_floats(D);
             const int64_t at = (int64_t)(seq.q0 + qi) * a.out.ts + (int64_t)qh * a.out.hs;
             const int64_t yat = ((int64_t)(seq.q0 + qi) * ((int64_t)a.kv_heads * a.group) + qh) * NB;
 #pragma unroll
@@ -588,8 +608,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 for (int e = 0; e < 32; ++e) o[e] = uncut ? __uint_as_float(v[e]) * inv : __uint_as_float(v[e]);
                 if (live && !uncut) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        *reinterpret_cast<float2*>(part + kb * 32 + e) = make_float2(o[e], o[e + 1]);
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part + kb * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
                 if (live && uncut && a.out.data) {
 #pragma unroll
