@@ -67,6 +67,7 @@ struct Smem {
     static constexpr int PART = REC / 2;                 // a record's codes and scales of K, or of V
     static constexpr int RAW = V + 2 * STEP * D * 2;     // rings of [K_SLOTS] and [V_SLOTS] parts
     static constexpr int BYTES = RAW + (K_SLOTS + V_SLOTS) * PART;
+    static_assert(SOFTMAX_WARPS * 32 * (D + 4) * 4 <= RAW, "output rows in the operands' place");
 };
 
 // Shared-memory operand: the low word of its descriptor holds the address and
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     // records that are not there; of eight steps: a softmax reads the flags of a step while later ones are copied
     // (a copy is at most four steps ahead of the products of a step, which follow its softmax)
     __shared__ int s_gone[2][8][STEP_RECORDS];
+    __shared__ uint64_t q_full;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
 
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             mbar_init(&p_full[i], 4);
         }
         mbar_init(&o_full, 1);
+        mbar_init(&q_full, SOFTMAX_WARPS);
         mbar_init(&drain, 1);
         s_abort = 0;
         fence_mbar_init();
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     constexpr bool SOFTMAX = decltype(softmax_role)::value;
     unsigned steps = 0, segments = 0;  // before this segment: phases of the barriers
     unsigned tile1_steps = 0;          // of them, those of tile 1
+    unsigned walked = 0;               // segments, those without keys among them
     for (int u = u0; u < u1;) {
         const int b = a.blocks == 1 ? entry : entry / a.blocks, block = entry - b * a.blocks;
         const Seq seq = attn::sequence(a, b, !cut && tid == 0);
@@ -258,64 +262,80 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         const int rows = seq.n * a.group, first_row = block * BLOCK_ROWS;
         const int tiles = rows - first_row > 128 ? 2 : 1;
 
-        // ---- the softmax warps lay down their rows of Q
+        // ---- the softmax warps lay down their rows of Q, whole rows a load; the others start at once
         const int tile = warp >> 2;  // of a softmax warp
         const int row = first_row + (tile << 7) + (tid & 127);
         const bool live = SOFTMAX && row < rows;
         const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
-        float f = 1.f;
+        float f = 1.f;  // from the row's S to its scores
         if (SOFTMAX && tile < tiles) {
-            // the row's bits, all loads on their way before the first is used
-            const unsigned short* from = reinterpret_cast<const unsigned short*>(a.q.data) +
-                                         (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs;
-            uint4 raw[NB * 4];
-            if (a.q.wide) {
+            // the warp's rows as they are, in the operand's order of values, from loads of whole rows
+            constexpr int LANES = NB == 3 ? 32 : NB * 8, PER = 32 / LANES;  // lanes a row, rows a load
+            constexpr int BATCH = 32 / PER < 16 ? 32 / PER : 16;           // loads on their way together
+            const int sub = lane / LANES, e = 4 * (lane % LANES);
+            const int64_t my_row = live ? (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs : -1;
+            uint8_t* q_tile = smem + SM::Q + tile * (128 * D * 2) + (warp & 3) * (4 * D * 16);
+            uint8_t* to = q_tile + ((e >> 5) * 4 + (lane & 3)) * 128 + (lane & 4) * 2;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += BATCH * PER) {
+                uint2 bits[BATCH];
 #pragma unroll
-                for (int k = 0; k < NB * 4; ++k)
-                    raw[k] = live ? __ldg(reinterpret_cast<const uint4*>(from) + k) : make_uint4(0, 0, 0, 0);
-            } else {
+                for (int k = 0; k < BATCH; ++k) {
+                    const int64_t at = __shfl_sync(FULL, my_row, r0 + k * PER + sub);  // of the row
+                    const unsigned short* p = reinterpret_cast<const unsigned short*>(a.q.data) + at + e;
+                    bits[k] = make_uint2(0, 0);
+                    if (at >= 0 && e < D) {
+                        if (a.q.wide)
+                            bits[k] = __ldg(reinterpret_cast<const uint2*>(p));
+                        else
+                            bits[k] = make_uint2(p[0] | (unsigned)p[1] << 16, p[2] | (unsigned)p[3] << 16);
+                    }
+                }
 #pragma unroll
-                for (int k = 0; k < NB * 4; ++k) {
-                    unsigned w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = live ? from[8 * k + 2 * e] | (unsigned)from[8 * k + 2 * e + 1] << 16 : 0;
-                    raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int k = 0; k < BATCH; ++k) {
+                    const int r = r0 + k * PER + sub;
+                    if (e < D)
+                        *reinterpret_cast<uint2*>(to + (r >> 3) * (D * 16) + (r & 7) * 16) =
+                            make_uint2(__byte_perm(bits[k].x, bits[k].y, 0x5410), __byte_perm(bits[k].x, bits[k].y, 0x7632));
                 }
             }
-            const auto pair = [&](int e, float* x) {  // values e, e + 1 (e even)
-                const uint4& r = raw[e / 8];
-                unpack2(e % 8 == 0 ? r.x : e % 8 == 2 ? r.y : e % 8 == 4 ? r.z : r.w, QMM_BF16, x);
-            };
+            __syncwarp();
+            // this thread's row, times a power of two, as fp16 in its place
+            uint8_t* mine = q_tile + (lane >> 3) * (D * 16) + (lane & 7) * 16;
+            uint4 raw[NB * 4];
             float top = 0.f;
 #pragma unroll
-            for (int e = 0; e < D; e += 2) {
-                float x[2];
-                pair(e, x);
-                top = fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1])));
+            for (int k = 0; k < NB * 4; ++k) {
+                raw[k] = lds128(mine + k * 128);
+                const unsigned w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x[2];
+                    unpack2(w[i], QMM_BF16, x);
+                    top = fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1])));
+                }
             }
             // top * 2^up in [2^13, 2^14); a negative scale goes into q', a scale of 0 makes it 0
             const int up = top > 0.f ? 13 - min(max(ilogbf(top), -100), 100) : 0;
             const float mul = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
             f = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)-up);
-            uint8_t* to = smem + SM::Q + tile * (128 * D * 2) + ((tid & 127) >> 3) * (D * 16) + (tid & 7) * 16;
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
+            for (int k = 0; k < NB * 4; ++k) {
+                unsigned w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[4], y[4];
-                    pair(32 * kb + 4 * c, x);
-                    pair(32 * kb + 4 * c + 2, x + 2);
-                    pair(32 * kb + 16 + 4 * c, y);
-                    pair(32 * kb + 16 + 4 * c + 2, y + 2);
-                    *reinterpret_cast<uint4*>(to + (kb * 4 + c) * 128) =
-                        make_uint4(attn::pack_half(x[0] * mul, x[2] * mul), attn::pack_half(x[1] * mul, x[3] * mul),
-                                   attn::pack_half(y[0] * mul, y[2] * mul), attn::pack_half(y[1] * mul, y[3] * mul));
+                for (int i = 0; i < 4; ++i) {
+                    float x[2];
+                    unpack2(w[i], QMM_BF16, x);
+                    w[i] = attn::pack_half(x[0] * mul, x[1] * mul);
                 }
+                *reinterpret_cast<uint4*>(mine + k * 128) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+        } else if (SOFTMAX) {
+            if (lane == 0) mbar_arrive(&q_full);
         }
-        __syncthreads();
 
         bool ok = true;
         if constexpr (!SOFTMAX) {
@@ -386,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 __syncwarp();
             };
             if (un) {
-                ok = wait(&k_full[us & 1], (us / 2) & 1);
+                ok = wait(&q_full, walked & 1) && wait(&k_full[us & 1], (us / 2) & 1);
                 fence_after();
                 for (int x = 0; x < ut && ok; ++x) scores(x, us);
             }
@@ -590,11 +610,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float* part = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + row - first_row) * attn_part_floats(D);
-            const int64_t at = (int64_t)(seq.q0 + qi) * a.out.ts + (int64_t)qh * a.out.hs;
             const int64_t yat = ((int64_t)(seq.q0 + qi) * ((int64_t)a.kv_heads * a.group) + qh) * NB;
+            // rows by way of shared memory (the operands are read), so that a warp stores whole rows
+            constexpr int PITCH = D + 4;
+            float* buf = reinterpret_cast<float*>(smem) + warp * (32 * PITCH);
+            __syncwarp();
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                __syncwarp();
                 uint32_t(&v)[32] = r[kb & 1];
                 if (ok && n) {
                     ld32(o_at + 32 * kb, v);
@@ -603,32 +625,49 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
-                float o[32];
+                const float by = uncut ? inv : 1.f;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = uncut ? __uint_as_float(v[e]) * inv : __uint_as_float(v[e]);
-                if (live && !uncut) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(part + kb * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(buf + lane * PITCH + kb * 32 + e) =
+                        make_float4(__uint_as_float(v[e]) * by, __uint_as_float(v[e + 1]) * by,
+                                    __uint_as_float(v[e + 2]) * by, __uint_as_float(v[e + 3]) * by);
+            }
+            __syncwarp();
+            const int warp_row = first_row + warp * 32, there = min(32, rows - warp_row);  // rows of this warp
+            if (!uncut) {
+                float* to = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + warp * 32) * attn_part_floats(D);
+                for (int i = lane; i < there * (D / 4); i += 32) {
+                    const int rr = i / (D / 4), e = 4 * (i - rr * (D / 4));
+                    *reinterpret_cast<float4*>(to + rr * attn_part_floats(D) + e) =
+                        *reinterpret_cast<const float4*>(buf + rr * PITCH + e);
                 }
-                if (live && uncut && a.out.data) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) storen<8>(a.out.data, at + kb * 32 + e, QMM_BF16, a.out.wide, o + e);
+            } else if (a.out.data) {
+                for (int i = lane; i < there * (D / 8); i += 32) {
+                    const int rr = i / (D / 8), e = 8 * (i - rr * (D / 8));
+                    const int gi = (warp_row + rr) / a.group, gh = head * a.group + warp_row + rr - gi * a.group;
+                    float o[8];
+                    *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(buf + rr * PITCH + e);
+                    *reinterpret_cast<float4*>(o + 4) = *reinterpret_cast<const float4*>(buf + rr * PITCH + e + 4);
+                    storen<8>(a.out.data, (int64_t)(seq.q0 + gi) * a.out.ts + (int64_t)gh * a.out.hs + e, QMM_BF16,
+                              a.out.wide, o);
                 }
-                if (live && uncut && a.yq) {
+            }
+            if (uncut && a.yq && live) {
+                const float* o = buf + lane * PITCH;
+                for (int kb = 0; kb < NB; ++kb) {
                     float top = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(o[e]));
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(o[kb * 32 + e]));
                     const float d = __fdiv_rn(top, 127.0f);
-#pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float q = d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(o[e], d)), -127.f), 127.f) : 0.f;
+                        const float q =
+                            d > 0.f ? fminf(fmaxf(roundf(__fdiv_rn(o[kb * 32 + e], d)), -127.f), 127.f) : 0.f;
                         a.yq[(yat + kb) * 32 + e] = (int8_t)(int)q;
                     }
                     a.yd[yat + kb] = f32_to_f16_bits(d);
                 }
             }
             if (!uncut && live) part[D] = ref - LIFT, part[D + 1] = l;
+            fence_async();  // the buffers are operands again
         }
         if (!ok) {
             if (lane == 0) atomicOr(a.err, ERR_TIMEOUT);
@@ -646,6 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         steps += n;
         if (tiles == 2) tile1_steps += n;
         segments += n > 0;
+        ++walked;
         u += unit_end - unit;
         unit = 0;
         if (++head == a.kv_heads) head = 0, ++entry;
