@@ -269,34 +269,32 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
         float f = 1.f;  // from the row's S to its scores
         if (SOFTMAX && tile < tiles) {
-            // the warp's rows as they are, in the operand's order of values, from loads of whole rows
-            constexpr int LANES = NB == 3 ? 32 : NB * 8, PER = 32 / LANES;  // lanes a row, rows a load
-            constexpr int BATCH = 32 / PER < 16 ? 32 / PER : 16;           // loads on their way together
-            const int sub = lane / LANES, e = 4 * (lane % LANES);
+            // The warp's rows as they are, in the operand's order of values: a load takes 32 bytes of
+            // each of 8 rows, which its store spreads over all banks.
+            const int sub = lane >> 2, quarter = lane & 3;
             const int64_t my_row = live ? (int64_t)(seq.q0 + qi) * a.q.ts + (int64_t)qh * a.q.hs : -1;
             uint8_t* q_tile = smem + SM::Q + tile * (128 * D * 2) + (warp & 3) * (4 * D * 16);
-            uint8_t* to = q_tile + ((e >> 5) * 4 + (lane & 3)) * 128 + (lane & 4) * 2;
-#pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += BATCH * PER) {
-                uint2 bits[BATCH];
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(a.q.data) + 4 * quarter;
+#pragma unroll 2
+            for (int r8 = 0; r8 < 4; ++r8) {
+                const int64_t at = __shfl_sync(FULL, my_row, r8 * 8 + sub);
+                const unsigned short* p = q + max(at, (int64_t)0);  // without a row, the first one's
+                uint2 bits[2 * NB];
+                if (a.q.wide) {  // no branch between the loads: each would wait for the one before
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int64_t at = __shfl_sync(FULL, my_row, r0 + k * PER + sub);  // of the row
-                    const unsigned short* p = reinterpret_cast<const unsigned short*>(a.q.data) + at + e;
-                    bits[k] = make_uint2(0, 0);
-                    if (at >= 0 && e < D) {
-                        if (a.q.wide)
-                            bits[k] = __ldg(reinterpret_cast<const uint2*>(p));
-                        else
-                            bits[k] = make_uint2(p[0] | (unsigned)p[1] << 16, p[2] | (unsigned)p[3] << 16);
-                    }
+                    for (int i = 0; i < 2 * NB; ++i) bits[i] = __ldg(reinterpret_cast<const uint2*>(p + 16 * i));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; ++i)
+                        bits[i] = make_uint2(p[16 * i] | (unsigned)p[16 * i + 1] << 16,
+                                             p[16 * i + 2] | (unsigned)p[16 * i + 3] << 16);
                 }
+                uint8_t* to = q_tile + r8 * (D * 16) + quarter * 128 + sub * 16;
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int r = r0 + k * PER + sub;
-                    if (e < D)
-                        *reinterpret_cast<uint2*>(to + (r >> 3) * (D * 16) + (r & 7) * 16) =
-                            make_uint2(__byte_perm(bits[k].x, bits[k].y, 0x5410), __byte_perm(bits[k].x, bits[k].y, 0x7632));
+                for (int i = 0; i < 2 * NB; ++i) {
+                    if (at < 0) bits[i] = make_uint2(0, 0);
+                    *reinterpret_cast<uint2*>(to + (i >> 1) * 512 + (i & 1) * 8) =
+                        make_uint2(__byte_perm(bits[i].x, bits[i].y, 0x5410), __byte_perm(bits[i].x, bits[i].y, 0x7632));
                 }
             }
             __syncwarp();
