@@ -116,9 +116,16 @@ bool prepared(AttnKernel k, int kind, int NB, int most) {
     return d;
 }
 
-constexpr void (*JOIN[8])(AttnArgs, int) = {
-    attn::attn_join_kernel<1>, attn::attn_join_kernel<2>, attn::attn_join_kernel<3>, attn::attn_join_kernel<4>,
-    attn::attn_join_kernel<5>, attn::attn_join_kernel<6>, attn::attn_join_kernel<7>, attn::attn_join_kernel<8>};
+using JoinKernel = void (*)(AttnArgs, int);
+
+template <int TEAM>
+JoinKernel join_kernel(int NB) {
+    static constexpr JoinKernel kernels[8] = {
+        attn::attn_join_kernel<1, TEAM>, attn::attn_join_kernel<2, TEAM>, attn::attn_join_kernel<3, TEAM>,
+        attn::attn_join_kernel<4, TEAM>, attn::attn_join_kernel<5, TEAM>, attn::attn_join_kernel<6, TEAM>,
+        attn::attn_join_kernel<7, TEAM>, attn::attn_join_kernel<8, TEAM>};
+    return kernels[NB - 1];
+}
 
 }  // namespace
 }  // namespace qmm
@@ -203,8 +210,11 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
         return QMM_ERR_CUDA;
     }
     if (p.mode == ATTN_CUT) {
-        // a block a row while there are few, then several rows a block
-        const int64_t y = std::min<int64_t>(p.block_rows, std::max<int64_t>(16, 4096 / p.items));
+        // a block's eight warps share a row of many parts, or take a row each of few
+        const bool shared = p.ctas > 16 * p.items;
+        const int64_t at_once = shared ? 1 : attn::JOIN_WARPS;
+        const int64_t y = std::min<int64_t>((p.block_rows + at_once - 1) / at_once,
+                                            std::max<int64_t>(16, 4096 / p.items));
         cfg.gridDim = dim3((unsigned)p.items, (unsigned)y);
         cfg.blockDim = dim3(attn::JOIN_WARPS * 32);
         cfg.dynamicSmemBytes = 0;
@@ -212,7 +222,8 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, JOIN[NB - 1], a, p.block_rows) != cudaSuccess) {
+        const JoinKernel join = shared ? join_kernel<attn::JOIN_WARPS>(NB) : join_kernel<1>(NB);
+        if (cudaLaunchKernelEx(&cfg, join, a, p.block_rows) != cudaSuccess) {
             cudaGetLastError();
             return QMM_ERR_CUDA;
         }

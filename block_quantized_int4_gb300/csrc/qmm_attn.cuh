@@ -850,43 +850,46 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     }
 }
 
-// Joins the parts of an item that was cut over CTAs: block (item, y) takes
-// rows y, y + gridDim.y, ...; warp w of it the parts w, w + 8, ..., eight at a
-// time, all of whose loads are on their way at once.  What each part gets
-// depends on its place alone, so results do not change from call to call.
+// Joins the parts of an item that was cut over CTAs.  TEAM warps share a row:
+// warp w of them takes the parts w, w + TEAM, ..., eight at a time, all of
+// whose loads are on their way at once; block (item, y) takes rows from
+// y * (8 / TEAM).  What each part gets depends on its place alone, so results
+// do not change from call to call.
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_AT_ONCE = 8;
 
-template <int NB>
+template <int NB, int TEAM>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
     attn_join_kernel(const __grid_constant__ AttnArgs a, int block_rows) {
-    constexpr int D = NB * 32;
-    __shared__ float s_o[JOIN_WARPS][D], s_m[JOIN_WARPS], s_l[JOIN_WARPS];
+    constexpr int D = NB * 32, ROWS = JOIN_WARPS / TEAM;  // rows a block works on at once
+    __shared__ float s_o[JOIN_WARPS][TEAM > 1 ? D : 1], s_m[JOIN_WARPS], s_l[JOIN_WARPS];
     const int entry = blockIdx.x / a.kv_heads, head = blockIdx.x - entry * a.kv_heads;
     const int b = a.blocks == 1 ? entry : entry / a.blocks, block = entry - b * a.blocks;
     const Seq seq = sequence(a, b, false);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TEAM, member = warp - team * TEAM;
     const int rows = min(block_rows, seq.n * a.group - block * block_rows);
-    if ((int)blockIdx.y >= rows) return;
+    if ((int)blockIdx.y * ROWS >= rows) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnMeta mt = a.meta[blockIdx.x];
     const int n = mt.last - mt.first + 1;
     if (n <= 1) return;
     const int64_t step = (int64_t)block_rows * attn_part_floats(D);
-    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        const float* base = a.part + (int64_t)mt.first * 2 * step + row * attn_part_floats(D);
+    for (int row0 = blockIdx.y * ROWS; row0 < rows; row0 += gridDim.y * ROWS) {
+        const int row = row0 + team;
+        const bool live = row < rows;
+        const float* base = a.part + (int64_t)mt.first * 2 * step + (live ? row : row0) * attn_part_floats(D);
         float m = -INFINITY, sum = 0.f, o[NB] = {};
-        for (int x0 = warp; x0 < n; x0 += JOIN_WARPS * JOIN_AT_ONCE) {
+        for (int x0 = member; x0 < n; x0 += TEAM * JOIN_AT_ONCE) {
             float pm[JOIN_AT_ONCE], pl[JOIN_AT_ONCE], po[JOIN_AT_ONCE][NB];
 #pragma unroll
             for (int i = 0; i < JOIN_AT_ONCE; ++i) {
-                const int x = x0 + i * JOIN_WARPS;
+                const int x = x0 + i * TEAM;
                 const float* p = base + 2 * step * x + (x == 0 && mt.slot ? step : 0);
-                const bool live = x < n;
-                pm[i] = live ? p[D] : -INFINITY;
-                pl[i] = live ? p[D + 1] : 0.f;
+                const bool there = x < n;
+                pm[i] = there ? p[D] : -INFINITY;
+                pl[i] = there ? p[D + 1] : 0.f;
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) po[i][kb] = live ? p[kb * 32 + lane] : 0.f;
+                for (int kb = 0; kb < NB; ++kb) po[i][kb] = there ? p[kb * 32 + lane] : 0.f;
             }
             float now = m;
 #pragma unroll
@@ -904,29 +907,35 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
             }
             m = now;
         }
-        if (lane == 0) s_m[warp] = m, s_l[warp] = sum;
+        if constexpr (TEAM > 1) {
+            if (lane == 0) s_m[warp] = m, s_l[warp] = sum;
 #pragma unroll
-        for (int kb = 0; kb < NB; ++kb) s_o[warp][kb * 32 + lane] = o[kb];
-        __syncthreads();
-        if (warp == 0) {
-            float top = -INFINITY, total = 0.f, v[NB] = {};
+            for (int kb = 0; kb < NB; ++kb) s_o[warp][kb * 32 + lane] = o[kb];
+            __syncthreads();
+            if (member == 0) {
+                m = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, s_m[w]);
-            const float use = top == -INFINITY ? 0.f : top;
+                for (int w = 0; w < TEAM; ++w) m = fmaxf(m, s_m[warp + w]);
+                const float use = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int w = 0; w < JOIN_WARPS; ++w) {
-                const float by = exp2_fast(s_m[w] - use);
-                total = fmaf(by, s_l[w], total);
+                for (int kb = 0; kb < NB; ++kb) o[kb] = 0.f;
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) v[kb] = fmaf(by, s_o[w][kb * 32 + lane], v[kb]);
+                for (int w = 0; w < TEAM; ++w) {
+                    const float by = exp2_fast(s_m[warp + w] - use);
+                    sum = fmaf(by, s_l[warp + w], sum);
+#pragma unroll
+                    for (int kb = 0; kb < NB; ++kb) o[kb] = fmaf(by, s_o[warp + w][kb * 32 + lane], o[kb]);
+                }
             }
-            const float inv = total > 0.f ? 1.f / total : 0.f;
-#pragma unroll
-            for (int kb = 0; kb < NB; ++kb) v[kb] *= inv;
-            const int global_row = block * block_rows + row, i = global_row / a.group;
-            write_row<NB>(a, seq.q0 + i, head * a.group + global_row - i * a.group, v, lane);
+            __syncthreads();
         }
-        __syncthreads();
+        if (member == 0 && live) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) o[kb] *= inv;
+            const int global_row = block * block_rows + row, i = global_row / a.group;
+            write_row<NB>(a, seq.q0 + i, head * a.group + global_row - i * a.group, o, lane);
+        }
     }
 }
 

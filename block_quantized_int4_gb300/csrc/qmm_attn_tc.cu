@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         const bool live = SOFTMAX && row < rows;
         const int qi = live ? row / a.group : 0, qh = head * a.group + (live ? row - qi * a.group : 0);
         float f = 1.f;  // from the row's S to its scores
-        if (SOFTMAX && tile < tiles) {
+        if (SOFTMAX && tile < tiles && n) {  // without keys the rows' zeros are written in this place at once
             // The warp's rows as they are, in the operand's order of values: a load takes 32 bytes of
             // each of 8 rows, which its store spreads over all banks.
             const int sub = lane >> 2, quarter = lane & 3;

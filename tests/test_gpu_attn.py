@@ -194,6 +194,18 @@ def test_many_rows(D, lens, nqs, causal, window, Hq, Hkv, page):
     c.check(c.run())
 
 
+def test_many_rows_of_sequences_without_keys():
+    """Items with nothing to attend to between others: zeros, every time (such an item writes its rows with
+    no products between its warps)."""
+    qmm = lib()
+    for D in (32, 64, 128):
+        c = Case(qmm, [0, 3, 0, 300, 0], [130, 64, 128, 40, 64], 4, 2, D, 96, "bf16", seed=D, q_start=True)
+        first = c.run()
+        c.check(first)
+        for _ in range(20):
+            assert torch.equal(first, c.run())
+
+
 def test_many_rows_of_many_keys():
     """Few row blocks and long contexts: items are cut over the CTAs, a CTA holds parts of several."""
     qmm = lib()
