@@ -15,7 +15,7 @@ namespace {
 struct Plan {
     bool tc;  // the tensor-memory kernel (qmm_attn_tc.cu)
     int mode, row_warps, token_warps, block_rows, blocks;  // token_warps: records of a unit
-    int ctas, cluster;  // CTAs of a cut launch, of a cluster
+    int ctas, cluster, start;  // CTAs of a cut launch, of a cluster; counts before an item's units
     int64_t items;
     size_t meta_bytes, part_bytes;
     int ring_bytes, part_at, smem;
@@ -64,6 +64,7 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     }
     if (p.mode == ATTN_CUT) {
         p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
+        p.start = p.items * units <= slots ? 0 : ATTN_START;
         p.meta_bytes = ((size_t)p.items * sizeof(AttnMeta) + 255) / 256 * 256;
         p.part_bytes = (size_t)p.ctas * 2 * p.block_rows * attn_part_floats(D) * 4;
     }
@@ -154,7 +155,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     const Plan p = plan_of(*op, device ? sms : DEFAULT_SMS);
     const size_t need = p.meta_bytes + p.part_bytes;
     // shares are counted in 31 bits
-    if (p.items * ((op->max_kv + GROUP - 1) / GROUP + 1) >= int64_t(1) << 31) return QMM_ERR_SHAPE;
+    if (p.items * ((op->max_kv + GROUP - 1) / GROUP + 1 + ATTN_START) >= int64_t(1) << 31) return QMM_ERR_SHAPE;
     if (need && (!op->workspace || op->workspace_bytes < need || reinterpret_cast<uintptr_t>(op->workspace) % 16))
         return QMM_ERR_WORKSPACE;
     if (!device) return QMM_ERR_DEVICE;
@@ -184,6 +185,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.blocks = p.blocks;
     a.mode = p.mode;
     a.cluster = p.cluster;
+    a.start = p.start;
     a.part_at = p.part_at;
     a.meta = static_cast<AttnMeta*>(op->workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);

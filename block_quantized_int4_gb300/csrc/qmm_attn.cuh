@@ -33,6 +33,15 @@
 
 namespace qmm {
 
+// A cut launch counts an item as its units and `start` more for what starting
+// and ending it costs a CTA: ATTN_START, or 0 where every unit can have a CTA.
+// (Counted as units alone, 128 queries of a sequence of a few keys, beside one
+// of 2048, made CTAs that walked 14 items of one unit: 116 us instead of 44;
+// sixteen ragged sequences up to 32000 tokens 111 us instead of 74.)  These
+// counts come before the item's first unit: a share that ends among them
+// leaves the item to the next CTA.
+constexpr int ATTN_START = 4;
+
 constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
 constexpr int ATTN_STAGES = 2;  // a token group's records: one in use, one in flight
@@ -64,6 +73,7 @@ struct AttnArgs {
     int ring_bytes, part_at;  // shared memory: the rows of q, a cluster's part
     int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
     int mode;               // AttnMode
+    int start;              // counts before an item's units (ATTN_CUT)
     int cluster;            // CTAs of a cluster (ATTN_CLUSTER)
     float* part;            // [ctas][2][rows][attn_part_floats]
     AttnMeta* meta;         // [sequence][row block][head]
@@ -225,19 +235,20 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int blo
     return r;
 }
 
-// A CTA's share [u0, u1) of all units, ordered by (sequence, row block, head,
+// A CTA's share [u0, u1) of all counts, ordered by (sequence, row block, head,
 // unit), and where u0 lies.  entry: sequence * blocks + row block.
 template <int WARPS>
 struct Share {
     int warp_units[WARPS];
-    int entry, start, units;  // the entry of u0, units before it (all heads) and its own (one head)
+    int entry, start, units;  // the entry of u0, counts before it (all heads) and its own (one head)
 };
 
 __device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries, int block_rows, int token_warps,
                                            bool report) {
     if (e >= entries) return 0;
     const int b = a.blocks == 1 ? e : e / a.blocks;
-    return span_of(a, sequence(a, b, report), e - b * a.blocks, block_rows, token_warps).units;
+    const int units = span_of(a, sequence(a, b, report), e - b * a.blocks, block_rows, token_warps).units;
+    return units ? units + a.start : 0;
 }
 
 // Inclusive sum of v over the block's threads and the block's total.
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     fence_mbar_init();
 
     struct {
-        int entry, head, unit;
+        int entry, head, unit;  // unit: in a cut launch first a count, a.start before unit 0
     } at;
     int u0, u1, share = 0;
     const bool cut = a.mode == ATTN_CUT;
@@ -397,7 +408,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             ++at.entry, at.head = 0, at.unit = 0;
             continue;
         }
-        int unit_end = cut ? min(sp.units, at.unit + (u1 - u)) : sp.units;
+        int counts = 0;  // of the share that this segment takes
+        int unit_end = sp.units;
+        if (cut) {
+            counts = min(sp.units + a.start - at.unit, u1 - u);
+            unit_end = at.unit + counts - a.start;
+            if (unit_end <= 0) break;  // the share ends before the item's first unit
+            at.unit = max(at.unit - a.start, 0);
+        }
         if (a.mode == ATTN_CLUSTER) {
             at.unit = (int)((int64_t)sp.units * rank / a.cluster);
             unit_end = (int)((int64_t)sp.units * (rank + 1) / a.cluster);
@@ -839,12 +857,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         }
         if (!cut) return;
         if (tid == 0 && at.unit == 0) {
-            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
+            // the item's counts end where its last unit does
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + counts + sp.units - unit_end - 1) / share;
             a.meta[(int64_t)at.entry * a.kv_heads + at.head] = AttnMeta{first, last, u != u0, 0};
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // buf is used before the ring's next copies
         __syncthreads();
-        u += unit_end - at.unit;
+        u += counts;
         at.unit = 0;
         if (++at.head == a.kv_heads) at.head = 0, ++at.entry;
     }

@@ -255,7 +255,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             ++entry, head = 0, unit = 0;
             continue;
         }
-        const int unit_end = cut ? min(sp.units, unit + (u1 - u)) : sp.units;
+        int counts = 0, unit_end = sp.units;
+        if (cut) {  // `unit` is a count: a.start before unit 0
+            counts = min(sp.units + a.start - unit, u1 - u);
+            unit_end = unit + counts - a.start;
+            if (unit_end <= 0) break;  // the share ends before the item's first unit
+            unit = max(unit - a.start, 0);
+        }
         const int rec0 = sp.lo / GROUP + unit * STEP_RECORDS;
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * STEP_RECORDS);
         const int n = rec_end > rec0 ? (rec_end - rec0 + STEP_RECORDS - 1) / STEP_RECORDS : 0;
@@ -677,14 +683,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         if (s_abort) break;
         if (cut && tid == 0 && unit == 0) {
             const bool uncut = unit_end == sp.units;
-            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + sp.units - 1) / share;
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + counts + sp.units - unit_end - 1) / share;
             a.meta[(int64_t)entry * a.kv_heads + head] = AttnMeta{first, last, u != u0, 0};
         }
         steps += n;
         if (tiles == 2) tile1_steps += n;
         segments += n > 0;
         ++walked;
-        u += unit_end - unit;
+        u += counts;
         unit = 0;
         if (++head == a.kv_heads) head = 0, ++entry;
         if (!cut) break;
