@@ -14,7 +14,8 @@ namespace {
 
 struct Plan {
     bool tc;  // the tensor-memory kernel (qmm_attn_tc.cu)
-    int mode, row_warps, token_warps, block_rows, blocks;  // token_warps: records of a unit
+    int tiles;  // of 8 rows (the other kernel)
+    int mode, unit, block_rows, blocks;  // unit: its records
     int ctas, cluster, start;  // CTAs of a cut launch, of a cluster; counts before an item's units
     int64_t items;
     size_t meta_bytes, part_bytes;
@@ -30,19 +31,17 @@ constexpr int64_t TC_MIN_ROWS = 64;
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
     const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
-    const int tile = attn_tile_rows(op.q.dtype);
     const int64_t rows = (int64_t)op.max_q * group;
     p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB && rows >= TC_MIN_ROWS;
-    p.row_warps = rows <= tile ? 1 : rows <= 2 * tile ? 2 : 4;
-    p.token_warps = ATTN_WARPS / p.row_warps;
-    p.block_rows = p.row_warps * tile;
-    if (p.tc) p.token_warps = ATTN_TC_RECORDS, p.block_rows = ATTN_TC_ROWS;
+    p.tiles = rows <= 8 ? 1 : 2;
+    p.unit = p.tc ? ATTN_TC_RECORDS : ATTN_WARPS;
+    p.block_rows = p.tc ? ATTN_TC_ROWS : p.tiles * 8;
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);
     p.items = (int64_t)op.n_seqs * p.blocks * op.cache.n_heads;
-    p.ring_bytes = attn_ring_bytes(D, p.row_warps, tile);
-    p.part_at = p.smem = p.ring_bytes + attn_q_bytes(D, p.row_warps);
-    const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.token_warps - 1) / p.token_warps;
-    const int64_t slots = p.tc ? sms : (int64_t)sms * attn_ctas(NB);
+    p.ring_bytes = attn_ring_bytes(D, p.tiles);
+    p.part_at = p.smem = p.ring_bytes + attn_q_bytes(D, p.tiles, op.q.dtype);
+    const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.unit - 1) / p.unit;
+    const int64_t slots = p.tc ? sms : (int64_t)sms * attn_ctas(NB, p.tiles);
     if (p.tc) p.smem = std::max(attn_tc_smem(NB), 120 * 1024);  // one CTA an SM: each takes all of tensor memory
     // As many CTAs an item as find room at once, while none has much to do;
     // beyond that equal shares, whose parts cost a second launch.
@@ -62,6 +61,8 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     } else {
         p.mode = ATTN_CUT;
     }
+    // shares are counted in 31 bits; that many items fill the device whole, too
+    if (p.mode == ATTN_CUT && p.items * (units + 1 + ATTN_START) >= int64_t(1) << 31) p.mode = ATTN_WHOLE;
     if (p.mode == ATTN_CUT) {
         p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
         p.start = p.items * units <= slots ? 0 : ATTN_START;
@@ -97,14 +98,16 @@ qmm_status check(const qmm_attn_op& op, bool pointers) {
     return QMM_OK;
 }
 
-AttnKernel kernel_of(int dtype, int NB) {
-    return dtype == QMM_F32 ? attn_kernel_f32(NB) : dtype == QMM_F16 ? attn_kernel_f16(NB) : attn_kernel_bf16(NB);
+AttnKernel kernel_of(int dtype, int NB, int tiles) {
+    if (dtype == QMM_F32) return tiles == 1 ? attn_kernel_f32_1(NB) : attn_kernel_f32_2(NB);
+    if (dtype == QMM_F16) return tiles == 1 ? attn_kernel_f16_1(NB) : attn_kernel_f16_2(NB);
+    return tiles == 1 ? attn_kernel_bf16_1(NB) : attn_kernel_bf16_2(NB);
 }
 
 // Opts a kernel into `most` bytes of dynamic shared memory, once a device.
 bool prepared(AttnKernel k, int kind, int NB, int most) {
     static std::mutex mu;
-    static bool done[64][4][8];
+    static bool done[64][7][8];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
@@ -154,8 +157,6 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     const bool device = device_facts(&sms, &optin);
     const Plan p = plan_of(*op, device ? sms : DEFAULT_SMS);
     const size_t need = p.meta_bytes + p.part_bytes;
-    // shares are counted in 31 bits
-    if (p.items * ((op->max_kv + GROUP - 1) / GROUP + 1 + ATTN_START) >= int64_t(1) << 31) return QMM_ERR_SHAPE;
     if (need && (!op->workspace || op->workspace_bytes < need || reinterpret_cast<uintptr_t>(op->workspace) % 16))
         return QMM_ERR_WORKSPACE;
     if (!device) return QMM_ERR_DEVICE;
@@ -181,7 +182,6 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.window = std::min(op->window, 1 << 29);
     a.scale_log2 = op->scale * 1.4426950408889634f;
     a.ring_bytes = p.ring_bytes;
-    a.row_warps = p.row_warps;
     a.blocks = p.blocks;
     a.mode = p.mode;
     a.cluster = p.cluster;
@@ -191,8 +191,8 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
     a.err = device_error_word();
     const int NB = op->cache.head_dim / QK;
-    const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB);
-    if (!prepared(kernel, p.tc ? 3 : op->q.dtype, NB, p.tc ? p.smem : optin - 4096)) return QMM_ERR_CUDA;
+    const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB, p.tiles);
+    if (!prepared(kernel, p.tc ? 6 : 2 * op->q.dtype + p.tiles - 1, NB, p.tc ? p.smem : optin - 4096)) return QMM_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.mode == ATTN_CUT ? p.ctas : p.items * p.cluster));

@@ -12,16 +12,22 @@
 // operands as exact fp16 integers, a few bit operations from the stored words,
 // and their products with fp16 parts of q' and of the weights are exact.
 //
+// Work.  A warp takes records of 32 keys, for all rows of the CTA (8 or 16).
+// Codes are the A operand of m16n8k16 (16 keys, or 16 columns of v), rows the
+// B operand, 8 a tile: so what is unpacked serves all rows, and a sum takes
+// half the registers of the other order (16-bit rows: 72 -> 54 us for sixteen
+// ragged sequences up to 32000 tokens).  What bounds it is issue: unpacking
+// the codes, and the pairs of fp16 parts with fp32 rows.
+//
 // Precision.  fp32 activations: q' and the weights are two fp16 parts, hi +
-// lo, 22 bits; a tile of m16n8k16 holds the hi parts of eight rows in its
-// upper and the lo parts in its lower half, so both parts meet each code in
-// one instruction.  16-bit activations: one part (exact for q, but for bf16
-// values below 2^-24 of the row's largest; a half step of 2^-12 for a weight,
-// next to 2^-9 or 2^-12 of the output's own), and for k the nibbles stay
-// masked as they are, the fp16 subnormals u 2^-24, with -8 sum_e q'_e as the
-// accumulator's start: one operation a register less, but the tensor core
-// aligns its addends to the largest, and starting from that large a value
-// costs 5 bits (fp32 rows: 4e-6 of the output against 2e-7 from q = u - 8).
+// lo, 22 bits, each multiplied by the codes q = u - 8.  16-bit activations: q'
+// is one part (exact, but for bf16 values below 2^-24 of the row's largest),
+// and for k the nibbles stay masked as they are, the fp16 subnormals u 2^-24,
+// with -8 sum_e q'_e as the accumulator's start: one operation a register
+// less, but the tensor core aligns its addends to the largest, and starting
+// from that large a value costs 5 bits (fp32 rows: 4e-6 of the output against
+// 2e-7 from q = u - 8).  A weight times d_v is rounded to fp16 once (fp16
+// activations, 2^-12) or twice (bf16, next to the output's own 2^-9).
 // Sums are fp32 throughout.  Weights times d_v are scaled by the power of two
 // that brings the largest d_v so far to 2^13, so they keep their bits whatever
 // the magnitude of v.
@@ -44,7 +50,7 @@ constexpr int ATTN_START = 4;
 
 constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
-constexpr int ATTN_STAGES = 2;  // a token group's records: one in use, one in flight
+constexpr int ATTN_STAGES = 2;  // a warp's records: one in use, one in flight
 
 // How the items (a row block of a sequence and key/value head) meet the CTAs:
 // one CTA an item; a cluster of CTAs an item, joined through shared memory; or
@@ -71,35 +77,39 @@ struct AttnArgs {
     int n_seqs, max_q, max_kv, causal, window;
     float scale_log2;
     int ring_bytes, part_at;  // shared memory: the rows of q, a cluster's part
-    int row_warps, blocks;  // warps along the rows of a CTA, row blocks a sequence at most
-    int mode;               // AttnMode
-    int start;              // counts before an item's units (ATTN_CUT)
-    int cluster;            // CTAs of a cluster (ATTN_CLUSTER)
-    float* part;            // [ctas][2][rows][attn_part_floats]
-    AttnMeta* meta;         // [sequence][row block][head]
+    int blocks;      // row blocks a sequence at most
+    int mode;        // AttnMode
+    int start;       // counts before an item's units (ATTN_CUT)
+    int cluster;     // CTAs of a cluster (ATTN_CLUSTER)
+    float* part;     // [ctas][2][rows][attn_part_floats]
+    AttnMeta* meta;  // [sequence][row block][head]
     int* err;
 };
 
-// The kernel of head size 32 * NB for one type of activations.
+// The kernel of head size 32 * NB for one type of activations and one or two
+// tiles of 8 rows a warp.
 using AttnKernel = void (*)(AttnArgs);
-AttnKernel attn_kernel_f32(int NB);
-AttnKernel attn_kernel_f16(int NB);
-AttnKernel attn_kernel_bf16(int NB);
+AttnKernel attn_kernel_f32_1(int NB);
+AttnKernel attn_kernel_f32_2(int NB);
+AttnKernel attn_kernel_f16_1(int NB);
+AttnKernel attn_kernel_f16_2(int NB);
+AttnKernel attn_kernel_bf16_1(int NB);
+AttnKernel attn_kernel_bf16_2(int NB);
 
 // Shared memory: the ring, later the joined rows, and the rows of q.
-inline int attn_ring_bytes(int D, int row_warps, int tile_rows) {
-    const int ring = ATTN_WARPS / row_warps * ATTN_STAGES * record_bytes(D), rows = ATTN_WARPS * tile_rows * D * 4;
+constexpr int ATTN_PAD = 4;  // floats after a joined row: rows two apart use other banks
+inline int attn_ring_bytes(int D, int NT) {
+    const int ring = ATTN_WARPS * ATTN_STAGES * record_bytes(D);
+    const int rows = ATTN_WARPS * 8 * NT * (D + ATTN_PAD) * 4;
     return ring > rows ? ring : rows;
 }
-inline int attn_q_bytes(int D, int row_warps) { return row_warps * (D / QK) * 1024; }
+inline int attn_q_bytes(int D, int NT, int dtype) { return NT * (D / QK) * 512 * (dtype == QMM_F32 ? 2 : 1); }
 
 // Floats of a row's part: D values, the reference and the sum; 16-byte rows.
 __host__ __device__ constexpr int attn_part_floats(int D) { return D + 4; }
 
-// Rows of a warp's tile.
-__host__ __device__ constexpr int attn_tile_rows(int dtype) { return dtype == QMM_F32 ? 8 : 16; }
 // CTAs an SM by registers (launch bound).
-constexpr int attn_ctas(int NB) { return NB <= 2 ? 4 : NB <= 4 ? 3 : 2; }
+constexpr int attn_ctas(int NB, int NT) { return NT == 1 ? (NB <= 2 ? 4 : NB <= 4 ? 3 : 2) : NB <= 2 ? 3 : 2; }
 
 #ifdef __CUDACC__
 namespace attn {
@@ -110,10 +120,18 @@ __device__ __forceinline__ void mma_add(float* c, const unsigned* a, unsigned b0
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_from(float* c, const unsigned* a, unsigned b0, unsigned b1, float x, float y) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+__device__ __forceinline__ void mma_from(float* c, const unsigned* a, unsigned b0, unsigned b1, const float* x) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(x), "f"(y));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+}
+
+// An 8 x 8 tile of 16-bit values (lane (g, c): row g, columns 2c, 2c + 1), transposed.
+__device__ __forceinline__ unsigned transposed(unsigned x) {
+    unsigned y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // Two fp32 lanes in one instruction, each rounded as its scalar form.
@@ -214,12 +232,12 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool report) {
 }
 
 // Keys [lo, hi) that any row of a row block sees, and its units (steps of
-// one record a token group); a block with rows but no keys has one unit, in
+// one record a warp); a block with rows but no keys has one unit, in
 // which its zeros are written.
 struct Span {
     int lo, hi, units;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int block, int block_rows, int token_warps) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int block, int block_rows, int unit_records) {
     Span r = {0, 0, 0};
     const int r0 = block * block_rows, rows = s.n * a.group;  // below 2^28 (checked on the host)
     if (r0 >= rows) return r;
@@ -230,7 +248,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int blo
         r.lo = r.hi = 0;
         r.units = 1;
     } else {
-        r.units = ((r.hi + GROUP - 1) / GROUP - r.lo / GROUP + token_warps - 1) / token_warps;
+        r.units = ((r.hi + GROUP - 1) / GROUP - r.lo / GROUP + unit_records - 1) / unit_records;
     }
     return r;
 }
@@ -243,11 +261,11 @@ struct Share {
     int entry, start, units;  // the entry of u0, counts before it (all heads) and its own (one head)
 };
 
-__device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries, int block_rows, int token_warps,
+__device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries, int block_rows, int unit_records,
                                            bool report) {
     if (e >= entries) return 0;
     const int b = a.blocks == 1 ? e : e / a.blocks;
-    const int units = span_of(a, sequence(a, b, report), e - b * a.blocks, block_rows, token_warps).units;
+    const int units = span_of(a, sequence(a, b, report), e - b * a.blocks, block_rows, unit_records).units;
     return units ? units + a.start : 0;
 }
 
@@ -276,13 +294,13 @@ __device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
 // then the place of u0).  The units of all heads fit 31 bits (checked on the
 // host).
 template <int THREADS>
-__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int token_warps, Share<THREADS / 32>& sh,
+__device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int unit_records, Share<THREADS / 32>& sh,
                                            int& u0, int& u1, int& share) {
     const int tid = threadIdx.x, entries = a.n_seqs * a.blocks;
     const bool one = entries <= THREADS;
     int units = 0, mine = 0, total;
     for (int e = tid; e < entries; e += THREADS) {
-        units = entry_units(a, e, entries, block_rows, token_warps, blockIdx.x == 0);
+        units = entry_units(a, e, entries, block_rows, unit_records, blockIdx.x == 0);
         mine += units;
     }
     int incl = block_scan<THREADS / 32>(mine, sh.warp_units, total);
@@ -295,7 +313,7 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, in
     for (int base = 0; base < entries; base += THREADS) {
         if (!one) {
             __syncthreads();
-            units = entry_units(a, base + tid, entries, block_rows, token_warps, false);
+            units = entry_units(a, base + tid, entries, block_rows, unit_records, false);
             incl = block_scan<THREADS / 32>(units, sh.warp_units, total);
         }
         const int start = before + (incl - units) * a.kv_heads;
@@ -342,26 +360,25 @@ __device__ __forceinline__ int scale_exponent(int bits) {  // exponent bits of f
 
 constexpr int REF_SLACK = 5;
 
-template <int NB, int DTYPE>
-__global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const __grid_constant__ AttnArgs a) {
+template <int NB, int DTYPE, int NT>
+__global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
     constexpr bool SPLIT = DTYPE == QMM_F32;
-    constexpr int D = NB * 32, REC = record_bytes(D), ROWS = attn_tile_rows(DTYPE);
-    constexpr int RS = SPLIT ? 1 : 2;  // rows a lane keeps statistics of
+    constexpr int PARTS = SPLIT ? 2 : 1;  // fp16 parts of q and of the weights
+    constexpr int D = NB * 32, REC = record_bytes(D), ROWS = 8 * NT, PITCH = D + ATTN_PAD;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Share<ATTN_WARPS> sh;
-    __shared__ float s_m[ATTN_WARPS][16], s_l[ATTN_WARPS][16];
+    __shared__ float s_m[ATTN_WARPS][ROWS], s_l[ATTN_WARPS][ROWS];
     __shared__ uint64_t s_full[ATTN_WARPS][ATTN_STAGES];
     __shared__ int s_gone[ATTN_WARPS][ATTN_STAGES];  // the record's page does not exist
     __shared__ int s_abort;
-    __shared__ float s_seed[SPLIT ? 1 : ATTN_WARPS][NB][16];
+    __shared__ __align__(8) int s_lo[ROWS], s_hi[ROWS];  // of a row: keys it sees,
+    __shared__ __align__(8) float s_f[ROWS];             // from its sums to its scores,
+    __shared__ __align__(8) float s_seed[NB][ROWS];      // -8 sum q' of each block
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int RW = a.row_warps, TW = ATTN_WARPS / RW;
-    const int wr = warp / TW, wt = warp - wr * TW;
-    const int block_rows = RW * ROWS;
-    uint8_t* ring = smem + wt * (ATTN_STAGES * REC);
-    uint64_t* full = s_full[wt];
+    uint8_t* ring = smem + warp * (ATTN_STAGES * REC);
+    uint64_t* full = s_full[warp];
     unsigned magic;  // kept in a register (signed_codes)
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
 
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
     const bool cut = a.mode == ATTN_CUT;
     int rank = 0;  // in the cluster
     if (cut) {
-        find_share<ATTN_THREADS>(a, block_rows, TW, sh, u0, u1, share);  // synchronises the block
+        find_share<ATTN_THREADS>(a, ROWS, ATTN_WARPS, sh, u0, u1, share);  // synchronises the block
         // the join kernel's blocks may come in beside the last of this one's (they wait for its end)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 >= u1) return;
@@ -398,11 +415,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
         u1 = 1;
     }
 
-    unsigned done = 0;  // records of this token group so far: stage and phase of the ring
+    unsigned done = 0;  // records of this warp so far: stage and phase of the ring
     for (int u = u0; u < u1;) {
         const int b = a.blocks == 1 ? at.entry : at.entry / a.blocks, block = at.entry - b * a.blocks;
         const Seq seq = sequence(a, b, !cut && tid == 0);
-        const Span sp = span_of(a, seq, block, block_rows, TW);
+        const Span sp = span_of(a, seq, block, ROWS, ATTN_WARPS);
         if (sp.units == 0) {
             if (!cut) return;  // of a cluster, all
             ++at.entry, at.head = 0, at.unit = 0;
@@ -420,30 +437,30 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             at.unit = (int)((int64_t)sp.units * rank / a.cluster);
             unit_end = (int)((int64_t)sp.units * (rank + 1) / a.cluster);
         }
-        const int rec0 = sp.lo / GROUP + at.unit * TW + wt;
-        const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * TW);
-        const int n_mine = rec_end > rec0 ? (rec_end - rec0 + TW - 1) / TW : 0;
+        const int rec0 = sp.lo / GROUP + at.unit * ATTN_WARPS + warp;
+        const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * ATTN_WARPS);
+        const int n_mine = rec_end > rec0 ? (rec_end - rec0 + ATTN_WARPS - 1) / ATTN_WARPS : 0;
 
-        // ---- the ring: the first warp of a token group copies whole records; its
-        // lanes look up the next 32 records' places in the cache at once
+        // ---- the ring: a warp copies its records whole; its lanes look up the next
+        // 32 records' places in the cache at once
         const int* table = a.pages + (int64_t)b * a.pages_stride;
         int place = -1;  // of record k = base + lane, in records; -1: its page does not exist
         const auto look_up = [&](int base) {
             const int k = base + lane;
             if (k < n_mine) {
-                const int rec = rec0 + k * TW, pg = rec / a.page_groups, page = table[pg];
+                const int rec = rec0 + k * ATTN_WARPS, pg = rec / a.page_groups, page = table[pg];
                 const bool gone = page < 0 || page >= a.n_pages;
                 if (gone) atomicOr(a.err, ERR_BAD_INDEX);
                 place = gone ? -1 : (page * a.kv_heads + at.head) * a.page_groups + rec - pg * a.page_groups;
             }
         };
         const auto issue = [&](int k) {
-            if (wr == 0 && k < n_mine) {
+            if (k < n_mine) {
                 if (k % 32 == 0) look_up(k);
                 const int from = __shfl_sync(FULL, place, k % 32);
                 if (lane == 0) {
                     const unsigned stage = (done + k) % ATTN_STAGES;
-                    s_gone[wt][stage] = from < 0;
+                    s_gone[warp][stage] = from < 0;
                     if (from < 0) {
                         mbar_arrive(&full[stage]);
                     } else {
@@ -453,41 +470,32 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 }
             }
         };
-        const auto sync_group = [&]() {
-            if (RW == 1)
-                __syncwarp();
-            else
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(RW * 32) : "memory");
-        };
 #pragma unroll
         for (int k = 0; k < ATTN_STAGES - 1; ++k) issue(k);
 
-        // ---- the rows of this lane; q' as MMA operands, its blocks spread over the token warps
+        // ---- q' as MMA operands, laid down once for the CTA: lane (g, c) takes its
+        // places of rows g (+ 8), the warps take turns at the blocks
         const int rows = seq.n * a.group;
-        int lo[RS], hi[RS];
-        float f[RS], seed[RS][NB];
-        uint4* qa = reinterpret_cast<uint4*>(smem + a.ring_bytes) + wr * (NB * 64) + lane;  // [block][k step][lane]
-        constexpr int MINE = (NB + 3) / 4;  // blocks of a warp when there are four token warps
-        float x[RS][MINE][8];
+        uint4* qb = reinterpret_cast<uint4*>(smem + a.ring_bytes) + lane;
+        constexpr int MINE = (NB + ATTN_WARPS - 1) / ATTN_WARPS;
+        float x[NT][MINE][8];
         const auto each_block = [&](auto&& body) {
-            if (TW == 4) {
 #pragma unroll
-                for (int i = 0; i < MINE; ++i)
-                    if (4 * i + wt < NB) body(x[0][i], x[RS - 1][i], 4 * i + wt);
-            } else {
-                for (int kb = wt; kb < NB; kb += TW) body(x[0][0], x[RS - 1][0], kb);
-            }
+            for (int i = 0; i < MINE; ++i)
+                if (ATTN_WARPS * i + warp < NB) body(i, ATTN_WARPS * i + warp);
         };
-        int64_t at_q[RS];
-        bool live[RS];
+        int64_t at_q[NT];
+        bool live[NT];
 #pragma unroll
-        for (int r = 0; r < RS; ++r) {
-            const int row = block * block_rows + wr * ROWS + g + 8 * r;
+        for (int r = 0; r < NT; ++r) {
+            const int row = block * ROWS + g + 8 * r;
             live[r] = row < rows;
             const int i = live[r] ? row / a.group : 0, h = live[r] ? row - i * a.group : 0;
             const int p = seq.L - seq.n + i;
-            hi[r] = live[r] && a.causal ? min(seq.L, p + 1) : sp.hi;
-            lo[r] = live[r] && a.window ? p - a.window + 1 : sp.lo;
+            if (c == 0 && warp == 0) {
+                s_hi[g + 8 * r] = live[r] && a.causal ? min(seq.L, p + 1) : sp.hi;
+                s_lo[g + 8 * r] = live[r] && a.window ? p - a.window + 1 : sp.lo;
+            }
             at_q[r] = (int64_t)(seq.q0 + i) * a.q.ts + (int64_t)(at.head * a.group + h) * a.q.hs + 4 * c;
         }
         const auto load = [&](float* y, int r, int kb) {
@@ -502,92 +510,99 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 loadn<4>(a.q.data, at_q[r] + 32 * kb + 16, DTYPE, 0, y + 4);
             }
         };
-        float top[RS] = {};
-        each_block([&](float* x0, float* x1, int kb) {
-            load(x0, 0, kb);
-            if (!SPLIT) load(x1, RS - 1, kb);
+        float top[NT] = {};
+        each_block([&](int i, int kb) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top[0] = fmaxf(top[0], fabsf(x0[e]));
-                if (!SPLIT) top[RS - 1] = fmaxf(top[RS - 1], fabsf(x1[e]));
+            for (int r = 0; r < NT; ++r) {
+                load(x[r][i], r, kb);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top[r] = fmaxf(top[r], fabsf(x[r][i][e]));
             }
         });
 #pragma unroll
-        for (int r = 0; r < RS; ++r) {
+        for (int r = 0; r < NT; ++r) {
             top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
             top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2));
-            if (TW > 1 && c == 0) s_m[warp][g + 8 * r] = top[r];
+            if (c == 0) s_m[warp][g + 8 * r] = top[r];
         }
-        if (TW > 1) __syncthreads();
-        float mul[RS];
+        __syncthreads();
+        float mul[NT];
 #pragma unroll
-        for (int r = 0; r < RS; ++r) {
-            for (int t = 0; TW > 1 && t < TW; ++t) top[r] = fmaxf(top[r], s_m[wr * TW + t][g + 8 * r]);
+        for (int r = 0; r < NT; ++r) {
+#pragma unroll
+            for (int t = 0; t < ATTN_WARPS; ++t) top[r] = fmaxf(top[r], s_m[t][g + 8 * r]);
             // top * 2^up in [2^13, 2^14); a negative scale goes into q', a scale of 0 makes it 0
             const int up = top[r] > 0.f ? 13 - min(max(ilogbf(top[r]), -100), 100) : 0;
             mul[r] = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
             // a masked nibble as it is (16-bit types) is the subnormal u 2^-24
-            f[r] = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)((SPLIT ? 0 : 24) - up));
+            if (c == 0 && warp == 0)
+                s_f[g + 8 * r] =
+                    a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)((SPLIT ? 0 : 24) - up));
         }
-        each_block([&](float* x0, float* x1, int kb) {
-            if (TW != 4) {
-                load(x0, 0, kb);
-                if (!SPLIT) load(x1, RS - 1, kb);
-            }
-            float sum[RS] = {};
+        each_block([&](int i, int kb) {
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
+            for (int r = 0; r < NT; ++r) {
                 // order of the operand's k places: values 4c, 4c+2 | 4c+1, 4c+3 of each half of the block
-                unsigned h[2][2];  // [row][k places]
+                unsigned h[4], lo[4];
+                float sum = 0.f;
 #pragma unroll
-                for (int r = 0; r < RS; ++r) {
+                for (int st = 0; st < 2; ++st) {
                     const float by = st ? mul[r] * 0.0625f : mul[r];  // high nibbles weigh 16
-                    const float* y = (r ? x1 : x0) + 4 * st;
+                    const float* y = x[r][i] + 4 * st;
                     const float y0 = y[0] * by, y1 = y[1] * by, y2 = y[2] * by, y3 = y[3] * by;
-                    h[r][0] = pack_half(y0, y2);
-                    h[r][1] = pack_half(y1, y3);
-                    const float2 p0 = unpack_half(h[r][0]), p1 = unpack_half(h[r][1]);
+                    h[2 * st] = pack_half(y0, y2);
+                    h[2 * st + 1] = pack_half(y1, y3);
+                    const float2 p0 = unpack_half(h[2 * st]), p1 = unpack_half(h[2 * st + 1]);
                     if (SPLIT) {
-                        h[1][0] = pack_half(y0 - p0.x, y2 - p0.y);
-                        h[1][1] = pack_half(y1 - p1.x, y3 - p1.y);
+                        lo[2 * st] = pack_half(y0 - p0.x, y2 - p0.y);
+                        lo[2 * st + 1] = pack_half(y1 - p1.x, y3 - p1.y);
                     } else {
                         const float part = p0.x + p0.y + p1.x + p1.y;
-                        sum[r] += st ? 16.f * part : part;
+                        sum += st ? 16.f * part : part;
                     }
                 }
-                qa[(2 * kb + st) * 32] = make_uint4(h[0][0], h[1][0], h[0][1], h[1][1]);
-            }
-            if (!SPLIT) {
-#pragma unroll
-                for (int r = 0; r < RS; ++r) {
-                    sum[r] += __shfl_xor_sync(FULL, sum[r], 1);
-                    sum[r] += __shfl_xor_sync(FULL, sum[r], 2);
-                    if (c == 0) s_seed[wr][kb][g + 8 * r] = sum[r] * (-8.f * 5.9604644775390625e-8f);  // -8 2^-24
+                uint4* to = qb + (r * NB + kb) * (PARTS * 32);
+                to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                if (SPLIT) to[32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (!SPLIT) {
+                    sum += __shfl_xor_sync(FULL, sum, 1);
+                    sum += __shfl_xor_sync(FULL, sum, 2);
+                    if (c == 0) s_seed[kb][g + 8 * r] = sum * (-8.f * 5.9604644775390625e-8f);  // -8 2^-24
                 }
             }
         });
         __syncthreads();
-        if (!SPLIT) {
-#pragma unroll
-            for (int r = 0; r < RS; ++r)
-#pragma unroll
-                for (int kb = 0; kb < NB; ++kb) seed[r][kb] = s_seed[wr][kb][g + 8 * r];
-        }
 
-        float acc[NB][4][4] = {};  // [block][n tile][rows g: 2 columns, rows g + 8 (or lo parts): 2 columns]
-        // keys that every row of the warp sees
-        const int lo_all = __reduce_max_sync(FULL, max(lo[0], lo[RS - 1]));
-        const int hi_all = __reduce_min_sync(FULL, min(hi[0], hi[RS - 1]));
-        float ref[RS];             // reference of the weights, w = exp2(s - ref)
-        float2 l[RS];              // and their sums
-        int top_bits = -1;         // exponent bits of the largest scale of v so far
-        float vs = 1.f, ds = 1.f;  // acc holds the weighted v times vs (on the weights) * ds (on the scales)
-        float unscale = 1.f;       // 1 / (vs * ds)
+        // From here a lane's rows are 2c and 2c + 1 of each tile (x, y of a float2).
+        float2 f[NT], ref[NT], l[NT];  // ref: reference of the weights, w = exp2(s - ref); l: their sums
+        int2 lo[NT], hi[NT];
+        float seed[NT][NB][4];
+        int lo_all = 0, hi_all = 0x7FFFFFFF;  // keys that every row of the warp sees
 #pragma unroll
-        for (int r = 0; r < RS; ++r) ref[r] = -INFINITY, l[r] = make_float2(0.f, 0.f);
+        for (int r = 0; r < NT; ++r) {
+            f[r] = *reinterpret_cast<const float2*>(&s_f[8 * r + 2 * c]);
+            lo[r] = *reinterpret_cast<const int2*>(&s_lo[8 * r + 2 * c]);
+            hi[r] = *reinterpret_cast<const int2*>(&s_hi[8 * r + 2 * c]);
+            lo_all = max(lo_all, max(lo[r].x, lo[r].y));
+            hi_all = min(hi_all, min(hi[r].x, hi[r].y));
+            ref[r] = make_float2(-INFINITY, -INFINITY);
+            l[r] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                float2 v = make_float2(0.f, 0.f);
+                if (!SPLIT) v = *reinterpret_cast<const float2*>(&s_seed[kb][8 * r + 2 * c]);
+                seed[r][kb][0] = seed[r][kb][2] = v.x, seed[r][kb][1] = seed[r][kb][3] = v.y;
+            }
+        }
+        lo_all = __reduce_max_sync(FULL, lo_all);
+        hi_all = __reduce_min_sync(FULL, hi_all);
+        float acc[NT][NB][2][4] = {};  // [tile][block][16 columns of D][column g, rows 2c, 2c + 1; column g + 8]
+        int top_bits = -1;             // exponent bits of the largest scale of v so far
+        float vs = 1.f, ds = 1.f;      // acc holds the weighted v times vs (on the weights) * ds (on the scales)
+        float unscale = 1.f;           // 1 / (vs * ds)
 
         for (int k = 0; k < n_mine; ++k) {
-            sync_group();  // the record before is read
+            __syncwarp();  // the record before is read
             issue(k + ATTN_STAGES - 1);
             const unsigned stage = (done + k) % ATTN_STAGES;
             bool gone = false;
@@ -598,33 +613,49 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                 }
                 gone = true;
             }
-            gone |= s_gone[wt][stage] != 0;
+            gone |= s_gone[warp][stage] != 0;
             const uint8_t* rec = ring + stage * REC;
-            const int tok0 = (rec0 + k * TW) * GROUP;
+            const int tok0 = (rec0 + k * ATTN_WARPS) * GROUP;
 
-            // scores
-            float2 s[4][RS] = {};
+            // scores: keys 8j + g of the record
+            float2 s[NT][4] = {};
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 w4 = lds128(rec + kb * 512 + lane * 16);
-                const uint4 d4 = lds128(rec + NB * 1024 + kb * 64 + c * 16);
+                const uint4 d4 = lds128(rec + NB * 1024 + kb * 64 + (g >> 1) * 16);
                 const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
-                const uint4 q0 = qa[2 * kb * 32], q1 = qa[(2 * kb + 1) * 32];
-                const unsigned qa0[4] = {q0.x, q0.y, q0.z, q0.w}, qa1[4] = {q1.x, q1.y, q1.z, q1.w};
+                uint4 q[NT][PARTS];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float t[4];
-                    const unsigned w8 = w[j] >> 8;
-                    const float2 dk = unpack_half(d[j]);
-                    if constexpr (SPLIT) {
-                        mma_from(t, qa0, signed_codes<0>(w[j], magic), signed_codes<0>(w8, magic), 0.f, 0.f);
-                        mma_add(t, qa1, signed_codes<1>(w[j], magic), signed_codes<1>(w8, magic));
-                        s[j][0] = fma2(dk, add2(make_float2(t[0], t[1]), make_float2(t[2], t[3])), s[j][0]);
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int e = 0; e < PARTS; ++e) q[r][e] = qb[((r * NB + kb) * PARTS + e) * 32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // 16 keys: rows 16i + g and 16i + 8 + g of the operand
+                    const unsigned x = w[2 * i], y = w[2 * i + 1], x8 = x >> 8, y8 = y >> 8;
+                    unsigned a0[4], a1[4];
+                    if (SPLIT) {
+                        a0[0] = signed_codes<0>(x, magic), a0[1] = signed_codes<0>(y, magic);
+                        a0[2] = signed_codes<0>(x8, magic), a0[3] = signed_codes<0>(y8, magic);
+                        a1[0] = signed_codes<1>(x, magic), a1[1] = signed_codes<1>(y, magic);
+                        a1[2] = signed_codes<1>(x8, magic), a1[3] = signed_codes<1>(y8, magic);
                     } else {
-                        mma_from(t, qa0, w[j] & 0x000F000Fu, w8 & 0x000F000Fu, seed[0][kb], seed[RS - 1][kb]);
-                        mma_add(t, qa1, w[j] & 0x00F000F0u, w8 & 0x00F000F0u);
-                        s[j][0] = fma2(dk, make_float2(t[0], t[1]), s[j][0]);
-                        s[j][RS - 1] = fma2(dk, make_float2(t[2], t[3]), s[j][RS - 1]);
+                        a0[0] = x & 0x000F000Fu, a0[1] = y & 0x000F000Fu, a0[2] = x8 & 0x000F000Fu;
+                        a0[3] = y8 & 0x000F000Fu, a1[0] = x & 0x00F000F0u, a1[1] = y & 0x00F000F0u;
+                        a1[2] = x8 & 0x00F000F0u, a1[3] = y8 & 0x00F000F0u;
+                    }
+                    const float dx = unpack_half(g & 1 ? d[2 * i] >> 16 : d[2 * i]).x;
+                    const float dy = unpack_half(g & 1 ? d[2 * i + 1] >> 16 : d[2 * i + 1]).x;
+#pragma unroll
+                    for (int r = 0; r < NT; ++r) {
+                        float t[4];
+                        mma_from(t, a0, q[r][0].x, q[r][0].y, seed[r][kb]);
+                        mma_add(t, a1, q[r][0].z, q[r][0].w);
+                        if (SPLIT) {
+                            mma_add(t, a0, q[r][PARTS - 1].x, q[r][PARTS - 1].y);
+                            mma_add(t, a1, q[r][PARTS - 1].z, q[r][PARTS - 1].w);
+                        }
+                        s[r][2 * i] = fma2(make_float2(dx, dx), make_float2(t[0], t[1]), s[r][2 * i]);
+                        s[r][2 * i + 1] = fma2(make_float2(dy, dy), make_float2(t[2], t[3]), s[r][2 * i + 1]);
                     }
                 }
             }
@@ -635,17 +666,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int r = 0; r < RS; ++r) {
-                        const int key = tok0 + 8 * j + 2 * c;
-                        if (gone || key < lo[r] || key >= hi[r]) s[j][r].x = -INFINITY;
-                        if (gone || key + 1 < lo[r] || key + 1 >= hi[r]) s[j][r].y = -INFINITY;
+                    for (int r = 0; r < NT; ++r) {
+                        const int key = tok0 + 8 * j + g;
+                        if (gone || key < lo[r].x || key >= hi[r].x) s[r][j].x = -INFINITY;
+                        if (gone || key < lo[r].y || key >= hi[r].y) s[r][j].y = -INFINITY;
                     }
             }
 
             // Scales of v, and the power of two that they and the weights share.
             // Keys that no row of the block sees may hold anything: their
-            // scales become zeros (each warp of the token group writes the
-            // same ones).
+            // scales become zeros.
             uint8_t* vscale = ring + stage * REC + NB * 1088;
             if (masked) {
 #pragma unroll
@@ -666,15 +696,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
             // The reference follows the running maximum by steps of more than
             // 2^REF_SLACK, so acc is rarely rescaled; so with the scales of v.
             int exponent = (any | any >> 16) & 0x7C00;
-            float m[RS];
+            float2 m[NT];
             bool moved = exponent > top_bits;
 #pragma unroll
-            for (int r = 0; r < RS; ++r) {
-                m[r] = s[0][r].x;
+            for (int r = 0; r < NT; ++r) {
+                m[r] = s[r][0];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m[r] = fmaxf(m[r], fmaxf(s[j][r].x, s[j][r].y));
-                m[r] *= f[r];  // f > 0
-                moved |= m[r] > ref[r] + REF_SLACK;
+                for (int j = 1; j < 4; ++j) m[r].x = fmaxf(m[r].x, s[r][j].x), m[r].y = fmaxf(m[r].y, s[r][j].y);
+                m[r] = mul2(m[r], f[r]);  // f > 0
+                moved |= m[r].x > ref[r].x + REF_SLACK || m[r].y > ref[r].y + REF_SLACK;
             }
             if (__any_sync(FULL, moved)) {
                 exponent = __reduce_max_sync(FULL, exponent);
@@ -688,43 +718,50 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                     top_bits = exponent;
                 }
 #pragma unroll
-                for (int r = 0; r < RS; ++r) {
-                    m[r] = fmaxf(m[r], __shfl_xor_sync(FULL, m[r], 1));
-                    m[r] = fmaxf(m[r], __shfl_xor_sync(FULL, m[r], 2));
-                    const float now = fmaxf(ref[r], m[r]);
-                    const float alpha = now == -INFINITY ? 0.f : exp2_fast(ref[r] - now);
+                for (int r = 0; r < NT; ++r) {
+#pragma unroll
+                    for (int o = 4; o < 32; o *= 2) {
+                        m[r].x = fmaxf(m[r].x, __shfl_xor_sync(FULL, m[r].x, o));
+                        m[r].y = fmaxf(m[r].y, __shfl_xor_sync(FULL, m[r].y, o));
+                    }
+                    const float2 now = make_float2(fmaxf(ref[r].x, m[r].x), fmaxf(ref[r].y, m[r].y));
+                    float2 by = make_float2(now.x == -INFINITY ? 0.f : exp2_fast(ref[r].x - now.x),
+                                            now.y == -INFINITY ? 0.f : exp2_fast(ref[r].y - now.y));
                     ref[r] = now;
-                    l[r] = mul2(l[r], make_float2(alpha, alpha));
-                    const float by = alpha * ratio;
+                    l[r] = mul2(l[r], by);
+                    by = mul2(by, make_float2(ratio, ratio));
 #pragma unroll
                     for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {
-                            acc[kb][n][2 * r] *= by, acc[kb][n][2 * r + 1] *= by;
-                            if (SPLIT) acc[kb][n][2] *= by, acc[kb][n][3] *= by;
+                        for (int e = 0; e < 4; ++e) {
+                            float* v = acc[r][kb][e >> 1] + 2 * (e & 1);
+                            v[0] *= by.x, v[1] *= by.y;
                         }
                 }
             }
-            float use[RS];  // nothing seen yet: every weight is exp2(-inf - 0)
+            // weights, as fp16 pairs of keys 8j + 2c, 8j + 2c + 1 of row g: the operand of v's product
+            unsigned ph[NT][4], pl[NT][4];
 #pragma unroll
-            for (int r = 0; r < RS; ++r) use[r] = ref[r] == -INFINITY ? 0.f : ref[r];
-            unsigned ph[4][RS], pl[4];  // weights as fp16: hi parts (both rows), lo parts
+            for (int r = 0; r < NT; ++r) {
+                // nothing seen yet: every weight is exp2(-inf - 0)
+                const float2 use = make_float2(ref[r].x == -INFINITY ? 0.f : -ref[r].x,
+                                               ref[r].y == -INFINITY ? 0.f : -ref[r].y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < RS; ++r) {
-                    const float2 x = fma2(s[j][r], make_float2(f[r], f[r]), make_float2(-use[r], -use[r]));
-                    const float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = fma2(s[r][j], f[r], use);
+                    float2 w = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                     l[r] = add2(l[r], w);
-                    s[j][r] = mul2(w, make_float2(vs, vs));
-                    if (DTYPE != QMM_F16) ph[j][r] = pack_half(s[j][r].x, s[j][r].y);
-                    if (SPLIT) {
-                        const float2 h = unpack_half(ph[j][r]);
-                        pl[j] = pack_half(s[j][r].x - h.x, s[j][r].y - h.y);
+                    w = mul2(w, make_float2(vs, vs));
+                    const unsigned h = pack_half(w.x, w.y);
+                    ph[r][j] = transposed(h);
+                    if (DTYPE != QMM_BF16) {
+                        const float2 p = unpack_half(h);
+                        pl[r][j] = transposed(pack_half(w.x - p.x, w.y - p.y));
                     }
                 }
+            }
 
-            // weights times v
+            // weights times v: columns g + 16 e (and + 8) of the block, a row of the operand each
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 w4 = lds128(rec + NB * 512 + kb * 512 + lane * 16);
@@ -738,88 +775,96 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB)) attn_kernel(const
                         vd[j] = pack_half(d.x * ds, d.y * ds);
                     }
                 }
-                unsigned pa[2][4];  // A operands of the two k steps: rows 0..7, 8..15, two tokens each
+                unsigned b[NT][4], bl[NT][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    unsigned &up = pa[j >> 1][2 * (j & 1)], &dn = pa[j >> 1][2 * (j & 1) + 1];
-                    const __half2 d = as_half2(vd[j]);
-                    if constexpr (SPLIT) {
-                        // (hi + lo) d as two parts: the product, and its exact error plus lo d
-                        const __half2 h = as_half2(ph[j][0]), pr = __hmul2(h, d);
-                        up = as_bits(pr);
-                        dn = as_bits(__hfma2(as_half2(pl[j]), d, __hfma2(h, d, __hneg2(pr))));
-                    } else if constexpr (DTYPE == QMM_BF16) {
-                        // two roundings of 2^-12, next to the output's 2^-9
-                        up = as_bits(__hmul2(as_half2(ph[j][0]), d));
-                        dn = as_bits(__hmul2(as_half2(ph[j][RS - 1]), d));
-                    } else {
-                        const float2 df = __half22float2(d), x = mul2(s[j][0], df), y = mul2(s[j][RS - 1], df);
-                        up = pack_half(x.x, x.y);
-                        dn = pack_half(y.x, y.y);
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __half2 d = as_half2(vd[j]), h = as_half2(ph[r][j]);
+                        if constexpr (SPLIT) {
+                            // (hi + lo) d as two parts: the product, and its exact error plus lo d
+                            const __half2 pr = __hmul2(h, d);
+                            b[r][j] = as_bits(pr);
+                            bl[r][j] = as_bits(__hfma2(as_half2(pl[r][j]), d, __hfma2(h, d, __hneg2(pr))));
+                        } else if constexpr (DTYPE == QMM_F16) {
+                            b[r][j] = as_bits(__hfma2(h, d, __hmul2(as_half2(pl[r][j]), d)));  // one rounding of (hi + lo) d
+                        } else {
+                            b[r][j] = as_bits(__hmul2(h, d));  // two roundings of 2^-12, next to the output's 2^-9
+                        }
                     }
-                }
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const unsigned x = w[2 * st], y = w[2 * st + 1], x8 = x >> 8, y8 = y >> 8;
-                    mma_add(acc[kb][0], pa[st], signed_codes<0>(x, magic), signed_codes<0>(y, magic));
-                    mma_add(acc[kb][1], pa[st], signed_codes<1>(x, magic), signed_codes<1>(y, magic));
-                    mma_add(acc[kb][2], pa[st], signed_codes<0>(x8, magic), signed_codes<0>(y8, magic));
-                    mma_add(acc[kb][3], pa[st], signed_codes<1>(x8, magic), signed_codes<1>(y8, magic));
-                }
+                for (int st = 0; st < 2; ++st)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const unsigned x = w[2 * st] >> (8 * e), y = w[2 * st + 1] >> (8 * e);
+                        const unsigned v[4] = {signed_codes<0>(x, magic), signed_codes<1>(x, magic),
+                                               signed_codes<0>(y, magic), signed_codes<1>(y, magic)};
+#pragma unroll
+                        for (int r = 0; r < NT; ++r) {
+                            mma_add(acc[r][kb][e], v, b[r][2 * st], b[r][2 * st + 1]);
+                            if (SPLIT) mma_add(acc[r][kb][e], v, bl[r][2 * st], bl[r][2 * st + 1]);
+                        }
+                    }
             }
         }
         done += n_mine;
 
-        // ---- join the token groups: O, maximum and sum of every row
+        // ---- join the warps: O, reference and sum of every row
 #pragma unroll
-        for (int r = 0; r < RS; ++r) {
-            float sum = l[r].x + l[r].y;
-            sum += __shfl_xor_sync(FULL, sum, 1);
-            sum += __shfl_xor_sync(FULL, sum, 2);
-            if (c == 0) s_m[warp][g + 8 * r] = ref[r], s_l[warp][g + 8 * r] = sum;
+        for (int r = 0; r < NT; ++r) {
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) {
+                l[r].x += __shfl_xor_sync(FULL, l[r].x, o);
+                l[r].y += __shfl_xor_sync(FULL, l[r].y, o);
+            }
+            if (g == 0) {
+                s_m[warp][8 * r + 2 * c] = ref[r].x, s_m[warp][8 * r + 2 * c + 1] = ref[r].y;
+                s_l[warp][8 * r + 2 * c] = l[r].x, s_l[warp][8 * r + 2 * c + 1] = l[r].y;
+            }
         }
         __syncthreads();  // the ring is read
-        float* buf = reinterpret_cast<float*>(smem);  // [warp][ROWS][D]
+        float* buf = reinterpret_cast<float*>(smem);  // [warp][ROWS][PITCH]
 #pragma unroll
-        for (int r = 0; r < RS; ++r) {
-            float m = -INFINITY;
-            for (int t = 0; t < TW; ++t) m = fmaxf(m, s_m[wr * TW + t][g + 8 * r]);
-            const float w = ref[r] == -INFINITY ? 0.f : exp2_fast(ref[r] - m) * unscale;
-            float* o = buf + (warp * ROWS + g + 8 * r) * D;
+        for (int r = 0; r < NT; ++r)
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb)
+            for (int y = 0; y < 2; ++y) {
+                const int row = 8 * r + 2 * c + y;
+                const float mine = y ? ref[r].y : ref[r].x;
+                float m = -INFINITY;
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float wn = n & 1 ? w * 0.0625f : w;  // high nibbles weigh 16
-                    float2 v;
-                    if (SPLIT)
-                        v = make_float2((acc[kb][n][0] + acc[kb][n][2]) * wn, (acc[kb][n][1] + acc[kb][n][3]) * wn);
-                    else
-                        v = make_float2(acc[kb][n][2 * r] * wn, acc[kb][n][2 * r + 1] * wn);
-                    *reinterpret_cast<float2*>(o + kb * 32 + n * 8 + 2 * c) = v;
-                }
-        }
+                for (int t = 0; t < ATTN_WARPS; ++t) m = fmaxf(m, s_m[t][row]);
+                const float w = mine == -INFINITY ? 0.f : exp2_fast(mine - m) * unscale;
+                float* o = buf + (warp * ROWS + row) * PITCH + g;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        o[kb * 32 + e * 16] = acc[r][kb][e][y] * w;
+                        o[kb * 32 + e * 16 + 8] = acc[r][kb][e][2 + y] * (w * 0.0625f);  // high nibbles weigh 16
+                    }
+            }
         __syncthreads();
         const bool uncut = a.mode != ATTN_CLUSTER && at.unit == 0 && unit_end == sp.units;
         float* part = nullptr;
         if (a.mode == ATTN_CLUSTER)
             part = reinterpret_cast<float*>(smem + a.part_at);
         else if (!uncut)  // a share's first segment keeps its part in slot 0, its last in slot 1
-            part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * block_rows * attn_part_floats(D);
+            part = a.part + ((int64_t)blockIdx.x * 2 + (u != u0)) * ROWS * attn_part_floats(D);
         const auto write = [&](int row, const float* o) {
-            const int global_row = block * block_rows + row, i = global_row / a.group;
+            const int global_row = block * ROWS + row, i = global_row / a.group;
             write_row<NB>(a, seq.q0 + i, at.head * a.group + global_row - i * a.group, o, lane);
         };
-        const int live_rows = min(block_rows, rows - block * block_rows);
+        const int live_rows = min(ROWS, rows - block * ROWS);
         for (int row = warp; row < live_rows; row += ATTN_WARPS) {
-            const int rw = row / ROWS, rr = row - rw * ROWS;
             float m = -INFINITY, sum = 0.f, o[NB] = {};
-            for (int t = 0; t < TW; ++t) m = fmaxf(m, s_m[rw * TW + t][rr]);
-            for (int t = 0; t < TW; ++t) {
-                const float mt = s_m[rw * TW + t][rr];
-                sum += mt == -INFINITY ? 0.f : s_l[rw * TW + t][rr] * exp2_fast(mt - m);
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) o[kb] += buf[((rw * TW + t) * ROWS + rr) * D + kb * 32 + lane];
+            for (int t = 0; t < ATTN_WARPS; ++t) m = fmaxf(m, s_m[t][row]);
+#pragma unroll
+            for (int t = 0; t < ATTN_WARPS; ++t) {
+                const float mt = s_m[t][row];
+                sum += mt == -INFINITY ? 0.f : s_l[t][row] * exp2_fast(mt - m);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) o[kb] += buf[(t * ROWS + row) * PITCH + kb * 32 + lane];
             }
             if (uncut) {
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
