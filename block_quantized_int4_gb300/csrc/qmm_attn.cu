@@ -25,15 +25,34 @@ struct Plan {
 constexpr int DEFAULT_SMS = 152;
 constexpr int64_t MAX_CTAS = 1024;  // the join kernel's parts of an item
 constexpr int MAX_CLUSTER = 8;
+// Units of a CTA up to which items stay whole or on a cluster: cutting costs a
+// second launch.  (8192 keys, D = 128, fp32, one token, 8 units: cut 11.3 us,
+// on a cluster 14.6; 4 x 5 queries over 4001 keys, D = 64, 4 units: cut 13.1,
+// whole 12.3.)
 constexpr int64_t MAX_UNITS_UNCUT = 6;
+// The tensor-memory kernel takes bf16 calls with this many rows a key/value
+// head (its tile has 256; with half as many, 8 x 4 queries over 4096 keys, D =
+// 128, it takes 51 us, the other 32), and this many counts of the other
+// kernel for each of its CTAs, because it takes 17 us for the smallest call.
+// (8 key/value heads, D = 128.  16 queries over 8190 keys, 14 counts: 30 us,
+// the other 29; 64 queries of 2 sequences of 512, 13 counts: 27 and 22; of
+// 1024, 20 counts: 31 and 37; 509 over 8190, 451 counts: 161 and 630.)
 constexpr int64_t TC_MIN_ROWS = 64;
+constexpr int64_t TC_MIN_COUNTS = 15;
+
+bool many_rows(int64_t rows, int64_t sequence_heads, int64_t max_kv, int64_t slots) {
+    const int64_t units = (max_kv + GROUP * ATTN_WARPS - 1) / (GROUP * ATTN_WARPS);
+    return rows >= TC_MIN_ROWS &&
+           sequence_heads * ((rows + 15) / 16) * (units + ATTN_START) >= TC_MIN_COUNTS * slots;
+}
 
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
     const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
     const int64_t rows = (int64_t)op.max_q * group;
-    p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB && rows >= TC_MIN_ROWS;
     p.tiles = rows <= 8 ? 1 : 2;
+    p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB &&
+           many_rows(rows, (int64_t)op.n_seqs * op.cache.n_heads, op.max_kv, (int64_t)sms * attn_ctas(NB, p.tiles));
     p.unit = p.tc ? ATTN_TC_RECORDS : ATTN_WARPS;
     p.block_rows = p.tc ? ATTN_TC_ROWS : p.tiles * 8;
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);

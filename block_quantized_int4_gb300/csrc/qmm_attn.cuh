@@ -46,7 +46,7 @@ namespace qmm {
 // sixteen ragged sequences up to 32000 tokens 111 us instead of 74.)  These
 // counts come before the item's first unit: a share that ends among them
 // leaves the item to the next CTA.
-constexpr int ATTN_START = 4;
+constexpr int ATTN_START = 3;
 
 constexpr int ATTN_WARPS = 4;
 constexpr int ATTN_THREADS = ATTN_WARPS * 32;
@@ -793,18 +793,35 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                         }
                     }
 #pragma unroll
-                for (int st = 0; st < 2; ++st)
+                for (int e = 0; e < 2; ++e) {
+                    float t[NT][4] = {};
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int st = 0; st < 2; ++st) {
                         const unsigned x = w[2 * st] >> (8 * e), y = w[2 * st + 1] >> (8 * e);
                         const unsigned v[4] = {signed_codes<0>(x, magic), signed_codes<1>(x, magic),
                                                signed_codes<0>(y, magic), signed_codes<1>(y, magic)};
 #pragma unroll
                         for (int r = 0; r < NT; ++r) {
-                            mma_add(acc[r][kb][e], v, b[r][2 * st], b[r][2 * st + 1]);
-                            if (SPLIT) mma_add(acc[r][kb][e], v, bl[r][2 * st], bl[r][2 * st + 1]);
+                            if constexpr (SPLIT) {
+                                mma_add(t[r], v, bl[r][2 * st], bl[r][2 * st + 1]);
+                                mma_add(t[r], v, b[r][2 * st], b[r][2 * st + 1]);
+                            } else {
+                                mma_add(acc[r][kb][e], v, b[r][2 * st], b[r][2 * st + 1]);
+                            }
                         }
                     }
+                    if constexpr (SPLIT) {
+                        // The tensor core truncates its sums: 32 keys at a time, and
+                        // the sums of those rounded to nearest.
+#pragma unroll
+                        for (int r = 0; r < NT; ++r) {
+                            float* o = acc[r][kb][e];
+                            const float2 lo2 = add2(make_float2(o[0], o[1]), make_float2(t[r][0], t[r][1]));
+                            const float2 hi2 = add2(make_float2(o[2], o[3]), make_float2(t[r][2], t[r][3]));
+                            o[0] = lo2.x, o[1] = lo2.y, o[2] = hi2.x, o[3] = hi2.y;
+                        }
+                    }
+                }
             }
         }
         done += n_mine;

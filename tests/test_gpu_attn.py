@@ -242,6 +242,76 @@ def test_many_rows_strided_quantized_and_missing_pages():
     c.check(out, lambda b, L: np.ones(L, bool) if b else np.arange(L) // 32 != 3)
 
 
+MAY_GROW = 1 << 18  # a max_kv that calls for the kernel of many rows, whatever the lengths are
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128])
+@pytest.mark.parametrize("lens,nqs,causal,window,Hq,Hkv,page", [
+    ([200], [64], True, 0, 1, 1, 32),
+    ([300, 128], [64, 64], True, 0, 4, 1, 64),
+    ([150, 64, 5], [100, 64, 5], True, 0, 6, 2, 32),
+    ([3, 700, 0, 257], [130, 40, 64, 1], True, 0, 4, 2, 96),
+    ([700, 90], [70, 90], True, 100, 3, 1, 32),
+    ([700, 90], [70, 90], False, 33, 3, 1, 128),
+    ([130, 127], [80, 80], False, 0, 8, 8, 32),
+    ([1, 128, 129, 127], [64, 64, 64, 64], True, 0, 2, 1, 32),
+    ([2000, 40, 1500], [64] * 3, True, 0, 2, 1, 64),
+])
+def test_many_rows_that_may_see_many_keys(D, lens, nqs, causal, window, Hq, Hkv, page):
+    qmm = lib()
+    c = Case(qmm, lens, nqs, Hq, Hkv, D, page, "bf16", causal, window, seed=D + len(lens), q_start=True,
+             extra_kv=MAY_GROW // page)
+    c.check(c.run(max_kv=MAY_GROW))
+
+
+@pytest.mark.parametrize("D", [32, 64, 96, 128])
+def test_many_rows_of_many_items(D):
+    """Row blocks enough for every CTA, of few keys or none, whole."""
+    qmm = lib()
+    lens, nqs = [0, 3, 129, 300, 70], [130, 64, 128, 40, 70]
+    for causal, window in ((True, 0), (False, 0), (True, 50)):
+        c = Case(qmm, lens * 14, nqs * 14, 4, 2, D, 96, "bf16", causal, window, seed=D + window, q_start=True)
+        first = c.run()
+        c.check(first)
+        for _ in range(10):
+            assert torch.equal(first, c.run())
+
+
+def test_many_rows_without_keys_that_may_see_many():
+    qmm = lib()
+    for D in (32, 64, 128):
+        c = Case(qmm, [0, 3, 0, 300, 0], [130, 64, 128, 40, 64], 4, 2, D, 96, "bf16", seed=D, q_start=True,
+                 extra_kv=MAY_GROW // 96)
+        first = c.run(max_kv=MAY_GROW)
+        c.check(first)
+        for _ in range(20):
+            assert torch.equal(first, c.run(max_kv=MAY_GROW))
+
+
+def test_many_rows_may_grow_strided_quantized_and_missing_pages():
+    qmm = lib()
+    qmm.qmm_last_device_error()
+    c = Case(qmm, [400, 300], [70, 70], 4, 2, 64, 32, "bf16", strided=1, seed=23, extra_kv=MAY_GROW // 32)
+    base = torch.full((140, 9, 65), 7.0, dtype=c.dtype, device=DEV)
+    out = base[:, 2:6, 1:]
+    qmm.qmm_attn_q4_0(c.op(out, max_kv=MAY_GROW))
+    c.check(out)
+    base[:, 2:6, 1:] = 7.0
+    assert (base == 7.0).all()
+    yq = torch.full((140, 256), 99, dtype=torch.int8, device=DEV)
+    yd = torch.full((140, 8), 99, dtype=torch.int16, device=DEV)
+    plain = torch.empty(140, 4, 64, dtype=c.dtype, device=DEV)
+    qmm.qmm_attn_q4_0(c.op(plain, yq=yq, yd=yd, max_kv=MAY_GROW))
+    # bf16 of the fp32 output that was quantized: off by half a bf16 step and half a code (and fp16's step in d)
+    d = yd.view(torch.float16).double()[:, :, None].expand(-1, -1, 32).reshape(140, 256)
+    off = (yq.double() * d - plain.double().view(140, 256)).abs()
+    assert (off <= 0.5 * d + plain.double().view(140, 256).abs() * (2.0 ** -8 + 2.0 ** -10)).all()
+    c.pages[0, 3] = c.cache.n_pages
+    out = c.run(max_kv=MAY_GROW)
+    assert qmm.qmm_last_device_error() == 10
+    c.check(out, lambda b, L: np.ones(L, bool) if b else np.arange(L) // 32 != 3)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_long_context(dtype):
     qmm = lib()
