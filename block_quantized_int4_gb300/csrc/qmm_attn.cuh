@@ -261,6 +261,16 @@ struct Share {
     int entry, start, units;  // the entry of u0, counts before it (all heads) and its own (one head)
 };
 
+// Every CTA gets `share` counts, the first `more` CTAs one more: shares rounded
+// up left CTAs without any (131000 tokens, fp32: 46.2 us instead of 44.0).
+struct Cut {
+    int share, more;
+    __device__ int cta_of(int u) const {
+        const int wide = more * (share + 1);
+        return u < wide ? u / (share + 1) : more + (u - wide) / share;
+    }
+};
+
 __device__ __forceinline__ int entry_units(const AttnArgs& a, int e, int entries, int block_rows, int unit_records,
                                            bool report) {
     if (e >= entries) return 0;
@@ -295,7 +305,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_units, int& total) {
 // host).
 template <int THREADS>
 __device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, int unit_records, Share<THREADS / 32>& sh,
-                                           int& u0, int& u1, int& share) {
+                                           int& u0, int& u1, Cut& cut) {
     const int tid = threadIdx.x, entries = a.n_seqs * a.blocks;
     const bool one = entries <= THREADS;
     int units = 0, mine = 0, total;
@@ -305,9 +315,10 @@ __device__ __forceinline__ void find_share(const AttnArgs& a, int block_rows, in
     }
     int incl = block_scan<THREADS / 32>(mine, sh.warp_units, total);
     const int all = total * a.kv_heads;
-    share = max((int)(((unsigned)all + gridDim.x - 1) / gridDim.x), 1);
-    u0 = (int)min((int64_t)share * blockIdx.x, (int64_t)all);
-    u1 = (int)min((int64_t)u0 + share, (int64_t)all);
+    cut.share = all / (int)gridDim.x;
+    cut.more = all - cut.share * (int)gridDim.x;
+    u0 = (int)blockIdx.x * cut.share + min((int)blockIdx.x, cut.more);
+    u1 = u0 + cut.share + ((int)blockIdx.x < cut.more);
     if (u0 >= u1) return;
     int before = 0;
     for (int base = 0; base < entries; base += THREADS) {
@@ -389,11 +400,12 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
     struct {
         int entry, head, unit;  // unit: in a cut launch first a count, a.start before unit 0
     } at;
-    int u0, u1, share = 0;
+    int u0, u1;
+    Cut shares = {};
     const bool cut = a.mode == ATTN_CUT;
     int rank = 0;  // in the cluster
     if (cut) {
-        find_share<ATTN_THREADS>(a, ROWS, ATTN_WARPS, sh, u0, u1, share);  // synchronises the block
+        find_share<ATTN_THREADS>(a, ROWS, ATTN_WARPS, sh, u0, u1, shares);  // synchronises the block
         // the join kernel's blocks may come in beside the last of this one's (they wait for its end)
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 >= u1) return;
@@ -920,7 +932,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
         if (!cut) return;
         if (tid == 0 && at.unit == 0) {
             // the item's counts end where its last unit does
-            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + counts + sp.units - unit_end - 1) / share;
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : shares.cta_of(u + counts + sp.units - unit_end - 1);
             a.meta[(int64_t)at.entry * a.kv_heads + at.head] = AttnMeta{first, last, u != u0, 0};
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // buf is used before the ring's next copies

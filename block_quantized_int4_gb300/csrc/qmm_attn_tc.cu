@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
 
     const bool cut = a.mode == ATTN_CUT;
-    int entry, head, unit = 0, u0 = 0, u1 = 1, share = 0;
+    int entry, head, unit = 0, u0 = 0, u1 = 1;
+    attn::Cut shares = {};
     if (cut) {
-        attn::find_share<THREADS>(a, BLOCK_ROWS, STEP_RECORDS, sh, u0, u1, share);
+        attn::find_share<THREADS>(a, BLOCK_ROWS, STEP_RECORDS, sh, u0, u1, shares);
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 < u1) {
             entry = sh.entry;
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         if (s_abort) break;
         if (cut && tid == 0 && unit == 0) {
             const bool uncut = unit_end == sp.units;
-            const int first = (int)blockIdx.x, last = uncut ? first - 1 : (u + counts + sp.units - unit_end - 1) / share;
+            const int first = (int)blockIdx.x, last = uncut ? first - 1 : shares.cta_of(u + counts + sp.units - unit_end - 1);
             a.meta[(int64_t)entry * a.kv_heads + head] = AttnMeta{first, last, u != u0, 0};
         }
         steps += n;
