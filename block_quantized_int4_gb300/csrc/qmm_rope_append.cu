@@ -65,6 +65,11 @@ __device__ __forceinline__ Two mul(Two a, float b) {
     return fast_two_sum(p.h, __fmaf_rn(a.l, b, p.l));
 }
 
+__device__ __forceinline__ float sum_of(Two a, Two b) {  // rounded once
+    const Two s = two_sum(a.h, b.h);
+    return __fadd_rn(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+
 // 1 / sqrt(sum / D + eps): rsqrtf's 22 bits and one step of the series
 // (1 - e)^(-1/2) = 1 + e/2 + 3 e^2 / 8, e = 1 - m r^2 (about 2^-22).
 __device__ __forceinline__ Two rms_inverse(Two sum, int D, float eps) {
@@ -80,6 +85,20 @@ __device__ __forceinline__ Two rms_inverse(Two sum, int D, float eps) {
 // ---------------------------------------------------------------- the kernel
 enum { GROUP_Q = 0, GROUP_K = 1, GROUP_V = 2 };
 
+// Quotients of numbers below 2^31 by one divisor d (Granlund and Montgomery):
+// m = (2^(31 + s) + e) / d with 2^s >= d and 0 < e <= d, so n m / 2^(31 + s) is
+// above n / d by less than 1 / d.
+struct Divide {
+    unsigned m, d;
+    int shift;
+    __host__ __device__ unsigned operator()(unsigned n) const { return (unsigned)((unsigned long long)n * m >> shift); }
+};
+Divide divide_by(unsigned d) {  // d in [1, 2^31)
+    int s = 0;
+    while ((1u << s) < d) ++s;
+    return Divide{(unsigned)((1ull << (31 + s)) / d + 1), d, 31 + s};
+}
+
 struct HeadsArgs {
     Heads in[3];  // q, k, v
     Heads out;    // of q
@@ -90,8 +109,8 @@ struct HeadsArgs {
     const int64_t* slots;
     uint8_t* cache;
     int64_t n_slots, n_pos, warps;  // warps: T * (sum of groups), below 2^31
-    int D, lanes, n_rot, pairs, page_size;
-    int table_wide;
+    Divide per_token, page;  // by the groups of a token, by the page size
+    int D, lanes, lanes_log2, n_rot, pairs;
     float eps, inv_D;
     int* err;
 };
@@ -102,8 +121,9 @@ struct HeadsArgs {
 // pairs (PAIRS): A and B follow one another, pairs (A0, A1), (A2, A3), (B0, B1),
 // (B2, B3).  Halves: pairs (Aj, Bj), A in the lower and B in the upper half of
 // the rotated part; lanes past it hold what passes.  In the FAST kernels runs
-// are whole aligned vectors (n_rot % 8 == 0 for halves, and 16-byte heads);
-// else every value has its own place.
+// are whole aligned vectors, of the table and of the norm's weights too
+// (n_rot % 8 == 0), and a lane's pairs are all rotated or none; else every
+// value has its own place.
 template <bool PAIRS, bool FAST>
 struct Places {
     int s0, n_rot, a0, b0;
@@ -119,7 +139,7 @@ struct Places {
         return s >= n_rot ? s : (s >> 1) + (s & 1) * (n_rot >> 1);
     }
     // Whether pair j is rotated, and the values that it is made of.
-    __device__ bool rotated(int j) const { return s0 + 2 * j < n_rot; }
+    __device__ bool rotated(int j) const { return (FAST ? s0 : s0 + 2 * j) < n_rot; }
     static __device__ int first(int j) { return PAIRS ? 2 * j : j; }
     static __device__ int second(int j) { return PAIRS ? 2 * j + 1 : j + 4; }
 };
@@ -166,17 +186,19 @@ __device__ __forceinline__ void store_runs(char* head, int a0, int b0, const flo
 }
 
 // cos and sin of the lane's four pairs, where they are rotated.
+template <bool FAST>
 __device__ __forceinline__ void load_turns(const HeadsArgs& a, int p, int s0, float2* cs) {
-    const float2* row = a.table + (int64_t)p * (a.n_rot / 2);
-    if (a.table_wide && s0 + 8 <= a.n_rot) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(row + s0 / 2));
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + s0 / 2 + 2));
+    const float2* row = a.table + (int64_t)p * (a.n_rot / 2) + s0 / 2;
+    if (FAST) {
+        if (s0 >= a.n_rot) return;
+        const float4 u = __ldg(reinterpret_cast<const float4*>(row));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(row + 2));
         cs[0] = make_float2(u.x, u.y), cs[1] = make_float2(u.z, u.w);
         cs[2] = make_float2(v.x, v.y), cs[3] = make_float2(v.z, v.w);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (s0 + 2 * j < a.n_rot) cs[j] = __ldg(row + s0 / 2 + j);
+            if (s0 + 2 * j < a.n_rot) cs[j] = __ldg(row + j);
     }
 }
 
@@ -265,12 +287,12 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned id = blockIdx.x * HEAD_WARPS + warp;
     if (id >= (unsigned)a.warps) return;
-    const int per_token = a.groups[0] + a.groups[1] + a.groups[2];
-    const int t = (int)(id / (unsigned)per_token);
-    int i = (int)(id - (unsigned)t * per_token), kind = GROUP_Q;
-    while (i >= a.groups[kind]) i -= a.groups[kind++];
+    const int t = (int)a.per_token(id);
+    int i = (int)(id - (unsigned)t * a.per_token.d);
+    const int kind = i < a.groups[0] ? GROUP_Q : i < a.groups[0] + a.groups[1] ? GROUP_K : GROUP_V;
+    if (kind != GROUP_Q) i -= kind == GROUP_K ? a.groups[0] : a.groups[0] + a.groups[1];
     const Heads& in = a.in[kind];
-    const int sub = lane / a.lanes, u = lane - sub * a.lanes, per = 32 / a.lanes;
+    const int sub = lane >> a.lanes_log2, u = lane & (a.lanes - 1), per = 32 >> a.lanes_log2;
     const int s0 = u * 8;
     const bool inside = s0 < a.D;
     const Places<PAIRS, FAST> at(s0, kind == GROUP_V ? 0 : a.n_rot);
@@ -295,13 +317,20 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
             if (lane == 0) atomicOr(a.err, ERR_BAD_INDEX);
             return;
         }
-        if (kind != GROUP_V) load_turns(a, p, s0, cs);
+        if (kind != GROUP_V) load_turns<FAST>(a, p, s0, cs);
     }
     float gamma[8];
     const float* norm = kind == GROUP_V ? nullptr : a.norm[kind];
     if (norm && inside) {
+        if (FAST) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(norm + at.a0));
+            const float4 w = __ldg(reinterpret_cast<const float4*>(norm + at.b0));
+            gamma[0] = v.x, gamma[1] = v.y, gamma[2] = v.z, gamma[3] = v.w;
+            gamma[4] = w.x, gamma[5] = w.y, gamma[6] = w.z, gamma[7] = w.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) gamma[j] = __ldg(norm + at.element(j));
+            for (int j = 0; j < 8; ++j) gamma[j] = __ldg(norm + at.element(j));
+        }
     }
     float x[8];
     const auto values = [&](int k, bool live) {
@@ -378,19 +407,25 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int jp = at.first(j), jq = at.second(j);
-            Two p = {x[jp], 0.f}, q = {x[jq], 0.f};
+            float p1 = x[jp], q1 = x[jq];
             if (norm) {
-                p = mul(r, two_prod(p.h, gamma[jp]));
-                q = mul(r, two_prod(q.h, gamma[jq]));
-            }
-            if (at.rotated(j)) {
-                const Two pc = mul(p, cs[j].x), qs = mul(q, -cs[j].y), qc = mul(q, cs[j].x), ps = mul(p, cs[j].y);
-                p = add(pc, qs);
-                q = add(qc, ps);
+                Two p = mul(r, two_prod(p1, gamma[jp]));
+                Two q = mul(r, two_prod(q1, gamma[jq]));
+                if (at.rotated(j)) {
+                    const Two pc = mul(p, cs[j].x), qs = mul(q, -cs[j].y), qc = mul(q, cs[j].x), ps = mul(p, cs[j].y);
+                    p = add(pc, qs);
+                    q = add(qc, ps);
+                }
+                p1 = __fadd_rn(p.h, p.l);
+                q1 = __fadd_rn(q.h, q.l);
+            } else if (at.rotated(j)) {  // the products are pairs as they are
+                const float p = p1, q = q1;
+                p1 = sum_of(two_prod(p, cs[j].x), two_prod(q, -cs[j].y));
+                q1 = sum_of(two_prod(q, cs[j].x), two_prod(p, cs[j].y));
             }
             if (live) {
-                st[at.element(jp)] = __fadd_rn(p.h, p.l);
-                st[at.element(jq)] = __fadd_rn(q.h, q.l);
+                st[at.element(jp)] = p1;
+                st[at.element(jq)] = q1;
             }
         }
         __syncwarp();
@@ -399,10 +434,10 @@ __global__ void __launch_bounds__(HEAD_WARPS * 32) heads_kernel(const __grid_con
             for (int j = 0; j < 8; ++j) x[j] = st[s0 + j];
         }
     }
-    const int64_t page =
-        (unsigned long long)slot >> 32 ? slot / a.page_size : (int64_t)((unsigned)slot / (unsigned)a.page_size);
-    const int in_page = (int)(slot - page * a.page_size);
-    uint8_t* rec = a.cache + ((page * a.heads[kind] + head0) * (a.page_size / GROUP) + in_page / GROUP) *
+    const int page_size = (int)a.page.d;
+    const int64_t page = (unsigned long long)slot >> 31 ? slot / page_size : (int64_t)a.page((unsigned)slot);
+    const int in_page = (int)(slot - page * page_size);
+    uint8_t* rec = a.cache + ((page * a.heads[kind] + head0) * (page_size / GROUP) + in_page / GROUP) *
                                  (int64_t)record_bytes(a.D);
     quantize_store(a, kind, x, live, u >> 2, u & 3, rec, in_page & 31);
 }
@@ -491,7 +526,6 @@ int groups_of(int heads, int lanes) { return (heads + 32 / lanes - 1) / (32 / la
 
 void set_rope(HeadsArgs& a, const qmm_rope& r, const int32_t* pos) {
     a.table = reinterpret_cast<const float2*>(r.table);
-    a.table_wide = r.n_rot % 8 == 0 && !misaligned(r.table, 16);
     a.n_pos = r.n_pos;
     a.n_rot = r.n_rot;
     a.pairs = r.pairs != 0;
@@ -505,7 +539,9 @@ constexpr int MANY = 4;  // q's head groups a warp takes when there is plenty of
 int64_t set_groups(HeadsArgs& a, int64_t T, int u) {
     for (int g = 0; g < 3; ++g) a.groups[g] = groups_of(a.heads[g], a.lanes);
     a.groups[GROUP_Q] = (a.groups[GROUP_Q] + u - 1) / u;
-    return T * (a.groups[0] + a.groups[1] + a.groups[2]);
+    const int all = a.groups[0] + a.groups[1] + a.groups[2];
+    a.per_token = divide_by(all);
+    return T * all;
 }
 
 template <int DT, bool PAIRS>
@@ -519,7 +555,10 @@ void launch_form(const HeadsArgs& a, bool many, cudaStream_t st) {
 
 qmm_status launch_heads(HeadsArgs& a, int64_t T, int sms, void* stream) {
     int dt = -1;
-    bool fast = a.pairs || a.n_rot % 8 == 0;
+    bool fast = a.n_rot % 8 == 0 && !misaligned(a.table, 16) && !misaligned(a.norm[0], 16) && !misaligned(a.norm[1], 16);
+    a.lanes_log2 = 0;
+    while (1 << a.lanes_log2 < a.lanes) ++a.lanes_log2;
+    if (!a.page.d) a.page = divide_by(1);
     const Heads* all[4] = {&a.in[0], &a.in[1], &a.in[2], &a.out};
     for (const Heads* h : all) {
         if (!h->data) continue;
@@ -646,7 +685,7 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
     set_rope(a, op->rope, op->pos);
     a.slots = op->slots;
     a.cache = op->cache.data;
-    a.page_size = op->cache.page_size;
+    a.page = divide_by(op->cache.page_size);
     a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
     return launch_heads(a, op->T, sms, stream);
 }
