@@ -447,7 +447,8 @@ struct ReadArgs {
     const uint8_t* cache;
     const int64_t* slots;
     int64_t n_slots, warps;
-    int D, lanes, heads, page_size;
+    Divide per_token, page;  // by the warps of a token, by the page size
+    int D, lanes, lanes_log2, heads;
     int* err;
 };
 
@@ -456,10 +457,9 @@ __global__ void __launch_bounds__(READ_WARPS * 32) kv_read_kernel(const __grid_c
     const int lane = threadIdx.x & 31;
     const unsigned id = blockIdx.x * READ_WARPS + (threadIdx.x >> 5);
     if (id >= (unsigned)a.warps) return;
-    const int per = (a.heads + 32 / a.lanes - 1) / (32 / a.lanes);
-    const int t = (int)(id / (unsigned)per);
-    const int sub = lane / a.lanes, u = lane - sub * a.lanes;
-    const int head = (int)(id - (unsigned)t * per) * (32 / a.lanes) + sub, s0 = u * 8;
+    const int t = (int)a.per_token(id);
+    const int sub = lane >> a.lanes_log2, u = lane & (a.lanes - 1);
+    const int head = (int)(id - (unsigned)t * a.per_token.d) * (32 >> a.lanes_log2) + sub, s0 = u * 8;
     if (head >= a.heads || s0 >= a.D) return;
     const int64_t slot = a.slots[t];
     if (slot >= a.n_slots) {
@@ -469,10 +469,10 @@ __global__ void __launch_bounds__(READ_WARPS * 32) kv_read_kernel(const __grid_c
     float x[8] = {}, y[8] = {};
     if (slot >= 0) {
         const int NB = a.D / QK, blk = u >> 2, r = u & 3;
-        const int64_t page =
-            (unsigned long long)slot >> 32 ? slot / a.page_size : (int64_t)((unsigned)slot / (unsigned)a.page_size);
-        const int in_page = (int)(slot - page * a.page_size), tok = in_page & 31;
-        const uint8_t* base = a.cache + ((page * a.heads + head) * (a.page_size / GROUP) + in_page / GROUP) *
+        const int page_size = (int)a.page.d;
+        const int64_t page = (unsigned long long)slot >> 31 ? slot / page_size : (int64_t)a.page((unsigned)slot);
+        const int in_page = (int)(slot - page * page_size), tok = in_page & 31;
+        const uint8_t* base = a.cache + ((page * a.heads + head) * (page_size / GROUP) + in_page / GROUP) *
                                             (int64_t)record_bytes(a.D);
         if (a.out[0].data) {
             const float d = f16_bits_to_f32(
@@ -522,6 +522,12 @@ int lanes_of(int D) {
     return n;
 }
 
+int log2_of(int lanes) {
+    int n = 0;
+    while (1 << n < lanes) ++n;
+    return n;
+}
+
 int groups_of(int heads, int lanes) { return (heads + 32 / lanes - 1) / (32 / lanes); }
 
 void set_rope(HeadsArgs& a, const qmm_rope& r, const int32_t* pos) {
@@ -556,8 +562,7 @@ void launch_form(const HeadsArgs& a, bool many, cudaStream_t st) {
 qmm_status launch_heads(HeadsArgs& a, int64_t T, int sms, void* stream) {
     int dt = -1;
     bool fast = a.n_rot % 8 == 0 && !misaligned(a.table, 16) && !misaligned(a.norm[0], 16) && !misaligned(a.norm[1], 16);
-    a.lanes_log2 = 0;
-    while (1 << a.lanes_log2 < a.lanes) ++a.lanes_log2;
+    a.lanes_log2 = log2_of(a.lanes);
     if (!a.page.d) a.page = divide_by(1);
     const Heads* all[4] = {&a.in[0], &a.in[1], &a.in[2], &a.out};
     for (const Heads* h : all) {
@@ -710,9 +715,11 @@ qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream) {
     a.out[1] = kernel_heads(op->v);
     a.cache = op->cache.data;
     a.slots = op->slots;
-    a.page_size = op->cache.page_size;
+    a.page = divide_by(op->cache.page_size);
     a.n_slots = (int64_t)op->cache.n_pages * op->cache.page_size;
     a.err = err;
+    a.lanes_log2 = log2_of(a.lanes);
+    a.per_token = divide_by(groups_of(a.heads, a.lanes));
     a.warps = op->T * groups_of(a.heads, a.lanes);
     if (a.warps > MAX_WARPS) return QMM_ERR_SHAPE;
     kv_read_kernel<<<(unsigned)((a.warps + READ_WARPS - 1) / READ_WARPS), READ_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
