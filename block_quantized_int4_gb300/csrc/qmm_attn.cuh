@@ -15,9 +15,20 @@
 // Work.  A warp takes records of 32 keys, for all rows of the CTA (8 or 16).
 // Codes are the A operand of m16n8k16 (16 keys, or 16 columns of v), rows the
 // B operand, 8 a tile: so what is unpacked serves all rows, and a sum takes
-// half the registers of the other order (16-bit rows: 72 -> 54 us for sixteen
-// ragged sequences up to 32000 tokens).  What bounds it is issue: unpacking
-// the codes, and the pairs of fp16 parts with fp32 rows.
+// half the registers of the other order (74 us became 54 for sixteen ragged
+// bf16 sequences up to 32000 tokens).  All four warps of a CTA take the same
+// rows, and more rows more CTAs, for what a record costs again is small beside
+// waiting for the warps of other rows (4 x 5 queries over 4001 tokens: 14.4 us
+// with one row group of warps, 18 to 21 with two or four).
+//
+// What bounds it.  One token over 524000 tokens, 64 heads on 8 of 128: bf16 106
+// us, 5.7 TB/s, 85% of a copy; fp32 146 us, 4.1 TB/s.  Memory is not waited for
+// (two records a warp are enough): a 32-token tile of a record is about 520
+// warp instructions in bf16 and 700 in fp32, most of them unpacking (LOP3,
+// fp16 adds), 32 and 64 MMAs among them, and 12 warps an SM fill 55% of the
+// issue slots between the fixed latencies of their chains.  131000 tokens take
+// 34 and 44 us: 8 us of start, look-ups, q and the second launch's join are
+// not shared among more keys.
 //
 // Precision.  fp32 activations: q' and the weights are two fp16 parts, hi +
 // lo, 22 bits, each multiplied by the codes q = u - 8.  16-bit activations: q'
@@ -41,9 +52,9 @@ namespace qmm {
 
 // A cut launch counts an item as its units and `start` more for what starting
 // and ending it costs a CTA: ATTN_START, or 0 where every unit can have a CTA.
-// (Counted as units alone, 128 queries of a sequence of a few keys, beside one
-// of 2048, made CTAs that walked 14 items of one unit: 116 us instead of 44;
-// sixteen ragged sequences up to 32000 tokens 111 us instead of 74.)  These
+// (Counted as 1, 2 and 4: sixteen ragged bf16 sequences up to 32000 tokens 62,
+// 52 and 48 us, 128 fp32 queries over 2 sequences up to 2048 42, 32.6 and
+// 33.3; as 3, 48 and 32.9.)  These
 // counts come before the item's first unit: a share that ends among them
 // leaves the item to the next CTA.
 constexpr int ATTN_START = 3;
@@ -108,7 +119,10 @@ inline int attn_q_bytes(int D, int NT, int dtype) { return NT * (D / QK) * 512 *
 // Floats of a row's part: D values, the reference and the sum; 16-byte rows.
 __host__ __device__ constexpr int attn_part_floats(int D) { return D + 4; }
 
-// CTAs an SM by registers (launch bound).
+// CTAs an SM by registers (launch bound).  One row tile, D = 128, fp32 over
+// 131000 tokens: 48.3 us with 3, 50.7 with 4, which spills.  Two row tiles, 8 x
+// 8 fp16 queries of 64 heads of 128: 71.6 with 2, 86.6 with 3; 4 x 5 fp32 of
+// 32 heads of 64: 18.2 with 3, 21.3 with 4.
 constexpr int attn_ctas(int NB, int NT) { return NT == 1 ? (NB <= 2 ? 4 : NB <= 4 ? 3 : 2) : NB <= 2 ? 3 : 2; }
 
 #ifdef __CUDACC__
@@ -943,7 +957,12 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
     }
 }
 
-// Joins the parts of an item that was cut over CTAs.  TEAM warps share a row:
+// Joins the parts of an item that was cut over CTAs: with the reference m_i,
+// sum l_i and weighted sum o_i of part i, out = sum_i e_i o_i / sum_i e_i l_i,
+// e_i = exp2(m_i - max m).  A few kilobytes a row, so latency bounds it, 3 to 5
+// us behind the first kernel; hence all loads at once, and warps side by side
+// where a row has many parts (one warp adding up 57 parts in turn took 50 us).
+// TEAM warps share a row:
 // warp w of them takes the parts w, w + TEAM, ..., eight at a time, all of
 // whose loads are on their way at once; block (item, y) takes rows from
 // y * (8 / TEAM).  What each part gets depends on its place alone, so results

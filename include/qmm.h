@@ -14,6 +14,10 @@
  *    dot_b = sum_{i<32} q_w,i * q_x,i is an exact int32 (llama.cpp guide 2.2,
  *    y ~ Delta * Delta_x * sum q_i q_x,i), accumulated in fp32.
  *
+ * Beside the products stands what a decode step has between its QKV and its O
+ * product: rotary heads, a paged Q4_0 cache of keys and values, and attention
+ * over it (last section).
+ *
  * Conventions for every entry point:
  *  - Pointers are DEVICE pointers unless stated otherwise; the caller owns
  *    and allocates every buffer (the library allocates no device memory).
@@ -761,6 +765,8 @@ QMM_API qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream);
  * it sees, with k and v the cached values d * q; 0 where it sees none.
  * Scores, softmax statistics and sums are fp32; with fp32 q and out the
  * products carry 22 bits of q and of the weights, with a 16-bit type 11.
+ * (bf16 calls of many queries multiply k and v as fp16: values of the cache
+ * beyond 65504 in magnitude are outside their domain.)
  * out.data may be NULL when yq and yd are given: Q8_0 of the fp32 output
  * (int8 [T][q.n_heads * head_dim], uint16 [T][q.n_heads * head_dim / 32]; as
  * qmm_quantize_q8_0, the O product's operand).  out has q's n_heads and type.
