@@ -30,29 +30,34 @@ constexpr int MAX_CLUSTER = 8;
 // on a cluster 14.6; 4 x 5 queries over 4001 keys, D = 64, 4 units: cut 13.1,
 // whole 12.3.)
 constexpr int64_t MAX_UNITS_UNCUT = 6;
+// A call's counts (the units of all items, and ATTN_START an item) in row
+// blocks of 16, a CTA of the kernel for them: what there is to do.
+//
+// With this many, 16 rows of a CTA share what is unpacked; with fewer, blocks
+// of 8 make more CTAs and shorter ones.  (fp32, 4 key/value heads of 64, group
+// 8.  128 queries over 301 keys, 3 counts: 9.7 us in blocks of 16, 8.7 in
+// blocks of 8; 16 over 8000, 4.6: 19.6 and 18.8; 8 sequences of 8 over 4000,
+// 9.8: 20.8 and 22.4; 512 over 2048, 43: 78 and 93.)
+constexpr int64_t WIDE_MIN_COUNTS = 6;
 // The tensor-memory kernel takes bf16 calls with this many rows a key/value
 // head (its tile has 256; with half as many, 8 x 4 queries over 4096 keys, D =
-// 128, it takes 51 us, the other 32), and this many counts of the other
-// kernel for each of its CTAs, because it takes 17 us for the smallest call.
-// (8 key/value heads, D = 128.  16 queries over 8190 keys, 14 counts: 30 us,
-// the other 29; 64 queries of 2 sequences of 512, 13 counts: 27 and 22; of
-// 1024, 20 counts: 31 and 37; 509 over 8190, 451 counts: 161 and 630.)
+// 128, it takes 51 us, the other 32), and this many counts, because it takes
+// 17 us for the smallest call.  (8 key/value heads, D = 128.  16 queries over
+// 8190 keys, 14 counts: 30 us, the other 29; 64 queries of 2 sequences of 512,
+// 13 counts: 27 and 22; of 1024, 20 counts: 31 and 37; 509 over 8190, 451
+// counts: 161 and 630.)
 constexpr int64_t TC_MIN_ROWS = 64;
 constexpr int64_t TC_MIN_COUNTS = 15;
-
-bool many_rows(int64_t rows, int64_t sequence_heads, int64_t max_kv, int64_t slots) {
-    const int64_t units = (max_kv + GROUP * ATTN_WARPS - 1) / (GROUP * ATTN_WARPS);
-    return rows >= TC_MIN_ROWS &&
-           sequence_heads * ((rows + 15) / 16) * (units + ATTN_START) >= TC_MIN_COUNTS * slots;
-}
 
 Plan plan_of(const qmm_attn_op& op, int sms) {
     Plan p = {};
     const int D = op.cache.head_dim, NB = D / QK, group = op.q.n_heads / op.cache.n_heads;
     const int64_t rows = (int64_t)op.max_q * group;
-    p.tiles = rows <= 8 ? 1 : 2;
-    p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB &&
-           many_rows(rows, (int64_t)op.n_seqs * op.cache.n_heads, op.max_kv, (int64_t)sms * attn_ctas(NB, p.tiles));
+    const int64_t steps = (op.max_kv + GROUP * ATTN_WARPS - 1) / (GROUP * ATTN_WARPS);
+    const int64_t counts = (int64_t)op.n_seqs * op.cache.n_heads * ((rows + 15) / 16) * (steps + ATTN_START);
+    const int64_t ctas = (int64_t)sms * attn_ctas(NB, 2);
+    p.tiles = rows > 8 && counts >= WIDE_MIN_COUNTS * ctas ? 2 : 1;
+    p.tc = op.q.dtype == QMM_BF16 && NB <= ATTN_TC_MAX_NB && rows >= TC_MIN_ROWS && counts >= TC_MIN_COUNTS * ctas;
     p.unit = p.tc ? ATTN_TC_RECORDS : ATTN_WARPS;
     p.block_rows = p.tc ? ATTN_TC_ROWS : p.tiles * 8;
     p.blocks = (int)((rows + p.block_rows - 1) / p.block_rows);

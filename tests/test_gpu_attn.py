@@ -312,6 +312,44 @@ def test_many_rows_may_grow_strided_quantized_and_missing_pages():
     c.check(out, lambda b, L: np.ones(L, bool) if b else np.arange(L) // 32 != 3)
 
 
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("dtype,n,L,Hq,Hkv,page,window", [
+    ("f32", 5, 300, 8, 1, 64, 0), ("f16", 5, 300, 8, 1, 96, 40), ("bf16", 5, 300, 8, 1, 32, 0),
+    ("f32", 33, 200, 3, 1, 32, 50), ("f16", 17, 130, 4, 2, 64, 0),
+])
+def test_wide_blocks(D, dtype, n, L, Hq, Hkv, page, window):
+    """Calls that may see so many keys that 16 rows share a CTA."""
+    qmm = lib()
+    c = Case(qmm, [L, 0, L // 2, n, 1], [n, 1, n, n, 0], Hq, Hkv, D, page, dtype, True, window, seed=n + D,
+             q_start=True, extra_kv=4 * MAY_GROW // page)
+    c.check(c.run(max_kv=4 * MAY_GROW))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_wide_blocks_of_many_items(dtype, D):
+    """As many items as CTAs, of few keys or none, whole."""
+    qmm = lib()
+    lens, nqs = [0, 3, 129, 300, 70], [3, 2, 5, 9, 4]
+    for causal, window in ((True, 0), (False, 50)):
+        c = Case(qmm, lens * 40, nqs * 40, 12, 4, D, 96, dtype, causal, window, seed=D + window, q_start=True)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_wide_blocks_on_clusters(dtype):
+    """Half as many items as CTAs, and few enough keys that two CTAs share each."""
+    qmm = lib()
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(0, 1536, 57)]
+    lens[:4] = [1536, 1535, 0, 1]
+    c = Case(qmm, lens, [4] * 57, 16, 4, 64, 64, dtype, seed=31, q_start=True)
+    first = c.run()
+    c.check(first)
+    for _ in range(3):
+        assert torch.equal(first, c.run())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
 def test_long_context(dtype):
     qmm = lib()
