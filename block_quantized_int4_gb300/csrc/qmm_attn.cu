@@ -24,12 +24,19 @@ struct Plan {
 
 constexpr int DEFAULT_SMS = 152;
 constexpr int64_t MAX_CTAS = 1024;  // the join kernel's parts of an item
-constexpr int MAX_CLUSTER = 8;
-// Units of a CTA up to which items stay whole or on a cluster: cutting costs a
-// second launch.  (8192 keys, D = 128, fp32, one token, 8 units: cut 11.3 us,
-// on a cluster 14.6; 4 x 5 queries over 4001 keys, D = 64, 4 units: cut 13.1,
-// whole 12.3.)
-constexpr int64_t MAX_UNITS_UNCUT = 6;
+// The largest cluster (above 8 a kernel has to be opted in).  One token of 32
+// heads of 64 over 4096 keys, fp32: 8.9 us on clusters of 8, 7.7 of 16.
+constexpr int MAX_CLUSTER = 16;
+// Units of a CTA up to which items stay whole or on clusters of c CTAs: cutting
+// costs a second launch, and every CTA's share then spans several items where
+// there are many.  (64 heads on 8 of 128, us uncut and cut.  32 fp32 tokens over
+// 900, c = 1, 8 units: 16.9 and 20.5; ragged up to 1500, 12 units: 18.7 and
+// 17.4; 8 over 2000, c = 4, 4 units: 12.3 and 14.5; 4 over 5000, c = 8, 5 units:
+// 14.0 and 15.6; 8 ragged up to 3500, c = 4, 7 units: 16.3 and 15.3; 2 over
+// 8192, c = 16, 4 units: 15.0 and 13.2.)  Fewer where CTAs would stay idle
+// beside the largest clusters (one token over 6000, 3 units: 11.4 and 10.0).
+int64_t units_uncut(int64_t c, bool idle) { return idle ? 2 : c <= 2 ? 8 : c <= 8 ? 6 : 3; }
+
 // A call's counts (the units of all items, and ATTN_START an item) in row
 // blocks of 16, a CTA of the kernel for them: what there is to do.
 //
@@ -67,11 +74,11 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
     const int64_t units = ((op.max_kv + GROUP - 1) / GROUP + p.unit - 1) / p.unit;
     const int64_t slots = p.tc ? sms : (int64_t)sms * attn_ctas(NB, p.tiles);
     if (p.tc) p.smem = std::max(attn_tc_smem(NB), 120 * 1024);  // one CTA an SM: each takes all of tensor memory
-    // As many CTAs an item as find room at once, while none has much to do (one
-    // token over 2048 of 32 heads of 64, fp32: 9.9 us as cut shares, 8.5 on
-    // clusters of 8); beyond that equal shares, whose parts cost a second launch.
+    // As many CTAs an item as find room at once, up to one a unit, while none has
+    // much to do; beyond that equal shares, whose parts cost a second launch.
     int64_t c = 1;
-    while (2 * c <= MAX_CLUSTER && 2 * c <= units && 2 * c * p.items <= slots) c *= 2;
+    while (2 * c <= MAX_CLUSTER && c < units && 2 * c * p.items <= slots) c *= 2;
+    const bool idle = c < units && 2 * c * p.items <= slots;
     if (p.tc) {
         // Whole items where they fill the SMs' rounds to three quarters; else
         // equal shares, whose parts cost a second launch.
@@ -79,7 +86,7 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
         c = 1;
         p.mode = units <= 2 || 4 * p.items >= 3 * rounds * slots ? ATTN_WHOLE : ATTN_CUT;
         p.cluster = 1;
-    } else if ((units + c - 1) / c <= MAX_UNITS_UNCUT) {
+    } else if ((units + c - 1) / c <= units_uncut(c, idle)) {
         p.mode = c > 1 ? ATTN_CLUSTER : ATTN_WHOLE;
         p.cluster = (int)c;
         if (c > 1) p.smem += p.block_rows * attn_part_floats(D) * 4;
@@ -129,7 +136,8 @@ AttnKernel kernel_of(int dtype, int NB, int tiles) {
     return tiles == 1 ? attn_kernel_bf16_1(NB) : attn_kernel_bf16_2(NB);
 }
 
-// Opts a kernel into `most` bytes of dynamic shared memory, once a device.
+// Opts a kernel into `most` bytes of dynamic shared memory and clusters of 16,
+// once a device.
 bool prepared(AttnKernel k, int kind, int NB, int most) {
     static std::mutex mu;
     static bool done[64][7][8];
@@ -139,6 +147,7 @@ bool prepared(AttnKernel k, int kind, int NB, int most) {
     bool& d = done[dev][kind][NB - 1];
     if (!d)
         d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess &&
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
             cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
                 cudaSuccess;
     if (!d) cudaGetLastError();

@@ -325,6 +325,21 @@ def test_wide_blocks(D, dtype, n, L, Hq, Hkv, page, window):
     c.check(c.run(max_kv=4 * MAY_GROW))
 
 
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("dtype,lens,n,window", [
+    ("f32", [4096], 1, 0), ("bf16", [4090, 1, 0, 129], 1, 0), ("f16", [1200, 1300], 1, 1000), ("f32", [2000], 9, 0),
+    ("f32", [257], 1, 0), ("bf16", [130], 3, 0),
+])
+def test_clusters(D, dtype, lens, n, window):
+    """Few items of few keys: a cluster of up to 16 CTAs an item, some of them with nothing to do."""
+    qmm = lib()
+    c = Case(qmm, lens, [n] * len(lens), 8, 1, D, 64, dtype, True, window, seed=D + n)
+    first = c.run()
+    c.check(first)
+    for _ in range(3):
+        assert torch.equal(first, c.run())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("D", [64, 128])
 def test_wide_blocks_of_many_items(dtype, D):
