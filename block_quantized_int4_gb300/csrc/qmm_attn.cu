@@ -43,9 +43,10 @@ int64_t units_uncut(int64_t c, bool idle) { return idle ? 2 : c <= 2 ? 8 : c <= 
 // With this many, 16 rows of a CTA share what is unpacked; with fewer, blocks
 // of 8 make more CTAs and shorter ones.  (fp32, 4 key/value heads of 64, group
 // 8.  128 queries over 301 keys, 3 counts: 9.7 us in blocks of 16, 8.7 in
-// blocks of 8; 16 over 8000, 4.6: 19.6 and 18.8; 8 sequences of 8 over 4000,
-// 9.8: 20.8 and 22.4; 512 over 2048, 43: 78 and 93.)
-constexpr int64_t WIDE_MIN_COUNTS = 6;
+// blocks of 8; 16 over 8000, 4.6: 19.6 and 18.8; 32 sequences of 2 over 4000,
+// 2 heads of 256, 7.4: 30.8 and 27.8; 8 of 8 over 4000, 9.8: 20.8 and 22.4; 512
+// over 2048, 43: 78 and 93.)
+constexpr int64_t WIDE_MIN_COUNTS = 8;
 // The tensor-memory kernel takes bf16 calls with this many rows a key/value
 // head (its tile has 256; with half as many, 8 x 4 queries over 4096 keys, D =
 // 128, it takes 51 us, the other 32), and this many counts, because it takes

@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
     }
 
     unsigned done = 0;  // records of this warp so far: stage and phase of the ring
+    bool stopped = false;  // a wait ran out: no more copies, what follows is not used
     for (int u = u0; u < u1;) {
         const int b = a.blocks == 1 ? at.entry : at.entry / a.blocks, block = at.entry - b * a.blocks;
         const Seq seq = sequence(a, b, !cut && tid == 0);
@@ -480,8 +481,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                 place = gone ? -1 : (page * a.kv_heads + at.head) * a.page_groups + rec - pg * a.page_groups;
             }
         };
+        int n_copy = stopped ? 0 : n_mine;
         const auto issue = [&](int k) {
-            if (k < n_mine) {
+            if (k < n_copy) {
                 if (k % 32 == 0) look_up(k);
                 const int from = __shfl_sync(FULL, place, k % 32);
                 if (lane == 0) {
@@ -637,7 +639,13 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                     s_abort = 1;
                     atomicOr(a.err, ERR_TIMEOUT);
                 }
-                gone = true;
+                if (n_copy) {  // the copies on their way end before the CTA does, or their own limit passes
+                    int never = 0;
+                    for (int x = k; x < min(k + ATTN_STAGES, n_copy); ++x)
+                        mbar_wait(&full[(done + x) % ATTN_STAGES], (done + x) / ATTN_STAGES & 1, &never);
+                }
+                n_copy = 0;
+                stopped = gone = true;
             }
             gone |= s_gone[warp][stage] != 0;
             const uint8_t* rec = ring + stage * REC;
@@ -710,6 +718,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                     if (gone || key < sp.lo || key >= sp.hi)
                         *reinterpret_cast<unsigned short*>(vscale + t * 64 + scale_at(lane)) = 0;
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later copy lands on them
                 __syncwarp();
             }
             unsigned any = 0;

@@ -351,13 +351,14 @@ def test_wide_blocks_of_many_items(dtype, D):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("longest", [1536, 2048])
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
-def test_wide_blocks_on_clusters(dtype):
+def test_wide_blocks_on_clusters(dtype, longest):
     """Half as many items as CTAs, and few enough keys that two CTAs share each."""
     qmm = lib()
     rng = np.random.default_rng(9)
-    lens = [int(x) for x in rng.integers(0, 1536, 57)]
-    lens[:4] = [1536, 1535, 0, 1]
+    lens = [int(x) for x in rng.integers(0, longest, 57)]
+    lens[:4] = [longest, longest - 1, 0, 1]
     c = Case(qmm, lens, [4] * 57, 16, 4, 64, 64, dtype, seed=31, q_start=True)
     first = c.run()
     c.check(first)

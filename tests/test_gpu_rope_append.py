@@ -247,6 +247,29 @@ def test_append_of_zeros_and_small_blocks():
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("top", [7.0, 7 * 2.0 ** -20, 7 * 3.0, 5.3, 1.7e-37, 3e4])
+def test_append_of_values_halfway_between_codes(top):
+    """Quotients at a half, a step of fp32 beside it, and over the whole range: codes as the division's."""
+    qmm = lib()
+    T, D = 64, 64
+    rng = np.random.default_rng(3)
+    d = np.float32(np.float32(top) / np.float32(7))
+    x = (rng.integers(-7, 7, (T, 2, D)) + 0.5).astype(np.float32) * d
+    for _ in range(2):  # none, one or two steps up or down
+        x = np.where(rng.random(x.shape) < 0.4, np.nextafter(x, np.float32(rng.choice([-1e38, 1e38]))), x)
+    x[rng.random(x.shape) < 0.1] = 0
+    x[..., ::32] = np.float32(top)
+    x = np.clip(x, -np.float32(top), np.float32(top))
+    kv = torch.tensor(x, dtype=torch.float32, device=DEV)
+    data = qmm.kv_cache_data(2, 32, 2, D).fill_(255)
+    before = data.clone()
+    slots = torch.arange(T, device=DEV)
+    qmm.qmm_kv_append_q4_0(qmm.kv_append_op(qmm.kv_cache(data, 32), kv, kv, slots))
+    want = R.q4_0_values(x.astype(np.float64))
+    _check_cache(data, before, slots, (want, want), 32, D)
+    assert qmm.qmm_last_device_error() == 0
+
+
 def test_empty_calls_and_another_stream():
     qmm = lib()
     data = qmm.kv_cache_data(2, 32, 1, 64).fill_(1)
