@@ -691,7 +691,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         fence_before();
         __syncthreads();
         fence_after();
-        if (s_abort) break;
+        if (s_abort) {
+            if constexpr (!SOFTMAX) {
+                if (ok && lane == 0 && (warp == WARP_LOAD_K || warp == WARP_LOAD_V)) {  // another warp's wait ran out
+                    const unsigned slots = warp == WARP_LOAD_V ? V_SLOTS : K_SLOTS, issued = (steps + n) * STEP_RECORDS;
+                    for (unsigned i = issued - min(issued, slots); i < issued; ++i)
+                        if (!wait(&raw_full[warp - WARP_LOAD_K][i % slots], (i / slots) & 1)) break;
+                }
+            }
+            break;
+        }
         if (cut && tid == 0 && unit == 0) {
             const bool uncut = unit_end == sp.units;
             const int first = (int)blockIdx.x, last = uncut ? first - 1 : shares.cta_of(u + counts + sp.units - unit_end - 1);
