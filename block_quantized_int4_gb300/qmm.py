@@ -538,7 +538,8 @@ def kv_read_op(cache, slots, k=None, v=None):
 
 def attn_op(cache, q, pages, kv_len, out=None, yq=None, yd=None, q_start=None, max_q=1, max_kv=None, scale=None,
             causal=True, window=0, workspace=None):
-    """A qmm_attn_op; q, out [T][n_heads][head_dim], pages int32 [n_seqs][...], kv_len int32 [n_seqs].
+    """A qmm_attn_op; q, out [T][n_heads][head_dim], pages int32 [n_seqs][...] (each row with its own storage),
+    kv_len int32 [n_seqs].
     max_kv defaults to what the page table can hold, scale to head_dim ** -0.5; without a
     workspace one is allocated (the op holds it)."""
     T, H, D = q.shape
@@ -546,6 +547,8 @@ def attn_op(cache, q, pages, kv_len, out=None, yq=None, yd=None, q_start=None, m
     if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != B or (pages.shape[1] > 1 and
                                                                                    pages.stride(1) != 1):
         raise ValueError("attn_op: pages is int32 [n_seqs][...] with contiguous rows")
+    if B > 1 and pages.stride(0) < pages.shape[1]:
+        raise ValueError("attn_op: rows of pages that share storage (an expanded table): pass a contiguous one")
     if D != cache.head_dim:
         raise ValueError("attn_op: q has the cache's head_dim")
     if out is not None:
@@ -558,7 +561,7 @@ def attn_op(cache, q, pages, kv_len, out=None, yq=None, yd=None, q_start=None, m
                 _ptr(_plain(yd, torch.int16, (T, H * D // QK), "yd")),
                 _ptr(_plain(q_start, torch.int32, (B + 1,), "q_start")),
                 _ptr(_plain(kv_len, torch.int32, (B,), "kv_len")), pages.data_ptr(),
-                max(pages.stride(0), pages.shape[1]), T, B, max_q, max_kv, int(bool(causal)), window,
+                pages.stride(0) if B > 1 else pages.shape[1], T, B, max_q, max_kv, int(bool(causal)), window,
                 D ** -0.5 if scale is None else scale, None, 0)
     n = qmm_attn_workspace_size(op)
     if workspace is None and n:
