@@ -40,7 +40,7 @@
 // 2e-7 from q = u - 8).  A weight times d_v is rounded to fp16 once (fp16
 // activations, 2^-12) or twice (bf16, next to the output's own 2^-9).
 // Sums are fp32 throughout.  Weights times d_v are scaled by the power of two
-// that brings the largest d_v so far to 2^13, so they keep their bits whatever
+// that brings the largest d_v so far to 2^9, so they keep their bits whatever
 // the magnitude of v.
 #pragma once
 
@@ -374,16 +374,18 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int 
 }
 
 // Exponents: 2^e <= the largest scale < 2^(e + 1); weights are at most
-// 2^REF_SLACK, so 2^total times weight and scale is below 2^15, and the
-// weights' own factor 2^(part of total) at most 2^(15 - REF_SLACK).
-// Scales below 2^-7 take the rest of the factor themselves.
-// (The OR of the scales' exponent bits stands for the largest: never below
-// it, and above it by little, as the margins of fp16 allow.)
+// 2^REF_SLACK, so 2^room times weight and scale is below 2^15 with room = 14 -
+// REF_SLACK - e.  Of it the weights take 2^MIN_WEIGHT_EXP to 2^(15 - REF_SLACK):
+// with less the low parts of ordinary weights would be subnormal (fp32 rows, 4096
+// keys, scales of v from 0.4 to 2.2: an error of 1.4e-5 with a factor of 2^-7,
+// 2.4e-7 with 2^8).  The rest goes into the scales: upwards below 2^-7, which is exact, and
+// downwards from 2^5 on, which is exact for scales down to 2^-18 of the largest.
 __device__ __forceinline__ int scale_exponent(int bits) {  // exponent bits of fp16
     return (bits >> 10) - 15 + (bits == 0);                // subnormal scales count as 2^-14
 }
 
 constexpr int REF_SLACK = 5;
+constexpr int MIN_WEIGHT_EXP = 5;
 
 template <int NB, int DTYPE, int NT>
 __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(const __grid_constant__ AttnArgs a) {
@@ -721,16 +723,16 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later copy lands on them
                 __syncwarp();
             }
-            unsigned any = 0;
+            __half2 any = __float2half2_rn(0.f);  // the largest magnitude
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint4 d4 = lds128(vscale + kb * 64 + c * 16);
-                any |= d4.x | d4.y;
-                any |= d4.z | d4.w;
+                any = __hmax2(__hmax2(any, __habs2(as_half2(d4.x))), __habs2(as_half2(d4.y)));
+                any = __hmax2(__hmax2(any, __habs2(as_half2(d4.z))), __habs2(as_half2(d4.w)));
             }
             // The reference follows the running maximum by steps of more than
             // 2^REF_SLACK, so acc is rarely rescaled; so with the scales of v.
-            int exponent = (any | any >> 16) & 0x7C00;
+            int exponent = max((int)(as_bits(any) & 0x7C00), (int)(as_bits(any) >> 16 & 0x7C00));
             float2 m[NT];
             bool moved = exponent > top_bits;
 #pragma unroll
@@ -745,9 +747,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                 exponent = __reduce_max_sync(FULL, exponent);
                 float ratio = 1.f;
                 if (exponent > top_bits) {
-                    const int room = 14 - REF_SLACK - scale_exponent(exponent), w = min(room, 15 - REF_SLACK);
+                    const int room = 14 - REF_SLACK - scale_exponent(exponent);
+                    const int w = min(max(room, MIN_WEIGHT_EXP), 15 - REF_SLACK);
                     vs = exp2f((float)w);
-                    ds = room > 21 - REF_SLACK ? exp2f((float)(room - w)) : 1.f;
+                    ds = room > 21 - REF_SLACK || room < w ? exp2f((float)(room - w)) : 1.f;
                     ratio = top_bits < 0 ? 1.f : vs * ds * unscale;
                     unscale = 1.f / (vs * ds);
                     top_bits = exponent;
@@ -804,11 +807,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                 const unsigned w[4] = {w4.x, w4.y, w4.z, w4.w};
                 unsigned vd[4] = {d4.x, d4.y, d4.z, d4.w};
                 if (ds != 1.f) {
+                    const __half2 by = __float2half2_rn(ds);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 d = unpack_half(vd[j]);
-                        vd[j] = pack_half(d.x * ds, d.y * ds);
-                    }
+                    for (int j = 0; j < 4; ++j) vd[j] = as_bits(__hmul2(as_half2(vd[j]), by));
                 }
                 unsigned b[NT][4], bl[NT][4];
 #pragma unroll
