@@ -37,8 +37,11 @@
 // with -8 sum_e q'_e as the accumulator's start: one operation a register
 // less, but the tensor core aligns its addends to the largest, and starting
 // from that large a value costs 5 bits (fp32 rows: 4e-6 of the output against
-// 2e-7 from q = u - 8).  A weight times d_v is rounded to fp16 once (fp16
-// activations, 2^-12) or twice (bf16, next to the output's own 2^-9).
+// 2e-7 from q = u - 8).  A weight times d_v is two fp16 parts, as for fp32 (one
+// part, 2^-12, was half of the error of fp16 outputs, which round at 2^-12
+// themselves: 2.6e-4 of the window case's output, 2.0e-4 with two); bf16, whose
+// outputs round at 2^-9, takes one, rounded twice (1.67e-3 against 1.65e-3; two
+// parts: 54 us instead of 48 for the sixteen ragged sequences, fp16 as bf16).
 // Sums are fp32 throughout.  Weights times d_v are scaled by the power of two
 // that brings the largest d_v so far to 2^9, so they keep their bits whatever
 // the magnitude of v.
@@ -817,13 +820,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const __half2 d = as_half2(vd[j]), h = as_half2(ph[r][j]);
-                        if constexpr (SPLIT) {
+                        if constexpr (DTYPE != QMM_BF16) {
                             // (hi + lo) d as two parts: the product, and its exact error plus lo d
                             const __half2 pr = __hmul2(h, d);
                             b[r][j] = as_bits(pr);
                             bl[r][j] = as_bits(__hfma2(as_half2(pl[r][j]), d, __hfma2(h, d, __hneg2(pr))));
-                        } else if constexpr (DTYPE == QMM_F16) {
-                            b[r][j] = as_bits(__hfma2(h, d, __hmul2(as_half2(pl[r][j]), d)));  // one rounding of (hi + lo) d
                         } else {
                             b[r][j] = as_bits(__hmul2(h, d));  // two roundings of 2^-12, next to the output's 2^-9
                         }
@@ -842,6 +843,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                                 mma_add(t[r], v, bl[r][2 * st], bl[r][2 * st + 1]);
                                 mma_add(t[r], v, b[r][2 * st], b[r][2 * st + 1]);
                             } else {
+                                if constexpr (DTYPE == QMM_F16) mma_add(acc[r][kb][e], v, bl[r][2 * st], bl[r][2 * st + 1]);
                                 mma_add(acc[r][kb][e], v, b[r][2 * st], b[r][2 * st + 1]);
                             }
                         }

@@ -763,8 +763,9 @@ QMM_API qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream);
  * window > 0.  Query head h reads key/value head h / (q.n_heads /
  * cache.n_heads).  out = sum_j softmax_j(scale * q . k_j) v_j over the keys
  * it sees, with k and v the cached values d * q; 0 where it sees none.
- * Scores, softmax statistics and sums are fp32; with fp32 q and out the
- * products carry 22 bits of q and of the weights, with a 16-bit type 11.
+ * Scores, softmax statistics and sums are fp32.  The products carry 22 bits
+ * of q and of the weights (fp32), q as it is and 22 bits of the weights (fp16),
+ * or 11 of both (bf16).
  * (bf16 calls of many queries multiply k and v as fp16: values of the cache
  * beyond 65504 in magnitude are outside their domain.)
  * out.data may be NULL when yq and yd are given: Q8_0 of the fp32 output
