@@ -620,8 +620,9 @@ qmm_status qmm_rope_table(float* table, int64_t n_pos, int32_t n_rot, double bas
     const int half = n_rot / 2;
     const double pi = 3.14159265358979323846;
     const auto place = [&](double turns) { return n_rot * std::log(orig_len / (2 * pi * turns)) / (2 * std::log(base)); };
+    // the method clamps both ends to the head's values, 0 .. n_rot - 1, so the ramp may end past the last pair
     const double lo = scaling == QMM_ROPE_RAMP ? std::max(0.0, std::floor(place(beta_fast))) : 0;
-    const double hi = scaling == QMM_ROPE_RAMP ? std::min(half - 1.0, std::ceil(place(beta_slow))) : 0;
+    const double hi = scaling == QMM_ROPE_RAMP ? std::min(n_rot - 1.0, std::ceil(place(beta_slow))) : 0;
     for (int i = 0; i < half; ++i) {
         const double f = std::pow(base, -2.0 * i / n_rot);
         const double r = scaling == QMM_ROPE_LINEAR ? 1.0

@@ -657,7 +657,7 @@ typedef enum qmm_rope_scaling {
 /* Fill a rotary table (set-up): table[p][i] = (m cos(p f_i), m sin(p f_i)),
  * angles and functions in 64 bits, rounded once.  QMM_ROPE_RAMP is the YaRN
  * method (Peng et al., 2023): with x(n) = n_rot ln(orig_len / (2 pi n)) /
- * (2 ln base), lo = max(0, floor(x(beta_fast))), hi = min(n_rot / 2 - 1,
+ * (2 ln base), lo = max(0, floor(x(beta_fast))), hi = min(n_rot - 1,
  * ceil(x(beta_slow))), r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):
  * f_i = plain_i (1 - r_i) + plain_i / factor * r_i and m = 0.1 ln(factor) + 1
  * (m = 1 otherwise; factor, orig_len and the betas are read only where they
