@@ -41,7 +41,7 @@ DevInfo g_dev[MAX_DEVICES];
 // Small-batch GEMM kernel choice (qmm_debug_gemm_kernel), process-wide.
 std::atomic<int> g_gemm_kernel{QMM_GEMM_KERNEL_AUTO};
 
-// Bounded-wait test settings of the streaming kernel (qmm_debug_stream_wait).
+// Bounded-wait test settings of the streaming and the attention kernels (qmm_debug_stream_wait).
 std::atomic<unsigned long long> g_stream_wait_ns{WAIT_LIMIT_NS};
 std::atomic<int> g_stream_withhold{0};
 
@@ -77,6 +77,8 @@ int* qmm::device_error_word() {
     const DevInfo* d = device_info();
     return d ? d->err : nullptr;
 }
+
+WaitSettings qmm::wait_settings() { return {g_stream_wait_ns.load(), g_stream_withhold.load()}; }
 
 bool qmm::device_facts(int* sms, int* smem_optin) {
     const DevInfo* d = device_info();

@@ -225,6 +225,9 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.meta = static_cast<AttnMeta*>(op->workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);
     a.err = device_error_word();
+    const WaitSettings wait = wait_settings();
+    a.wait_ns = wait.limit_ns;
+    a.withhold = wait.withhold;
     const int NB = op->cache.head_dim / QK;
     const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB, p.tiles);
     if (!prepared(kernel, p.tc ? 6 : 2 * op->q.dtype + p.tiles - 1, NB, p.tc ? p.smem : optin - 4096)) return QMM_ERR_CUDA;

@@ -38,7 +38,7 @@
 // less, but the tensor core aligns its addends to the largest, and starting
 // from that large a value costs 5 bits (fp32 rows: 4e-6 of the output against
 // 2e-7 from q = u - 8).  A weight times d_v is two fp16 parts, as for fp32 (one
-// part, 2^-12, was half of the error of fp16 outputs, which round at 2^-12
+// part, 2^-12, would show beside fp16 outputs, which round at 2^-12
 // themselves: 2.6e-4 of the window case's output, 2.0e-4 with two); bf16, whose
 // outputs round at 2^-9, takes one, rounded twice (1.67e-3 against 1.65e-3; two
 // parts: 54 us instead of 48 for the sixteen ragged sequences, fp16 as bf16).
@@ -98,6 +98,8 @@ struct AttnArgs {
     float* part;     // [ctas][2][rows][attn_part_floats]
     AttnMeta* meta;  // [sequence][row block][head]
     int* err;
+    unsigned long long wait_ns;  // bound of a wait
+    int withhold;                // records whose copies a warp holds back, the last of its share (0 or 1)
 };
 
 // The kernel of head size 32 * NB for one type of activations and one or two
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
     }
 
     unsigned done = 0;  // records of this warp so far: stage and phase of the ring
-    bool stopped = false;  // a wait ran out: no more copies, what follows is not used
+    bool stopped = false;  // a wait of this warp ran out: it takes no more records, and the outputs are not used
     for (int u = u0; u < u1;) {
         const int b = a.blocks == 1 ? at.entry : at.entry / a.blocks, block = at.entry - b * a.blocks;
         const Seq seq = sequence(a, b, !cut && tid == 0);
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
         }
         const int rec0 = sp.lo / GROUP + at.unit * ATTN_WARPS + warp;
         const int rec_end = min((sp.hi + GROUP - 1) / GROUP, sp.lo / GROUP + unit_end * ATTN_WARPS);
-        const int n_mine = rec_end > rec0 ? (rec_end - rec0 + ATTN_WARPS - 1) / ATTN_WARPS : 0;
+        const int n_mine = rec_end > rec0 && !stopped ? (rec_end - rec0 + ATTN_WARPS - 1) / ATTN_WARPS : 0;
 
         // ---- the ring: a warp copies its records whole; its lanes look up the next
         // 32 records' places in the cache at once
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                 place = gone ? -1 : (page * a.kv_heads + at.head) * a.page_groups + rec - pg * a.page_groups;
             }
         };
-        int n_copy = stopped ? 0 : n_mine;
+        const int n_copy = n_mine - a.withhold;
         const auto issue = [&](int k) {
             if (k < n_copy) {
                 if (k % 32 == 0) look_up(k);
@@ -638,21 +640,21 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
             __syncwarp();  // the record before is read
             issue(k + ATTN_STAGES - 1);
             const unsigned stage = (done + k) % ATTN_STAGES;
-            bool gone = false;
-            if (!mbar_wait(&full[stage], (done + k) / ATTN_STAGES & 1, (volatile int*)&s_abort)) {
+            // a vote: lanes that disagree about a copy that lands at the limit would part
+            if (!__all_sync(FULL, mbar_wait(&full[stage], (done + k) / ATTN_STAGES & 1, &s_abort, a.wait_ns))) {
                 if (lane == 0) {
                     s_abort = 1;
                     atomicOr(a.err, ERR_TIMEOUT);
                 }
-                if (n_copy) {  // the copies on their way end before the CTA does, or their own limit passes
-                    int never = 0;
-                    for (int x = k; x < min(k + ATTN_STAGES, n_copy); ++x)
-                        mbar_wait(&full[(done + x) % ATTN_STAGES], (done + x) / ATTN_STAGES & 1, &never);
-                }
-                n_copy = 0;
-                stopped = gone = true;
+                // the copies on their way end before the CTA does, or their own limit passes
+                int never = 0;
+                for (int x = k; x < min(k + ATTN_STAGES, n_copy); ++x)
+                    mbar_wait(&full[(done + x) % ATTN_STAGES], (done + x) / ATTN_STAGES & 1, &never, a.wait_ns);
+                __syncwarp();
+                stopped = true;
+                break;
             }
-            gone |= s_gone[warp][stage] != 0;
+            const bool gone = s_gone[warp][stage] != 0;
             const uint8_t* rec = ring + stage * REC;
             const int tok0 = (rec0 + k * ATTN_WARPS) * GROUP;
 

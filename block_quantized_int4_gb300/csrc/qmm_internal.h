@@ -12,4 +12,12 @@ bool device_facts(int* sms, int* smem_optin);
 // qmm_last_device_error), or null without an sm_103 device.
 int* device_error_word();
 
+// How long a wait on the device may take, and whether kernels hold back their
+// last copy so that one runs out (qmm_debug_stream_wait).
+struct WaitSettings {
+    unsigned long long limit_ns;
+    int withhold;
+};
+WaitSettings wait_settings();
+
 }  // namespace qmm
