@@ -227,6 +227,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.err = device_error_word();
     const WaitSettings wait = wait_settings();
     a.wait_ns = wait.limit_ns;
+    a.wait_ns_tc = attn_tc_wait_ns(wait.limit_ns);
     a.withhold = wait.withhold;
     const int NB = op->cache.head_dim / QK;
     const AttnKernel kernel = p.tc ? attn_tc_kernel(NB) : kernel_of(op->q.dtype, NB, p.tiles);

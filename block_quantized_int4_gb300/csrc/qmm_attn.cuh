@@ -99,6 +99,7 @@ struct AttnArgs {
     AttnMeta* meta;  // [sequence][row block][head]
     int* err;
     unsigned long long wait_ns;  // bound of a wait
+    unsigned wait_ns_tc;         // the same, as the tensor-memory kernel takes it
     int withhold;                // records whose copies a warp holds back, the last of its share (0 or 1)
 };
 

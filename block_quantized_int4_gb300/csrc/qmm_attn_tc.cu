@@ -39,9 +39,11 @@
 // Keys and values are fp16 here: one beyond 65504 in magnitude is infinite.
 //
 // Operands lie as K-major core matrices of 8 rows x 16 bytes without swizzle.
-// Every wait is bounded; on expiry the error word is set and the CTA ends.
+// Every wait is bounded in time; on expiry the error word is set, copies and
+// products on their way are waited for, and the CTA ends.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "qmm_attn.cuh"
@@ -159,23 +161,30 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QMM_U8(r, 0), QMM_U8(r, 8) : : "memory");
 }
 
-// A bounded wait: up to 2^24 tries, each held back by the hardware for some
-// tens of cycles (seconds in all).  The loop is five instructions, for up to
-// six warps of a scheduler poll while the others compute.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+// A bounded wait.  The hardware holds a try back for 1 to 2 us (whatever time it is
+// asked for), so counting tries bounds no time: the clock does, by its low 32 bits.
+// The loop is short because its copies crowd the instruction cache: with the
+// 64-bit clock and an abort flag of the CTA in it, 509 queries over 8190 tokens
+// took 172 us instead of 162.  Lanes may disagree where a phase ends at the limit:
+// callers vote.
+constexpr unsigned MAX_WAIT_NS = 4000000000u;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned limit_ns) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 t, t0;\n\tmov.u32 t0, 0;\n"
         "AGAIN:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "@p bra DONE;\n\t"
-        "add.u32 n, n, 1;\n\t"
-        "setp.lt.u32 q, n, 16777216;\n\t"
+        "mov.u32 t, %globaltimer_lo;\n\t"
+        "setp.eq.u32 q, t0, 0;\n\t"
+        "@q mov.u32 t0, t;\n\t"
+        "sub.u32 t, t, t0;\n\t"
+        "setp.lt.u32 q, t, %3;\n\t"
         "@q bra AGAIN;\n"
         "DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(limit_ns)
         : "memory");
     return ok != 0;
 }
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     __shared__ int s_gone[2][8][STEP_RECORDS];
     __shared__ uint64_t q_full;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort[2];  // of a segment and the next: a warp may still read one when another sets the other
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         mbar_init(&o_full, 1);
         mbar_init(&q_full, SOFTMAX_WARPS);
         mbar_init(&drain, 1);
-        s_abort = 0;
+        s_abort[0] = s_abort[1] = 0;
         fence_mbar_init();
     }
     if (warp == WARP_MMA) {
@@ -353,6 +362,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         }
 
         bool ok = true;
+        unsigned issued = 0;  // of a loading warp: records whose copies are under way or done
+        const auto voted = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(FULL, wait(bar, parity, a.wait_ns_tc)) != 0;
+        };
         if constexpr (!SOFTMAX) {
         if (warp == WARP_LOAD_K || warp == WARP_LOAD_V) {
             // ---------------- records: four a step, two steps in flight; codes and scales of K or of V
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             const int* table = a.pages + (int64_t)b * a.pages_stride;
             const unsigned slots = kv ? V_SLOTS : K_SLOTS;
             uint8_t* ring = smem + SM::RAW + kv * (K_SLOTS * SM::PART);
-            unsigned issued = steps * STEP_RECORDS;  // records so far, one after the other over all segments
+            issued = steps * STEP_RECORDS;  // one after the other over all segments
             for (int t = 0; t < n && ok; ++t) {
                 const unsigned it = steps + t;
                 const int rec = rec0 + t * STEP_RECORDS + lane;
@@ -375,8 +388,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 __syncwarp();
                 for (int r = 0; r < STEP_RECORDS; ++r) {
                     const unsigned i = it * STEP_RECORDS + r, slot = i % slots;
-                    if (i >= slots) ok = __all_sync(FULL, wait(&raw_empty[kv][slot], (i / slots - 1) & 1));
-                    if (!ok) break;
+                    if (i >= slots) ok = voted(&raw_empty[kv][slot], (i / slots - 1) & 1);
+                    if (!ok || (a.withhold && t == n - 1 && r == STEP_RECORDS - 1)) break;
                     if (lane == r) {
                         uint64_t* full = &raw_full[kv][slot];
                         if (place < 0) {
@@ -392,10 +405,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     __syncwarp();
                     issued = i + 1;
                 }
-            }
-            if (!ok && lane == 0) {  // copies on their way land before the CTA ends
-                for (unsigned i = issued - min(issued, slots); i < issued; ++i)
-                    if (!wait(&raw_full[kv][i % slots], (i / slots) & 1)) break;
             }
         } else if (warp == WARP_MMA) {
             // ---------------- products
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 __syncwarp();
             };
             if (un) {
-                ok = wait(&q_full, walked & 1) && wait(&k_full[us & 1], (us / 2) & 1);
+                ok = __all_sync(FULL, wait(&q_full, walked & 1, a.wait_ns_tc) && wait(&k_full[us & 1], (us / 2) & 1, a.wait_ns_tc));
                 fence_after();
                 for (int x = 0; x < ut && ok; ++x) scores(x, us);
             }
@@ -429,8 +438,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 const unsigned it = us + t;
                 const uint32_t v0 = v_lo + (it & 1) * BUFFER;
                 for (int x = 0; x < ut && ok; ++x) {
-                    if (x == 0) ok = wait(&v_full[it & 1], (it / 2) & 1);
-                    ok = ok && wait(&p_full[x], (x ? us1 + t : it) & 1);
+                    bool there = x != 0 || wait(&v_full[it & 1], (it / 2) & 1, a.wait_ns_tc);
+                    there = there && wait(&p_full[x], (x ? us1 + t : it) & 1, a.wait_ns_tc);
+                    ok = __all_sync(FULL, there);
                     if (!ok) break;
                     fence_after();
                     const uint32_t to = ud + O_COL + x * 128, w = ud + S_COL + x * 128;
@@ -445,20 +455,19 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                     }
                     __syncwarp();
                     if (t + 1 < un) {
-                        if (x == 0) ok = wait(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1);
+                        if (x == 0) ok = voted(&k_full[(it + 1) & 1], ((it + 1) / 2) & 1);
                         if (!ok) break;
                         fence_after();
                         scores(x, it + 1);
                     }
                 }
             }
-            ok = __all_sync(FULL, ok);
             if (un && one) {
                 if (ok) {
                     commit(&o_full);
                 } else {  // products on their way end before tensor memory is freed
                     commit(&drain);
-                    wait(&drain, 0);
+                    wait(&drain, 0, a.wait_ns_tc);
                 }
             }
             __syncwarp();
@@ -471,8 +480,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
                 const unsigned i = it * STEP_RECORDS + rr, slots = kv ? V_SLOTS : K_SLOTS, slot = i % slots;
-                bool there = wait(&raw_full[kv][slot], (i / slots) & 1);
-                if (it >= 2) there = there && wait(kv ? &v_empty[st] : &k_empty[st], (it / 2 - 1) & 1);
+                bool there = wait(&raw_full[kv][slot], (i / slots) & 1, a.wait_ns_tc);
+                if (it >= 2) there = there && wait(kv ? &v_empty[st] : &k_empty[st], (it / 2 - 1) & 1, a.wait_ns_tc);
                 ok = __all_sync(FULL, there);
                 if (!ok) break;
                 const uint8_t* rec = smem + SM::RAW + (kv * K_SLOTS + slot) * SM::PART;
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             uint32_t r[2][32];
             for (int t = 0; t < n; ++t) {
                 __syncwarp();
-                ok = __all_sync(FULL, wait(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1));
+                ok = voted(&s_full[tile], (tile ? tile1_steps + t : steps + t) & 1);
                 if (!ok) break;
                 fence_after();
                 const int key0 = (rec0 + t * STEP_RECORDS) * GROUP;
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&p_full[tile]);
             }
             // ---- the row's output, or its part
-            if (ok && n) ok = __all_sync(FULL, wait(&o_full, segments & 1));
+            if (ok && n) ok = voted(&o_full, segments & 1);
             fence_after();
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -685,18 +694,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             fence_async();  // the buffers are operands again
         }
         if (!ok) {
-            if (lane == 0) atomicOr(a.err, ERR_TIMEOUT);
-            s_abort = 1;
+            if (lane == 0) {
+                atomicOr(a.err, ERR_TIMEOUT);
+                s_abort[walked & 1] = 1;
+            }
         }
         fence_before();
         __syncthreads();
         fence_after();
-        if (s_abort) {
+        if (s_abort[walked & 1]) {
             if constexpr (!SOFTMAX) {
-                if (ok && lane == 0 && (warp == WARP_LOAD_K || warp == WARP_LOAD_V)) {  // another warp's wait ran out
-                    const unsigned slots = warp == WARP_LOAD_V ? V_SLOTS : K_SLOTS, issued = (steps + n) * STEP_RECORDS;
+                if (n && lane == 0 && (warp == WARP_LOAD_K || warp == WARP_LOAD_V)) {
+                    // copies on their way land before the CTA ends, or their own limit passes
+                    const unsigned slots = warp == WARP_LOAD_V ? V_SLOTS : K_SLOTS;
                     for (unsigned i = issued - min(issued, slots); i < issued; ++i)
-                        if (!wait(&raw_full[warp - WARP_LOAD_K][i % slots], (i / slots) & 1)) break;
+                        if (!wait(&raw_full[warp - WARP_LOAD_K][i % slots], (i / slots) & 1, a.wait_ns_tc)) break;
                 }
             }
             break;
@@ -743,5 +755,9 @@ int attn_tc_smem(int NB) {
 }
 
 int attn_tc_threads() { return attn_tc::THREADS; }
+
+unsigned attn_tc_wait_ns(unsigned long long limit_ns) {
+    return (unsigned)std::min<unsigned long long>(limit_ns, attn_tc::MAX_WAIT_NS);
+}
 
 }  // namespace qmm

@@ -13,5 +13,6 @@ constexpr int ATTN_TC_MAX_NB = 4;     // head sizes up to 128: O of two tiles is
 AttnKernel attn_tc_kernel(int NB);
 int attn_tc_smem(int NB);
 int attn_tc_threads();
+unsigned attn_tc_wait_ns(unsigned long long limit_ns);  // the bound of a wait: 4 s at most
 
 }  // namespace qmm

@@ -45,3 +45,13 @@ def test_warp_mma_kernel(lens, n, Hq, Hkv, D, dtype):
     qmm = lib()
     assert qmm.qmm_last_device_error() == 0
     _run_out_and_recover(Case(qmm, lens, [n] * len(lens), Hq, Hkv, D, 64, dtype, seed=D))
+
+
+@pytest.mark.parametrize("D", [32, 128])
+@pytest.mark.parametrize("many", [13, 14])
+def test_tensor_memory_kernel(D, many):
+    """Whole items, one or two a CTA, of 0 to 3 steps; two tiles and one."""
+    qmm = lib()
+    assert qmm.qmm_last_device_error() == 0
+    c = Case(qmm, [0, 3, 129, 300, 70] * many, [130, 64, 128, 40, 70] * many, 4, 2, D, 96, "bf16", seed=D, q_start=True)
+    _run_out_and_recover(c)
