@@ -221,6 +221,7 @@ qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     a.mode = p.mode;
     a.cluster = p.cluster;
     a.start = p.start;
+    a.ctas = p.ctas;
     a.part_at = p.part_at;
     a.meta = static_cast<AttnMeta*>(op->workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(op->workspace) + p.meta_bytes);

@@ -95,6 +95,7 @@ struct AttnArgs {
     int mode;        // AttnMode
     int start;       // counts before an item's units (ATTN_CUT)
     int cluster;     // CTAs of a cluster (ATTN_CLUSTER)
+    int ctas;        // CTAs of a cut launch
     float* part;     // [ctas][2][rows][attn_part_floats]
     AttnMeta* meta;  // [sequence][row block][head]
     int* err;
@@ -998,8 +999,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
     if ((int)blockIdx.y * ROWS >= rows) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnMeta mt = a.meta[blockIdx.x];
+    // not cut; or never written, by a CTA of which a wait ran out, and then it may hold anything
+    if (mt.first < 0 || mt.last <= mt.first || mt.last >= a.ctas) return;
     const int n = mt.last - mt.first + 1;
-    if (n <= 1) return;
     const int64_t step = (int64_t)block_rows * attn_part_floats(D);
     for (int row0 = blockIdx.y * ROWS; row0 < rows; row0 += gridDim.y * ROWS) {
         const int row = row0 + team;

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from parity import lib
-from test_gpu_attn import Case
+from test_gpu_attn import DEV, MAY_GROW, Case
 
 pytestmark = pytest.mark.gpu
 TIMEOUT = 6  # QMM_ERR_TIMEOUT
@@ -55,3 +55,28 @@ def test_tensor_memory_kernel(D, many):
     assert qmm.qmm_last_device_error() == 0
     c = Case(qmm, [0, 3, 129, 300, 70] * many, [130, 64, 128, 40, 70] * many, 4, 2, D, 96, "bf16", seed=D, q_start=True)
     _run_out_and_recover(c)
+
+
+@pytest.mark.parametrize("lens,nqs,D", [([200], [64], 64), ([2000, 40, 1500], [64] * 3, 128), ([3, 700, 0, 257], [130, 40, 64, 1], 32)])
+@pytest.mark.parametrize("left", [(0, 2 ** 31 - 1), (-2 ** 31, 2 ** 31 - 1), (1 << 20, 1 << 21), (2, 40)])
+def test_cut_items_of_the_tensor_memory_kernel(lens, nqs, D, left):
+    """An aborted CTA leaves the places unwritten that say which parts make an item; whatever was in the workspace,
+    nothing outside it is read."""
+    qmm = lib()
+    assert qmm.qmm_last_device_error() == 0
+    c = Case(qmm, lens, nqs, 4, 2, D, 96, "bf16", seed=D, q_start=True, extra_kv=MAY_GROW // 96)
+    want = c.run(max_kv=MAY_GROW)
+    c.check(want)
+    out = torch.empty_like(want)
+    op = c.op(out, max_kv=MAY_GROW)
+    words = op._keep[-1].view(torch.int32)
+    words.copy_(torch.tensor([left[0], left[1], 1, 0], dtype=torch.int32, device=DEV).repeat(words.numel() // 4))
+    prev = qmm.qmm_debug_stream_wait(1_000_000, withhold_last_copy=True)
+    try:
+        qmm.qmm_attn_q4_0(op)
+        assert qmm.qmm_last_device_error() == TIMEOUT
+    finally:
+        qmm.qmm_debug_stream_wait(prev, withhold_last_copy=False)
+    qmm.qmm_attn_q4_0(op)
+    assert qmm.qmm_last_device_error() == 0
+    assert torch.equal(out, want)
