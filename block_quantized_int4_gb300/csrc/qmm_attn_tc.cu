@@ -36,7 +36,10 @@
 // Steps of 64 keys with S double buffered: 198 to 240 us against 172 then,
 // twice the waits and commits.
 //
-// Keys and values are fp16 here: one beyond 65504 in magnitude is infinite.
+// Keys and values are fp16 here.  Where a scale that some row sees is so large
+// that d (u - 8) might not fit, the segment is done again with keys and values in
+// sixteenths (exact but for scales below 2^-10): its products and sums so far are
+// not used, and no output has been written.
 //
 // Operands lie as K-major core matrices of 8 rows x 16 bytes without swizzle.
 // Every wait is bounded in time; on expiry the error word is set, copies and
@@ -189,10 +192,23 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned li
     return ok != 0;
 }
 
-// Two codes times a pair of scales: nibbles 0 and 4 of w.
-__device__ __forceinline__ unsigned scaled_codes(unsigned w, __half2 d, unsigned magic) {
-    return attn::as_bits(__hmul2(attn::as_half2(attn::signed_codes<0>(w, magic)), d));
+constexpr float MAX_SCALE = 8188.f;  // 8 MAX_SCALE is the largest fp16
+constexpr float WIDE = 16.f;         // what codes are divided by beyond it
+
+// Two codes times a pair of scales: nibbles 0 and 4 of w.  `magic` is the fp16
+// pair that the nibbles are OR-ed into, 1024 or (sixteenths) 64, and eight units of
+// its last place are u = 8.
+__device__ __forceinline__ unsigned magic_codes(bool sixteenths) { return sixteenths ? 0x54005400u : 0x64006400u; }
+__device__ __forceinline__ unsigned scaled_codes(unsigned w, __half2 d, unsigned magic, __half2 eight) {
+    unsigned bits;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(bits) : "r"(w), "n"(0x000F000Fu), "r"(magic));
+    return attn::as_bits(__hmul2(__hsub2(attn::as_half2(bits), eight), d));
 }
+
+struct Place {  // where a walk stands
+    int entry, head, unit, u;
+    unsigned steps, segments, tile1_steps, walked;
+};
 
 template <int NB>
 __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a) {
@@ -208,7 +224,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     __shared__ int s_gone[2][8][STEP_RECORDS];
     __shared__ uint64_t q_full;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort[2];  // of a segment and the next: a warp may still read one when another sets the other
+    // of a segment and the next: a warp may still read one when another sets the other
+    __shared__ int s_abort[2];
+    __shared__ unsigned s_large[2];  // the segment (walked + 1) that has scales above MAX_SCALE
+    __shared__ Place s_place;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -230,6 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
         mbar_init(&q_full, SOFTMAX_WARPS);
         mbar_init(&drain, 1);
         s_abort[0] = s_abort[1] = 0;
+        s_large[0] = s_large[1] = 0;
         fence_mbar_init();
     }
     if (warp == WARP_MMA) {
@@ -244,29 +264,36 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
     const uint32_t tmem = s_tmem;
 
     const bool cut = a.mode == ATTN_CUT;
-    int entry, head, unit = 0, u0 = 0, u1 = 1;
+    int entry0 = 0, head0 = 0, unit0 = 0, u0 = 0, u1 = 1;
     attn::Cut shares = {};
     if (cut) {
         attn::find_share<THREADS>(a, BLOCK_ROWS, STEP_RECORDS, sh, u0, u1, shares);
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (u0 < u1) {
-            entry = sh.entry;
-            head = (u0 - sh.start) / sh.units;
-            unit = u0 - sh.start - head * sh.units;
+            entry0 = sh.entry;
+            head0 = (u0 - sh.start) / sh.units;
+            unit0 = u0 - sh.start - head0 * sh.units;
         }
     } else {  // later row blocks (more keys) first
         const int e = blockIdx.x / a.kv_heads, b = e / a.blocks;
-        head = blockIdx.x - e * a.kv_heads;
-        entry = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
+        head0 = blockIdx.x - e * a.kv_heads;
+        entry0 = b * a.blocks + (a.blocks - 1 - (e - b * a.blocks));
     }
 
-    // The walk over the CTA's segments, once for each kind of warp (their register budgets differ).
-    const auto walk = [&](auto softmax_role) {
-    constexpr bool SOFTMAX = decltype(softmax_role)::value;
-    unsigned steps = 0, segments = 0;  // before this segment: phases of the barriers
-    unsigned tile1_steps = 0;          // of them, those of tile 1
-    unsigned walked = 0;               // segments, those without keys among them
-    for (int u = u0; u < u1;) {
+    // The walk over the CTA's segments, once for each kind of warp (their register budgets differ), and
+    // once more from a segment with large scales on, which is then done in sixteenths: true where the first
+    // walk met one, and where it stood is in shared memory.  (One walk that can turn back: 4 x 512 queries
+    // 81.2 us instead of 78.8, by registers that were spilled.)
+    const auto walk = [&](auto softmax_role, auto turns_back) {
+    constexpr bool SOFTMAX = decltype(softmax_role)::value, TURNS_BACK = decltype(turns_back)::value;
+    Place at = {entry0, head0, unit0, u0, 0, 0, 0, 0};
+    if constexpr (TURNS_BACK) at = s_place;
+    int entry = at.entry, head = at.head, unit = at.unit;
+    unsigned steps = at.steps, segments = at.segments;  // before this segment: phases of the barriers
+    unsigned tile1_steps = at.tile1_steps;              // of them, those of tile 1
+    unsigned walked = at.walked;                        // segments, those without keys among them
+    bool wide = TURNS_BACK;                             // this segment is done in sixteenths
+    for (int u = at.u; u < u1;) {
         const int b = a.blocks == 1 ? entry : entry / a.blocks, block = entry - b * a.blocks;
         const Seq seq = attn::sequence(a, b, !cut && tid == 0);
         const Span sp = attn::span_of(a, seq, block, BLOCK_ROWS, STEP_RECORDS);
@@ -343,6 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             const int up = top > 0.f ? 13 - min(max(ilogbf(top), -100), 100) : 0;
             const float mul = a.scale_log2 == 0.f ? 0.f : copysignf(exp2f((float)up), a.scale_log2);
             f = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2) * exp2f((float)-up);
+            if (wide) f *= WIDE;
 #pragma unroll
             for (int k = 0; k < NB * 4; ++k) {
                 unsigned w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -475,8 +503,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             // ---------------- K or V of a step as operands, a record a warp
             const int kv = warp < WARP_K, rr = kv ? (warp - WARP_V) & 3 : warp - WARP_K, g = lane >> 2, c = lane & 3;
             const int half = (warp - WARP_V) >> 2;  // of the blocks of V
-            unsigned magic;
-            asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+            const unsigned magic = magic_codes(wide);
+            const __half2 eight = attn::as_half2(magic + 0x00080008u);
+            __half2 top = __float2half2_rn(0.f);  // of the scales that a row may see
             for (int t = 0; t < n; ++t) {
                 const unsigned it = steps + t, st = it & 1;
                 const unsigned i = it * STEP_RECORDS + rr, slots = kv ? V_SLOTS : K_SLOTS, slot = i % slots;
@@ -502,9 +531,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                             unsigned one = __byte_perm(ds[j], 0, g & 1 ? 0x3232 : 0x1010);
                             if (!all && !seen(8 * j + g)) one = 0;
                             const __half2 d = attn::as_half2(one);
+                            top = __hmax2(top, __habs2(d));
                             *reinterpret_cast<uint4*>(to + kb * 512 + j * (D * 16)) =
-                                make_uint4(scaled_codes(ws[j], d, magic), scaled_codes(ws[j] >> 8, d, magic),
-                                           scaled_codes(ws[j] >> 4, d, magic), scaled_codes(ws[j] >> 12, d, magic));
+                                make_uint4(scaled_codes(ws[j], d, magic, eight), scaled_codes(ws[j] >> 8, d, magic, eight),
+                                           scaled_codes(ws[j] >> 4, d, magic, eight), scaled_codes(ws[j] >> 12, d, magic, eight));
                         }
                     }
                 } else {
@@ -522,13 +552,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                                 if (!seen(8 * j + 2 * c + 1)) two &= 0x0000FFFFu;
                             }
                             const __half2 d = attn::as_half2(two);
+                            top = __hmax2(top, __habs2(d));
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 *reinterpret_cast<unsigned*>(to + (kb * 4 + e) * (STEP * 16) + j * 128) =
-                                    scaled_codes(ws[j] >> (4 * e), d, magic);
+                                    scaled_codes(ws[j] >> (4 * e), d, magic, eight);
                         }
                     }
                 }
+                if (__hgt2_mask(top, __float2half2_rn(MAX_SCALE))) s_large[walked & 1] = walked + 1;
                 fence_async();
                 __syncwarp();
                 if (lane == 0) {
@@ -631,6 +663,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             // ---- the row's output, or its part
             if (ok && n) ok = voted(&o_full, segments & 1);
             fence_after();
+            if (wide || *(volatile unsigned*)&s_large[walked & 1] != walked + 1) {
             const bool uncut = unit == 0 && unit_end == sp.units;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float* part = a.part + (((int64_t)blockIdx.x * 2 + (u != u0)) * BLOCK_ROWS + row - first_row) * attn_part_floats(D);
@@ -649,7 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0;
                 }
-                const float by = uncut ? inv : 1.f;
+                const float by = (uncut ? inv : 1.f) * (wide ? WIDE : 1.f);
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4*>(buf + lane * PITCH + kb * 32 + e) =
@@ -692,6 +725,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             }
             if (!uncut && live) part[D] = ref - LIFT, part[D + 1] = l;
             fence_async();  // the buffers are operands again
+            }
         }
         if (!ok) {
             if (lane == 0) {
@@ -713,27 +747,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
             }
             break;
         }
+        const bool again = !wide && *(volatile unsigned*)&s_large[walked & 1] == walked + 1;
+        steps += n;
+        if (tiles == 2) tile1_steps += n;
+        segments += n > 0;
+        ++walked;
+        if (again) unit = cut ? unit_end - counts + a.start : 0;
+        if constexpr (TURNS_BACK) {
+            wide = again;
+            if (again) continue;
+        } else if (again) {
+            if (tid == 0) s_place = Place{entry, head, unit, u, steps, segments, tile1_steps, walked};
+            __syncthreads();
+            return true;
+        }
         if (cut && tid == 0 && unit == 0) {
             const bool uncut = unit_end == sp.units;
             const int first = (int)blockIdx.x, last = uncut ? first - 1 : shares.cta_of(u + counts + sp.units - unit_end - 1);
             a.meta[(int64_t)entry * a.kv_heads + head] = AttnMeta{first, last, u != u0, 0};
         }
-        steps += n;
-        if (tiles == 2) tile1_steps += n;
-        segments += n > 0;
-        ++walked;
         u += counts;
         unit = 0;
         if (++head == a.kv_heads) head = 0, ++entry;
         if (!cut) break;
     }
+    return false;
     };
     if (warp < SOFTMAX_WARPS) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-        walk(std::true_type{});
+        if (walk(std::true_type{}, std::false_type{})) walk(std::true_type{}, std::true_type{});
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-        walk(std::false_type{});
+        if (walk(std::false_type{}, std::false_type{})) walk(std::false_type{}, std::true_type{});
     }
     __syncthreads();
     if (warp == WARP_MMA)

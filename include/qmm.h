@@ -767,8 +767,6 @@ QMM_API qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream);
  * Scores, softmax statistics and sums are fp32.  The products carry 22 bits
  * of q and of the weights (fp32), q as it is and 22 bits of the weights (fp16),
  * or 11 of both (bf16).
- * (bf16 calls of many queries multiply k and v as fp16: values of the cache
- * beyond 65504 in magnitude are outside their domain.)
  * out.data may be NULL when yq and yd are given: Q8_0 of the fp32 output
  * (int8 [T][q.n_heads * head_dim], uint16 [T][q.n_heads * head_dim / 32]; as
  * qmm_quantize_q8_0, the O product's operand).  out has q's n_heads and type.

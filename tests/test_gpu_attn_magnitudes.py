@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 from parity import lib
-from test_gpu_attn import Case
+from test_gpu_attn import MAY_GROW, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,21 @@ def test_a_long_diffuse_softmax_over_scales_around_two():
     c = Case(qmm, lens, [1], 2, 1, 64, 256, "f32", seed=2, scale=0.02,
              cache_scale=_scales(lens, 256, 64, lambda shape: np.full(shape, 3.0)))
     c.check(c.run())
+
+
+@pytest.mark.parametrize("top", [6000.0, 60000.0])
+@pytest.mark.parametrize("max_kv", [None, MAY_GROW])
+@pytest.mark.parametrize("lens,nqs,Hq,Hkv,D", [([300, 128], [64, 64], 4, 1, 64), ([700, 0, 90], [130, 5, 90], 2, 1, 128),
+                                               ([2000], [64], 2, 1, 32)])
+def test_values_beyond_fp16(top, max_kv, lens, nqs, Hq, Hkv, D):
+    """Cached values d q above 65504 (d itself is fp16), in some records or all, in calls of few and of many keys."""
+    qmm = lib()
+    rng = np.random.default_rng(len(lens))
+    for share in (0.02, 1.0):
+        def draw(shape):
+            return np.where(rng.random(shape[:3] + (1,)) < share, top, 0.5) * np.ones(shape)
+        s = _scales(lens, 64, D, draw)
+        s[..., :D] = draw(s.shape)[..., :D]
+        c = Case(qmm, lens, nqs, Hq, Hkv, D, 64, "bf16", seed=D, q_start=True, scale=0.3 / top,
+                 extra_kv=0 if max_kv is None else max_kv // 64, cache_scale=s)
+        c.check(c.run(**({} if max_kv is None else {"max_kv": max_kv})))
