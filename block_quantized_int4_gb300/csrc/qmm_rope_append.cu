@@ -146,19 +146,20 @@ struct Places {
 };
 
 // The bits of a lane's eight values; loaded by themselves, so that several
-// heads' loads are on their way before the first is used.
+// heads' loads are on their way before the first is used.  Plain loads: heads may
+// be rotated in place, and what a launch writes must not be read as constant.
 template <int DT, bool PAIRS>
 struct Raw {
     using Run = typename std::conditional<DT == QMM_F32, uint4, uint2>::type;
     Run a, b;
     __device__ void load(const char* head, int a0, int b0) {
         if constexpr (DT != QMM_F32 && PAIRS) {  // one run of 16 bytes
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(head + a0 * 2));
+            const uint4 v = *reinterpret_cast<const uint4*>(head + a0 * 2);
             a = make_uint2(v.x, v.y), b = make_uint2(v.z, v.w);
         } else {
             constexpr int size = DT == QMM_F32 ? 4 : 2;
-            a = __ldg(reinterpret_cast<const Run*>(head + a0 * size));
-            b = __ldg(reinterpret_cast<const Run*>(head + b0 * size));
+            a = *reinterpret_cast<const Run*>(head + a0 * size);
+            b = *reinterpret_cast<const Run*>(head + b0 * size);
         }
     }
     __device__ void values(float* x) const {
