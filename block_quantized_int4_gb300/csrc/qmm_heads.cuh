@@ -123,11 +123,30 @@ inline qmm_status check_heads(const qmm_heads& h, int n_heads) {
     return QMM_OK;
 }
 
+// Whether two of the T * n_heads rows of D values share places.  Nested layouts
+// (all heads of a token before the next token's, or the other way round) are seen
+// at once; else j steps of one stride are compared with the steps of the other on
+// both sides of them.
+inline bool rows_overlap(const qmm_heads& h, int64_t T, int D) {
+    using wide = __int128;
+    const wide n[2] = {T, h.n_heads}, s[2] = {h.token_stride, h.head_stride};
+    for (int i = 0; i < 2; ++i)
+        if (n[i] > 1 && s[i] < D) return true;
+    const int few = n[0] < n[1] ? 0 : 1, many = 1 - few;
+    if (n[few] <= 1 || (n[few] - 1) * s[few] + D <= s[many] || (n[many] - 1) * s[many] + D <= s[few]) return false;
+    if (n[few] > 1 << 17) return true;  // more rows than a launch takes
+    for (wide j = 1; j < n[few]; ++j) {
+        const wide at = j * s[few], k = at / s[many];
+        if (k >= 1 && k < n[many] && at - k * s[many] < D) return true;
+        if (k + 1 < n[many] && (k + 1) * s[many] - at < D) return true;
+    }
+    return false;
+}
+
 // The same for heads that are written: rows of D values that do not overlap.
 inline qmm_status check_output(const qmm_heads& h, int n_heads, int64_t T, int D) {
     if (qmm_status s = check_heads(h, n_heads)) return s;
-    if ((h.n_heads > 1 && h.head_stride < D) || (T > 1 && h.token_stride < D)) return QMM_ERR_SHAPE;
-    return QMM_OK;
+    return rows_overlap(h, T, D) ? QMM_ERR_SHAPE : QMM_OK;
 }
 
 inline Heads kernel_heads(const qmm_heads& h) {

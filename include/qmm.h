@@ -625,8 +625,9 @@ typedef enum qmm_dtype { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
 
 /* Heads of T tokens: value e of head h of token t is element
  * t * token_stride + h * head_stride + e of data, of type dtype.  Any
- * strides; data aligned to its element (loads are wide where the strides and
- * the address allow them). */
+ * strides, but rows of an output must not share places (QMM_ERR_SHAPE); data
+ * aligned to its element (loads are wide where the strides and the address
+ * allow them). */
 typedef struct qmm_heads {
     void*   data;
     int64_t token_stride;

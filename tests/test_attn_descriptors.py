@@ -38,3 +38,32 @@ def test_page_tables_stay_inside_their_storage(qmm):
         for b in range(B):
             at = pages.data_ptr() + 4 * b * op.pages_stride
             assert at == pages[b].data_ptr(), (tuple(pages.shape), pages.stride())
+
+
+def _status(qmm, T, H, ts, hs, D=64):
+    """qmm_rope_heads into heads of these strides (addresses are never read: no device, or turned down before)."""
+    import ctypes
+    x = qmm.Heads(0x10000, H * D, D, H, 0)
+    op = qmm.RopeOp(x, qmm.Heads(0x10000, ts, hs, H, 0), qmm.Rope(), None, None, T, D, 1e-5)
+    return qmm.library_handle().qmm_rope_heads(ctypes.byref(op), None)
+
+
+def test_rows_of_an_output_that_overlap_are_turned_down(qmm):
+    """Against all pairs of rows, each D values long."""
+    D = 64
+    seen = set()
+    for T in (1, 2, 3, 4, 7):
+        for H in (1, 2, 3, 5):
+            for ts in (0, 32, 64, 96, 128, 192, 320, 448):
+                for hs in (0, 32, 64, 80, 128, 192, 256, 64 * 7):
+                    at = sorted(t * ts + h * hs for t in range(T) for h in range(H))
+                    overlap = any(b - a < D for a, b in zip(at, at[1:]))
+                    seen.add(overlap)
+                    if overlap:
+                        assert _status(qmm, T, H, ts, hs) == 2, (T, H, ts, hs)
+                    elif not torch.cuda.is_available():
+                        assert _status(qmm, T, H, ts, hs) == 4, (T, H, ts, hs)
+    assert seen == {True, False}
+    if not torch.cuda.is_available():
+        assert _status(qmm, 5, 3, 1 << 62, 64) == 4 and _status(qmm, 5, 3, 64, 1 << 62) == 4  # no product overflows
+    assert _status(qmm, 40, 1 << 20, 64, 64) == 2
