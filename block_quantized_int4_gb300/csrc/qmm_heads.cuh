@@ -14,6 +14,9 @@ namespace qmm {
 
 constexpr int MAX_HEAD = 256;  // largest head size
 constexpr int GROUP = 32;      // tokens of a cache record
+constexpr int MAX_HEADS = 1 << 24;                // heads of an argument, tokens of a call and
+constexpr int64_t MAX_TOKENS = int64_t(1) << 31;  // records of a cache, so that no product of
+constexpr int64_t MAX_RECORDS = INT32_MAX;        // sizes leaves the kernels' indexes
 
 inline int dtype_size(int dtype) { return dtype == QMM_F32 ? 4 : 2; }
 
@@ -118,7 +121,7 @@ __device__ __forceinline__ void storen(char* p, int64_t i, int dtype, int wide, 
 inline qmm_status check_heads(const qmm_heads& h, int n_heads) {
     if (h.dtype != QMM_F32 && h.dtype != QMM_F16 && h.dtype != QMM_BF16) return QMM_ERR_ARG;
     if (!h.data || h.n_heads <= 0 || h.token_stride < 0 || h.head_stride < 0) return QMM_ERR_ARG;
-    if (n_heads && h.n_heads != n_heads) return QMM_ERR_SHAPE;
+    if ((n_heads && h.n_heads != n_heads) || h.n_heads > MAX_HEADS) return QMM_ERR_SHAPE;
     if (reinterpret_cast<uintptr_t>(h.data) % dtype_size(h.dtype)) return QMM_ERR_ALIGN;
     return QMM_OK;
 }
@@ -162,6 +165,7 @@ inline qmm_status check_cache(const qmm_kv_cache& c, bool data) {
     if (c.n_pages < 0 || c.page_size <= 0 || c.n_heads <= 0) return QMM_ERR_ARG;
     if (c.page_size % GROUP || c.page_size > 1 << 20 || c.n_heads > 1 << 16 || !valid_head_dim(c.head_dim))
         return QMM_ERR_SHAPE;
+    if ((int64_t)c.n_pages * c.n_heads * (c.page_size / GROUP) > MAX_RECORDS) return QMM_ERR_SHAPE;
     if (data && !c.data) return QMM_ERR_ARG;
     if (data && reinterpret_cast<uintptr_t>(c.data) % 16) return QMM_ERR_ALIGN;
     return QMM_OK;

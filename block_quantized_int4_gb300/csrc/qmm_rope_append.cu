@@ -642,7 +642,7 @@ qmm_status qmm_rope_table(float* table, int64_t n_pos, int32_t n_rot, double bas
 
 qmm_status qmm_rope_heads(const qmm_rope_op* op, void* stream) {
     if (!op || op->T < 0) return QMM_ERR_ARG;
-    if (!valid_head_dim(op->head_dim)) return QMM_ERR_SHAPE;
+    if (!valid_head_dim(op->head_dim) || op->T > MAX_TOKENS) return QMM_ERR_SHAPE;
     if (op->T == 0) return QMM_OK;
     if (qmm_status s = check_heads(op->x, 0)) return s;
     if (qmm_status s = check_output(op->y, op->x.n_heads, op->T, op->head_dim)) return s;
@@ -673,6 +673,7 @@ qmm_status qmm_kv_cache_bytes(const qmm_kv_cache* cache, size_t* bytes) {
 
 qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
     if (!op || op->T < 0) return QMM_ERR_ARG;
+    if (op->T > MAX_TOKENS) return QMM_ERR_SHAPE;
     if (qmm_status s = check_cache(op->cache, op->T > 0)) return s;
     if (op->T == 0) return QMM_OK;
     const int D = op->cache.head_dim;
@@ -711,6 +712,7 @@ qmm_status qmm_kv_append_q4_0(const qmm_kv_append_op* op, void* stream) {
 
 qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream) {
     if (!op || op->T < 0) return QMM_ERR_ARG;
+    if (op->T > MAX_TOKENS) return QMM_ERR_SHAPE;
     if (qmm_status s = check_cache(op->cache, op->T > 0)) return s;
     if (op->T == 0 || (!op->k.data && !op->v.data)) return QMM_OK;
     if (op->k.data)

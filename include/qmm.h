@@ -712,7 +712,8 @@ typedef struct qmm_kv_cache {
     int32_t head_dim;
 } qmm_kv_cache;
 
-/* Bytes of cache->data (data itself is not looked at). */
+/* Bytes of cache->data (data itself is not looked at).  A cache has fewer
+ * than 2^31 records (QMM_ERR_SHAPE from every entry that takes one). */
 QMM_API qmm_status qmm_kv_cache_bytes(const qmm_kv_cache* cache, size_t* bytes);
 
 /* Write T tokens into the cache, one launch: k is normalised (k_norm fp32

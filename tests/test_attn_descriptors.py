@@ -67,3 +67,27 @@ def test_rows_of_an_output_that_overlap_are_turned_down(qmm):
     if not torch.cuda.is_available():
         assert _status(qmm, 5, 3, 1 << 62, 64) == 4 and _status(qmm, 5, 3, 64, 1 << 62) == 4  # no product overflows
     assert _status(qmm, 40, 1 << 20, 64, 64) == 2
+
+
+def test_sizes_beyond_the_kernels_indexes_are_turned_down(qmm):
+    """Records are counted in 31 bits on the device and bytes in size_t; products of the sizes must not wrap."""
+    import ctypes
+    lib = qmm.library_handle()
+    out = ctypes.c_size_t(7)
+    for n_pages, page, heads, ok in ((1 << 20, 256, 8, True), ((1 << 31) - 1, 32, 1, True), ((1 << 31) - 1, 32, 2, False),
+                                     (1 << 16, 1 << 20, 1, False), ((1 << 31) - 1, 1 << 20, 1 << 16, False), (0, 1 << 20, 1 << 16, True),
+                                     (1 << 30, 64, 1, False)):
+        c = qmm.KvCache(0x10000, n_pages, page, heads, 256)
+        st = lib.qmm_kv_cache_bytes(ctypes.byref(c), ctypes.byref(out))
+        assert st == (0 if ok else 2), (n_pages, page, heads)
+        if ok:
+            assert out.value == n_pages * heads * (page // 32) * 36 * 256
+    h = lambda n=4: qmm.Heads(0x10000, 1 << 10, 1 << 6, n, 0)  # noqa: E731
+    cache = qmm.KvCache(0x10000, 8, 64, 4, 64)
+    for T in (1 << 33, 1 << 60, 1 << 61, 1 << 62, (1 << 63) - 1):  # T times the warps of a token wraps for most
+        op = qmm.RopeOp(h(), h(), qmm.Rope(), None, None, T, 64, 1e-5)
+        assert lib.qmm_rope_heads(ctypes.byref(op), None) == 2, T
+        op = qmm.KvAppendOp(cache, h(), h(), qmm.Heads(), qmm.Heads(), qmm.Rope(), 0x10000, 0x10000, None, None, T, 1e-5, 0)
+        assert lib.qmm_kv_append_q4_0(ctypes.byref(op), None) == 2, T
+        op = qmm.KvReadOp(cache, h(), h(), 0x10000, T)
+        assert lib.qmm_kv_read_q4_0(ctypes.byref(op), None) == 2, T
