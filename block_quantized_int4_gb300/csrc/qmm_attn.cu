@@ -183,6 +183,17 @@ qmm_status qmm_attn_workspace_size(const qmm_attn_op* op, size_t* bytes) {
     return QMM_OK;
 }
 
+qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* mode) {
+    if (!op || !kernel || !mode) return QMM_ERR_ARG;
+    if (qmm_status s = check(*op, false)) return s;
+    int sms = DEFAULT_SMS, optin = 0;
+    device_facts(&sms, &optin);
+    const Plan p = plan_of(*op, sms);
+    *kernel = p.tc ? QMM_ATTN_KERNEL_TMEM : p.tiles == 2 ? QMM_ATTN_KERNEL_ROWS_16 : QMM_ATTN_KERNEL_ROWS_8;
+    *mode = p.mode;
+    return QMM_OK;
+}
+
 qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream) {
     if (!op) return QMM_ERR_ARG;
     const bool empty = op->n_seqs == 0 || op->T == 0 || op->max_q == 0;

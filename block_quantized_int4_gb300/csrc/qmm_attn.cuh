@@ -70,7 +70,7 @@ constexpr int ATTN_STAGES = 2;  // a warp's records: one in use, one in flight
 // one CTA an item; a cluster of CTAs an item, joined through shared memory; or
 // all units in equal shares, items cut where a share ends and their parts
 // joined by a second kernel.
-enum AttnMode { ATTN_WHOLE = 0, ATTN_CLUSTER = 1, ATTN_CUT = 2 };
+enum AttnMode { ATTN_WHOLE = QMM_ATTN_MODE_WHOLE, ATTN_CLUSTER = QMM_ATTN_MODE_CLUSTER, ATTN_CUT = QMM_ATTN_MODE_CUT };
 
 struct AttnMeta {  // of an item: the CTAs that its units are cut over
     int first, last;  // first > last: not cut

@@ -150,6 +150,7 @@ SIGNATURES = {
     "qmm_kv_read_q4_0": [ctypes.POINTER(KvReadOp), _P],
     "qmm_attn_workspace_size": [ctypes.POINTER(AttnOp), ctypes.POINTER(_SZ)],
     "qmm_attn_q4_0": [ctypes.POINTER(AttnOp), _P],
+    "qmm_debug_attn_plan": [ctypes.POINTER(AttnOp), ctypes.POINTER(_INT), ctypes.POINTER(_INT)],
     "qmm_last_device_error": [_P],
 }
 for _name, _args in SIGNATURES.items():
@@ -604,6 +605,17 @@ def qmm_attn_workspace_size(op) -> int:
 
 def qmm_attn_q4_0(op, stream=None):
     _check(_lib.qmm_attn_q4_0(ctypes.byref(op), _stream(stream)), "qmm_attn_q4_0")
+
+
+ATTN_ROWS_8, ATTN_ROWS_16, ATTN_TMEM = 0, 1, 2
+ATTN_WHOLE, ATTN_CLUSTER, ATTN_CUT = 0, 1, 2
+
+
+def qmm_debug_attn_plan(op):
+    """(kernel, mode) of qmm_attn_q4_0 for this op."""
+    kernel, mode = _INT(0), _INT(0)
+    _check(_lib.qmm_debug_attn_plan(ctypes.byref(op), ctypes.byref(kernel), ctypes.byref(mode)), "qmm_debug_attn_plan")
+    return kernel.value, mode.value
 
 
 def qmm_last_device_error(stream=None) -> int:

@@ -803,6 +803,18 @@ typedef struct qmm_attn_op {
 QMM_API qmm_status qmm_attn_workspace_size(const qmm_attn_op* op, size_t* bytes);
 QMM_API qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream);
 
+/* How qmm_attn_q4_0 would run this op (its pointers are not looked at), for
+ * tests and timing: the kernel, and how the items (a block of rows of a
+ * sequence and key/value head) meet the CTAs.  Without a device the plan is
+ * that of 152 SMs. */
+#define QMM_ATTN_KERNEL_ROWS_8 0   /* warp MMA, blocks of 8 rows               */
+#define QMM_ATTN_KERNEL_ROWS_16 1  /* warp MMA, blocks of 16 rows              */
+#define QMM_ATTN_KERNEL_TMEM 2     /* tcgen05, blocks of 256 rows              */
+#define QMM_ATTN_MODE_WHOLE 0      /* a CTA an item                            */
+#define QMM_ATTN_MODE_CLUSTER 1    /* a cluster of CTAs an item                */
+#define QMM_ATTN_MODE_CUT 2        /* equal shares, joined by a second launch  */
+QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* mode);
+
 /* ---------------------------------------------------------------------
  * Errors raised on the device
  * ------------------------------------------------------------------- */
