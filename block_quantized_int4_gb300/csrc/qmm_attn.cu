@@ -95,7 +95,10 @@ Plan plan_of(const qmm_attn_op& op, int sms) {
         p.mode = ATTN_CUT;
     }
     // shares are counted in 31 bits; that many items fill the device whole, too
-    if (p.mode == ATTN_CUT && p.items * (units + 1 + ATTN_START) >= int64_t(1) << 31) p.mode = ATTN_WHOLE;
+    if (p.mode == ATTN_CUT && p.items * (units + 1 + ATTN_START) >= int64_t(1) << 31) {
+        p.mode = ATTN_WHOLE;
+        p.cluster = 1;
+    }
     if (p.mode == ATTN_CUT) {
         p.ctas = (int)std::min<int64_t>({slots, p.items * units, MAX_CTAS});
         p.start = p.items * units <= slots ? 0 : ATTN_START;
