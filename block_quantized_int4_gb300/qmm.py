@@ -174,9 +174,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object, which costs 3 us a call.  Not part of torch's public
+# interface: where it is missing, the public form serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s):
     if s is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream() costs 3 us
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
