@@ -75,6 +75,8 @@ class AttentionLayer:
         """Cache the keys and values of x [T][hidden] (fp32), the tokens from position 0, and attend over them:
         the attention's output [T][heads][head_dim]."""
         qmm, T = self.qmm, x.shape[0]
+        if T > self.max_len:
+            raise ValueError(f"prefill: {T} tokens, and the cache holds {self.max_len}")
         z = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-5) * self.gamma
         xq, xd = qmm.quantize_q8_0(z.contiguous())
         qkv = torch.cat([qmm.gemm(*self.qkv_w, xq[i:i + 64], xd[i:i + 64]) for i in range(0, T, 64)])
