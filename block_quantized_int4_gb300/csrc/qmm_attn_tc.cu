@@ -8,8 +8,9 @@
 // tcgen05.mma with accumulators in tensor memory:
 //   S = Q K^T   M = 128 rows, N = 128 keys, both operands in shared memory
 //   O += P V    M = 128 rows, N = D, P from tensor memory, V^T from shared
-// Scales meet the codes here (d * (u - 8) rounded to fp16, 2^-12), so this form
-// serves bf16 alone, whose output rounds at 2^-9.
+// Scales meet the codes here (d * (u - 8) rounded to fp16, 2^-12), and weights are
+// fp16, so this form serves bf16 alone, whose output rounds at 2^-9 (error 1.69e-3,
+// of which the output's rounding alone is 1.66e-3).
 //
 // A CTA (one an SM, 24 warps) holds two row tiles of 128 rows and walks the
 // keys in steps of 128 (4 records):
@@ -29,10 +30,13 @@
 // run.  The operands of K and V are double buffered.
 //
 // What bounds it.  509 queries over 8190 tokens, 64 heads on 8 of 128: 161 us,
-// 823 TFLOP/s, 44% of the library's best large product (the warp-MMA kernel:
-// 630 us).  A step of 128 keys takes 3000 cycles: a row's 128 scores pass one
-// thread (read, exponential, packed, written back), and the two tiles' MMAs
-// fill 42% of it, of which S reads both operands from shared memory.
+// 824 TFLOP/s, 44% of the library's best large product (the warp-MMA kernel:
+// 630 us).  128 items on 128 of the 152 SMs; the longest CTA takes 318,000 cycles
+// for its 64 steps of 128 keys, 4970 a step with start and end counted in, and a
+// step is 11,500 warp instructions (softmax, unpacking, polling), 61% of the issue
+// slots of the SMs in use.  A row's 128 scores pass one thread (read, exponential,
+// packed, written back); MMAs fill 42%, of which S reads both operands from shared
+// memory.
 // Steps of 64 keys with S double buffered: 198 to 240 us against 172 then,
 // twice the waits and commits.
 //
