@@ -629,13 +629,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_tc_kernel(const __grid_consta
                                 st16(o_at + 16 * i, x);
                             }
                         }
-                        const __half2 a2 = __float2half2_rn(alpha);
                         wait_st();
                         for (int i = 0; i < q; ++i) {
                             ld16(s_at + 16 * i, x);
                             wait_ld(x);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = attn::as_bits(__hmul2(attn::as_half2(x[e]), a2));
+                            for (int e = 0; e < 16; ++e) {  // in fp32: alpha may be far below fp16's least
+                                const float2 w = attn::mul2(attn::unpack_half(x[e]), make_float2(alpha, alpha));
+                                x[e] = attn::pack_half(w.x, w.y);
+                            }
                             st16(s_at + 16 * i, x);
                         }
                     }

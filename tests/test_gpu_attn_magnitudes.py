@@ -67,3 +67,20 @@ def test_values_beyond_fp16(top, max_kv, lens, nqs, Hq, Hkv, D):
         c = Case(qmm, lens, nqs, Hq, Hkv, D, 64, "bf16", seed=D, q_start=True, scale=0.3 / top,
                  extra_kv=0 if max_kv is None else max_kv // 64, cache_scale=s)
         c.check(c.run(**({} if max_kv is None else {"max_kv": max_kv})))
+
+
+@pytest.mark.parametrize("D", [32, 128])
+@pytest.mark.parametrize("share", [0.1, 1.0])
+def test_values_beyond_fp16_in_whole_items(D, share):
+    """As many items as fill the tensor-memory kernel's CTAs, some with large scales and some without, and no keys."""
+    qmm = lib()
+    rng = np.random.default_rng(D)
+    lens, nqs = [0, 3, 129, 300, 70] * 14, [130, 64, 128, 40, 70] * 14
+    s = _scales(lens, 96, D, lambda shape: np.where(rng.random(shape[:3] + (1,)) < share, 60000.0, 0.5) * np.ones(shape))
+    s[..., :D] = s[..., D:]
+    c = Case(qmm, lens, nqs, 4, 2, D, 96, "bf16", seed=D, q_start=True, scale=0.3 / 60000, cache_scale=s)
+    first = c.run()
+    assert qmm.qmm_debug_attn_plan(c.op(first)) == (qmm.ATTN_TMEM, qmm.ATTN_WHOLE)
+    c.check(first)
+    for _ in range(5):
+        assert np.array_equal(first.float().cpu().numpy(), c.run().float().cpu().numpy())
