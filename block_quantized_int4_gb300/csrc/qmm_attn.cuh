@@ -388,6 +388,8 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, int64_t token, int 
 // keys, scales of v from 0.4 to 2.2: an error of 1.4e-5 with a factor of 2^-7,
 // 2.4e-7 with 2^8).  The rest goes into the scales: upwards below 2^-7, which is exact, and
 // downwards from 2^5 on, which is exact for scales down to 2^-18 of the largest.
+// A weight's parts end at fp16's 2^-25: at 2^-35 of the reference, 2^-30 beside
+// scales of 2^5 and more.
 __device__ __forceinline__ int scale_exponent(int bits) {  // exponent bits of fp16
     return (bits >> 10) - 15 + (bits == 0);                // subnormal scales count as 2^-14
 }

@@ -768,7 +768,8 @@ QMM_API qmm_status qmm_kv_read_q4_0(const qmm_kv_read_op* op, void* stream);
  * it sees, with k and v the cached values d * q; 0 where it sees none.
  * Scores, softmax statistics and sums are fp32.  The products carry 22 bits
  * of q and of the weights (fp32), q as it is and 22 bits of the weights (fp16),
- * or 11 of both (bf16).  Scores beyond 2^26 in magnitude are outside the
+ * or 11 of both (bf16); weights far below a row's largest are kept to 2^-30
+ * of it.  Scores beyond 2^26 in magnitude are outside the
  * domain; a query with a NaN or an infinity gives NaN in its own row alone.
  * out.data may be NULL when yq and yd are given: Q8_0 of the fp32 output
  * (int8 [T][q.n_heads * head_dim], uint16 [T][q.n_heads * head_dim / 32]; as
