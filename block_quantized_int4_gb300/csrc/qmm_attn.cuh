@@ -43,7 +43,9 @@
 // of 35.6 over 131000 tokens, 757 instead of 649 for 509 queries over 8190).  bf16,
 // whose outputs round at 2^-9, takes one, rounded twice (1.67e-3 against 1.65e-3;
 // two parts: 54 us instead of 48 for the sixteen ragged sequences).
-// Sums are fp32 throughout.  Weights times d_v are scaled by the power of two
+// Sums are fp32 throughout, to nearest but for what the tensor core adds up, which
+// truncates: scores over the 32 values of a block, weighted v over 32 keys (fp32,
+// fp16) or over all keys of a warp (bf16).  Weights times d_v are scaled by the power of two
 // that brings the largest d_v so far to 2^9, so they keep their bits whatever
 // the magnitude of v.
 #pragma once
@@ -846,18 +848,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, attn_ctas(NB, NT)) attn_kernel(c
                                                signed_codes<0>(y, magic), signed_codes<1>(y, magic)};
 #pragma unroll
                         for (int r = 0; r < NT; ++r) {
-                            if constexpr (SPLIT) {
+                            if constexpr (DTYPE != QMM_BF16) {
                                 mma_add(t[r], v, bl[r][2 * st], bl[r][2 * st + 1]);
                                 mma_add(t[r], v, b[r][2 * st], b[r][2 * st + 1]);
                             } else {
-                                if constexpr (DTYPE == QMM_F16) mma_add(acc[r][kb][e], v, bl[r][2 * st], bl[r][2 * st + 1]);
                                 mma_add(acc[r][kb][e], v, b[r][2 * st], b[r][2 * st + 1]);
                             }
                         }
                     }
-                    if constexpr (SPLIT) {
+                    if constexpr (DTYPE != QMM_BF16) {
                         // The tensor core truncates its sums: 32 keys at a time, and
-                        // the sums of those rounded to nearest.
+                        // the sums of those rounded to nearest.  (Over 524288 keys of
+                        // a CTA fp16 outputs were 1.5e-4 low, bf16's are 7e-5.)
 #pragma unroll
                         for (int r = 0; r < NT; ++r) {
                             float* o = acc[r][kb][e];

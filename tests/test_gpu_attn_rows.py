@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import attn_reference as R
 from parity import lib
-from test_gpu_attn import MAY_GROW, Case, _np
+from test_gpu_attn import DEV, MAY_GROW, Case, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +48,24 @@ def test_fp16_outputs_are_rounded_once(lens, nqs, Hq, Hkv, D, window):
     out = _np(c.run())
     rounding = np.linalg.norm(ref.astype(np.float16).astype(np.float64) - ref)
     assert np.linalg.norm(out - ref) <= 1.03 * rounding, np.linalg.norm(out - ref) / rounding
+
+
+@pytest.mark.parametrize("dtype,ratio", [(torch.float16, 1.03), (torch.bfloat16, 1.03)])
+def test_long_sums_have_no_drift(dtype, ratio):
+    """524288 keys of one CTA (more sequences than CTAs find room, which share their pages), nearly equal weights: the
+    sum's own error stays far below the output's rounding, as above."""
+    qmm = lib()
+    B, L, D, page, scale = 460, 1 << 19, 32, 256, 0.05
+    small = R.random_cache(L // page, 1, page, D, np.random.default_rng(5))
+    small[..., -4 * D:] = np.abs(small[..., -4 * D:].view(np.float16)).view(np.uint8)
+    K, V = (torch.tensor(x.transpose(1, 0, 2, 3).reshape(L, D), device=DEV) for x in R.cache_values(small, D))
+    q = torch.randn(B, 1, D, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(dtype)
+    out = torch.empty_like(q)
+    pages = torch.arange(L // page, dtype=torch.int32, device=DEV)[None].repeat(B, 1)
+    qmm.qmm_attn_q4_0(qmm.attn_op(qmm.kv_cache(torch.tensor(small, device=DEV), page), q, pages,
+                                  torch.full((B,), L, dtype=torch.int32, device=DEV), out, max_kv=L, scale=scale))
+    ref = torch.softmax(scale * (q.double()[:, 0] @ K.T), -1) @ V
+    rounding = (ref.to(dtype).double() - ref).norm().item()
+    err = (out.double()[:, 0] - ref).norm().item()
+    assert err <= ratio * rounding, err / rounding
+    assert qmm.qmm_last_device_error() == 0
