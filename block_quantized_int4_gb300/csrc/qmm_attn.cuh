@@ -27,7 +27,7 @@
 // warp instructions in bf16 and 700 in fp32, most of them unpacking (LOP3,
 // fp16 adds), 32 and 64 MMAs among them, and 12 warps an SM fill 55% of the
 // issue slots between the fixed latencies of their chains.  131000 tokens take
-// 34 (bf16), 39 (fp16) and 44 us (fp32): 8 us of start, look-ups, q and the second
+// 34 (bf16), 40 (fp16) and 44 us (fp32): 8 us of start, look-ups, q and the second
 // launch's join are not shared among more keys.
 //
 // Precision.  fp32 activations: q' and the weights are two fp16 parts, hi +
@@ -39,8 +39,9 @@
 // from that large a value costs 5 bits (fp32 rows: 4e-6 of the output against
 // 2e-7 from q = u - 8).  A weight times d_v is two fp16 parts, as for fp32: one
 // part, 2^-12, would show beside fp16 outputs, which round at 2^-12 themselves
-// (2.6e-4 of the window case's output, 2.0e-4 with two, which cost 38.9 us instead
-// of 35.6 over 131000 tokens, 757 instead of 649 for 509 queries over 8190).  bf16,
+// (2.6e-4 of the window case's output, 2.0e-4 with two and sums to nearest, which
+// cost 39.6 us instead of 35.6 over 131000 tokens, 783 instead of 649 for 509
+// queries over 8190).  bf16,
 // whose outputs round at 2^-9, takes one, rounded twice (1.67e-3 against 1.65e-3;
 // two parts: 54 us instead of 48 for the sixteen ragged sequences).
 // Sums are fp32 throughout, to nearest but for what the tensor core adds up, which
@@ -131,7 +132,7 @@ __host__ __device__ constexpr int attn_part_floats(int D) { return D + 4; }
 
 // CTAs an SM by registers (launch bound).  One row tile, D = 128, fp32 over
 // 131000 tokens: 48.3 us with 3, 50.7 with 4, which spills.  Two row tiles, 8 x
-// 8 fp16 queries over 4000 tokens, 64 heads of 128: 61.1 with 2, 63.6 with 3; 4 x 5
+// 8 fp16 queries over 4000 tokens, 64 heads of 128: 62.7 with 2, 68.4 with 3; 4 x 5
 // fp32 of 32 heads of 64: 18.2 with 3, 21.3 with 4.
 constexpr int attn_ctas(int NB, int NT) { return NT == 1 ? (NB <= 2 ? 4 : NB <= 4 ? 3 : 2) : NB <= 2 ? 3 : 2; }
 
