@@ -1,0 +1,412 @@
+// qmm_route.cuh -- routing to experts in general form: softmax or sigmoid
+// scores, a bias that enters the choice alone, groups of experts, top-k,
+// renormalised and scaled gates.
+//
+// The choice is that of the scores in 64 bits: c_e = s_e + b_e, the group
+// scores, and equal values to the lower index.  Without a bias c is replaced
+// by the logit (both scores are strictly increasing).  A warp takes a token;
+// each lane holds PER consecutive experts of one group and an ordered 32-bit
+// key of each:
+//  - a logit's own order is exact in 32 bits; c and the sums of two are
+//    computed in fp32, with a bound on their error.  Where two values whose
+//    order decides anything are closer than that bound and not of equal
+//    operands, the token is done again with 64-bit keys (route_slow; about
+//    three tokens in a thousand of sigmoid scores with a bias, 256 experts);
+//  - the k-th largest of the 32 lanes' best keys bounds the k-th largest key
+//    from below, so that only keys from there on are candidates: about 1.3 k
+//    of them, one a lane, each ranked against all others.  (More than 32, as
+//    with most experts switched off: route_slow, too.)
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "qmm_device.cuh"
+#include "qmm_moe_group.cuh"
+#include "qmm_route.h"
+
+namespace qmm {
+namespace route {
+
+constexpr int MAX_K = 64;
+constexpr int WARPS = 8;         // of a block
+constexpr int GROUP_WARPS = 16;  // of the one block that also groups the slots
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Ordered keys.  0: taken or not there; 1: an expert that takes no part.
+__device__ __forceinline__ uint32_t key32(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);  // -0 as +0
+    return max(u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u), 2u);
+}
+__device__ __forceinline__ float value32(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ unsigned long long key64(double v) {
+    const unsigned long long u = __double_as_longlong(v + 0.0);
+    return max(u ^ ((u >> 63) ? ~0ull : 1ull << 63), 2ull);
+}
+
+// What a warp leaves for its gates: the chosen experts in order, one more
+// than k where the choice is checked.
+struct Chosen {
+    uint32_t cand_key[32];
+    int cand_id[32];
+    int id[MAX_K];
+    float key[33];
+};
+
+// Where a lane's experts lie: `count` of them from `first` on.
+struct Place {
+    int first, count, lanes;  // lanes: of a group
+};
+
+__device__ __forceinline__ Place place_of(const RouteArgs& a, int lane) {
+    Place p;
+    p.lanes = 32 / a.n_groups;
+    const int g = lane / p.lanes, at = (lane - g * p.lanes) * a.per;
+    p.first = g * a.group_size + at;
+    p.count = max(0, min(a.per, a.group_size - at));
+    return p;
+}
+
+// A lane's logits as fp32; experts that take no part (-inf, NaN) as -inf.
+template <int PER, typename T>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, const T* row, const Place& p, float (&l)[PER]) {
+    constexpr int BYTES = PER * (int)sizeof(T), V = BYTES < 16 ? BYTES : 16, N = V / (int)sizeof(T);
+    union Vec {
+        T e[N];
+        uint4 q;
+        uint2 d;
+        uint32_t w;
+        unsigned short h;
+    };
+    if (a.vec && p.count == PER) {
+#pragma unroll
+        for (int i = 0; i < PER; i += N) {
+            Vec v;
+            const T* src = row + p.first + i;
+            if constexpr (V == 16) v.q = *reinterpret_cast<const uint4*>(src);
+            if constexpr (V == 8) v.d = *reinterpret_cast<const uint2*>(src);
+            if constexpr (V == 4) v.w = *reinterpret_cast<const uint32_t*>(src);
+            if constexpr (V == 2) v.h = *reinterpret_cast<const unsigned short*>(src);
+#pragma unroll
+            for (int j = 0; j < N; ++j) l[i + j] = as_float(v.e[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) l[i] = i < p.count ? as_float(row[p.first + i]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = l[i] > -INFINITY ? l[i] : -INFINITY;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+// Logits in 64 bits -> score.
+__device__ __forceinline__ double score64(const RouteArgs& a, float l, double top, double sum) {
+    if (!(l > -INFINITY)) return 0.0;
+    return a.softmax ? exp((double)l - top) / sum : 1.0 / (1.0 + exp(-(double)l));
+}
+
+// The whole choice with 64-bit keys, by k rounds over all experts.  Every lane
+// of the warp; leaves the chosen experts in out.id.
+template <int PER, typename T>
+__device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen& out) {
+    const int lane = threadIdx.x & 31;
+    const Place p = place_of(a, lane);
+    float l[PER];
+    load_logits<PER, T>(a, row, p, l);
+    const bool top2 = a.n_groups > 1 && a.top2;
+    double top = -INFINITY, sum = 0.0;
+    if (a.softmax && (a.bias || top2)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = fmax(top, (double)l[i]);
+        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL, top, o));
+        for (int i = 0; i < PER; ++i)
+            if (l[i] > -INFINITY) sum += exp((double)l[i] - top);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    }
+    unsigned long long key[PER];
+    double first = -INFINITY, second = -INFINITY;  // of this lane's group
+    for (int i = 0; i < PER; ++i) {
+        const bool live = l[i] > -INFINITY;
+        double c = l[i];
+        if (live && (a.bias || top2)) {
+            const double s = score64(a, l[i], top, sum), b = a.bias ? (double)a.bias[p.first + i] : 0.0;
+            if (a.bias) c = s + b;
+            const double v = s + b;
+            if (v > first) {
+                second = first;
+                first = v;
+            } else if (v > second) {
+                second = v;
+            }
+        } else if (live) {
+            first = fmax(first, c);
+        }
+        key[i] = i < p.count ? (live ? key64(c) : 1ull) : 0ull;
+    }
+    if (a.n_groups > 1) {
+        for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+            const double f = __shfl_xor_sync(FULL, first, o), s = __shfl_xor_sync(FULL, second, o);
+            second = fmax(fmin(first, f), fmax(second, s));
+            first = fmax(first, f);
+        }
+        const double mine = top2 && second > -INFINITY ? first + second : first;
+        const int g = lane / p.lanes;
+        int before = 0;
+        for (int h = 0; h < a.n_groups; ++h) {
+            const double v = __shfl_sync(FULL, mine, h * p.lanes);
+            before += v > mine || (v == mine && h < g);
+        }
+        if (before >= a.top_groups)
+            for (int i = 0; i < PER; ++i) key[i] = 0;
+    }
+    for (int j = 0; j < a.k; ++j) {
+        unsigned long long best = 0;
+        int at = 0;
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] >= best) {
+                best = key[i];
+                at = i;
+            }
+        unsigned long long most = best;
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(FULL, most, o));
+        const int owner = __ffs(__ballot_sync(FULL, best == most)) - 1;
+        if (lane == owner) {
+            out.id[j] = p.first + at;
+            for (int i = 0; i < PER; ++i)
+                if (i == at) key[i] = 0;
+        }
+    }
+    __syncwarp();
+}
+
+// One token.
+template <int PER, typename T>
+__device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out) {
+    const int lane = threadIdx.x & 31;
+    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
+    const Place p = place_of(a, lane);
+    const bool grouped = a.n_groups > 1, top2 = grouped && a.top2;
+    const bool scores = a.bias || top2;  // scores enter the choice
+    float l[PER];
+    load_logits<PER, T>(a, row, p, l);
+
+    // softmax: the largest logit and the sum of exponentials
+    float top = 0.f, sum = 1.f;
+    if (a.softmax && (scores || !a.renorm)) {
+        float m = l[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+        top = warp_max(m);
+        sum = 0.f;
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) sum += exp2f((l[i] - top) * 1.4426950408889634f);
+        }
+        sum = warp_sum(sum);
+    }
+
+    // keys; and the error that c and group scores may have.  exp2f and the
+    // divisions are off by 2^-21.5 of the largest score at most (an exponent's
+    // rounding, |x| 2^-24, weighs s or s (1 - s), below 0.4 / |x|), softmax by
+    // the sum's own error besides; c by its own rounding.
+    const float unit = a.softmax ? __fdividef(1.f, sum) : 1.f, slack = unit * (a.softmax ? 0x1p-18f : 0x1p-19f);
+    uint32_t key[PER];
+    float first = -INFINITY, second = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool live = l[i] > -INFINITY;
+        float c = l[i];
+        if (scores) {
+            const float e = exp2f((a.softmax ? l[i] - top : -l[i]) * 1.4426950408889634f);
+            const float s = a.softmax ? e * unit : __fdividef(1.f, 1.f + e);
+            const float v = a.bias ? s + (i < p.count ? __ldg(a.bias + p.first + i) : 0.f) : s;
+            if (a.bias) c = v;
+            if (top2) second = fmaxf(second, fminf(first, live ? v : -INFINITY));
+            first = fmaxf(first, live ? v : -INFINITY);
+        } else {
+            first = fmaxf(first, c);
+        }
+        key[i] = i < p.count ? (live ? key32(c) : 1u) : 0u;
+    }
+    bool again = false;
+    if (grouped) {
+        for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+            const float f = __shfl_xor_sync(FULL, first, o);
+            if (top2) {
+                const float s = __shfl_xor_sync(FULL, second, o);
+                second = fmaxf(fminf(first, f), fmaxf(second, s));
+            }
+            first = fmaxf(first, f);
+        }
+        const float mine = top2 && second > -INFINITY ? first + second : first;
+        const int g = lane / p.lanes;
+        int before = 0;
+        for (int h = 0; h < a.n_groups; ++h) {
+            const float v = __shfl_sync(FULL, mine, h * p.lanes);
+            before += v > mine || (v == mine && h < g);
+        }
+        const bool stays = before < a.top_groups;
+        if (scores) {
+            // groups on either side of the border that are too close
+            const uint32_t in = __reduce_min_sync(FULL, stays && g < a.n_groups ? key32(mine) : 0xFFFFFFFFu);
+            const uint32_t no = __reduce_max_sync(FULL, !stays && g < a.n_groups ? key32(mine) : 0u);
+            const float hi = value32(in), lo = no ? value32(no) : -INFINITY;
+            const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
+            again = lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size));
+        }
+        if (!stays) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) key[i] = 0;
+        }
+    }
+
+    // candidates: keys from the n-th best of the lanes' best on (n = k, and one
+    // more where the border is checked)
+    const int n = a.k + (a.bias ? 1 : 0);
+    uint32_t floor_key = 1;
+    if (n <= 32) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+        for (int j = 0; j < n; ++j) {
+            floor_key = __reduce_max_sync(FULL, best);
+            const uint32_t who = __ballot_sync(FULL, best == floor_key);
+            if (lane == __ffs(who) - 1) best = 0;
+        }
+        floor_key = max(floor_key, 1u);
+    }
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mask |= (key[i] >= floor_key ? 1u : 0u) << i;
+    const int have = __popc(mask);
+    int end = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, end, o);
+        if (lane >= o) end += v;
+    }
+    const int total = __shfl_sync(FULL, end, 31);
+    again = again || total > 32;
+    if (!again) {
+        int at = end - have;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if ((mask >> i) & 1u) {
+                out.cand_key[at] = key[i];
+                out.cand_id[at] = p.first + i;
+                ++at;
+            }
+        __syncwarp();
+        // candidates lie in index order: of equal keys the earlier ranks first
+        const uint32_t mine = lane < total ? out.cand_key[lane] : 0u;
+        int rank = 0;
+        for (int d = 0; d < total; ++d) {
+            const uint32_t v = out.cand_key[d];
+            rank += v > mine || (v == mine && d < lane);
+        }
+        if (lane < total && rank < n) {
+            const int e = out.cand_id[lane];
+            if (rank < a.k) out.id[rank] = e;
+            if (a.bias) out.key[rank] = mine > 1 ? value32(mine) : -INFINITY;
+        }
+        __syncwarp();
+        if (a.bias) {
+            // neighbours that are too close, but for equal logits with equal biases
+            // among the chosen (at the border a third may be close to both)
+            const int pairs = min(total, n) - 1;
+            bool close = false;
+            if (lane < pairs) {
+                const float hi = out.key[lane], lo = out.key[lane + 1];
+                if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-22f * (fabsf(hi) + fabsf(lo)))) {
+                    close = true;
+                    if (lane + 1 < a.k) {
+                        const int e = out.id[lane], f = out.id[lane + 1];
+                        close = !(as_float(row[e]) == as_float(row[f]) && a.bias[e] == a.bias[f]);
+                    }
+                }
+            }
+            again = __any_sync(FULL, close);
+        }
+    }
+    if (again) route_slow<PER, T>(a, row, out);
+
+    // gates of the chosen: lane j has the j-th and the (j + 32)-th
+    float lj[2], s[2];
+    int id[2];
+    float most = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int j = lane + 32 * r;
+        id[r] = j < a.k ? out.id[j] : 0;
+        lj[r] = j < a.k ? as_float(row[id[r]]) : -INFINITY;
+        lj[r] = lj[r] > -INFINITY ? lj[r] : -INFINITY;
+        most = fmaxf(most, lj[r]);
+    }
+    if (a.renorm) most = warp_max(most);
+    // renormalised, softmax needs no sum over all; neither do sigmoids that
+    // are e^l to the last bit (below e^-30), whose quotients fp32 would lose
+    const bool exps = a.softmax || (a.renorm && most < -30.f);
+    const float ref = a.renorm ? most : a.softmax ? top : 0.f;
+    float part = 0.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        s[r] = lj[r] > -INFINITY ? (exps ? expf(lj[r] - ref) : 1.f / (1.f + expf(-lj[r]))) : 0.f;
+        part += s[r];
+    }
+    float div = a.softmax ? sum : 1.f;
+    if (a.renorm) div = warp_sum(part);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int j = lane + 32 * r;
+        if (j < a.k) {
+            a.ids[(int64_t)t * a.k + j] = id[r];
+            a.gates[(int64_t)t * a.k + j] = s[r] > 0.f ? s[r] / div * a.scale : 0.f;
+        }
+    }
+    __syncwarp();  // out is written again for the next token
+}
+
+template <int PER, typename T, bool GROUP>
+__global__ void __launch_bounds__(GROUP ? GROUP_WARPS * 32 : WARPS * 32) route_kernel(const __grid_constant__ RouteArgs a, MoeWs ws,
+                                                                                           int* err) {
+    // launched after the kernel that writes the logits, possibly early
+    // (programmatic dependent launch): nothing is read before it completes
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int NW = GROUP ? GROUP_WARPS : WARPS;
+    __shared__ Chosen chosen[NW];
+    const int warp = threadIdx.x >> 5;
+    for (int64_t t = (int64_t)blockIdx.x * NW + warp; t < a.T; t += (int64_t)gridDim.x * NW)
+        route_one<PER, T>(a, (int)t, chosen[warp]);
+    if constexpr (GROUP) {
+        __syncthreads();
+        moe_group_block(a.ids, a.T * a.k, a.n_groups * a.group_size, ws, err);
+    }
+}
+
+// The kernels of one type, by the experts of a lane (1, 2, 4, .. 32).
+template <typename T>
+RouteKernel kernel_of(int slot, bool group) {
+    static constexpr RouteKernel plain[6] = {route_kernel<1, T, false>,  route_kernel<2, T, false>,
+                                             route_kernel<4, T, false>,  route_kernel<8, T, false>,
+                                             route_kernel<16, T, false>, route_kernel<32, T, false>};
+    static constexpr RouteKernel grouping[6] = {route_kernel<1, T, true>,  route_kernel<2, T, true>,
+                                                route_kernel<4, T, true>,  route_kernel<8, T, true>,
+                                                route_kernel<16, T, true>, route_kernel<32, T, true>};
+    return group ? grouping[slot] : plain[slot];
+}
+
+}  // namespace route
+}  // namespace qmm

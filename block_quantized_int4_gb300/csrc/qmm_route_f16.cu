@@ -1,0 +1,8 @@
+// qmm_route_f16.cu -- routing to experts, f16 logits.
+#include "qmm_route.cuh"
+
+namespace qmm {
+
+RouteKernel route_kernel_f16(int slot, bool group) { return route::kernel_of<__half>(slot, group); }
+
+}  // namespace qmm

@@ -103,6 +103,16 @@ class AttnOp(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class MoeRouteOp(ctypes.Structure):
+    """qmm_moe_route_op of include/qmm.h."""
+    _fields_ = [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("gates", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 # name -> argtypes (the trailing stream is a void*)
 SIGNATURES = {
     "qmm_quantize_q4_0": [_P, _I64, _I64, _I64, _P, _P, _P],
@@ -124,6 +134,7 @@ SIGNATURES = {
     "qmm_moe_gemv": [_P, _P, _I32, _I64, _I64, _P, _I32, _I32, _P, _P, _INT, _P, _P, _SZ, _P],
     "qmm_moe_gemv_static": [_P, _P, _I32, _I64, _I64, _P, _I32, _I32, _P, _P, _INT, _P, _P],
     "qmm_moe_combine": [_P, _P, _I32, _I32, _I64, _P, _P],
+    "qmm_moe_route": [ctypes.POINTER(MoeRouteOp), _P],
     "qmm_moe_router_topk": [_P, _I32, _I32, _I32, _P, _P, _P, _SZ, _P],
     "qmm_moe_layer_f32": [_P, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "qmm_quantize_rowwise": [_P, _I64, _I64, _I64, _I32, _P, _P, _P],
@@ -458,9 +469,42 @@ def qmm_moe_combine(z, gates, T, k, N, y, stream=None):
     _check(_lib.qmm_moe_combine(_ptr(z), _ptr(gates), T, k, N, _ptr(y), _stream(stream)), "qmm_moe_combine")
 
 
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+ROUTE_GROUP_MAX, ROUTE_GROUP_TOP2 = 0, 1
+
+
+def moe_route_op(logits, ids, gates, bias=None, score=ROUTE_SIGMOID, n_groups=1, top_groups=1,
+                 group_score=ROUTE_GROUP_MAX, renormalize=True, scale=1.0, workspace=None):
+    """A qmm_moe_route_op; logits [T][E] of fp32, fp16 or bf16 with contiguous rows' values, ids int32 and gates
+    fp32 [T][k].  The op holds its tensors."""
+    T, E, ld = _rows(logits, "moe_route_op: logits")
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("moe_route_op: ids is [T][k]")
+    k = ids.shape[1]
+    op = MoeRouteOp(logits.data_ptr(), ld, _ptr(_plain(bias, torch.float32, (E,), "bias")),
+                    _ptr(_plain(ids, torch.int32, (T, k), "ids")), _ptr(_plain(gates, torch.float32, (T, k), "gates")),
+                    _DTYPES[logits.dtype], T, E, k, score, n_groups, top_groups, group_score, int(bool(renormalize)),
+                    scale, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    op._keep = (logits, ids, gates, bias, workspace)
+    return op
+
+
+def qmm_moe_route(op, stream=None):
+    _check(_lib.qmm_moe_route(ctypes.byref(op), _stream(stream)), "qmm_moe_route")
+
+
 # ------------------------------------------------------------------ attention over a 4-bit paged cache
 ROPE_PLAIN, ROPE_LINEAR, ROPE_RAMP = 0, 1, 2
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _rows(t, what):
+    """(rows, values of a row, row stride) of a tensor [rows][values] with contiguous values."""
+    if t.dim() != 2 or t.dtype not in _DTYPES or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: [rows][values] of fp32, fp16 or bf16 with contiguous values, got "
+                         f"{tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    # the stride of one row alone means nothing
+    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def heads(t):

@@ -486,6 +486,56 @@ QMM_API qmm_status qmm_moe_layer_f32(const float* logits, int32_t T, int32_t E, 
                                      int64_t H, int64_t F, const float* x, int32_t* ids, float* gates, float* h,
                                      float* z, float* y, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Routing in general form: scores by softmax or sigmoid, a bias for balance,
+ * groups of experts, gates as the model has them (qmm_moe_router_topk is the
+ * form with fp32 logits, sigmoid scores and renormalised gates). */
+typedef enum qmm_route_score { QMM_ROUTE_SOFTMAX = 0, QMM_ROUTE_SIGMOID = 1 } qmm_route_score;
+typedef enum qmm_route_group {
+    QMM_ROUTE_GROUP_MAX = 0, /* a group's score is its largest c              */
+    QMM_ROUTE_GROUP_TOP2 = 1 /* the sum of its two largest (of one: that one) */
+} qmm_route_group;
+
+/* For each token t < T, with l = logits[t * ld .. + E) of type dtype
+ * (qmm_dtype; ld >= E elements):
+ *   s_e = 1 / (1 + exp(-l_e)), or exp(l_e) / sum_i exp(l_i);
+ *   c_e = s_e + bias[e] (bias fp32 [E]; without one c orders as l does);
+ *   the E / n_groups experts from g E / n_groups on are group g; the
+ *     top_groups groups of largest score stay;
+ *   ids[t][0..k-1]: their k experts of largest c, in decreasing order;
+ *   gates[t][j] = scale * s_{ids[t][j]}, divided by the sum of the k chosen s
+ *     with renormalize != 0; fp32.
+ * The choice is that of c and of the groups' scores in 64 bits; equal ones go
+ * to the lower index.  An expert whose logit is -inf (or NaN) takes no part:
+ * s_e = 0, it adds nothing to a group's score, and it comes after all others
+ * (by index) where k asks for more than there are.  With softmax, +inf is
+ * outside the domain, as are biases that are not finite: ids are then some
+ * experts, gates have no meaning.  n_groups is a power of two up to 32 that
+ * divides E (1: no groups), 1 <= top_groups <= n_groups, E <=
+ * QMM_ROUTER_MAX_EXPERTS, 1 <= k <= QMM_ROUTER_MAX_K and k <= top_groups * E /
+ * n_groups, else QMM_ERR_SHAPE.  ids int32 [T][k], gates fp32 [T][k].
+ * workspace: NULL, or at least qmm_moe_workspace_size(E, T, k) bytes, 16-byte
+ * aligned, any contents: the chosen slots are then grouped by expert there as
+ * by qmm_moe_group_ids, for qmm_moe_gemv_pregrouped and its kind (T * k <=
+ * 2^24).  T == 0 is a no-op. */
+typedef struct qmm_moe_route_op {
+    const void* logits;
+    int64_t ld;
+    const float* bias;
+    int32_t* ids;
+    float* gates;
+    int32_t dtype;
+    int32_t T, E, k;
+    int32_t score;
+    int32_t n_groups;
+    int32_t top_groups;
+    int32_t group_score;
+    int32_t renormalize;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+} qmm_moe_route_op;
+QMM_API qmm_status qmm_moe_route(const qmm_moe_route_op* op, void* stream);
+
 /* ---------------------------------------------------------------------
  * Expert hot-store (Colibri page, "Arquitectura del Sistema": a
  * least-recently-used cache of experts per layer, an optional hot store in
