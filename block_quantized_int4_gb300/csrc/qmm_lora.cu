@@ -1,0 +1,149 @@
+// qmm_lora.cu -- qmm_lora on the host: argument checks and the launch.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "qmm.h"
+#include "qmm_internal.h"
+#include "qmm_lora.h"
+
+namespace qmm {
+namespace {
+
+bool off(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+size_t size_of(int dtype) { return dtype == QMM_F32 ? 4 : 2; }
+
+bool known(int dtype) { return dtype == QMM_F32 || dtype == QMM_F16 || dtype == QMM_BF16; }
+
+// Rows of a matrix start on `bytes` boundaries.
+bool even(const void* p, int64_t stride, size_t size, size_t bytes) {
+    return !off(p, bytes) && (stride * size) % bytes == 0;
+}
+
+qmm_status check(const qmm_lora_op& op) {
+    if (op.T < 0 || op.N <= 0 || op.n_segs < 0 || op.n_adapters <= 0 || op.max_rank <= 0) return QMM_ERR_ARG;
+    if (!known(op.x_dtype) || !known(op.w_dtype) || !known(op.y_dtype)) return QMM_ERR_ARG;
+    if (op.ldx < op.K || op.lda < op.K || op.ldb < op.max_rank || op.a_stride < 0 || op.b_stride < 0 ||
+        op.ldy < op.N || (op.base && op.ld_base < op.N))
+        return QMM_ERR_ARG;
+    const int64_t far = int64_t(1) << 40;
+    if (op.K <= 0 || op.K % LORA_CHUNK || op.K > 1 << 24 || op.N > 1 << 28 || op.T > 1 << 28 || op.n_segs > 1 << 16 ||
+        op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > far || op.ldb > far || op.a_stride > far ||
+        op.b_stride > far || op.ldy > far || op.ld_base > far)
+        return QMM_ERR_SHAPE;
+    if (!op.seg_start && op.n_segs && (op.T % op.n_segs || op.T / op.n_segs > 1 << 28)) return QMM_ERR_SHAPE;
+    if (op.T == 0 || op.n_segs == 0) return QMM_OK;
+    if (!op.x || !op.a || !op.b || !op.y || !op.seg_adapter) return QMM_ERR_ARG;
+    if (op.base == op.y && op.ld_base != op.ldy && op.T > 1) return QMM_ERR_SHAPE;  // in place: one stride
+    const size_t xs = size_of(op.x_dtype), ws = size_of(op.w_dtype), ys = size_of(op.y_dtype);
+    if (!even(op.x, op.T > 1 ? op.ldx : 0, xs, 16) || !even(op.a, op.lda, ws, 16) || (op.a_stride * ws) % 16 ||
+        off(op.b, ws) || off(op.y, ys) || off(op.base, ys) || off(op.ranks, 4) || off(op.scales, 4) ||
+        off(op.seg_start, 4) || off(op.seg_adapter, 4))
+        return QMM_ERR_ALIGN;
+    return QMM_OK;
+}
+
+LoraKernel kernel_of(int x, int w, bool low) {
+    if (x == QMM_F32)
+        return w == QMM_F32 ? lora_kernel_f32_f32(low) : w == QMM_F16 ? lora_kernel_f32_f16(low) : lora_kernel_f32_bf16(low);
+    if (x == QMM_F16)
+        return w == QMM_F32 ? lora_kernel_f16_f32(low) : w == QMM_F16 ? lora_kernel_f16_f16(low) : lora_kernel_f16_bf16(low);
+    return w == QMM_F32 ? lora_kernel_bf16_f32(low) : w == QMM_F16 ? lora_kernel_bf16_f16(low) : lora_kernel_bf16_bf16(low);
+}
+
+// Opts a kernel into the device's shared memory and clusters of 16, once a device.
+bool prepared(LoraKernel k, int kind, int optin) {
+    static std::mutex mu;
+    static bool done[64][18];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    std::lock_guard<std::mutex> lk(mu);
+    bool& d = done[dev][kind];
+    if (!d)
+        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 1024) == cudaSuccess &&
+            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    if (!d) cudaGetLastError();
+    return d;
+}
+
+}  // namespace
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
+    if (!op) return QMM_ERR_ARG;
+    if (qmm_status s = check(*op)) return s;
+    if (op->T == 0 || op->n_segs == 0) return QMM_OK;
+    int sms = 0, optin = 0;
+    if (!device_facts(&sms, &optin)) return QMM_ERR_DEVICE;
+    LoraArgs a = {};
+    a.x = op->x;
+    a.a = op->a;
+    a.b = op->b;
+    a.base = op->base;
+    a.y = op->y;
+    a.ldx = op->ldx;
+    a.lda = op->lda;
+    a.a_stride = op->a_stride;
+    a.ldb = op->ldb;
+    a.b_stride = op->b_stride;
+    a.ld_base = op->ld_base;
+    a.ldy = op->ldy;
+    a.ranks = op->ranks;
+    a.scales = op->scales;
+    a.seg_start = op->seg_start;
+    a.seg_adapter = op->seg_adapter;
+    a.T = op->T;
+    a.N = (int)op->N;
+    a.K = (int)op->K;
+    a.n_segs = op->n_segs;
+    a.seg_rows = (int)(op->T / op->n_segs);
+    a.n_adapters = op->n_adapters;
+    a.max_rank = op->max_rank;
+    a.y_type = op->y_dtype;
+    a.err = device_error_word();
+    const bool low = op->max_rank <= 16;
+    const size_t ws = size_of(op->w_dtype), ys = size_of(op->y_dtype), lane = (low ? 4 : 8) * ws;
+    a.vec_b = even(op->b, op->ldb, ws, std::min<size_t>(16, lane)) && (op->b_stride * ws) % std::min<size_t>(16, lane) == 0;
+    a.vec_y = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16);
+    a.vec_base = op->base && even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16);
+    // Tiles: of each segment's rows, the last one short.
+    const int64_t rows = op->seg_start ? op->T : a.seg_rows;
+    const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / LORA_ROWS)
+                                        : op->n_segs * ((rows + LORA_ROWS - 1) / LORA_ROWS);
+    const int mtiles = (int)(std::min<int64_t>(rows, LORA_ROWS) + 15) / 16;
+    int64_t c = tiles * 8 <= 2 * (int64_t)sms ? 8 : 4;
+    while (c > 1 && c * 2 > op->K / LORA_CHUNK) c /= 2;
+    a.cluster = (int)c;
+    // Shared memory: the parts of h for the largest split that a tile may take,
+    // and its fragments.
+    const int room = lora_rank_room(op->max_rank);
+    size_t part = 0;
+    for (int rg = 1; rg <= (room + 63) / 64; ++rg)
+        part = std::max(part, (size_t)std::max(8 / rg, mtiles) * 16 * (std::min(room, 64 * rg) + 8) * 4);
+    a.frag_at = (int)part;
+    const size_t smem = part + (size_t)mtiles * 16 * room * lora_frag_bytes(op->x_dtype, op->w_dtype);
+    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, low);
+    if (!prepared(kernel, (op->x_dtype * 3 + op->w_dtype) * 2 + low, optin)) return QMM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * c));
+    cfg.blockDim = dim3(LORA_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)c;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return QMM_ERR_CUDA;
+    }
+    return QMM_OK;
+}

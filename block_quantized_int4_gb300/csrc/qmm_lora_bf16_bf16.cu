@@ -1,0 +1,10 @@
+// qmm_lora_bf16_bf16.cu -- low-rank adapters, bf16 rows and bf16 adapters.
+#include "qmm_lora.cuh"
+
+namespace qmm {
+
+LoraKernel lora_kernel_bf16_bf16(bool low) {
+    return low ? lora::lora_kernel<__nv_bfloat16, __nv_bfloat16, true> : lora::lora_kernel<__nv_bfloat16, __nv_bfloat16, false>;
+}
+
+}  // namespace qmm

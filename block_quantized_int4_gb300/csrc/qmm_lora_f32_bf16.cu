@@ -1,0 +1,10 @@
+// qmm_lora_f32_bf16.cu -- low-rank adapters, f32 rows and bf16 adapters.
+#include "qmm_lora.cuh"
+
+namespace qmm {
+
+LoraKernel lora_kernel_f32_bf16(bool low) {
+    return low ? lora::lora_kernel<float, __nv_bfloat16, true> : lora::lora_kernel<float, __nv_bfloat16, false>;
+}
+
+}  // namespace qmm

@@ -113,6 +113,18 @@ class MoeRouteOp(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class LoraOp(ctypes.Structure):
+    """qmm_lora_op of include/qmm.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("base", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("a_stride", ctypes.c_int64), ("ldb", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("ld_base", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ranks", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("seg_start", ctypes.c_void_p), ("seg_adapter", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("n_segs", ctypes.c_int32),
+                ("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
+
+
 # name -> argtypes (the trailing stream is a void*)
 SIGNATURES = {
     "qmm_quantize_q4_0": [_P, _I64, _I64, _I64, _P, _P, _P],
@@ -162,6 +174,7 @@ SIGNATURES = {
     "qmm_attn_workspace_size": [ctypes.POINTER(AttnOp), ctypes.POINTER(_SZ)],
     "qmm_attn_q4_0": [ctypes.POINTER(AttnOp), _P],
     "qmm_debug_attn_plan": [ctypes.POINTER(AttnOp), ctypes.POINTER(_INT), ctypes.POINTER(_INT)],
+    "qmm_lora": [ctypes.POINTER(LoraOp), _P],
     "qmm_last_device_error": [_P],
 }
 for _name, _args in SIGNATURES.items():
@@ -667,6 +680,42 @@ def qmm_debug_attn_plan(op):
     kernel, mode = _INT(0), _INT(0)
     _check(_lib.qmm_debug_attn_plan(ctypes.byref(op), ctypes.byref(kernel), ctypes.byref(mode)), "qmm_debug_attn_plan")
     return kernel.value, mode.value
+
+
+# ------------------------------------------------------------------ low-rank adapters
+def lora_op(x, a, b, y, seg_adapter, base=None, seg_start=None, ranks=None, scales=None):
+    """A qmm_lora_op; x [T][K], base and y [T][N], a [n_adapters][max_rank][K], b [n_adapters][N][max_rank],
+    seg_adapter int32 [n_segs], seg_start int32 [n_segs + 1] (None: segments of T / n_segs rows).  Every row's values
+    are contiguous.  The op holds its tensors."""
+    T, K, ldx = _rows(x, "lora_op: x")
+    Ty, N, ldy = _rows(y, "lora_op: y")
+    ld_base = 0
+    if base is not None:
+        _same(base, y, "lora_op: base and y")
+        ld_base = _rows(base, "lora_op: base")[2]
+        if base.dtype != y.dtype:
+            raise ValueError("lora_op: base has y's type")
+    for w in (a, b):
+        if w.dim() != 3 or w.dtype not in _DTYPES or (w.shape[2] > 1 and w.stride(2) != 1):
+            raise ValueError("lora_op: adapters are [n_adapters][rows][values] of fp32, fp16 or bf16 with contiguous "
+                             "values")
+    n, r = a.shape[:2]
+    if Ty != T or a.shape[2] != K or tuple(b.shape) != (n, N, r) or a.dtype != b.dtype or seg_adapter.dim() != 1:
+        raise ValueError(f"lora_op: x {tuple(x.shape)}, a {tuple(a.shape)} {a.dtype}, b {tuple(b.shape)} {b.dtype} and "
+                         f"y {tuple(y.shape)} do not go together")
+    S = seg_adapter.shape[0]
+    op = LoraOp(_ptr(x), _ptr(a), _ptr(b), _ptr(base), _ptr(y), ldx, a.stride(1) if r > 1 else K,
+                a.stride(0) if n > 1 else 0, b.stride(1) if N > 1 else r, b.stride(0) if n > 1 else 0, ld_base, ldy,
+                _ptr(_plain(ranks, torch.int32, (n,), "ranks")), _ptr(_plain(scales, torch.float32, (n,), "scales")),
+                _ptr(_plain(seg_start, torch.int32, (S + 1,), "seg_start")),
+                _ptr(_plain(seg_adapter, torch.int32, (S,), "seg_adapter")), T, N, K, S, n, r, _DTYPES[x.dtype],
+                _DTYPES[a.dtype], _DTYPES[y.dtype])
+    op._keep = (x, a, b, y, seg_adapter, base, seg_start, ranks, scales)
+    return op
+
+
+def qmm_lora(op, stream=None):
+    _check(_lib.qmm_lora(ctypes.byref(op), _stream(stream)), "qmm_lora")
 
 
 def qmm_last_device_error(stream=None) -> int:

@@ -868,6 +868,69 @@ QMM_API qmm_status qmm_attn_q4_0(const qmm_attn_op* op, void* stream);
 QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* mode);
 
 /* ---------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection
+ * ------------------------------------------------------------------- */
+
+#define QMM_LORA_MAX_RANK 256
+
+/* y[t] = base[t] + scales[a] * B_a (A_a x[t]) for the T rows of a batch: the
+ * adapters' part of a projection whose shared weights are multiplied by
+ * qmm_gemm_q4_0_q8_0 or its kind (base is its output; y may be base).
+ *  - Rows are in segments: segment i is rows [seg_start[i], seg_start[i + 1])
+ *    (int32 [n_segs + 1]), or with seg_start NULL rows [i L, (i + 1) L) with L =
+ *    T / n_segs (n_segs divides T; n_segs == T: a token of each request).
+ *    Its rows use adapter seg_adapter[i] (int32 [n_segs]), or none with -1: y
+ *    is base there (0 without a base).  Rows in no segment are left as they
+ *    are.  Segments next to one another may use the same adapter; rows of one
+ *    adapter in one segment share its reads.
+ *  - x [T][K], row stride ldx, type x_dtype (qmm_dtype); base (or NULL) and y
+ *    [T][N], row strides ld_base and ldy, type y_dtype; strides in elements.
+ *    y may be base (with its stride), else it overlaps no input.
+ *  - Adapters, type w_dtype: A_a is [max_rank][K] at a + i * a_stride, row
+ *    stride lda, B_a is [N][max_rank] at b + i * b_stride, row stride ldb >=
+ *    max_rank, i = the adapter's number.  ranks (int32 [n_adapters], or NULL:
+ *    max_rank) gives each its own rank r <= max_rank: of A_a only the first r
+ *    rows, of B_a only the first r columns are read.  scales: fp32
+ *    [n_adapters], or NULL (1).
+ *  - A x is held in fp32, and both products' sums are fp32; 16-bit x and
+ *    adapters enter as they are, fp32 ones and A x to 2^-23 of a value (A x to
+ *    2^-18 where x, the adapters and y are all bf16).  y is rounded once.  A row
+ *    of x with a NaN or an infinity gives non-finite values in its own row
+ *    alone.
+ * K % 32 == 0, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
+ * else QMM_ERR_SHAPE.  x and a: 16-byte aligned, ldx, lda and a_stride
+ * multiples of 16 bytes, else QMM_ERR_ALIGN; b, base and y: aligned to their
+ * element (16-byte aligned rows are faster).  Device values out of range set
+ * the device error word (QMM_ERR_BAD_INDEX): seg_start is brought into [0, T]
+ * and into order, an adapter outside [-1, n_adapters) counts as -1, a rank
+ * outside [0, max_rank] as the nearer end.  T == 0 or n_segs == 0 is a no-op.
+ * One launch, no workspace. */
+typedef struct qmm_lora_op {
+    const void* x;
+    const void* a;
+    const void* b;
+    const void* base;
+    void* y;
+    int64_t ldx;
+    int64_t lda, a_stride;
+    int64_t ldb, b_stride;
+    int64_t ld_base;
+    int64_t ldy;
+    const int32_t* ranks;
+    const float* scales;
+    const int32_t* seg_start;
+    const int32_t* seg_adapter;
+    int64_t T, N, K;
+    int32_t n_segs;
+    int32_t n_adapters;
+    int32_t max_rank;
+    int32_t x_dtype;
+    int32_t w_dtype;
+    int32_t y_dtype;
+} qmm_lora_op;
+QMM_API qmm_status qmm_lora(const qmm_lora_op* op, void* stream);
+
+/* ---------------------------------------------------------------------
  * Errors raised on the device
  * ------------------------------------------------------------------- */
 
