@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <mutex>
 
 #include "qmm.h"
@@ -24,13 +25,14 @@ bool even(const void* p, int64_t stride, size_t size, size_t bytes) {
 
 qmm_status check(const qmm_lora_op& op) {
     if (op.T < 0 || op.N <= 0 || op.n_segs < 0 || op.n_adapters <= 0 || op.max_rank <= 0) return QMM_ERR_ARG;
-    if (!known(op.x_dtype) || !known(op.w_dtype) || !known(op.y_dtype)) return QMM_ERR_ARG;
+    if (!known(op.x_dtype) || !known(op.w_dtype) || (op.y_dtype != op.x_dtype && op.y_dtype != QMM_F32))
+        return QMM_ERR_ARG;
     if (op.ldx < op.K || op.lda < op.K || op.ldb < op.max_rank || op.a_stride < 0 || op.b_stride < 0 ||
         op.ldy < op.N || (op.base && op.ld_base < op.N))
         return QMM_ERR_ARG;
     const int64_t far = int64_t(1) << 40;
     if (op.K <= 0 || op.K % LORA_CHUNK || op.K > 1 << 24 || op.N > 1 << 28 || op.T > 1 << 28 || op.n_segs > 1 << 16 ||
-        op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > far || op.ldb > far || op.a_stride > far ||
+        op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > 1 << 24 || op.ldb > far || op.a_stride > far ||
         op.b_stride > far || op.ldy > far || op.ld_base > far)
         return QMM_ERR_SHAPE;
     if (!op.seg_start && op.n_segs && (op.T % op.n_segs || op.T / op.n_segs > 1 << 28)) return QMM_ERR_SHAPE;
@@ -45,18 +47,19 @@ qmm_status check(const qmm_lora_op& op) {
     return QMM_OK;
 }
 
-LoraKernel kernel_of(int x, int w, bool low) {
-    if (x == QMM_F32)
-        return w == QMM_F32 ? lora_kernel_f32_f32(low) : w == QMM_F16 ? lora_kernel_f32_f16(low) : lora_kernel_f32_bf16(low);
-    if (x == QMM_F16)
-        return w == QMM_F32 ? lora_kernel_f16_f32(low) : w == QMM_F16 ? lora_kernel_f16_f16(low) : lora_kernel_f16_bf16(low);
-    return w == QMM_F32 ? lora_kernel_bf16_f32(low) : w == QMM_F16 ? lora_kernel_bf16_f16(low) : lora_kernel_bf16_bf16(low);
+LoraKernel kernel_of(int x, int w, bool f32, bool low) {
+    static LoraKernel (*const kernels[3][3])(bool, bool) = {
+        {lora_kernel_f32_f32, lora_kernel_f32_f16, lora_kernel_f32_bf16},
+        {lora_kernel_f16_f32, lora_kernel_f16_f16, lora_kernel_f16_bf16},
+        {lora_kernel_bf16_f32, lora_kernel_bf16_f16, lora_kernel_bf16_bf16}};
+    static_assert(QMM_F32 == 0 && QMM_F16 == 1 && QMM_BF16 == 2, "the order of the types");
+    return kernels[x][w](f32, low);
 }
 
 // Opts a kernel into the device's shared memory and clusters of 16, once a device.
 bool prepared(LoraKernel k, int kind, int optin) {
     static std::mutex mu;
-    static bool done[64][18];
+    static bool done[64][36];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
@@ -103,31 +106,38 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.seg_rows = (int)(op->T / op->n_segs);
     a.n_adapters = op->n_adapters;
     a.max_rank = op->max_rank;
-    a.y_type = op->y_dtype;
     a.err = device_error_word();
-    const bool low = op->max_rank <= 16;
-    const size_t ws = size_of(op->w_dtype), ys = size_of(op->y_dtype), lane = (low ? 4 : 8) * ws;
-    a.vec_b = even(op->b, op->ldb, ws, std::min<size_t>(16, lane)) && (op->b_stride * ws) % std::min<size_t>(16, lane) == 0;
+    const bool low = op->max_rank <= 16, f32 = op->y_dtype == QMM_F32;
+    const int room = lora_rank_room(op->max_rank);
+    const size_t ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
+    a.vec_b = even(op->b, op->ldb, ws, 16) && (op->b_stride * ws) % 16 == 0;
     a.vec_y = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16);
     a.vec_base = op->base && even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16);
     // Tiles: of each segment's rows, the last one short.
+    a.tile_rows = room > 128 ? 32 : 64;
     const int64_t rows = op->seg_start ? op->T : a.seg_rows;
-    const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / LORA_ROWS)
-                                        : op->n_segs * ((rows + LORA_ROWS - 1) / LORA_ROWS);
-    const int mtiles = (int)(std::min<int64_t>(rows, LORA_ROWS) + 15) / 16;
+    const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / a.tile_rows)
+                                        : op->n_segs * ((rows + a.tile_rows - 1) / a.tile_rows);
+    const int mtiles = (int)(std::min<int64_t>(rows, a.tile_rows) + 15) / 16;
     int64_t c = tiles * 8 <= 2 * (int64_t)sms ? 8 : 4;
+    if (const char* e = getenv("QMM_LORA_C")) c = atoi(e);
     while (c > 1 && c * 2 > op->K / LORA_CHUNK) c /= 2;
-    a.cluster = (int)c;
+    while ((1 << a.cluster_shift) < c) ++a.cluster_shift;
     // Shared memory: the parts of h for the largest split that a tile may take,
-    // and its fragments.
-    const int room = lora_rank_room(op->max_rank);
-    size_t part = 0;
-    for (int rg = 1; rg <= (room + 63) / 64; ++rg)
-        part = std::max(part, (size_t)std::max(8 / rg, mtiles) * 16 * (std::min(room, 64 * rg) + 8) * 4);
-    a.frag_at = (int)part;
-    const size_t smem = part + (size_t)mtiles * 16 * room * lora_frag_bytes(op->x_dtype, op->w_dtype);
-    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, low);
-    if (!prepared(kernel, (op->x_dtype * 3 + op->w_dtype) * 2 + low, optin)) return QMM_ERR_CUDA;
+    // its fragments, and the ring of columns: two CTAs an SM, unless two of the
+    // smallest stages do not fit.
+    int part = 0;
+    for (int rg = 1; rg <= (room + LORA_GROUP_RANKS - 1) / LORA_GROUP_RANKS; ++rg)
+        part = std::max(part, std::max(8 / rg, mtiles) * 16 * (std::min(room, LORA_GROUP_RANKS * rg) + 8) * 4);
+    a.frag_at = part;
+    a.ring_at = (part + mtiles * 16 * room * lora_frag_bytes(op->w_dtype) + 127) / 128 * 128;
+    const int stage = 32 * (room * (int)ws + (a.vec_base ? mtiles * 16 * (int)ys : 0));
+    int tot = low ? 72 : 110;
+    if (const char* e = getenv("QMM_LORA_SMEM")) tot = atoi(e);
+    a.ring_bytes = std::max(tot * 1024 - a.ring_at, 2 * stage);
+    const size_t smem = a.ring_at + a.ring_bytes;
+    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, low);
+    if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 2 + low, optin)) return QMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c));
     cfg.blockDim = dim3(LORA_THREADS);

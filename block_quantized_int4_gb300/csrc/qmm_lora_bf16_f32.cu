@@ -3,8 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_bf16_f32(bool low) {
-    return low ? lora::lora_kernel<__nv_bfloat16, float, true> : lora::lora_kernel<__nv_bfloat16, float, false>;
-}
+LoraKernel lora_kernel_bf16_f32(bool f32, bool low) { return lora::kernel_of<__nv_bfloat16, float>(f32, low); }
 
 }  // namespace qmm

@@ -3,8 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f16_f32(bool low) {
-    return low ? lora::lora_kernel<__half, float, true> : lora::lora_kernel<__half, float, false>;
-}
+LoraKernel lora_kernel_f16_f32(bool f32, bool low) { return lora::kernel_of<__half, float>(f32, low); }
 
 }  // namespace qmm

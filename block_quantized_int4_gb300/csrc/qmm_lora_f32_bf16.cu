@@ -3,8 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_bf16(bool low) {
-    return low ? lora::lora_kernel<float, __nv_bfloat16, true> : lora::lora_kernel<float, __nv_bfloat16, false>;
-}
+LoraKernel lora_kernel_f32_bf16(bool f32, bool low) { return lora::kernel_of<float, __nv_bfloat16>(f32, low); }
 
 }  // namespace qmm

@@ -3,8 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_f16(bool low) {
-    return low ? lora::lora_kernel<float, __half, true> : lora::lora_kernel<float, __half, false>;
-}
+LoraKernel lora_kernel_f32_f16(bool f32, bool low) { return lora::kernel_of<float, __half>(f32, low); }
 
 }  // namespace qmm

@@ -3,8 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_f32(bool low) {
-    return low ? lora::lora_kernel<float, float, true> : lora::lora_kernel<float, float, false>;
-}
+LoraKernel lora_kernel_f32_f32(bool f32, bool low) { return lora::kernel_of<float, float>(f32, low); }
 
 }  // namespace qmm

@@ -884,8 +884,9 @@ QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* 
  *    are.  Segments next to one another may use the same adapter; rows of one
  *    adapter in one segment share its reads.
  *  - x [T][K], row stride ldx, type x_dtype (qmm_dtype); base (or NULL) and y
- *    [T][N], row strides ld_base and ldy, type y_dtype; strides in elements.
- *    y may be base (with its stride), else it overlaps no input.
+ *    [T][N], row strides ld_base and ldy, type y_dtype (x_dtype or QMM_F32, else
+ *    QMM_ERR_ARG); strides in elements.  y may be base (with its stride), else
+ *    it overlaps no input.
  *  - Adapters, type w_dtype: A_a is [max_rank][K] at a + i * a_stride, row
  *    stride lda, B_a is [N][max_rank] at b + i * b_stride, row stride ldb >=
  *    max_rank, i = the adapter's number.  ranks (int32 [n_adapters], or NULL:
@@ -894,10 +895,9 @@ QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* 
  *    [n_adapters], or NULL (1).
  *  - A x is held in fp32, and both products' sums are fp32; 16-bit x and
  *    adapters enter as they are, fp32 ones and A x to 2^-23 of a value (A x to
- *    2^-18 where x, the adapters and y are all bf16).  y is rounded once.  A row
- *    of x with a NaN or an infinity gives non-finite values in its own row
- *    alone.
- * K % 32 == 0, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
+ *    2^-18 with bf16 adapters and 16-bit y).  y is rounded once.  A row of x with
+ *    a NaN or an infinity gives non-finite values in its own row alone.
+ * K % 32 == 0, lda <= 2^24, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
  * else QMM_ERR_SHAPE.  x and a: 16-byte aligned, ldx, lda and a_stride
  * multiples of 16 bytes, else QMM_ERR_ALIGN; b, base and y: aligned to their
  * element (16-byte aligned rows are faster).  Device values out of range set

@@ -30,13 +30,13 @@ def test_refusals(qmm):
     assert _call(qmm, T=0) == 0 and _call(qmm, n_segs=0) == 0
     assert _call(qmm, T=0, x=None, a=None, b=None, y=None, base=None, seg_adapter=None) == 0
     for bad in ({"T": -1}, {"N": 0}, {"n_segs": -1}, {"n_adapters": 0}, {"max_rank": 0}, {"x_dtype": 3},
-                {"w_dtype": -1}, {"y_dtype": 3}, {"ldx": 63}, {"lda": 32}, {"ldb": 7}, {"ldy": 39}, {"ld_base": 39},
+                {"w_dtype": -1}, {"y_dtype": 3}, {"y_dtype": 1}, {"y_dtype": 2, "x_dtype": 1}, {"ldx": 63}, {"lda": 32}, {"ldb": 7}, {"ldy": 39}, {"ld_base": 39},
                 {"a_stride": -8}, {"b_stride": -8}, {"x": None}, {"a": None}, {"b": None}, {"y": None},
                 {"seg_adapter": None}):
         assert _call(qmm, **bad) == 1, bad
     for bad in ({"K": 0}, {"K": 48}, {"K": 1 << 25, "ldx": 1 << 25, "lda": 1 << 25}, {"max_rank": 257, "ldb": 257},
                 {"T": 7}, {"n_segs": 65537, "T": 65537}, {"T": (1 << 28) + 1, "n_segs": 1}, {"N": 1 << 29, "ldy": 1 << 29, "ld_base": 1 << 29},
-                {"ldx": 1 << 41}, {"b_stride": 1 << 41}, {"ld_base": 48}):
+                {"ldx": 1 << 41}, {"lda": (1 << 24) + 32}, {"b_stride": 1 << 41}, {"ld_base": 48}):
         assert _call(qmm, **bad) == 2, bad
     for bad in ({"x": A16 + 8}, {"ldx": 66}, {"a": A16 + 8}, {"lda": 68}, {"a_stride": 516}, {"b": A16 + 1},
                 {"y": A16 + 2, "base": None}, {"base": A16 + 2}, {"ranks": A16 + 2}, {"scales": A16 + 2},
