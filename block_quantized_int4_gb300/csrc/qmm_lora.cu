@@ -111,8 +111,8 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int room = lora_rank_room(op->max_rank);
     const size_t ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
     a.vec_b = even(op->b, op->ldb, ws, 16) && (op->b_stride * ws) % 16 == 0;
-    a.vec_y = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16);
     a.vec_base = op->base && even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16);
+    a.vec_out = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16) && (a.vec_base || !op->base);
     // Tiles: of each segment's rows, the last one short.
     a.tile_rows = room > 128 ? 32 : 64;
     const int64_t rows = op->seg_start ? op->T : a.seg_rows;

@@ -127,14 +127,7 @@ __device__ __forceinline__ Raw<T> zero_raw() {
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = make_uint4(0, 0, 0, 0);
     return r;
 }
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p) {
-    Raw<T> r;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
-    return r;
-}
-// Of these, x's: every value is read once.
+// x and base: every value is read once.
 template <typename T>
 __device__ __forceinline__ Raw<T> stream_raw(const T* p) {
     Raw<T> r;
@@ -146,6 +139,19 @@ __device__ __forceinline__ Raw<T> stream_raw(const T* p) {
                      : "l"(reinterpret_cast<const uint4*>(p) + i));
     }
     return r;
+}
+
+// The same where `in` is true.
+template <typename T>
+__device__ __forceinline__ void load_raw_if(Raw<T>& r, const T* p, bool in) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        uint4& q = r.q[i];
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)
+            : "l"(reinterpret_cast<const uint4*>(p) + i), "r"((int)in));
+    }
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& q, int i) {
@@ -329,34 +335,17 @@ struct Eight {
     float v[8];
 };
 
-// Fewer than eight of them, or not on a 16-byte boundary.
+// The end of a row, or what does not lie on 16-byte boundaries: y = e (+ base).
 template <typename Y>
-__device__ __noinline__ Eight load_plain(const Y* p, int n) {
-    Eight e;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e.v[j] = j < n ? as_float(p[j]) : 0.f;
-    return e;
-}
-template <typename Y>
-__device__ __noinline__ void store_plain(Y* p, int n, Eight e) {
+__device__ __noinline__ void finish_plain(Y* p, const Y* base, int n, Eight e) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        if (j < n) put(p + j, e.v[j]);
+        if (j < n) put(p + j, base ? as_float(base[j]) + e.v[j] : e.v[j]);
 }
 
 template <typename Y>
-__device__ __forceinline__ Eight eight(const Raw<Y>& r) {
-    Eight e;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e.v[j] = value(r, j);
-    return e;
-}
-
-template <typename Y>
-__device__ __forceinline__ void store_eight(Y* p, int n, bool vec, const Eight& e) {
-    if (!vec || n < 8) {
-        store_plain(p, n, e);
-    } else if constexpr (sizeof(Y) == 4) {
+__device__ __forceinline__ void store_eight(Y* p, const Eight& e) {
+    if constexpr (sizeof(Y) == 4) {
         reinterpret_cast<float4*>(p)[0] = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
         reinterpret_cast<float4*>(p)[1] = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
     } else if constexpr (std::is_same<Y, __half>::value) {
@@ -495,7 +484,7 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
     constexpr int RC = LOW ? 16 : 32;            // ranks of a chunk
     constexpr int MPC = BF ? RC / 16 : RC / 8;   // MMAs of a chunk
     constexpr int PARTS = BF ? 3 : 2;            // of a value of h (the third of bf16 for fp32 outputs alone)
-    constexpr int AHEAD = T::wide_x ? 2 : 4;     // chunks of x that are loaded at a time
+    constexpr int AHEAD = T::wide_x ? 1 : 2;     // chunks of x that are loaded before the ones in use
     constexpr int ys = sizeof(Y);
     const Y* base = static_cast<const Y*>(a.base);
     Y* y = static_cast<Y*>(a.y);
@@ -514,7 +503,7 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
     const int mtiles = (t.rows + 15) >> 4;
     const int N = a.N, blocks = (N + 31) / 32;  // of 32 columns
     const int nb0 = (int)(blocks * cta >> cs), nb1 = (int)(blocks * (cta + 1) >> cs);  // N <= 2^28, C <= 16: 32 bits do
-    const bool vec_y = a.vec_y, vec_base = a.vec_base;
+    const bool vec_base = a.vec_base;
 
     int rank = 0;
     if (t.adapter >= 0) {
@@ -527,22 +516,27 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
         if (a.y == a.base) return;
         for (int r = 0; r < t.rows; ++r)
             for (int n = nb0 * 32 + threadIdx.x * 8; n < min(N, nb1 * 32); n += LORA_THREADS * 8) {
-                Eight e = {};
-                if (vec_base && n + 8 <= N)
-                    e = eight(stream_raw(base + (t.row + r) * a.ld_base + n));
-                else if (base)
-                    e = load_plain(base + (t.row + r) * a.ld_base + n, N - n);
-                store_eight(y + (t.row + r) * a.ldy + n, N - n, vec_y, e);
+                Y* to = y + (t.row + r) * a.ldy + n;
+                const Y* from = base ? base + (t.row + r) * a.ld_base + n : nullptr;
+                const Eight e = {};
+                if (!a.vec_out || n + 8 > N) {
+                    finish_plain(to, from, N - n, e);
+                } else {
+                    const Raw<Y> v = from ? stream_raw(from) : zero_raw<Y>();
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(Y) / 2; ++i) reinterpret_cast<uint4*>(to)[i] = v.q[i];
+                }
             }
         return;
     }
 
-    // The columns' copies start now: a stage has as many 32-column blocks as
-    // there are warps beside each other on 16 rows, or as many as fit.
+    // The columns' copies start now: a stage has two 32-column blocks for each
+    // of the warps beside each other on 16 rows, or fewer where three stages of
+    // them do not fit.
     const int room = (rank + RC - 1) / RC * RC;      // ranks of h, the last of them zeros
     const int mshift = mtiles > 2 ? 2 : mtiles - 1;  // 1, 2 or 4 warps take the rows of a block
     const int b_units = room * (int)sizeof(W) / 16;
-    int bshift = 3 - mshift, depth, base_at, stage_bytes;
+    int bshift = 4 - mshift, depth, base_at, stage_bytes;
     for (;; --bshift) {
         base_at = (32 * b_units * 16) << bshift;
         stage_bytes = base_at + (vec_base ? (mtiles * 16 * 32 * ys) << bshift : 0);
@@ -583,26 +577,36 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
             const bool two = t.rows > mt * 16 + 8;
             const X* x0 = static_cast<const X*>(a.x) + (t.row + min(r0, t.rows - 1)) * a.ldx + 8 * c;
             const X* x1 = static_cast<const X*>(a.x) + (t.row + min(r0 + 8, t.rows - 1)) * a.ldx + 8 * c;
-            uint32_t w_at[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) w_at[j] = (uint32_t)(min(rr + 8 * j + g, rank - 1) * a.lda + 8 * c);
+            const W* w0 = wa + (int64_t)(rr + g) * a.lda + 8 * c;
+            // rows of A up to a multiple of 8, as far as there are any, are read
+            const int w_rows = min((rank + 7) & ~7, a.max_rank) - rr - g;
             float acc[NT][4] = {};
+            Raw<W> w[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) w[j] = zero_raw<W>();
+            Raw<X> v0[AHEAD], v1[AHEAD], n0[AHEAD], n1[AHEAD];
+            const int last = max(0, c1 - 1) * LORA_CHUNK;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int at = min((c0 + i) * LORA_CHUNK, last);
+                n0[i] = stream_raw(x0 + at);
+                n1[i] = two ? stream_raw(x1 + at) : n0[i];
+            }
             for (int ch = c0; ch < c1; ch += AHEAD) {
-                Raw<X> v0[AHEAD], v1[AHEAD];
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int at = min(ch + i, c1 - 1) * LORA_CHUNK;
-                    v0[i] = stream_raw(x0 + at);
-                    v1[i] = two ? stream_raw(x1 + at) : v0[i];
+                    v0[i] = n0[i];
+                    v1[i] = n1[i];
+                    const int at = min((ch + AHEAD + i) * LORA_CHUNK, last);
+                    n0[i] = stream_raw(x0 + at);
+                    n1[i] = two ? stream_raw(x1 + at) : n0[i];
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
                     if (ch + i >= c1) break;
-                    const W* wc = wa + (ch + i) * LORA_CHUNK;
-                    Raw<W> w[NT];
+                    const W* wc = w0 + (ch + i) * LORA_CHUNK;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        if (j < nt) w[j] = load_raw(wc + w_at[j]);
+                    for (int j = 0; j < NT; ++j) load_raw_if(w[j], wc + 8 * j * a.lda, 8 * j < w_rows);
                     uint32_t o0[T::words], o1[T::words];
                     operand<X, W>(v0[i], o0);
                     operand<X, W>(v1[i], o1);
@@ -697,58 +701,66 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
     // 3. the columns, stage by stage; a warp takes 16 rows of a 32-column block.
     // Column q of MMA block i is column 8 (q / 2) + 2 i + q % 2 of the 32, so
     // that lane c of a row gets columns 8 c .. 8 c + 7.
-    const int mt = warp & ((1 << mshift) - 1), wb = warp >> mshift, r0 = mt * 16 + g;
-    const bool here = mt < mtiles && wb < nblk, in0 = r0 < t.rows, in1 = r0 + 8 < t.rows;
+    const int mt = warp & ((1 << mshift) - 1), wb = warp >> mshift, r0 = mt * 16 + g, beside = WARPS >> mshift;
+    const bool in0 = r0 < t.rows, in1 = r0 + 8 < t.rows;
     uint32_t frag = smem_u32(smem) + a.frag_at + (mt * chunks * MPC * PARTS * 32 + lane) * 16;
-    const uint32_t b_swz = swizzle(g, b_units, sizeof(W) == 4) * 16;
+    const uint32_t b_swz = swizzle(g, b_units, sizeof(W) == 4) * 16, b_two = 2 * b_units * 16;
     uint32_t b_lane = (wb * 32 + 8 * (g >> 1) + (g & 1)) * b_units * 16;
     const int across = per * ys / 16;
     const uint32_t base_swz = swizzle(g, across, ys == 4) * 16;
     uint32_t base_lane = base_at + r0 * across * 16 + (wb * 4 + c) * (ys / 2) * 16;
-    Y* y0 = y + (t.row + r0) * a.ldy + first_n + wb * 32 + 8 * c;
-    keep(frag), keep(b_lane), keep(base_lane), keep(y0);
+    int n = first_n + wb * 32 + 8 * c;
+    Y* y0 = y + (t.row + r0) * a.ldy + n;
+    Y* y1 = y0 + 8 * a.ldy;
+    keep(frag), keep(b_lane), keep(base_lane), keep(y0), keep(y1), keep(n);
     const int ahead = depth - 1;
     Fill<W, Y> fill = fill_init<W, Y>(a, b, rank, b_units, first_n + ahead * per, bshift, base_at, t.row, t.rows);
     keep(fill.b), keep(fill.base), keep(fill.b_dst), keep(fill.base_dst), keep(fill.col), keep(fill.b_bytes);
     keep(fill.row), keep(fill.at);
     int slot = 0;
-    for (int st = 0; st < stages; ++st, y0 += per) {
+    for (int st = 0; st < stages; ++st) {
         copies_wait(depth - 2);
         __syncthreads();
         if (st + ahead < stages) {
-            const int n = first_n + (st + ahead) * per;
-            fill_stage(fill, a, b_units, bshift, n, min(per, nb1 * 32 - n), t.rows,
+            const int at = first_n + (st + ahead) * per;
+            fill_stage(fill, a, b_units, bshift, at, min(per, nb1 * 32 - at), t.rows,
                        ring + (slot ? slot - 1 : ahead) * stage_bytes);
         }
         copies_commit();
-        const int n0 = first_n + st * per + wb * 32, n = n0 + 8 * c;
-        if (here && n0 < nb1 * 32) {
+        const int nb = min(nblk, nb1 - nb0 - (st << bshift));  // blocks of this stage
+        for (int blk = mt < mtiles ? wb : nblk; blk < nb; blk += beside) {
             const uint32_t stage = ring + slot * stage_bytes;
+            uint32_t src = stage + b_lane + (blk - wb) * 32 * b_units * 16, f = frag;
             float d[4][4] = {};
-            for (int ch = 0; ch < chunks; ++ch) {
+            for (int ch = 0; ch < chunks; ++ch, f += MPC * PARTS * 512) {
                 Raw<W> w[4];  // LOW: the first half of each
+                if constexpr (!LOW && sizeof(W) == 4) {
+                    const uint32_t u0 = src + ((ch * 128 + c * 32) ^ b_swz), u1 = src + ((ch * 128 + c * 32 + 16) ^ b_swz);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t src = stage + b_lane + 2 * i * b_units * 16;
-                    if constexpr (!LOW && sizeof(W) == 4) {
-                        w[i].q[0] = lds(src + ((ch * 128 + c * 32) ^ b_swz));
-                        w[i].q[1] = lds(src + ((ch * 128 + c * 32 + 16) ^ b_swz));
-                    } else if constexpr (!LOW) {
-                        w[i].q[0] = lds(src + ((ch * 64 + c * 16) ^ b_swz));
-                    } else if constexpr (sizeof(W) == 4) {
-                        w[i].q[0] = lds(src + c * 16);
-                    } else {
-                        const uint2 v = lds64(src + c * 8);
+                    for (int i = 0; i < 4; ++i) {
+                        w[i].q[0] = lds(u0 + i * b_two);
+                        w[i].q[1] = lds(u1 + i * b_two);
+                    }
+                } else if constexpr (!LOW) {
+                    const uint32_t u = src + ((ch * 64 + c * 16) ^ b_swz);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i].q[0] = lds(u + i * b_two);
+                } else if constexpr (sizeof(W) == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i].q[0] = lds(src + c * 16 + i * b_two);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 v = lds64(src + c * 8 + i * b_two);
                         w[i].q[0] = make_uint4(v.x, v.y, 0, 0);
                     }
                 }
 #pragma unroll
                 for (int m = 0; m < MPC; ++m) {
-                    const uint32_t f = frag + (ch * MPC + m) * PARTS * 512;
-                    const uint4 hi = lds(f), lo = lds(f + 512);
+                    const uint4 hi = lds(f + m * PARTS * 512), lo = lds(f + m * PARTS * 512 + 512);
                     if constexpr (BF) {
                         if constexpr (ys == 4) {
-                            const uint4 least = lds(f + 1024);
+                            const uint4 least = lds(f + m * PARTS * 512 + 1024);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mma_bf16(d[i], least.x, least.y, least.z, least.w, m ? w[i].q[0].z : w[i].q[0].x,
@@ -771,27 +783,37 @@ __global__ void __launch_bounds__(LORA_THREADS, LOW ? 3 : 2) lora_kernel(const _
                     }
                 }
             }
+            Eight e0, e1;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!(h ? in1 : in0)) continue;
-                Eight e = {};
-                if (vec_base) {
-                    const uint32_t src = stage + base_lane + h * 8 * across * 16;
-                    Raw<Y> v;
-                    v.q[0] = lds(src ^ base_swz);
-                    if constexpr (ys == 4) v.q[1] = lds((src + 16) ^ base_swz);
-                    e = eight(v);
-                } else if (base) {
-                    e = load_plain(base + (t.row + r0 + 8 * h) * a.ld_base + n, N - n);
+            for (int i = 0; i < 4; ++i) {
+                e0.v[2 * i] = d[i][0], e0.v[2 * i + 1] = d[i][1];
+                e1.v[2 * i] = d[i][2], e1.v[2 * i + 1] = d[i][3];
+            }
+            if (vec_base) {  // of rows that are not there, too: what the stage holds
+                const uint32_t at = stage + base_lane + (blk - wb) * (32 * ys);
+                Raw<Y> v0, v1;
+                v0.q[0] = lds(at ^ base_swz);
+                v1.q[0] = lds((at + 8 * across * 16) ^ base_swz);
+                if constexpr (ys == 4) {
+                    v0.q[1] = lds((at + 16) ^ base_swz);
+                    v1.q[1] = lds((at + 8 * across * 16 + 16) ^ base_swz);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e.v[2 * i] += d[i][2 * h];
-                    e.v[2 * i + 1] += d[i][2 * h + 1];
-                }
-                store_eight(h ? y0 + 8 * a.ldy : y0, N - n, vec_y, e);
+                for (int e = 0; e < 8; ++e) e0.v[e] += value(v0, e), e1.v[e] += value(v1, e);
+            }
+            const int off = (blk - wb) * 32, left = N - n - off;
+            if (a.vec_out && (nb0 + (st << bshift) + blk) * 32 + 32 <= N) {
+                if (in0) store_eight(y0 + off, e0);
+                if (in1) store_eight(y1 + off, e1);
+            } else {
+                const Y* b0 = base && !vec_base ? base + (t.row + r0) * a.ld_base + n + off : nullptr;
+                if (in0) finish_plain(y0 + off, b0, left, e0);
+                if (in1) finish_plain(y1 + off, b0 ? b0 + 8 * a.ld_base : nullptr, left, e1);
             }
         }
+        n += per;
+        y0 += per;
+        y1 += per;
         slot = slot + 1 == depth ? 0 : slot + 1;
     }
 }

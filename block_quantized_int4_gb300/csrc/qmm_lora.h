@@ -22,7 +22,7 @@ struct LoraArgs {
     int N, K, n_segs, seg_rows, n_adapters, max_rank;
     int tile_rows;      // at most
     int cluster_shift;  // of the CTAs of a tile, a power of two
-    int vec_b, vec_y, vec_base;
+    int vec_b, vec_base, vec_out;  // rows on 16-byte boundaries: of B, of base, of y and base (if any)
     int frag_at, ring_at, ring_bytes;  // shared memory: parts of h, its fragments, the columns' ring
     int* err;
 };
