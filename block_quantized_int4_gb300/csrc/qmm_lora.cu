@@ -31,7 +31,7 @@ qmm_status check(const qmm_lora_op& op) {
         op.ldy < op.N || (op.base && op.ld_base < op.N))
         return QMM_ERR_ARG;
     const int64_t far = int64_t(1) << 40;
-    if (op.K <= 0 || op.K % LORA_CHUNK || op.K > 1 << 24 || op.N > 1 << 28 || op.T > 1 << 28 || op.n_segs > 1 << 16 ||
+    if (op.K <= 0 || op.K % 32 || op.K > 1 << 24 || op.N > 1 << 28 || op.T > 1 << 28 || op.n_segs > 1 << 16 ||
         op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > 1 << 24 || op.ldb > far || op.a_stride > far ||
         op.b_stride > far || op.ldy > far || op.ld_base > far)
         return QMM_ERR_SHAPE;
@@ -47,19 +47,19 @@ qmm_status check(const qmm_lora_op& op) {
     return QMM_OK;
 }
 
-LoraKernel kernel_of(int x, int w, bool f32, bool low) {
-    static LoraKernel (*const kernels[3][3])(bool, bool) = {
+LoraKernel kernel_of(int x, int w, bool f32, int tile) {
+    static LoraKernel (*const kernels[3][3])(bool, int) = {
         {lora_kernel_f32_f32, lora_kernel_f32_f16, lora_kernel_f32_bf16},
         {lora_kernel_f16_f32, lora_kernel_f16_f16, lora_kernel_f16_bf16},
         {lora_kernel_bf16_f32, lora_kernel_bf16_f16, lora_kernel_bf16_bf16}};
     static_assert(QMM_F32 == 0 && QMM_F16 == 1 && QMM_BF16 == 2, "the order of the types");
-    return kernels[x][w](f32, low);
+    return kernels[x][w](f32, tile);
 }
 
 // Opts a kernel into the device's shared memory and clusters of 16, once a device.
 bool prepared(LoraKernel k, int kind, int optin) {
     static std::mutex mu;
-    static bool done[64][36];
+    static bool done[64][54];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
@@ -107,9 +107,10 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.n_adapters = op->n_adapters;
     a.max_rank = op->max_rank;
     a.err = device_error_word();
-    const bool low = op->max_rank <= 16, f32 = op->y_dtype == QMM_F32;
-    const int room = lora_rank_room(op->max_rank);
-    const size_t ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
+    const bool f32 = op->y_dtype == QMM_F32;
+    const int tile = op->max_rank <= 16 ? 0 : op->max_rank <= 32 ? 1 : 2, rt = 16 << tile;
+    const int room = (op->max_rank + rt - 1) / rt * rt;
+    const int xs = size_of(op->x_dtype), ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
     a.vec_b = even(op->b, op->ldb, ws, 16) && (op->b_stride * ws) % 16 == 0;
     a.vec_base = op->base && even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16);
     a.vec_out = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16) && (a.vec_base || !op->base);
@@ -118,26 +119,28 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int64_t rows = op->seg_start ? op->T : a.seg_rows;
     const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / a.tile_rows)
                                         : op->n_segs * ((rows + a.tile_rows - 1) / a.tile_rows);
-    const int mtiles = (int)(std::min<int64_t>(rows, a.tile_rows) + 15) / 16;
+    const int tile_rows = (int)std::min<int64_t>(rows, a.tile_rows), mtiles = (tile_rows + 15) / 16;
     int64_t c = tiles * 8 <= 2 * (int64_t)sms ? 8 : 4;
     if (const char* e = getenv("QMM_LORA_C")) c = atoi(e);
-    while (c > 1 && c * 2 > op->K / LORA_CHUNK) c /= 2;
+    while (c > 1 && c * LORA_CHUNK > op->K) c /= 2;
     while ((1 << a.cluster_shift) < c) ++a.cluster_shift;
-    // Shared memory: the parts of h for the largest split that a tile may take,
-    // its fragments, and the ring of columns: two CTAs an SM, unless two of the
-    // smallest stages do not fit.
-    int part = 0;
-    for (int rg = 1; rg <= (room + LORA_GROUP_RANKS - 1) / LORA_GROUP_RANKS; ++rg)
-        part = std::max(part, std::max(8 / rg, mtiles) * 16 * (std::min(room, LORA_GROUP_RANKS * rg) + 8) * 4);
-    a.frag_at = part;
-    a.ring_at = (part + mtiles * 16 * room * lora_frag_bytes(op->w_dtype) + 127) / 128 * 128;
-    const int stage = 32 * (room * (int)ws + (a.vec_base ? mtiles * 16 * (int)ys : 0));
-    int tot = low ? 72 : 110;
-    if (const char* e = getenv("QMM_LORA_SMEM")) tot = atoi(e);
-    a.ring_bytes = std::max(tot * 1024 - a.ring_at, 2 * stage);
-    const size_t smem = a.ring_at + a.ring_bytes;
-    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, low);
-    if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 2 + low, optin)) return QMM_ERR_CUDA;
+    // Shared memory: the parts of h (of 16-row blocks, one to four of a tile's and
+    // four in all at most), its fragments, and the ring.
+    const int m2 = mtiles > 2 ? 4 : mtiles;
+    const int frag = op->w_dtype == QMM_BF16 ? (f32 ? 6 : 4) : 8;
+    a.frag_at = 4 * 16 * (room + 8) * 4;
+    a.ring_at = (a.frag_at + mtiles * 16 * room * frag + 127) / 128 * 128;
+    const int chunk = LORA_CHUNK * (mtiles * 16 * xs + rt * ws);
+    const int block = 32 * (room * ws + (a.vec_base ? tile_rows * ys : 0));
+    int total = tile == 0 ? 72 : 110;
+    if (const char* e = getenv("QMM_LORA_SMEM")) total = atoi(e);
+    const int least = (std::max(chunk, block) + 127) / 128 * 128, most = std::max(4 * chunk, 8 / m2 * block);
+    const int share = (total * 1024 - a.ring_at) / 4 / 128 * 128;
+    a.slot_bytes = std::max(least, std::min(most, share));
+    a.depth = std::max(2, std::min(4, (total * 1024 - a.ring_at) / a.slot_bytes));
+    const size_t smem = a.ring_at + (size_t)a.depth * a.slot_bytes;
+    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, tile);
+    if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 3 + tile, optin)) return QMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c));
     cfg.blockDim = dim3(LORA_THREADS);

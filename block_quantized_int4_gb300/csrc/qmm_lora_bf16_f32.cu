@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_bf16_f32(bool f32, bool low) { return lora::kernel_of<__nv_bfloat16, float>(f32, low); }
+LoraKernel lora_kernel_bf16_f32(bool f32, int tile) { return lora::kernel_of<__nv_bfloat16, float>(f32, tile); }
 
 }  // namespace qmm

@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_bf16(bool f32, bool low) { return lora::kernel_of<float, __nv_bfloat16>(f32, low); }
+LoraKernel lora_kernel_f32_bf16(bool f32, int tile) { return lora::kernel_of<float, __nv_bfloat16>(f32, tile); }
 
 }  // namespace qmm

@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_f16(bool f32, bool low) { return lora::kernel_of<float, __half>(f32, low); }
+LoraKernel lora_kernel_f32_f16(bool f32, int tile) { return lora::kernel_of<float, __half>(f32, tile); }
 
 }  // namespace qmm
