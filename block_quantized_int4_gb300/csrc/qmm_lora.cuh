@@ -42,7 +42,17 @@
 namespace qmm {
 namespace lora {
 
-constexpr int WARPS = LORA_THREADS / 32;
+constexpr int WARPS = 8;               // that multiply; one more copies
+constexpr int THREADS = WARPS * 32;    // of these
+
+// Barriers between the warp that copies and those that multiply, by slot.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+constexpr int BAR_FULL = 1, BAR_EMPTY = 5, BAR_MULTIPLY = 9;  // four of the first two
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -357,10 +367,10 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (threadIdx.x == 0) s_tile[2] = 0;
         int before = 0;
-        for (int s0 = 0; s0 < a.n_segs; s0 += LORA_THREADS) {
+        for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
             const int s = s0 + threadIdx.x;
             int n = 0, first = 0, last = 0;
-            if (s < a.n_segs) {
+            if (s < a.n_segs && threadIdx.x < THREADS) {
                 const int f = a.seg_start[s], l = a.seg_start[s + 1];
                 first = max(0, min(f, (int)a.T));
                 last = max(first, min(l, (int)a.T));
@@ -373,7 +383,7 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
                 const int v = __shfl_up_sync(FULL, end, o);
                 if (lane >= o) end += v;
             }
-            if (lane == 31) s_sum[warp] = end;
+            if (lane == 31 && warp < WARPS) s_sum[warp] = end;
             __syncthreads();
             int all = 0;
 #pragma unroll
@@ -471,12 +481,10 @@ struct Work {
     int chunk0, chunks, km, a_at;  // a_at: bytes of x's rows in a chunk
     const X* x;
     const W* wa;
-    int x_left, x_to, a_to;
     // 2: columns
     const W* wb;
     const Y* base;
     int n_begin, n_end, per, blk_shift, base_at;
-    int b_to, base_to, base_col, base_left;
 
     // Column `col` of a 32-column block lies in row 8 i + q for column q of its
     // MMA i, q / 2 * 8 + 2 i + q % 2 = col: a lane's outputs are then eight
@@ -485,65 +493,77 @@ struct Work {
         return (col & ~31) | (((col >> 1) & 3) * 8 + ((col >> 3) & 3) * 2 + (col & 1));
     }
 
-    // A copy costs an address and little else: counts are constants, rows that
-    // are not there are left out (x) or zeros (A, B) by what is known of them
-    // from the start.
+    // The warp that copies.  Counts are constants where whole tiles are there;
+    // rows that are not are left out (x, base) or zeros (A, B).
     __device__ __forceinline__ void fill_chunks(uint32_t slot, int group, int first) {
-        constexpr int XS = LORA_THREADS / XU, AS = LORA_THREADS / AU;  // rows that are copied at a time
-        const int n = min(km, chunks - first);
+        constexpr int XS = 32 / XU, AS = 32 / AU;  // rows that are copied at a time
+        const int lane = threadIdx.x & 31, n = min(km, chunks - first);
         int k0 = (chunk0 + first) * LORA_CHUNK;
         const W* wg = wa + (int64_t)group * RT * a.lda;
-        const int w_left = rank - group * RT - (int)threadIdx.x / AU;
+        const int x_row = lane / XU, w_row = lane / AU, w_left = rank - group * RT - w_row;
 #pragma unroll 1
         for (int j = 0; j < n; ++j, k0 += LORA_CHUNK, slot += a_at + RT * AT::pitch) {
             // the last chunk may be half of one
-            const bool xin = k0 + LORA_CHUNK <= a.K || (threadIdx.x % XU) * 2 < XU;
-            const bool win = k0 + LORA_CHUNK <= a.K || (threadIdx.x % AU) * 2 < AU;
+            const bool xin = k0 + LORA_CHUNK <= a.K || (lane % XU) * 2 < XU;
+            const bool win = k0 + LORA_CHUNK <= a.K || (lane % AU) * 2 < AU;
             const X* xs = x + (xin ? k0 : 0);
+            const int xb = xin ? 16 : 0;
+#pragma unroll 1
+            for (int r = 0; r < t.rows; r += 16) {
+#pragma unroll
+                for (int i = 0; i < 16 / XS; ++i)
+                    if (r + i * XS + x_row < t.rows)
+                        copy16(slot + r * XT::pitch + XT::at(i * XS + x_row, lane % XU), xs + i * XS * a.ldx, xb);
+                xs += 16 * a.ldx;
+            }
             const W* ws = wg + (win ? k0 : 0);
+            const uint32_t to = slot + a_at;
 #pragma unroll
-            for (int i = 0; i < 64 / XS; ++i)
-                if (i * XS < x_left) copy16(slot + x_to + i * XS * XT::pitch, xs + i * XS * a.ldx, xin ? 16 : 0);
-#pragma unroll
-            for (int i = 0; i < (RT + AS - 1) / AS; ++i)
-                if (RT >= AS || threadIdx.x < RT * AU) {
-                    const bool in = win && i * AS < w_left;
-                    copy16(slot + a_at + a_to + i * AS * AT::pitch, in ? ws + i * AS * a.lda : wa, in ? 16 : 0);
-                }
+            for (int i = 0; i < RT / AS; ++i) {
+                const bool in = win && i * AS < w_left;
+                copy16(to + AT::at(i * AS + w_row, lane % AU), in ? ws + i * AS * a.lda : wa, in ? 16 : 0);
+            }
         }
     }
 
     __device__ __forceinline__ void fill_columns(uint32_t slot, int n) {
-        constexpr int BS = LORA_THREADS / BU;
-        const int cols = min(per, n_end - n), col = threadIdx.x / BU, unit = threadIdx.x % BU;
+        constexpr int BS = 32 / BU;  // 32 columns are BU copies of a lane
+        const int lane = threadIdx.x & 31, cols = min(per, n_end - n), col = lane / BU, unit = lane % BU;
         const W* src = wb + (n - n_begin) * a.ldb;
         const bool plain = !a.vec_b || n + cols > a.N;
 #pragma unroll 1
         for (int g = 0; g < groups; ++g, src += RT) {
             const int bytes = max(0, min(16, (rank - g * RT - unit * WE) * (int)sizeof(W)));
-            const uint32_t to = slot + g * per * BT::pitch;
-            if (!plain) {
-                const W* from = bytes ? src : static_cast<const W*>(a.b);
-                const int64_t step = bytes ? a.ldb : 0;
-#pragma unroll
-                for (int i = 0; i < 256 / BS; ++i)
-                    if (col + i * BS < cols)
-                        copy16(to + (BS % 32 ? BT::at(place(col + i * BS), unit) : b_to + i * BS * BT::pitch),
-                               from + i * BS * step, bytes);
-            } else {
+            const W* from = bytes ? src : static_cast<const W*>(a.b);
+            const int64_t ld = bytes ? a.ldb : 0;
+            uint32_t to = slot + g * per * BT::pitch;
 #pragma unroll 1
-                for (int i = col; i < cols; i += BS)
-                    copy_plain(to + BT::at(place(i), unit), src + (i - col) * a.ldb, n + i < a.N ? bytes : 0);
+            for (int c0 = 0; c0 < cols; c0 += 32, to += 32 * BT::pitch, from += 32 * ld) {
+                if (!plain) {
+#pragma unroll
+                    for (int i = 0; i < BU; ++i) copy16(to + BT::at(place(col + i * BS), unit), from + i * BS * ld, bytes);
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < BU; ++i)
+                        copy_plain(to + BT::at(place(col + i * BS), unit), from + i * BS * ld,
+                                   n + c0 + col + i * BS < a.N ? bytes : 0);
+                }
             }
         }
-        if (a.vec_base && base_col < cols) {
-            const int bytes = max(0, min(16, (a.N - n - base_col) * (int)sizeof(Y)));
-            const Y* from = bytes ? base + n : static_cast<const Y*>(a.base);
-            const int shift = blk_shift + (YU == 8 ? 3 : 2), step = LORA_THREADS >> shift;
-            const int64_t ld = bytes ? step * a.ld_base : 0;
-            uint32_t dst = slot + base_to;
-#pragma unroll 4
-            for (int r = 0; r < base_left; r += step, dst += step << shift << 4, from += ld) copy16(dst, from, bytes);
+        if (a.vec_base) {
+            // a row is 4 to 64 units: whole ones, or 32 units at a time
+            const int shift = blk_shift + (YU == 8 ? 3 : 2), wide = max(0, shift - 5), s = min(shift, 5);
+            const int row = lane >> s, step = 32 >> s;
+#pragma unroll 1
+            for (int h = 0; h < 1 << wide; ++h) {
+                const int u = (lane & ((1 << s) - 1)) + h * 32, at = u * YE;
+                const int left = at < cols ? max(0, min(16, (a.N - n - at) * (int)sizeof(Y))) : 0;
+                const Y* from = left ? base + row * a.ld_base + n + at : static_cast<const Y*>(a.base);
+                const int64_t ld = left ? step * a.ld_base : 0;
+#pragma unroll 8
+                for (int r = row; r < t.rows; r += step, from += ld)
+                    copy16(slot + base_at + ((r << shift) + (u ^ base_key(r, shift))) * 16, from, left);
+            }
         }
     }
     // Eight lanes read a unit (two, of fp32) of four column groups of two rows.
@@ -554,6 +574,7 @@ struct Work {
 
 template <typename X, typename W, typename Y, int RT>
 __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+    static_assert(LORA_THREADS == THREADS + 32, "one warp copies");
     using K = Work<X, W, Y, RT>;
     using H = Hidden<W, Y>;
     constexpr bool FLUSH = sizeof(X) == 4 || sizeof(W) == 4 || sizeof(Y) == 4;
@@ -607,7 +628,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     const uint32_t ring = smem_u32(smem) + a.ring_at;
     K k = {a, t, rank, groups};
     {
-        const int all = (a.K + LORA_CHUNK - 1) / LORA_CHUNK, tid = threadIdx.x;
+        const int all = (a.K + LORA_CHUNK - 1) / LORA_CHUNK, tid = lane;  // (of the warp that copies)
         k.chunk0 = (int)((int64_t)all * cta >> cs);
         k.chunks = (int)((int64_t)all * (cta + 1) >> cs) - k.chunk0;
         k.a_at = mtiles * 16 * K::XT::pitch;
@@ -616,9 +637,6 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
         k.x = static_cast<const X*>(a.x) + (t.row + tid / K::XU) * a.ldx + tid % K::XU * K::XE;
         k.wa = static_cast<const W*>(a.a) + t.adapter * a.a_stride;
         k.wa += (tid / K::AU < rank ? tid / K::AU : 0) * a.lda + tid % K::AU * K::WE;
-        k.x_left = t.rows - tid / K::XU;
-        k.x_to = K::XT::at(tid / K::XU, tid % K::XU);
-        k.a_to = K::AT::at(tid / K::AU, tid % K::AU);
         k.n_begin = nb0 * 32;
         k.n_end = nb1 * 32;
         k.wb = static_cast<const W*>(a.b) + t.adapter * a.b_stride + (k.n_begin + tid / K::BU) * a.ldb + tid % K::BU * K::WE;
@@ -627,30 +645,51 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
         while (k.blk_shift && (block << k.blk_shift) > slot_bytes) --k.blk_shift;
         k.per = 32 << k.blk_shift;
         k.base_at = k.per * groups * K::BT::pitch;
-        k.b_to = K::BT::at(K::place(tid / K::BU), tid % K::BU);
-        const int shift = k.blk_shift + (K::YU == 8 ? 3 : 2), row = tid >> shift, unit = tid & ((1 << shift) - 1);
-        k.base_left = t.rows - row;
-        k.base_col = unit * K::YE;
-        k.base_to = k.base_at + ((row << shift) + (unit ^ K::base_key(row, shift))) * 16;
-        k.base = base + (t.row + row) * a.ld_base + k.base_col;
+        k.base = base + t.row * a.ld_base;
     }
     const int stage_k = (k.chunks + k.km - 1) / k.km, stages_k = stage_k * groups;  // of a group of ranks, of all
     const int stages_n = (nb1 - nb0 + (1 << k.blk_shift) - 1) >> k.blk_shift;
-    int next = 0, next_group = 0, next_chunk = 0, next_slot = 0;
-    const auto fill = [&] {
-        const uint32_t to = ring + next_slot * slot_bytes;
-        if (next < stages_k) {
-            k.fill_chunks(to, next_group, next_chunk);
-            next_chunk += k.km;
-            if (next_chunk >= k.chunks) next_chunk = 0, ++next_group;
-        } else if (next < stages_k + stages_n) {
-            k.fill_columns(to, k.n_begin + (next - stages_k) * k.per);
-        }
-        copies_commit();
-        ++next;
-        next_slot = next_slot + 1 == depth ? 0 : next_slot + 1;
-    };
-    for (int i = 0; i < depth - 1; ++i) fill();
+    const int stages = stages_k + stages_n;
+
+    if (warp == WARPS) {
+        // A stage is handed over when the two after it are on their way.  The
+        // cluster's barriers stand where no slot is free before the third step.
+        constexpr int LAG = 2;
+        int fill = 0, fill_slot = 0, done = 0, done_slot = 0, group = 0, chunk = 0;
+        const auto hand_over = [&] {
+            bar_arrive(BAR_FULL + done_slot, LORA_THREADS);
+            ++done;
+            done_slot = done_slot + 1 == depth ? 0 : done_slot + 1;
+        };
+        const auto run = [&](int until) {
+            for (; fill < until; ++fill) {
+                if (fill >= depth) bar_sync(BAR_EMPTY + fill_slot, LORA_THREADS);
+                const uint32_t to = ring + fill_slot * slot_bytes;
+                if (fill < stages_k) {
+                    k.fill_chunks(to, group, chunk);
+                    chunk += k.km;
+                    if (chunk >= k.chunks) chunk = 0, ++group;
+                } else {
+                    k.fill_columns(to, k.n_begin + (fill - stages_k) * k.per);
+                }
+                copies_commit();
+                fill_slot = fill_slot + 1 == depth ? 0 : fill_slot + 1;
+                const int lag = min(LAG, depth - 1);
+                if (fill - done >= lag) {
+                    copies_wait(lag);
+                    hand_over();
+                }
+            }
+        };
+        run(min(stages, stages_k + depth));
+        copies_wait(0);
+        while (done < fill) hand_over();
+        if (cs) cluster_barrier(), cluster_barrier();
+        run(stages);
+        copies_wait(0);
+        while (done < fill) hand_over();
+        return;
+    }
 
     // 1. parts of h: [part of a stage's K][16 * mtiles][room + 8] fp32.  A warp
     // has 16 rows, half of the ranks, and all of K, a half or a quarter.
@@ -663,9 +702,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
         float acc[NT][4] = {};
         int chunk = 0;
         for (int s = 0; s < stages_k; ++s) {
-            copies_wait(depth - 2);
-            __syncthreads();
-            fill();
+            bar_sync(BAR_FULL + slot, LORA_THREADS);
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
                 uint32_t xt = ring + slot * slot_bytes;
@@ -691,6 +728,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
                     }
                 }
             }
+            if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, LORA_THREADS);
             chunk += k.km;
             slot = slot + 1 == depth ? 0 : slot + 1;
             if (chunk >= k.chunks) {  // the group's sums are done
@@ -711,7 +749,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     if (cs)
         cluster_barrier();
     else
-        __syncthreads();
+        bar_sync(BAR_MULTIPLY, THREADS);
 
     // 2. this CTA's share of h, four ranks of a row at a time on the cluster's
     // number of lanes: each adds up the parts of one CTA, a butterfly adds these
@@ -721,7 +759,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
         const int q0 = (int)(quads * cta >> cs), q1 = (int)(quads * (cta + 1) >> cs);
         const uint32_t other = threadIdx.x & ((1u << cs) - 1), part = smem_u32(smem), frag = part + a.frag_at;
         const uint32_t from = cs ? peer(part, other) : part, to = cs ? peer(frag, other) : frag;
-        for (int qb = q0; qb < q1; qb += LORA_THREADS >> cs) {
+        for (int qb = q0; qb < q1; qb += THREADS >> cs) {
             const int q = qb + (threadIdx.x >> cs);
             const bool mine = q < q1;
             const int row = mine ? q / per_row : 0, j = mine ? (q - row * per_row) * 4 : 0;
@@ -747,7 +785,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     if (cs)
         cluster_barrier();
     else
-        __syncthreads();
+        bar_sync(BAR_MULTIPLY, THREADS);
 
     // 3. the columns; a warp takes 16 rows of a 32-column block
     const int blk = warp >> mshift, r0 = mt * 16 + g;
@@ -759,13 +797,15 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     int n = k.n_begin + blk * 32 + 8 * c;
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
-    for (int s = 0; s < stages_n; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        copies_wait(depth - 2);
-        __syncthreads();
-        fill();
+    for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
+        bar_sync(BAR_FULL + slot, LORA_THREADS);
         const uint32_t stage = ring + slot * slot_bytes;
+        const int full = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
-        if (mt >= mtiles || blk >= 1 << k.blk_shift || n - 8 * c >= k.n_end) continue;
+        if (mt >= mtiles || blk >= 1 << k.blk_shift || n - 8 * c >= k.n_end) {
+            if (s + depth < stages) bar_arrive(BAR_EMPTY + full, LORA_THREADS);
+            continue;
+        }
         float d[4][4] = {};
         for (int gr = 0; gr < groups; ++gr) {
 #pragma unroll
@@ -805,6 +845,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
                 }
             }
         }
+        if (s + depth < stages) bar_arrive(BAR_EMPTY + full, LORA_THREADS);
         if (a.vec_out && n - 8 * c + 32 <= N) {
             if (in0) store_eight(y0, e0);
             if (in1) store_eight(y1, e1);

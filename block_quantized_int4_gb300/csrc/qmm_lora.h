@@ -5,7 +5,7 @@
 
 namespace qmm {
 
-constexpr int LORA_THREADS = 256;
+constexpr int LORA_THREADS = 288;
 constexpr int LORA_CHUNK = 64;  // columns of x that are multiplied at a time
 
 struct LoraArgs {
