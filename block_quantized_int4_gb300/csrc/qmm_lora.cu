@@ -143,7 +143,7 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 3 + tile, optin)) return QMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c));
-    cfg.blockDim = dim3(LORA_THREADS);
+    cfg.blockDim = dim3(256 + 32 * (rt == 16 ? LORA_COPIERS<16> : LORA_COPIERS<64>));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];

@@ -42,8 +42,8 @@
 namespace qmm {
 namespace lora {
 
-constexpr int WARPS = 8;               // that multiply; one more copies
-constexpr int THREADS = WARPS * 32;    // of these
+constexpr int WARPS = 8;             // that multiply
+constexpr int THREADS = WARPS * 32;  // of these
 
 // Barriers between the warp that copies and those that multiply, by slot.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -470,13 +470,14 @@ struct Work {
     static constexpr int XU = LORA_CHUNK * sizeof(X) / 16, AU = LORA_CHUNK * sizeof(W) / 16, BU = RT * sizeof(W) / 16;
     static constexpr int XE = 16 / sizeof(X), WE = 16 / sizeof(W), YE = 16 / sizeof(Y);
     static constexpr int YU = 32 / YE;  // units of a row of base in a 32-column block
+    static constexpr int COPIERS = LORA_COPIERS<RT>;  // warps that copy, a part of each stage each
     using XT = Tile<X, XU>;
     using AT = Tile<W, AU>;
     using BT = Tile<W, BU>;
 
     const LoraArgs& a;
     RowTile t;
-    int rank, groups;
+    int rank, groups, copier;
     // 1: chunks of K of this CTA, chunks of a stage, and where this thread's units come from
     int chunk0, chunks, km, a_at;  // a_at: bytes of x's rows in a chunk
     const X* x;
@@ -508,19 +509,21 @@ struct Work {
             const bool win = k0 + LORA_CHUNK <= a.K || (lane % AU) * 2 < AU;
             const X* xs = x + (xin ? k0 : 0);
             const int xb = xin ? 16 : 0;
+            xs += 16 * copier * a.ldx;
 #pragma unroll 1
-            for (int r = 0; r < t.rows; r += 16) {
+            for (int r = 16 * copier; r < t.rows; r += 16 * COPIERS) {
 #pragma unroll
                 for (int i = 0; i < 16 / XS; ++i)
                     if (r + i * XS + x_row < t.rows)
                         copy16(slot + r * XT::pitch + XT::at(i * XS + x_row, lane % XU), xs + i * XS * a.ldx, xb);
-                xs += 16 * a.ldx;
+                xs += 16 * COPIERS * a.ldx;
             }
-            const W* ws = wg + (win ? k0 : 0);
-            const uint32_t to = slot + a_at;
+            const int first_row = copier * (RT / COPIERS), left = w_left - first_row;
+            const W* ws = wg + (win ? k0 : 0) + first_row * a.lda;
+            const uint32_t to = slot + a_at + first_row * AT::pitch;
 #pragma unroll
-            for (int i = 0; i < RT / AS; ++i) {
-                const bool in = win && i * AS < w_left;
+            for (int i = 0; i < RT / COPIERS / AS; ++i) {
+                const bool in = win && i * AS < left;
                 copy16(to + AT::at(i * AS + w_row, lane % AU), in ? ws + i * AS * a.lda : wa, in ? 16 : 0);
             }
         }
@@ -534,26 +537,29 @@ struct Work {
 #pragma unroll 1
         for (int g = 0; g < groups; ++g, src += RT) {
             const int bytes = max(0, min(16, (rank - g * RT - unit * WE) * (int)sizeof(W)));
-            const W* from = bytes ? src : static_cast<const W*>(a.b);
             const int64_t ld = bytes ? a.ldb : 0;
+            // half a block of columns (a quarter, ..) of each copier
+            constexpr int PART = BU / COPIERS;
+            const int c1 = col + copier * PART * BS;
+            const W* from = (bytes ? src : static_cast<const W*>(a.b)) + copier * PART * BS * ld;
             uint32_t to = slot + g * per * BT::pitch;
 #pragma unroll 1
             for (int c0 = 0; c0 < cols; c0 += 32, to += 32 * BT::pitch, from += 32 * ld) {
                 if (!plain) {
 #pragma unroll
-                    for (int i = 0; i < BU; ++i) copy16(to + BT::at(place(col + i * BS), unit), from + i * BS * ld, bytes);
+                    for (int i = 0; i < PART; ++i) copy16(to + BT::at(place(c1 + i * BS), unit), from + i * BS * ld, bytes);
                 } else {
 #pragma unroll 1
-                    for (int i = 0; i < BU; ++i)
-                        copy_plain(to + BT::at(place(col + i * BS), unit), from + i * BS * ld,
-                                   n + c0 + col + i * BS < a.N ? bytes : 0);
+                    for (int i = 0; i < PART; ++i)
+                        copy_plain(to + BT::at(place(c1 + i * BS), unit), from + i * BS * ld,
+                                   n + c0 + c1 + i * BS < a.N ? bytes : 0);
                 }
             }
         }
         if (a.vec_base) {
             // a row is 4 to 64 units: whole ones, or 32 units at a time
             const int shift = blk_shift + (YU == 8 ? 3 : 2), wide = max(0, shift - 5), s = min(shift, 5);
-            const int row = lane >> s, step = 32 >> s;
+            const int row = (lane >> s) + copier * (32 >> s), step = COPIERS * 32 >> s;
 #pragma unroll 1
             for (int h = 0; h < 1 << wide; ++h) {
                 const int u = (lane & ((1 << s) - 1)) + h * 32, at = u * YE;
@@ -573,8 +579,8 @@ struct Work {
 };
 
 template <typename X, typename W, typename Y, int RT>
-__global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
-    static_assert(LORA_THREADS == THREADS + 32, "one warp copies");
+__global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+    constexpr int ALL = THREADS + 32 * LORA_COPIERS<RT>;
     using K = Work<X, W, Y, RT>;
     using H = Hidden<W, Y>;
     constexpr bool FLUSH = sizeof(X) == 4 || sizeof(W) == 4 || sizeof(Y) == 4;
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     if (rank == 0) {  // y = base
         if (a.y == a.base) return;
         for (int r = 0; r < t.rows; ++r)
-            for (int n = nb0 * 32 + threadIdx.x * 8; n < min(N, nb1 * 32); n += LORA_THREADS * 8) {
+            for (int n = nb0 * 32 + threadIdx.x * 8; n < min(N, nb1 * 32); n += ALL * 8) {
                 Y* to = y + (t.row + r) * a.ldy + n;
                 const Y* from = base ? base + (t.row + r) * a.ld_base + n : nullptr;
                 if (!a.vec_out || n + 8 > N) {
@@ -626,7 +632,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     const int mtiles = (t.rows + 15) >> 4, mshift = mtiles > 2 ? 2 : mtiles - 1;  // 1, 2 or 4 warps on 16 rows each
     const int groups = (rank + RT - 1) / RT, room = groups * RT, depth = a.depth, slot_bytes = a.slot_bytes;
     const uint32_t ring = smem_u32(smem) + a.ring_at;
-    K k = {a, t, rank, groups};
+    K k = {a, t, rank, groups, warp - WARPS};
     {
         const int all = (a.K + LORA_CHUNK - 1) / LORA_CHUNK, tid = lane;  // (of the warp that copies)
         k.chunk0 = (int)((int64_t)all * cta >> cs);
@@ -651,19 +657,19 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     const int stages_n = (nb1 - nb0 + (1 << k.blk_shift) - 1) >> k.blk_shift;
     const int stages = stages_k + stages_n;
 
-    if (warp == WARPS) {
+    if (warp >= WARPS) {
         // A stage is handed over when the two after it are on their way.  The
         // cluster's barriers stand where no slot is free before the third step.
         constexpr int LAG = 2;
         int fill = 0, fill_slot = 0, done = 0, done_slot = 0, group = 0, chunk = 0;
         const auto hand_over = [&] {
-            bar_arrive(BAR_FULL + done_slot, LORA_THREADS);
+            bar_arrive(BAR_FULL + done_slot, ALL);
             ++done;
             done_slot = done_slot + 1 == depth ? 0 : done_slot + 1;
         };
         const auto run = [&](int until) {
             for (; fill < until; ++fill) {
-                if (fill >= depth) bar_sync(BAR_EMPTY + fill_slot, LORA_THREADS);
+                if (fill >= depth) bar_sync(BAR_EMPTY + fill_slot, ALL);
                 const uint32_t to = ring + fill_slot * slot_bytes;
                 if (fill < stages_k) {
                     k.fill_chunks(to, group, chunk);
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
         float acc[NT][4] = {};
         int chunk = 0;
         for (int s = 0; s < stages_k; ++s) {
-            bar_sync(BAR_FULL + slot, LORA_THREADS);
+            bar_sync(BAR_FULL + slot, ALL);
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
                 uint32_t xt = ring + slot * slot_bytes;
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
                     }
                 }
             }
-            if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, LORA_THREADS);
+            if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, ALL);
             chunk += k.km;
             slot = slot + 1 == depth ? 0 : slot + 1;
             if (chunk >= k.chunks) {  // the group's sums are done
@@ -798,12 +804,12 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
     for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        bar_sync(BAR_FULL + slot, LORA_THREADS);
+        bar_sync(BAR_FULL + slot, ALL);
         const uint32_t stage = ring + slot * slot_bytes;
         const int full = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
         if (mt >= mtiles || blk >= 1 << k.blk_shift || n - 8 * c >= k.n_end) {
-            if (s + depth < stages) bar_arrive(BAR_EMPTY + full, LORA_THREADS);
+            if (s + depth < stages) bar_arrive(BAR_EMPTY + full, ALL);
             continue;
         }
         float d[4][4] = {};
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(LORA_THREADS, RT == 16 ? 3 : 2) lora_kernel(co
                 }
             }
         }
-        if (s + depth < stages) bar_arrive(BAR_EMPTY + full, LORA_THREADS);
+        if (s + depth < stages) bar_arrive(BAR_EMPTY + full, ALL);
         if (a.vec_out && n - 8 * c + 32 <= N) {
             if (in0) store_eight(y0, e0);
             if (in1) store_eight(y1, e1);

@@ -5,7 +5,10 @@
 
 namespace qmm {
 
-constexpr int LORA_THREADS = 288;
+// Warps of a CTA that copy, by the ranks of its kernel (16: three CTAs an SM and
+// 72 registers a thread with one; 32 and 64: two CTAs either way).
+template <int RANKS>
+constexpr int LORA_COPIERS = RANKS == 16 ? 1 : 2;
 constexpr int LORA_CHUNK = 64;  // columns of x that are multiplied at a time
 
 struct LoraArgs {
