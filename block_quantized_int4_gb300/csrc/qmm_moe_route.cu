@@ -11,7 +11,6 @@
 namespace qmm {
 namespace {
 
-constexpr int BLOCK_WARPS = 8;  // route::WARPS
 // Tokens up to which one block routes them all and groups their slots, too:
 // beyond that the grouping is a launch of its own.
 constexpr int ONE_BLOCK_TOKENS = 64;
@@ -76,14 +75,15 @@ extern "C" qmm_status qmm_moe_route(const qmm_moe_route_op* op, void* stream) {
     const bool even = a.n_groups == 1 || a.group_size % (1 << slot) == 0;
     a.per = even ? 1 << slot : (a.group_size + lanes - 1) / lanes;
     a.vec = even && !off(op->logits, vec) && (op->T == 1 || op->ld * size % vec == 0);
+    const bool scores = op->bias || (a.n_groups > 1 && a.top2);
     const bool group = op->workspace && op->T <= ONE_BLOCK_TOKENS;
-    const RouteKernel kernel = op->dtype == QMM_F32   ? route_kernel_f32(slot, group)
-                               : op->dtype == QMM_F16 ? route_kernel_f16(slot, group)
-                                                      : route_kernel_bf16(slot, group);
+    const RouteKernel kernel = op->dtype == QMM_F32   ? route_kernel_f32(slot, scores, group)
+                               : op->dtype == QMM_F16 ? route_kernel_f16(slot, scores, group)
+                                                      : route_kernel_bf16(slot, scores, group);
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(group ? 512 : BLOCK_WARPS * 32);
+    cfg.blockDim = dim3(32 * (group ? route_group_warps(1 << slot) : ROUTE_WARPS));
     cfg.gridDim = dim3(
-        group ? 1 : (unsigned)std::min<int64_t>(((int64_t)op->T + BLOCK_WARPS - 1) / BLOCK_WARPS, 8 * (int64_t)sms));
+        group ? 1 : (unsigned)std::min<int64_t>(((int64_t)op->T + ROUTE_WARPS - 1) / ROUTE_WARPS, 8 * (int64_t)sms));
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -31,17 +31,17 @@ namespace qmm {
 namespace route {
 
 constexpr int MAX_K = 64;
-constexpr int WARPS = 8;         // of a block
-constexpr int GROUP_WARPS = 16;  // of the one block that also groups the slots
+constexpr int WARPS = ROUTE_WARPS;
 
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Ordered keys.  0: taken or not there; 1: an expert that takes no part.
+// Ordered keys.  An expert that takes no part has -inf; 0: taken or not there.
+constexpr uint32_t KEY_OUT = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key32(float v) {
-    const uint32_t u = __float_as_uint(v + 0.f);  // -0 as +0
-    return max(u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u), 2u);
+    const int u = __float_as_int(v + 0.f);  // -0 as +0
+    return (uint32_t)(u ^ ((u >> 31) | (int)0x80000000));
 }
 __device__ __forceinline__ float value32(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
@@ -51,13 +51,13 @@ __device__ __forceinline__ unsigned long long key64(double v) {
     return max(u ^ ((u >> 63) ? ~0ull : 1ull << 63), 2ull);
 }
 
-// What a warp leaves for its gates: the chosen experts in order, one more
-// than k where the choice is checked.
-struct Chosen {
-    uint32_t cand_key[32];
-    int cand_id[32];
-    int id[MAX_K];
-    float key[33];
+// A warp's candidates and choice.
+struct __align__(16) Chosen {
+    uint32_t key[36];  // of candidates, then zeros up to a multiple of four
+    int cand[32];
+    int id[MAX_K];     // the chosen in order; one more where the border is checked
+    float value[33];   // and their keys
+    double exact[32];
 };
 
 // Where a lane's experts lie: `count` of them from `first` on.
@@ -102,7 +102,18 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, const T* row, co
         for (int i = 0; i < PER; ++i) l[i] = i < p.count ? as_float(row[p.first + i]) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = l[i] > -INFINITY ? l[i] : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = fmaxf(l[i], -INFINITY);  // of a NaN: -inf
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -117,6 +128,19 @@ __device__ __forceinline__ double score64(const RouteArgs& a, float l, double to
     return a.softmax ? exp((double)l - top) / sum : 1.0 / (1.0 + exp(-(double)l));
 }
 
+// The 64-bit largest logit and sum of exponentials of a token's softmax.
+template <int PER>
+__device__ __forceinline__ void softmax64(const float (&l)[PER], double& top, double& sum) {
+    top = -INFINITY;
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = fmax(top, (double)l[i]);
+    for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL, top, o));
+    for (int i = 0; i < PER; ++i)
+        if (l[i] > -INFINITY) sum += exp((double)l[i] - top);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+}
+
 // The whole choice with 64-bit keys, by k rounds over all experts.  Every lane
 // of the warp; leaves the chosen experts in out.id.
 template <int PER, typename T>
@@ -127,14 +151,7 @@ __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen
     load_logits<PER, T>(a, row, p, l);
     const bool top2 = a.n_groups > 1 && a.top2;
     double top = -INFINITY, sum = 0.0;
-    if (a.softmax && (a.bias || top2)) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) top = fmax(top, (double)l[i]);
-        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL, top, o));
-        for (int i = 0; i < PER; ++i)
-            if (l[i] > -INFINITY) sum += exp((double)l[i] - top);
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    }
+    if (a.softmax && (a.bias || top2)) softmax64(l, top, sum);
     unsigned long long key[PER];
     double first = -INFINITY, second = -INFINITY;  // of this lane's group
     for (int i = 0; i < PER; ++i) {
@@ -191,20 +208,67 @@ __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen
     __syncwarp();
 }
 
-// One token.
+// Experts of this lane in `mask` become candidates, in index order over the
+// lanes; how many there are (more than 32: none is written).
+__device__ __forceinline__ int collect(uint32_t mask, int first, const uint32_t* key, Chosen& out) {
+    const int lane = threadIdx.x & 31, have = __popc(mask);
+    int end = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, end, o);
+        if (lane >= o) end += v;
+    }
+    const int total = __shfl_sync(FULL, end, 31);
+    if (total > 32) return total;
+    __syncwarp();
+    for (int at = end - have; mask; ++at, mask &= mask - 1) {
+        const int i = __ffs(mask) - 1;
+        out.cand[at] = first + i;
+        out.key[at] = key[i];
+    }
+    if (lane < 4) out.key[total + lane] = 0;
+    __syncwarp();
+    return total;
+}
+
+// The candidates that 32 bits do not order, each in 64 bits on a lane of its
+// own: those that may be among the k largest are all there.
 template <int PER, typename T>
-__device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out) {
+__device__ __noinline__ void order64(const RouteArgs& a, const T* row, int total, Chosen& out) {
+    const int lane = threadIdx.x & 31;
+    double top = 0.0, sum = 1.0;
+    if (a.softmax) {
+        float l[PER];
+        load_logits<PER, T>(a, row, place_of(a, lane), l);
+        softmax64(l, top, sum);
+    }
+    const int e = lane < total ? out.cand[lane] : 0;
+    const float l = fmaxf(as_float(row[e]), -INFINITY);
+    const double mine = l > -INFINITY ? score64(a, l, top, sum) + (a.bias ? (double)a.bias[e] : 0.0) : -INFINITY;
+    out.exact[lane] = mine;
+    __syncwarp();
+    int rank = 0;
+    for (int d = 0; d < total; ++d) {
+        const double v = out.exact[d];
+        rank += v > mine || (v == mine && d < lane);
+    }
+    if (lane < total && rank < a.k) out.id[rank] = e;
+    __syncwarp();
+}
+
+// One token.  SCORES: the choice takes scores (a bias, or groups by the sum of
+// two), not logits alone.  keys: 32 * PER words of shared memory.
+template <int PER, typename T, bool SCORES>
+__device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place& p, uint32_t* keys, Chosen& out) {
     const int lane = threadIdx.x & 31;
     const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
-    const Place p = place_of(a, lane);
     const bool grouped = a.n_groups > 1, top2 = grouped && a.top2;
-    const bool scores = a.bias || top2;  // scores enter the choice
     float l[PER];
     load_logits<PER, T>(a, row, p, l);
 
     // softmax: the largest logit and the sum of exponentials
     float top = 0.f, sum = 1.f;
-    if (a.softmax && (scores || !a.renorm)) {
+    if (a.softmax && (SCORES || !a.renorm)) {
         float m = l[0];
 #pragma unroll
         for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
@@ -212,36 +276,38 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out
         sum = 0.f;
         if (top > -INFINITY) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sum += exp2f((l[i] - top) * 1.4426950408889634f);
+            for (int i = 0; i < PER; ++i) sum += ex2((l[i] - top) * 1.4426950408889634f);
         }
         sum = warp_sum(sum);
     }
 
-    // keys; and the error that c and group scores may have.  exp2f and the
-    // divisions are off by 2^-21.5 of the largest score at most (an exponent's
+    // keys; and the error that c and group scores may have.  Exponentials and
+    // reciprocals are off by 2^-21 of the largest score at most (an exponent's
     // rounding, |x| 2^-24, weighs s or s (1 - s), below 0.4 / |x|), softmax by
     // the sum's own error besides; c by its own rounding.
-    const float unit = a.softmax ? __fdividef(1.f, sum) : 1.f, slack = unit * (a.softmax ? 0x1p-18f : 0x1p-19f);
+    const float unit = a.softmax && SCORES ? rcp(sum) : 1.f, slack = unit * (a.softmax ? 0x1p-18f : 0x1p-19f);
     uint32_t key[PER];
     float first = -INFINITY, second = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const bool live = l[i] > -INFINITY;
         float c = l[i];
-        if (scores) {
-            const float e = exp2f((a.softmax ? l[i] - top : -l[i]) * 1.4426950408889634f);
-            const float s = a.softmax ? e * unit : __fdividef(1.f, 1.f + e);
-            const float v = a.bias ? s + (i < p.count ? __ldg(a.bias + p.first + i) : 0.f) : s;
+        if constexpr (SCORES) {
+            const float e = ex2((a.softmax ? l[i] - top : -l[i]) * 1.4426950408889634f);
+            float v = a.softmax ? e * unit : rcp(1.f + e);
+            if (a.bias) v += i < p.count ? __ldg(a.bias + p.first + i) : 0.f;
+            v = l[i] > -INFINITY ? fmaxf(v, -INFINITY) : -INFINITY;
             if (a.bias) c = v;
-            if (top2) second = fmaxf(second, fminf(first, live ? v : -INFINITY));
-            first = fmaxf(first, live ? v : -INFINITY);
-        } else {
-            first = fmaxf(first, c);
+            if (top2) second = fmaxf(second, fminf(first, v));
+            first = fmaxf(first, v);
         }
-        key[i] = i < p.count ? (live ? key32(c) : 1u) : 0u;
+        key[i] = key32(c);
     }
-    bool again = false;
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
+    bool stays = p.count > 0, again = false;
     if (grouped) {
+        if constexpr (!SCORES) first = p.count > 0 ? value32(best) : -INFINITY;
         for (int o = p.lanes >> 1; o > 0; o >>= 1) {
             const float f = __shfl_xor_sync(FULL, first, o);
             if (top2) {
@@ -253,82 +319,78 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out
         const float mine = top2 && second > -INFINITY ? first + second : first;
         const int g = lane / p.lanes;
         int before = 0;
+#pragma unroll 4
         for (int h = 0; h < a.n_groups; ++h) {
             const float v = __shfl_sync(FULL, mine, h * p.lanes);
             before += v > mine || (v == mine && h < g);
         }
-        const bool stays = before < a.top_groups;
-        if (scores) {
+        const bool in = before < a.top_groups;
+        if constexpr (SCORES) {
             // groups on either side of the border that are too close
-            const uint32_t in = __reduce_min_sync(FULL, stays && g < a.n_groups ? key32(mine) : 0xFFFFFFFFu);
-            const uint32_t no = __reduce_max_sync(FULL, !stays && g < a.n_groups ? key32(mine) : 0u);
-            const float hi = value32(in), lo = no ? value32(no) : -INFINITY;
+            const float hi = value32(__reduce_min_sync(FULL, in ? key32(mine) : 0xFFFFFFFFu));
+            const uint32_t no = __reduce_max_sync(FULL, in ? 0u : key32(mine));
+            const float lo = no ? value32(no) : -INFINITY;
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
             again = lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size));
         }
-        if (!stays) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) key[i] = 0;
-        }
+        stays = stays && in;
     }
 
     // candidates: keys from the n-th best of the lanes' best on (n = k, and one
     // more where the border is checked)
-    const int n = a.k + (a.bias ? 1 : 0);
-    uint32_t floor_key = 1;
-    if (n <= 32) {
-        uint32_t best = key[0];
+    const int n = a.k + (SCORES && a.bias ? 1 : 0);
+    const uint32_t there = !stays ? 0u : PER == 32 && p.count == 32 ? 0xFFFFFFFFu : (1u << p.count) - 1u;
 #pragma unroll
-        for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-        for (int j = 0; j < n; ++j) {
-            floor_key = __reduce_max_sync(FULL, best);
-            const uint32_t who = __ballot_sync(FULL, best == floor_key);
-            if (lane == __ffs(who) - 1) best = 0;
-        }
-        floor_key = max(floor_key, 1u);
+    for (int i = 0; i < PER; i += PER < 4 ? PER : 4) {
+        if constexpr (PER >= 4)
+            *reinterpret_cast<uint4*>(keys + lane * PER + i) = make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+        else if constexpr (PER == 2)
+            *reinterpret_cast<uint2*>(keys + lane * PER) = make_uint2(key[0], key[1]);
+        else
+            keys[lane] = key[0];
     }
-    uint32_t mask = 0;
+    const auto from = [&](uint32_t floor_key) {
+        uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mask |= (key[i] >= floor_key ? 1u : 0u) << i;
-    const int have = __popc(mask);
-    int end = have;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, end, o);
-        if (lane >= o) end += v;
-    }
-    const int total = __shfl_sync(FULL, end, 31);
-    again = again || total > 32;
+        for (int i = 0; i < PER; ++i) mask |= (key[i] >= floor_key ? 1u : 0u) << i;
+        return collect(mask & there, p.first, keys + lane * PER, out);
+    };
+    int total = 33;
     if (!again) {
-        int at = end - have;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if ((mask >> i) & 1u) {
-                out.cand_key[at] = key[i];
-                out.cand_id[at] = p.first + i;
-                ++at;
+        uint32_t floor_key = KEY_OUT;
+        if (n <= 32) {
+            uint32_t rest = stays ? best : 0u;
+            for (int j = 0; j < n; ++j) {
+                floor_key = __reduce_max_sync(FULL, rest);
+                const uint32_t who = __ballot_sync(FULL, rest == floor_key);
+                if (lane == __ffs(who) - 1) rest = 0;
             }
-        __syncwarp();
+            floor_key = max(floor_key, KEY_OUT);
+        }
+        total = from(floor_key);
+    }
+    again = total > 32;
+    if (!again) {
         // candidates lie in index order: of equal keys the earlier ranks first
-        const uint32_t mine = lane < total ? out.cand_key[lane] : 0u;
+        const uint32_t mine = lane < total ? out.key[lane] : 0u;
         int rank = 0;
-        for (int d = 0; d < total; ++d) {
-            const uint32_t v = out.cand_key[d];
-            rank += v > mine || (v == mine && d < lane);
+        for (int d = 0; d < total; d += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(out.key + d);
+            rank += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+            rank += (v.x == mine && d < lane) + (v.y == mine && d + 1 < lane) + (v.z == mine && d + 2 < lane) +
+                    (v.w == mine && d + 3 < lane);
         }
         if (lane < total && rank < n) {
-            const int e = out.cand_id[lane];
-            if (rank < a.k) out.id[rank] = e;
-            if (a.bias) out.key[rank] = mine > 1 ? value32(mine) : -INFINITY;
+            out.id[rank] = out.cand[lane];
+            if (SCORES && a.bias) out.value[rank] = value32(mine);
         }
         __syncwarp();
-        if (a.bias) {
+        if (SCORES && a.bias) {
             // neighbours that are too close, but for equal logits with equal biases
             // among the chosen (at the border a third may be close to both)
-            const int pairs = min(total, n) - 1;
             bool close = false;
-            if (lane < pairs) {
-                const float hi = out.key[lane], lo = out.key[lane + 1];
+            if (lane < min(total, n) - 1) {
+                const float hi = out.value[lane], lo = out.value[lane + 1];
                 if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-22f * (fabsf(hi) + fabsf(lo)))) {
                     close = true;
                     if (lane + 1 < a.k) {
@@ -337,7 +399,13 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out
                     }
                 }
             }
-            again = __any_sync(FULL, close);
+            if (__any_sync(FULL, close)) {
+                // all that may be among the k largest, in 64 bits
+                const float kth = out.value[a.k - 1];
+                total = from(max(KEY_OUT, key32(kth - (2.f * slack + 0x1p-21f * fabsf(kth)))));
+                again = total > 32;
+                if (!again) order64<PER, T>(a, row, total, out);
+            }
         }
     }
     if (again) route_slow<PER, T>(a, row, out);
@@ -378,18 +446,20 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, Chosen& out
     __syncwarp();  // out is written again for the next token
 }
 
-template <int PER, typename T, bool GROUP>
-__global__ void __launch_bounds__(GROUP ? GROUP_WARPS * 32 : WARPS * 32) route_kernel(const __grid_constant__ RouteArgs a, MoeWs ws,
+template <int PER, typename T, bool SCORES, bool GROUP>
+__global__ void __launch_bounds__((GROUP ? route_group_warps(PER) : WARPS) * 32, GROUP ? 1 : PER <= 16 ? 4 : 3) route_kernel(const __grid_constant__ RouteArgs a, MoeWs ws,
                                                                                            int* err) {
     // launched after the kernel that writes the logits, possibly early
     // (programmatic dependent launch): nothing is read before it completes
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int NW = GROUP ? GROUP_WARPS : WARPS;
+    constexpr int NW = GROUP ? route_group_warps(PER) : WARPS;
     __shared__ Chosen chosen[NW];
+    __shared__ __align__(16) uint32_t keys[NW][32 * PER];
     const int warp = threadIdx.x >> 5;
+    const Place p = place_of(a, threadIdx.x & 31);
     for (int64_t t = (int64_t)blockIdx.x * NW + warp; t < a.T; t += (int64_t)gridDim.x * NW)
-        route_one<PER, T>(a, (int)t, chosen[warp]);
+        route_one<PER, T, SCORES>(a, (int)t, p, keys[warp], chosen[warp]);
     if constexpr (GROUP) {
         __syncthreads();
         moe_group_block(a.ids, a.T * a.k, a.n_groups * a.group_size, ws, err);
@@ -397,15 +467,18 @@ __global__ void __launch_bounds__(GROUP ? GROUP_WARPS * 32 : WARPS * 32) route_k
 }
 
 // The kernels of one type, by the experts of a lane (1, 2, 4, .. 32).
+template <typename T, bool SCORES, bool GROUP>
+RouteKernel kernel_of(int slot) {
+    static constexpr RouteKernel kernels[6] = {
+        route_kernel<1, T, SCORES, GROUP>, route_kernel<2, T, SCORES, GROUP>,  route_kernel<4, T, SCORES, GROUP>,
+        route_kernel<8, T, SCORES, GROUP>, route_kernel<16, T, SCORES, GROUP>, route_kernel<32, T, SCORES, GROUP>};
+    return kernels[slot];
+}
 template <typename T>
-RouteKernel kernel_of(int slot, bool group) {
-    static constexpr RouteKernel plain[6] = {route_kernel<1, T, false>,  route_kernel<2, T, false>,
-                                             route_kernel<4, T, false>,  route_kernel<8, T, false>,
-                                             route_kernel<16, T, false>, route_kernel<32, T, false>};
-    static constexpr RouteKernel grouping[6] = {route_kernel<1, T, true>,  route_kernel<2, T, true>,
-                                                route_kernel<4, T, true>,  route_kernel<8, T, true>,
-                                                route_kernel<16, T, true>, route_kernel<32, T, true>};
-    return group ? grouping[slot] : plain[slot];
+RouteKernel kernel_of(int slot, bool scores, bool group) {
+    return group ? scores ? kernel_of<T, true, true>(slot) : kernel_of<T, false, true>(slot)
+                 : scores ? kernel_of<T, true, false>(slot)
+                          : kernel_of<T, false, false>(slot);
 }
 
 }  // namespace route

@@ -21,12 +21,18 @@ struct RouteArgs {
     float scale;
 };
 
+constexpr int ROUTE_WARPS = 8;  // of a block
+// Of the one block that also groups the slots, by the experts of a lane: as many
+// as their shared memory allows.
+__host__ __device__ constexpr int route_group_warps(int per) { return per <= 8 ? 16 : per <= 16 ? 8 : 4; }
+
 using RouteKernel = void (*)(RouteArgs, MoeWs, int*);
 
-// The kernel for lanes of up to 1 << slot experts; group: one block, which
-// builds the tables of the workspace, too.
-RouteKernel route_kernel_f32(int slot, bool group);
-RouteKernel route_kernel_f16(int slot, bool group);
-RouteKernel route_kernel_bf16(int slot, bool group);
+// The kernel for lanes of up to 1 << slot experts; scores: the choice takes
+// scores, not logits alone; group: one block, which builds the tables of the
+// workspace, too.
+RouteKernel route_kernel_f32(int slot, bool scores, bool group);
+RouteKernel route_kernel_f16(int slot, bool scores, bool group);
+RouteKernel route_kernel_bf16(int slot, bool scores, bool group);
 
 }  // namespace qmm

@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-RouteKernel route_kernel_bf16(int slot, bool group) { return route::kernel_of<__nv_bfloat16>(slot, group); }
+RouteKernel route_kernel_bf16(int slot, bool scores, bool group) { return route::kernel_of<__nv_bfloat16>(slot, scores, group); }
 
 }  // namespace qmm

@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-RouteKernel route_kernel_f16(int slot, bool group) { return route::kernel_of<__half>(slot, group); }
+RouteKernel route_kernel_f16(int slot, bool scores, bool group) { return route::kernel_of<__half>(slot, scores, group); }
 
 }  // namespace qmm

@@ -3,6 +3,6 @@
 
 namespace qmm {
 
-RouteKernel route_kernel_f32(int slot, bool group) { return route::kernel_of<float>(slot, group); }
+RouteKernel route_kernel_f32(int slot, bool scores, bool group) { return route::kernel_of<float>(slot, scores, group); }
 
 }  // namespace qmm
