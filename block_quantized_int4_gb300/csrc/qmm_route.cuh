@@ -122,10 +122,10 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Logits in 64 bits -> score.
+// Logits in 64 bits -> score (0 of -inf).
 __device__ __forceinline__ double score64(const RouteArgs& a, float l, double top, double sum) {
-    if (!(l > -INFINITY)) return 0.0;
-    return a.softmax ? exp((double)l - top) / sum : 1.0 / (1.0 + exp(-(double)l));
+    const double e = exp(a.softmax ? (double)l - top : -(double)l);
+    return a.softmax ? (l > -INFINITY ? e / sum : 0.0) : 1.0 / (1.0 + e);
 }
 
 // The 64-bit largest logit and sum of exponentials of a token's softmax.
@@ -141,6 +141,56 @@ __device__ __forceinline__ void softmax64(const float (&l)[PER], double& top, do
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
 }
 
+// Whether the group of a lane stays, in 64 bits; c: each expert's score and
+// bias (its logit where these do not enter the choice).
+template <int PER>
+__device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, const float (&l)[PER], double (&c)[PER]) {
+    const bool top2 = a.n_groups > 1 && a.top2;
+    if (a.bias || top2) {
+        double top = 0.0, sum = 1.0;
+        if (a.softmax) softmax64(l, top, sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c[i] = score64(a, l[i], top, sum);  // side by side: the 64-bit pipe is slow
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c[i] += i < p.count ? (double)a.bias[p.first + i] : 0.0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c[i] = l[i];
+    }
+    double first = -INFINITY, second = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const double v = l[i] > -INFINITY ? c[i] : -INFINITY;
+        second = v > first ? first : v > second ? v : second;
+        first = v > first ? v : first;
+    }
+    for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+        const double f = __shfl_xor_sync(FULL, first, o), s = __shfl_xor_sync(FULL, second, o);
+        second = fmax(fmin(first, f), fmax(second, s));
+        first = fmax(first, f);
+    }
+    const double mine = top2 && second > -INFINITY ? first + second : first;
+    const int g = (threadIdx.x & 31) / p.lanes;
+    int before = 0;
+    for (int h = 0; h < a.n_groups; ++h) {
+        const double v = __shfl_sync(FULL, mine, h * p.lanes);
+        before += v > mine || (v == mine && h < g);
+    }
+    return before < a.top_groups;
+}
+
+// Groups on either side of the border that 32 bits do not order.
+template <int PER, typename T>
+__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row) {
+    const Place p = place_of(a, threadIdx.x & 31);
+    float l[PER];
+    load_logits<PER, T>(a, row, p, l);
+    double c[PER];
+    return groups64(a, p, l, c);
+}
+
 // The whole choice with 64-bit keys, by k rounds over all experts.  Every lane
 // of the warp; leaves the chosen experts in out.id.
 template <int PER, typename T>
@@ -149,45 +199,12 @@ __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen
     const Place p = place_of(a, lane);
     float l[PER];
     load_logits<PER, T>(a, row, p, l);
-    const bool top2 = a.n_groups > 1 && a.top2;
-    double top = -INFINITY, sum = 0.0;
-    if (a.softmax && (a.bias || top2)) softmax64(l, top, sum);
+    double c[PER];
+    const bool stays = groups64(a, p, l, c);
     unsigned long long key[PER];
-    double first = -INFINITY, second = -INFINITY;  // of this lane's group
-    for (int i = 0; i < PER; ++i) {
-        const bool live = l[i] > -INFINITY;
-        double c = l[i];
-        if (live && (a.bias || top2)) {
-            const double s = score64(a, l[i], top, sum), b = a.bias ? (double)a.bias[p.first + i] : 0.0;
-            if (a.bias) c = s + b;
-            const double v = s + b;
-            if (v > first) {
-                second = first;
-                first = v;
-            } else if (v > second) {
-                second = v;
-            }
-        } else if (live) {
-            first = fmax(first, c);
-        }
-        key[i] = i < p.count ? (live ? key64(c) : 1ull) : 0ull;
-    }
-    if (a.n_groups > 1) {
-        for (int o = p.lanes >> 1; o > 0; o >>= 1) {
-            const double f = __shfl_xor_sync(FULL, first, o), s = __shfl_xor_sync(FULL, second, o);
-            second = fmax(fmin(first, f), fmax(second, s));
-            first = fmax(first, f);
-        }
-        const double mine = top2 && second > -INFINITY ? first + second : first;
-        const int g = lane / p.lanes;
-        int before = 0;
-        for (int h = 0; h < a.n_groups; ++h) {
-            const double v = __shfl_sync(FULL, mine, h * p.lanes);
-            before += v > mine || (v == mine && h < g);
-        }
-        if (before >= a.top_groups)
-            for (int i = 0; i < PER; ++i) key[i] = 0;
-    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        key[i] = stays && i < p.count ? l[i] > -INFINITY ? key64(a.bias ? c[i] : (double)l[i]) : 1ull : 0ull;
     for (int j = 0; j < a.k; ++j) {
         unsigned long long best = 0;
         int at = 0;
@@ -259,7 +276,8 @@ __device__ __noinline__ void order64(const RouteArgs& a, const T* row, int total
 // One token.  SCORES: the choice takes scores (a bias, or groups by the sum of
 // two), not logits alone.  keys: 32 * PER words of shared memory.
 template <int PER, typename T, bool SCORES>
-__device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place& p, uint32_t* keys, Chosen& out) {
+__device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place& p, const float (&bias)[PER],
+                                          uint32_t* keys, Chosen& out) {
     const int lane = threadIdx.x & 31;
     const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
     const bool grouped = a.n_groups > 1, top2 = grouped && a.top2;
@@ -294,7 +312,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         if constexpr (SCORES) {
             const float e = ex2((a.softmax ? l[i] - top : -l[i]) * 1.4426950408889634f);
             float v = a.softmax ? e * unit : rcp(1.f + e);
-            if (a.bias) v += i < p.count ? __ldg(a.bias + p.first + i) : 0.f;
+            v += bias[i];
             v = l[i] > -INFINITY ? fmaxf(v, -INFINITY) : -INFINITY;
             if (a.bias) c = v;
             if (top2) second = fmaxf(second, fminf(first, v));
@@ -305,7 +323,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
     uint32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    bool stays = p.count > 0, again = false;
+    bool stays = p.count > 0;
     if (grouped) {
         if constexpr (!SCORES) first = p.count > 0 ? value32(best) : -INFINITY;
         for (int o = p.lanes >> 1; o > 0; o >>= 1) {
@@ -324,14 +342,14 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             const float v = __shfl_sync(FULL, mine, h * p.lanes);
             before += v > mine || (v == mine && h < g);
         }
-        const bool in = before < a.top_groups;
+        bool in = before < a.top_groups;
         if constexpr (SCORES) {
             // groups on either side of the border that are too close
             const float hi = value32(__reduce_min_sync(FULL, in ? key32(mine) : 0xFFFFFFFFu));
             const uint32_t no = __reduce_max_sync(FULL, in ? 0u : key32(mine));
             const float lo = no ? value32(no) : -INFINITY;
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
-            again = lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size));
+            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size))) in = groups_again<PER, T>(a, row);
         }
         stays = stays && in;
     }
@@ -355,30 +373,30 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         for (int i = 0; i < PER; ++i) mask |= (key[i] >= floor_key ? 1u : 0u) << i;
         return collect(mask & there, p.first, keys + lane * PER, out);
     };
-    int total = 33;
-    if (!again) {
-        uint32_t floor_key = KEY_OUT;
-        if (n <= 32) {
-            uint32_t rest = stays ? best : 0u;
-            for (int j = 0; j < n; ++j) {
-                floor_key = __reduce_max_sync(FULL, rest);
-                const uint32_t who = __ballot_sync(FULL, rest == floor_key);
-                if (lane == __ffs(who) - 1) rest = 0;
-            }
-            floor_key = max(floor_key, KEY_OUT);
+    uint32_t floor_key = KEY_OUT;
+    if (n <= 32) {
+        // the smallest of those that fewer than n are larger than
+        const uint32_t mine = stays ? best : 0u;
+        out.key[lane] = mine;
+        __syncwarp();
+        int larger = 0;
+#pragma unroll
+        for (int d = 0; d < 32; d += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(out.key + d);
+            larger += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
         }
-        total = from(floor_key);
+        floor_key = max(__reduce_min_sync(FULL, larger < n ? mine : 0xFFFFFFFFu), KEY_OUT);
     }
-    again = total > 32;
+    int total = from(floor_key);
+    bool again = total > 32;
     if (!again) {
         // candidates lie in index order: of equal keys the earlier ranks first
         const uint32_t mine = lane < total ? out.key[lane] : 0u;
         int rank = 0;
         for (int d = 0; d < total; d += 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(out.key + d);
-            rank += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
-            rank += (v.x == mine && d < lane) + (v.y == mine && d + 1 < lane) + (v.z == mine && d + 2 < lane) +
-                    (v.w == mine && d + 3 < lane);
+            rank += (v.x >= mine + (d >= lane)) + (v.y >= mine + (d + 1 >= lane)) + (v.z >= mine + (d + 2 >= lane)) +
+                    (v.w >= mine + (d + 3 >= lane));
         }
         if (lane < total && rank < n) {
             out.id[rank] = out.cand[lane];
@@ -458,8 +476,11 @@ __global__ void __launch_bounds__((GROUP ? route_group_warps(PER) : WARPS) * 32,
     __shared__ __align__(16) uint32_t keys[NW][32 * PER];
     const int warp = threadIdx.x >> 5;
     const Place p = place_of(a, threadIdx.x & 31);
+    float bias[PER];  // of this lane's experts, whatever the token
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bias[i] = SCORES && a.bias && i < p.count ? a.bias[p.first + i] : 0.f;
     for (int64_t t = (int64_t)blockIdx.x * NW + warp; t < a.T; t += (int64_t)gridDim.x * NW)
-        route_one<PER, T, SCORES>(a, (int)t, p, keys[warp], chosen[warp]);
+        route_one<PER, T, SCORES>(a, (int)t, p, bias, keys[warp], chosen[warp]);
     if constexpr (GROUP) {
         __syncthreads();
         moe_group_block(a.ids, a.T * a.k, a.n_groups * a.group_size, ws, err);
