@@ -10,8 +10,11 @@
 //  - a logit's own order is exact in 32 bits; c and the sums of two are
 //    computed in fp32, with a bound on their error.  Where two values whose
 //    order decides anything are closer than that bound and not of equal
-//    operands, the token is done again with 64-bit keys (route_slow; about
-//    three tokens in a thousand of sigmoid scores with a bias, 256 experts);
+//    operands (about three tokens in a thousand of sigmoid scores with a bias,
+//    256 experts), these are computed again as sums of two fp32 numbers, and
+//    what these do not order either, in 64 bits (route_slow).  (All of the close
+//    ones in 64 bits, at 16 cycles an instruction: 32003 tokens of 256 experts in
+//    8 groups 44 us, with these 10 us the last of them.)
 //  - the k-th largest of the 32 lanes' best keys bounds the k-th largest key
 //    from below, so that only keys from there on are candidates: about 1.3 k
 //    of them, one a lane, each ranked against all others.  (More than 32, as
@@ -26,6 +29,7 @@
 #include "qmm_device.cuh"
 #include "qmm_moe_group.cuh"
 #include "qmm_route.h"
+#include "qmm_route_pair.cuh"
 
 namespace qmm {
 namespace route {
@@ -57,7 +61,7 @@ struct __align__(16) Chosen {
     int cand[32];
     int id[MAX_K];     // the chosen in order; one more where the border is checked
     float value[33];   // and their keys
-    double exact[32];
+    float2 pair[32];
 };
 
 // Where a lane's experts lie: `count` of them from `first` on.
@@ -136,6 +140,7 @@ __device__ __forceinline__ void softmax64(const float (&l)[PER], double& top, do
 #pragma unroll
     for (int i = 0; i < PER; ++i) top = fmax(top, (double)l[i]);
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(FULL, top, o));
+#pragma unroll 1
     for (int i = 0; i < PER; ++i)
         if (l[i] > -INFINITY) sum += exp((double)l[i] - top);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
@@ -149,8 +154,8 @@ __device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, con
     if (a.bias || top2) {
         double top = 0.0, sum = 1.0;
         if (a.softmax) softmax64(l, top, sum);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) c[i] = score64(a, l[i], top, sum);  // side by side: the 64-bit pipe is slow
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i) c[i] = score64(a, l[i], top, sum);
         if (a.bias) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) c[i] += i < p.count ? (double)a.bias[p.first + i] : 0.0;
@@ -179,16 +184,6 @@ __device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, con
         before += v > mine || (v == mine && h < g);
     }
     return before < a.top_groups;
-}
-
-// Groups on either side of the border that 32 bits do not order.
-template <int PER, typename T>
-__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row) {
-    const Place p = place_of(a, threadIdx.x & 31);
-    float l[PER];
-    load_logits<PER, T>(a, row, p, l);
-    double c[PER];
-    return groups64(a, p, l, c);
 }
 
 // The whole choice with 64-bit keys, by k rounds over all experts.  Every lane
@@ -248,29 +243,115 @@ __device__ __forceinline__ int collect(uint32_t mask, int first, const uint32_t*
     return total;
 }
 
-// The candidates that 32 bits do not order, each in 64 bits on a lane of its
-// own: those that may be among the k largest are all there.
-template <int PER, typename T>
-__device__ __noinline__ void order64(const RouteArgs& a, const T* row, int total, Chosen& out) {
-    const int lane = threadIdx.x & 31;
-    double top = 0.0, sum = 1.0;
-    if (a.softmax) {
-        float l[PER];
-        load_logits<PER, T>(a, row, place_of(a, lane), l);
-        softmax64(l, top, sum);
+// Scores as pairs: their largest error, 2^-42 of `unit` (1, or a softmax's
+// largest score) and 2^-46 of what they are added to, with a margin of 8.
+struct Scores {
+    float top;
+    Pair inverse;  // of the softmax's sum
+    float unit;
+
+    template <typename T>
+    __device__ __forceinline__ Scores(const RouteArgs& a, const T* row, const Place& p)
+        : top(0.f), inverse{1.f, 0.f}, unit(1.f) {
+        if (!a.softmax) return;
+        top = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < p.count; ++i) top = fmaxf(top, as_float(row[p.first + i]));
+        top = warp_max(top);
+        if (!(top > -INFINITY)) return;
+        Pair sum = {0.f, 0.f};
+#pragma unroll 1
+        for (int i = 0; i < p.count; ++i) sum = add(sum, power(as_float(row[p.first + i])));
+        for (int o = 16; o > 0; o >>= 1)
+            sum = add(sum, Pair{__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
+        inverse = reciprocal(sum);
+        unit = inverse.hi;
     }
+    __device__ __forceinline__ Pair power(float l) const {
+        return l - top > -87.f ? exp_pair(two_sum(l, -top)) : Pair{0.f, 0.f};  // -inf and NaN, too
+    }
+    // With the bias; -inf of an expert that takes no part.
+    __device__ __forceinline__ Pair of(const RouteArgs& a, float l, float bias) const {
+        if (!(l > -INFINITY)) return {-INFINITY, 0.f};
+        return add(a.softmax ? mul(power(l), inverse) : sigmoid_pair(l), bias);
+    }
+    __device__ __forceinline__ float tolerance(float size) const { return 0x1p-39f * unit + 0x1p-43f * size; }
+};
+
+__device__ __forceinline__ float distance(Pair a, Pair b) {
+    return fabsf(__fadd_rn(__fadd_rn(a.hi, -b.hi), __fadd_rn(a.lo, -b.lo)));  // NaN of two -inf
+}
+
+// Whether the lane's group stays, where fp32 does not tell; `close`: pairs do
+// not, either.  (Short loops: code that runs for few tokens comes from afar, and
+// eight experts side by side took 15 us where these take 5.)
+template <typename T>
+__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, bool& close) {
+    const Place p = place_of(a, threadIdx.x & 31);
+    const Scores s(a, row, p);
+    Pair first = {-INFINITY, 0.f}, second = first;
+#pragma unroll 1
+    for (int i = 0; i < p.count; ++i) {
+        const Pair v = s.of(a, as_float(row[p.first + i]), a.bias ? a.bias[p.first + i] : 0.f);
+        if (before(v, first)) {
+            second = first;
+            first = v;
+        } else if (before(v, second)) {
+            second = v;
+        }
+    }
+    for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+        const Pair f = {__shfl_xor_sync(FULL, first.hi, o), __shfl_xor_sync(FULL, first.lo, o)};
+        const Pair g = {__shfl_xor_sync(FULL, second.hi, o), __shfl_xor_sync(FULL, second.lo, o)};
+        const Pair low = before(first, f) ? f : first, rest = before(second, g) ? second : g;
+        first = before(f, first) ? f : first;
+        second = before(low, rest) ? low : rest;
+    }
+    const Pair mine = a.top2 && second.hi > -INFINITY ? add(first, second) : first;
+    const float size = first.hi > -INFINITY ? fabsf(first.hi) + (second.hi > -INFINITY ? fabsf(second.hi) : 0.f) : 0.f;
+    const float tolerance = s.tolerance(warp_max(size));
+    const int g = (threadIdx.x & 31) / p.lanes;
+    int ahead = 0;
+    for (int h = 0; h < a.n_groups; ++h) {
+        const Pair v = {__shfl_sync(FULL, mine.hi, h * p.lanes), __shfl_sync(FULL, mine.lo, h * p.lanes)};
+        ahead += before(v, mine) || (!before(mine, v) && h < g);
+    }
+    const bool in = ahead < a.top_groups;
+    bool near = false;
+    for (int h = 0; h < a.n_groups; ++h) {
+        const Pair v = {__shfl_sync(FULL, mine.hi, h * p.lanes), __shfl_sync(FULL, mine.lo, h * p.lanes)};
+        const bool other = __shfl_sync(FULL, (int)in, h * p.lanes) != (int)in;
+        near |= other && distance(v, mine) <= tolerance;
+    }
+    close = __any_sync(FULL, near);
+    return in;
+}
+
+// The order of the candidates, each as a pair on a lane of its own, where fp32
+// does not tell (all that may be among the k largest are there); false: pairs do
+// not, either.
+template <typename T>
+__device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, int total, Chosen& out) {
+    const int lane = threadIdx.x & 31;
+    const Scores s(a, row, place_of(a, lane));
     const int e = lane < total ? out.cand[lane] : 0;
-    const float l = fmaxf(as_float(row[e]), -INFINITY);
-    const double mine = l > -INFINITY ? score64(a, l, top, sum) + (a.bias ? (double)a.bias[e] : 0.0) : -INFINITY;
-    out.exact[lane] = mine;
+    const float l = fmaxf(as_float(row[e]), -INFINITY), bias = a.bias ? a.bias[e] : 0.f;
+    const Pair mine = s.of(a, l, bias);
+    out.pair[lane] = make_float2(mine.hi, mine.lo);
     __syncwarp();
     int rank = 0;
+    bool near = false;
     for (int d = 0; d < total; ++d) {
-        const double v = out.exact[d];
-        rank += v > mine || (v == mine && d < lane);
+        const float2 q = out.pair[d];
+        const Pair v = {q.x, q.y};
+        rank += before(v, mine) || (!before(mine, v) && d < lane);
+        const float l_d = __shfl_sync(FULL, l, d), bias_d = __shfl_sync(FULL, bias, d);
+        const bool same = l_d == l && bias_d == bias;
+        near |= !same && distance(v, mine) <= s.tolerance(fabsf(mine.hi));
     }
     if (lane < total && rank < a.k) out.id[rank] = e;
     __syncwarp();
+    return !__any_sync(FULL, near && lane < total && rank < a.k);
 }
 
 // One token.  SCORES: the choice takes scores (a bias, or groups by the sum of
@@ -323,7 +404,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
     uint32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    bool stays = p.count > 0;
+    bool stays = p.count > 0, again = false;
     if (grouped) {
         if constexpr (!SCORES) first = p.count > 0 ? value32(best) : -INFINITY;
         for (int o = p.lanes >> 1; o > 0; o >>= 1) {
@@ -337,7 +418,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         const float mine = top2 && second > -INFINITY ? first + second : first;
         const int g = lane / p.lanes;
         int before = 0;
-#pragma unroll 4
+#pragma unroll 1
         for (int h = 0; h < a.n_groups; ++h) {
             const float v = __shfl_sync(FULL, mine, h * p.lanes);
             before += v > mine || (v == mine && h < g);
@@ -349,7 +430,8 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             const uint32_t no = __reduce_max_sync(FULL, in ? 0u : key32(mine));
             const float lo = no ? value32(no) : -INFINITY;
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
-            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size))) in = groups_again<PER, T>(a, row);
+            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size)))
+                in = groups_again(a, row, again);
         }
         stays = stays && in;
     }
@@ -388,7 +470,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         floor_key = max(__reduce_min_sync(FULL, larger < n ? mine : 0xFFFFFFFFu), KEY_OUT);
     }
     int total = from(floor_key);
-    bool again = total > 32;
+    again = again || total > 32;
     if (!again) {
         // candidates lie in index order: of equal keys the earlier ranks first
         const uint32_t mine = lane < total ? out.key[lane] : 0u;
@@ -418,11 +500,10 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
                 }
             }
             if (__any_sync(FULL, close)) {
-                // all that may be among the k largest, in 64 bits
+                // all that may be among the k largest, as pairs
                 const float kth = out.value[a.k - 1];
                 total = from(max(KEY_OUT, key32(kth - (2.f * slack + 0x1p-21f * fabsf(kth)))));
-                again = total > 32;
-                if (!again) order64<PER, T>(a, row, total, out);
+                again = total > 32 || !order_again(a, row, total, out);
             }
         }
     }
