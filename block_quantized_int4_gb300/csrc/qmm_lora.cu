@@ -107,6 +107,9 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.n_adapters = op->n_adapters;
     a.max_rank = op->max_rank;
     a.err = device_error_word();
+    const WaitSettings wait = wait_settings();
+    a.wait_ns = wait.limit_ns;
+    a.withhold = wait.withhold;
     const bool f32 = op->y_dtype == QMM_F32;
     const int tile = op->max_rank <= 16 ? 0 : op->max_rank <= 32 ? 1 : 2, rt = 16 << tile;
     const int room = (op->max_rank + rt - 1) / rt * rt;

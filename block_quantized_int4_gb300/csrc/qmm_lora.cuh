@@ -45,14 +45,16 @@ namespace lora {
 constexpr int WARPS = 8;             // that multiply
 constexpr int THREADS = WARPS * 32;  // of these
 
-// Barriers between the warp that copies and those that multiply, by slot.
+// Between the warps that copy and those that multiply: a slot is full when the
+// copies into it have landed (an mbarrier that counts copying threads), and empty
+// when all eight warps have arrived.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-constexpr int BAR_FULL = 1, BAR_EMPTY = 5, BAR_MULTIPLY = 9;  // four of the first two
+constexpr int BAR_EMPTY = 1, BAR_MULTIPLY = 5;  // four of the first
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -60,9 +62,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t cta) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
@@ -84,15 +85,22 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most n groups are on their way.
-__device__ __forceinline__ void copies_wait(int n) {
-    if (n >= 2)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (n == 1)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+// All of this thread's copies have landed.
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// An arrival of this thread when its copies until now have landed.
+__device__ __forceinline__ void arrive_with_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Waits for a slot; when that runs out the error word says so, and what follows
+// has no meaning but ends like the rest.
+__device__ __forceinline__ void wait_full(uint64_t* bar, uint32_t parity, const LoraArgs& a) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000))
+        if (global_ns() - t0 > a.wait_ns) {
+            atomicOr(a.err, ERR_TIMEOUT);
+            return;
+        }
 }
 __device__ __forceinline__ uint4 lds(uint32_t addr) {
     uint4 v;
@@ -529,7 +537,8 @@ struct Work {
         }
     }
 
-    __device__ __forceinline__ void fill_columns(uint32_t slot, int n) {
+    // Whether plain stores were among the copies.
+    __device__ __forceinline__ bool fill_columns(uint32_t slot, int n) {
         constexpr int BS = 32 / BU;  // 32 columns are BU copies of a lane
         const int lane = threadIdx.x & 31, cols = min(per, n_end - n), col = lane / BU, unit = lane % BU;
         const W* src = wb + (n - n_begin) * a.ldb;
@@ -571,6 +580,7 @@ struct Work {
                     copy16(slot + base_at + ((r << shift) + (u ^ base_key(r, shift))) * 16, from, left);
             }
         }
+        return plain;
     }
     // Eight lanes read a unit (two, of fp32) of four column groups of two rows.
     __device__ static __forceinline__ int base_key(int row, int shift) {
@@ -586,6 +596,9 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     constexpr bool FLUSH = sizeof(X) == 4 || sizeof(W) == 4 || sizeof(Y) == 4;
     constexpr int NT = RT / 16;  // blocks of 8 ranks of a warp: half of RT
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[4];
+    if (threadIdx.x == 0)
+        for (int i = 0; i < 4; ++i) mbar_init(&full[i], 32 * K::COPIERS);
     // launched after the kernels that write x and base, possibly early
     // (programmatic dependent launch): nothing is read before they complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -597,6 +610,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const RowTile t = find_tile(a, blockIdx.x >> cs);
     if (t.rows == 0) return;  // of all CTAs of the cluster
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    __syncthreads();  // full is there
     const int N = a.N, blocks = (N + 31) / 32;
     const int nb0 = (int)((int64_t)blocks * cta >> cs), nb1 = (int)((int64_t)blocks * (cta + 1) >> cs);
     const Y* base = static_cast<const Y*>(a.base);
@@ -653,47 +667,63 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         k.base_at = k.per * groups * K::BT::pitch;
         k.base = base + t.row * a.ld_base;
     }
-    const int stage_k = (k.chunks + k.km - 1) / k.km, stages_k = stage_k * groups;  // of a group of ranks, of all
+    const int stage_k = k.km == 4   ? (k.chunks + 3) >> 2
+                        : k.km == 2 ? (k.chunks + 1) >> 1
+                        : k.km == 1 ? k.chunks
+                                    : (k.chunks + 2) / 3,
+              stages_k = stage_k * groups;  // of a group of ranks, of all
     const int stages_n = (nb1 - nb0 + (1 << k.blk_shift) - 1) >> k.blk_shift;
     const int stages = stages_k + stages_n;
 
+    // stage s, by COPIERS warps; the last arrival may be withheld (a test's)
+    const auto fill = [&](int s, int slot, int group, int chunk) {
+        const uint32_t to = ring + slot * slot_bytes;
+        bool plain = false;
+        if (s < stages_k)
+            k.fill_chunks(to, group, chunk);
+        else
+            plain = k.fill_columns(to, k.n_begin + (s - stages_k) * k.per);
+        if (a.withhold && s == stages - 1) return;
+        if (plain) {
+            copies_wait();
+            mbar_arrive(&full[slot]);
+        } else {
+            arrive_with_copies(&full[slot]);
+        }
+    };
+    // the warps that multiply fill the ring for the first time, all at once
+    {
+        const int s = warp / K::COPIERS;
+        if (s < min(depth, stages)) {
+            int group = 0, chunk = s * k.km;
+            while (chunk >= k.chunks && s < stages_k) chunk -= stage_k * k.km, ++group;
+            k.copier = warp % K::COPIERS;
+            fill(s, s, group, chunk);
+        }
+    }
+    const bool direct = t.rows <= 16;  // how h is put together; see there
     if (warp >= WARPS) {
-        // A stage is handed over when the two after it are on their way.  The
-        // cluster's barriers stand where no slot is free before the third step.
-        constexpr int LAG = 2;
-        int fill = 0, fill_slot = 0, done = 0, done_slot = 0, group = 0, chunk = 0;
-        const auto hand_over = [&] {
-            bar_arrive(BAR_FULL + done_slot, ALL);
-            ++done;
-            done_slot = done_slot + 1 == depth ? 0 : done_slot + 1;
+        int slot = 0, group = 0, chunk = 0;
+        const auto step = [&] {
+            chunk += k.km;
+            if (chunk >= k.chunks) chunk = 0, ++group;
         };
-        const auto run = [&](int until) {
-            for (; fill < until; ++fill) {
-                if (fill >= depth) bar_sync(BAR_EMPTY + fill_slot, ALL);
-                const uint32_t to = ring + fill_slot * slot_bytes;
-                if (fill < stages_k) {
-                    k.fill_chunks(to, group, chunk);
-                    chunk += k.km;
-                    if (chunk >= k.chunks) chunk = 0, ++group;
-                } else {
-                    k.fill_columns(to, k.n_begin + (fill - stages_k) * k.per);
-                }
-                copies_commit();
-                fill_slot = fill_slot + 1 == depth ? 0 : fill_slot + 1;
-                const int lag = min(LAG, depth - 1);
-                if (fill - done >= lag) {
-                    copies_wait(lag);
-                    hand_over();
-                }
+        for (int s = 0; s < depth; ++s) step();
+        const auto run = [&](int from, int until) {
+            for (int s = from; s < until; ++s) {
+                bar_sync(BAR_EMPTY + slot, ALL);
+                fill(s, slot, group, chunk);
+                step();
+                slot = slot + 1 == depth ? 0 : slot + 1;
             }
         };
-        run(min(stages, stages_k + depth));
-        copies_wait(0);
-        while (done < fill) hand_over();
-        if (cs) cluster_barrier(), cluster_barrier();
-        run(stages);
-        copies_wait(0);
-        while (done < fill) hand_over();
+        // no slot is free for more before the third step
+        const int before = max(depth, min(stages, stages_k + depth));
+        run(depth, before);
+        if (cs) cluster_arrive(), cluster_wait(), cluster_arrive();
+        run(before, stages);
+        copies_wait();
+        if (cs) cluster_wait();
         return;
     }
 
@@ -702,21 +732,25 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int mt = warp & ((1 << mshift) - 1), kways = 4 >> mshift;
     const int ps = room + 8;
     int slot = 0;
+    uint32_t parity = 0;
     {
         const int half = (warp >> mshift) & 1, kq = warp >> (mshift + 1);
         float* part = reinterpret_cast<float*>(smem) + (kq * mtiles * 16 + mt * 16 + g) * ps + half * (RT / 2) + 2 * c;
         float acc[NT][4] = {};
         int chunk = 0;
+        // of a stage's chunks, or of a chunk's steps, those of this part of K
+        const bool by_chunk = k.km >= kways;
         for (int s = 0; s < stages_k; ++s) {
-            bar_sync(BAR_FULL + slot, ALL);
+            wait_full(&full[slot], parity, a);
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
-                uint32_t xt = ring + slot * slot_bytes;
-                for (int j = 0; j < n; ++j, xt += k.a_at + RT * K::AT::pitch) {
+                const int chunk_bytes = k.a_at + RT * K::AT::pitch, step = by_chunk ? kways : 1;
+                uint32_t xt = ring + slot * slot_bytes + (by_chunk ? kq * chunk_bytes : 0);
+                for (int j = by_chunk ? kq : 0; j < n; j += step, xt += step * chunk_bytes) {
                     float d[NT][4] = {};
 #pragma unroll
                     for (int st = 0; st < 4; ++st)
-                        if ((st & (kways - 1)) == kq) {
+                        if (by_chunk || (st & (kways - 1)) == kq) {
                             Frag<X> xf[2];
                             Frag<W> wf[NT];
                             load16<X, K::XU>(xt, mt * 16, st, xf);
@@ -737,6 +771,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, ALL);
             chunk += k.km;
             slot = slot + 1 == depth ? 0 : slot + 1;
+            parity ^= slot == 0;
             if (chunk >= k.chunks) {  // the group's sums are done
                 chunk = 0;
 #pragma unroll
@@ -753,18 +788,21 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         }
     }
     if (cs)
-        cluster_barrier();
+        cluster_arrive(), cluster_wait();
     else
         bar_sync(BAR_MULTIPLY, THREADS);
 
-    // 2. this CTA's share of h, four ranks of a row at a time on the cluster's
-    // number of lanes: each adds up the parts of one CTA, a butterfly adds these
-    // (in one order for all), and each hands the sum, scaled and cut, to one CTA.
+    // 2. h, four ranks of a row at a time on the cluster's number of lanes: each
+    // adds up the parts of one CTA, and a butterfly adds these (in one order for
+    // all).  A CTA does so for a share of h, scales it, and each lane hands it to
+    // one CTA; or, of up to 16 rows, for all of it (a barrier of the cluster, of
+    // 0.7 to 1.8 us, is then waited for at the end alone).
     {
         const int per_row = room / 4, quads = t.rows * per_row;
-        const int q0 = (int)(quads * cta >> cs), q1 = (int)(quads * (cta + 1) >> cs);
+        const int q0 = direct ? 0 : (int)(quads * cta >> cs), q1 = direct ? quads : (int)(quads * (cta + 1) >> cs);
         const uint32_t other = threadIdx.x & ((1u << cs) - 1), part = smem_u32(smem), frag = part + a.frag_at;
-        const uint32_t from = cs ? peer(part, other) : part, to = cs ? peer(frag, other) : frag;
+        const uint32_t from = cs ? peer(part, other) : part;
+        const uint32_t to = cs ? peer(frag, direct ? cta : other) : frag;
         for (int qb = q0; qb < q1; qb += THREADS >> cs) {
             const int q = qb + (threadIdx.x >> cs);
             const bool mine = q < q1;
@@ -783,13 +821,14 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                 h.z += __shfl_xor_sync(FULL, h.z, o);
                 h.w += __shfl_xor_sync(FULL, h.w, o);
             }
-            if (!mine) continue;
+            if (!mine || (direct && other)) continue;
             h.x *= scale, h.y *= scale, h.z *= scale, h.w *= scale;
             H::put(to, row, j, room / 16, h);
         }
     }
-    if (cs)
-        cluster_barrier();
+    if (cs) cluster_arrive();
+    if (cs && !direct)
+        cluster_wait();
     else
         bar_sync(BAR_MULTIPLY, THREADS);
 
@@ -804,12 +843,13 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
     for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        bar_sync(BAR_FULL + slot, ALL);
+        wait_full(&full[slot], parity, a);
         const uint32_t stage = ring + slot * slot_bytes;
-        const int full = slot;
+        const int at_slot = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
+        parity ^= slot == 0;
         if (mt >= mtiles || blk >= 1 << k.blk_shift || n - 8 * c >= k.n_end) {
-            if (s + depth < stages) bar_arrive(BAR_EMPTY + full, ALL);
+            if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
             continue;
         }
         float d[4][4] = {};
@@ -851,7 +891,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                 }
             }
         }
-        if (s + depth < stages) bar_arrive(BAR_EMPTY + full, ALL);
+        if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
         if (a.vec_out && n - 8 * c + 32 <= N) {
             if (in0) store_eight(y0, e0);
             if (in1) store_eight(y1, e1);
@@ -861,6 +901,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             if (in1) finish_plain(y1, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
         }
     }
+    if (cs && direct) cluster_wait();
 }
 
 template <typename X, typename W, typename Y>

@@ -27,6 +27,8 @@ struct LoraArgs {
     // shared memory: parts of h, its fragments, the ring's slots
     int frag_at, ring_at, slot_bytes, depth;
     int* err;
+    unsigned long long wait_ns;  // bound of a wait, and whether the last copy's arrival is held back (qmm_debug_stream_wait)
+    int withhold;
 };
 
 using LoraKernel = void (*)(LoraArgs);
