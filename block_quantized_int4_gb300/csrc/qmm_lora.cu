@@ -2,7 +2,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <mutex>
 
 #include "qmm.h"
@@ -56,7 +55,7 @@ LoraKernel kernel_of(int x, int w, bool f32, int tile) {
     return kernels[x][w](f32, tile);
 }
 
-// Opts a kernel into the device's shared memory and clusters of 16, once a device.
+// Opts a kernel into the device's shared memory, once a device.
 bool prepared(LoraKernel k, int kind, int optin) {
     static std::mutex mu;
     static bool done[64][54];
@@ -65,8 +64,7 @@ bool prepared(LoraKernel k, int kind, int optin) {
     std::lock_guard<std::mutex> lk(mu);
     bool& d = done[dev][kind];
     if (!d)
-        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 1024) == cudaSuccess &&
-            cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+        d = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 1024) == cudaSuccess;
     if (!d) cudaGetLastError();
     return d;
 }
@@ -123,8 +121,15 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / a.tile_rows)
                                         : op->n_segs * ((rows + a.tile_rows - 1) / a.tile_rows);
     const int tile_rows = (int)std::min<int64_t>(rows, a.tile_rows), mtiles = (tile_rows + 15) / 16;
-    int64_t c = tiles * 8 <= 2 * (int64_t)sms ? 8 : 4;
-    if (const char* e = getenv("QMM_LORA_C")) c = atoi(e);
+    // CTAs of a tile: eight while the tiles find room at once (short segments
+    // count half: their CTAs are done early), else four: a CTA's start, its share of h
+    // and the barriers take 8 us whatever it has to do.  (us with four and with
+    // eight: one row of 2048 -> 2048, rank 16, 7.3 and 6.6; 48 of 8192 -> 8192, rank
+    // 16, 22 and 14; 2039 rows of 5632 -> 8192 65 and 60; 64 segments of one row of
+    // 2048 -> 5632, rank 64, 22 and 28; 4093 rows of 8192 -> 28672 165 and 178.)
+    const int64_t room_for = (int64_t)sms * (tile == 0 ? 3 : 2);
+    const int64_t busy = op->seg_start ? std::min(tiles, op->T / a.tile_rows + op->n_segs / 2) : tiles;
+    int64_t c = busy * LORA_MAX_CLUSTER <= room_for ? LORA_MAX_CLUSTER : 4;
     while (c > 1 && c * LORA_CHUNK > op->K) c /= 2;
     while ((1 << a.cluster_shift) < c) ++a.cluster_shift;
     // Shared memory: the parts of h (of 16-row blocks, one to four of a tile's and
@@ -135,12 +140,11 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.ring_at = (a.frag_at + mtiles * 16 * room * frag + 127) / 128 * 128;
     const int chunk = LORA_CHUNK * (mtiles * 16 * xs + rt * ws);
     const int block = 32 * (room * ws + (a.vec_base ? tile_rows * ys : 0));
-    int total = tile == 0 ? 72 : 110;
-    if (const char* e = getenv("QMM_LORA_SMEM")) total = atoi(e);
+    const int total = (tile == 0 ? 72 : 110) * 1024;  // three CTAs an SM, two
     const int least = (std::max(chunk, block) + 127) / 128 * 128, most = std::max(4 * chunk, 8 / m2 * block);
-    const int share = (total * 1024 - a.ring_at) / 4 / 128 * 128;
+    const int share = (total - a.ring_at) / 4 / 128 * 128;
     a.slot_bytes = std::max(least, std::min(most, share));
-    a.depth = std::max(2, std::min(4, (total * 1024 - a.ring_at) / a.slot_bytes));
+    a.depth = std::max(2, std::min(4, (total - a.ring_at) / a.slot_bytes));
     const size_t smem = a.ring_at + (size_t)a.depth * a.slot_bytes;
     const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, tile);
     if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 3 + tile, optin)) return QMM_ERR_CUDA;

@@ -4,8 +4,8 @@
 //
 // One launch.  A cluster of CTAs takes a tile of up to 64 rows of a segment:
 //   1. h = A x: each CTA sums over its part of K;
-//   2. the parts of h meet through distributed shared memory: each CTA adds up
-//      a share of them in a fixed order, scales it and hands it to all;
+//   2. the parts of h meet through distributed shared memory: each CTA adds all
+//      of them up;
 //   3. y = base + h B^T: each CTA has its part of the N columns.
 // x, base and y pass once; A and B are read once a tile (from L2 where tiles
 // share an adapter).  So the bound is memory for the ranks in use: 2 r flops
@@ -76,9 +76,6 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr) {
                  : "r"(addr));
     return v;
 }
-__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
 
 // ---------------------------------------------------------------- copies, loads
 // 16 bytes global -> shared, the last 16 - n of them zeros.
@@ -106,6 +103,9 @@ __device__ __forceinline__ uint4 lds(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 __device__ __forceinline__ float2 lds_pair(uint32_t addr) {
     float2 v;
@@ -302,7 +302,7 @@ struct Hidden {
     static constexpr bool bf16 = std::is_same<W, __nv_bfloat16>::value;
     static constexpr int parts = bf16 && sizeof(Y) == 4 ? 3 : 2, mmas = bf16 ? 1 : 2, bytes = mmas * parts * 512;
 
-    // Values k .. k + 3 of a row, k a multiple of 4, to `to` (where the tile's fragments are, at any CTA); k16s: of a row.
+    // Values k .. k + 3 of a row, k a multiple of 4, to `to`, where the tile's fragments are; k16s: of a row.
     __device__ static __forceinline__ void put(uint32_t to, int row, int k, int k16s, const float4& h) {
         const uint32_t at = to + ((row >> 4) * k16s + (k >> 4)) * bytes + (row & 7) * 64 + ((row >> 3) & 1) * 4;
         if constexpr (bf16) {
@@ -310,16 +310,16 @@ struct Hidden {
             float2 v0 = make_float2(h.x, h.y), v1 = make_float2(h.z, h.w);
 #pragma unroll
             for (int p = 0; p < parts; ++p) {
-                st_peer(b + p * 512, bf16_part(v0));
-                st_peer(b + p * 512 + 16, bf16_part(v1));
+                sts(b + p * 512, bf16_part(v0));
+                sts(b + p * 512 + 16, bf16_part(v1));
             }
         } else {
             const uint32_t b = at + ((k >> 3) & 1) * parts * 512 + ((k >> 1) & 3) * 16;
             const float v[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                st_peer(b + (i >> 1) * 16 + (i & 1) * 8, tf_high(v[i]));
-                st_peer(b + (i >> 1) * 16 + (i & 1) * 8 + 512, tf_low(v[i]));
+                sts(b + (i >> 1) * 16 + (i & 1) * 8, tf_high(v[i]));
+                sts(b + (i >> 1) * 16 + (i & 1) * 8 + 512, tf_low(v[i]));
             }
         }
     }
@@ -701,7 +701,6 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             fill(s, s, group, chunk);
         }
     }
-    const bool direct = t.rows <= 16;  // how h is put together; see there
     if (warp >= WARPS) {
         int slot = 0, group = 0, chunk = 0;
         const auto step = [&] {
@@ -792,45 +791,37 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     else
         bar_sync(BAR_MULTIPLY, THREADS);
 
-    // 2. h, four ranks of a row at a time on the cluster's number of lanes: each
-    // adds up the parts of one CTA, and a butterfly adds these (in one order for
-    // all).  A CTA does so for a share of h, scales it, and each lane hands it to
-    // one CTA; or, of up to 16 rows, for all of it (a barrier of the cluster, of
-    // 0.7 to 1.8 us, is then waited for at the end alone).
+    // 2. h, four ranks of a row at a time: every CTA adds up the parts of all,
+    // in one order, scales the sums and cuts them up for itself.  The cluster
+    // waits for one another's reads at the end alone.  (Shares of h that each CTA
+    // summed for all, over a second barrier, took 7 us at 64 rows of 32 ranks and
+    // 8 CTAs, scattered stores to the others most of it.)
     {
         const int per_row = room / 4, quads = t.rows * per_row;
-        const int q0 = direct ? 0 : (int)(quads * cta >> cs), q1 = direct ? quads : (int)(quads * (cta + 1) >> cs);
-        const uint32_t other = threadIdx.x & ((1u << cs) - 1), part = smem_u32(smem), frag = part + a.frag_at;
-        const uint32_t from = cs ? peer(part, other) : part;
-        const uint32_t to = cs ? peer(frag, direct ? cta : other) : frag;
-        for (int qb = q0; qb < q1; qb += THREADS >> cs) {
-            const int q = qb + (threadIdx.x >> cs);
-            const bool mine = q < q1;
-            const int row = mine ? q / per_row : 0, j = mine ? (q - row * per_row) * 4 : 0;
-            float4 v[4];
+        const uint32_t part = smem_u32(smem), frag = part + a.frag_at;
+        int row = threadIdx.x / per_row, j = threadIdx.x - row * per_row;
+        const int rows_on = THREADS / per_row, j_on = THREADS - rows_on * per_row;
+        for (int q = threadIdx.x; q < quads; q += THREADS) {
+            float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t at = part + (row * ps + 4 * j) * 4;
+            for (int kp = 0; kp < kways; ++kp, at += mtiles * 16 * ps * 4) {
+                float4 v[LORA_MAX_CLUSTER];  // all on their way at once
 #pragma unroll
-            for (int kp = 0; kp < 4; ++kp)
-                if (kp < kways) v[kp] = ld_peer(from + ((kp * mtiles * 16 + row) * ps + j) * 4);
-            float4 h = v[0];
+                for (int s = 0; s < LORA_MAX_CLUSTER; ++s)
+                    if (s < 1 << cs) v[s] = ld_peer(cs ? peer(at, s) : at);
 #pragma unroll
-            for (int kp = 1; kp < 4; ++kp)
-                if (kp < kways) h.x += v[kp].x, h.y += v[kp].y, h.z += v[kp].z, h.w += v[kp].w;
-            for (int o = 1; o < 1 << cs; o <<= 1) {
-                h.x += __shfl_xor_sync(FULL, h.x, o);
-                h.y += __shfl_xor_sync(FULL, h.y, o);
-                h.z += __shfl_xor_sync(FULL, h.z, o);
-                h.w += __shfl_xor_sync(FULL, h.w, o);
+                for (int s = 0; s < LORA_MAX_CLUSTER; ++s)
+                    if (s < 1 << cs) h.x += v[s].x, h.y += v[s].y, h.z += v[s].z, h.w += v[s].w;
             }
-            if (!mine || (direct && other)) continue;
             h.x *= scale, h.y *= scale, h.z *= scale, h.w *= scale;
-            H::put(to, row, j, room / 16, h);
+            H::put(frag, row, 4 * j, room / 16, h);
+            row += rows_on;
+            j += j_on;
+            if (j >= per_row) j -= per_row, ++row;
         }
     }
     if (cs) cluster_arrive();
-    if (cs && !direct)
-        cluster_wait();
-    else
-        bar_sync(BAR_MULTIPLY, THREADS);
+    bar_sync(BAR_MULTIPLY, THREADS);
 
     // 3. the columns; a warp takes 16 rows of a 32-column block
     const int blk = warp >> mshift, r0 = mt * 16 + g;
@@ -901,7 +892,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             if (in1) finish_plain(y1, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
         }
     }
-    if (cs && direct) cluster_wait();
+    if (cs) cluster_wait();
 }
 
 template <typename X, typename W, typename Y>

@@ -9,6 +9,7 @@ namespace qmm {
 // 72 registers a thread with one; 32 and 64: two CTAs either way).
 template <int RANKS>
 constexpr int LORA_COPIERS = RANKS == 16 ? 1 : 2;
+constexpr int LORA_MAX_CLUSTER = 8;  // CTAs of a tile
 constexpr int LORA_CHUNK = 64;  // columns of x that are multiplied at a time
 
 struct LoraArgs {
