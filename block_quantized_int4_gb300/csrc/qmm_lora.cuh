@@ -89,14 +89,15 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 __device__ __forceinline__ void arrive_with_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Waits for a slot; when that runs out the error word says so, and what follows
-// has no meaning but ends like the rest.
-__device__ __forceinline__ void wait_full(uint64_t* bar, uint32_t parity, const LoraArgs& a) {
-    if (mbar_try_wait(bar, parity)) return;
+// Waits for a slot while none has run out (`live`); when one does the error word
+// says so, and what follows has no meaning but ends like the rest.
+__device__ __forceinline__ void wait_full(uint64_t* bar, uint32_t parity, const LoraArgs& a, bool& live) {
+    if (!live || mbar_try_wait(bar, parity)) return;
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait_sleep(bar, parity, 20000))
         if (global_ns() - t0 > a.wait_ns) {
             atomicOr(a.err, ERR_TIMEOUT);
+            live = false;
             return;
         }
 }
@@ -733,6 +734,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int ps = room + 8;
     int slot = 0;
     uint32_t parity = 0;
+    bool live = true;
     {
         const int half = (warp >> mshift) & 1, kq = warp >> (mshift + 1);
         float* part = reinterpret_cast<float*>(smem) + (kq * mtiles * 16 + mt * 16 + g) * ps + half * (RT / 2) + 2 * c;
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         // of a stage's chunks, or of a chunk's steps, those of this part of K
         const bool by_chunk = k.km >= kways;
         for (int s = 0; s < stages_k; ++s) {
-            wait_full(&full[slot], parity, a);
+            wait_full(&full[slot], parity, a, live);
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
                 const int chunk_bytes = k.a_at + RT * K::AT::pitch, step = by_chunk ? kways : 1;
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
     for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        wait_full(&full[slot], parity, a);
+        wait_full(&full[slot], parity, a, live);
         const uint32_t stage = ring + slot * slot_bytes;
         const int at_slot = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;

@@ -238,13 +238,14 @@ QMM_API qmm_status qmm_debug_gemm_kernel(int kernel, int* previous);
 
 /* Test hook of the failure handling of the streaming GEMV kernel (the
  * kernel of qmm_gemv_fused, qmm_gemv_fused_op, qmm_gemv_q4_0_f32 and the
- * 1-8 token qmm_gemm_q4_0_q8_0) and of the kernels of qmm_attn_q4_0: every
- * wait on the device is bounded, and this sets the bound of the launches
- * that follow, process-wide: limit_ns in [1e3, 1e10] (the default is 2e9,
- * two seconds).  With withhold_last_copy = 1 the producer of every CTA (in
- * attention every warp that copies) never issues its last copy, so the
+ * 1-8 token qmm_gemm_q4_0_q8_0) and of the kernels of qmm_attn_q4_0 and
+ * qmm_lora: every wait on the device is bounded, and this sets the bound of the
+ * launches that follow, process-wide: limit_ns in [1e3, 1e10] (the default is
+ * 2e9, two seconds).  With withhold_last_copy = 1 the producer of every CTA (in
+ * attention every warp that copies) never issues its last copy (in qmm_lora:
+ * never tells of it), so the
  * wait for it runs out: the launch ends, outputs that depend on it are not
- * written (attention: have no meaning), the device error word gets
+ * written (attention, qmm_lora: have no meaning), the device error word gets
  * QMM_ERR_TIMEOUT (read with qmm_last_device_error), and the context stays
  * usable; every copy that was issued lands before the CTA ends.
  * withhold_last_copy = 0 restores normal operation.  `previous_limit_ns`
