@@ -227,29 +227,34 @@ __device__ __forceinline__ void load16(uint32_t tile, int row, int step, Frag<T>
     }
 }
 
-// The other operand: N blocks of 8 rows from `row` on.
+// The other operand: N blocks of 8 rows from `row` on.  A lane's place for it ..
 template <typename T, int UNITS, int N>
-__device__ __forceinline__ void load8(uint32_t tile, int row, int step, Frag<T> (&f)[N]) {
+__device__ __forceinline__ uint32_t place8(int row, int step) {
     const int lane = threadIdx.x & 31;
     using L = Tile<T, UNITS>;
+    if constexpr (sizeof(T) == 4) return L::at(row + (lane >> 2), step * 4 + ((lane & 3) >> 1)) + (lane & 1) * 8;
+    return L::at(row + (lane & 7) + (N == 1 ? 0 : lane >> 4) * 8, step * 2 + ((lane >> 3) & 1));
+}
+// .. and the loads from there on (of fp32 the second eight k are two units on: a
+// bit that the places of rows and steps leave to the key).
+template <typename T, int UNITS, int N>
+__device__ __forceinline__ void load8(uint32_t at, Frag<T> (&f)[N]) {
+    using L = Tile<T, UNITS>;
     if constexpr (sizeof(T) == 4) {
-        const int r = row + (lane >> 2), u = step * 4 + ((lane & 3) >> 1);
-        const uint32_t low = tile + (lane & 1) * 8;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float2 v = lds_pair(low + L::at(r, u + 2 * e) + n * 8 * L::pitch);
+                const float2 v = lds_pair((at ^ (32 * e)) + n * 8 * L::pitch);
                 f[n].w[0][e] = __float_as_uint(v.x);
                 f[n].w[1][e] = __float_as_uint(v.y);
             }
     } else if constexpr (N == 1) {
-        ldsm2(tile + L::at(row + (lane & 7), step * 2 + ((lane >> 3) & 1)), f[0].w[0][0], f[0].w[0][1]);
+        ldsm2(at, f[0].w[0][0], f[0].w[0][1]);
     } else {
-        const uint32_t a = tile + L::at(row + (lane & 7) + (lane >> 4) * 8, step * 2 + ((lane >> 3) & 1));
 #pragma unroll
         for (int n = 0; n < N; n += 2)
-            ldsm4(a + n * 8 * L::pitch, f[n].w[0][0], f[n].w[0][1], f[n + 1].w[0][0], f[n + 1].w[0][1]);
+            ldsm4(at + n * 8 * L::pitch, f[n].w[0][0], f[n].w[0][1], f[n + 1].w[0][0], f[n + 1].w[0][1]);
     }
 }
 
@@ -443,17 +448,24 @@ __device__ __noinline__ void finish_plain(Y* p, const Y* base, int n, Eight e) {
         if (j < n) put(p + j, base ? as_float(base[j]) + e.v[j] : e.v[j]);
 }
 
+__device__ __forceinline__ void store16(void* p, uint4 v, bool in) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((int)in)
+                 : "memory");
+}
+
 template <typename Y>
-__device__ __forceinline__ void store_eight(Y* p, const Eight& e) {
+__device__ __forceinline__ void store_eight(Y* p, const Eight& e, bool in) {
     if constexpr (sizeof(Y) == 4) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(e.v);
+        store16(p, make_uint4(v[0], v[1], v[2], v[3]), in);
+        store16(p + 4, make_uint4(v[4], v[5], v[6], v[7]), in);
     } else if constexpr (std::is_same<Y, __half>::value) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_f16(e.v[0], e.v[1]), pack_f16(e.v[2], e.v[3]),
-                                                  pack_f16(e.v[4], e.v[5]), pack_f16(e.v[6], e.v[7]));
+        store16(p, make_uint4(pack_f16(e.v[0], e.v[1]), pack_f16(e.v[2], e.v[3]), pack_f16(e.v[4], e.v[5]),
+                              pack_f16(e.v[6], e.v[7])), in);
     } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(e.v[0], e.v[1]), pack_bf16(e.v[2], e.v[3]),
-                                                  pack_bf16(e.v[4], e.v[5]), pack_bf16(e.v[6], e.v[7]));
+        store16(p, make_uint4(pack_bf16(e.v[0], e.v[1]), pack_bf16(e.v[2], e.v[3]), pack_bf16(e.v[4], e.v[5]),
+                              pack_bf16(e.v[6], e.v[7])), in);
     }
 }
 
@@ -756,7 +768,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                             Frag<X> xf[2];
                             Frag<W> wf[NT];
                             load16<X, K::XU>(xt, mt * 16, st, xf);
-                            load8<W, K::AU, NT>(xt + k.a_at, half * (RT / 2), st, wf);
+                            load8<W, K::AU, NT>(xt + k.a_at + place8<W, K::AU, NT>(half * (RT / 2), st), wf);
                             if constexpr (FLUSH)
                                 multiply<X, W, NT>(d, xf, wf);
                             else
@@ -830,9 +842,20 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int blk = warp >> mshift, r0 = mt * 16 + g;
     const bool in0 = r0 < t.rows, in1 = r0 + 8 < t.rows, vec_base = a.vec_base;
     const uint32_t frag = smem_u32(smem) + a.frag_at + mt * (room / 16) * H::bytes + lane * 16;
-    const int base_shift = k.blk_shift + (K::YU == 8 ? 3 : 2), base_pitch = 16 << base_shift;
-    const uint32_t base_key = K::base_key(g, base_shift) * 16;
-    const uint32_t base_lane = k.base_at + r0 * base_pitch + (blk * K::YU + c * (K::YU / 4)) * 16;
+    // base of rows g and g + 8; rows that are not there read the last one's
+    uint32_t base_of[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int shift = k.blk_shift + (K::YU == 8 ? 3 : 2), r = min(r0 + 8 * h, t.rows - 1);
+        base_of[h] = k.base_at + ((r << shift) + ((blk * K::YU + c * (K::YU / 4)) ^ K::base_key(r, shift))) * 16;
+        asm volatile("" : "+r"(base_of[h]));
+    }
+    uint32_t b_at[RT / 16];  // kept, not worked out again for each stage
+#pragma unroll
+    for (int st = 0; st < RT / 16; ++st) {
+        b_at[st] = place8<W, K::BU, 4>(blk * 32, st);
+        asm volatile("" : "+r"(b_at[st]));
+    }
     int n = k.n_begin + blk * 32 + 8 * c;
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
@@ -847,21 +870,23 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             continue;
         }
         float d[4][4] = {};
-        for (int gr = 0; gr < groups; ++gr) {
+        uint32_t group_at = stage, h_at = frag;
+#pragma unroll 1
+        for (int gr = 0; gr < groups; ++gr, group_at += k.per * K::BT::pitch, h_at += RT / 16 * H::bytes) {
 #pragma unroll
             for (int st = 0; st < RT / 16; ++st) {
                 Frag<W> wf[4];
-                load8<W, K::BU, 4>(stage + gr * k.per * K::BT::pitch, blk * 32, st, wf);
+                load8<W, K::BU, 4>(group_at + b_at[st], wf);
                 if constexpr (sizeof(Y) == 4) {
                     // sums of 16 ranks leave the tensor core, which truncates
                     float part[4][4] = {};
-                    H::template multiply<4>(part, frag + (gr * (RT / 16) + st) * H::bytes, wf);
+                    H::template multiply<4>(part, h_at + st * H::bytes, wf);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) d[i][e] += part[i][e];
                 } else {
-                    H::template multiply<4>(d, frag + (gr * (RT / 16) + st) * H::bytes, wf);
+                    H::template multiply<4>(d, h_at + st * H::bytes, wf);
                 }
             }
         }
@@ -872,14 +897,13 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             e1.v[2 * i] = d[i][2], e1.v[2 * i + 1] = d[i][3];
         }
         if (vec_base) {
-            const uint32_t at = stage + base_lane;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!(h ? in1 : in0)) continue;
                 Eight& e = h ? e1 : e0;
-                const uint4 q = lds((at + h * 8 * base_pitch) ^ base_key);
+                const uint32_t at = stage + base_of[h];
+                const uint4 q = lds(at);
                 if constexpr (sizeof(Y) == 4) {
-                    const uint4 r = lds((at + h * 8 * base_pitch + 16) ^ base_key);
+                    const uint4 r = lds(at ^ 16);  // of fp32 two units, next to one another
                     e.v[0] += __uint_as_float(q.x), e.v[1] += __uint_as_float(q.y);
                     e.v[2] += __uint_as_float(q.z), e.v[3] += __uint_as_float(q.w);
                     e.v[4] += __uint_as_float(r.x), e.v[5] += __uint_as_float(r.y);
@@ -897,8 +921,8 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         }
         if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
         if (a.vec_out && n - 8 * c + 32 <= N) {
-            if (in0) store_eight(y0, e0);
-            if (in1) store_eight(y1, e1);
+            store_eight(y0, e0, in0);
+            store_eight(y1, e1, in1);
         } else {
             const Y* b = base && !vec_base ? base + (t.row + r0) * a.ld_base + n : nullptr;
             if (in0) finish_plain(y0, b, N - n, e0);

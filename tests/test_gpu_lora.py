@@ -106,6 +106,22 @@ def test_strides_and_alignment(x, w):
                  seed=rank).check()
 
 
+@pytest.mark.parametrize("x,w,y", [("f32", "f32", "f32"), ("f32", "bf16", "f32"), ("f16", "f16", "f16"),
+                                   ("bf16", "bf16", "bf16"), ("bf16", "bf16", "f32"), ("f16", "f32", "f16")])
+@pytest.mark.parametrize("rank", [40, 64, 100, 128])
+def test_prompts(x, w, y, rank):
+    """Enough rows for tiles of 128: whole ones, and 1 to 127 rows left of a segment."""
+    lens = [1, 300, 128, 0, 17, 250, 33, 511, 90, 64, 200, 127]
+    segs, at = [], 2
+    for i, n in enumerate(lens):
+        segs.append((at, at + n, i % 4 - 1))
+        at += n
+    Case(at + 5, 200, 192, rank, segs, x, w, y, seed=rank).check()
+    Case(at + 5, 71, 2048, rank, segs, x, w, y, ranks=[rank, 7, 33], base=False, ypad=1, seed=rank).check()
+    if rank == 64:
+        Case(4 * 400, 100, 128, rank, [(400 * i, 400 * i + 400, i % 3) for i in range(4)], x, w, y, uniform=True).check()
+
+
 def test_ranks_of_their_own():
     """Smaller adapters in the same storage: NaN and infinity behind their ranks; a rank of 0 is none."""
     for x, w in (("f32", "f16"), ("f32", "f32"), ("bf16", "bf16"), ("f16", "f16")):
