@@ -31,7 +31,7 @@ qmm_status check(const qmm_lora_op& op) {
         return QMM_ERR_ARG;
     const int64_t far = int64_t(1) << 40;
     if (op.K <= 0 || op.K % 32 || op.K > 1 << 24 || op.N > 1 << 28 || op.T > 1 << 28 || op.n_segs > 1 << 16 ||
-        op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > 1 << 24 || op.ldb > far || op.a_stride > far ||
+        op.max_rank > QMM_LORA_MAX_RANK || op.ldx > far || op.lda > far || op.ldb > far || op.a_stride > far ||
         op.b_stride > far || op.ldy > far || op.ld_base > far)
         return QMM_ERR_SHAPE;
     if (!op.seg_start && op.n_segs && (op.T % op.n_segs || op.T / op.n_segs > 1 << 28)) return QMM_ERR_SHAPE;

@@ -898,7 +898,7 @@ QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* 
  *    adapters enter as they are, fp32 ones and A x to 2^-23 of a value (A x to
  *    2^-18 with bf16 adapters and 16-bit y).  y is rounded once.  A row of x with
  *    a NaN or an infinity gives non-finite values in its own row alone.
- * K % 32 == 0, lda <= 2^24, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
+ * K % 32 == 0, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
  * else QMM_ERR_SHAPE.  x and a: 16-byte aligned, ldx, lda and a_stride
  * multiples of 16 bytes, else QMM_ERR_ALIGN; b, base and y: aligned to their
  * element (16-byte aligned rows are faster).  Device values out of range set

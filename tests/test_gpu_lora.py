@@ -213,3 +213,58 @@ def test_captured_on_another_stream():
         c.y.fill_(-7)
         graph.replay()
         R.check(c.y, *c.want())
+
+
+@pytest.mark.parametrize("x,w", [("f32", "bf16"), ("bf16", "bf16"), ("f16", "f32")])
+def test_no_adapter(x, w):
+    """Segments of none take base as it is, or zeros: whole rows, odd ones, base at any element; in place nothing."""
+    for N, ypad, yat in [(1, 0, 0), (9, 0, 0), (64, 0, 0), (71, 1, 0), (2051, 0, 1), (4104, 8, 8), (5000, 4, 2)]:
+        for base in (True, False):
+            c = Case(80, N, 64, 8, [(0, 64, -1), (64, 67, 0), (67, 80, -1)], x, w, ypad=ypad, yat=yat, base=base, seed=N)
+            c.check()
+            none = torch.tensor([*range(64), *range(67, 80)], device=DEV)
+            assert torch.equal(c.y[none], c.base[none] if base else torch.zeros_like(c.y[none]))
+
+
+@pytest.mark.parametrize("x,w", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32")])
+def test_offsets_that_pass_32_bits(x, w):
+    """Rows of A, adapters in storage, rows of x, base and y more than 2^31 values from their first."""
+    rank, K, N, far = 9, 64, 40, (1 << 28) + 64
+    c = Case(9, N, K, rank, [(0, 4, 1), (4, 9, 0)], x, w, adapters=2, seed=3)
+
+    def spread(t, stride):  # the same values, `stride` apart in the second last dimension
+        gap = torch.empty((t.shape[-2] - 1) * stride + t.shape[-1], dtype=t.dtype, device=DEV)
+        out = torch.as_strided(gap, t.shape[-2:], (stride, 1))
+        out.copy_(t)
+        return out
+
+    want, err = c.want()
+    a, b = c.a, c.b
+    for i in range(2):  # one adapter at a time: rows of A far apart
+        c.a = spread(a[i], far)[None]
+        c.b = b[i:i + 1]
+        scales, c.scales = c.scales, c.scales[i:i + 1]
+        lo, hi = (0, 4) if i else (4, 9)
+        start = torch.tensor([lo, hi], dtype=torch.int32, device=DEV)
+        c.y.fill_(-7)
+        c.qmm.qmm_lora(c.qmm.lora_op(c.x, c.a, c.b, c.y, torch.zeros(1, dtype=torch.int32, device=DEV), base=c.base,
+                                     seg_start=start, scales=c.scales))
+        R.check(c.y[lo:hi], want[lo:hi], err[lo:hi])
+        c.scales = scales
+    c.a, c.b = a, b
+    del a, b
+    c.x, c.base, y = spread(c.x, far), spread(c.base, far), c.y
+    c.y = spread(c.y, far)
+    c.qmm.qmm_lora(c.op())
+    R.check(c.y, want, err)
+    c.x, c.base, c.y = c.x.contiguous(), c.base.contiguous(), y
+    for name in ("a", "b"):  # whole adapters far apart
+        t = getattr(c, name)
+        buf = torch.empty((1 << 31) + 64 + t[0].numel(), dtype=t.dtype, device=DEV)
+        v = torch.as_strided(buf, t.shape, ((1 << 31) + 64, t.shape[-1], 1))
+        v.copy_(t)
+        setattr(c, name, v)
+    c.y.fill_(-7)
+    c.qmm.qmm_lora(c.op())
+    R.check(c.y, want, err)
+    assert c.qmm.qmm_last_device_error() == 0

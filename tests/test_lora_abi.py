@@ -36,7 +36,7 @@ def test_refusals(qmm):
         assert _call(qmm, **bad) == 1, bad
     for bad in ({"K": 0}, {"K": 48}, {"K": 1 << 25, "ldx": 1 << 25, "lda": 1 << 25}, {"max_rank": 257, "ldb": 257},
                 {"T": 7}, {"n_segs": 65537, "T": 65537}, {"T": (1 << 28) + 1, "n_segs": 1}, {"N": 1 << 29, "ldy": 1 << 29, "ld_base": 1 << 29},
-                {"ldx": 1 << 41}, {"lda": (1 << 24) + 32}, {"b_stride": 1 << 41}, {"ld_base": 48}):
+                {"ldx": 1 << 41}, {"lda": 1 << 41}, {"b_stride": 1 << 41}, {"ld_base": 48}):
         assert _call(qmm, **bad) == 2, bad
     for bad in ({"x": A16 + 8}, {"ldx": 66}, {"a": A16 + 8}, {"lda": 68}, {"a_stride": 516}, {"b": A16 + 1},
                 {"y": A16 + 2, "base": None}, {"base": A16 + 2}, {"ranks": A16 + 2}, {"scales": A16 + 2},
