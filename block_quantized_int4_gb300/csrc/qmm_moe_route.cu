@@ -66,15 +66,13 @@ extern "C" qmm_status qmm_moe_route(const qmm_moe_route_op* op, void* stream) {
     a.top2 = op->group_score == QMM_ROUTE_GROUP_TOP2;
     a.renorm = op->renormalize != 0;
     a.scale = op->scale;
-    // Lanes hold 1, 2, 4, .. 32 experts of one group.  Where these do not
-    // divide the groups they hold as few as share a group out, by plain loads.
+    // Lanes hold 1, 2, 4, .. 32 experts of one group, up to four side by side.
     const int lanes = 32 / a.n_groups;
     int slot = 0;
     while ((lanes << slot) < a.group_size) ++slot;
-    const size_t size = size_of(op->dtype), vec = std::min<size_t>(16, size << slot);
-    const bool even = a.n_groups == 1 || a.group_size % (1 << slot) == 0;
-    a.per = even ? 1 << slot : (a.group_size + lanes - 1) / lanes;
-    a.vec = even && !off(op->logits, vec) && (op->T == 1 || op->ld * size % vec == 0);
+    const int beside = std::min(4, 1 << slot);
+    a.vec = a.group_size % beside == 0 && !off(op->logits, beside * size_of(op->dtype)) &&
+            (op->T == 1 || op->ld % beside == 0);
     const bool scores = op->bias || (a.n_groups > 1 && a.top2);
     const bool group = op->workspace && op->T <= ONE_BLOCK_TOKENS;
     const RouteKernel kernel = op->dtype == QMM_F32   ? route_kernel_f32(slot, scores, group)

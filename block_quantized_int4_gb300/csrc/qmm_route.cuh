@@ -41,14 +41,10 @@ __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// Ordered keys.  An expert that takes no part has -inf; 0: taken or not there.
-constexpr uint32_t KEY_OUT = 0x007FFFFFu;
+// Ordered keys.
 __device__ __forceinline__ uint32_t key32(float v) {
     const int u = __float_as_int(v + 0.f);  // -0 as +0
     return (uint32_t)(u ^ ((u >> 31) | (int)0x80000000));
-}
-__device__ __forceinline__ float value32(uint32_t k) {
-    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 __device__ __forceinline__ unsigned long long key64(double v) {
     const unsigned long long u = __double_as_longlong(v + 0.0);
@@ -57,56 +53,94 @@ __device__ __forceinline__ unsigned long long key64(double v) {
 
 // A warp's candidates and choice.
 struct __align__(16) Chosen {
-    uint32_t key[36];  // of candidates, then zeros up to a multiple of four
+    float c[36];       // of candidates, then -inf up to a multiple of four
     int cand[32];
     int id[MAX_K];     // the chosen in order; one more where the border is checked
-    float value[33];   // and their keys
+    float value[33];   // and their c
     float2 pair[32];
 };
 
-// Where a lane's experts lie: `count` of them from `first` on.
+// Where a lane's experts lie: four (two, one) side by side, and again behind
+// those of the other lanes of the group, so that loads and stores of a warp are
+// contiguous.  (With all of a lane's experts side by side 65521 tokens of 512
+// fp32 logits were bound by the shared memory's data path, 82% of its peak.)
+template <int PER>
+constexpr int BESIDE = PER < 4 ? PER : 4;
 struct Place {
-    int first, count, lanes;  // lanes: of a group
+    int first, lanes, group;  // lanes: of a group
+    int shift, step;
+    uint32_t there;  // those that there are
+
+    __device__ __forceinline__ int expert(int i) const { return first + (i >> shift) * step + (i & ((1 << shift) - 1)); }
 };
 
+template <int PER>
 __device__ __forceinline__ Place place_of(const RouteArgs& a, int lane) {
+    constexpr int V = BESIDE<PER>;
     Place p;
     p.lanes = 32 / a.n_groups;
-    const int g = lane / p.lanes, at = (lane - g * p.lanes) * a.per;
-    p.first = g * a.group_size + at;
-    p.count = max(0, min(a.per, a.group_size - at));
+    p.group = lane / p.lanes;
+    const int at = (lane - p.group * p.lanes) * V;
+    p.first = p.group * a.group_size + at;
+    p.shift = V == 4 ? 2 : V - 1;
+    p.step = p.lanes * V;
+    p.there = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) p.there |= (at + i / V * p.step + i % V < a.group_size ? 1u : 0u) << i;
     return p;
 }
 
-// A lane's logits as fp32; experts that take no part (-inf, NaN) as -inf.
+template <int BYTES>
+struct VecWord;
+template <>
+struct VecWord<16> {
+    using type = uint4;
+};
+template <>
+struct VecWord<8> {
+    using type = uint2;
+};
+template <>
+struct VecWord<4> {
+    using type = uint32_t;
+};
+template <>
+struct VecWord<2> {
+    using type = unsigned short;
+};
+
+// A lane's logits as fp32; experts that are not there as -inf.
 template <int PER, typename T>
 __device__ __forceinline__ void load_logits(const RouteArgs& a, const T* row, const Place& p, float (&l)[PER]) {
-    constexpr int BYTES = PER * (int)sizeof(T), V = BYTES < 16 ? BYTES : 16, N = V / (int)sizeof(T);
-    union Vec {
-        T e[N];
-        uint4 q;
-        uint2 d;
-        uint32_t w;
-        unsigned short h;
+    constexpr int V = BESIDE<PER>;
+    union alignas(V * sizeof(T)) Vec {
+        T e[V];
+        typename VecWord<V * (int)sizeof(T)>::type word;
     };
-    if (a.vec && p.count == PER) {
 #pragma unroll
-        for (int i = 0; i < PER; i += N) {
+    for (int i = 0; i < PER; i += V) {
+        const T* src = row + p.first + i / V * p.step;
+        if (a.vec) {
             Vec v;
-            const T* src = row + p.first + i;
-            if constexpr (V == 16) v.q = *reinterpret_cast<const uint4*>(src);
-            if constexpr (V == 8) v.d = *reinterpret_cast<const uint2*>(src);
-            if constexpr (V == 4) v.w = *reinterpret_cast<const uint32_t*>(src);
-            if constexpr (V == 2) v.h = *reinterpret_cast<const unsigned short*>(src);
+            if (p.there >> i & 1) {
+                v.word = *reinterpret_cast<const decltype(v.word)*>(src);
 #pragma unroll
-            for (int j = 0; j < N; ++j) l[i + j] = as_float(v.e[j]);
+                for (int j = 0; j < V; ++j) l[i + j] = as_float(v.e[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) l[i + j] = -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[i + j] = p.there >> (i + j) & 1 ? as_float(src[j]) : -INFINITY;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) l[i] = i < p.count ? as_float(row[p.first + i]) : -INFINITY;
     }
+}
+// Experts that take no part (-inf, NaN) as -inf.
+template <int PER>
+__device__ __forceinline__ void no_nan(float (&l)[PER]) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = fmaxf(l[i], -INFINITY);  // of a NaN: -inf
+    for (int i = 0; i < PER; ++i) l[i] = fmaxf(l[i], -INFINITY);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -120,10 +154,16 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
+// NaNs do not count.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float warp_min(float v) {
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // Logits in 64 bits -> score (0 of -inf).
@@ -158,7 +198,7 @@ __device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, con
         for (int i = 0; i < PER; ++i) c[i] = score64(a, l[i], top, sum);
         if (a.bias) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) c[i] += i < p.count ? (double)a.bias[p.first + i] : 0.0;
+            for (int i = 0; i < PER; ++i) c[i] += p.there >> i & 1 ? (double)a.bias[p.expert(i)] : 0.0;
         }
     } else {
 #pragma unroll
@@ -177,7 +217,7 @@ __device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, con
         first = fmax(first, f);
     }
     const double mine = top2 && second > -INFINITY ? first + second : first;
-    const int g = (threadIdx.x & 31) / p.lanes;
+    const int g = p.group;
     int before = 0;
     for (int h = 0; h < a.n_groups; ++h) {
         const double v = __shfl_sync(FULL, mine, h * p.lanes);
@@ -191,15 +231,16 @@ __device__ __forceinline__ bool groups64(const RouteArgs& a, const Place& p, con
 template <int PER, typename T>
 __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen& out) {
     const int lane = threadIdx.x & 31;
-    const Place p = place_of(a, lane);
+    const Place p = place_of<PER>(a, lane);
     float l[PER];
     load_logits<PER, T>(a, row, p, l);
+    no_nan(l);
     double c[PER];
     const bool stays = groups64(a, p, l, c);
     unsigned long long key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        key[i] = stays && i < p.count ? l[i] > -INFINITY ? key64(a.bias ? c[i] : (double)l[i]) : 1ull : 0ull;
+        key[i] = stays && p.there >> i & 1 ? l[i] > -INFINITY ? key64(a.bias ? c[i] : (double)l[i]) : 1ull : 0ull;
     for (int j = 0; j < a.k; ++j) {
         unsigned long long best = 0;
         int at = 0;
@@ -210,9 +251,10 @@ __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen
             }
         unsigned long long most = best;
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(FULL, most, o));
-        const int owner = __ffs(__ballot_sync(FULL, best == most)) - 1;
-        if (lane == owner) {
-            out.id[j] = p.first + at;
+        // (a lane's experts and the places in it rise together)
+        const int e = p.expert(at);
+        if (__reduce_min_sync(FULL, best == most ? e : INT_MAX) == e && best == most) {
+            out.id[j] = e;
             for (int i = 0; i < PER; ++i)
                 if (i == at) key[i] = 0;
         }
@@ -220,25 +262,23 @@ __device__ __noinline__ void route_slow(const RouteArgs& a, const T* row, Chosen
     __syncwarp();
 }
 
-// Experts of this lane in `mask` become candidates, in index order over the
-// lanes; how many there are (more than 32: none is written).
-__device__ __forceinline__ int collect(uint32_t mask, int first, const uint32_t* key, Chosen& out) {
-    const int lane = threadIdx.x & 31, have = __popc(mask);
-    int end = have;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, end, o);
-        if (lane >= o) end += v;
-    }
-    const int total = __shfl_sync(FULL, end, 31);
-    if (total > 32) return total;
+// Experts of this lane in `mask` become candidates, the first of every lane, then
+// the second ..; how many there are (more than 32: not all are written).
+template <int PER>
+__device__ __forceinline__ int collect(uint32_t mask, const Place& p, const float* values, Chosen& out) {
+    constexpr int V = BESIDE<PER>;
+    const int lane = threadIdx.x & 31;
+    int total = 0;
     __syncwarp();
-    for (int at = end - have; mask; ++at, mask &= mask - 1) {
-        const int i = __ffs(mask) - 1;
-        out.cand[at] = first + i;
-        out.key[at] = key[i];
+    for (uint32_t some; total <= 32 && (some = __ballot_sync(FULL, mask != 0)) != 0; total += __popc(some)) {
+        const int at = total + __popc(some & ((1u << lane) - 1u)), i = __ffs(mask) - 1;
+        if (mask && at < 32) {
+            out.cand[at] = p.expert(i);
+            out.c[at] = fmaxf(values[i / V * 32 * V + lane * V + i % V], -INFINITY) + 0.f;  // -0 as +0
+        }
+        mask &= mask - 1;
     }
-    if (lane < 4) out.key[total + lane] = 0;
+    if (total <= 32 && lane < 4) out.c[total + lane] = -INFINITY;
     __syncwarp();
     return total;
 }
@@ -256,12 +296,12 @@ struct Scores {
         if (!a.softmax) return;
         top = -INFINITY;
 #pragma unroll 1
-        for (int i = 0; i < p.count; ++i) top = fmaxf(top, as_float(row[p.first + i]));
+        for (uint32_t m = p.there; m; m &= m - 1) top = fmaxf(top, as_float(row[p.expert(__ffs(m) - 1)]));
         top = warp_max(top);
         if (!(top > -INFINITY)) return;
         Pair sum = {0.f, 0.f};
 #pragma unroll 1
-        for (int i = 0; i < p.count; ++i) sum = add(sum, power(as_float(row[p.first + i])));
+        for (uint32_t m = p.there; m; m &= m - 1) sum = add(sum, power(as_float(row[p.expert(__ffs(m) - 1)])));
         for (int o = 16; o > 0; o >>= 1)
             sum = add(sum, Pair{__shfl_xor_sync(FULL, sum.hi, o), __shfl_xor_sync(FULL, sum.lo, o)});
         inverse = reciprocal(sum);
@@ -286,13 +326,13 @@ __device__ __forceinline__ float distance(Pair a, Pair b) {
 // not, either.  (Short loops: code that runs for few tokens comes from afar, and
 // eight experts side by side took 15 us where these take 5.)
 template <typename T>
-__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, bool& close) {
-    const Place p = place_of(a, threadIdx.x & 31);
+__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, const Place p, uint32_t mask, bool& close) {
     const Scores s(a, row, p);
     Pair first = {-INFINITY, 0.f}, second = first;
 #pragma unroll 1
-    for (int i = 0; i < p.count; ++i) {
-        const Pair v = s.of(a, as_float(row[p.first + i]), a.bias ? a.bias[p.first + i] : 0.f);
+    for (; mask; mask &= mask - 1) {
+        const int e = p.expert(__ffs(mask) - 1);
+        const Pair v = s.of(a, as_float(row[e]), a.bias ? a.bias[e] : 0.f);
         if (before(v, first)) {
             second = first;
             first = v;
@@ -310,7 +350,7 @@ __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, bool
     const Pair mine = a.top2 && second.hi > -INFINITY ? add(first, second) : first;
     const float size = first.hi > -INFINITY ? fabsf(first.hi) + (second.hi > -INFINITY ? fabsf(second.hi) : 0.f) : 0.f;
     const float tolerance = s.tolerance(warp_max(size));
-    const int g = (threadIdx.x & 31) / p.lanes;
+    const int g = p.group;
     int ahead = 0;
     for (int h = 0; h < a.n_groups; ++h) {
         const Pair v = {__shfl_sync(FULL, mine.hi, h * p.lanes), __shfl_sync(FULL, mine.lo, h * p.lanes)};
@@ -331,9 +371,9 @@ __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, bool
 // does not tell (all that may be among the k largest are there); false: pairs do
 // not, either.
 template <typename T>
-__device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, int total, Chosen& out) {
+__device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, const Place p, int total, Chosen& out) {
     const int lane = threadIdx.x & 31;
-    const Scores s(a, row, place_of(a, lane));
+    const Scores s(a, row, p);
     const int e = lane < total ? out.cand[lane] : 0;
     const float l = fmaxf(as_float(row[e]), -INFINITY), bias = a.bias ? a.bias[e] : 0.f;
     const Pair mine = s.of(a, l, bias);
@@ -344,7 +384,7 @@ __device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, int t
     for (int d = 0; d < total; ++d) {
         const float2 q = out.pair[d];
         const Pair v = {q.x, q.y};
-        rank += before(v, mine) || (!before(mine, v) && d < lane);
+        rank += before(v, mine) || (!before(mine, v) && out.cand[d] < e);
         const float l_d = __shfl_sync(FULL, l, d), bias_d = __shfl_sync(FULL, bias, d);
         const bool same = l_d == l && bias_d == bias;
         near |= !same && distance(v, mine) <= s.tolerance(fabsf(mine.hi));
@@ -355,10 +395,10 @@ __device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, int t
 }
 
 // One token.  SCORES: the choice takes scores (a bias, or groups by the sum of
-// two), not logits alone.  keys: 32 * PER words of shared memory.
+// two), not logits alone.  values: 32 * PER words of shared memory.
 template <int PER, typename T, bool SCORES>
 __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place& p, const float (&bias)[PER],
-                                          uint32_t* keys, Chosen& out) {
+                                          float* values, Chosen& out) {
     const int lane = threadIdx.x & 31;
     const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
     const bool grouped = a.n_groups > 1, top2 = grouped && a.top2;
@@ -368,6 +408,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
     // softmax: the largest logit and the sum of exponentials
     float top = 0.f, sum = 1.f;
     if (a.softmax && (SCORES || !a.renorm)) {
+        no_nan(l);
         float m = l[0];
 #pragma unroll
         for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
@@ -380,33 +421,34 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         sum = warp_sum(sum);
     }
 
-    // keys; and the error that c and group scores may have.  Exponentials and
-    // reciprocals are off by 2^-21 of the largest score at most (an exponent's
-    // rounding, |x| 2^-24, weighs s or s (1 - s), below 0.4 / |x|), softmax by
-    // the sum's own error besides; c by its own rounding.
-    const float unit = a.softmax && SCORES ? rcp(sum) : 1.f, slack = unit * (a.softmax ? 0x1p-18f : 0x1p-19f);
-    uint32_t key[PER];
+    // what decides, with the error that a score may have.  A sigmoid's exponential
+    // is off by 2^-22 and by 1.5 |x| 2^-24 of its exponent, which weighs s (1 - s)
+    // (1/4 at most, 0.23 / |x|), 1 + e by 2^-24, its reciprocal by 2^-23: together
+    // below 4.4 * 2^-24.  A softmax's sum of up to 1024 and its reciprocal are off by
+    // 60 * 2^-24 (the terms by 4 and 2.5 |x|, with |x| 6.9 on average at most, 36
+    // additions, 2), the same for all scores, so that the difference of two has that
+    // once, and 6 * 2^-24 of the largest score for either.
+    const float unit = a.softmax && SCORES ? rcp(sum) : 1.f, slack = unit * (a.softmax ? 0x1p-18f : 0x1p-21f);
+    float c[PER];  // NaN here and there where it is the logit
     float first = -INFINITY, second = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        float c = l[i];
+        c[i] = l[i];
         if constexpr (SCORES) {
             const float e = ex2((a.softmax ? l[i] - top : -l[i]) * 1.4426950408889634f);
-            float v = a.softmax ? e * unit : rcp(1.f + e);
-            v += bias[i];
-            v = l[i] > -INFINITY ? fmaxf(v, -INFINITY) : -INFINITY;
-            if (a.bias) c = v;
+            float v = (a.softmax ? e * unit : rcp(1.f + e)) + bias[i];
+            v = l[i] > -INFINITY ? v : -INFINITY;
+            if (a.bias) c[i] = v;
             if (top2) second = fmaxf(second, fminf(first, v));
             first = fmaxf(first, v);
         }
-        key[i] = key32(c);
     }
-    uint32_t best = key[0];
+    float best = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) best = max(best, key[i]);
-    bool stays = p.count > 0, again = false;
+    for (int i = 0; i < PER; ++i) best = fmaxf(best, c[i]);
+    bool stays = p.there != 0, again = false;
     if (grouped) {
-        if constexpr (!SCORES) first = p.count > 0 ? value32(best) : -INFINITY;
+        if constexpr (!SCORES) first = best;
         for (int o = p.lanes >> 1; o > 0; o >>= 1) {
             const float f = __shfl_xor_sync(FULL, first, o);
             if (top2) {
@@ -416,73 +458,101 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             first = fmaxf(first, f);
         }
         const float mine = top2 && second > -INFINITY ? first + second : first;
-        const int g = lane / p.lanes;
+        const uint32_t key = key32(mine);
+        const int g = p.group;
+        uint32_t* keys = reinterpret_cast<uint32_t*>(out.c);
+        if (lane == g * p.lanes) keys[g] = key;
+        if (lane < 2) keys[a.n_groups + lane] = 0;
+        __syncwarp();
         int before = 0;
-#pragma unroll 1
-        for (int h = 0; h < a.n_groups; ++h) {
-            const float v = __shfl_sync(FULL, mine, h * p.lanes);
-            before += v > mine || (v == mine && h < g);
+        for (int h = 0; h < a.n_groups; h += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + h);
+            before += (v.x >= key + (h >= g)) + (v.y >= key + (h + 1 >= g)) + (v.z >= key + (h + 2 >= g)) +
+                      (v.w >= key + (h + 3 >= g));
         }
+        __syncwarp();
         bool in = before < a.top_groups;
         if constexpr (SCORES) {
             // groups on either side of the border that are too close
-            const float hi = value32(__reduce_min_sync(FULL, in ? key32(mine) : 0xFFFFFFFFu));
-            const uint32_t no = __reduce_max_sync(FULL, in ? 0u : key32(mine));
-            const float lo = no ? value32(no) : -INFINITY;
+            const float hi = warp_min(in ? mine : INFINITY), lo = warp_max(in ? -INFINITY : mine);
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
             if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size)))
-                in = groups_again(a, row, again);
+            {
+                // of these, all that may be among the best (the two best) of a group
+                const float least = (top2 ? second : first) - (2.f * slack + 0x1p-22f * size);
+                uint32_t mask = p.there;
+                if (a.bias) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) mask &= ~((c[i] < least ? 1u : 0u) << i);
+                }
+                in = groups_again(a, row, p, mask, again);
+            }
         }
         stays = stays && in;
     }
 
-    // candidates: keys from the n-th best of the lanes' best on (n = k, and one
+    // candidates: experts from the n-th best of the lanes' best on (n = k, and one
     // more where the border is checked)
     const int n = a.k + (SCORES && a.bias ? 1 : 0);
-    const uint32_t there = !stays ? 0u : PER == 32 && p.count == 32 ? 0xFFFFFFFFu : (1u << p.count) - 1u;
+    const uint32_t there = stays ? p.there : 0u;
 #pragma unroll
-    for (int i = 0; i < PER; i += PER < 4 ? PER : 4) {
+    for (int i = 0; i < PER; i += BESIDE<PER>) {
+        float* to = values + 32 * i + lane * BESIDE<PER>;
         if constexpr (PER >= 4)
-            *reinterpret_cast<uint4*>(keys + lane * PER + i) = make_uint4(key[i], key[i + 1], key[i + 2], key[i + 3]);
+            *reinterpret_cast<float4*>(to) = make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
         else if constexpr (PER == 2)
-            *reinterpret_cast<uint2*>(keys + lane * PER) = make_uint2(key[0], key[1]);
+            *reinterpret_cast<float2*>(to) = make_float2(c[0], c[1]);
         else
-            keys[lane] = key[0];
+            *to = c[0];
     }
-    const auto from = [&](uint32_t floor_key) {
-        uint32_t mask = 0;
+    const auto from = [&](float floor) {
+        uint32_t mask = there;
+        if (floor > -INFINITY) {
+            mask = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mask |= (key[i] >= floor_key ? 1u : 0u) << i;
-        return collect(mask & there, p.first, keys + lane * PER, out);
+            for (int i = 0; i < PER; ++i) mask |= (c[i] >= floor ? 1u : 0u) << i;
+            mask &= there;
+        }
+        return collect<PER>(mask, p, values, out);
     };
-    uint32_t floor_key = KEY_OUT;
+    float floor = -INFINITY;
     if (n <= 32) {
         // the smallest of those that fewer than n are larger than
-        const uint32_t mine = stays ? best : 0u;
-        out.key[lane] = mine;
+        const float mine = stays ? best : -INFINITY;
+        out.c[lane] = mine;
         __syncwarp();
-        int larger = 0;
+        float larger = 0.f;  // (counted by the other pipe than the comparisons')
 #pragma unroll
         for (int d = 0; d < 32; d += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(out.key + d);
-            larger += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+            const float4 v = *reinterpret_cast<const float4*>(out.c + d);
+            if (v.x > mine) larger += 1.f;
+            if (v.y > mine) larger += 1.f;
+            if (v.z > mine) larger += 1.f;
+            if (v.w > mine) larger += 1.f;
         }
-        floor_key = max(__reduce_min_sync(FULL, larger < n ? mine : 0xFFFFFFFFu), KEY_OUT);
+        floor = warp_min(larger < (float)n ? mine : INFINITY);
     }
-    int total = from(floor_key);
+    int total = from(floor);
     again = again || total > 32;
     if (!again) {
-        // candidates lie in index order: of equal keys the earlier ranks first
-        const uint32_t mine = lane < total ? out.key[lane] : 0u;
-        int rank = 0;
+        const float mine = lane < total ? out.c[lane] : -INFINITY;
+        float larger = 0.f;
         for (int d = 0; d < total; d += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(out.key + d);
-            rank += (v.x >= mine + (d >= lane)) + (v.y >= mine + (d + 1 >= lane)) + (v.z >= mine + (d + 2 >= lane)) +
-                    (v.w >= mine + (d + 3 >= lane));
+            const float4 v = *reinterpret_cast<const float4*>(out.c + d);
+            if (v.x > mine) larger += 1.f;
+            if (v.y > mine) larger += 1.f;
+            if (v.z > mine) larger += 1.f;
+            if (v.w > mine) larger += 1.f;
         }
+        int rank = (int)larger;
+        // of equal ones the lower expert first
+        uint32_t same = __match_any_sync(FULL, __float_as_uint(mine)) & ~(1u << lane);
+        if (lane < total)
+            for (same &= 0xFFFFFFFFu >> (32 - total); same; same &= same - 1)
+                rank += out.cand[__ffs(same) - 1] < out.cand[lane];
         if (lane < total && rank < n) {
             out.id[rank] = out.cand[lane];
-            if (SCORES && a.bias) out.value[rank] = value32(mine);
+            if (SCORES && a.bias) out.value[rank] = mine;
         }
         __syncwarp();
         if (SCORES && a.bias) {
@@ -491,7 +561,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             bool close = false;
             if (lane < min(total, n) - 1) {
                 const float hi = out.value[lane], lo = out.value[lane + 1];
-                if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-22f * (fabsf(hi) + fabsf(lo)))) {
+                if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-23f * (fabsf(hi) + fabsf(lo)))) {
                     close = true;
                     if (lane + 1 < a.k) {
                         const int e = out.id[lane], f = out.id[lane + 1];
@@ -502,19 +572,22 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             if (__any_sync(FULL, close)) {
                 // all that may be among the k largest, as pairs
                 const float kth = out.value[a.k - 1];
-                total = from(max(KEY_OUT, key32(kth - (2.f * slack + 0x1p-21f * fabsf(kth)))));
-                again = total > 32 || !order_again(a, row, total, out);
+                total = from(kth - (2.f * slack + 0x1p-21f * fabsf(kth)));
+                again = total > 32 || !order_again(a, row, p, total, out);
             }
         }
     }
     if (again) route_slow<PER, T>(a, row, out);
 
     // gates of the chosen: lane j has the j-th and the (j + 32)-th
+    const int halves = a.k > 32 ? 2 : 1;
     float lj[2], s[2];
     int id[2];
     float most = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        lj[r] = -INFINITY;
+        if (r >= halves) break;
         const int j = lane + 32 * r;
         id[r] = j < a.k ? out.id[j] : 0;
         lj[r] = j < a.k ? as_float(row[id[r]]) : -INFINITY;
@@ -529,6 +602,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
     float part = 0.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        if (r >= halves) break;
         s[r] = lj[r] > -INFINITY ? (exps ? expf(lj[r] - ref) : 1.f / (1.f + expf(-lj[r]))) : 0.f;
         part += s[r];
     }
@@ -537,7 +611,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int j = lane + 32 * r;
-        if (j < a.k) {
+        if (r < halves && j < a.k) {
             a.ids[(int64_t)t * a.k + j] = id[r];
             a.gates[(int64_t)t * a.k + j] = s[r] > 0.f ? s[r] / div * a.scale : 0.f;
         }
@@ -554,14 +628,15 @@ __global__ void __launch_bounds__((GROUP ? route_group_warps(PER) : WARPS) * 32,
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int NW = GROUP ? route_group_warps(PER) : WARPS;
     __shared__ Chosen chosen[NW];
-    __shared__ __align__(16) uint32_t keys[NW][32 * PER];
+    __shared__ __align__(16) float values[NW][32 * PER];
     const int warp = threadIdx.x >> 5;
-    const Place p = place_of(a, threadIdx.x & 31);
+    const Place p = place_of<PER>(a, threadIdx.x & 31);
     float bias[PER];  // of this lane's experts, whatever the token
 #pragma unroll
-    for (int i = 0; i < PER; ++i) bias[i] = SCORES && a.bias && i < p.count ? a.bias[p.first + i] : 0.f;
+    for (int i = 0; i < PER; ++i)  // a NaN puts its expert last
+        bias[i] = SCORES && a.bias && p.there >> i & 1 ? fmaxf(a.bias[p.expert(i)], -INFINITY) : 0.f;
     for (int64_t t = (int64_t)blockIdx.x * NW + warp; t < a.T; t += (int64_t)gridDim.x * NW)
-        route_one<PER, T, SCORES>(a, (int)t, p, bias, keys[warp], chosen[warp]);
+        route_one<PER, T, SCORES>(a, (int)t, p, bias, values[warp], chosen[warp]);
     if constexpr (GROUP) {
         __syncthreads();
         moe_group_block(a.ids, a.T * a.k, a.n_groups * a.group_size, ws, err);

@@ -15,7 +15,6 @@ struct RouteArgs {
     float* gates;
     int T, k;
     int n_groups, group_size, top_groups;  // n_groups a power of two up to 32
-    int per;                               // experts of a lane
     int vec;                               // rows and lanes start on vector loads' boundaries
     int softmax, top2, renorm;
     float scale;

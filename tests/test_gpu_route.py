@@ -216,3 +216,26 @@ def test_rows_behind_the_last_token_stay():
     gates = torch.full((16, 6), -3.0, device=DEV)
     qmm.qmm_moe_route(qmm.moe_route_op(l, ids[:9], gates[:9]))
     assert (ids[9:] == -3).all() and (gates[9:] == -3).all() and (ids[:9] >= 0).all()
+
+
+@pytest.mark.parametrize("G,top2", [(1, False), (8, False), (8, True)])
+def test_outside_the_domain(G, top2):
+    """Infinite logits with softmax and biases that are not finite: some experts of the range, all others as ever."""
+    qmm, E, k = lib(), 128, 8
+    l = _logits(300, E, "f32", 9)
+    l[5::7, 3] = float("inf")
+    l[6::7, 40:50] = float("inf")
+    for value in (float("inf"), float("-inf"), float("nan")):
+        b = _bias(E, 9)
+        b[[1, 17, 90]] = value
+        for bias in (None, b):
+            for score in ("softmax", "sigmoid"):
+                ids, _ = _run(qmm, l, k, score, bias=bias, n_groups=G, top_groups=max(1, G // 2), top2=top2)
+                assert ((ids >= 0) & (ids < E)).all()
+    whole = torch.ones(300, dtype=torch.bool)
+    whole[5::7] = whole[6::7] = False
+    keep = l[whole.to(DEV)]
+    ids, gates = _run(qmm, l, k, "softmax", bias=_bias(E, 9), n_groups=G, top_groups=max(1, G // 2), top2=top2)
+    rids, rgates = _run(qmm, keep, k, "softmax", bias=_bias(E, 9), n_groups=G, top_groups=max(1, G // 2), top2=top2)
+    assert torch.equal(ids[whole.to(DEV)], rids) and torch.equal(gates[whole.to(DEV)], rgates)
+    assert qmm.qmm_last_device_error() == 0
