@@ -73,6 +73,7 @@ extern "C" qmm_status qmm_moe_route(const qmm_moe_route_op* op, void* stream) {
     const int beside = std::min(4, 1 << slot);
     a.vec = a.group_size % beside == 0 && !off(op->logits, beside * size_of(op->dtype)) &&
             (op->T == 1 || op->ld % beside == 0);
+    if (a.vec && lanes << slot == a.group_size) a.vec = 2;
     const bool scores = op->bias || (a.n_groups > 1 && a.top2);
     const bool group = op->workspace && op->T <= ONE_BLOCK_TOKENS;
     const RouteKernel kernel = op->dtype == QMM_F32   ? route_kernel_f32(slot, scores, group)

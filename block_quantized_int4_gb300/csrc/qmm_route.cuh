@@ -117,6 +117,16 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, const T* row, co
         T e[V];
         typename VecWord<V * (int)sizeof(T)>::type word;
     };
+    if (a.vec == 2) {
+#pragma unroll
+        for (int i = 0; i < PER; i += V) {
+            Vec v;
+            v.word = *reinterpret_cast<const decltype(v.word)*>(row + p.first + i / V * p.step);
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[i + j] = as_float(v.e[j]);
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < PER; i += V) {
         const T* src = row + p.first + i / V * p.step;

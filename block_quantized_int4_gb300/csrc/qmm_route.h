@@ -15,7 +15,7 @@ struct RouteArgs {
     float* gates;
     int T, k;
     int n_groups, group_size, top_groups;  // n_groups a power of two up to 32
-    int vec;                               // rows and lanes start on vector loads' boundaries
+    int vec;                               // rows and lanes start on vector loads' boundaries; 2: all lanes are full
     int softmax, top2, renorm;
     float scale;
 };
