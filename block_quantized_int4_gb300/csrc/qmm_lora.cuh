@@ -364,11 +364,15 @@ struct RowTile {
     int rows, adapter;  // rows == 0: none; adapter < 0: none
 };
 
-// The tile of this number, counting 64 rows at a time through the segments.
+// The tile of this number, counting 64 rows at a time through the segments; tiles
+// of up to 16 rows come last, where one look sees all segments: they are done
+// soon, and 64 rows that started behind 40 rows of one made a mix of 1013, 6144 ->
+// 2051, rank 24, fp16 take 52 us instead of 43.
 // Every thread of the block; starts that are out of order or out of range are
 // brought into it (the first block looks at all of them).
 __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
-    __shared__ int s_sum[WARPS], s_tile[3];
+    __shared__ uint32_t s_sum[WARPS];
+    __shared__ int s_tile[3];
     RowTile t = {0, 0, -1};
     int seg = -1;
     if (!a.seg_start) {
@@ -381,39 +385,47 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
     } else {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (threadIdx.x == 0) s_tile[2] = 0;
+        // counts of both kinds in one number: below 2^23, and up to 256
+        const bool split = a.n_segs <= THREADS && a.T <= 1 << 27;
+        const uint32_t counts = split ? 0x7FFFFFu : 0xFFFFFFFFu;
+        const int shift = a.tile_rows == 64 ? 6 : 5;
         int before = 0;
         for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
             const int s = s0 + threadIdx.x;
-            int n = 0, first = 0, last = 0;
+            int n = 0, few = 0, first = 0, last = 0;
             if (s < a.n_segs && threadIdx.x < THREADS) {
                 const int f = a.seg_start[s], l = a.seg_start[s + 1];
                 first = max(0, min(f, (int)a.T));
                 last = max(first, min(l, (int)a.T));
                 if (blockIdx.x == 0 && (first != f || last != l)) atomicOr(a.err, ERR_BAD_INDEX);
-                n = (last - first + a.tile_rows - 1) / a.tile_rows;
+                n = (last - first + a.tile_rows - 1) >> shift;
+                const int left = (last - first) & (a.tile_rows - 1);
+                few = split && left > 0 && left <= 16;
+                n -= few;
             }
-            int end = n;
+            uint32_t end = n | (uint32_t)few << 23;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(FULL, end, o);
+                const uint32_t v = __shfl_up_sync(FULL, end, o);
                 if (lane >= o) end += v;
             }
             if (lane == 31 && warp < WARPS) s_sum[warp] = end;
             __syncthreads();
-            int all = 0;
+            uint32_t all = 0;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 if (w < warp) end += s_sum[w];
                 all += s_sum[w];
             }
-            const int at = tile - (before + end - n);
-            if (at >= 0 && at < n) {
+            int at = tile - (before + (int)(end & counts) - n), tiles = n;
+            if (few && tile - (int)(all & counts) == (int)(end >> 23) - 1) at = n, tiles = n + 1;
+            if (at >= 0 && at < tiles) {
                 s_tile[0] = s;
                 s_tile[1] = first + at * a.tile_rows;
                 s_tile[2] = min(a.tile_rows, last - first - at * a.tile_rows);
             }
             __syncthreads();
-            before += all;
+            before += (int)(all & counts);
             if (before > tile && blockIdx.x != 0) break;
         }
         seg = s_tile[0];
