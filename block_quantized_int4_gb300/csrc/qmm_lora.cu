@@ -46,19 +46,19 @@ qmm_status check(const qmm_lora_op& op) {
     return QMM_OK;
 }
 
-LoraKernel kernel_of(int x, int w, bool f32, int tile) {
-    static LoraKernel (*const kernels[3][3])(bool, int) = {
+LoraKernel kernel_of(int x, int w, bool f32, bool whole, int tile) {
+    static LoraKernel (*const kernels[3][3])(bool, bool, int) = {
         {lora_kernel_f32_f32, lora_kernel_f32_f16, lora_kernel_f32_bf16},
         {lora_kernel_f16_f32, lora_kernel_f16_f16, lora_kernel_f16_bf16},
         {lora_kernel_bf16_f32, lora_kernel_bf16_f16, lora_kernel_bf16_bf16}};
     static_assert(QMM_F32 == 0 && QMM_F16 == 1 && QMM_BF16 == 2, "the order of the types");
-    return kernels[x][w](f32, tile);
+    return kernels[x][w](f32, whole, tile);
 }
 
 // Opts a kernel into the device's shared memory, once a device.
 bool prepared(LoraKernel k, int kind, int optin) {
     static std::mutex mu;
-    static bool done[64][54];
+    static bool done[64][108];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(mu);
@@ -113,8 +113,12 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int room = (op->max_rank + rt - 1) / rt * rt;
     const int xs = size_of(op->x_dtype), ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
     a.vec_b = even(op->b, op->ldb, ws, 16) && (op->b_stride * ws) % 16 == 0;
-    a.vec_base = op->base && even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16);
-    a.vec_out = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16) && (a.vec_base || !op->base);
+    a.vec_out = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16) &&
+                (!op->base || even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16));
+    // Outputs of 16 bytes, with base through the ring: a kernel of its own.  (One for
+    // both had the registers and the code of both: 4093 rows of 8192 -> 28672, bf16,
+    // 173 us instead of 164, 2039 rows of 5632 -> 8192, fp32, 54 instead of 48.)
+    const bool whole = a.vec_out && a.N % 8 == 0;
     // Tiles: of each segment's rows, the last one short.
     a.tile_rows = room > 128 ? 32 : 64;
     const int64_t rows = op->seg_start ? op->T : a.seg_rows;
@@ -139,15 +143,15 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.frag_at = 4 * 16 * (room + 8) * 4;
     a.ring_at = (a.frag_at + mtiles * 16 * room * frag + 127) / 128 * 128;
     const int chunk = LORA_CHUNK * (mtiles * 16 * xs + rt * ws);
-    const int block = 32 * (room * ws + (a.vec_base ? tile_rows * ys : 0));
+    const int block = 32 * (room * ws + (whole && op->base ? tile_rows * ys : 0));
     const int total = (tile == 0 ? 72 : 110) * 1024;  // three CTAs an SM, two
     const int least = (std::max(chunk, block) + 127) / 128 * 128, most = std::max(4 * chunk, 8 / m2 * block);
     const int share = (total - a.ring_at) / 4 / 128 * 128;
     a.slot_bytes = std::max(least, std::min(most, share));
     a.depth = std::max(2, std::min(4, (total - a.ring_at) / a.slot_bytes));
     const size_t smem = a.ring_at + (size_t)a.depth * a.slot_bytes;
-    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, tile);
-    if (!prepared(kernel, ((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 3 + tile, optin)) return QMM_ERR_CUDA;
+    const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, whole, tile);
+    if (!prepared(kernel, (((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 2 + whole) * 3 + tile, optin)) return QMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c));
     cfg.blockDim = dim3(256 + 32 * (rt == 16 ? LORA_COPIERS<16> : LORA_COPIERS<64>));

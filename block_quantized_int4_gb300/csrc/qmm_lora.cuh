@@ -452,12 +452,22 @@ struct Eight {
     float v[8];
 };
 
-// The end of a row, or what does not lie on 16-byte boundaries: y = e (+ base).
+// A row's part of rows that start anywhere: y = e (+ base) at two of every eight
+// columns, so that four lanes store eight side by side.  (y may be base: all loads
+// first, and of its own values.)
 template <typename Y>
 __device__ __noinline__ void finish_plain(Y* p, const Y* base, int n, Eight e) {
+    Y b[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) put(p + j, base ? as_float(base[j]) + e.v[j] : e.v[j]);
+    for (int j = 0; j < 8; ++j) {
+        const int at = (j >> 1) * 8 + (j & 1);
+        b[j] = base && at < n ? base[at] : Y(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int at = (j >> 1) * 8 + (j & 1);
+        if (at < n) put(p + at, as_float(b[j]) + e.v[j]);
+    }
 }
 
 __device__ __forceinline__ void store16(void* p, uint4 v, bool in) {
@@ -499,7 +509,7 @@ __device__ __noinline__ void copy_plain(uint32_t dst, const W* src, int bytes) {
 
 // ---------------------------------------------------------------- the kernel
 // RT: ranks that are multiplied at a time (of more, groups one after another).
-template <typename X, typename W, typename Y, int RT>
+template <typename X, typename W, typename Y, int RT, bool WHOLE>
 struct Work {
     static constexpr int XU = LORA_CHUNK * sizeof(X) / 16, AU = LORA_CHUNK * sizeof(W) / 16, BU = RT * sizeof(W) / 16;
     static constexpr int XE = 16 / sizeof(X), WE = 16 / sizeof(W), YE = 16 / sizeof(Y);
@@ -525,7 +535,7 @@ struct Work {
     // MMA i, q / 2 * 8 + 2 i + q % 2 = col: a lane's outputs are then eight
     // consecutive columns.
     __device__ static __forceinline__ int place(int col) {
-        return (col & ~31) | (((col >> 1) & 3) * 8 + ((col >> 3) & 3) * 2 + (col & 1));
+        return !WHOLE ? col : (col & ~31) | (((col >> 1) & 3) * 8 + ((col >> 3) & 3) * 2 + (col & 1));
     }
 
     // The warp that copies.  Counts are constants where whole tiles are there;
@@ -591,7 +601,7 @@ struct Work {
                 }
             }
         }
-        if (a.vec_base) {
+        if (WHOLE && a.base) {
             // a row is 4 to 64 units: whole ones, or 32 units at a time
             const int shift = blk_shift + (YU == 8 ? 3 : 2), wide = max(0, shift - 5), s = min(shift, 5);
             const int row = (lane >> s) + copier * (32 >> s), step = COPIERS * 32 >> s;
@@ -614,10 +624,10 @@ struct Work {
     }
 };
 
-template <typename X, typename W, typename Y, int RT>
+template <typename X, typename W, typename Y, int RT, bool WHOLE>
 __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
     constexpr int ALL = THREADS + 32 * LORA_COPIERS<RT>;
-    using K = Work<X, W, Y, RT>;
+    using K = Work<X, W, Y, RT, WHOLE>;
     using H = Hidden<W, Y>;
     constexpr bool FLUSH = sizeof(X) == 4 || sizeof(W) == 4 || sizeof(Y) == 4;
     constexpr int NT = RT / 16;  // blocks of 8 ranks of a warp: half of RT
@@ -708,7 +718,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         k.n_end = nb1 * 32;
         k.wb = static_cast<const W*>(a.b) + t.adapter * a.b_stride + (k.n_begin + tid / K::BU) * a.ldb + tid % K::BU * K::WE;
         k.blk_shift = 3 - mshift;
-        const int block = 32 * (groups * K::BT::pitch + (a.vec_base ? t.rows * (int)sizeof(Y) : 0));
+        const int block = 32 * (groups * K::BT::pitch + (WHOLE && base ? t.rows * (int)sizeof(Y) : 0));
         while (k.blk_shift && (block << k.blk_shift) > slot_bytes) --k.blk_shift;
         k.per = 32 << k.blk_shift;
         k.base_at = k.per * groups * K::BT::pitch;
@@ -873,7 +883,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
 
     // 3. the columns; a warp takes 16 rows of a 32-column block
     const int blk = warp >> mshift, r0 = mt * 16 + g;
-    const bool in0 = r0 < t.rows, in1 = r0 + 8 < t.rows, vec_base = a.vec_base;
+    const bool in0 = r0 < t.rows, in1 = r0 + 8 < t.rows;
     const uint32_t frag = smem_u32(smem) + a.frag_at + mt * (room / 16) * H::bytes + lane * 16;
     // base of rows g and g + 8; rows that are not there read the last one's
     uint32_t base_of[2];
@@ -889,7 +899,8 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         b_at[st] = place8<W, K::BU, 4>(blk * 32, st);
         asm volatile("" : "+r"(b_at[st]));
     }
-    int n = k.n_begin + blk * 32 + 8 * c;
+    constexpr int FIRST = WHOLE ? 8 : 2;  // a lane's columns in a block start at c times this
+    int n = k.n_begin + blk * 32 + FIRST * c;
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
     for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
@@ -898,7 +909,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         const int at_slot = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
         parity ^= slot == 0;
-        if (mt >= mtiles || blk >= 1 << k.blk_shift || n - 8 * c >= k.n_end) {
+        if (mt >= mtiles || blk >= 1 << k.blk_shift || n - FIRST * c >= k.n_end) {
             if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
             continue;
         }
@@ -929,7 +940,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             e0.v[2 * i] = d[i][0], e0.v[2 * i + 1] = d[i][1];
             e1.v[2 * i] = d[i][2], e1.v[2 * i + 1] = d[i][3];
         }
-        if (vec_base) {
+        if (WHOLE && base) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 Eight& e = h ? e1 : e0;
@@ -953,11 +964,11 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             }
         }
         if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
-        if (a.vec_out && n - 8 * c + 32 <= N) {
-            store_eight(y0, e0, in0);
-            store_eight(y1, e1, in1);
+        if constexpr (WHOLE) {
+            store_eight(y0, e0, in0 && n < N);
+            store_eight(y1, e1, in1 && n < N);
         } else {
-            const Y* b = base && !vec_base ? base + (t.row + r0) * a.ld_base + n : nullptr;
+            const Y* b = base ? base + (t.row + r0) * a.ld_base + n : nullptr;
             if (in0) finish_plain(y0, b, N - n, e0);
             if (in1) finish_plain(y1, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
         }
@@ -965,16 +976,18 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     if (cs) cluster_wait();
 }
 
-template <typename X, typename W, typename Y>
+template <typename X, typename W, typename Y, bool WHOLE>
 LoraKernel kernel_of_rank(int tile) {
-    return tile == 0   ? lora_kernel<X, W, Y, 16>
-           : tile == 1 ? lora_kernel<X, W, Y, 32>
-                       : lora_kernel<X, W, Y, 64>;
+    return tile == 0   ? lora_kernel<X, W, Y, 16, WHOLE>
+           : tile == 1 ? lora_kernel<X, W, Y, 32, WHOLE>
+                       : lora_kernel<X, W, Y, 64, WHOLE>;
 }
 
 template <typename X, typename W>
-LoraKernel kernel_of(bool f32, int tile) {
-    return f32 ? kernel_of_rank<X, W, float>(tile) : kernel_of_rank<X, W, X>(tile);
+LoraKernel kernel_of(bool f32, bool whole, int tile) {
+    return f32 ? whole ? kernel_of_rank<X, W, float, true>(tile) : kernel_of_rank<X, W, float, false>(tile)
+               : whole ? kernel_of_rank<X, W, X, true>(tile)
+                       : kernel_of_rank<X, W, X, false>(tile);
 }
 
 }  // namespace lora

@@ -24,7 +24,7 @@ struct LoraArgs {
     int N, K, n_segs, seg_rows, n_adapters, max_rank;
     int tile_rows;                 // at most
     int cluster_shift;             // of the CTAs of a tile, a power of two
-    int vec_b, vec_base, vec_out;  // rows on 16-byte boundaries: of B, of base, of y and base (if any)
+    int vec_b, vec_out;            // rows on 16-byte boundaries: of B, of y and base (if any)
     // shared memory: parts of h, its fragments, the ring's slots
     int frag_at, ring_at, slot_bytes, depth;
     int* err;
@@ -35,15 +35,16 @@ struct LoraArgs {
 using LoraKernel = void (*)(LoraArgs);
 
 // Kernels by the types of x and of the adapters; f32: fp32 base and y, else
-// x's type; tile: 16, 32 or 64 ranks at a time.
-LoraKernel lora_kernel_f32_f32(bool f32, int tile);
-LoraKernel lora_kernel_f32_f16(bool f32, int tile);
-LoraKernel lora_kernel_f32_bf16(bool f32, int tile);
-LoraKernel lora_kernel_f16_f32(bool f32, int tile);
-LoraKernel lora_kernel_f16_f16(bool f32, int tile);
-LoraKernel lora_kernel_f16_bf16(bool f32, int tile);
-LoraKernel lora_kernel_bf16_f32(bool f32, int tile);
-LoraKernel lora_kernel_bf16_f16(bool f32, int tile);
-LoraKernel lora_kernel_bf16_bf16(bool f32, int tile);
+// x's type; whole: rows of y and base on 16-byte boundaries and of a multiple of
+// eight columns; tile: 16, 32 or 64 ranks at a time.
+LoraKernel lora_kernel_f32_f32(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_f32_f16(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_f32_bf16(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_f16_f32(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_f16_f16(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_f16_bf16(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_bf16_f32(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_bf16_f16(bool f32, bool whole, int tile);
+LoraKernel lora_kernel_bf16_bf16(bool f32, bool whole, int tile);
 
 }  // namespace qmm

@@ -3,6 +3,8 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_bf16_f16(bool f32, int tile) { return lora::kernel_of<__nv_bfloat16, __half>(f32, tile); }
+LoraKernel lora_kernel_bf16_f16(bool f32, bool whole, int tile) {
+    return lora::kernel_of<__nv_bfloat16, __half>(f32, whole, tile);
+}
 
 }  // namespace qmm

@@ -3,6 +3,8 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f16_f32(bool f32, int tile) { return lora::kernel_of<__half, float>(f32, tile); }
+LoraKernel lora_kernel_f16_f32(bool f32, bool whole, int tile) {
+    return lora::kernel_of<__half, float>(f32, whole, tile);
+}
 
 }  // namespace qmm

@@ -3,6 +3,8 @@
 
 namespace qmm {
 
-LoraKernel lora_kernel_f32_bf16(bool f32, int tile) { return lora::kernel_of<float, __nv_bfloat16>(f32, tile); }
+LoraKernel lora_kernel_f32_bf16(bool f32, bool whole, int tile) {
+    return lora::kernel_of<float, __nv_bfloat16>(f32, whole, tile);
+}
 
 }  // namespace qmm
