@@ -15,10 +15,10 @@
 //    what these do not order either, in 64 bits (route_slow).  (All of the close
 //    ones in 64 bits, at 16 cycles an instruction: 32003 tokens of 256 experts in
 //    8 groups 44 us, with these 10 us the last of them.)
-//  - the k-th largest of the 32 lanes' best keys bounds the k-th largest key
-//    from below, so that only keys from there on are candidates: about 1.3 k
-//    of them, one a lane, each ranked against all others.  (More than 32, as
-//    with most experts switched off: route_slow, too.)
+//  - the k-th largest of the 32 lanes' best bounds the k-th largest from below,
+//    so that only experts from there on are candidates: about 1.3 k of them, one
+//    a lane, each ranked against all others.  More than 32, as with most experts
+//    switched off or in few lanes: k rounds over all.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,9 +55,11 @@ __device__ __forceinline__ unsigned long long key64(double v) {
 struct __align__(16) Chosen {
     float c[36];       // of candidates, then -inf up to a multiple of four
     int cand[32];
-    int id[MAX_K];     // the chosen in order; one more where the border is checked
-    float value[33];   // and their c
-    float2 pair[32];
+    int id[MAX_K + 1];  // the chosen in order; one more where the border is checked
+    union {
+        float value[MAX_K + 1];  // and their c
+        float2 pair[32];
+    };
 };
 
 // Where a lane's experts lie: four (two, one) side by side, and again behind
@@ -280,7 +282,7 @@ __device__ __forceinline__ int collect(uint32_t mask, const Place& p, const floa
     const int lane = threadIdx.x & 31;
     int total = 0;
     __syncwarp();
-    for (uint32_t some; total <= 32 && (some = __ballot_sync(FULL, mask != 0)) != 0; total += __popc(some)) {
+    for (uint32_t some; (some = __ballot_sync(FULL, mask != 0)) != 0; total += __popc(some)) {
         const int at = total + __popc(some & ((1u << lane) - 1u)), i = __ffs(mask) - 1;
         if (mask && at < 32) {
             out.cand[at] = p.expert(i);
@@ -291,6 +293,38 @@ __device__ __forceinline__ int collect(uint32_t mask, const Place& p, const floa
     if (total <= 32 && lane < 4) out.c[total + lane] = -INFINITY;
     __syncwarp();
     return total;
+}
+
+// The n first of the experts that are `there` by n rounds over all: where more than
+// 32 may be among them.
+template <int PER>
+__device__ __noinline__ void pick(uint32_t there, const Place p, const float* values, int n, Chosen& out) {
+    constexpr int V = BESIDE<PER>;
+    const int lane = threadIdx.x & 31;
+    uint32_t key[PER];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        key[i] = there >> i & 1 ? key32(fmaxf(values[i / V * 32 * V + lane * V + i % V], -INFINITY)) : 0u;
+#pragma unroll 1
+    for (int r = 0; r < n; ++r) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] >= best) best = key[i], at = i;
+        const uint32_t most = __reduce_max_sync(FULL, best);
+        // (a lane's experts and the places in it rise together)
+        const int e = p.expert(at), first = __reduce_min_sync(FULL, best == most ? e : INT_MAX);
+        if (best == most && e == first) {
+            out.id[r] = e;
+            out.value[r] = __uint_as_float(most ^ ((most >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i == at) key[i] = 0;
+        }
+    }
+    __syncwarp();
 }
 
 // Scores as pairs: their largest error, 2^-42 of `unit` (1, or a softmax's
@@ -543,8 +577,10 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
         floor = warp_min(larger < (float)n ? mine : INFINITY);
     }
     int total = from(floor);
-    again = again || total > 32;
-    if (!again) {
+    if (total > 32) {
+        __syncwarp();
+        pick<PER>(there, p, values, n, out);
+    } else {
         const float mine = lane < total ? out.c[lane] : -INFINITY;
         float larger = 0.f;
         for (int d = 0; d < total; d += 4) {
@@ -565,26 +601,27 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             if (SCORES && a.bias) out.value[rank] = mine;
         }
         __syncwarp();
-        if (SCORES && a.bias) {
-            // neighbours that are too close, but for equal logits with equal biases
-            // among the chosen (at the border a third may be close to both)
-            bool close = false;
-            if (lane < min(total, n) - 1) {
-                const float hi = out.value[lane], lo = out.value[lane + 1];
-                if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-23f * (fabsf(hi) + fabsf(lo)))) {
-                    close = true;
-                    if (lane + 1 < a.k) {
-                        const int e = out.id[lane], f = out.id[lane + 1];
-                        close = !(as_float(row[e]) == as_float(row[f]) && a.bias[e] == a.bias[f]);
-                    }
+    }
+    if (SCORES && a.bias) {
+        // neighbours that are too close, but for equal logits with equal biases
+        // among the chosen (at the border a third may be close to both)
+        bool close = false;
+        for (int j = lane; j < min(total, n) - 1; j += 32) {
+            const float hi = out.value[j], lo = out.value[j + 1];
+            if (lo > -INFINITY && !(hi - lo > 2.f * slack + 0x1p-23f * (fabsf(hi) + fabsf(lo)))) {
+                bool differ = true;
+                if (j + 1 < a.k) {
+                    const int e = out.id[j], f = out.id[j + 1];
+                    differ = !(as_float(row[e]) == as_float(row[f]) && a.bias[e] == a.bias[f]);
                 }
+                close = close || differ;
             }
-            if (__any_sync(FULL, close)) {
-                // all that may be among the k largest, as pairs
-                const float kth = out.value[a.k - 1];
-                total = from(kth - (2.f * slack + 0x1p-21f * fabsf(kth)));
-                again = total > 32 || !order_again(a, row, p, total, out);
-            }
+        }
+        if (!again && __any_sync(FULL, close)) {
+            // all that may be among the k largest, as pairs
+            const float kth = out.value[a.k - 1];
+            total = from(kth - (2.f * slack + 0x1p-21f * fabsf(kth)));
+            again = total > 32 || !order_again(a, row, p, total, out);
         }
     }
     if (again) route_slow<PER, T>(a, row, out);

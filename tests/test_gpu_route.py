@@ -239,3 +239,14 @@ def test_outside_the_domain(G, top2):
     rids, rgates = _run(qmm, keep, k, "softmax", bias=_bias(E, 9), n_groups=G, top_groups=max(1, G // 2), top2=top2)
     assert torch.equal(ids[whole.to(DEV)], rids) and torch.equal(gates[whole.to(DEV)], rgates)
     assert qmm.qmm_last_device_error() == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_more_candidates_than_lanes(score):
+    """Few experts left, or few lanes with all of them: chosen in rounds, the switched off ones last and by index."""
+    for E, k, G, top in [(56, 13, 8, 6), (384, 14, 8, 1), (128, 16, 2, 1), (512, 33, 1, 1), (1024, 64, 32, 2), (72, 15, 1, 1)]:
+        for dtype, masked in [("f32", 0.0), ("bf16", 0.0), ("f16", 0.9)]:
+            l = _logits(211, E, dtype, E + k, masked=masked)
+            for bias in (None, _bias(E, k)):
+                for top2 in ((False, True) if G > 1 else (False,)):
+                    _check(lib(), l, k, score, bias, n_groups=G, top_groups=top, top2=top2, renorm=k % 2 == 0)
