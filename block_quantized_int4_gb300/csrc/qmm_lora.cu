@@ -112,7 +112,8 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int tile = op->max_rank <= 16 ? 0 : op->max_rank <= 32 ? 1 : 2, rt = 16 << tile;
     const int room = (op->max_rank + rt - 1) / rt * rt;
     const int xs = size_of(op->x_dtype), ws = size_of(op->w_dtype), ys = size_of(op->y_dtype);
-    a.vec_b = even(op->b, op->ldb, ws, 16) && (op->b_stride * ws) % 16 == 0;
+    const auto even_b = [&](int to) { return even(op->b, op->ldb, ws, to) && (op->b_stride * ws) % to == 0; };
+    a.vec_b = even_b(16) ? 16 : even_b(4) ? 4 : 0;
     a.vec_out = even(op->y, op->T > 1 ? op->ldy : 0, ys, 16) &&
                 (!op->base || even(op->base, op->T > 1 ? op->ld_base : 0, ys, 16));
     // Outputs of 16 bytes, with base through the ring: a kernel of its own.  (One for
@@ -136,6 +137,14 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     int64_t c = busy * LORA_MAX_CLUSTER <= room_for ? LORA_MAX_CLUSTER : 4;
     while (c > 1 && c * LORA_CHUNK > op->K) c /= 2;
     while ((1 << a.cluster_shift) < c) ++a.cluster_shift;
+    // Clusters of a tile: more while all find room at once and a CTA keeps 256 columns,
+    // or 1024 where h is dear and B's copies are not.  (One row of 5632 -> 8192, rank
+    // 14, 16.4 and 9.2 us, 206 of 10112 -> 28672, rank 64, 73.5 and 42.8; 645 of 4096
+    // -> 8066, rank 128, 77.9 and with 512 columns 105; 9 of 8192 -> 5632, rank 85, rows
+    // of B on 4 bytes, 101 and with 352 75.)
+    const int64_t blocks = (op->N + 31) / 32, keep = room > 64 && a.vec_b == 16 ? 32 : 8;
+    while ((tiles * c << (a.parts_shift + 1)) <= room_for && blocks >> (a.cluster_shift + a.parts_shift + 1) >= keep)
+        ++a.parts_shift;
     // Shared memory: the parts of h (of 16-row blocks, one to four of a tile's and
     // four in all at most), its fragments, and the ring.
     const int m2 = mtiles > 2 ? 4 : mtiles;
@@ -153,7 +162,7 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const LoraKernel kernel = kernel_of(op->x_dtype, op->w_dtype, f32, whole, tile);
     if (!prepared(kernel, (((op->x_dtype * 3 + op->w_dtype) * 2 + f32) * 2 + whole) * 3 + tile, optin)) return QMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * c));
+    cfg.gridDim = dim3((unsigned)(tiles * c << a.parts_shift));
     cfg.blockDim = dim3(256 + 32 * (rt == 16 ? LORA_COPIERS<16> : LORA_COPIERS<64>));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);

@@ -7,6 +7,8 @@
 //   2. the parts of h meet through distributed shared memory: each CTA adds all
 //      of them up;
 //   3. y = base + h B^T: each CTA has its part of the N columns.
+// Few tiles with many columns have several clusters each, which find h each and
+// share the columns.
 // x, base and y pass once; A and B are read once a tile (from L2 where tiles
 // share an adapter).  So the bound is memory for the ranks in use: 2 r flops
 // against the 2 or 4 bytes of a value of x.
@@ -82,6 +84,10 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr) {
 // 16 bytes global -> shared, the last 16 - n of them zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// The same of 4 bytes.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // All of this thread's copies have landed.
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -491,20 +497,31 @@ __device__ __forceinline__ void store_eight(Y* p, const Eight& e, bool in) {
     }
 }
 
-// Units of B that do not lie on 16-byte boundaries.
+// A unit of B whose rows lie on 16-byte boundaries (the last block's), on 4-byte
+// ones, or on neither: a plain store then.  Nothing is read for no bytes.
 template <typename W>
-__device__ __noinline__ void copy_plain(uint32_t dst, const W* src, int bytes) {
-    uint32_t v[4] = {0, 0, 0, 0};
+__device__ __noinline__ void copy_uneven(uint32_t dst, const W* src, int bytes, int vec, const void* safe) {
+    if (vec == 16) {
+        copy16(dst, bytes ? src : safe, bytes);
+    } else if (vec == 4) {
 #pragma unroll
-    for (int e = 0; e < 16 / (int)sizeof(W); ++e)
-        if (e * (int)sizeof(W) < bytes) {
-            if constexpr (sizeof(W) == 4)
-                v[e] = reinterpret_cast<const uint32_t*>(src)[e];
-            else
-                v[e >> 1] |= (uint32_t) reinterpret_cast<const unsigned short*>(src)[e] << (16 * (e & 1));
+        for (int q = 0; q < 4; ++q) {
+            const int n = max(0, min(4, bytes - 4 * q));
+            copy4(dst + 4 * q, n ? reinterpret_cast<const uint32_t*>(src) + q : safe, n);
         }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
+    } else {
+        uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 16 / (int)sizeof(W); ++e)
+            if (e * (int)sizeof(W) < bytes) {
+                if constexpr (sizeof(W) == 4)
+                    v[e] = reinterpret_cast<const uint32_t*>(src)[e];
+                else
+                    v[e >> 1] |= (uint32_t) reinterpret_cast<const unsigned short*>(src)[e] << (16 * (e & 1));
+            }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+    }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -578,7 +595,7 @@ struct Work {
         constexpr int BS = 32 / BU;  // 32 columns are BU copies of a lane
         const int lane = threadIdx.x & 31, cols = min(per, n_end - n), col = lane / BU, unit = lane % BU;
         const W* src = wb + (n - n_begin) * a.ldb;
-        const bool plain = !a.vec_b || n + cols > a.N;
+        const bool whole = a.vec_b == 16 && n + cols <= a.N;
 #pragma unroll 1
         for (int g = 0; g < groups; ++g, src += RT) {
             const int bytes = max(0, min(16, (rank - g * RT - unit * WE) * (int)sizeof(W)));
@@ -590,14 +607,14 @@ struct Work {
             uint32_t to = slot + g * per * BT::pitch;
 #pragma unroll 1
             for (int c0 = 0; c0 < cols; c0 += 32, to += 32 * BT::pitch, from += 32 * ld) {
-                if (!plain) {
+                if (whole) {
 #pragma unroll
                     for (int i = 0; i < PART; ++i) copy16(to + BT::at(place(c1 + i * BS), unit), from + i * BS * ld, bytes);
                 } else {
 #pragma unroll 1
                     for (int i = 0; i < PART; ++i)
-                        copy_plain(to + BT::at(place(c1 + i * BS), unit), from + i * BS * ld,
-                                   n + c0 + c1 + i * BS < a.N ? bytes : 0);
+                        copy_uneven(to + BT::at(place(c1 + i * BS), unit), from + i * BS * ld,
+                                    n + c0 + c1 + i * BS < a.N ? bytes : 0, a.vec_b, a.b);
                 }
             }
         }
@@ -616,7 +633,7 @@ struct Work {
                     copy16(slot + base_at + ((r << shift) + (u ^ base_key(r, shift))) * 16, from, left);
             }
         }
-        return plain;
+        return !a.vec_b;
     }
     // Eight lanes read a unit (two, of fp32) of four column groups of two rows.
     __device__ static __forceinline__ int base_key(int row, int shift) {
@@ -643,12 +660,14 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     // shifts: a division costs more than most of what follows
     const int cs = a.cluster_shift;
     const uint32_t cta = cs ? cluster_rank() : 0;
-    const RowTile t = find_tile(a, blockIdx.x >> cs);
+    const int parts = a.parts_shift, part = (blockIdx.x >> cs) & ((1 << parts) - 1);
+    const RowTile t = find_tile(a, blockIdx.x >> (cs + parts));
     if (t.rows == 0) return;  // of all CTAs of the cluster
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     __syncthreads();  // full is there
     const int N = a.N, blocks = (N + 31) / 32;
-    const int nb0 = (int)((int64_t)blocks * cta >> cs), nb1 = (int)((int64_t)blocks * (cta + 1) >> cs);
+    const int64_t share = (part << cs) + (int)cta;  // of the columns
+    const int nb0 = (int)(blocks * share >> (cs + parts)), nb1 = (int)(blocks * (share + 1) >> (cs + parts));
     const Y* base = static_cast<const Y*>(a.base);
     Y* y = static_cast<Y*>(a.y);
 

@@ -24,7 +24,9 @@ struct LoraArgs {
     int N, K, n_segs, seg_rows, n_adapters, max_rank;
     int tile_rows;                 // at most
     int cluster_shift;             // of the CTAs of a tile, a power of two
-    int vec_b, vec_out;            // rows on 16-byte boundaries: of B, of y and base (if any)
+    int parts_shift;               // of the clusters of a tile, which share its columns
+    int vec_b;                     // rows of B on 16-byte boundaries, on 4-byte ones, or 0
+    int vec_out;                   // rows of y and base (if any) on 16-byte boundaries
     // shared memory: parts of h, its fragments, the ring's slots
     int frag_at, ring_at, slot_bytes, depth;
     int* err;

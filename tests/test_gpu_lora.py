@@ -268,3 +268,25 @@ def test_offsets_that_pass_32_bits(x, w):
     c.qmm.qmm_lora(c.op())
     R.check(c.y, want, err)
     assert c.qmm.qmm_last_device_error() == 0
+
+
+@pytest.mark.parametrize("x,w", [("f32", "f32"), ("f32", "bf16"), ("f16", "f16"), ("bf16", "bf16")])
+def test_few_rows_with_many_columns(x, w):
+    """A tile's columns shared by several clusters: even and odd numbers of them, a cut of one CTA, no adapter."""
+    for N in (2048, 6000, 8191, 28672):
+        Case(3, N, 256, 16, [(0, 1, 0), (1, 1, 2), (1, 3, 1)], x, w, seed=N).check()
+        Case(70, N, 64, 40, [(0, 64, 0), (64, 70, -1)], x, w, seed=N).check()
+    c = Case(1, 20000, 2048, 8, [(0, 1, 0)], x, w)
+    whole = c.check()
+    c.y.copy_(c.base)
+    c.qmm.qmm_lora(c.op(in_place=True))
+    assert torch.equal(c.y, whole)
+
+
+@pytest.mark.parametrize("w", ["f32", "f16", "bf16"])
+def test_rows_of_b_on_4_bytes(w):
+    """Ranks and strides that are no multiple of 16 bytes: 4-byte copies, plain ones, and the last columns of either."""
+    for rank, bpad, bat in [(6, 0, 0), (44, 0, 0), (42, 4, 2), (7, 0, 0), (67, 0, 1), (66, 0, 4), (130, 0, 0)]:
+        for N in (64, 75, 515):
+            Case(18, N, 128, rank, [(0, 1, 1), (1, 18, 0)], "f32", w, bpad=bpad, bat=bat, seed=rank).check()
+            Case(18, N, 128, rank, [(0, 1, 1), (1, 18, 0)], "f32", w, bpad=bpad, bat=bat, ranks=[rank, 1, rank - 1]).check()
