@@ -153,7 +153,11 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     a.ring_at = (a.frag_at + mtiles * 16 * room * frag + 127) / 128 * 128;
     const int chunk = LORA_CHUNK * (mtiles * 16 * xs + rt * ws);
     const int block = 32 * (room * ws + (whole && op->base ? tile_rows * ys : 0));
-    const int total = (tile == 0 ? 72 : 110) * 1024;  // three CTAs an SM, two
+    const int64_t ctas = tiles * c << a.parts_shift;
+    // One CTA an SM, two, three: few CTAs have deeper rings.  (us with two or three and
+    // with one: 6 rows of one of 2048 -> 2048, rank 128, fp32, 28.1 and 19.8; 18 of 6144
+    // -> 2048, rank 64, fp16, 16.4 and 12.3; 645 of 4096 -> 8066, rank 128, 77.9 and 84.8.)
+    const int total = (ctas <= sms ? 220 : tile || ctas <= 2 * sms ? 110 : 72) * 1024;
     const int least = (std::max(chunk, block) + 127) / 128 * 128, most = std::max(4 * chunk, 8 / m2 * block);
     const int share = (total - a.ring_at) / 4 / 128 * 128;
     a.slot_bytes = std::max(least, std::min(most, share));

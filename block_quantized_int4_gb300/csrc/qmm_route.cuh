@@ -5,20 +5,23 @@
 // The choice is that of the scores in 64 bits: c_e = s_e + b_e, the group
 // scores, and equal values to the lower index.  Without a bias c is replaced
 // by the logit (both scores are strictly increasing).  A warp takes a token;
-// each lane holds PER consecutive experts of one group and an ordered 32-bit
-// key of each:
-//  - a logit's own order is exact in 32 bits; c and the sums of two are
-//    computed in fp32, with a bound on their error.  Where two values whose
-//    order decides anything are closer than that bound and not of equal
-//    operands (about three tokens in a thousand of sigmoid scores with a bias,
-//    256 experts), these are computed again as sums of two fp32 numbers, and
-//    what these do not order either, in 64 bits (route_slow).  (All of the close
-//    ones in 64 bits, at 16 cycles an instruction: 32003 tokens of 256 experts in
-//    8 groups 44 us, with these 10 us the last of them.)
+// each lane holds PER experts of one group:
+//  - a logit's own order is exact; c and the sums of two are computed in fp32,
+//    with a bound on their error.  Where two values whose order decides anything
+//    are closer than that bound and not of equal operands (about one token in a
+//    thousand of sigmoid scores with a bias, 256 experts), these are computed
+//    again as sums of two fp32 numbers, and what these do not order either, in 64
+//    bits (route_slow).  (All of the close ones in 64 bits, at 16 cycles an
+//    instruction, took 10 us more for 32003 tokens of 256 experts in 8 groups, a
+//    bound of four times the width 5.)
 //  - the k-th largest of the 32 lanes' best bounds the k-th largest from below,
 //    so that only experts from there on are candidates: about 1.3 k of them, one
 //    a lane, each ranked against all others.  More than 32, as with most experts
 //    switched off or in few lanes: k rounds over all.
+// What bounds it: the logits pass once (65521 tokens of 512, fp32: 44 us, 3.1
+// TB/s), but a token takes some 530 warp instructions, 890 with sigmoid, bias and
+// groups (32003 tokens of 256: 36 us), comparisons most of them: their pipe is 53%
+// and 60% busy at 30 warps an SM, which registers limit.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,7 +68,8 @@ struct __align__(16) Chosen {
 // Where a lane's experts lie: four (two, one) side by side, and again behind
 // those of the other lanes of the group, so that loads and stores of a warp are
 // contiguous.  (With all of a lane's experts side by side 65521 tokens of 512
-// fp32 logits were bound by the shared memory's data path, 82% of its peak.)
+// fp32 logits were bound by the shared memory's data path, 82% of its peak: 62 us
+// instead of 49.)
 template <int PER>
 constexpr int BESIDE = PER < 4 ? PER : 4;
 struct Place {
@@ -367,8 +371,9 @@ __device__ __forceinline__ float distance(Pair a, Pair b) {
 }
 
 // Whether the lane's group stays, where fp32 does not tell; `close`: pairs do
-// not, either.  (Short loops: code that runs for few tokens comes from afar, and
-// eight experts side by side took 15 us where these take 5.)
+// not, either.  mask: experts that may be among their group's best.  (Short loops:
+// code that runs for few tokens comes from afar; with eight experts side by side
+// 4864 tokens of 256 in 8 groups took 15.3 us, so 11.0, of which these tokens 3.)
 template <typename T>
 __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, const Place p, uint32_t mask, bool& close) {
     const Scores s(a, row, p);
