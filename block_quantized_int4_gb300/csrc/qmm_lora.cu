@@ -120,11 +120,16 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     // both had the registers and the code of both: 4093 rows of 8192 -> 28672, bf16,
     // 173 us instead of 164, 2039 rows of 5632 -> 8192, fp32, 54 instead of 48.)
     const bool whole = a.vec_out && a.N % 8 == 0;
-    // Tiles: of each segment's rows, the last one short.
-    a.tile_rows = room > 128 ? 32 : 64;
+    // Tiles: of each segment's rows, the last one short; fewer rows while all find an
+    // SM for each of their CTAs (33 rows of 8192 -> 1024, rank 16, 16.7 and 10.0 us; 34 of
+    // 5632 -> 1024, rank 128, 34.8 and 21.6).
     const int64_t rows = op->seg_start ? op->T : a.seg_rows;
-    const int64_t tiles = op->seg_start ? std::min(op->T, op->n_segs + op->T / a.tile_rows)
-                                        : op->n_segs * ((rows + a.tile_rows - 1) / a.tile_rows);
+    const auto tiles_of = [&](int n) {
+        return op->seg_start ? std::min(op->T, op->n_segs + op->T / n) : op->n_segs * ((rows + n - 1) / n);
+    };
+    a.tile_rows = room > 128 ? 32 : 64;
+    while (a.tile_rows > 16 && tiles_of(a.tile_rows / 2) * LORA_MAX_CLUSTER <= sms) a.tile_rows /= 2;
+    const int64_t tiles = tiles_of(a.tile_rows);
     const int tile_rows = (int)std::min<int64_t>(rows, a.tile_rows), mtiles = (tile_rows + 15) / 16;
     // CTAs of a tile: eight while the tiles find room at once (short segments
     // count half: their CTAs are done early), else four: a CTA's start, its share of h

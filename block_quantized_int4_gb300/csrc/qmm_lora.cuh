@@ -397,7 +397,7 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
         // counts of both kinds in one number: below 2^23, and up to 256
         const bool split = a.n_segs <= THREADS && a.T <= 1 << 27;
         const uint32_t counts = split ? 0x7FFFFFu : 0xFFFFFFFFu;
-        const int shift = a.tile_rows == 64 ? 6 : 5;
+        const int shift = __ffs(a.tile_rows) - 1;
         int before = 0;
         for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
             const int s = s0 + threadIdx.x;
