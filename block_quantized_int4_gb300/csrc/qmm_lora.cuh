@@ -645,7 +645,8 @@ struct Work {
 };
 
 template <typename X, typename W, typename Y, int RT, bool WHOLE>
-__global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 : 2) lora_kernel(const __grid_constant__ LoraArgs a) {
+__global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 : 2)
+    lora_kernel(const __grid_constant__ LoraArgs a) {
     constexpr int ALL = THREADS + 32 * LORA_COPIERS<RT>;
     using K = Work<X, W, Y, RT, WHOLE>;
     using H = Hidden<W, Y>;

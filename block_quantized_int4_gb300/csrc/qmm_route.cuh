@@ -672,8 +672,8 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
 }
 
 template <int PER, typename T, bool SCORES, bool GROUP>
-__global__ void __launch_bounds__((GROUP ? route_group_warps(PER) : WARPS) * 32, GROUP ? 1 : PER <= 16 ? 4 : 3) route_kernel(const __grid_constant__ RouteArgs a, MoeWs ws,
-                                                                                           int* err) {
+__global__ void __launch_bounds__((GROUP ? route_group_warps(PER) : WARPS) * 32, GROUP ? 1 : PER <= 16 ? 4 : 3)
+    route_kernel(const __grid_constant__ RouteArgs a, MoeWs ws, int* err) {
     // launched after the kernel that writes the logits, possibly early
     // (programmatic dependent launch): nothing is read before it completes
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
