@@ -134,9 +134,9 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     // CTAs of a tile: eight while the tiles find room at once (short segments
     // count half: their CTAs are done early), else four: a CTA's start, its share of h
     // and the barriers take 8 us whatever it has to do.  (us with four and with
-    // eight: one row of 2048 -> 2048, rank 16, 7.3 and 6.6; 48 of 8192 -> 8192, rank
-    // 16, 22 and 14; 2039 rows of 5632 -> 8192 65 and 60; 64 segments of one row of
-    // 2048 -> 5632, rank 64, 22 and 28; 4093 rows of 8192 -> 28672 165 and 178.)
+    // eight: one row of 2048 -> 2048, rank 16, 6.8 and 6.4; 48 of 8192 -> 8192, rank
+    // 16, 17.3 and 13.6; 2039 rows of 5632 -> 8192 66 and 45; 64 segments of one row of
+    // 2048 -> 5632, rank 64, 22.5 and 29.0; 4093 rows of 8192 -> 28672 163 and 172.)
     const int64_t room_for = (int64_t)sms * (tile == 0 ? 3 : 2);
     const int64_t busy = op->seg_start ? std::min(tiles, op->T / a.tile_rows + op->n_segs / 2) : tiles;
     int64_t c = busy * LORA_MAX_CLUSTER <= room_for ? LORA_MAX_CLUSTER : 4;
