@@ -525,8 +525,7 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             // groups on either side of the border that are too close
             const float hi = warp_min(in ? mine : INFINITY), lo = warp_max(in ? -INFINITY : mine);
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
-            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size)))
-            {
+            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size))) {
                 // of these, all that may be among the best (the two best) of a group
                 const float least = (top2 ? second : first) - (2.f * slack + 0x1p-22f * size);
                 uint32_t mask = p.there;
