@@ -30,10 +30,11 @@
 // is lost, and with fp32 on both sides the product of the lower parts, 2^-22 of
 // a term).  h is fp32.  The second product reads it in two such parts, or, of
 // bf16 B, in two parts of bf16 for 16-bit outputs (2^-18 is lost, against their
-// rounding of 2^-12 or 2^-9) and three for fp32 outputs.  Where anything is
-// fp32, sums of 64 columns leave the tensor core, which truncates, for fp32
-// additions; with fp32 outputs those of 16 ranks, too (rank 256, all fp32: error
-// 2.0e-6 of the result without).
+// rounding of 2^-12 or 2^-9) and three for fp32 outputs.  The tensor core
+// truncates its sums, so those of 64 columns leave it for fp32 additions (left
+// there, fp16 sums of 2^23 positive terms came out 1.7e-3 low; 4093 rows of 8192 ->
+// 28672, rank 64, bf16, take 168 us instead of 163); with fp32 outputs those of 16
+// ranks, too (rank 256, all fp32: error 2.0e-6 of the result without).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -650,7 +651,6 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     constexpr int ALL = THREADS + 32 * LORA_COPIERS<RT>;
     using K = Work<X, W, Y, RT, WHOLE>;
     using H = Hidden<W, Y>;
-    constexpr bool FLUSH = sizeof(X) == 4 || sizeof(W) == 4 || sizeof(Y) == 4;
     constexpr int NT = RT / 16;  // blocks of 8 ranks of a warp: half of RT
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[4];
@@ -835,17 +835,12 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                             Frag<W> wf[NT];
                             load16<X, K::XU>(xt, mt * 16, st, xf);
                             load8<W, K::AU, NT>(xt + k.a_at + place8<W, K::AU, NT>(half * (RT / 2), st), wf);
-                            if constexpr (FLUSH)
-                                multiply<X, W, NT>(d, xf, wf);
-                            else
-                                multiply<X, W, NT>(acc, xf, wf);
+                            multiply<X, W, NT>(d, xf, wf);
                         }
-                    if constexpr (FLUSH) {
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                    for (int i = 0; i < NT; ++i)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[i][e] += d[i][e];
-                    }
+                        for (int e = 0; e < 4; ++e) acc[i][e] += d[i][e];
                 }
             }
             if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, ALL);
