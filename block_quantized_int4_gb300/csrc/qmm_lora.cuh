@@ -12,7 +12,7 @@
 // x, base and y pass once; A and B are read once a tile (from L2 where tiles
 // share an adapter).  So the bound is memory for the ranks in use: 2 r flops
 // against the 2 or 4 bytes of a value of x.  Measured: 4093 rows of 8192 -> 28672,
-// rank 64, bf16, 163 us, 3.5 TB/s (fixed latencies at 17 warps an SM: the phases
+// rank 64, bf16, 171 us, 3.3 TB/s (fixed latencies at 17 warps an SM: the phases
 // take turns in a CTA, and two CTAs fill the shared memory); one row of 2048 ->
 // 2048 6.5 us, the chain of its phases, of which h's way through the cluster 3.
 //
@@ -33,7 +33,7 @@
 // rounding of 2^-12 or 2^-9) and three for fp32 outputs.  The tensor core
 // truncates its sums, so those of 64 columns leave it for fp32 additions (left
 // there, fp16 sums of 2^23 positive terms came out 1.7e-3 low; 4093 rows of 8192 ->
-// 28672, rank 64, bf16, take 168 us instead of 163); with fp32 outputs those of 16
+// 28672, rank 64, bf16, took 168 us instead of 163); with fp32 outputs those of 16
 // ranks, too (rank 256, all fp32: error 2.0e-6 of the result without).
 #pragma once
 
@@ -52,16 +52,10 @@ namespace lora {
 constexpr int WARPS = 8;             // that multiply
 constexpr int THREADS = WARPS * 32;  // of these
 
-// Between the warps that copy and those that multiply: a slot is full when the
-// copies into it have landed (an mbarrier that counts copying threads), and empty
-// when all eight warps have arrived.
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(int id, int threads) {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-constexpr int BAR_EMPTY = 1, BAR_MULTIPLY = 5;  // four of the first
+constexpr int BAR_MULTIPLY = 1;
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -99,17 +93,33 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 __device__ __forceinline__ void arrive_with_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Waits for a slot while none has run out (`live`); when one does the error word
-// says so, and what follows has no meaning but ends like the rest.
-__device__ __forceinline__ void wait_full(uint64_t* bar, uint32_t parity, const LoraArgs& a, bool& live) {
-    if (!live || mbar_try_wait(bar, parity)) return;
+// Between the warps that copy and those that multiply: a slot is full when the
+// copies into it have landed, and empty when all eight warps have read it, by
+// mbarriers that count threads.  (A named barrier for the latter is 2 to 3% faster
+// for prompts, but takes the arrivals of warps that no longer wait for others', and
+// closes without the warps that copy, which then never leave it.  Arrivals of one
+// lane a warp: 171.4 us instead of 170.6 for 4093 rows.)
+//
+// A warp waits while no wait of its CTA has run out (`live`, the same in all
+// lanes).  When one does the error word says so, and what follows has no meaning:
+// the warps that copy fill no more slots, the others read what lies there, and
+// all end as ever.
+struct Ring {
+    uint64_t full[4], empty[4];
+    int dead;  // a wait has run out
+};
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const LoraArgs& a, volatile int* dead, bool& live) {
+    if (!live || __all_sync(FULL, mbar_try_wait(bar, parity))) return;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 20000))
-        if (global_ns() - t0 > a.wait_ns) {
-            atomicOr(a.err, ERR_TIMEOUT);
+    while (!__all_sync(FULL, mbar_try_wait_sleep(bar, parity, 20000))) {
+        const bool late = global_ns() - t0 > a.wait_ns;
+        if (late) *dead = 1;
+        if (__any_sync(FULL, late || *dead)) {
+            if (late) atomicOr(a.err, ERR_TIMEOUT);
             live = false;
             return;
         }
+    }
 }
 __device__ __forceinline__ uint4 lds(uint32_t addr) {
     uint4 v;
@@ -653,9 +663,11 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     using H = Hidden<W, Y>;
     constexpr int NT = RT / 16;  // blocks of 8 ranks of a warp: half of RT
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[4];
-    if (threadIdx.x == 0)
-        for (int i = 0; i < 4; ++i) mbar_init(&full[i], 32 * K::COPIERS);
+    __shared__ Ring sync;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(&sync.full[i], 32 * K::COPIERS), mbar_init(&sync.empty[i], THREADS);
+        sync.dead = 0;
+    }
     // launched after the kernels that write x and base, possibly early
     // (programmatic dependent launch): nothing is read before they complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const RowTile t = find_tile(a, blockIdx.x >> (cs + parts));
     if (t.rows == 0) return;  // of all CTAs of the cluster
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    __syncthreads();  // full is there
+    __syncthreads();  // sync is there
     const int N = a.N, blocks = (N + 31) / 32;
     const int64_t share = (part << cs) + (int)cta;  // of the columns
     const int nb0 = (int)(blocks * share >> (cs + parts)), nb1 = (int)(blocks * (share + 1) >> (cs + parts));
@@ -755,7 +767,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int stages_n = (nb1 - nb0 + (1 << k.blk_shift) - 1) >> k.blk_shift;
     const int stages = stages_k + stages_n;
 
-    // stage s, by COPIERS warps; the last arrival may be withheld (a test's)
+    // stage s, by COPIERS warps; arrivals from the middle on may be withheld (a test's)
     const auto fill = [&](int s, int slot, int group, int chunk) {
         const uint32_t to = ring + slot * slot_bytes;
         bool plain = false;
@@ -763,14 +775,15 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             k.fill_chunks(to, group, chunk);
         else
             plain = k.fill_columns(to, k.n_begin + (s - stages_k) * k.per);
-        if (a.withhold && s == stages - 1) return;
+        if (a.withhold && s >= stages / 2) return;
         if (plain) {
             copies_wait();
-            mbar_arrive(&full[slot]);
+            mbar_arrive(&sync.full[slot]);
         } else {
-            arrive_with_copies(&full[slot]);
+            arrive_with_copies(&sync.full[slot]);
         }
     };
+    bool live = true;
     // the warps that multiply fill the ring for the first time, all at once
     {
         const int s = warp / K::COPIERS;
@@ -783,6 +796,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     }
     if (warp >= WARPS) {
         int slot = 0, group = 0, chunk = 0;
+        uint32_t parity = 0;
         const auto step = [&] {
             chunk += k.km;
             if (chunk >= k.chunks) chunk = 0, ++group;
@@ -790,10 +804,12 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         for (int s = 0; s < depth; ++s) step();
         const auto run = [&](int from, int until) {
             for (int s = from; s < until; ++s) {
-                bar_sync(BAR_EMPTY + slot, ALL);
+                wait(&sync.empty[slot], parity, a, &sync.dead, live);
+                if (!live) return;
                 fill(s, slot, group, chunk);
                 step();
                 slot = slot + 1 == depth ? 0 : slot + 1;
+                parity ^= slot == 0;
             }
         };
         // no slot is free for more before the third step
@@ -812,7 +828,9 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int ps = room + 8;
     int slot = 0;
     uint32_t parity = 0;
-    bool live = true;
+    const auto release = [&](int s, int at) {  // stage s has been read
+        if (s + depth < stages) mbar_arrive(&sync.empty[at]);
+    };
     {
         const int half = (warp >> mshift) & 1, kq = warp >> (mshift + 1);
         float* part = reinterpret_cast<float*>(smem) + (kq * mtiles * 16 + mt * 16 + g) * ps + half * (RT / 2) + 2 * c;
@@ -821,7 +839,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         // of a stage's chunks, or of a chunk's steps, those of this part of K
         const bool by_chunk = k.km >= kways;
         for (int s = 0; s < stages_k; ++s) {
-            wait_full(&full[slot], parity, a, live);
+            wait(&sync.full[slot], parity, a, &sync.dead, live);
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
                 const int chunk_bytes = k.a_at + RT * K::AT::pitch, step = by_chunk ? kways : 1;
@@ -843,7 +861,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                         for (int e = 0; e < 4; ++e) acc[i][e] += d[i][e];
                 }
             }
-            if (s + depth < stages) bar_arrive(BAR_EMPTY + slot, ALL);
+            release(s, slot);
             chunk += k.km;
             slot = slot + 1 == depth ? 0 : slot + 1;
             parity ^= slot == 0;
@@ -922,13 +940,13 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     Y* y0 = y + (t.row + r0) * a.ldy + n;
     Y* y1 = y0 + 8 * a.ldy;
     for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        wait_full(&full[slot], parity, a, live);
+        wait(&sync.full[slot], parity, a, &sync.dead, live);
         const uint32_t stage = ring + slot * slot_bytes;
         const int at_slot = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
         parity ^= slot == 0;
         if (mt >= mtiles || blk >= 1 << k.blk_shift || n - FIRST * c >= k.n_end) {
-            if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
+            release(s, at_slot);
             continue;
         }
         float d[4][4] = {};
@@ -981,7 +999,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
                 }
             }
         }
-        if (s + depth < stages) bar_arrive(BAR_EMPTY + at_slot, ALL);
+        release(s, at_slot);
         if constexpr (WHOLE) {
             store_eight(y0, e0, in0 && n < N);
             store_eight(y1, e1, in1 && n < N);

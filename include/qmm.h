@@ -243,8 +243,7 @@ QMM_API qmm_status qmm_debug_gemm_kernel(int kernel, int* previous);
  * launches that follow, process-wide: limit_ns in [1e3, 1e10] (the default is
  * 2e9, two seconds).  With withhold_last_copy = 1 the producer of every CTA (in
  * attention every warp that copies) never issues its last copy (in qmm_lora:
- * never tells of it), so the
- * wait for it runs out: the launch ends, outputs that depend on it are not
+ * never tells of its copies from the middle one on), so the wait for it runs out: the launch ends, outputs that depend on it are not
  * written (attention, qmm_lora: have no meaning), the device error word gets
  * QMM_ERR_TIMEOUT (read with qmm_last_device_error), and the context stays
  * usable; every copy that was issued lands before the CTA ends.
