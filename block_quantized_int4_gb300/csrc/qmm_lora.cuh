@@ -1009,6 +1009,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             if (in1) finish_plain(y1, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
         }
     }
+    if (!live) copies_wait();  // these warps' own, of the first stages; otherwise they have been waited for
     if (cs) cluster_wait();
 }
 
