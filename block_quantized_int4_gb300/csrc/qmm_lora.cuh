@@ -388,10 +388,12 @@ struct RowTile {
 // of up to 16 rows come last, where one look sees all segments: they are done
 // soon, and 64 rows that started behind 40 rows of one made a mix of 1013, 6144 ->
 // 2051, rank 24, fp16 take 52 us instead of 43.
-// Every thread of the block; starts that are out of order or out of range are
-// brought into it (the first block looks at all of them).
+// Every thread of the block.  A start counts as the largest of those up to it,
+// brought into [0, T], so that segments never share rows (which tiles of two CTAs
+// would write) and their tiles are never more than were launched; an order that is
+// not kept is seen between neighbours (the first block looks at all of them).
 __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
-    __shared__ uint32_t s_sum[WARPS];
+    __shared__ uint2 s_sum[WARPS];  // a warp's tiles; whether its starts are out of order or range
     __shared__ int s_tile[3];
     RowTile t = {0, 0, -1};
     int seg = -1;
@@ -409,34 +411,69 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
         const bool split = a.n_segs <= THREADS && a.T <= 1 << 27;
         const uint32_t counts = split ? 0x7FFFFFu : 0xFFFFFFFFu;
         const int shift = __ffs(a.tile_rows) - 1;
-        int before = 0;
+        int before = 0, top = 0;  // top: the largest start until now, once the order was not kept
+        bool order = true;
         for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
             const int s = s0 + threadIdx.x;
+            const bool there = s < a.n_segs && threadIdx.x < THREADS;
             int n = 0, few = 0, first = 0, last = 0;
-            if (s < a.n_segs && threadIdx.x < THREADS) {
+            bool bad = false;
+            if (there) {
                 const int f = a.seg_start[s], l = a.seg_start[s + 1];
                 first = max(0, min(f, (int)a.T));
                 last = max(first, min(l, (int)a.T));
-                if (blockIdx.x == 0 && (first != f || last != l)) atomicOr(a.err, ERR_BAD_INDEX);
+                bad = first != f || last != l;
+                if (bad && blockIdx.x == 0) atomicOr(a.err, ERR_BAD_INDEX);
+            }
+            uint32_t end = 0, all = 0, wrong = 0;
+            bool again = !order;
+            do {
+                if (again) {
+                    int most = first;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_up_sync(FULL, most, o);
+                        if (lane >= o) most = max(most, v);
+                    }
+                    __syncthreads();  // s_sum has been read
+                    if (lane == 31 && warp < WARPS) s_sum[warp].x = most;
+                    __syncthreads();
+                    most = max(most, top);
+                    for (int w = 0; w < WARPS; ++w) {
+                        const int v = (int)s_sum[w].x;
+                        if (w < warp) most = max(most, v);
+                        top = max(top, v);
+                    }
+                    __syncthreads();
+                    if (there) {
+                        first = most;
+                        last = max(most, last);
+                    }
+                }
                 n = (last - first + a.tile_rows - 1) >> shift;
                 const int left = (last - first) & (a.tile_rows - 1);
                 few = split && left > 0 && left <= 16;
                 n -= few;
-            }
-            uint32_t end = n | (uint32_t)few << 23;
+                end = n | (uint32_t)few << 23;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(FULL, end, o);
-                if (lane >= o) end += v;
-            }
-            if (lane == 31 && warp < WARPS) s_sum[warp] = end;
-            __syncthreads();
-            uint32_t all = 0;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t v = __shfl_up_sync(FULL, end, o);
+                    if (lane >= o) end += v;
+                }
+                const bool any = __any_sync(FULL, bad);
+                if (lane == 31 && warp < WARPS) s_sum[warp] = make_uint2(end, any);
+                __syncthreads();
+                all = wrong = 0;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                if (w < warp) end += s_sum[w];
-                all += s_sum[w];
-            }
+                for (int w = 0; w < WARPS; ++w) {
+                    const uint2 v = s_sum[w];
+                    if (w < warp) end += v.x;
+                    all += v.x;
+                    wrong |= v.y;
+                }
+                again = order && wrong;
+                order = order && !wrong;
+            } while (again);
             int at = tile - (before + (int)(end & counts) - n), tiles = n;
             if (few && tile - (int)(all & counts) == (int)(end >> 23) - 1) at = n, tiles = n + 1;
             if (at >= 0 && at < tiles) {

@@ -902,9 +902,10 @@ QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* 
  * else QMM_ERR_SHAPE.  x and a: 16-byte aligned, ldx, lda and a_stride
  * multiples of 16 bytes, else QMM_ERR_ALIGN; b, base and y: aligned to their
  * element (16-byte aligned rows are faster, of b 4-byte aligned ones nearly so).
- * Device values out of range set the device error word (QMM_ERR_BAD_INDEX):
- * seg_start is brought into [0, T] and into order, an adapter outside [-1, n_adapters) counts as -1, a rank
- * outside [0, max_rank] as the nearer end.  T == 0 or n_segs == 0 is a no-op.
+ * Device values out of range set the device error word (QMM_ERR_BAD_INDEX): a
+ * start below one before it, or outside [0, T], counts as the largest of those
+ * up to it, brought into [0, T]; an adapter outside [-1, n_adapters) counts as
+ * -1, a rank outside [0, max_rank] as the nearer end.  T == 0 or n_segs == 0 is a no-op.
  * One launch, no workspace. */
 typedef struct qmm_lora_op {
     const void* x;
