@@ -740,22 +740,26 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         const int first = nb0 * 32, cols = min(N, nb1 * 32) - first;
         if (a.vec_out) {
             constexpr int YE = 16 / (int)sizeof(Y);
-            const int units = cols / YE, all = units * t.rows;
-            for (int i = threadIdx.x; i < all; i += 4 * ALL) {
-                uint4 v[4];
+            // all rows as one list, or of long rows (whose list would pass 31 bits) one at a time
+            const int units = cols / YE, at_once = units <= 1 << 24 ? t.rows : 1, all = units * at_once;
+            for (int r0 = 0; r0 < t.rows; r0 += at_once)
+                for (int i = threadIdx.x; i < all; i += 4 * ALL) {
+                    uint4 v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int q = i + j * ALL, r = q / units;
-                    v[j] = make_uint4(0, 0, 0, 0);
-                    if (q < all && base)
-                        v[j] = *reinterpret_cast<const uint4*>(base + (t.row + r) * a.ld_base + first + (q - r * units) * YE);
-                }
+                    for (int j = 0; j < 4; ++j) {
+                        const int q = i + j * ALL, r = q / units;
+                        v[j] = make_uint4(0, 0, 0, 0);
+                        if (q < all && base)
+                            v[j] = *reinterpret_cast<const uint4*>(base + (t.row + r0 + r) * a.ld_base + first +
+                                                                   (q - r * units) * YE);
+                    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int q = i + j * ALL, r = q / units;
-                    if (q < all) *reinterpret_cast<uint4*>(y + (t.row + r) * a.ldy + first + (q - r * units) * YE) = v[j];
+                    for (int j = 0; j < 4; ++j) {
+                        const int q = i + j * ALL, r = q / units;
+                        if (q < all)
+                            *reinterpret_cast<uint4*>(y + (t.row + r0 + r) * a.ldy + first + (q - r * units) * YE) = v[j];
+                    }
                 }
-            }
         }
         const int done = a.vec_out ? cols - cols % (16 / (int)sizeof(Y)) : 0, left = cols - done;
         for (int n = threadIdx.x; n < left; n += ALL)
