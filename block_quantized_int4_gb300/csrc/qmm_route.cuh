@@ -525,7 +525,14 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             // groups on either side of the border that are too close
             const float hi = warp_min(in ? mine : INFINITY), lo = warp_max(in ? -INFINITY : mine);
             const float size = first > -INFINITY ? fabsf(first) + (second > -INFINITY ? fabsf(second) : 0.f) : 0.f;
-            if (lo > -INFINITY && !(hi - lo > 4.f * slack + 0x1p-21f * warp_max(size))) {
+            const float largest = warp_max(size);
+            // (sums of two biases may pass fp32: below all others they are in order with
+            // them, but not among themselves or with groups that have no experts left)
+            const bool open = lo > -INFINITY ? !(hi - lo > 4.f * slack + 0x1p-21f * largest)
+                                             : largest == INFINITY && hi <= -0x1p127f;
+            if (open && largest == INFINITY) {
+                again = true;
+            } else if (open) {
                 // of these, all that may be among the best (the two best) of a group
                 const float least = (top2 ? second : first) - (2.f * slack + 0x1p-22f * size);
                 uint32_t mask = p.there;
