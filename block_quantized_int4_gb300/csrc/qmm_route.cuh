@@ -366,10 +366,6 @@ struct Scores {
     __device__ __forceinline__ float tolerance(float size) const { return 0x1p-39f * unit + 0x1p-43f * size; }
 };
 
-__device__ __forceinline__ float distance(Pair a, Pair b) {
-    return fabsf(__fadd_rn(__fadd_rn(a.hi, -b.hi), __fadd_rn(a.lo, -b.lo)));  // NaN of two -inf
-}
-
 // Whether the lane's group stays, where fp32 does not tell; `close`: pairs do
 // not, either.  mask: experts that may be among their group's best.  (Short loops:
 // code that runs for few tokens comes from afar; with eight experts side by side
@@ -410,15 +406,15 @@ __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* row, cons
     for (int h = 0; h < a.n_groups; ++h) {
         const Pair v = {__shfl_sync(FULL, mine.hi, h * p.lanes), __shfl_sync(FULL, mine.lo, h * p.lanes)};
         const bool other = __shfl_sync(FULL, (int)in, h * p.lanes) != (int)in;
-        near |= other && distance(v, mine) <= tolerance;
+        near |= other && unsure(mine, v, tolerance);
     }
     close = __any_sync(FULL, near);
     return in;
 }
 
 // The order of the candidates, each as a pair on a lane of its own, where fp32
-// does not tell (all that may be among the k largest are there); false: pairs do
-// not, either.
+// does not tell (all that may be among the k largest and take part are there);
+// false: pairs do not, either.
 template <typename T>
 __device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, const Place p, int total, Chosen& out) {
     const int lane = threadIdx.x & 31;
@@ -436,7 +432,7 @@ __device__ __noinline__ bool order_again(const RouteArgs& a, const T* row, const
         rank += before(v, mine) || (!before(mine, v) && out.cand[d] < e);
         const float l_d = __shfl_sync(FULL, l, d), bias_d = __shfl_sync(FULL, bias, d);
         const bool same = l_d == l && bias_d == bias;
-        near |= !same && distance(v, mine) <= s.tolerance(fabsf(mine.hi));
+        near |= !same && unsure(mine, v, s.tolerance(fabsf(mine.hi)));
     }
     if (lane < total && rank < a.k) out.id[rank] = e;
     __syncwarp();
@@ -629,9 +625,10 @@ __device__ __forceinline__ void route_one(const RouteArgs& a, int t, const Place
             }
         }
         if (!again && __any_sync(FULL, close)) {
-            // all that may be among the k largest, as pairs
+            // all that may be among the k largest, as pairs; of fewer than k that take part
+            // these alone: the others are in order behind them
             const float kth = out.value[a.k - 1];
-            total = from(kth - (2.f * slack + 0x1p-21f * fabsf(kth)));
+            total = from(fmaxf(kth - (2.f * slack + 0x1p-21f * fabsf(kth)), -0x1.fffffep127f));
             again = total > 32 || !order_again(a, row, p, total, out);
         }
     }

@@ -84,5 +84,12 @@ QMM_PAIR Pair sigmoid_pair(float l) {
 
 QMM_PAIR bool before(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
+// Whether two values may be in either order when their difference is off by up to
+// `tolerance`.  What takes no part (-inf) is last, however large the tolerance.
+QMM_PAIR bool unsure(Pair a, Pair b, float tolerance) {
+    const float d = fabsf(__fadd_rn(__fadd_rn(a.hi, -b.hi), __fadd_rn(a.lo, -b.lo)));
+    return a.hi > -INFINITY && b.hi > -INFINITY && d <= tolerance;
+}
+
 }  // namespace route
 }  // namespace qmm
