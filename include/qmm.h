@@ -896,8 +896,9 @@ QMM_API qmm_status qmm_debug_attn_plan(const qmm_attn_op* op, int* kernel, int* 
  *    [n_adapters], or NULL (1).
  *  - A x is held in fp32, and both products' sums are fp32; 16-bit x and
  *    adapters enter as they are, fp32 ones and A x to 2^-23 of a value (A x to
- *    2^-18 with bf16 adapters and 16-bit y).  y is rounded once.  A row of x with
- *    a NaN or an infinity gives non-finite values in its own row alone.
+ *    2^-18 with bf16 adapters and 16-bit y), or to 2^-133 where that is more;
+ *    from 2^128 - 2^119 on these may count as infinite.  y is rounded once.  A row
+ *    of x with a NaN or an infinity gives non-finite values in its own row alone.
  * K % 32 == 0, max_rank <= QMM_LORA_MAX_RANK, n_segs <= 65536, T and N <= 2^28,
  * else QMM_ERR_SHAPE.  x and a: 16-byte aligned, ldx, lda and a_stride
  * multiples of 16 bytes, else QMM_ERR_ALIGN; b, base and y: aligned to their
