@@ -95,31 +95,30 @@ __device__ __forceinline__ void arrive_with_copies(uint64_t* bar) {
 }
 // Between the warps that copy and those that multiply: a slot is full when the
 // copies into it have landed, and empty when all eight warps have read it, by
-// mbarriers that count threads.  (A named barrier for the latter is 2 to 3% faster
+// mbarriers that count threads.  (A named barrier for the latter is 2 to 4% faster
 // for prompts, but takes the arrivals of warps that no longer wait for others', and
-// closes without the warps that copy, which then never leave it.  Arrivals of one
-// lane a warp: 171.4 us instead of 170.6 for 4093 rows.)
+// closes without the warps that copy, which then never leave it.)
 //
-// A warp waits while no wait of its CTA has run out (`live`, the same in all
-// lanes).  When one does the error word says so, and what follows has no meaning:
-// the warps that copy fill no more slots, the others read what lies there, and
-// all end as ever.
+// A wait gives up, for all lanes of its warp, when its time has run out or that of
+// another of the CTA: the error word says so, the warp leaves the ring, and what
+// follows has no meaning but ends as ever.
 struct Ring {
     uint64_t full[4], empty[4];
-    int dead;  // a wait has run out
+    int dead;      // a wait has run out
+    int disorder;  // of the segments' starts
 };
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, const LoraArgs& a, volatile int* dead, bool& live) {
-    if (!live || __all_sync(FULL, mbar_try_wait(bar, parity))) return;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const LoraArgs& a, volatile int* dead) {
+    if (__all_sync(FULL, mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = global_ns();
     while (!__all_sync(FULL, mbar_try_wait_sleep(bar, parity, 20000))) {
         const bool late = global_ns() - t0 > a.wait_ns;
-        if (late) *dead = 1;
-        if (__any_sync(FULL, late || *dead)) {
-            if (late) atomicOr(a.err, ERR_TIMEOUT);
-            live = false;
-            return;
+        if (late) {
+            atomicOr(a.err, ERR_TIMEOUT);
+            *dead = 1;
         }
+        if (__any_sync(FULL, *dead)) return false;
     }
+    return true;
 }
 __device__ __forceinline__ uint4 lds(uint32_t addr) {
     uint4 v;
@@ -384,16 +383,92 @@ struct RowTile {
     int rows, adapter;  // rows == 0: none; adapter < 0: none
 };
 
-// The tile of this number, counting 64 rows at a time through the segments; tiles
-// of up to 16 rows come last, where one look sees all segments: they are done
-// soon, and 64 rows that started behind 40 rows of one made a mix of 1013, 6144 ->
-// 2051, rank 24, fp16 take 52 us instead of 43.
+// The segment of a tile and the tile's place in it, to s_tile (segment, first row,
+// rows), counting tile_rows at a time through the segments; tiles of up to 16 rows
+// come last, where one look sees all segments: they are done soon, and 64 rows that
+// started behind 40 rows of one made a mix of 1013, 6144 -> 2051, rank 24, fp16 take
+// 52 us instead of 43.
 // Every thread of the block.  A start counts as the largest of those up to it,
 // brought into [0, T], so that segments never share rows (which tiles of two CTAs
-// would write) and their tiles are never more than were launched; an order that is
-// not kept is seen between neighbours (the first block looks at all of them).
-__device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
-    __shared__ uint2 s_sum[WARPS];  // a warp's tiles; whether its starts are out of order or range
+// would write) and their tiles are never more than were launched.  An order that
+// is not kept is seen between neighbours, and all is counted again, ORDERED: with
+// the largest start until now carried along.  (The first block looks at all of
+// them.)
+template <bool ORDERED>
+__device__ __forceinline__ void find_segment(const LoraArgs& a, int tile, volatile int* disorder, int (&s_tile)[3]) {
+    __shared__ uint32_t s_sum[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) s_tile[2] = 0;
+    // counts of both kinds in one number: below 2^23, and up to 256
+    const bool split = a.n_segs <= THREADS && a.T <= 1 << 27;
+    const uint32_t counts = split ? 0x7FFFFFu : 0xFFFFFFFFu;
+    const int shift = __ffs(a.tile_rows) - 1;
+    int before = 0, top = 0;  // top: the largest start until now
+    for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
+        const int s = s0 + threadIdx.x;
+        int n = 0, few = 0, first = 0, last = 0;
+        if (s < a.n_segs && threadIdx.x < THREADS) {
+            const int f = a.seg_start[s], l = a.seg_start[s + 1];
+            first = max(0, min(f, (int)a.T));
+            last = max(first, min(l, (int)a.T));
+            if (!ORDERED && (first != f || last != l)) {
+                *disorder = 1;
+                if (blockIdx.x == 0) atomicOr(a.err, ERR_BAD_INDEX);
+            }
+        }
+        if constexpr (ORDERED) {
+            int most = first;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(FULL, most, o);
+                if (lane >= o) most = max(most, v);
+            }
+            if (lane == 31 && warp < WARPS) s_sum[warp] = most;
+            __syncthreads();
+            most = max(most, top);
+            for (int w = 0; w < WARPS; ++w) {
+                const int v = (int)s_sum[w];
+                if (w < warp) most = max(most, v);
+                top = max(top, v);
+            }
+            __syncthreads();
+            if (s < a.n_segs && threadIdx.x < THREADS) {
+                first = most;
+                last = max(most, last);
+            }
+        }
+        n = (last - first + a.tile_rows - 1) >> shift;
+        const int left = (last - first) & (a.tile_rows - 1);
+        few = split && left > 0 && left <= 16;
+        n -= few;
+        uint32_t end = n | (uint32_t)few << 23;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(FULL, end, o);
+            if (lane >= o) end += v;
+        }
+        if (lane == 31 && warp < WARPS) s_sum[warp] = end;
+        __syncthreads();
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) end += s_sum[w];
+            all += s_sum[w];
+        }
+        int at = tile - (before + (int)(end & counts) - n), tiles = n;
+        if (few && tile - (int)(all & counts) == (int)(end >> 23) - 1) at = n, tiles = n + 1;
+        if (at >= 0 && at < tiles) {
+            s_tile[0] = s;
+            s_tile[1] = first + at * a.tile_rows;
+            s_tile[2] = min(a.tile_rows, last - first - at * a.tile_rows);
+        }
+        __syncthreads();
+        before += (int)(all & counts);
+        if (before > tile && blockIdx.x != 0) break;
+    }
+}
+
+__device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile, volatile int* disorder) {
     __shared__ int s_tile[3];
     RowTile t = {0, 0, -1};
     int seg = -1;
@@ -405,85 +480,10 @@ __device__ __forceinline__ RowTile find_tile(const LoraArgs& a, int tile) {
         t.row = (int64_t)seg * a.seg_rows + at;
         t.rows = min(a.tile_rows, a.seg_rows - at);
     } else {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (threadIdx.x == 0) s_tile[2] = 0;
-        // counts of both kinds in one number: below 2^23, and up to 256
-        const bool split = a.n_segs <= THREADS && a.T <= 1 << 27;
-        const uint32_t counts = split ? 0x7FFFFFu : 0xFFFFFFFFu;
-        const int shift = __ffs(a.tile_rows) - 1;
-        int before = 0, top = 0;  // top: the largest start until now, once the order was not kept
-        bool order = true;
-        for (int s0 = 0; s0 < a.n_segs; s0 += THREADS) {
-            const int s = s0 + threadIdx.x;
-            const bool there = s < a.n_segs && threadIdx.x < THREADS;
-            int n = 0, few = 0, first = 0, last = 0;
-            bool bad = false;
-            if (there) {
-                const int f = a.seg_start[s], l = a.seg_start[s + 1];
-                first = max(0, min(f, (int)a.T));
-                last = max(first, min(l, (int)a.T));
-                bad = first != f || last != l;
-                if (bad && blockIdx.x == 0) atomicOr(a.err, ERR_BAD_INDEX);
-            }
-            uint32_t end = 0, all = 0, wrong = 0;
-            bool again = !order;
-            do {
-                if (again) {
-                    int most = first;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int v = __shfl_up_sync(FULL, most, o);
-                        if (lane >= o) most = max(most, v);
-                    }
-                    __syncthreads();  // s_sum has been read
-                    if (lane == 31 && warp < WARPS) s_sum[warp].x = most;
-                    __syncthreads();
-                    most = max(most, top);
-                    for (int w = 0; w < WARPS; ++w) {
-                        const int v = (int)s_sum[w].x;
-                        if (w < warp) most = max(most, v);
-                        top = max(top, v);
-                    }
-                    __syncthreads();
-                    if (there) {
-                        first = most;
-                        last = max(most, last);
-                    }
-                }
-                n = (last - first + a.tile_rows - 1) >> shift;
-                const int left = (last - first) & (a.tile_rows - 1);
-                few = split && left > 0 && left <= 16;
-                n -= few;
-                end = n | (uint32_t)few << 23;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t v = __shfl_up_sync(FULL, end, o);
-                    if (lane >= o) end += v;
-                }
-                const bool any = __any_sync(FULL, bad);
-                if (lane == 31 && warp < WARPS) s_sum[warp] = make_uint2(end, any);
-                __syncthreads();
-                all = wrong = 0;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) {
-                    const uint2 v = s_sum[w];
-                    if (w < warp) end += v.x;
-                    all += v.x;
-                    wrong |= v.y;
-                }
-                again = order && wrong;
-                order = order && !wrong;
-            } while (again);
-            int at = tile - (before + (int)(end & counts) - n), tiles = n;
-            if (few && tile - (int)(all & counts) == (int)(end >> 23) - 1) at = n, tiles = n + 1;
-            if (at >= 0 && at < tiles) {
-                s_tile[0] = s;
-                s_tile[1] = first + at * a.tile_rows;
-                s_tile[2] = min(a.tile_rows, last - first - at * a.tile_rows);
-            }
-            __syncthreads();
-            before += (int)(all & counts);
-            if (before > tile && blockIdx.x != 0) break;
+        find_segment<false>(a, tile, disorder, s_tile);
+        if (*disorder) {
+            __syncthreads();  // s_tile is read by none
+            find_segment<true>(a, tile, disorder, s_tile);
         }
         seg = s_tile[0];
         t.row = s_tile[1];
@@ -703,8 +703,9 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     __shared__ Ring sync;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(&sync.full[i], 32 * K::COPIERS), mbar_init(&sync.empty[i], THREADS);
-        sync.dead = 0;
+        sync.dead = sync.disorder = 0;
     }
+    __syncthreads();  // sync is there
     // launched after the kernels that write x and base, possibly early
     // (programmatic dependent launch): nothing is read before they complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -714,10 +715,9 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     const int cs = a.cluster_shift;
     const uint32_t cta = cs ? cluster_rank() : 0;
     const int parts = a.parts_shift, part = (blockIdx.x >> cs) & ((1 << parts) - 1);
-    const RowTile t = find_tile(a, blockIdx.x >> (cs + parts));
+    const RowTile t = find_tile(a, blockIdx.x >> (cs + parts), &sync.disorder);
     if (t.rows == 0) return;  // of all CTAs of the cluster
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    __syncthreads();  // sync is there
     const int N = a.N, blocks = (N + 31) / 32;
     const int64_t share = (part << cs) + (int)cta;  // of the columns
     const int nb0 = (int)(blocks * share >> (cs + parts)), nb1 = (int)(blocks * (share + 1) >> (cs + parts));
@@ -824,7 +824,6 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
             arrive_with_copies(&sync.full[slot]);
         }
     };
-    bool live = true;
     // the warps that multiply fill the ring for the first time, all at once
     {
         const int s = warp / K::COPIERS;
@@ -838,6 +837,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     if (warp >= WARPS) {
         int slot = 0, group = 0, chunk = 0;
         uint32_t parity = 0;
+        asm volatile("" : "+r"(k.a_at));  // kept, not worked out again for each stage (2039 rows, fp32, rank 64: 105 -> 95 us)
         const auto step = [&] {
             chunk += k.km;
             if (chunk >= k.chunks) chunk = 0, ++group;
@@ -845,8 +845,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         for (int s = 0; s < depth; ++s) step();
         const auto run = [&](int from, int until) {
             for (int s = from; s < until; ++s) {
-                wait(&sync.empty[slot], parity, a, &sync.dead, live);
-                if (!live) return;
+                if (!wait(&sync.empty[slot], parity, a, &sync.dead)) return;
                 fill(s, slot, group, chunk);
                 step();
                 slot = slot + 1 == depth ? 0 : slot + 1;
@@ -880,7 +879,7 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         // of a stage's chunks, or of a chunk's steps, those of this part of K
         const bool by_chunk = k.km >= kways;
         for (int s = 0; s < stages_k; ++s) {
-            wait(&sync.full[slot], parity, a, &sync.dead, live);
+            if (!wait(&sync.full[slot], parity, a, &sync.dead)) break;
             if (mt < mtiles) {
                 const int n = min(k.km, k.chunks - chunk);
                 const int chunk_bytes = k.a_at + RT * K::AT::pitch, step = by_chunk ? kways : 1;
@@ -979,9 +978,8 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     constexpr int FIRST = WHOLE ? 8 : 2;  // a lane's columns in a block start at c times this
     int n = k.n_begin + blk * 32 + FIRST * c;
     Y* y0 = y + (t.row + r0) * a.ldy + n;
-    Y* y1 = y0 + 8 * a.ldy;
-    for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per, y1 += k.per) {
-        wait(&sync.full[slot], parity, a, &sync.dead, live);
+    for (int s = stages_k; s < stages; ++s, n += k.per, y0 += k.per) {
+        if (!wait(&sync.full[slot], parity, a, &sync.dead)) break;
         const uint32_t stage = ring + slot * slot_bytes;
         const int at_slot = slot;
         slot = slot + 1 == depth ? 0 : slot + 1;
@@ -1043,14 +1041,15 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
         release(s, at_slot);
         if constexpr (WHOLE) {
             store_eight(y0, e0, in0 && n < N);
-            store_eight(y1, e1, in1 && n < N);
+            store_eight(y0 + 8 * a.ldy, e1, in1 && n < N);
         } else {
             const Y* b = base ? base + (t.row + r0) * a.ld_base + n : nullptr;
             if (in0) finish_plain(y0, b, N - n, e0);
-            if (in1) finish_plain(y1, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
+            if (in1) finish_plain(y0 + 8 * a.ldy, b ? b + 8 * a.ld_base : nullptr, N - n, e1);
         }
     }
-    if (!live) copies_wait();  // these warps' own, of the first stages; otherwise they have been waited for
+    // these warps' own copies, of the first stages; unless a wait gave up they have been waited for
+    if (*static_cast<volatile int*>(&sync.dead)) copies_wait();
     if (cs) cluster_wait();
 }
 
