@@ -136,7 +136,8 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     // and the barriers take 8 us whatever it has to do.  (us with four and with
     // eight: one row of 2048 -> 2048, rank 16, 6.8 and 6.4; 48 of 8192 -> 8192, rank
     // 16, 17.3 and 13.6; 2039 rows of 5632 -> 8192 66 and 45; 64 segments of one row of
-    // 2048 -> 5632, rank 64, 22.5 and 29.0; 4093 rows of 8192 -> 28672 163 and 172.)
+    // 2048 -> 5632, rank 64, 22.5 and 29.0; 4093 rows of 8192 -> 28672 163 and 172; these
+    // and the figures of the rules below are of the day each was chosen.)
     const int64_t room_for = (int64_t)sms * (tile == 0 ? 3 : 2);
     const int64_t busy = op->seg_start ? std::min(tiles, op->T / a.tile_rows + op->n_segs / 2) : tiles;
     int64_t c = busy * LORA_MAX_CLUSTER <= room_for ? LORA_MAX_CLUSTER : 4;
@@ -161,7 +162,10 @@ extern "C" qmm_status qmm_lora(const qmm_lora_op* op, void* stream) {
     const int64_t ctas = tiles * c << a.parts_shift;
     // One CTA an SM, two, three: few CTAs have deeper rings.  (us with two or three and
     // with one: 6 rows of one of 2048 -> 2048, rank 128, fp32, 28.1 and 19.8; 18 of 6144
-    // -> 2048, rank 64, fp16, 16.4 and 12.3; 645 of 4096 -> 8066, rank 128, 77.9 and 84.8.)
+    // -> 2048, rank 64, fp16, 16.4 and 12.3; the rule loses at 645 of 4096 -> 8066, rank
+    // 128, 77.9 and 84.8.)  Where two slots at least do not fit beside h a CTA has more
+    // than its share: fp32 rows with fp32 adapters of 33 to 64 ranks, 64 rows a tile,
+    // need 116,736 bytes and are one CTA an SM.
     const int total = (ctas <= sms ? 220 : tile || ctas <= 2 * sms ? 110 : 72) * 1024;
     const int least = (std::max(chunk, block) + 127) / 128 * 128, most = std::max(4 * chunk, 8 / m2 * block);
     const int share = (total - a.ring_at) / 4 / 128 * 128;

@@ -12,9 +12,11 @@
 // x, base and y pass once; A and B are read once a tile (from L2 where tiles
 // share an adapter).  So the bound is memory for the ranks in use: 2 r flops
 // against the 2 or 4 bytes of a value of x.  Measured: 4093 rows of 8192 -> 28672,
-// rank 64, bf16, 171 us, 3.3 TB/s (fixed latencies at 17 warps an SM: the phases
-// take turns in a CTA, and two CTAs fill the shared memory); one row of 2048 ->
-// 2048 6.5 us, the chain of its phases, of which h's way through the cluster 3.
+// rank 64, bf16, 166 us, 3.4 TB/s (the columns take 111 of a CTA's 143 us, the
+// last 171; shared memory's data path is at 72% of its peak in the cycles that an
+// SM is busy, the tensor pipe at 42%, at 18 warps an SM: two CTAs fill the shared
+// memory); one row of 2048 -> 2048 6.3 us, the chain of its phases, of which h's way
+// through the cluster 2.6.
 //
 // x and A (64 columns of K at a time), then B and base (32-column blocks of N)
 // come through one ring of asynchronous copies: the first columns are on their
@@ -736,8 +738,8 @@ __global__ void __launch_bounds__(THREADS + 32 * LORA_COPIERS<RT>, RT == 16 ? 3 
     }
     if (rank == 0) {
         // y = base, several loads at a time of each thread: with one, 4093 rows of 8192
-        // bf16 took 47 us and 2051 fp16, which start anywhere, 93, and now 34 and 17
-        // (3.9 and 2.0 TB/s)
+        // bf16 took 47 us and 2051 fp16, which start anywhere, 93, and now 30 and 17
+        // (4.5 and 2.0 TB/s)
         if (a.y == a.base) return;
         const int first = nb0 * 32, cols = min(N, nb1 * 32) - first;
         if (a.vec_out) {

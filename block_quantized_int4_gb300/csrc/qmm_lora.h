@@ -6,7 +6,8 @@
 namespace qmm {
 
 // Warps of a CTA that copy, by the ranks of its kernel (16: three CTAs an SM and
-// 72 registers a thread with one; 32 and 64: two CTAs either way).
+// 72 registers a thread with one; 32 and 64: two CTAs either way, as far as
+// registers go).
 template <int RANKS>
 constexpr int LORA_COPIERS = RANKS == 16 ? 1 : 2;
 constexpr int LORA_MAX_CLUSTER = 8;  // CTAs of a tile

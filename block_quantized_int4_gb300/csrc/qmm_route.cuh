@@ -20,8 +20,9 @@
 //    switched off or in few lanes: k rounds over all.
 // What bounds it: the logits pass once (65521 tokens of 512, fp32: 44 us, 3.1
 // TB/s), but a token takes some 530 warp instructions, 890 with sigmoid, bias and
-// groups (32003 tokens of 256: 36 us), comparisons most of them: their pipe is 53%
-// and 60% busy at 30 warps an SM, which registers limit.
+// groups (32003 tokens of 256: 36 us; 15 of them reach spilled registers),
+// comparisons most of them: their pipe is 53% and 61% busy at 28 warps an SM, which
+// registers limit.
 #pragma once
 
 #include <cuda_bf16.h>
